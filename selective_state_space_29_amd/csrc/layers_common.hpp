@@ -1,0 +1,47 @@
+// Helpers shared by the layer operators (mamba_layers.h): storage types, 16-byte vectors, launch
+// checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mamba_layers.h"
+#include "common.hpp"
+
+namespace mscan {
+
+// fp32 to bf16, to nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ bf16_t to_bf16(float v) {
+    const __bf16 h = (__bf16)v;
+    bf16_t r;
+    __builtin_memcpy(&r.bits, &h, 2);
+    return r;
+}
+
+template <typename S>
+__device__ __forceinline__ S from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) { return to_bf16(v); }
+
+// V consecutive elements moved as one access where V * sizeof(S) allows it.
+template <typename S, int V>
+struct __align__(V * sizeof(S)) Pack {
+    S v[V];
+};
+
+// Sum over the 64 lanes of a wave, the same bits in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+inline int launch_status() { return hipGetLastError() == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_LAUNCH; }
+
+inline int64_t align256(int64_t n) { return (n + 255) & ~(int64_t)255; }
+
+int layers_cus();  // compute units of the current device (layers.hip); 256 if the runtime cannot say
+
+}  // namespace mscan

@@ -1,0 +1,35 @@
+// Launchers of the layer operators, each in a translation unit of its own; the entry points in
+// layers.hip validate and call these.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/mamba_layers.h"
+
+namespace mscan {
+
+// How a gated-scan call is laid out on the GPU: channels per workgroup, sequence segments.
+struct GatedPlan {
+    int ch, nseg;
+    int64_t seg_len;
+};
+GatedPlan gated_plan(const mamba_gated_shape& s, int cus);
+GatedPlan gated_bwd_plan(const mamba_gated_shape& s, int cus);
+
+struct GatedParams;
+struct GatedBwdParams;
+int launch_gated_fwd(const GatedParams& q, const GatedPlan& plan, bool bf16, hipStream_t stream);
+int launch_gated_checkpoints(const GatedParams& q, const GatedPlan& plan, bool bf16, hipStream_t stream);
+int launch_gated_bwd(const GatedBwdParams& q, const GatedPlan& plan, float* dlam, bool bf16, hipStream_t stream);
+
+int launch_norm_fwd(const mamba_norm_ptrs& p, const mamba_norm_shape& s, float eps, bool bf16, hipStream_t stream);
+int launch_norm_bwd(const mamba_norm_bwd_ptrs& p, const mamba_norm_shape& s, bool bf16, hipStream_t stream);
+int64_t norm_bwd_workspace(const mamba_norm_shape& s);
+
+int launch_embedding_fwd(const void* ids, bool ids64, const void* weight, void* y, const mamba_embedding_shape& s,
+                         float scale, bool bf16, hipStream_t stream);
+int launch_embedding_bwd(const void* ids, bool ids64, const void* dy, void* dweight, void* ws,
+                         const mamba_embedding_shape& s, float scale, bool bf16, hipStream_t stream);
+int64_t embedding_bwd_workspace(const mamba_embedding_shape& s);
+
+}  // namespace mscan

@@ -1,0 +1,424 @@
+"""The layer operators on the GPU against 64-bit references (tests/layers_ref.py).
+
+Bars, as max |g - r| / (1 + |r|): fp32 1e-4, the scan's fp32 bar. The recurrence's own error stays
+below it here: a relative error of about 2^-22 a step (gates and decay, a few roundings each) over the
+at most 100 steps that decays up to 0.99 remember is 2.4e-5. Layer norm and the embedding's sums of up
+to 2^12 terms err by at most 2^12 2^-24 of their terms' magnitude. A bf16 output adds its own
+rounding, 2^-9 of it (a value next to a rounding boundary may fall to either side: 2^-8).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import layers_ref as ref
+from selective_state_space_29_amd import layers
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TOL = 1e-4
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def close(got, want, tol=TOL):
+    got, want = got.detach().cpu(), want.detach().cpu()
+    assert got.shape == want.shape, (got.shape, want.shape)
+    if got.numel() == 0:
+        return
+    room = tol * (1 + want.abs()) + (2.0 ** -8 * want.abs() if got.dtype == BF16 else 0.0)
+    err = (got.double() - want).abs()
+    assert bool((err <= room).all()), f"max error {float((err - room).max()):.3e} over the bar, at {int((err - room).argmax())}"
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def gated_case(seed, B, L, D, dtype, h0=True, reset=False, decay=(0.5, 0.99)):
+    g = gen(seed)
+    t = {k: torch.randn(B, L, D, generator=g).to(dtype) for k in ("x", "r", "i", "dy")}
+    t["lam"] = ref.lam_for(decay[0] + (decay[1] - decay[0]) * torch.rand(D, generator=g))
+    t["h0"] = torch.randn(B, D, generator=g) if h0 else None
+    t["reset"] = torch.rand(B, L, generator=g) < 0.02 if reset else None
+    t["dlast"] = torch.randn(B, D, generator=g)
+    return t
+
+
+def dev(t):
+    return {k: None if v is None else v.to(DEV) for k, v in t.items()}
+
+
+def check_gated(t, tol=TOL):
+    d = dev(t)
+    kw = dict(h0=d["h0"], reset=d["reset"])
+    y, last = layers.gated_scan_fn(d["x"], d["r"], d["i"], d["lam"], return_last_state=True, **kw)
+    yr, lr = ref.gated_scan(t["x"], t["r"], t["i"], t["lam"], h0=t["h0"], reset=t["reset"])
+    close(y, yr, tol)
+    close(last, lr, tol)
+    want = ref.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], h0=t["h0"], reset=t["reset"], dlast=t["dlast"])
+    ck = torch.full(layers.gated_checkpoint_shape(*t["x"].shape), float("nan"), device=DEV)
+    y2 = layers.gated_scan_fn(d["x"], d["r"], d["i"], d["lam"], checkpoints_out=ck, **kw)
+    assert torch.equal(y2, y)
+    for checkpoints in (ck, None):
+        g = layers.gated_scan_bwd(d["x"], d["r"], d["i"], d["lam"], d["dy"], dlast_state=d["dlast"], checkpoints=checkpoints,
+                                  want_dh0=True, **kw)
+        for k in ("x", "r", "i", "h0"):
+            close(g[k], want[k], tol)
+        # a sum of B L terms of either sign: judged against the sum of their magnitudes
+        scale = 1 + (want["lam"].abs().max() + t["x"].shape[0] * t["x"].shape[1] * 1e-2)
+        assert float((g["lam"].cpu().double() - want["lam"]).abs().max()) <= tol * float(scale)
+
+
+SIZES = [(1, 1, 1), (2, 1, 64), (3, 2, 5), (2, 8, 130), (2, 9, 65), (1, 15, 16), (2, 16, 63), (1, 17, 64), (2, 127, 33),
+         (1, 128, 64), (3, 129, 17), (1, 255, 128), (2, 256, 96), (1, 257, 31), (2, 700, 70)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_gated_sizes(size, dtype):
+    check_gated(gated_case(hash(size) % 1000, *size, dtype, h0=size[1] % 2 == 0, reset=size[2] % 2 == 0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,L,D", [(1, 5000, 8), (1, 4097, 40), (2, 2500, 100), (24, 300, 600)])
+def test_gated_split_and_wide(B, L, D, dtype):
+    """Few long rows (the sequence split over workgroups) and enough rows for the widest groups."""
+    check_gated(gated_case(7, B, L, D, dtype, reset=True))
+
+
+def test_gated_slow_decay_carries_over_segments():
+    t = gated_case(8, 1, 6000, 4, F32, decay=(0.9999, 0.99999))
+    # the memory is the whole sequence: 6000 steps of 2^-22 is 1.4e-3
+    check_gated(t, tol=2e-3)
+
+
+@pytest.mark.parametrize("where", ["first", "all", "last", "none"])
+def test_gated_resets(where):
+    t = gated_case(9, 2, 300, 33, F32, reset=True)
+    t["reset"].fill_(where == "all")
+    if where == "first":
+        t["reset"][:, 0] = True
+    if where == "last":
+        t["reset"][:, -1] = True
+    check_gated(t)
+    if where == "first":  # the initial state is forgotten: it gets no gradient
+        d = dev(t)
+        g = layers.gated_scan_bwd(d["x"], d["r"], d["i"], d["lam"], d["dy"], h0=d["h0"], reset=d["reset"])
+        assert not g["h0"].any()
+
+
+def test_gated_packed_sequences_do_not_see_each_other():
+    """Two sequences packed with a reset between them give, where their steps fall on the same run and
+    chunk boundaries, exactly what they give alone."""
+    t = dev(gated_case(10, 1, 512, 70, F32, h0=False))
+    reset = torch.zeros(1, 512, dtype=torch.uint8, device=DEV)
+    reset[0, 256] = 7
+    y = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], reset=reset)
+    first = torch.zeros(1, 256, dtype=torch.bool, device=DEV)
+    first[0, 0] = True  # a reset step has no decay to normalise by: its input enters whole
+    parts = [layers.gated_scan_fn(*(t[k][:, s].contiguous() for k in "xri"), t["lam"], reset=f)
+             for s, f in ((slice(0, 256), None), (slice(256, 512), first))]
+    close(y, torch.cat(parts, 1).double(), 1e-6)
+    other = t["x"].clone()
+    other[:, :256] = float("inf")  # nothing of the first reaches the second
+    y2 = layers.gated_scan_fn(other, t["r"], t["i"], t["lam"], reset=reset)
+    assert torch.equal(y2[:, 256:], y[:, 256:])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gated_extreme_gates(dtype):
+    """Gates fully open and shut, decays of 0 and 1: no NaN, and the reference's values."""
+    t = gated_case(11, 2, 40, 12, dtype)
+    big = torch.tensor([-200.0, -90.0, -30.0, 0.0, 30.0, 90.0, 200.0])
+    t["r"][0] = big[torch.randint(0, 7, (40, 12), generator=gen(1))].to(dtype)
+    t["i"][1] = big[torch.randint(0, 7, (40, 12), generator=gen(2))].to(dtype)
+    t["lam"][:6] = torch.tensor([-300.0, -60.0, -20.0, 20.0, 60.0, 300.0])
+    check_gated(t)
+
+
+def test_gated_reset_forgets_bad_gradients():
+    """The adjoint's direction: an infinite gradient after a reset does not reach the steps before."""
+    t = dev(gated_case(17, 1, 600, 40, F32, h0=False))
+    reset = torch.zeros(1, 600, dtype=torch.bool, device=DEV)
+    reset[0, 300] = True
+    kw = dict(reset=reset)
+    a = layers.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], **kw)
+    t["dy"][:, 400] = float("inf")
+    t["x"][:, 200] = float("nan")
+    b = layers.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], **kw)
+    for k in ("x", "r", "i"):
+        assert torch.equal(a[k][:, :200], b[k][:, :200]), k
+        assert torch.equal(a[k][:, 401:], b[k][:, 401:]), k
+        assert b[k][:, 300].isfinite().all() if k == "r" else True
+
+
+def test_gated_bad_values_stay_in_their_channel():
+    t = dev(gated_case(12, 2, 300, 20, F32))
+    y0 = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], h0=t["h0"])
+    t["x"][0, 100, 3] = float("nan")
+    t["x"][1, 50, 7] = float("inf")
+    y = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], h0=t["h0"])
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[0, 100:, 3] = bad[1, 50:, 7] = True
+    assert torch.equal(y[~bad], y0[~bad])
+    assert y[0, 100:, 3].isnan().all() and not y[1, 50:, 7].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [48, 51])
+def test_gated_strided_inputs(D, dtype):
+    """Slices of a merged projection, a transposed batch, an output with gaps: the contiguous bits."""
+    g = gen(13)
+    p = torch.randn(3, 200, 3 * D, generator=g).to(dtype).to(DEV)
+    x, r, i = p.split(D, dim=-1)
+    lam = torch.rand(D, generator=g).to(DEV)
+    want = layers.gated_scan_fn(x.contiguous(), r.contiguous(), i.contiguous(), lam)
+    assert torch.equal(layers.gated_scan_fn(x, r, i, lam), want)
+    swapped = [v.transpose(0, 1).contiguous().transpose(0, 1) for v in (x, r, i)]
+    assert torch.equal(layers.gated_scan_fn(*swapped, lam), want)
+    out = torch.full((3, 200, D + 5), 9.0, dtype=dtype, device=DEV)
+    layers.gated_scan_fn(x, r, i, lam, out=out[..., :D])
+    assert torch.equal(out[..., :D], want) and bool((out[..., D:] == 9).all())
+    scan_layout = [v.transpose(1, 2).contiguous().transpose(1, 2) for v in (x, r, i)]  # unit stride along len
+    assert torch.equal(layers.gated_scan_fn(*scan_layout, lam), want)
+    dy = torch.randn(3, 200, D, generator=g).to(dtype).to(DEV)
+    a = layers.gated_scan_bwd(x, r, i, lam, dy)
+    b = layers.gated_scan_bwd(x.contiguous(), r.contiguous(), i.contiguous(), lam, dy.transpose(0, 1).contiguous().transpose(0, 1))
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
+def test_gated_decode_continues_a_prompt():
+    """A prompt, then one step a call with the state updated in place, against one long call."""
+    t = dev(gated_case(14, 4, 160, 90, F32, h0=False))
+    yall, last = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], return_last_state=True)
+    _, state = layers.gated_scan_fn(*(t[k][:, :150] for k in "xri"), t["lam"], return_last_state=True)
+    for s in range(150, 160):
+        y, same = layers.gated_scan_fn(*(t[k][:, s:s + 1] for k in "xri"), t["lam"], h0=state, return_last_state=True,
+                                       last_state_out=state)
+        assert same is state
+        close(y, yall[:, s:s + 1].double(), 1e-5)
+    close(state, last.double(), 1e-5)
+
+
+def test_gated_repeats_bit_for_bit_and_on_another_stream():
+    t = dev(gated_case(15, 2, 3000, 100, BF16, reset=True))
+    kw = dict(h0=t["h0"], reset=t["reset"])
+
+    def once():
+        y = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], **kw)
+        g = layers.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], **kw)
+        return [y, *g.values()]
+
+    a, b = once(), once()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c = once()
+    torch.cuda.current_stream().wait_stream(s)
+    for p, q, w in zip(a, b, c):
+        assert torch.equal(p, q) and torch.equal(p, w)
+
+
+def test_gated_autograd_and_differences():
+    t = dev(gated_case(16, 2, 50, 20, F32))
+    leaves = [t[k].requires_grad_() for k in ("x", "r", "i", "lam", "h0")]
+    w = torch.randn(2, 50, 20, device=DEV, dtype=torch.float64)
+
+    def loss():
+        y, last = layers.gated_scan(leaves[0], leaves[1], leaves[2], leaves[3], h0=leaves[4], return_last_state=True)
+        return (y.double() * w).sum() + (last.double() * w[:, 0]).sum()
+
+    grads = torch.autograd.grad(loss(), leaves)
+    for leaf, g in zip(leaves, grads):
+        # central differences along a random direction: truncation ~ step^2, rounding ~ 2^-22 sqrt(2000) / step
+        v = torch.randn_like(leaf)
+        v /= v.norm()
+        step = 1e-2
+        with torch.no_grad():
+            leaf += step * v
+            up = loss()
+            leaf -= 2 * step * v
+            down = loss()
+            leaf += step * v
+        want = float((up - down) / (2 * step))
+        assert abs(float((g.double() * v).sum()) - want) <= 5e-3 * (1 + abs(want))
+
+
+def test_gated_empty():
+    lam = torch.zeros(5, device=DEV)
+    e = torch.zeros(2, 0, 5, device=DEV)
+    h0 = torch.randn(2, 5, device=DEV)
+    y, last = layers.gated_scan_fn(e, e, e, lam, h0=h0, return_last_state=True)
+    assert y.shape == (2, 0, 5) and torch.equal(last, h0)
+    _, last = layers.gated_scan_fn(e, e, e, lam, return_last_state=True)
+    assert not last.any()
+    g = layers.gated_scan_bwd(e, e, e, lam, e, h0=h0, dlast_state=h0)
+    assert torch.equal(g["h0"], h0) and not g["lam"].any()
+    n = torch.zeros(0, 7, 5, device=DEV)
+    assert layers.gated_scan_fn(n, n, n, lam).shape == (0, 7, 5)
+    assert not layers.gated_scan_bwd(n, n, n, lam, n)["lam"].any()
+    z = torch.zeros(2, 7, 0, device=DEV)
+    assert layers.gated_scan_fn(z, z, z, torch.zeros(0, device=DEV)).shape == (2, 7, 0)
+
+
+def test_gated_offsets_past_32_bits():
+    """Outputs past 4 GiB: the last rows of a long bf16 tensor, which begin a sequence."""
+    L, D = 1_100_000, 2048
+    x = torch.empty(1, L, D, dtype=BF16, device=DEV).fill_(0.5)
+    lam = ref.lam_for(torch.full((D,), 0.9)).to(DEV)
+    tail = torch.randn(1, 1000, D, device=DEV).to(BF16)
+    x[:, -1000:] = tail
+    reset = torch.zeros(1, L, dtype=torch.uint8, device=DEV)
+    reset[0, -1000] = 1
+    y = layers.gated_scan_fn(x, x, x, lam, reset=reset)
+    some = tail[..., ::64].cpu()
+    want, _ = ref.gated_scan(some, some, some, lam[::64].cpu(), reset=reset[:, -1000:].cpu())
+    close(y[:, -1000:, ::64], want)
+    assert x.numel() * 2 > 1 << 32
+
+
+# ---- layer norm ----
+
+NORM = [(1, 1), (3, 2), (5, 7), (4, 64), (9, 96), (2, 511), (7, 768), (33, 1000), (6, 1024), (5, 1025), (3, 2048), (4, 4096),
+        (2, 5001), (2, 8192), (3, 16384), (2, 20000), (1, 40001), (2, 70000), (1500, 24)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim", NORM)
+def test_norm(rows, dim, dtype):
+    g = gen(rows * 7 + dim)
+    x, res, dy, dt = (torch.randn(rows, dim, generator=g).to(dtype) * s for s in (1, 3, 1, 1))
+    x = x + torch.tensor(2.0, dtype=dtype)
+    w, b = 1 + 0.3 * torch.randn(dim, generator=g), torch.randn(dim, generator=g)
+    for with_res in (False, True):
+        t = (x.double() + res.double()).to(dtype) if with_res else x
+        X, R, W, Bi = x.to(DEV), res.to(DEV) if with_res else None, w.to(DEV), b.to(DEV)
+        out, stats = layers.layer_norm_fn(X, W, Bi, 1e-5, residual=R, return_stats=True)
+        y, tg = out if with_res else (out, X)
+        if with_res:
+            assert torch.equal(tg.cpu(), t)
+        close(y, ref.layer_norm(t, w, b))
+        grads = layers.layer_norm_bwd(tg, W, dy.to(DEV), stats, dresidual=dt.to(DEV) if with_res else None)
+        want = ref.layer_norm_bwd(t, w, dy, dresidual=dt if with_res else None)
+        # a row of one or two values is constant or +-1: rstd reaches 316, and dx's terms cancel
+        close(grads["x"], want["x"], TOL if dim > 2 else 5e-2)
+        for k in ("weight", "bias"):
+            close(grads[k], want[k])
+
+
+def test_norm_defaults_strides_and_in_place_layouts():
+    g = gen(20)
+    base = torch.randn(6, 5, 200, generator=g).to(DEV)
+    x = base[:, 1:4, 20:120]  # rows that are not evenly spaced: copied; the last dimension is
+    close(layers.layer_norm_fn(x), ref.layer_norm(x.cpu()))
+    even = base[:, 2, 7:150]  # evenly spaced rows, unaligned: read in place
+    out, stats = layers.layer_norm_fn(even, return_stats=True)
+    close(out, ref.layer_norm(even.cpu()))
+    dy = base[:, 3, 1:144]
+    grads = layers.layer_norm_bwd(even, None, dy, stats, want_dbias=False)
+    want = ref.layer_norm_bwd(even.cpu(), None, dy.cpu())
+    close(grads["x"], want["x"])
+    close(grads["weight"], want["weight"])
+    assert "bias" not in grads
+    close(layers.layer_norm_fn(x.transpose(1, 2)), ref.layer_norm(x.cpu().transpose(1, 2)))
+
+
+def test_norm_constant_rows_and_bad_values():
+    x = torch.full((4, 300), 5.0, device=DEV)
+    assert not layers.layer_norm_fn(x).any()
+    x[1, 7] = float("nan")
+    x[2, 9] = float("inf")
+    y = layers.layer_norm_fn(x)
+    assert not y[0].any() and not y[3].any() and y[1].isnan().all() and y[2].isnan().all()
+    big = torch.randn(3, 500, device=DEV) * 1e15 + 1e16  # squares stay finite, the mean is large
+    close(layers.layer_norm_fn(big, eps=0.0), ref.layer_norm(big.cpu(), eps=0.0), 1e-3)
+
+
+def test_norm_autograd_differences_and_empty():
+    x, res, w, b = (torch.randn(*s, device=DEV).requires_grad_() for s in ((7, 40), (7, 40), (40,), (40,)))
+    v1, v2 = torch.randn(2, 7, 40, device=DEV, dtype=torch.float64)
+
+    def loss():
+        y, t = layers.layer_norm(x, w, b, residual=res)
+        return (y.double() * v1).sum() + (t.double() * v2).sum()
+
+    grads = torch.autograd.grad(loss(), (x, res, w, b))
+    assert torch.equal(grads[0], grads[1])
+    for leaf, g in zip((x, res, w, b), grads):
+        d = torch.randn_like(leaf)
+        d /= d.norm()
+        with torch.no_grad():
+            leaf += 1e-2 * d
+            up = loss()
+            leaf -= 2e-2 * d
+            down = loss()
+            leaf += 1e-2 * d
+        want = float((up - down) / 2e-2)
+        assert abs(float((g.double() * d).sum()) - want) <= 5e-3 * (1 + abs(want))
+    e = torch.zeros(0, 8, device=DEV)
+    y, st = layers.layer_norm_fn(e, return_stats=True)
+    g = layers.layer_norm_bwd(e, None, e, st)
+    assert y.shape == (0, 8) and not g["weight"].any() and not g["bias"].any()
+
+
+# ---- embedding ----
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 1, 1), (5, 3, 7), (64, 10, 64), (65, 1, 40), (300, 500, 33), (1000, 40, 768),
+                                              (700, 7, 1030), (2100, 2, 24), (5000, 3, 16), (4096, 60000, 8), (129, 2, 520)])
+def test_embedding(tokens, vocab, dim, dtype):
+    g = gen(tokens + vocab)
+    ids = torch.randint(-1, vocab + 1, (tokens,), generator=g)
+    w, dy = torch.randn(vocab, dim, generator=g).to(dtype), torch.randn(tokens, dim, generator=g).to(dtype)
+    for it in (torch.int64, torch.int32):
+        y = layers.embedding_fn(ids.to(it).to(DEV), w.to(DEV), 2.5)
+        close(y, ref.embedding(ids, w, 2.5))
+        dw = layers.embedding_bwd(ids.to(it).to(DEV), dy.to(DEV), vocab, 0.5)
+        close(dw, ref.embedding_bwd(ids, dy, vocab, 0.5), TOL * max(1, tokens // vocab / 200))
+
+
+def test_embedding_gradient_repeats_bit_for_bit():
+    """Integer atomics place the tokens in any order; the sums are taken in token order."""
+    g = gen(30)
+    ids = (torch.rand(20000, generator=g) ** 8 * 300).long().to(DEV)  # a few ids take thousands
+    dy = torch.randn(20000, 40, generator=g).to(DEV)
+    a = layers.embedding_bwd(ids, dy, 300)
+    for _ in range(3):
+        assert torch.equal(layers.embedding_bwd(ids, dy, 300), a)
+    # in token order in pieces of at most 64: the first rows of an id that has at most 64 tokens
+    few = (torch.bincount(ids, minlength=300) <= 64).nonzero()[:, 0].tolist()
+    for v in few[:5]:
+        s = torch.zeros(40)
+        for t in (ids == v).nonzero()[:, 0].tolist():
+            s += dy[t].cpu()
+        assert torch.equal(a[v].cpu(), s)
+
+
+def test_embedding_shapes_padding_and_autograd():
+    w = torch.randn(11, 6, device=DEV, requires_grad=True)
+    ids = torch.tensor([[3, -1, 3], [10, 11, 2 ** 40]], device=DEV)
+    y = layers.embedding(ids, w, 3.0)
+    close(y, ref.embedding(ids.cpu(), w.detach().cpu(), 3.0))
+    y.sum().backward()
+    want = torch.zeros(11, 6)
+    want[3], want[10] = 6.0, 3.0
+    assert torch.equal(w.grad.cpu(), want)
+    none = torch.zeros(0, dtype=torch.int64, device=DEV)
+    assert layers.embedding_fn(none, w).shape == (0, 6)
+    assert not layers.embedding_bwd(none, torch.zeros(0, 6, device=DEV), 11).any()
+    assert not layers.embedding_bwd(torch.full((100,), -1, device=DEV), torch.ones(100, 6, device=DEV), 11).any()
+    pad = torch.randn(5, 9, device=DEV)[:, :6]  # a weight with gaps between its rows
+    close(layers.embedding_fn(torch.tensor([4, 0], device=DEV), pad), pad.cpu().double()[[4, 0]])
+
+
+def test_embedding_offsets_past_32_bits():
+    V, D = 1_200_000, 2048
+    w = torch.empty(V, D, dtype=BF16, device=DEV).fill_(1.0)
+    w[-1] = torch.arange(D, device=DEV).to(BF16)
+    ids = torch.tensor([V - 1, 0], device=DEV)
+    y = layers.embedding_fn(ids, w)
+    assert torch.equal(y[0], w[-1]) and bool((y[1] == 1).all())
+    dw = layers.embedding_bwd(ids, y, V)
+    assert torch.equal(dw[-1], y[0]) and bool((dw[0] == 1).all()) and not dw[1:-1].any()
