@@ -191,6 +191,50 @@ int mamba_embedding_bwd(const void* ids, int ids64, const void* dy, void* dweigh
                         void* stream);
 int64_t mamba_embedding_bwd_workspace_bytes(const mamba_embedding_shape* s);
 
+/*
+ * Gated feed-forward block up to its product: h = act(x w_gate^T) * (x w_up^T), act = silu or gelu in
+ * its tanh form, and its gradient, which recomputes both projections:
+ *   dg = dh u act'(g), du = dh act(g), each rounded to bf16 once as an operand of the products
+ *   dx = dg w_gate + du w_up;  dw_gate = dg^T x;  dw_up = du^T x
+ *  - x (rows, dim), w_gate, w_up (hidden, dim), h, dh (rows, hidden); all bf16, row strides free,
+ *    products accumulated in fp32. dtype must be MAMBA_SCAN_BF16 (MAMBA_SCAN_ERR_UNSUPPORTED for F32).
+ *  - workspace: mamba_gated_ffn_workspace_bytes() / ..._bwd_workspace_bytes(), 256-byte aligned.
+ */
+#define MAMBA_FFN_SILU 0
+#define MAMBA_FFN_GELU_TANH 1
+
+typedef struct mamba_ffn_shape {
+    int64_t rows, dim, hidden;
+} mamba_ffn_shape;
+
+typedef struct mamba_ffn_ptrs {
+    const void* x;
+    const void* w_gate;
+    const void* w_up;
+    void* h;
+    int64_t x_stride, w_gate_stride, w_up_stride, h_stride;
+    void* workspace;
+    int64_t workspace_bytes;
+} mamba_ffn_ptrs;
+
+typedef struct mamba_ffn_bwd_ptrs {
+    const void* x;
+    const void* w_gate;
+    const void* w_up;
+    const void* dh;
+    void* dx;        /* (rows, dim) contiguous */
+    void* dw_gate;   /* (hidden, dim) contiguous */
+    void* dw_up;
+    int64_t x_stride, w_gate_stride, w_up_stride, dh_stride;
+    void* workspace;
+    int64_t workspace_bytes;
+} mamba_ffn_bwd_ptrs;
+
+int mamba_gated_ffn_fwd(const mamba_ffn_ptrs* p, const mamba_ffn_shape* s, int act, mamba_scan_dtype dtype, void* stream);
+int mamba_gated_ffn_bwd(const mamba_ffn_bwd_ptrs* p, const mamba_ffn_shape* s, int act, mamba_scan_dtype dtype, void* stream);
+int64_t mamba_gated_ffn_workspace_bytes(const mamba_ffn_ptrs* p, const mamba_ffn_shape* s);
+int64_t mamba_gated_ffn_bwd_workspace_bytes(const mamba_ffn_shape* s);
+
 /* MAMBA_LAYERS_ABI_VERSION of the built library. */
 int mamba_layers_abi_version(void);
 

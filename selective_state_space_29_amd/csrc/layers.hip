@@ -397,4 +397,90 @@ int mamba_embedding_bwd(const void* ids, int ids64, const void* dy, void* dweigh
                                 static_cast<hipStream_t>(stream));
 }
 
+// ---- gated feed-forward ----
+
+static bool ffn_bad_shape(const mamba_ffn_shape& s) {
+    constexpr int64_t most = (int64_t)1 << 30;
+    return s.rows < 0 || s.dim < 0 || s.hidden < 0 || s.rows > most || s.dim > most || s.hidden > most;
+}
+
+// Tiles address 256 rows of an operand with 32-bit byte offsets.
+static bool ffn_too_wide(const mamba_ffn_shape& s, int64_t xs, int64_t gs, int64_t us) {
+    constexpr int64_t most = (int64_t)1 << 21;
+    return s.dim > most || s.hidden > most / 2 || (s.rows > 1 && xs > most) || (s.hidden > 1 && (gs > most || us > most));
+}
+
+int64_t mamba_gated_ffn_workspace_bytes(const mamba_ffn_ptrs* p, const mamba_ffn_shape* s) {
+    if (!p || !s) return MAMBA_SCAN_ERR_NULL;
+    if (ffn_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
+    return s->rows * s->hidden == 0 || s->dim == 0 ? 0 : ffn_workspace(*p, *s);
+}
+
+int64_t mamba_gated_ffn_bwd_workspace_bytes(const mamba_ffn_shape* s) {
+    if (!s) return MAMBA_SCAN_ERR_NULL;
+    if (ffn_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
+    return s->rows == 0 || s->hidden == 0 || s->dim == 0 ? 0 : ffn_bwd_workspace(*s);
+}
+
+int mamba_gated_ffn_fwd(const mamba_ffn_ptrs* p, const mamba_ffn_shape* s, int act, mamba_scan_dtype dtype, void* stream) {
+    if (!p || !s) return MAMBA_SCAN_ERR_NULL;
+    if (dtype != MAMBA_SCAN_BF16) return dtype == MAMBA_SCAN_F32 ? MAMBA_SCAN_ERR_UNSUPPORTED : MAMBA_SCAN_ERR_DTYPE;
+    if (ffn_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
+    if (bad_span(s->rows, p->x_stride) || bad_span(s->hidden, p->w_gate_stride) || bad_span(s->hidden, p->w_up_stride) ||
+        bad_span(s->rows, p->h_stride))
+        return MAMBA_SCAN_ERR_SHAPE;
+    if (act != MAMBA_FFN_SILU && act != MAMBA_FFN_GELU_TANH) return MAMBA_SCAN_ERR_ARGS;
+    if ((s->rows * s->dim > 0 && !p->x) || (s->hidden * s->dim > 0 && (!p->w_gate || !p->w_up)) ||
+        (s->rows * s->hidden > 0 && !p->h))
+        return MAMBA_SCAN_ERR_NULL;
+    for (const void* q : {p->x, p->w_gate, p->w_up, (const void*)p->h})
+        if (misaligned(q, 2)) return MAMBA_SCAN_ERR_ARGS;
+    if (s->rows > 1 && p->h_stride < s->hidden) return MAMBA_SCAN_ERR_ARGS;
+    if (ffn_too_wide(*s, p->x_stride, p->w_gate_stride, p->w_up_stride)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    const int rc = check_workspace(p->workspace, p->workspace_bytes, mamba_gated_ffn_workspace_bytes(p, s));
+    if (rc != MAMBA_SCAN_OK) return rc;
+    const Bytes ins[] = {bytes_of(p->x, 2, 1, 0, s->rows, p->x_stride, s->dim),
+                         bytes_of(p->w_gate, 2, 1, 0, s->hidden, p->w_gate_stride, s->dim),
+                         bytes_of(p->w_up, 2, 1, 0, s->hidden, p->w_up_stride, s->dim),
+                         flat(p->workspace, p->workspace_bytes)};
+    const Bytes outs[] = {bytes_of(p->h, 2, 1, 0, s->rows, p->h_stride, s->hidden)};
+    if (any_overlap(ins, outs)) return MAMBA_SCAN_ERR_ARGS;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (s->rows * s->hidden == 0) return MAMBA_SCAN_OK;
+    if (s->dim == 0) return launch_ffn_zero(p->h, s->rows, s->hidden, p->h_stride, hs);
+    return launch_ffn_fwd(*p, *s, act, hs);
+}
+
+int mamba_gated_ffn_bwd(const mamba_ffn_bwd_ptrs* p, const mamba_ffn_shape* s, int act, mamba_scan_dtype dtype, void* stream) {
+    if (!p || !s) return MAMBA_SCAN_ERR_NULL;
+    if (dtype != MAMBA_SCAN_BF16) return dtype == MAMBA_SCAN_F32 ? MAMBA_SCAN_ERR_UNSUPPORTED : MAMBA_SCAN_ERR_DTYPE;
+    if (ffn_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
+    if (bad_span(s->rows, p->x_stride) || bad_span(s->hidden, p->w_gate_stride) || bad_span(s->hidden, p->w_up_stride) ||
+        bad_span(s->rows, p->dh_stride))
+        return MAMBA_SCAN_ERR_SHAPE;
+    if (act != MAMBA_FFN_SILU && act != MAMBA_FFN_GELU_TANH) return MAMBA_SCAN_ERR_ARGS;
+    if ((s->rows * s->dim > 0 && (!p->x || !p->dx)) || (s->hidden * s->dim > 0 && (!p->w_gate || !p->w_up || !p->dw_gate || !p->dw_up)) ||
+        (s->rows * s->hidden > 0 && !p->dh))
+        return MAMBA_SCAN_ERR_NULL;
+    for (const void* q : {p->x, p->w_gate, p->w_up, p->dh, (const void*)p->dx, (const void*)p->dw_gate, (const void*)p->dw_up})
+        if (misaligned(q, 2)) return MAMBA_SCAN_ERR_ARGS;
+    if (ffn_too_wide(*s, p->x_stride, p->w_gate_stride, p->w_up_stride)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    const int rc = check_workspace(p->workspace, p->workspace_bytes, mamba_gated_ffn_bwd_workspace_bytes(s));
+    if (rc != MAMBA_SCAN_OK) return rc;
+    const Bytes ins[] = {bytes_of(p->x, 2, 1, 0, s->rows, p->x_stride, s->dim),
+                         bytes_of(p->w_gate, 2, 1, 0, s->hidden, p->w_gate_stride, s->dim),
+                         bytes_of(p->w_up, 2, 1, 0, s->hidden, p->w_up_stride, s->dim),
+                         bytes_of(p->dh, 2, 1, 0, s->rows, p->dh_stride, s->hidden), flat(p->workspace, p->workspace_bytes)};
+    const Bytes outs[] = {flat(p->dx, s->rows * s->dim * 2), flat(p->dw_gate, s->hidden * s->dim * 2),
+                          flat(p->dw_up, s->hidden * s->dim * 2)};
+    if (any_overlap(ins, outs)) return MAMBA_SCAN_ERR_ARGS;
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (s->rows == 0 || s->hidden == 0 || s->dim == 0) {
+        int e = launch_ffn_zero(p->dx, s->rows, s->dim, s->dim, hs);
+        if (e == MAMBA_SCAN_OK) e = launch_ffn_zero(p->dw_gate, s->hidden, s->dim, s->dim, hs);
+        return e == MAMBA_SCAN_OK ? launch_ffn_zero(p->dw_up, s->hidden, s->dim, s->dim, hs) : e;
+    }
+    return launch_ffn_bwd(*p, *s, act, hs);
+}
+
 }  // extern "C"

@@ -32,4 +32,10 @@ int launch_embedding_bwd(const void* ids, bool ids64, const void* dy, void* dwei
                          const mamba_embedding_shape& s, float scale, bool bf16, hipStream_t stream);
 int64_t embedding_bwd_workspace(const mamba_embedding_shape& s);
 
+int launch_ffn_fwd(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s, int act, hipStream_t stream);
+int launch_ffn_bwd(const mamba_ffn_bwd_ptrs& p, const mamba_ffn_shape& s, int act, hipStream_t stream);
+int launch_ffn_zero(void* p, int64_t rows, int64_t cols, int64_t stride, hipStream_t stream);
+int64_t ffn_workspace(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s);
+int64_t ffn_bwd_workspace(const mamba_ffn_shape& s);
+
 }  // namespace mscan

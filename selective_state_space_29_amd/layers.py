@@ -1,5 +1,5 @@
 """Python binding of the layer operators' C ABI (``include/mamba_layers.h``): the gated linear
-recurrence, layer norm and the token embedding, each with its gradient.
+recurrence, layer norm, the token embedding and the gated feed-forward block, each with its gradient.
 
 As in :mod:`.scan`, every step runs in ``libmamba_scan.so``; this module checks arguments, allocates
 outputs and workspaces with torch and launches on torch's current HIP stream. There is no CPU
@@ -71,6 +71,22 @@ class EmbeddingShape(ctypes.Structure):
     _fields_ = [("tokens", _I64), ("vocab", _I64), ("dim", _I64)]
 
 
+class FfnShape(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("dim", _I64), ("hidden", _I64)]
+
+
+class FfnPtrs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("x", "w_gate", "w_up", "h")] + [
+        (n, _I64) for n in ("x_stride", "w_gate_stride", "w_up_stride", "h_stride")] + [
+        ("workspace", _P), ("workspace_bytes", _I64)]
+
+
+class FfnBwdPtrs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("x", "w_gate", "w_up", "dh", "dx", "dw_gate", "dw_up")] + [
+        (n, _I64) for n in ("x_stride", "w_gate_stride", "w_up_stride", "dh_stride")] + [
+        ("workspace", _P), ("workspace_bytes", _I64)]
+
+
 _lib = None
 
 
@@ -91,7 +107,11 @@ def _load():
             ("mamba_layer_norm_bwd_workspace_bytes", _I64, [ref(NormShape)]),
             ("mamba_embedding_fwd", _I, [_P, _I, _P, _P, ref(EmbeddingShape), _F, _I, _P]),
             ("mamba_embedding_bwd", _I, [_P, _I, _P, _P, _P, _I64, ref(EmbeddingShape), _F, _I, _P]),
-            ("mamba_embedding_bwd_workspace_bytes", _I64, [ref(EmbeddingShape)])):
+            ("mamba_embedding_bwd_workspace_bytes", _I64, [ref(EmbeddingShape)]),
+            ("mamba_gated_ffn_fwd", _I, [ref(FfnPtrs), ref(FfnShape), _I, _I, _P]),
+            ("mamba_gated_ffn_bwd", _I, [ref(FfnBwdPtrs), ref(FfnShape), _I, _I, _P]),
+            ("mamba_gated_ffn_workspace_bytes", _I64, [ref(FfnPtrs), ref(FfnShape)]),
+            ("mamba_gated_ffn_bwd_workspace_bytes", _I64, [ref(FfnShape)])):
         f = getattr(lib, name)
         f.restype, f.argtypes = restype, argtypes
     _lib = lib
@@ -516,3 +536,95 @@ class Embedding(torch.autograd.Function):
 def embedding(ids, weight, scale=1.0):
     """Differentiable :func:`embedding_fn`."""
     return Embedding.apply(ids, weight, scale) if _grad_on(weight) else embedding_fn(ids, weight, scale)
+
+
+# ---- gated feed-forward ----
+
+_ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _ffn_inputs(x, w_gate, w_up, activation, entry):
+    dtype = _dtype(x, "x")
+    _need_gpu(x, entry)
+    if activation not in _ACTS:
+        raise ValueError(f"activation must be one of {sorted(_ACTS)}, got {activation!r}")
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise ValueError("x must be (..., dim) and w_gate (hidden, dim)")
+    for name, w in (("w_gate", w_gate), ("w_up", w_up)):
+        if w.dtype is not x.dtype or w.device != x.device:
+            raise TypeError(f"{name} must have x's dtype and device")
+        if w.dim() != 2 or w.shape != w_gate.shape or w.shape[1] != x.shape[-1]:
+            raise ValueError(f"{name} must be (hidden, dim) with dim = {x.shape[-1]}, got {tuple(w.shape)}")
+    return dtype, _ACTS[activation], _rows(x, "x"), _inner(w_gate), _inner(w_up)
+
+
+def gated_ffn_fn(x, w_gate, w_up, activation="silu"):
+    """h = act(x w_gate^T) * (x w_up^T): both projections, the activation ("silu", or "gelu_tanh": gelu
+    in its tanh form) and the product in one kernel. x: (..., dim), w_gate, w_up: (hidden, dim), all
+    bfloat16; fp32 sums; returns (..., hidden) in bfloat16."""
+    lib = _load()
+    dtype, act, xr, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_fn")
+    rows, dim = xr.shape
+    hidden = wg.shape[0]
+    dev = x.device
+    h = torch.empty((*x.shape[:-1], hidden), dtype=x.dtype, device=dev)
+    shape = FfnShape(rows, dim, hidden)
+    ptrs = FfnPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu),
+                   hidden, None, 0)
+    n = lib.mamba_gated_ffn_workspace_bytes(ptrs, shape)
+    if n:
+        ws = _workspace(n, "mamba_gated_ffn_workspace_bytes", dev)
+        ptrs.workspace, ptrs.workspace_bytes = ws.data_ptr(), n
+    with _on(dev):
+        rc = lib.mamba_gated_ffn_fwd(ptrs, shape, act, dtype, _stream(dev))
+    if rc != 0:
+        _raise(rc, "mamba_gated_ffn_fwd")
+    return h
+
+
+def gated_ffn_bwd(x, w_gate, w_up, dh, activation="silu"):
+    """Gradients of :func:`gated_ffn_fn` for incoming dh (h's shape, bfloat16): a dict of x, w_gate and
+    w_up in bfloat16. Both projections are recomputed from x; the gradients of their outputs are rounded
+    to bfloat16 once, as the operands of the products."""
+    lib = _load()
+    dtype, act, xr, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_bwd")
+    rows, dim = xr.shape
+    hidden = wg.shape[0]
+    dev = x.device
+    if dh.dtype is not x.dtype or dh.device != dev:
+        raise TypeError("dh must have x's dtype and device")
+    if dh.shape != (*x.shape[:-1], hidden):
+        raise ValueError(f"dh must be {(*x.shape[:-1], hidden)}, got {tuple(dh.shape)}")
+    gr = _rows(dh, "dh")
+    out = {"x": torch.empty(x.shape, dtype=x.dtype, device=dev), "w_gate": torch.empty((hidden, dim), dtype=x.dtype, device=dev),
+           "w_up": torch.empty((hidden, dim), dtype=x.dtype, device=dev)}
+    shape = FfnShape(rows, dim, hidden)
+    n = lib.mamba_gated_ffn_bwd_workspace_bytes(shape)
+    ws = _workspace(n, "mamba_gated_ffn_bwd_workspace_bytes", dev)
+    ptrs = FfnBwdPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), gr.data_ptr(), out["x"].data_ptr(), out["w_gate"].data_ptr(),
+                      out["w_up"].data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu), _row_stride(gr), _ptr(ws), n)
+    with _on(dev):
+        rc = lib.mamba_gated_ffn_bwd(ptrs, shape, act, dtype, _stream(dev))
+    if rc != 0:
+        _raise(rc, "mamba_gated_ffn_bwd")
+    return out
+
+
+class GatedFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, activation):
+        ctx.save_for_backward(x, w_gate, w_up)
+        ctx.activation = activation
+        return gated_ffn_fn(x, w_gate, w_up, activation)
+
+    @staticmethod
+    def backward(ctx, dh):
+        g = gated_ffn_bwd(*ctx.saved_tensors, dh, ctx.activation)
+        return g["x"], g["w_gate"], g["w_up"], None
+
+
+def gated_ffn(x, w_gate, w_up, activation="silu"):
+    """Differentiable :func:`gated_ffn_fn`."""
+    if not _grad_on(x, w_gate, w_up):
+        return gated_ffn_fn(x, w_gate, w_up, activation)
+    return GatedFfn.apply(x, w_gate, w_up, activation)

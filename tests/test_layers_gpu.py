@@ -4,7 +4,7 @@ Bars, as max |g - r| / (1 + |r|): fp32 1e-4, the scan's fp32 bar. The recurrence
 below it here: a relative error of about 2^-22 a step (gates and decay, a few roundings each) over the
 at most 100 steps that decays up to 0.99 remember is 2.4e-5. Layer norm and the embedding's sums of up
 to 2^12 terms err by at most 2^12 2^-24 of their terms' magnitude. A bf16 output adds its own
-rounding, 2^-9 of it (a value next to a rounding boundary may fall to either side: 2^-8).
+rounding, at most 2^-8 of it (8 significant bits).
 """
 
 import numpy as np
