@@ -6,7 +6,7 @@ namespace mscan {
 
 namespace {
 
-constexpr int kFwdSteps = 256;  // steps per chunk of the forward, 16 runs of 16
+constexpr int kFwdSteps = 256;  // segments are whole chunks of either forward kernel, 16 runs of 16 or 8 steps
 constexpr int kStepMaxLen = 8;  // calls up to this length run the short kernel
 
 // The widest channel group that still gives every compute unit work; segments where even the
@@ -46,14 +46,14 @@ __global__ __launch_bounds__(256) void gated_dlam_kernel(const float* part, int6
 
 template <typename S, int CH, int MODE>
 void run_fwd(const GatedParams& q, hipStream_t stream) {
-    constexpr int W = CH / 4, TS = 16;  // 64 / CH sub-runs per wave: 16 runs of 16 steps
+    constexpr int TS = sizeof(S) == 2 ? 16 : 8;  // fp32 rows take twice the registers
     constexpr int share = CH * (int)sizeof(S) < 128 ? 128 / (CH * (int)sizeof(S)) : 1;
     const int nseg = MODE == kGatedPairs ? q.nseg - 1 : q.nseg;
     const int64_t grid = gated_blocks((q.dim + CH - 1) / CH, q.batch, nseg, share);
     if (q.reset)
-        hipLaunchKernelGGL((gated_fwd_kernel<S, CH, W, TS, true, MODE>), dim3((unsigned)grid), dim3(W * 64), 0, stream, q);
+        hipLaunchKernelGGL((gated_fwd_kernel<S, CH, TS, true, MODE>), dim3((unsigned)grid), dim3(CH * 16), 0, stream, q);
     else
-        hipLaunchKernelGGL((gated_fwd_kernel<S, CH, W, TS, false, MODE>), dim3((unsigned)grid), dim3(W * 64), 0, stream, q);
+        hipLaunchKernelGGL((gated_fwd_kernel<S, CH, TS, false, MODE>), dim3((unsigned)grid), dim3(CH * 16), 0, stream, q);
 }
 
 template <typename S, int MODE>
@@ -65,14 +65,14 @@ void pick_fwd(const GatedParams& q, int ch, hipStream_t stream) {
 
 template <typename S, int CH, int MODE>
 void run_bwd(const GatedBwdParams& q, hipStream_t stream) {
-    constexpr int W = CH / 4, TS = 8;
+    constexpr int TS = 8;
     constexpr int share = CH * (int)sizeof(S) < 128 ? 128 / (CH * (int)sizeof(S)) : 1;
     const int nseg = MODE == kGatedPairs ? q.nseg - 1 : q.nseg;
     const int64_t grid = gated_blocks((q.dim + CH - 1) / CH, q.batch, nseg, share);
     if (q.reset)
-        hipLaunchKernelGGL((gated_bwd_kernel<S, CH, W, TS, true, MODE>), dim3((unsigned)grid), dim3(W * 64), 0, stream, q);
+        hipLaunchKernelGGL((gated_bwd_kernel<S, CH, TS, true, MODE>), dim3((unsigned)grid), dim3(CH * 16), 0, stream, q);
     else
-        hipLaunchKernelGGL((gated_bwd_kernel<S, CH, W, TS, false, MODE>), dim3((unsigned)grid), dim3(W * 64), 0, stream, q);
+        hipLaunchKernelGGL((gated_bwd_kernel<S, CH, TS, false, MODE>), dim3((unsigned)grid), dim3(CH * 16), 0, stream, q);
 }
 
 template <typename S, int MODE>

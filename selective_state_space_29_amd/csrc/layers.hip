@@ -89,12 +89,11 @@ bool gated_bad_shape(const mamba_gated_shape& s) {
     return s.batch > 0 && s.dim > 0 && s.len > ((int64_t)1 << 48) / (s.batch * s.dim);
 }
 
-// Lanes address a row with 32-bit byte offsets, with up to 48 rows between a wave's sub-runs. Wider
-// row strides take 64-channel groups, whose waves read one row at a time.
+// Lanes address the rows of a chunk (256 steps at most) with 32-bit byte offsets.
 bool gated_wide(const mamba_gated_shape& s, const int64_t* st, int n) {
     for (int k = 0; k < n; ++k)
-        if (s.len > 1 && st[2 * k + 1] * 48 + s.dim >= ((int64_t)1 << 29)) return true;
-    return false;
+        if (s.len > 1 && st[2 * k + 1] * 64 + s.dim >= ((int64_t)1 << 28)) return true;
+    return s.dim >= (int64_t)1 << 28;
 }
 
 struct GatedLayout {
@@ -174,16 +173,15 @@ int mamba_gated_scan_fwd(const mamba_gated_ptrs* p, const mamba_gated_shape* s, 
     q.sx_b = st->x[0], q.sx_t = st->x[1], q.sr_b = st->r[0], q.sr_t = st->r[1];
     q.si_b = st->i[0], q.si_t = st->i[1], q.sy_b = st->y[0], q.sy_t = st->y[1];
     q.c = c;
-    if (s->dim >= ((int64_t)1 << 29) || rows >= ((int64_t)1 << 38)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    if (gated_wide(*s, sts, 4) || rows >= ((int64_t)1 << 38)) return MAMBA_SCAN_ERR_UNSUPPORTED;
     if (s->len == 0) {  // no step: the final state is the initial one (the short kernel's loop is empty)
         q.nseg = 1;
         return p->last_state ? launch_gated_fwd(q, GatedPlan{64, 1, 0}, dtype == MAMBA_SCAN_BF16, hs) : MAMBA_SCAN_OK;
     }
-    GatedPlan plan = gated_plan(*s, layers_cus());
+    const GatedPlan plan = gated_plan(*s, layers_cus());
     const int64_t need = gated_agg_bytes(*s, plan);
     const int rc = check_workspace(p->workspace, p->workspace_bytes, need);
     if (rc != MAMBA_SCAN_OK) return rc;
-    if (gated_wide(*s, sts, 4)) plan.ch = 64;
     q.agg = static_cast<float2*>(p->workspace);
     q.nseg = plan.nseg, q.seg_len = plan.seg_len;
     if (s->batch * ((s->dim + plan.ch - 1) / plan.ch) * plan.nseg > kMaxGrid - 64) return MAMBA_SCAN_ERR_UNSUPPORTED;
@@ -234,7 +232,7 @@ int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape*
             if (meet(outs[a], outs[b]) && !(a < 3 && interleaved(outs[a], outs[b], ost[a], ost[b], *s, es)))
                 return MAMBA_SCAN_ERR_ARGS;
     }
-    if (s->dim >= ((int64_t)1 << 29) || rows >= ((int64_t)1 << 38)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    if (gated_wide(*s, sts, 7) || rows >= ((int64_t)1 << 38)) return MAMBA_SCAN_ERR_UNSUPPORTED;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool bf16 = dtype == MAMBA_SCAN_BF16;
 
@@ -252,8 +250,7 @@ int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape*
         if (e == MAMBA_SCAN_OK && p->dh0 && rows > 0) e = launch_bwd_fill(p->dh0, p->dlast_state, rows, hs);
         return e;
     }
-    GatedPlan fplan = fplan0, bplan = bplan0;
-    if (gated_wide(*s, sts, 7)) fplan.ch = bplan.ch = 64;
+    const GatedPlan fplan = fplan0, bplan = bplan0;
     if (s->batch * ((s->dim + 15) / 16) * (int64_t)(fplan.nseg > bplan.nseg ? fplan.nseg : bplan.nseg) > kMaxGrid - 64)
         return MAMBA_SCAN_ERR_UNSUPPORTED;
     char* ws = static_cast<char*>(p->workspace);
