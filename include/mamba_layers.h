@@ -45,8 +45,10 @@ extern "C" {
  *    decoder's state updated in place). reset: (batch, len) bytes, contiguous, or NULL.
  *  - checkpoints: NULL, or (batch, ceil(len / MAMBA_GATED_CHECKPOINT), dim) fp32 that receives the
  *    state before steps 0, 128, 256, ... for the backward pass.
- *  - workspace: mamba_gated_workspace_bytes(), 256-byte aligned (0 bytes unless the sequence is split
- *    over the GPU, as for few long rows).
+ *  - workspace: mamba_gated_workspace_bytes(), 256-byte aligned (0 bytes unless several workgroups share
+ *    a row's sequence, as for few long rows: they pass the state on through it).
+ *  - Row strides up to 2^22 elements or so (64 stride + dim < 2^28), dim < 2^28, and batch * dim / 64
+ *    below 2^23; MAMBA_SCAN_ERR_UNSUPPORTED otherwise.
  *  - c must be finite and >= 0.
  */
 #define MAMBA_GATED_CHECKPOINT 128
@@ -114,8 +116,8 @@ int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape*
 
 /* Workspace bytes of the forward and of the backward (have_checkpoints: whether the call will be
  * given them), or a negative error code. They depend on the current device's compute-unit count. */
-int64_t mamba_gated_workspace_bytes(const mamba_gated_shape* s);
-int64_t mamba_gated_bwd_workspace_bytes(const mamba_gated_shape* s, int have_checkpoints);
+int64_t mamba_gated_workspace_bytes(const mamba_gated_shape* s, mamba_scan_dtype dtype);
+int64_t mamba_gated_bwd_workspace_bytes(const mamba_gated_shape* s, mamba_scan_dtype dtype, int have_checkpoints);
 
 /*
  * Layer norm over the last dimension of (rows, dim), with the residual added on the way:

@@ -3,18 +3,26 @@
 //   e_t = c log2(e) softplus(lam) sigmoid(r_t)   (= -log2 a_t)      a_t = 2^-e_t
 //   h_t = a_t h_{t-1} + b_t,   b_t = m_t sigmoid(i_t) x_t,   m_t = sqrt(1 - a_t^2)
 //
-// One lane owns one channel and a run of TS consecutive steps. A workgroup owns CH consecutive
-// channels of one batch and walks the sequence in chunks: its CH / 4 waves, of 64 / CH sub-runs each,
-// hold 16 consecutive runs, so a chunk is 16 TS steps read as rows of CH contiguous channels. Each lane
-// scans its run from a zero state and writes the run's pair (product of a, end state) to LDS; there the
-// 16 pairs of a channel are scanned by the 16 lanes of one DPP row (every thread has one pair to scan:
-// 16 CH pairs, 16 CH threads), which also carries the channel's state from chunk to chunk; each lane
-// takes back the state entering its run, and one FMA a step gives the states. Every input is read once,
-// so nothing but the inputs and outputs passes through HBM. (The alternative, one pass for the pairs of
-// all chunks and a second for the states, reads the inputs and computes the gates twice.)
+// One lane owns one channel and a run of TS consecutive steps. A workgroup owns 64 consecutive channels
+// of one batch and walks the sequence in chunks: its 16 waves hold 16 consecutive runs, so a chunk is
+// 16 TS steps read as rows of 64 contiguous channels. Each lane scans its run from a zero state and
+// writes the run's pair (product of a, end state) to LDS; there the 16 pairs of a channel are scanned by
+// the 16 lanes of one DPP row (16 x 64 pairs, 1024 threads), which also carries the channel's state from
+// chunk to chunk; each lane takes back the state entering its run, and one FMA a step gives the states.
+// Every input is read once, so nothing but the inputs and outputs passes through HBM. (The alternative,
+// one pass for the pairs of all chunks and a second for the states, reads the inputs and computes the
+// gates twice.)
 //
-// Few rows: the sequence is split into segments, one workgroup each, and a pre-pass over all but the
-// last writes the segments' pairs; a workgroup folds those of the segments before its own, in order.
+// Few rows: `ways` workgroups share a (batch, channel group). Each takes the next chunk by a ticket,
+// scans it without its state and publishes the chunk's pair; the state entering chunk 16 k + j is that
+// entering chunk 16 k, published by the one before it, carried over the published pairs of chunks 16 k ..
+// 16 k + j - 1 (the lanes of a DPP row again). Every state is composed in this one order whoever works on
+// the chunks, so the results do not depend on timing, and states pass from workgroup to workgroup only
+// every 16 chunks. (Passing every chunk's state on to the next cost 4.7 us a chunk, a store and a load
+// through memory that all XCDs see: 1855 us at 4 x 100000 x 1024 where 64 unshared workgroups take 1336.)
+// Every wait ends: of the chunks not yet done, the first is the earliest ticket of the workgroup that
+// holds it (tickets are taken in rising order, up to two ahead), so it is being worked on, and what it
+// waits for belongs to chunks before it.
 #pragma once
 
 #include <type_traits>
@@ -33,11 +41,10 @@ struct GatedParams {
     void* y;
     float* last;
     float* ck;
-    float2* agg;        // (batch, nseg, dim): the segments' pairs
+    uint64_t* chain;    // with ways > 1: GatedChain's words, zero before the launch
     int64_t batch, len, dim, nck;
     int64_t sx_b, sx_t, sr_b, sr_t, si_b, si_t, sy_b, sy_t;
-    int64_t seg_len;    // steps per segment, a multiple of the chunk and of MAMBA_GATED_CHECKPOINT
-    int nseg;
+    int ways;
     float c;
 };
 
@@ -55,16 +62,22 @@ struct GatedBwdParams {
     void* dr;
     void* di;
     float* dh0;
-    float* part;        // (batch * nseg, dim): sums of q
-    float2* agg;        // (batch, nseg, dim): the segments' adjoint pairs
+    float* dlam;
+    float* part;        // (batch, nck, dim): each chunk's sum of q
+    uint64_t* chain;
     int64_t batch, len, dim, nck;
     int64_t sx_b, sx_t, sr_b, sr_t, si_b, si_t, sdy_b, sdy_t, sdx_b, sdx_t, sdr_b, sdr_t, sdi_b, sdi_t;
-    int64_t seg_len;
-    int nseg;
+    int ways;
     float c;
 };
 
 constexpr int kGatedCk = MAMBA_GATED_CHECKPOINT;
+
+// Steps of a run of the forward. Alone on its chain a workgroup walks 128-step chunks (8 x 2048 x 1536
+// bf16: 58 us; 64 with 256 steps, where the first chunk's load and the last one's stores stand alone, and
+// 62 with 128 steps loaded two chunks ahead). Chained workgroups exchange a pair per chunk, and 256 steps
+// halve that (4 x 100000 x 1024: 1002 us, 1366 with 128); fp32 rows take twice the registers and keep 128.
+constexpr int gated_fwd_ts(int bytes, bool chain) { return bytes == 2 && chain ? 16 : 8; }
 
 __device__ __forceinline__ float sigmoid_f(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
 
@@ -121,33 +134,46 @@ __device__ __forceinline__ float decay_step(float& e, bool on) {
     return hw_exp2(-e);
 }
 
-// Which (channel group, batch, segment) a workgroup works on. Workgroups go to the 8 XCDs in turn;
-// groups of channels narrower than a 128-byte line are dealt so that the `share` groups of one line
-// run on the same XCD, whose L2 then fetches the line once.
+// A workgroup's chain (batch, channel group): the ways of one chain are 8 workgroups apart, so that they
+// run on the same XCD and the slots pass through its L2.
 struct GatedPlace {
-    int64_t group, b, seg;
+    int64_t chain, group, b;
     bool ok;
 };
-__device__ __forceinline__ GatedPlace gated_place(int64_t groups, int64_t batch, int nseg, int share) {
-    const int64_t id = blockIdx.x, slot = id >> 3;
-    const int64_t lin = ((slot / share) * 8 + (id & 7)) * share + slot % share;
+__device__ __forceinline__ GatedPlace gated_place(int64_t groups, int64_t batch, int ways) {
+    const int64_t id = blockIdx.x;
     GatedPlace p;
-    p.group = lin % groups;
-    const int64_t rest = lin / groups;
-    p.b = rest % batch;
-    p.seg = rest / batch;
-    p.ok = p.seg < nseg;
+    p.chain = id / (8 * ways) * 8 + id % 8;
+    p.ok = p.chain < groups * batch;
+    p.group = p.chain % groups;
+    p.b = p.chain / groups;
     return p;
 }
-inline int64_t gated_blocks(int64_t groups, int64_t batch, int nseg, int share) {
-    const int64_t n = groups * batch * nseg, q = 8 * share;
-    return (n + q - 1) / q * q;
-}
+inline int64_t gated_blocks(int64_t chains, int ways) { return (chains + 7) / 8 * 8 * ways; }
 
-// Rows of a chunk are addressed through a buffer descriptor at the wave's first row: the lane's offset
-// (its sub-run's first row and its channel) in a register, the row within the run in a scalar. A lane
-// without a row or channel uses an offset past the buffer, which reads 0 and drops stores, so neither
-// needs a branch.
+// What the workgroups of a chain pass on: values beside a mark that they are there.
+__device__ __forceinline__ void word_put(uint64_t* w, float v) {
+    __hip_atomic_store(w, (uint64_t)1 << 32 | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t word_look(const uint64_t* w) {
+    return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+struct GatedChain {
+    uint64_t* pairs;   // (batch, chunks, dim, 2)
+    uint64_t* states;  // (batch, chunks / 16, dim): entering chunks 16, 32, ...
+    int* tickets;      // (batch * groups)
+    static __host__ __device__ int64_t state_rows(int64_t chunks) { return (chunks + 15) / 16; }
+    static __host__ __device__ int64_t words(int64_t batch, int64_t dim, int64_t chunks) {
+        return batch * dim * (2 * chunks + state_rows(chunks)) + (batch * ((dim + 63) / 64) + 1) / 2;
+    }
+    __device__ __forceinline__ GatedChain(uint64_t* w, int64_t batch, int64_t dim, int64_t chunks)
+        : pairs(w), states(w + batch * dim * 2 * chunks),
+          tickets(reinterpret_cast<int*>(w + batch * dim * (2 * chunks + state_rows(chunks)))) {}
+};
+
+// Rows of a chunk are addressed through a buffer descriptor at the run's first row: the lane's channel in
+// a register, the row within the run in a scalar. A lane without a row or channel uses an offset past
+// the buffer, which reads 0 and drops stores, so neither needs a branch.
 constexpr uint32_t kGatedDrop = 0xFFFFFFF0u;
 template <typename P>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t gated_rsrc(P* base) {
@@ -171,23 +197,22 @@ template <typename S>
 struct Seq {
     S* base;        // of the batch
     int64_t st;     // elements between steps
-    uint32_t off;   // the lane's offset in the wave's rows, bytes
-    __device__ __forceinline__ Seq(S* p, int64_t st_, int lane_row, int64_t d)
-        : base(p), st(st_), off((uint32_t)(lane_row * (int)st_ + (int)d) * (uint32_t)sizeof(S)) {}
+    uint32_t off;   // the lane's channel, bytes
+    __device__ __forceinline__ Seq(S* p, int64_t st_, int64_t d) : base(p), st(st_), off((uint32_t)d * (uint32_t)sizeof(S)) {}
     __device__ __forceinline__ int row_bytes() const { return (int)st * (int)sizeof(S); }
 };
 
 template <typename S, int TS, bool FULL>
-__device__ __forceinline__ void gated_rows(S (&v)[TS], const Seq<const S>& q, int64_t t_wave, int left) {
-    const __amdgpu_buffer_rsrc_t r = gated_rsrc(q.base + t_wave * q.st);
+__device__ __forceinline__ void gated_rows(S (&v)[TS], const Seq<const S>& q, int64_t t_run, int left) {
+    const __amdgpu_buffer_rsrc_t r = gated_rsrc(q.base + t_run * q.st);
 #pragma unroll
     for (int k = 0; k < TS; ++k) row_load(v[k], r, FULL || k < left ? q.off : kGatedDrop, k * q.row_bytes());
 }
 
-// The reset bytes of a wave's R * TS steps as one bit each.
+// The reset bytes of a run as one bit each.
 template <int N>
-__device__ __forceinline__ uint64_t gated_reset_bits(const uint8_t* reset, int64_t t_wave, int64_t len, int lane) {
-    const int64_t t = t_wave + lane;
+__device__ __forceinline__ uint64_t gated_reset_bits(const uint8_t* reset, int64_t t_run, int64_t len, int lane) {
+    const int64_t t = t_run + lane;
     const bool on = lane < N && t < len && reset[t < len ? t : len - 1] != 0;
     return __ballot(on);
 }
@@ -213,80 +238,152 @@ __device__ __forceinline__ void row_scan(float& a, float& h) {
     step(dpp_from<shift + 8>(a, 1.0f), dpp_from<shift + 8>(h, 0.0f));
 }
 
-enum { kGatedStates = 0, kGatedPairs = 1, kGatedCkOnly = 2 };  // y and states; pairs only; checkpoints only
+// The value entering chunk `cur` of a chain's walk, in every lane of the channel's DPP row: `pair` is the
+// chunk's own, published first; `first` enters chunk 0.
+template <bool RESET>
+__device__ __forceinline__ float chain_entry(const GatedChain& c, int64_t b, int64_t D, int64_t ds, bool live, int n, int cur,
+                                             int row_lane, float2 pair, float first) {
+    if (row_lane == 15 && live) {
+        uint64_t* w = c.pairs + ((b * n + cur) * D + ds) * 2;
+        word_put(w, pair.x);
+        word_put(w + 1, pair.y);
+    }
+    const int block = cur / 16, j = cur % 16;
+    float a = 1.0f, h = 0.0f, state = first;
+    if (row_lane < j) {
+        const uint64_t* w = c.pairs + ((b * n + block * 16 + row_lane) * D + ds) * 2;
+        uint64_t va = word_look(w), vh = word_look(w + 1);
+        while (!(va >> 32 && vh >> 32)) {
+            __builtin_amdgcn_s_sleep(1);
+            va = word_look(w), vh = word_look(w + 1);
+        }
+        a = __uint_as_float((uint32_t)va);
+        h = __uint_as_float((uint32_t)vh);
+    }
+    if (block > 0) {
+        const uint64_t* w = c.states + (b * GatedChain::state_rows(n) + block) * D + ds;
+        uint64_t v = word_look(w);
+        while (!(v >> 32)) {
+            __builtin_amdgcn_s_sleep(1);
+            v = word_look(w);
+        }
+        state = __uint_as_float((uint32_t)v);
+    }
+    row_scan<true, RESET>(a, h);
+    return decay_fma<RESET>(dpp_from<kRowBcast + 15>(a, 1.0f), state, dpp_from<kRowBcast + 15>(h, 0.0f));
+}
+// The value leaving chunk `cur`, for the block of 16 chunks after it.
+__device__ __forceinline__ void chain_exit(const GatedChain& c, int64_t b, int64_t D, int64_t ds, bool live, int n, int cur,
+                                           float after) {
+    if (cur % 16 == 15 && live && cur + 1 < n) word_put(c.states + (b * GatedChain::state_rows(n) + (cur + 1) / 16) * D + ds, after);
+}
 
-constexpr int kRuns = 16;  // runs of a chunk: the lanes of a DPP row
+constexpr int kRuns = 16;   // runs of a chunk: the lanes of a DPP row
+constexpr int kChans = 64;  // channels of a workgroup: the lanes of a wave
+constexpr int kPitch = kChans + 4;  // a run's row in LDS: the 16 runs x 4 channels a wave scans lie in distinct banks
 
-// Pitch of a run's row of CH pairs in LDS: 4 more, so that the 16 runs x 4 channels a wave scans lie in
-// distinct banks.
-template <int CH>
-constexpr int kPitch = CH + 4;
+// The walk of a workgroup over the chunks of its chain, number 0 .. n - 1 in the order of the walk: all of
+// them, or those it gets tickets for. The ticket after the next is asked for at the start of a chunk and
+// passed on by the chunk's barriers.
+template <bool CHAIN>
+struct ChunkWalk {
+    int* ticket;
+    int (&lds)[2];
+    int n, cur, next, turn = 0;
+    __device__ __forceinline__ ChunkWalk(int* t, int (&l)[2], int n_) : ticket(t), lds(l), n(n_) {
+        cur = draw();
+        next = 1;
+    }
+    __device__ __forceinline__ int draw() {
+        if constexpr (!CHAIN) return 0;
+        __syncthreads();
+        if (threadIdx.x == 0) lds[0] = atomicAdd(ticket, 1);
+        __syncthreads();
+        return __builtin_amdgcn_readfirstlane(lds[0]);
+    }
+    // The second ticket, a memory round trip after the first: the chain's other workgroups have drawn
+    // their first by then, and neighbouring chunks are worked on side by side.
+    __device__ __forceinline__ void second() {
+        if constexpr (CHAIN) {
+            next = draw();
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ void ask() {  // before the chunk's first barrier
+        if constexpr (CHAIN)
+            if (threadIdx.x == 0) lds[turn] = atomicAdd(ticket, 1);
+    }
+    __device__ __forceinline__ void advance() {  // after it; lds[turn] is written again two chunks on
+        cur = next;
+        if constexpr (CHAIN) {
+            next = __builtin_amdgcn_readfirstlane(lds[turn]);
+            turn ^= 1;
+        } else {
+            ++next;
+        }
+    }
+};
 
-template <typename S, int CH, int TS, bool RESET, int MODE>
-__global__ __launch_bounds__(CH * 16) __attribute__((amdgpu_waves_per_eu(4))) void gated_fwd_kernel(GatedParams p) {
-    constexpr int R = 64 / CH, STEPS = kRuns * TS;
-    static_assert(kGatedCk % TS == 0 && R * TS <= 64);
-    __shared__ float2 s_pair[kRuns * kPitch<CH>];
-    __shared__ float s_in[kRuns * kPitch<CH>];
+template <typename S, int TS, bool RESET, bool STATES, bool CHAIN>
+__global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
+    constexpr int STEPS = kRuns * TS;
+    static_assert(kGatedCk % TS == 0);
+    __shared__ float2 s_pair[kRuns * kPitch];
+    __shared__ float s_in[kRuns * kPitch];
+    __shared__ int s_ticket[2];
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ch = lane % CH, sub = lane / CH, run = wave * R + sub;
-    const int s_run = lane & 15, s_ch = wave * 4 + (lane >> 4);  // the pair this thread scans
-    constexpr int share = CH * (int)sizeof(S) < 128 ? 128 / (CH * (int)sizeof(S)) : 1;
+    const int run = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int s_run = lane & 15, s_ch = run * 4 + (lane >> 4);  // the pair this thread scans
     const int64_t D = p.dim, L = p.len;
-    const int nseg = MODE == kGatedPairs ? p.nseg - 1 : p.nseg;
-    const GatedPlace at = gated_place((D + CH - 1) / CH, p.batch, nseg, share);
+    const GatedPlace at = gated_place((D + kChans - 1) / kChans, p.batch, p.ways);
     if (!at.ok) return;
-    const int64_t b = at.b, seg = at.seg;
-    const int64_t d_own = at.group * CH + ch, d_scan = at.group * CH + s_ch;
-    const bool live = d_own < D;
-    const int64_t d = live ? d_own : D - 1, ds = d_scan < D ? d_scan : D - 1;
-    const int64_t t_begin = seg * p.seg_len;
-    const int64_t t_end = t_begin + p.seg_len < L ? t_begin + p.seg_len : L;
+    const int64_t b = at.b;
+    const int64_t d_own = at.group * kChans + lane, d_scan = at.group * kChans + s_ch;
+    const bool live = d_own < D, s_live = d_scan < D;
+    const int64_t d = live ? d_own : D - 1, ds = s_live ? d_scan : D - 1;
 
-    const int rows = sub * TS;
-    const Seq<const S> x(static_cast<const S*>(p.x) + b * p.sx_b, p.sx_t, rows, d);
-    const Seq<const S> r(static_cast<const S*>(p.r) + b * p.sr_b, p.sr_t, rows, d);
-    const Seq<const S> i(static_cast<const S*>(p.i) + b * p.si_b, p.si_t, rows, d);
-    const Seq<S> y(static_cast<S*>(p.y) + b * p.sy_b, p.sy_t, rows, d);
+    const Seq<const S> x(static_cast<const S*>(p.x) + b * p.sx_b, p.sx_t, d);
+    const Seq<const S> r(static_cast<const S*>(p.r) + b * p.sr_b, p.sr_t, d);
+    const Seq<const S> i(static_cast<const S*>(p.i) + b * p.si_b, p.si_t, d);
+    const Seq<S> y(static_cast<S*>(p.y) + b * p.sy_b, p.sy_t, d);
     const uint8_t* reset = RESET ? p.reset + b * L : nullptr;
     const float tl = p.c * kLog2e * softplus_f(p.lam[d]);
 
-    float carry = 0.0f, carry_a = 1.0f;  // the scanned channel's state (and, for pairs, its decay so far)
-    if (MODE != kGatedPairs) {
-        carry = p.h0 ? p.h0[b * D + ds] : 0.0f;
-        for (int64_t q = 0; q < seg; ++q) {
-            const float2 v = p.agg[(b * p.nseg + q) * D + ds];
-            carry = decay_fma<RESET>(v.x, carry, v.y);
-        }
-    }
+    float carry = p.h0 ? p.h0[b * D + ds] : 0.0f;  // the scanned channel's state entering the chunk
+    const int n = (int)((L + STEPS - 1) / STEPS);
+    const GatedChain chain(p.chain, p.batch, D, n);
+    const float first = carry;
+    ChunkWalk<CHAIN> walk(chain.tickets + at.chain, s_ticket, n);
 
     S nx[TS], nr[TS], ni[TS];
     uint64_t nbits = 0;
     auto fetch_as = [&](int64_t t0, auto full) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
-        const int64_t tw = t0 + wave * R * TS;
-        const int left = (int)(t_end - tw - rows < TS ? t_end - tw - rows : TS);
-        gated_rows<S, TS, FULL>(nr, r, tw, left);
-        gated_rows<S, TS, FULL>(ni, i, tw, left);
-        gated_rows<S, TS, FULL>(nx, x, tw, left);
-        if (RESET) nbits = gated_reset_bits<R * TS>(reset, tw, L, lane);
+        const int64_t tr = t0 + run * TS;
+        const int left = (int)(L - tr < TS ? L - tr : TS);
+        gated_rows<S, TS, FULL>(nr, r, tr, left);
+        gated_rows<S, TS, FULL>(ni, i, tr, left);
+        gated_rows<S, TS, FULL>(nx, x, tr, left);
+        if (RESET) nbits = gated_reset_bits<TS>(reset, tr, L, lane);
     };
-    auto fetch = [&](int64_t t0) __attribute__((always_inline)) {
-        if (t0 + STEPS <= t_end) fetch_as(t0, std::true_type{});
+    auto fetch = [&](int chunk) __attribute__((always_inline)) {
+        const int64_t t0 = (int64_t)chunk * STEPS;
+        if (t0 + STEPS <= L) fetch_as(t0, std::true_type{});
         else fetch_as(t0, std::false_type{});
     };
-    fetch(t_begin);
-    auto chunk = [&](int64_t t0, auto tail) __attribute__((always_inline)) {
+    if (walk.cur < n) fetch(walk.cur);
+    walk.second();
+    auto chunk = [&](auto tail) __attribute__((always_inline)) {
         constexpr bool TAIL = decltype(tail)::value;
+        const int64_t t0 = (int64_t)walk.cur * STEPS, tr = t0 + run * TS;
         S cx[TS], cr[TS], ci[TS];
 #pragma unroll
         for (int k = 0; k < TS; ++k) cx[k] = nx[k], cr[k] = nr[k], ci[k] = ni[k];
-        const uint64_t bits = RESET ? nbits >> (sub * TS) : 0;
-        if (t0 + STEPS < t_end) fetch(t0 + STEPS);
-        const int64_t t_run = t0 + (int64_t)run * TS;
-        const int left = (int)(t_end - t_run < TS ? t_end - t_run : TS);  // steps of this run that exist
+        const uint64_t bits = nbits;
+        walk.ask();
+        if (walk.next < n) fetch(walk.next);
+        const int left = (int)(L - tr < TS ? L - tr : TS);  // steps of this run that exist
 
         float a[TS], bb[TS], esum = 0.0f, h = 0.0f;
 #pragma unroll
@@ -304,35 +401,34 @@ __global__ __launch_bounds__(CH * 16) __attribute__((amdgpu_waves_per_eu(4))) vo
             esum += e;
             h = decay_fma<RESET>(a[k], h, bb[k]);
         }
-        s_pair[run * kPitch<CH> + ch] = make_float2(decay_of<RESET>(esum), h);
+        s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), h);
         __syncthreads();
-        float2 v = s_pair[s_run * kPitch<CH> + s_ch];
-        row_scan<true, RESET>(v.x, v.y);
-        const float after = decay_fma<RESET>(v.x, carry, v.y);
-        s_in[s_run * kPitch<CH> + s_ch] = dpp_from<kRowShr + 1>(after, carry);
-        carry = dpp_from<kRowBcast + 15>(after, 0.0f);
-        if (MODE == kGatedPairs) carry_a = pair_product<RESET>(carry_a, dpp_from<kRowBcast + 15>(v.x, 0.0f));
-        __syncthreads();
-        float in = s_in[run * kPitch<CH> + ch];
-        if (MODE != kGatedPairs) {
-            if (p.ck && live && t_run % kGatedCk == 0 && left > 0) p.ck[(b * p.nck + t_run / kGatedCk) * D + d] = in;
+        {
+            float2 v = s_pair[s_run * kPitch + s_ch];
+            row_scan<true, RESET>(v.x, v.y);
+            if constexpr (CHAIN) carry = chain_entry<RESET>(chain, b, D, ds, s_live, n, walk.cur, s_run, v, first);
+            const float after = decay_fma<RESET>(v.x, carry, v.y);
+            if constexpr (CHAIN) chain_exit(chain, b, D, ds, s_live && s_run == 15, n, walk.cur, after);
+            s_in[s_run * kPitch + s_ch] = dpp_from<kRowShr + 1>(after, carry);
+            carry = dpp_from<kRowBcast + 15>(after, 0.0f);
         }
-        if (MODE == kGatedStates) {
-            const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + (t0 + wave * R * TS) * y.st);
+        __syncthreads();
+        float in = s_in[run * kPitch + lane];
+        if (p.ck && live && tr % kGatedCk == 0 && left > 0) p.ck[(b * p.nck + tr / kGatedCk) * D + d] = in;
+        if (STATES) {
+            const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + tr * y.st);
 #pragma unroll
             for (int k = 0; k < TS; ++k) {
                 in = decay_fma<RESET>(a[k], in, bb[k]);
                 row_store(from_f32<S>(in), o, live && (!TAIL || k < left) ? y.off : kGatedDrop, k * y.row_bytes());
             }
+            if (p.last && walk.cur == n - 1 && s_run == 15 && s_live) p.last[b * D + ds] = carry;
         }
+        walk.advance();
     };
-    int64_t t0 = t_begin;
-    for (; t0 + STEPS <= t_end; t0 += STEPS) chunk(t0, std::false_type{});
-    if (t0 < t_end) chunk(t0, std::true_type{});
-    if (s_run == 15 && d_scan < D) {
-        if (MODE == kGatedPairs) p.agg[(b * p.nseg + seg) * D + ds] = make_float2(carry_a, carry);
-        if (MODE == kGatedStates && p.last && seg == p.nseg - 1) p.last[b * D + ds] = carry;
-    }
+    const int whole = (int)(L / STEPS);
+    while (walk.cur < whole) chunk(std::false_type{});
+    if (walk.cur < n) chunk(std::true_type{});
 }
 
 // Short calls (decode): one thread per channel of a batch, step after step.
@@ -368,82 +464,88 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p) {
 // come from its checkpoint by the forward's local scan and row scan; the adjoint mu_t = a_t g_t, with
 // g_t = dy_t + mu_{t+1}, is the same recurrence from the right, mu_t = a_t mu_{t+1} + a_t dy_t, whose
 // runs have the same product of a: one exchange serves both directions. Kept per step between the scans
-// and the outputs: a, b, e, m sigmoid(i), b (1 - sigmoid(i)), (s / m) a sigmoid(i) x / s, dy.
-// MODE kGatedPairs: the adjoint pairs of whole segments (all but the first), from r and dy alone.
-template <typename S, int CH, int TS, bool RESET, int MODE>
-__global__ __launch_bounds__(CH * 16) __attribute__((amdgpu_waves_per_eu(4))) void gated_bwd_kernel(GatedBwdParams p) {
-    constexpr int R = 64 / CH, STEPS = kRuns * TS;
-    constexpr bool FULL_MODE = MODE != kGatedPairs;
-    static_assert(STEPS == kGatedCk && R * TS <= 64);
-    __shared__ float2 s_pair[kRuns * kPitch<CH>];
-    __shared__ float s_mu[kRuns * kPitch<CH>];
-    __shared__ float2 s_in[kRuns * kPitch<CH>];
+// and the outputs: a, b, e, m sigmoid(i), b (1 - sigmoid(i)), (s / m) a sigmoid(i) x / s, dy. Each
+// chunk's sum of q is written by itself (added up in order afterwards), so that it does not matter which
+// workgroup of a chain had which chunk.
+template <typename S, int TS, bool RESET, bool CHAIN>
+__global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
+    constexpr int STEPS = kRuns * TS;
+    static_assert(STEPS == kGatedCk);
+    __shared__ float2 s_pair[kRuns * kPitch];
+    __shared__ float s_mu[kRuns * kPitch];
+    __shared__ float2 s_in[kRuns * kPitch];
+    __shared__ float s_acc[kRuns * kPitch];
+    __shared__ int s_ticket[2];
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ch = lane % CH, sub = lane / CH, run = wave * R + sub;
-    const int s_run = lane & 15, s_ch = wave * 4 + (lane >> 4);
-    constexpr int share = CH * (int)sizeof(S) < 128 ? 128 / (CH * (int)sizeof(S)) : 1;
+    const int run = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int s_run = lane & 15, s_ch = run * 4 + (lane >> 4);
     const int64_t D = p.dim, L = p.len;
-    const int nseg = MODE == kGatedPairs ? p.nseg - 1 : p.nseg;
-    const GatedPlace at = gated_place((D + CH - 1) / CH, p.batch, nseg, share);
+    const GatedPlace at = gated_place((D + kChans - 1) / kChans, p.batch, p.ways);
     if (!at.ok) return;
-    const int64_t b = at.b, seg = MODE == kGatedPairs ? at.seg + 1 : at.seg;
-    const int64_t d_own = at.group * CH + ch, d_scan = at.group * CH + s_ch;
-    const bool live = d_own < D;
-    const int64_t d = live ? d_own : D - 1, ds = d_scan < D ? d_scan : D - 1;
-    const int64_t t_begin = seg * p.seg_len;
-    const int64_t t_end = t_begin + p.seg_len < L ? t_begin + p.seg_len : L;
+    const int64_t b = at.b;
+    const int64_t d_own = at.group * kChans + lane, d_scan = at.group * kChans + s_ch;
+    const bool live = d_own < D, s_live = d_scan < D;
+    const int64_t d = live ? d_own : D - 1, ds = s_live ? d_scan : D - 1;
 
-    const int rows = sub * TS;
-    const Seq<const S> x(static_cast<const S*>(p.x) + b * p.sx_b, p.sx_t, rows, d);
-    const Seq<const S> r(static_cast<const S*>(p.r) + b * p.sr_b, p.sr_t, rows, d);
-    const Seq<const S> i(static_cast<const S*>(p.i) + b * p.si_b, p.si_t, rows, d);
-    const Seq<const S> dy(static_cast<const S*>(p.dy) + b * p.sdy_b, p.sdy_t, rows, d);
-    const Seq<S> dx(static_cast<S*>(p.dx) + b * p.sdx_b, p.sdx_t, rows, d);
-    const Seq<S> dr(static_cast<S*>(p.dr) + b * p.sdr_b, p.sdr_t, rows, d);
-    const Seq<S> di(static_cast<S*>(p.di) + b * p.sdi_b, p.sdi_t, rows, d);
+    const Seq<const S> x(static_cast<const S*>(p.x) + b * p.sx_b, p.sx_t, d);
+    const Seq<const S> r(static_cast<const S*>(p.r) + b * p.sr_b, p.sr_t, d);
+    const Seq<const S> i(static_cast<const S*>(p.i) + b * p.si_b, p.si_t, d);
+    const Seq<const S> dy(static_cast<const S*>(p.dy) + b * p.sdy_b, p.sdy_t, d);
+    const Seq<S> dx(static_cast<S*>(p.dx) + b * p.sdx_b, p.sdx_t, d);
+    const Seq<S> dr(static_cast<S*>(p.dr) + b * p.sdr_b, p.sdr_t, d);
+    const Seq<S> di(static_cast<S*>(p.di) + b * p.sdi_b, p.sdi_t, d);
     const uint8_t* reset = RESET ? p.reset + b * L : nullptr;
     const float tl = p.c * kLog2e * softplus_f(p.lam[d]);
     const float inv_tl = tl > 1e-30f ? hw_rcp(tl) : 0.0f;  // sigmoid(r) = e / tl; below, every q is 0
 
-    float carry = 0.0f, carry_a = 1.0f;  // mu entering from the right, of the scanned channel
-    if (FULL_MODE) {
-        carry = p.dlast ? p.dlast[b * D + ds] : 0.0f;
-        for (int64_t q = p.nseg - 1; q > seg; --q) {
-            const float2 v = p.agg[(b * p.nseg + q) * D + ds];
-            carry = decay_fma<RESET>(v.x, carry, v.y);
-        }
-    }
-    float acc = 0.0f;
+    float carry = p.dlast ? p.dlast[b * D + ds] : 0.0f;  // mu entering the chunk from the right
+    const int n = (int)((L + STEPS - 1) / STEPS);  // chunk n - 1 - (number of the walk)
+    const GatedChain chain(p.chain, p.batch, D, n);
+    const float first = carry;
+    ChunkWalk<CHAIN> walk(chain.tickets + at.chain, s_ticket, n);
 
     S nx[TS], nr[TS], ni[TS], ng[TS];
     uint64_t nbits = 0;
     float nck = 0.0f;
-    auto fetch_as = [&](int64_t t0, auto full) __attribute__((always_inline)) {
+    auto fetch_as = [&](int chunk, auto full) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
-        const int64_t tw = t0 + wave * R * TS;
-        const int left = (int)(t_end - tw - rows < TS ? t_end - tw - rows : TS);
-        gated_rows<S, TS, FULL>(nr, r, tw, left);
-        gated_rows<S, TS, FULL>(ng, dy, tw, left);
-        if (FULL_MODE) gated_rows<S, TS, FULL>(ni, i, tw, left);
-        if (FULL_MODE) gated_rows<S, TS, FULL>(nx, x, tw, left);
-        if (RESET) nbits = gated_reset_bits<R * TS>(reset, tw, L, lane);
-        if (FULL_MODE) nck = p.ck[(b * p.nck + t0 / kGatedCk) * D + ds];
+        const int64_t tr = (int64_t)chunk * STEPS + run * TS;
+        const int left = (int)(L - tr < TS ? L - tr : TS);
+        gated_rows<S, TS, FULL>(nr, r, tr, left);
+        gated_rows<S, TS, FULL>(ng, dy, tr, left);
+        gated_rows<S, TS, FULL>(ni, i, tr, left);
+        gated_rows<S, TS, FULL>(nx, x, tr, left);
+        if (RESET) nbits = gated_reset_bits<TS>(reset, tr, L, lane);
+        nck = p.ck[(b * p.nck + chunk) * D + ds];
     };
-    const int64_t t_last = t_begin + (t_end - t_begin - 1) / STEPS * STEPS;
-    if (t_last + STEPS <= t_end) fetch_as(t_last, std::true_type{});
-    else fetch_as(t_last, std::false_type{});
-    auto chunk = [&](int64_t t0, auto tail) __attribute__((always_inline)) {
+    if (walk.cur < n) {
+        if (walk.cur > 0 || L % STEPS == 0) fetch_as(n - 1 - walk.cur, std::true_type{});
+        else fetch_as(n - 1 - walk.cur, std::false_type{});
+    }
+    walk.second();
+    int sums_of = -1;  // the chunk whose sums of q lie in s_acc
+    auto flush = [&]() __attribute__((always_inline)) {  // after a barrier; over the runs, in a fixed order
+        if (sums_of < 0) return;
+        float q = s_acc[s_run * kPitch + s_ch];
+        q += dpp_from<kRowShl + 8>(q, 0.0f);
+        q += dpp_from<kRowShl + 4>(q, 0.0f);
+        q += dpp_from<kRowShl + 2>(q, 0.0f);
+        q += dpp_from<kRowShl + 1>(q, 0.0f);
+        if (s_run == 0 && s_live) p.part[(b * p.nck + sums_of) * D + ds] = q;
+    };
+    auto chunk = [&](auto tail) __attribute__((always_inline)) {
         constexpr bool TAIL = decltype(tail)::value;
+        const int which = n - 1 - walk.cur;
+        const int64_t tr = (int64_t)which * STEPS + run * TS;
         S cx[TS], cr[TS], ci[TS], cg[TS];
 #pragma unroll
         for (int k = 0; k < TS; ++k) cx[k] = nx[k], cr[k] = nr[k], ci[k] = ni[k], cg[k] = ng[k];
-        const uint64_t bits = RESET ? nbits >> (sub * TS) : 0;
+        const uint64_t bits = nbits;
         const float ck = nck;
-        if (t0 > t_begin) fetch_as(t0 - STEPS, std::true_type{});
-        const int64_t t_run = t0 + (int64_t)run * TS;
-        const int left = (int)(t_end - t_run < TS ? t_end - t_run : TS);
+        walk.ask();
+        if (walk.next < n) fetch_as(n - 1 - walk.next, std::true_type{});  // only the walk's first chunk is cut short
+        const int left = (int)(L - tr < TS ? L - tr : TS);
 
         float e[TS], a[TS], bb[TS], ms[TS], bi[TS], z[TS], g[TS];
         float esum = 0.0f, hl = 0.0f, mu = 0.0f;
@@ -457,86 +559,74 @@ __global__ __launch_bounds__(CH * 16) __attribute__((amdgpu_waves_per_eu(4))) vo
                 if (past) a[k] = 1.0f, e[k] = g[k] = 0.0f;
             }
             esum += e[k];
-            if constexpr (FULL_MODE) {
-                const float w = one_minus_sq(e[k], a[k]);
-                const float rm = w > 1.1754944e-38f ? __builtin_amdgcn_rsqf(w) : 0.0f;  // 1 / m, or 0 with m
-                const float si = sigmoid_f(to_f32(ci[k]));
-                const float gx = past ? 0.0f : si * to_f32(cx[k]);
-                const float m = w * rm;
-                ms[k] = m * si;
-                bb[k] = m * gx;
-                bi[k] = bb[k] * (1.0f - si);
-                z[k] = gx * a[k] * rm;
-                hl = decay_fma<RESET>(a[k], hl, bb[k]);
-            }
+            const float w = one_minus_sq(e[k], a[k]);
+            const float rm = w > 1.1754944e-38f ? __builtin_amdgcn_rsqf(w) : 0.0f;  // 1 / m, or 0 with m
+            const float si = sigmoid_f(to_f32(ci[k]));
+            const float gx = past ? 0.0f : si * to_f32(cx[k]);
+            const float m = w * rm;
+            ms[k] = m * si;
+            bb[k] = m * gx;
+            bi[k] = bb[k] * (1.0f - si);
+            z[k] = gx * a[k] * rm;
+            hl = decay_fma<RESET>(a[k], hl, bb[k]);
         }
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k) mu = decay_mul<RESET>(a[k], g[k] + mu);
-        s_pair[run * kPitch<CH> + ch] = make_float2(decay_of<RESET>(esum), hl);
-        s_mu[run * kPitch<CH> + ch] = mu;
+        s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), hl);
+        s_mu[run * kPitch + lane] = mu;
         __syncthreads();
         {
-            float2 v = s_pair[s_run * kPitch<CH> + s_ch];
-            float ra = v.x, rmu = s_mu[s_run * kPitch<CH> + s_ch];
+            float2 v = s_pair[s_run * kPitch + s_ch];
+            float ra = v.x, rmu = s_mu[s_run * kPitch + s_ch];
             row_scan<false, RESET>(ra, rmu);
+            if constexpr (CHAIN)  // the chunk's adjoint pair is lane 0's, published by lane 15
+                carry = chain_entry<RESET>(chain, b, D, ds, s_live, n, walk.cur, s_run,
+                                           make_float2(dpp_from<kRowBcast + 0>(ra, 0.0f), dpp_from<kRowBcast + 0>(rmu, 0.0f)), first);
             const float after = decay_fma<RESET>(ra, carry, rmu);
+            if constexpr (CHAIN) chain_exit(chain, b, D, ds, s_live && s_run == 0, n, walk.cur, after);
             float2 o;
             o.y = dpp_from<kRowShl + 1>(after, carry);  // the adjoint entering the run from the right
             carry = dpp_from<kRowBcast + 0>(after, 0.0f);
-            if (FULL_MODE) {
-                row_scan<true, RESET>(v.x, v.y);
-                o.x = dpp_from<kRowShr + 1>(decay_fma<RESET>(v.x, ck, v.y), ck);  // the state entering it
-                s_in[s_run * kPitch<CH> + s_ch] = o;
-            } else {
-                carry_a = pair_product<RESET>(carry_a, dpp_from<kRowBcast + 0>(ra, 0.0f));
-            }
+            row_scan<true, RESET>(v.x, v.y);
+            o.x = dpp_from<kRowShr + 1>(decay_fma<RESET>(v.x, ck, v.y), ck);  // the state entering it
+            s_in[s_run * kPitch + s_ch] = o;
+            flush();
         }
         __syncthreads();
-        if (FULL_MODE) {
-            const float2 o = s_in[run * kPitch<CH> + ch];
-            float h = o.x, in = o.y;
+        const float2 o = s_in[run * kPitch + lane];
+        float in = o.y, acc = 0.0f;
+        {
+            float h = o.x;
 #pragma unroll
             for (int k = 0; k < TS; ++k) {  // z becomes z - h before the step
                 z[k] -= h;
                 h = decay_fma<RESET>(a[k], h, bb[k]);
             }
-            const int64_t tw = t0 + wave * R * TS;
-            const __amdgpu_buffer_rsrc_t ox = gated_rsrc(dx.base + tw * dx.st), oi = gated_rsrc(di.base + tw * di.st),
-                                         orr = gated_rsrc(dr.base + tw * dr.st);
-#pragma unroll
-            for (int k = TS - 1; k >= 0; --k) {
-                const bool put = live && (!TAIL || k < left);
-                const float gk = g[k] + in;
-                in = decay_mul<RESET>(a[k], gk);
-                const float ek = RESET ? __builtin_fminf(e[k], 1e30f) : e[k];
-                const float q = decay_mul<RESET>(in * (ek * kLn2), z[k]);
-                acc += !TAIL || k < left ? q : 0.0f;
-                row_store(from_f32<S>(gk * ms[k]), ox, put ? dx.off : kGatedDrop, k * dx.row_bytes());
-                row_store(from_f32<S>(gk * bi[k]), oi, put ? di.off : kGatedDrop, k * di.row_bytes());
-                row_store(from_f32<S>(decay_mul<RESET>(q, __builtin_fmaf(-ek, inv_tl, 1.0f))), orr, put ? dr.off : kGatedDrop,
-                          k * dr.row_bytes());
-            }
         }
+        const __amdgpu_buffer_rsrc_t ox = gated_rsrc(dx.base + tr * dx.st), oi = gated_rsrc(di.base + tr * di.st),
+                                     orr = gated_rsrc(dr.base + tr * dr.st);
+#pragma unroll
+        for (int k = TS - 1; k >= 0; --k) {
+            const bool put = live && (!TAIL || k < left);
+            const float gk = g[k] + in;
+            in = decay_mul<RESET>(a[k], gk);
+            const float ek = RESET ? __builtin_fminf(e[k], 1e30f) : e[k];
+            const float q = decay_mul<RESET>(in * (ek * kLn2), z[k]);
+            acc += !TAIL || k < left ? q : 0.0f;
+            row_store(from_f32<S>(gk * ms[k]), ox, put ? dx.off : kGatedDrop, k * dx.row_bytes());
+            row_store(from_f32<S>(gk * bi[k]), oi, put ? di.off : kGatedDrop, k * di.row_bytes());
+            row_store(from_f32<S>(decay_mul<RESET>(q, __builtin_fmaf(-ek, inv_tl, 1.0f))), orr, put ? dr.off : kGatedDrop,
+                      k * dr.row_bytes());
+        }
+        s_acc[run * kPitch + lane] = acc;
+        sums_of = which;
+        if (p.dh0 && walk.cur == n - 1 && s_run == 0 && s_live) p.dh0[b * D + ds] = carry;
+        walk.advance();
     };
-    int64_t t0 = t_last;
-    if (t0 + STEPS > t_end) {
-        chunk(t0, std::true_type{});
-        t0 -= STEPS;
-    }
-    for (; t0 >= t_begin; t0 -= STEPS) chunk(t0, std::false_type{});
-    if (!FULL_MODE) {
-        if (s_run == 0 && d_scan < D) p.agg[(b * p.nseg + seg) * D + ds] = make_float2(carry_a, carry);
-        return;
-    }
-    if (p.dh0 && seg == 0 && s_run == 0 && d_scan < D) p.dh0[b * D + ds] = carry;
-    // q summed over the runs, in run order
-    s_mu[run * kPitch<CH> + ch] = acc;
+    if (walk.cur == 0 && L % STEPS) chunk(std::true_type{});
+    while (walk.cur < n) chunk(std::false_type{});
     __syncthreads();
-    if (wave == 0 && sub == 0 && live) {
-        float sum = 0.0f;
-        for (int q = 0; q < kRuns; ++q) sum += s_mu[q * kPitch<CH> + ch];
-        p.part[(b * p.nseg + seg) * D + d] = sum;
-    }
+    flush();
 }
 
 }  // namespace mscan

@@ -96,24 +96,36 @@ bool gated_wide(const mamba_gated_shape& s, const int64_t* st, int n) {
     return s.dim >= (int64_t)1 << 28;
 }
 
-struct GatedLayout {
-    int64_t agg, ck, part, total;
-};
-
 int64_t gated_nck(const mamba_gated_shape& s) { return (s.len + kGatedCk - 1) / kGatedCk; }
 
-int64_t gated_agg_bytes(const mamba_gated_shape& s, const GatedPlan& p) {
-    return p.nseg > 1 ? align256(s.batch * p.nseg * s.dim * 8) : 0;
+int64_t gated_chain_bytes(const mamba_gated_shape& s, int ways, int chunk) {
+    return ways > 1 ? align256(GatedChain::words(s.batch, s.dim, (s.len + chunk - 1) / chunk) * 8) : 0;
+}
+int gated_fwd_chunk(bool bf16) { return 16 * gated_fwd_ts(bf16 ? 2 : 4, true); }
+
+// Workspace of the backward: chain storage (the checkpoint pass's and then the backward's own),
+// recomputed checkpoints, the chunks' sums of q.
+struct GatedLayout {
+    int fwd_ways, bwd_ways;
+    int64_t ck, part, total;
+};
+
+GatedLayout gated_bwd_layout(const mamba_gated_shape& s, bool bf16, bool have_ck) {
+    GatedLayout l;
+    const int cus = layers_cus();
+    l.fwd_ways = gated_fwd_ways(s, bf16, cus);
+    l.bwd_ways = gated_bwd_ways(s, cus);
+    const int64_t f = have_ck ? 0 : gated_chain_bytes(s, l.fwd_ways, gated_fwd_chunk(bf16)),
+                  b = gated_chain_bytes(s, l.bwd_ways, kGatedCk);
+    l.ck = f > b ? f : b;
+    l.part = l.ck + (have_ck ? 0 : align256(s.batch * gated_nck(s) * s.dim * 4));
+    l.total = l.part + align256(s.batch * gated_nck(s) * s.dim * 4);
+    return l;
 }
 
-GatedLayout gated_bwd_layout(const mamba_gated_shape& s, const GatedPlan& f, const GatedPlan& b, bool have_ck) {
-    GatedLayout l;
-    l.agg = 0;
-    const int64_t fa = have_ck ? 0 : gated_agg_bytes(s, f), ba = gated_agg_bytes(s, b);
-    l.ck = fa > ba ? fa : ba;  // the forward's pairs are dead before the backward's are written
-    l.part = l.ck + (have_ck ? 0 : align256(s.batch * gated_nck(s) * s.dim * 4));
-    l.total = l.part + align256(s.batch * b.nseg * s.dim * 4);
-    return l;
+// Chunks and tickets are counted in 32 bits, the launch in workgroups.
+bool gated_too_long(const mamba_gated_shape& s) {
+    return s.len > (int64_t)1 << 36 || s.batch * ((s.dim + 63) / 64) + 8 > kMaxGrid / 256;
 }
 
 }  // namespace
@@ -122,19 +134,21 @@ extern "C" {
 
 int mamba_layers_abi_version(void) { return MAMBA_LAYERS_ABI_VERSION; }
 
-int64_t mamba_gated_workspace_bytes(const mamba_gated_shape* s) {
+int64_t mamba_gated_workspace_bytes(const mamba_gated_shape* s, mamba_scan_dtype dtype) {
     if (!s) return MAMBA_SCAN_ERR_NULL;
+    if (bad_dtype(dtype)) return MAMBA_SCAN_ERR_DTYPE;
     if (gated_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
     if (s->batch * s->dim == 0 || s->len == 0) return 0;
-    return gated_agg_bytes(*s, gated_plan(*s, layers_cus()));
+    const bool bf16 = dtype == MAMBA_SCAN_BF16;
+    return gated_chain_bytes(*s, gated_fwd_ways(*s, bf16, layers_cus()), gated_fwd_chunk(bf16));
 }
 
-int64_t mamba_gated_bwd_workspace_bytes(const mamba_gated_shape* s, int have_checkpoints) {
+int64_t mamba_gated_bwd_workspace_bytes(const mamba_gated_shape* s, mamba_scan_dtype dtype, int have_checkpoints) {
     if (!s) return MAMBA_SCAN_ERR_NULL;
+    if (bad_dtype(dtype)) return MAMBA_SCAN_ERR_DTYPE;
     if (gated_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
     if (s->batch * s->dim == 0 || s->len == 0) return 0;
-    const int cus = layers_cus();
-    return gated_bwd_layout(*s, gated_plan(*s, cus), gated_bwd_plan(*s, cus), have_checkpoints != 0).total;
+    return gated_bwd_layout(*s, dtype == MAMBA_SCAN_BF16, have_checkpoints != 0).total;
 }
 
 int mamba_gated_scan_fwd(const mamba_gated_ptrs* p, const mamba_gated_shape* s, const mamba_gated_strides* st, float c,
@@ -173,19 +187,16 @@ int mamba_gated_scan_fwd(const mamba_gated_ptrs* p, const mamba_gated_shape* s, 
     q.sx_b = st->x[0], q.sx_t = st->x[1], q.sr_b = st->r[0], q.sr_t = st->r[1];
     q.si_b = st->i[0], q.si_t = st->i[1], q.sy_b = st->y[0], q.sy_t = st->y[1];
     q.c = c;
-    if (gated_wide(*s, sts, 4) || rows >= ((int64_t)1 << 38)) return MAMBA_SCAN_ERR_UNSUPPORTED;
-    if (s->len == 0) {  // no step: the final state is the initial one (the short kernel's loop is empty)
-        q.nseg = 1;
-        return p->last_state ? launch_gated_fwd(q, GatedPlan{64, 1, 0}, dtype == MAMBA_SCAN_BF16, hs) : MAMBA_SCAN_OK;
-    }
-    const GatedPlan plan = gated_plan(*s, layers_cus());
-    const int64_t need = gated_agg_bytes(*s, plan);
-    const int rc = check_workspace(p->workspace, p->workspace_bytes, need);
+    if (gated_wide(*s, sts, 4) || gated_too_long(*s)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    const bool bf16 = dtype == MAMBA_SCAN_BF16;
+    q.ways = 1;
+    if (s->len == 0)  // no step: the final state is the initial one (the short kernel's loop is empty)
+        return p->last_state ? launch_gated_fwd(q, bf16, hs) : MAMBA_SCAN_OK;
+    q.ways = gated_fwd_ways(*s, bf16, layers_cus());
+    const int rc = check_workspace(p->workspace, p->workspace_bytes, gated_chain_bytes(*s, q.ways, gated_fwd_chunk(bf16)));
     if (rc != MAMBA_SCAN_OK) return rc;
-    q.agg = static_cast<float2*>(p->workspace);
-    q.nseg = plan.nseg, q.seg_len = plan.seg_len;
-    if (s->batch * ((s->dim + plan.ch - 1) / plan.ch) * plan.nseg > kMaxGrid - 64) return MAMBA_SCAN_ERR_UNSUPPORTED;
-    return launch_gated_fwd(q, plan, dtype == MAMBA_SCAN_BF16, hs);
+    q.chain = static_cast<uint64_t*>(p->workspace);
+    return launch_gated_fwd(q, bf16, hs);
 }
 
 int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape* s, const mamba_gated_bwd_strides* st,
@@ -211,10 +222,8 @@ int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape*
         if (s->len > 1 && o[1] < s->dim) return MAMBA_SCAN_ERR_ARGS;
         if (s->batch > 1 && s->len > 0 && o[0] < (s->len - 1) * o[1] + s->dim) return MAMBA_SCAN_ERR_ARGS;
     }
-    const int cus = layers_cus();
-    const bool have_ck = p->checkpoints != nullptr;
-    const GatedPlan fplan0 = gated_plan(*s, cus), bplan0 = gated_bwd_plan(*s, cus);
-    const GatedLayout l = gated_bwd_layout(*s, fplan0, bplan0, have_ck);
+    const bool have_ck = p->checkpoints != nullptr, bf16 = dtype == MAMBA_SCAN_BF16;
+    const GatedLayout l = gated_bwd_layout(*s, bf16, have_ck);
     const int rc = check_workspace(p->workspace, p->workspace_bytes, cells > 0 ? l.total : 0);
     if (rc != MAMBA_SCAN_OK) return rc;
     auto seq = [&](const void* q, const int64_t* t) { return bytes_of(q, es, s->batch, t[0], s->len, t[1], s->dim); };
@@ -232,9 +241,8 @@ int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape*
             if (meet(outs[a], outs[b]) && !(a < 3 && interleaved(outs[a], outs[b], ost[a], ost[b], *s, es)))
                 return MAMBA_SCAN_ERR_ARGS;
     }
-    if (gated_wide(*s, sts, 7) || rows >= ((int64_t)1 << 38)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    if (gated_wide(*s, sts, 7) || gated_too_long(*s)) return MAMBA_SCAN_ERR_UNSUPPORTED;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    const bool bf16 = dtype == MAMBA_SCAN_BF16;
 
     GatedBwdParams q{};
     q.x = p->x, q.r = p->r, q.i = p->i, q.lam = p->lam, q.h0 = p->h0, q.reset = p->reset;
@@ -250,26 +258,24 @@ int mamba_gated_scan_bwd(const mamba_gated_bwd_ptrs* p, const mamba_gated_shape*
         if (e == MAMBA_SCAN_OK && p->dh0 && rows > 0) e = launch_bwd_fill(p->dh0, p->dlast_state, rows, hs);
         return e;
     }
-    const GatedPlan fplan = fplan0, bplan = bplan0;
-    if (s->batch * ((s->dim + 15) / 16) * (int64_t)(fplan.nseg > bplan.nseg ? fplan.nseg : bplan.nseg) > kMaxGrid - 64)
-        return MAMBA_SCAN_ERR_UNSUPPORTED;
     char* ws = static_cast<char*>(p->workspace);
     if (!have_ck) {
         GatedParams f{};
         f.x = p->x, f.r = p->r, f.i = p->i, f.lam = p->lam, f.h0 = p->h0, f.reset = p->reset;
         f.ck = reinterpret_cast<float*>(ws + l.ck);
-        f.agg = reinterpret_cast<float2*>(ws + l.agg);
         f.batch = s->batch, f.len = s->len, f.dim = s->dim, f.nck = q.nck;
         f.sx_b = q.sx_b, f.sx_t = q.sx_t, f.sr_b = q.sr_b, f.sr_t = q.sr_t, f.si_b = q.si_b, f.si_t = q.si_t;
-        f.c = c, f.nseg = fplan.nseg, f.seg_len = fplan.seg_len;
-        const int e = launch_gated_checkpoints(f, fplan, bf16, hs);
+        f.c = c, f.ways = l.fwd_ways;
+        f.chain = reinterpret_cast<uint64_t*>(ws);
+        const int e = launch_gated_checkpoints(f, bf16, hs);
         if (e != MAMBA_SCAN_OK) return e;
         q.ck = f.ck;
     }
-    q.agg = reinterpret_cast<float2*>(ws + l.agg);
+    q.chain = reinterpret_cast<uint64_t*>(ws);
+    q.ways = l.bwd_ways;
     q.part = reinterpret_cast<float*>(ws + l.part);
-    q.nseg = bplan.nseg, q.seg_len = bplan.seg_len;
-    return launch_gated_bwd(q, bplan, p->dlam, bf16, hs);
+    q.dlam = p->dlam;
+    return launch_gated_bwd(q, bf16, hs);
 }
 
 // ---- layer norm ----

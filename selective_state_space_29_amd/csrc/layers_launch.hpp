@@ -8,19 +8,14 @@
 
 namespace mscan {
 
-// How a gated-scan call is laid out on the GPU: channels per workgroup, sequence segments.
-struct GatedPlan {
-    int ch, nseg;
-    int64_t seg_len;
-};
-GatedPlan gated_plan(const mamba_gated_shape& s, int cus);
-GatedPlan gated_bwd_plan(const mamba_gated_shape& s, int cus);
-
 struct GatedParams;
 struct GatedBwdParams;
-int launch_gated_fwd(const GatedParams& q, const GatedPlan& plan, bool bf16, hipStream_t stream);
-int launch_gated_checkpoints(const GatedParams& q, const GatedPlan& plan, bool bf16, hipStream_t stream);
-int launch_gated_bwd(const GatedBwdParams& q, const GatedPlan& plan, float* dlam, bool bf16, hipStream_t stream);
+// workgroups per chain of 64 channels (1: no chain storage is needed)
+int gated_fwd_ways(const mamba_gated_shape& s, bool bf16, int cus);
+int gated_bwd_ways(const mamba_gated_shape& s, int cus);
+int launch_gated_fwd(const GatedParams& q, bool bf16, hipStream_t stream);
+int launch_gated_checkpoints(const GatedParams& q, bool bf16, hipStream_t stream);
+int launch_gated_bwd(const GatedBwdParams& q, bool bf16, hipStream_t stream);
 
 int launch_norm_fwd(const mamba_norm_ptrs& p, const mamba_norm_shape& s, float eps, bool bf16, hipStream_t stream);
 int launch_norm_bwd(const mamba_norm_bwd_ptrs& p, const mamba_norm_shape& s, bool bf16, hipStream_t stream);

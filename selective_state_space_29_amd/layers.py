@@ -100,8 +100,8 @@ def _load():
             ("mamba_layers_abi_version", _I, []),
             ("mamba_gated_scan_fwd", _I, [ref(GatedPtrs), ref(GatedShape), ref(GatedStrides), _F, _I, _P]),
             ("mamba_gated_scan_bwd", _I, [ref(GatedBwdPtrs), ref(GatedShape), ref(GatedBwdStrides), _F, _I, _P]),
-            ("mamba_gated_workspace_bytes", _I64, [ref(GatedShape)]),
-            ("mamba_gated_bwd_workspace_bytes", _I64, [ref(GatedShape), _I]),
+            ("mamba_gated_workspace_bytes", _I64, [ref(GatedShape), _I]),
+            ("mamba_gated_bwd_workspace_bytes", _I64, [ref(GatedShape), _I, _I]),
             ("mamba_layer_norm_fwd", _I, [ref(NormPtrs), ref(NormShape), _F, _I, _P]),
             ("mamba_layer_norm_bwd", _I, [ref(NormBwdPtrs), ref(NormShape), _I, _P]),
             ("mamba_layer_norm_bwd_workspace_bytes", _I64, [ref(NormShape)]),
@@ -257,7 +257,7 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
     if checkpoints_out is not None:
         _check_gated_checkpoints(checkpoints_out, x)
     shape = GatedShape(batch, length, dim)
-    n = lib.mamba_gated_workspace_bytes(shape)
+    n = lib.mamba_gated_workspace_bytes(shape, dtype)
     ws = _workspace(n, "mamba_gated_workspace_bytes", dev) if n else None
     ptrs = GatedPtrs(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _ptr(h0), _ptr(reset), y.data_ptr(), _ptr(last),
                      _ptr(checkpoints_out), _ptr(ws), n)
@@ -298,7 +298,7 @@ def gated_scan_bwd(x, r, i, lam, dy, *, c=8.0, h0=None, reset=None, dlast_state=
     if want_dh0:
         out["h0"] = torch.empty((batch, dim), dtype=torch.float32, device=dev)
     shape = GatedShape(batch, length, dim)
-    n = lib.mamba_gated_bwd_workspace_bytes(shape, checkpoints is not None)
+    n = lib.mamba_gated_bwd_workspace_bytes(shape, dtype, checkpoints is not None)
     ws = _workspace(n, "mamba_gated_bwd_workspace_bytes", dev)
     ptrs = GatedBwdPtrs(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _ptr(h0), _ptr(reset), dy.data_ptr(),
                         _ptr(dlast), _ptr(checkpoints), dx.data_ptr(), dr.data_ptr(), di.data_ptr(),
