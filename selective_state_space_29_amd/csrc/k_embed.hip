@@ -5,16 +5,22 @@
 // Gradient: dweight[v] = scale * sum of dy over the tokens of v. The tokens are gathered into one
 // list per id and each id's rows are added in token order, so every row of dweight is written exactly
 // once, by one wave, and the sums do not depend on timing:
-//   count    how many tokens each id has (integer atomics)
+//   count    how many tokens each id has, and each token's place among its id's (in no order: whoever
+//            adds to the count first)
 //   place    each id takes a stretch of the list (any order between ids), cut into pieces of kPiece
 //            tokens where it has more
-//   fill     tokens into their id's stretch, in any order (integer atomics)
-//   order    stretches above kPiece tokens put into token order: up to kRank tokens by counting the
+//   fill     tokens into their id's stretch
+//   order    stretches above kPiece tokens copied in token order: up to kRank tokens by counting the
 //            smaller ones, more by walking all ids in order and keeping the id's
-//   reduce   one wave an id: zeros, or the sum of its rows, sorted by the wave itself up to kPiece
-//            tokens; pieces of longer stretches give partial sums
+//   reduce   one wave an id and 64 packs of columns: the sum of its rows, sorted by the wave itself up
+//            to kPiece tokens; pieces of longer stretches give partial sums; the remaining waves write
+//            zeros for ids without tokens
 //   join     the partial sums of the long stretches, in order
+// Words are frequent unevenly, and integer atomics on one address are served one by one (1100 tokens of
+// one id among 16384 made the count 14 us, now 7), so a wave adds the tokens of an id at once.
 // The bytes that must move are dy read once and dweight written once.
+#include <type_traits>
+
 #include "layers_common.hpp"
 #include "layers_launch.hpp"
 
@@ -22,8 +28,9 @@ namespace mscan {
 
 namespace {
 
-constexpr int kPiece = 64;
+constexpr int kPiece = 64;  // of which a wave loads 16 rows at a time
 constexpr int kRank = 2048;
+constexpr int kSlice = 256;  // tokens of a long stretch that one workgroup ranks
 
 template <typename I>
 __device__ __forceinline__ int64_t id_at(const void* ids, int64_t t) {
@@ -58,18 +65,20 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const void* ids, const S
 
 // The workspace of the gradient.
 struct Lists {
-    int* count;    // (vocab) tokens of each id
-    int* start;    // (vocab) where its stretch begins
-    int* cursor;   // (vocab) places taken
-    int* list;     // (tokens) the stretches
-    int* longs;    // ids with more than kPiece tokens
+    int* totals;      // {list length, ids with up to kPiece tokens, ids with more, pieces}
+    int* count;       // (vocab) tokens of each id
+    int* start;       // (vocab) where its stretch begins
+    int* place;       // (tokens) a token's place in it
+    int* list;        // (tokens) the stretches
+    int* sorted;      // (tokens) those of the longs in token order, at the same places
+    int* shorts;      // ids with up to kPiece tokens
+    int* longs;       // ids with more
     int* long_piece;  // their first piece
     int* piece_id;    // of each piece: its id, and which of the id's pieces it is
     int* piece_at;
-    int* totals;   // {list length, longs, pieces}
-    float* part;   // (pieces, dim)
-    int64_t clear;  // ints from `count` to zero
-    int64_t max_long, max_piece, bytes;
+    float* part;      // (pieces, dim)
+    int64_t clear;    // ints from `totals` to zero
+    int64_t max_short, max_long, max_piece, bytes;
 };
 
 Lists lists_of(void* ws, const mamba_embedding_shape& s) {
@@ -81,14 +90,18 @@ Lists lists_of(void* ws, const mamba_embedding_shape& s) {
         o = align256(o + ints * 4);
         return q;
     };
-    l.max_long = s.tokens / (kPiece + 1) + 1;
-    l.max_piece = s.tokens / kPiece + l.max_long;
+    l.max_short = s.tokens < s.vocab ? s.tokens : s.vocab;
+    l.max_long = s.tokens / (kPiece + 1);
+    if (l.max_long > s.vocab) l.max_long = s.vocab;
+    l.max_piece = l.max_long > 0 ? s.tokens / kPiece + l.max_long : 0;
     l.totals = take(4);
     l.count = take(s.vocab);
-    l.cursor = take(s.vocab);
-    l.clear = o / 4;  // totals, count and cursor lie together at the start
+    l.clear = o / 4;  // totals and count lie together at the start
     l.start = take(s.vocab);
+    l.place = take(s.tokens);
     l.list = take(s.tokens);
+    l.sorted = take(l.max_long > 0 ? s.tokens : 0);
+    l.shorts = take(l.max_short);
     l.longs = take(l.max_long);
     l.long_piece = take(l.max_long);
     l.piece_id = take(l.max_piece);
@@ -102,33 +115,76 @@ __global__ __launch_bounds__(256) void zero_kernel(int* p, int64_t n) {
     for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) p[k] = 0;
 }
 
+// The lanes of a wave that hold the same id: how many, the first of them, and this lane's rank.
+struct Mates {
+    int n, first, rank;
+};
+__device__ __forceinline__ Mates mates_of(int id, bool ok, int lane) {
+    Mates m{0, lane, 0};
+    for (uint64_t todo = __ballot(ok); todo;) {
+        const int first = __builtin_ctzll(todo), want = __builtin_amdgcn_readlane(id, first);
+        const uint64_t same = __ballot(ok && id == want);
+        if (ok && id == want) m = Mates{(int)__popcll(same), first, (int)__popcll(same & (((uint64_t)1 << lane) - 1))};
+        todo &= ~same;
+    }
+    return m;
+}
+
 template <typename I>
 __global__ __launch_bounds__(256) void count_kernel(const void* ids, int64_t tokens, int64_t vocab, Lists l) {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= tokens) return;
-    const int64_t id = id_at<I>(ids, t);
-    if (id >= 0 && id < vocab) atomicAdd(&l.count[id], 1);
+    const int lane = threadIdx.x & 63;
+    const int64_t id = t < tokens ? id_at<I>(ids, t) : -1;
+    const bool ok = id >= 0 && id < vocab;
+    const Mates m = mates_of((int)id, ok, lane);
+    int base = 0;
+    if (ok && m.first == lane) base = atomicAdd(&l.count[id], m.n);
+    base = __shfl(base, m.first, 64);
+    if (ok) l.place[t] = base + m.rank;
 }
 
-__global__ __launch_bounds__(256) void place_kernel(int64_t vocab, Lists l) {
-    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int lane = threadIdx.x & 63;
-    const int n = v < vocab ? l.count[v] : 0;
-    int before = n;  // inclusive prefix sum over the wave
+// Exclusive prefix sum over a workgroup of 1024, and the total in `all`; `lds` holds 16 values of its own.
+__device__ __forceinline__ int group_prefix(int v, int* lds, int& all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int sum = v;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-        const int o = __shfl_up(before, m, 64);
-        if (lane >= m) before += o;
+        const int o = __shfl_up(sum, m, 64);
+        if (lane >= m) sum += o;
     }
-    int base = 0;
-    if (lane == 63) base = atomicAdd(&l.totals[0], before);
-    base = __shfl(base, 63, 64);
-    if (v < vocab) l.start[v] = base + before - n;
-    if (n > kPiece) {
-        const int pieces = (n + kPiece - 1) / kPiece;
-        const int at = atomicAdd(&l.totals[1], 1), first = atomicAdd(&l.totals[2], pieces);
-        l.longs[at] = (int)v;
-        l.long_piece[at] = first;
+    if (lane == 63) lds[wave] = sum;
+    __syncthreads();
+    int before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        before += w < wave ? lds[w] : 0;
+        all += lds[w];
+    }
+    return before + sum - v;
+}
+
+__global__ __launch_bounds__(1024) void place_kernel(int64_t vocab, Lists l) {
+    __shared__ int lds[4][16], base[4];
+    const int64_t v = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+    const int n = v < vocab ? l.count[v] : 0;
+    const bool few = n > 0 && n <= kPiece, many = n > kPiece;
+    const int pieces = many ? (n + kPiece - 1) / kPiece : 0;
+    int all[4];
+    const int at = group_prefix(n, lds[0], all[0]), sh = group_prefix(few, lds[1], all[1]);
+    const int lg = group_prefix(many, lds[2], all[2]), pc = group_prefix(pieces, lds[3], all[3]);
+    if (threadIdx.x < 4 && all[0] > 0) {
+        const int mine = threadIdx.x == 0 ? all[0] : threadIdx.x == 1 ? all[1] : threadIdx.x == 2 ? all[2] : all[3];
+        base[threadIdx.x] = mine ? atomicAdd(&l.totals[threadIdx.x], mine) : 0;
+    }
+    __syncthreads();
+    if (all[0] == 0 || v >= vocab) return;
+    l.start[v] = base[0] + at;
+    if (few) l.shorts[base[1] + sh] = (int)v;
+    if (many) {
+        l.longs[base[2] + lg] = (int)v;
+        const int first = base[3] + pc;
+        l.long_piece[base[2] + lg] = first;
         for (int q = 0; q < pieces; ++q) {
             l.piece_id[first + q] = (int)v;
             l.piece_at[first + q] = q;
@@ -141,113 +197,152 @@ __global__ __launch_bounds__(256) void fill_kernel(const void* ids, int64_t toke
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= tokens) return;
     const int64_t id = id_at<I>(ids, t);
-    if (id >= 0 && id < vocab) l.list[l.start[id] + atomicAdd(&l.cursor[id], 1)] = (int)t;
+    if (id >= 0 && id < vocab) l.list[l.start[id] + l.place[t]] = (int)t;
 }
 
+// blockIdx.x: long stretches in turn; blockIdx.y: slices of kSlice tokens of one.
 template <typename I>
 __global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t tokens, Lists l) {
-    __shared__ int s_tok[kRank];
-    __shared__ int s_wave[16];
+    __shared__ __align__(16) int s_tok[kRank + 16];
+    __shared__ int s_part[4][kSlice];
+    constexpr int U = 8;  // of 1024 ids walked at a time
+    __shared__ int s_hits[U][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int q = blockIdx.x; q < l.totals[1]; q += gridDim.x) {
-        const int id = l.longs[q], n = l.count[id];
-        int* list = l.list + l.start[id];
+    for (int q = blockIdx.x; q < l.totals[2]; q += gridDim.x) {
+        const int id = l.longs[q], n = l.count[id], start = l.start[id];
         if (n <= kRank) {
-            for (int k = threadIdx.x; k < n; k += 1024) s_tok[k] = list[k];
+            const int k0 = blockIdx.y * kSlice;
+            if (k0 >= n) continue;
+            for (int k = threadIdx.x; k < n + 15; k += 1024) s_tok[k] = k < n ? l.list[start + k] : 0x7fffffff;
             __syncthreads();
-            for (int k = threadIdx.x; k < n; k += 1024) {
-                const int mine = s_tok[k];
-                int rank = 0;
-                for (int j = 0; j < n; ++j) rank += s_tok[j] < mine;
-                list[rank] = mine;
+            // 4 threads count for each token of the slice, a quarter of the stretch each
+            const int k = k0 + (threadIdx.x & (kSlice - 1)), part = threadIdx.x / kSlice;
+            const int quarter = ((n + 3) / 4 + 3) / 4 * 4;
+            const int mine = k < n ? s_tok[k] : 0;
+            int rank = 0;
+#pragma unroll 4
+            for (int j = part * quarter; j < (part + 1) * quarter && j < n; j += 4) {
+                const int4 o = *reinterpret_cast<const int4*>(&s_tok[j]);
+                rank += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
             }
+            s_part[part][threadIdx.x & (kSlice - 1)] = rank;
             __syncthreads();
-        } else {
+            if (part == 0 && k < n) l.sorted[start + rank + s_part[1][threadIdx.x] + s_part[2][threadIdx.x] + s_part[3][threadIdx.x]] = mine;
+            __syncthreads();
+        } else if (blockIdx.y == 0) {
             int base = 0;
-            for (int64_t t0 = 0; t0 < tokens && base < n; t0 += 1024) {
-                const int64_t t = t0 + threadIdx.x;
-                const bool hit = t < tokens && id_at<I>(ids, t) == id;
-                const uint64_t m = __ballot(hit);
-                if (lane == 0) s_wave[wave] = __popcll(m);
-                __syncthreads();
-                int before = 0, all = 0;
-                for (int w = 0; w < 16; ++w) {
-                    before += w < wave ? s_wave[w] : 0;
-                    all += s_wave[w];
+            for (int64_t t0 = 0; t0 < tokens && base < n; t0 += 1024 * U) {
+                uint64_t hits[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t t = t0 + u * 1024 + threadIdx.x;
+                    hits[u] = __ballot(t < tokens && id_at<I>(ids, t < tokens ? t : 0) == id);
+                    if (lane == 0) s_hits[u][wave] = (int)__popcll(hits[u]);
                 }
-                if (hit) list[base + before + __popcll(m & (((uint64_t)1 << lane) - 1))] = (int)t;
-                base += all;
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    int before = 0, all = 0;
+                    for (int w = 0; w < 16; ++w) {
+                        before += w < wave ? s_hits[u][w] : 0;
+                        all += s_hits[u][w];
+                    }
+                    if (hits[u] >> lane & 1)
+                        l.sorted[start + base + before + __popcll(hits[u] & (((uint64_t)1 << lane) - 1))] =
+                            (int)(t0 + u * 1024 + threadIdx.x);
+                    base += all;
+                }
                 __syncthreads();
             }
         }
     }
 }
 
-// Rows of dweight, one wave each: waves below vocab own an id, the following ones a piece.
+// The sum of up to kPiece rows of dy at the lane's pack of columns, row k being lane k's token.
+template <typename S, int V>
+__device__ __forceinline__ void sum_rows(const S* dy, int64_t dim, int64_t c, int tok, int n, float (&s)[V]) {
+    using P = Pack<S, V>;
+    const bool in = c < dim;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.0f;
+    auto add = [&](int k, auto many) __attribute__((always_inline)) {
+        constexpr int U = decltype(many)::value;
+        P v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = __builtin_amdgcn_readlane(tok, k + u);
+            if (in) v[u] = *reinterpret_cast<const P*>(dy + t * dim + c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] += to_f32(v[u].v[j]);
+    };
+    int k = 0;
+    for (; k + 16 <= n; k += 16) add(k, std::integral_constant<int, 16>{});
+    for (; k + 4 <= n; k += 4) add(k, std::integral_constant<int, 4>{});
+    if (k + 2 <= n) {
+        add(k, std::integral_constant<int, 2>{});
+        k += 2;
+    }
+    if (k < n) add(k, std::integral_constant<int, 1>{});
+}
+
+constexpr int kZeroIds = 16;  // ids a wave looks at for rows of zeros
+
+// One wave each: the pieces, the ids with up to kPiece tokens (both for every 64 packs of columns), and
+// stretches of kZeroIds ids of which those without tokens get zeros.
 template <typename S, int V>
 __global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t vocab, int64_t dim, float scale, Lists l) {
     using P = Pack<S, V>;
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int id, n, tok = 0;
-    float* part = nullptr;
-    if (wave < vocab) {
-        id = (int)wave;
-        n = l.count[id];
-        if (n > kPiece) return;
-        if (lane < n) tok = l.list[l.start[id] + lane];
-        // into token order: each lane's rank among the wave's tokens, then the token sent there
-        int rank = lane;
-        if (n > 1) {
-            rank = 0;
-            for (int j = 0; j < n; ++j) rank += __builtin_amdgcn_readlane(tok, j) < tok;
-            if (lane >= n) rank = lane;
+    int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cols = (int)((dim + 64 * V - 1) / (64 * V));
+    const int64_t zeros = (vocab + kZeroIds - 1) / kZeroIds;
+    float s[V];
+    if (wave < l.max_piece * cols) {
+        const int64_t q = wave / cols, c = (wave - q * cols) * 64 * V + lane * V;
+        if (q >= l.totals[3]) return;
+        const int id = l.piece_id[q], from = l.piece_at[q] * kPiece;
+        const int all = l.count[id], n = all - from < kPiece ? all - from : kPiece;
+        const int tok = lane < n ? l.sorted[l.start[id] + from + lane] : 0;
+        sum_rows<S, V>(dy, dim, c, tok, n, s);
+        if (c < dim) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l.part[q * dim + c + j] = s[j];
         }
-        tok = __builtin_amdgcn_ds_permute(rank * 4, tok);
-    } else {
-        const int64_t q = wave - vocab;
-        if (q >= l.totals[2]) return;
-        id = l.piece_id[q];
-        const int from = l.piece_at[q] * kPiece;
-        n = l.count[id] - from < kPiece ? l.count[id] - from : kPiece;
-        if (lane < n) tok = l.list[l.start[id] + from + lane];
-        part = l.part + q * dim;
+        return;
     }
-    for (int64_t c = (int64_t)lane * V; c - (int64_t)lane * V < dim; c += 64 * V) {
-        const bool in = c < dim;
-        float s[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = 0.0f;
-        int k = 0;
-        for (; k + 4 <= n; k += 4) {
-            P v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t t = __builtin_amdgcn_readlane(tok, k + u);
-                if (in) v[u] = *reinterpret_cast<const P*>(dy + t * dim + c);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < V; ++j) s[j] += to_f32(v[u].v[j]);
-        }
-        for (; k < n; ++k) {
-            const int64_t t = __builtin_amdgcn_readlane(tok, k);
-            P v;
-            if (in) v = *reinterpret_cast<const P*>(dy + t * dim + c);
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] += to_f32(v.v[j]);
-        }
-        if (!in) continue;
-        if (part) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) part[c + j] = s[j];
-        } else {
+    wave -= l.max_piece * cols;
+    if (wave < zeros) {
+        const int64_t v0 = wave * kZeroIds;
+        for (uint64_t todo = __ballot(lane < kZeroIds && v0 + lane < vocab && l.count[v0 + lane < vocab ? v0 + lane : 0] == 0); todo;
+             todo &= todo - 1) {
+            const int64_t v = v0 + __builtin_ctzll(todo);
             P o;
 #pragma unroll
-            for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(s[j] * scale);
-            *reinterpret_cast<P*>(dweight + (int64_t)id * dim + c) = o;
+            for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(0.0f);
+            for (int64_t c = (int64_t)lane * V; c < dim; c += 64 * V) *reinterpret_cast<P*>(dweight + v * dim + c) = o;
         }
+        return;
+    }
+    wave -= zeros;
+    const int64_t q = wave / cols, c = (wave - q * cols) * 64 * V + lane * V;
+    if (q >= l.totals[1]) return;
+    const int id = l.shorts[q], n = l.count[id];
+    int tok = lane < n ? l.list[l.start[id] + lane] : 0;
+    // into token order: each lane's rank among the wave's tokens, then the token sent there
+    if (n > 1) {
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += __builtin_amdgcn_readlane(tok, j) < tok;
+        tok = __builtin_amdgcn_ds_permute((lane < n ? rank : lane) * 4, tok);
+    }
+    sum_rows<S, V>(dy, dim, c, tok, n, s);
+    if (c < dim) {
+        P o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(s[j] * scale);
+        *reinterpret_cast<P*>(dweight + (int64_t)id * dim + c) = o;
     }
 }
 
@@ -255,7 +350,7 @@ template <typename S>
 __global__ __launch_bounds__(256) void join_kernel(S* dweight, int64_t dim, float scale, Lists l) {
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= dim) return;
-    for (int q = blockIdx.y; q < l.totals[1]; q += gridDim.y) {
+    for (int q = blockIdx.y; q < l.totals[2]; q += gridDim.y) {
         const int id = l.longs[q], pieces = (l.count[id] + kPiece - 1) / kPiece;
         const float* part = l.part + (int64_t)l.long_piece[q] * dim + c;
         float s = 0.0f;
@@ -273,11 +368,20 @@ int fwd_go(const void* ids, const void* w, void* y, const mamba_embedding_shape&
     return launch_status();
 }
 
+// The widest pack (16 bytes and down) that rows of `dim` elements at both pointers are multiples of.
+template <typename S, int V = 16 / sizeof(S), typename F>
+int with_pack(int64_t dim, const void* a, const void* b, F&& f) {
+    if constexpr (V == 1) {
+        return f(std::integral_constant<int, 1>{});
+    } else {
+        const bool ok = dim % V == 0 && (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) % (V * sizeof(S)) == 0;
+        return ok ? f(std::integral_constant<int, V>{}) : with_pack<S, V / 2>(dim, a, b, f);
+    }
+}
+
 template <typename S, typename I>
 int fwd_typed(const void* ids, const void* w, void* y, const mamba_embedding_shape& s, float scale, hipStream_t stream) {
-    constexpr int V = 16 / sizeof(S);
-    const bool ok = s.dim % V == 0 && (reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(y)) % 16 == 0;
-    return ok ? fwd_go<S, V, I>(ids, w, y, s, scale, stream) : fwd_go<S, 1, I>(ids, w, y, s, scale, stream);
+    return with_pack<S>(s.dim, w, y, [&](auto v) { return fwd_go<S, decltype(v)::value, I>(ids, w, y, s, scale, stream); });
 }
 
 template <typename S, typename I>
@@ -287,25 +391,23 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
     auto grid = [](int64_t n, int64_t per) { return dim3((unsigned)((n + per - 1) / per)); };
     const int64_t zb = (l.clear + 255) / 256;
     hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(zb < 2048 ? zb : 2048)), dim3(256), 0, stream, l.totals, l.clear);
-    if (s.tokens > 0) hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
-    hipLaunchKernelGGL(place_kernel, grid(s.vocab, 256), dim3(256), 0, stream, s.vocab, l);
-    if (s.tokens > 0) hipLaunchKernelGGL((fill_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
-    const bool longs = s.tokens > kPiece;
-    if (longs)
-        hipLaunchKernelGGL((order_kernel<I>), dim3((unsigned)(l.max_long < 512 ? l.max_long : 512)), dim3(1024), 0, stream, ids,
-                           s.tokens, l);
-    const int64_t waves = s.vocab + (longs ? l.max_piece : 0);
-    constexpr int V = 16 / sizeof(S);
-    const bool ok = s.dim % V == 0 && (reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(dw)) % 16 == 0;
-    if (ok)
-        hipLaunchKernelGGL((reduce_kernel<S, V>), grid(waves, 4), dim3(256), 0, stream, static_cast<const S*>(dy),
+    if (s.tokens > 0) {
+        hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
+        hipLaunchKernelGGL(place_kernel, grid(s.vocab, 1024), dim3(1024), 0, stream, s.vocab, l);
+        hipLaunchKernelGGL((fill_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
+    }
+    const unsigned longs = (unsigned)(l.max_long < 512 ? l.max_long : 512);
+    if (longs) hipLaunchKernelGGL((order_kernel<I>), dim3(longs, kRank / kSlice), dim3(1024), 0, stream, ids, s.tokens, l);
+    with_pack<S>(s.dim, dy, dw, [&](auto v) {
+        const int64_t cols = (s.dim + 64 * decltype(v)::value - 1) / (64 * decltype(v)::value);
+        const int64_t waves = (l.max_piece + l.max_short) * cols + (s.vocab + kZeroIds - 1) / kZeroIds;
+        hipLaunchKernelGGL((reduce_kernel<S, decltype(v)::value>), grid(waves, 4), dim3(256), 0, stream, static_cast<const S*>(dy),
                            static_cast<S*>(dw), s.vocab, s.dim, scale, l);
-    else
-        hipLaunchKernelGGL((reduce_kernel<S, 1>), grid(waves, 4), dim3(256), 0, stream, static_cast<const S*>(dy),
-                           static_cast<S*>(dw), s.vocab, s.dim, scale, l);
+        return 0;
+    });
     if (longs)
-        hipLaunchKernelGGL((join_kernel<S>), dim3((unsigned)((s.dim + 255) / 256), (unsigned)(l.max_long < 512 ? l.max_long : 512)),
-                           dim3(256), 0, stream, static_cast<S*>(dw), s.dim, scale, l);
+        hipLaunchKernelGGL((join_kernel<S>), dim3((unsigned)((s.dim + 255) / 256), longs), dim3(256), 0, stream,
+                           static_cast<S*>(dw), s.dim, scale, l);
     return launch_status();
 }
 

@@ -9,6 +9,10 @@
 //   dx = rstd (g - mean(g) - n mean(g n)) + dresidual,   dweight = sum_rows dy n,   dbias = sum_rows dy.
 // A workgroup walks its rows and keeps the two column sums in registers; it writes one row of partial
 // sums, and a second kernel adds the workgroups' in order, so the result does not depend on timing.
+#include <initializer_list>
+#include <type_traits>
+#include <utility>
+
 #include "layers_common.hpp"
 #include "layers_launch.hpp"
 
@@ -380,43 +384,46 @@ __global__ __launch_bounds__(256) void norm_cols_kernel(const float* part, int b
     }
 }
 
-bool pack_ok(const void* p, int64_t stride, int64_t bytes, int64_t es) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0 && stride * es % bytes == 0);
-}
-
-constexpr int kFwdVals = 32;  // values of a row a lane holds, forward and backward (three sums beside them)
-constexpr int kBwdVals = 16;
-constexpr int64_t kBwdBlocks = 256;
+// Values of a row a lane holds. Few, so that many rows are in flight: at 16384 rows of 2048 bf16 with a
+// residual the forward takes 52 us with 8 a lane (four waves a row) and 82 with 32 (one wave a row); the
+// backward, which keeps two column sums and the weight beside them, 110 us forward and backward at
+// 40000 x 768 with at most 8 and 155 with 16. The widest rows take what is left of 16 waves' registers.
+constexpr int fwd_vals(int wpr) { return wpr == 16 ? 32 : 16; }
+constexpr int bwd_vals(int wpr) { return wpr == 16 ? 16 : 8; }
+constexpr int kFwdWavesPerCu = 16;  // 25.5 us at 16384 x 768; 33 with 32 (fewer rows share a wave's weights), 25.0 with 8
+constexpr int64_t kBwdBlocks = 256;  // of 16 waves; their partial column sums are written and read once more
 
 template <typename S, int V, int NV, int WPR>
 int fwd_go(const NormArgs& q, hipStream_t stream) {
     constexpr int WAVES = WPR > kFwdWaves ? WPR : kFwdWaves, RPB = WAVES / WPR;
     const int64_t need = (q.rows + RPB - 1) / RPB;
-    const int64_t most = (int64_t)layers_cus() * 32 / WAVES;  // a few rows a wave: the weights are read once for them
+    const int64_t most = (int64_t)layers_cus() * kFwdWavesPerCu / WAVES;  // a few rows a wave: the weights are read once for them
     hipLaunchKernelGGL((norm_fwd_kernel<S, V, NV, WPR>), dim3((unsigned)(need < most ? need : most)), dim3(64 * WAVES), 0, stream, q);
     return launch_status();
 }
 
+// The smallest instantiated number of packs that holds `nv` (1, 2, 3, 4, 6, 8, 12, 16, 24, 32; at most M).
+template <int M, int N = 1, typename F>
+auto with_packs(int64_t nv, F&& f) {
+    constexpr int next = N < 4 ? N + 1 : N % 3 == 0 ? N / 3 * 4 : N / 2 * 3;
+    if constexpr (next > M || N >= M) {
+        return f(std::integral_constant<int, N < M ? M : N>{});
+    } else {
+        return nv <= N ? f(std::integral_constant<int, N>{}) : with_packs<M, next>(nv, f);
+    }
+}
+
 template <typename S, int V, int WPR>
 int fwd_width(const NormArgs& q, hipStream_t stream) {
-    const int64_t nv = (q.dim + 64 * WPR * V - 1) / (64 * WPR * V);
-    constexpr int M = kFwdVals / V;  // the most packs a lane holds
-    if (nv <= 1) return fwd_go<S, V, 1, WPR>(q, stream);
-    if (nv <= 2 && M >= 2) return fwd_go<S, V, 2, WPR>(q, stream);
-    if (nv <= 3 && M >= 3) return fwd_go<S, V, 3, WPR>(q, stream);
-    if (nv <= 4 && M >= 4) return fwd_go<S, V, 4, WPR>(q, stream);
-    if constexpr (M >= 8)
-        if (nv <= 8) return fwd_go<S, V, 8, WPR>(q, stream);
-    if constexpr (M >= 16)
-        if (nv <= 16) return fwd_go<S, V, 16, WPR>(q, stream);
-    return fwd_go<S, V, M, WPR>(q, stream);
+    return with_packs<(fwd_vals(WPR) / V > 1 ? fwd_vals(WPR) / V : 1)>(
+        (q.dim + 64 * WPR * V - 1) / (64 * WPR * V), [&](auto nv) { return fwd_go<S, V, decltype(nv)::value, WPR>(q, stream); });
 }
 
 template <typename S, int V>
 int fwd_vec(const NormArgs& q, hipStream_t stream) {
-    if (q.dim <= 64 * kFwdVals) return fwd_width<S, V, 1>(q, stream);
-    if (q.dim <= 256 * kFwdVals) return fwd_width<S, V, 4>(q, stream);
-    if (q.dim <= 1024 * kFwdVals) return fwd_width<S, V, 16>(q, stream);
+    if (q.dim <= 64 * fwd_vals(1)) return fwd_width<S, V, 1>(q, stream);
+    if (q.dim <= 256 * fwd_vals(4)) return fwd_width<S, V, 4>(q, stream);
+    if (q.dim <= 1024 * fwd_vals(16)) return fwd_width<S, V, 16>(q, stream);
     hipLaunchKernelGGL((norm_fwd_wide_kernel<S>), dim3((unsigned)q.rows), dim3(1024), 0, stream, q);
     return launch_status();
 }
@@ -431,25 +438,15 @@ int64_t bwd_go(const NormBwdArgs& q, hipStream_t stream) {
 
 template <typename S, int V, int WPR>
 int64_t bwd_width(const NormBwdArgs& q, hipStream_t stream) {
-    const int64_t nv = (q.dim + 64 * WPR * V - 1) / (64 * WPR * V);
-    constexpr int M = kBwdVals / V;
-    if (nv <= 1) return bwd_go<S, V, 1, WPR>(q, stream);
-    if constexpr (M >= 4) {
-        if (nv <= 2) return bwd_go<S, V, 2, WPR>(q, stream);
-        if (nv <= 3) return bwd_go<S, V, 3, WPR>(q, stream);
-    }
-    if constexpr (M >= 16) {
-        if (nv <= 4) return bwd_go<S, V, 4, WPR>(q, stream);
-        if (nv <= 8) return bwd_go<S, V, 8, WPR>(q, stream);
-    }
-    return bwd_go<S, V, M, WPR>(q, stream);
+    return with_packs<(bwd_vals(WPR) / V > 1 ? bwd_vals(WPR) / V : 1)>(
+        (q.dim + 64 * WPR * V - 1) / (64 * WPR * V), [&](auto nv) { return bwd_go<S, V, decltype(nv)::value, WPR>(q, stream); });
 }
 
 template <typename S, int V>
 int64_t bwd_vec(const NormBwdArgs& q, hipStream_t stream) {
-    if (q.dim <= 64 * kBwdVals) return bwd_width<S, V, 1>(q, stream);
-    if (q.dim <= 256 * kBwdVals) return bwd_width<S, V, 4>(q, stream);
-    if (q.dim <= 1024 * kBwdVals) return bwd_width<S, V, 16>(q, stream);
+    if (q.dim <= 64 * bwd_vals(1)) return bwd_width<S, V, 1>(q, stream);
+    if (q.dim <= 256 * bwd_vals(4)) return bwd_width<S, V, 4>(q, stream);
+    if (q.dim <= 1024 * bwd_vals(16)) return bwd_width<S, V, 16>(q, stream);
     hipLaunchKernelGGL((norm_bwd_wide_kernel<S>), dim3((unsigned)q.rows), dim3(1024), 0, stream, q);
     if (!q.part) return 0;
     const int64_t n = q.rows < 64 ? q.rows : 64;
@@ -457,20 +454,31 @@ int64_t bwd_vec(const NormBwdArgs& q, hipStream_t stream) {
     return n;
 }
 
+// The widest pack (16 bytes and down) that the width, pointers and row strides are multiples of, and that
+// leaves less than half of a wave idle over the width (200000 x 100 bf16: 141 us with packs of 4, on 25
+// lanes, 113 with single elements).
+template <typename S, int V = 16 / sizeof(S), typename F>
+auto with_pack(int64_t dim, std::initializer_list<std::pair<const void*, int64_t>> rows, F&& f) {
+    if constexpr (V == 1) {
+        return f(std::integral_constant<int, 1>{});
+    } else {
+        bool ok = dim % V == 0 && dim > 32 * V;
+        for (const auto& r : rows)
+            ok = ok && (!r.first || (reinterpret_cast<uintptr_t>(r.first) % (V * sizeof(S)) == 0 && r.second % V == 0));
+        return ok ? f(std::integral_constant<int, V>{}) : with_pack<S, V / 2>(dim, rows, f);
+    }
+}
+
 template <typename S>
 int fwd_typed(const NormArgs& q, hipStream_t stream) {
-    constexpr int V = 16 / sizeof(S), es = sizeof(S);
-    const bool ok = q.dim % V == 0 && pack_ok(q.x, q.sx, 16, es) && pack_ok(q.res, q.sres, 16, es) &&
-                    pack_ok(q.y, q.sy, 16, es) && pack_ok(q.sum, q.ssum, 16, es);
-    return ok ? fwd_vec<S, V>(q, stream) : fwd_vec<S, 1>(q, stream);
+    return with_pack<S>(q.dim, {{q.x, q.sx}, {q.res, q.sres}, {q.y, q.sy}, {q.sum, q.ssum}},
+                        [&](auto v) { return fwd_vec<S, decltype(v)::value>(q, stream); });
 }
 
 template <typename S>
 int64_t bwd_typed(const NormBwdArgs& q, hipStream_t stream) {
-    constexpr int V = 16 / sizeof(S), es = sizeof(S);
-    const bool ok = q.dim % V == 0 && pack_ok(q.t, q.st, 16, es) && pack_ok(q.dy, q.sdy, 16, es) &&
-                    pack_ok(q.dres, q.sdres, 16, es) && pack_ok(q.dx, q.sdx, 16, es);
-    return ok ? bwd_vec<S, V>(q, stream) : bwd_vec<S, 1>(q, stream);
+    return with_pack<S>(q.dim, {{q.t, q.st}, {q.dy, q.sdy}, {q.dres, q.sdres}, {q.dx, q.sdx}},
+                        [&](auto v) { return bwd_vec<S, decltype(v)::value>(q, stream); });
 }
 
 }  // namespace

@@ -31,11 +31,20 @@ struct __align__(V * sizeof(S)) Pack {
     S v[V];
 };
 
-// Sum over the 64 lanes of a wave, the same bits in every lane.
+// Sum over the 64 lanes of a wave, the same bits in every lane: prefix sums of the 16-lane rows (DPP
+// row_shr), then of the rows (row_bcast), and lane 63's total to all.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
+    v = dpp_add<0x111, 0xf>(v);
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);  // rows 1 and 3 take the row before's total
+    v = dpp_add<0x143, 0xc>(v);  // rows 2 and 3 take the first half's
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 inline int launch_status() { return hipGetLastError() == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_LAUNCH; }
