@@ -12,13 +12,15 @@
 //   fill     tokens into their id's stretch
 //   order    stretches above kPiece tokens copied in token order: up to kRank tokens by counting the
 //            smaller ones, more by walking all ids in order and keeping the id's
+//            (other workgroups of this launch write zeros for ids without tokens)
 //   reduce   one wave an id and 64 packs of columns: the sum of its rows, sorted by the wave itself up
-//            to kPiece tokens; pieces of longer stretches give partial sums; the remaining waves write
-//            zeros for ids without tokens
+//            to kPiece tokens; pieces of longer stretches give partial sums
 //   join     the partial sums of the long stretches, in order
 // Words are frequent unevenly, and integer atomics on one address are served one by one (1100 tokens of
 // one id among 16384 made the count 14 us, now 7), so a wave adds the tokens of an id at once.
-// The bytes that must move are dy read once and dweight written once.
+// The bytes that must move are dy read once and dweight written once: 102 MB, 22 us at the rate of a large
+// copy, at 16384 tokens (a quarter of them padding), 50000 x 768 bf16. Measured there: 48 us in seven
+// launches, of which zeros and order 15, reduce 11, count 8; the plain index_add form takes 295.
 #include <type_traits>
 
 #include "layers_common.hpp"
@@ -28,7 +30,8 @@ namespace mscan {
 
 namespace {
 
-constexpr int kPiece = 64;  // of which a wave loads 16 rows at a time
+constexpr int kPiece = 64;
+constexpr int kBatch = 8;   // rows a wave loads at a time (16: 13.0 against 13.1 us at 16384 tokens, and more registers)
 constexpr int kRank = 2048;
 constexpr int kSlice = 256;  // tokens of a long stretch that one workgroup ranks
 
@@ -200,18 +203,45 @@ __global__ __launch_bounds__(256) void fill_kernel(const void* ids, int64_t toke
     if (id >= 0 && id < vocab) l.list[l.start[id] + l.place[t]] = (int)t;
 }
 
-// blockIdx.x: long stretches in turn; blockIdx.y: slices of kSlice tokens of one.
+constexpr int kZeroIds = 64;  // ids a workgroup looks at for rows of zeros
+
+// Rows of zeros for the ids without tokens among kZeroIds.
+__device__ __forceinline__ void zero_rows(char* dweight, int64_t row_bytes, int64_t v0, int64_t vocab, const int* count) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int k = wave; k < kZeroIds; k += 16) {
+        const int64_t v = v0 + k;
+        if (v >= vocab || count[v] != 0) continue;
+        char* row = dweight + v * row_bytes;
+        if (row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(row) % 16 == 0) {
+            for (int64_t c = lane * 16; c < row_bytes; c += 64 * 16) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+        } else if (reinterpret_cast<uintptr_t>(row) % 4 == 0 && row_bytes % 4 == 0) {
+            for (int64_t c = lane * 4; c < row_bytes; c += 64 * 4) *reinterpret_cast<uint32_t*>(row + c) = 0;
+        } else {
+            for (int64_t c = lane * 2; c < row_bytes; c += 64 * 2) *reinterpret_cast<uint16_t*>(row + c) = 0;
+        }
+    }
+}
+
+// The first `order` workgroups put long stretches into order, slice by slice; the others write the rows of
+// ids without tokens, which fill the memory system meanwhile.
 template <typename I>
-__global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t tokens, Lists l) {
+__global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t tokens, Lists l, int order, char* dweight,
+                                                     int64_t row_bytes, int64_t vocab) {
     __shared__ __align__(16) int s_tok[kRank + 16];
     __shared__ int s_part[4][kSlice];
     constexpr int U = 8;  // of 1024 ids walked at a time
     __shared__ int s_hits[U][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int q = blockIdx.x; q < l.totals[2]; q += gridDim.x) {
+    constexpr int slices = kRank / kSlice;
+    if ((int)blockIdx.x >= order) {
+        zero_rows(dweight, row_bytes, (int64_t)(blockIdx.x - order) * kZeroIds, vocab, l.count);
+        return;
+    }
+    const int slice = blockIdx.x % slices;
+    for (int q = blockIdx.x / slices; q < l.totals[2]; q += order / slices) {
         const int id = l.longs[q], n = l.count[id], start = l.start[id];
         if (n <= kRank) {
-            const int k0 = blockIdx.y * kSlice;
+            const int k0 = slice * kSlice;
             if (k0 >= n) continue;
             for (int k = threadIdx.x; k < n + 15; k += 1024) s_tok[k] = k < n ? l.list[start + k] : 0x7fffffff;
             __syncthreads();
@@ -229,7 +259,7 @@ __global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t to
             __syncthreads();
             if (part == 0 && k < n) l.sorted[start + rank + s_part[1][threadIdx.x] + s_part[2][threadIdx.x] + s_part[3][threadIdx.x]] = mine;
             __syncthreads();
-        } else if (blockIdx.y == 0) {
+        } else if (slice == 0) {
             int base = 0;
             for (int64_t t0 = 0; t0 < tokens && base < n; t0 += 1024 * U) {
                 uint64_t hits[U];
@@ -262,87 +292,62 @@ __global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t to
 template <typename S, int V>
 __device__ __forceinline__ void sum_rows(const S* dy, int64_t dim, int64_t c, int tok, int n, float (&s)[V]) {
     using P = Pack<S, V>;
-    const bool in = c < dim;
+    const S* at = dy + (c < dim ? c : 0);  // lanes past the row read its beginning: no branch around the loads
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] = 0.0f;
-    auto add = [&](int k, auto many) __attribute__((always_inline)) {
+    // rows k .. k + U - 1, of which the first `left` count (the others repeat the last one)
+    auto add = [&](int k, int left, auto many) __attribute__((always_inline)) {
         constexpr int U = decltype(many)::value;
         P v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t t = __builtin_amdgcn_readlane(tok, k + u);
-            if (in) v[u] = *reinterpret_cast<const P*>(dy + t * dim + c);
+            const int64_t t = __builtin_amdgcn_readlane(tok, u < left ? k + u : k + left - 1);
+            v[u] = *reinterpret_cast<const P*>(at + t * dim);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[j] += to_f32(v[u].v[j]);
+            for (int j = 0; j < V; ++j) s[j] += u < left ? to_f32(v[u].v[j]) : 0.0f;
     };
     int k = 0;
-    for (; k + 16 <= n; k += 16) add(k, std::integral_constant<int, 16>{});
-    for (; k + 4 <= n; k += 4) add(k, std::integral_constant<int, 4>{});
-    if (k + 2 <= n) {
-        add(k, std::integral_constant<int, 2>{});
-        k += 2;
-    }
-    if (k < n) add(k, std::integral_constant<int, 1>{});
+    for (; k + kBatch <= n; k += kBatch) add(k, kBatch, std::integral_constant<int, kBatch>{});
+    if (n - k > 4) add(k, n - k, std::integral_constant<int, kBatch>{});
+    else if (n - k > 1) add(k, n - k, std::integral_constant<int, 4>{});
+    else if (n - k == 1) add(k, 1, std::integral_constant<int, 1>{});
 }
 
-constexpr int kZeroIds = 16;  // ids a wave looks at for rows of zeros
-
-// One wave each: the pieces, the ids with up to kPiece tokens (both for every 64 packs of columns), and
-// stretches of kZeroIds ids of which those without tokens get zeros.
+// The pieces and the ids with up to kPiece tokens, a wave for every 64 packs of columns of each, in turns.
 template <typename S, int V>
-__global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t vocab, int64_t dim, float scale, Lists l) {
+__global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l) {
     using P = Pack<S, V>;
     const int lane = threadIdx.x & 63;
-    int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = (int)((dim + 64 * V - 1) / (64 * V));
-    const int64_t zeros = (vocab + kZeroIds - 1) / kZeroIds;
-    float s[V];
-    if (wave < l.max_piece * cols) {
-        const int64_t q = wave / cols, c = (wave - q * cols) * 64 * V + lane * V;
-        if (q >= l.totals[3]) return;
-        const int id = l.piece_id[q], from = l.piece_at[q] * kPiece;
-        const int all = l.count[id], n = all - from < kPiece ? all - from : kPiece;
-        const int tok = lane < n ? l.sorted[l.start[id] + from + lane] : 0;
+    const int pieces = l.totals[3], shorts = l.totals[1];
+    const int64_t items = (int64_t)(pieces + shorts) * cols, step = (int64_t)gridDim.x * 4;
+    for (int64_t k = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); k < items; k += step) {
+        const int64_t q = k / cols, c = (k - q * cols) * 64 * V + lane * V;
+        const bool whole = q >= pieces;  // of an id's tokens
+        const int id = __builtin_amdgcn_readfirstlane(whole ? l.shorts[q - pieces] : l.piece_id[q]);
+        const int from = whole ? 0 : __builtin_amdgcn_readfirstlane(l.piece_at[q]) * kPiece;
+        const int left = __builtin_amdgcn_readfirstlane(l.count[id]) - from, n = left < kPiece ? left : kPiece;
+        int tok = lane < n ? (whole ? l.list : l.sorted)[l.start[id] + from + lane] : 0;
+        if (whole && n > 1) {  // into token order: each lane's rank among the wave's tokens, then the token sent there
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += __builtin_amdgcn_readlane(tok, j) < tok;
+            tok = __builtin_amdgcn_ds_permute((lane < n ? rank : lane) * 4, tok);
+        }
+        float s[V];
         sum_rows<S, V>(dy, dim, c, tok, n, s);
-        if (c < dim) {
+        if (c >= dim) continue;
+        if (whole) {
+            P o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(s[j] * scale);
+            *reinterpret_cast<P*>(dweight + (int64_t)id * dim + c) = o;
+        } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) l.part[q * dim + c + j] = s[j];
         }
-        return;
-    }
-    wave -= l.max_piece * cols;
-    if (wave < zeros) {
-        const int64_t v0 = wave * kZeroIds;
-        for (uint64_t todo = __ballot(lane < kZeroIds && v0 + lane < vocab && l.count[v0 + lane < vocab ? v0 + lane : 0] == 0); todo;
-             todo &= todo - 1) {
-            const int64_t v = v0 + __builtin_ctzll(todo);
-            P o;
-#pragma unroll
-            for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(0.0f);
-            for (int64_t c = (int64_t)lane * V; c < dim; c += 64 * V) *reinterpret_cast<P*>(dweight + v * dim + c) = o;
-        }
-        return;
-    }
-    wave -= zeros;
-    const int64_t q = wave / cols, c = (wave - q * cols) * 64 * V + lane * V;
-    if (q >= l.totals[1]) return;
-    const int id = l.shorts[q], n = l.count[id];
-    int tok = lane < n ? l.list[l.start[id] + lane] : 0;
-    // into token order: each lane's rank among the wave's tokens, then the token sent there
-    if (n > 1) {
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += __builtin_amdgcn_readlane(tok, j) < tok;
-        tok = __builtin_amdgcn_ds_permute((lane < n ? rank : lane) * 4, tok);
-    }
-    sum_rows<S, V>(dy, dim, c, tok, n, s);
-    if (c < dim) {
-        P o;
-#pragma unroll
-        for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(s[j] * scale);
-        *reinterpret_cast<P*>(dweight + (int64_t)id * dim + c) = o;
     }
 }
 
@@ -397,12 +402,15 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
         hipLaunchKernelGGL((fill_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
     }
     const unsigned longs = (unsigned)(l.max_long < 512 ? l.max_long : 512);
-    if (longs) hipLaunchKernelGGL((order_kernel<I>), dim3(longs, kRank / kSlice), dim3(1024), 0, stream, ids, s.tokens, l);
+    const unsigned order = longs * (kRank / kSlice);
+    hipLaunchKernelGGL((order_kernel<I>), dim3(order + (unsigned)((s.vocab + kZeroIds - 1) / kZeroIds)), dim3(1024), 0, stream,
+                       ids, s.tokens, l, (int)order, static_cast<char*>(dw), s.dim * (int64_t)sizeof(S), s.vocab);
     with_pack<S>(s.dim, dy, dw, [&](auto v) {
         const int64_t cols = (s.dim + 64 * decltype(v)::value - 1) / (64 * decltype(v)::value);
-        const int64_t waves = (l.max_piece + l.max_short) * cols + (s.vocab + kZeroIds - 1) / kZeroIds;
-        hipLaunchKernelGGL((reduce_kernel<S, decltype(v)::value>), grid(waves, 4), dim3(256), 0, stream, static_cast<const S*>(dy),
-                           static_cast<S*>(dw), s.vocab, s.dim, scale, l);
+        const int64_t waves = (l.max_piece + l.max_short) * cols, most = (int64_t)layers_cus() * 64;
+        if (waves == 0) return 0;
+        hipLaunchKernelGGL((reduce_kernel<S, decltype(v)::value>), grid(waves < most ? waves : most, 4), dim3(256), 0, stream, static_cast<const S*>(dy),
+                           static_cast<S*>(dw), s.dim, scale, l);
         return 0;
     });
     if (longs)
