@@ -39,8 +39,13 @@ class GatedPtrs(ctypes.Structure):
                                   "workspace")] + [("workspace_bytes", _I64)]
 
 
+def _strides(*names):
+    """The {batch, len} strides of the named tensors, one field each (an array field costs 0.5 us more)."""
+    return [(f"{n}_{k}", _I64) for n in names for k in ("batch", "len")]
+
+
 class GatedStrides(ctypes.Structure):
-    _fields_ = [(n, _I64 * 2) for n in ("x", "r", "i", "y")]
+    _fields_ = _strides("x", "r", "i", "y")
 
 
 class GatedBwdPtrs(ctypes.Structure):
@@ -49,7 +54,7 @@ class GatedBwdPtrs(ctypes.Structure):
 
 
 class GatedBwdStrides(ctypes.Structure):
-    _fields_ = [(n, _I64 * 2) for n in ("x", "r", "i", "dy", "dx", "dr", "di")]
+    _fields_ = _strides("x", "r", "i", "dy", "dx", "dr", "di")
 
 
 class NormShape(ctypes.Structure):
@@ -133,32 +138,36 @@ def _need_gpu(x, entry):
         raise ValueError(f"{entry} runs on the GPU only: inputs must be device tensors")
 
 
-class _on:
-    """The device of a call made current for its launch (only where it is not)."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, dev):
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+# The handle of a device's current stream: torch's own getter where it has one (0.1 us), else by way of
+# a Stream object (2 us of the 12 that a decode step's call may take).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+def _launch(entry, x, f, *args):
+    """Call a library entry on x's device and its current stream; raise what it refuses."""
+    dev = x.get_device()
+    if torch.cuda.current_device() == dev:
+        rc = f(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, _raw_stream(dev))
+    if rc != 0:
+        _raise(rc, entry)
 
 
-def _f32(x, name, shape, dev):
+def _on_device(x, f, *args):
+    """A size query that depends on the device it is asked for."""
+    if torch.cuda.current_device() == x.get_device():
+        return f(*args)
+    with torch.cuda.device(x.get_device()):
+        return f(*args)
+
+
+def _f32(x, name, shape, like):
     """A parameter or state in fp32, contiguous, of the given shape (or None)."""
     if x is None:
         return None
-    if x.device != dev:
+    if x.get_device() != like.get_device():
         raise ValueError(f"{name} must be on the device of the activations")
     if x.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(x.shape)}")
@@ -171,18 +180,18 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
-def _workspace(n, entry, dev):
+def _workspace(n, entry, like):
     if n < 0:
         _raise(int(n), entry)
-    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
 def _same(x, like, name):
-    if x.dtype is not like.dtype or x.device != like.device:
+    if x.dtype is not like.dtype or x.get_device() != like.get_device():
         raise TypeError(f"{name} must have x's dtype and device")
     if x.shape != like.shape:
         raise ValueError(f"{name} must have x's shape {tuple(like.shape)}, got {tuple(x.shape)}")
-    return _inner(x)
+    return x
 
 
 def _inner(x):
@@ -196,12 +205,12 @@ def gated_checkpoint_shape(batch, length, dim):
     return (batch, -(-length // GATED_CHECKPOINT), dim)
 
 
-def _reset(reset, batch, length, dev):
+def _reset(reset, batch, length, like):
     if reset is None:
         return None
     if reset.dtype not in (torch.bool, torch.uint8):
         raise TypeError(f"reset must be bool or uint8, got {reset.dtype}")
-    if reset.shape != (batch, length) or reset.device != dev:
+    if reset.shape != (batch, length) or reset.get_device() != like.get_device():
         raise ValueError(f"reset must be (batch, len) = {(batch, length)} on x's device")
     return reset if reset.is_contiguous() else reset.contiguous()
 
@@ -212,14 +221,21 @@ def _gated_inputs(x, r, i, lam, h0, reset, entry):
     if x.dim() != 3:
         raise ValueError(f"x must be (batch, len, dim), got {tuple(x.shape)}")
     batch, length, dim = x.shape
-    dev = x.device
-    return (dtype, _inner(x), _same(r, x, "r"), _same(i, x, "i"), _f32(lam, "lam", (dim,), dev),
-            _f32(h0, "h0", (batch, dim), dev), _reset(reset, batch, length, dev))
+    return (dtype, x, _same(r, x, "r"), _same(i, x, "i"), _f32(lam, "lam", (dim,), x), _f32(h0, "h0", (batch, dim), x),
+            _reset(reset, batch, length, x))
 
 
-def _bt(x):
-    s = x.stride()
-    return (s[0] if x.shape[0] > 1 else 0, s[1] if x.shape[1] > 1 else 0)
+_MAX_ROW_STRIDE = 1 << 21  # elements; the kernels' offsets within a run are 32-bit
+
+
+def _seq(x):
+    """x, copied where its last dimension is strided or its rows lie too far apart, and its strides
+    {batch, len}. (Those of a dimension of one element are arbitrary in torch and never used.)"""
+    batch, length, dim = x.stride()
+    if (dim != 1 and x.shape[2] > 1) or (length > _MAX_ROW_STRIDE and x.shape[1] > 1):
+        x = x.contiguous()
+        batch, length, _ = x.stride()
+    return x, batch, length
 
 
 def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state=False, checkpoints_out=None, out=None,
@@ -240,32 +256,30 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
     lib = _load()
     dtype, x, r, i, lam, h0, reset = _gated_inputs(x, r, i, lam, h0, reset, "gated_scan_fn")
     batch, length, dim = x.shape
-    dev = x.device
+    (x, *xs), (r, *rs), (i, *is_) = _seq(x), _seq(r), _seq(i)
     if out is None:
-        y = torch.empty((batch, length, dim), dtype=x.dtype, device=dev)
+        y = x.new_empty((batch, length, dim))
     else:
         y = out
-        if y.shape != x.shape or y.dtype is not x.dtype or y.device != dev or (dim > 1 and y.stride(2) != 1):
+        if y.shape != x.shape or y.dtype is not x.dtype or y.device != x.device or (dim > 1 and y.stride(2) != 1):
             raise ValueError("out must have x's shape, dtype and device and unit stride along dim")
     last = None
     if return_last_state:
         last = last_state_out
         if last is None:
-            last = torch.empty((batch, dim), dtype=torch.float32, device=dev)
-        elif last.shape != (batch, dim) or last.dtype is not torch.float32 or last.device != dev or not last.is_contiguous():
+            last = x.new_empty((batch, dim), dtype=torch.float32)
+        elif last.shape != (batch, dim) or last.dtype is not torch.float32 or last.device != x.device or not last.is_contiguous():
             raise ValueError("last_state_out must be a contiguous float32 (batch, dim) tensor on x's device")
     if checkpoints_out is not None:
         _check_gated_checkpoints(checkpoints_out, x)
     shape = GatedShape(batch, length, dim)
-    n = lib.mamba_gated_workspace_bytes(shape, dtype)
-    ws = _workspace(n, "mamba_gated_workspace_bytes", dev) if n else None
+    n = _on_device(x, lib.mamba_gated_workspace_bytes, shape, dtype)
+    ws = _workspace(n, "mamba_gated_workspace_bytes", x) if n else None
+    ys = y.stride()
     ptrs = GatedPtrs(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _ptr(h0), _ptr(reset), y.data_ptr(), _ptr(last),
                      _ptr(checkpoints_out), _ptr(ws), n)
-    st = GatedStrides(_bt(x), _bt(r), _bt(i), _bt(y))
-    with _on(dev):
-        rc = lib.mamba_gated_scan_fwd(ptrs, shape, st, c, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_gated_scan_fwd")
+    st = GatedStrides(*xs, *rs, *is_, ys[0], ys[1])
+    _launch("mamba_gated_scan_fwd", x, lib.mamba_gated_scan_fwd, ptrs, shape, st, c, dtype)
     return (y, last) if return_last_state else y
 
 
@@ -285,30 +299,26 @@ def gated_scan_bwd(x, r, i, lam, dy, *, c=8.0, h0=None, reset=None, dlast_state=
     lib = _load()
     dtype, x, r, i, lam, h0, reset = _gated_inputs(x, r, i, lam, h0, reset, "gated_scan_bwd")
     batch, length, dim = x.shape
-    dev = x.device
-    dy = _same(dy, x, "dy")
-    dlast = _f32(dlast_state, "dlast_state", (batch, dim), dev)
+    (x, *xs), (r, *rs), (i, *is_), (dy, *gs) = _seq(x), _seq(r), _seq(i), _seq(_same(dy, x, "dy"))
+    dlast = _f32(dlast_state, "dlast_state", (batch, dim), x)
     if checkpoints is not None:
         _check_gated_checkpoints(checkpoints, x)
     if want_dh0 is None:
         want_dh0 = h0 is not None
-    g = torch.empty((batch, length, 3 * dim), dtype=x.dtype, device=dev)
+    g = x.new_empty((batch, length, 3 * dim))
     dx, dr, di = g[..., :dim], g[..., dim:2 * dim], g[..., 2 * dim:]
-    out = {"x": dx, "r": dr, "i": di, "lam": torch.empty((dim,), dtype=torch.float32, device=dev)}
+    out = {"x": dx, "r": dr, "i": di, "lam": x.new_empty((dim,), dtype=torch.float32)}
     if want_dh0:
-        out["h0"] = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+        out["h0"] = x.new_empty((batch, dim), dtype=torch.float32)
     shape = GatedShape(batch, length, dim)
-    n = lib.mamba_gated_bwd_workspace_bytes(shape, dtype, checkpoints is not None)
-    ws = _workspace(n, "mamba_gated_bwd_workspace_bytes", dev)
+    n = _on_device(x, lib.mamba_gated_bwd_workspace_bytes, shape, dtype, checkpoints is not None)
+    ws = _workspace(n, "mamba_gated_bwd_workspace_bytes", x)
     ptrs = GatedBwdPtrs(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _ptr(h0), _ptr(reset), dy.data_ptr(),
                         _ptr(dlast), _ptr(checkpoints), dx.data_ptr(), dr.data_ptr(), di.data_ptr(),
                         out["lam"].data_ptr(), _ptr(out.get("h0")), _ptr(ws), n)
-    t = _bt(dx)
-    st = GatedBwdStrides(_bt(x), _bt(r), _bt(i), _bt(dy), t, t, t)
-    with _on(dev):
-        rc = lib.mamba_gated_scan_bwd(ptrs, shape, st, c, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_gated_scan_bwd")
+    t = g.stride()[:2]
+    st = GatedBwdStrides(*xs, *rs, *is_, *gs, *t, *t, *t)
+    _launch("mamba_gated_scan_bwd", x, lib.mamba_gated_scan_bwd, ptrs, shape, st, c, dtype)
     return out
 
 
@@ -373,26 +383,22 @@ def layer_norm_fn(x, weight=None, bias=None, eps=1e-5, *, residual=None, return_
     lib = _load()
     dtype = _dtype(x, "x")
     _need_gpu(x, "layer_norm_fn")
-    dev = x.device
     shape = x.shape
     if residual is not None:
-        if residual.dtype is not x.dtype or residual.device != dev:
+        if residual.dtype is not x.dtype or residual.get_device() != x.get_device():
             raise TypeError("residual must have x's dtype and device")
         if residual.shape != shape:
             raise ValueError(f"residual must have x's shape {tuple(shape)}, got {tuple(residual.shape)}")
     xr = _rows(x, "x")
     rows, dim = xr.shape
     rr = None if residual is None else _rows(residual, "residual")
-    weight, bias = _f32(weight, "weight", (dim,), dev), _f32(bias, "bias", (dim,), dev)
-    y = torch.empty(shape, dtype=x.dtype, device=dev)
-    t = None if residual is None else torch.empty(shape, dtype=x.dtype, device=dev)
-    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev) if return_stats else None
+    weight, bias = _f32(weight, "weight", (dim,), x), _f32(bias, "bias", (dim,), x)
+    y = x.new_empty(shape)
+    t = None if residual is None else x.new_empty(shape)
+    stats = x.new_empty((rows, 2), dtype=torch.float32) if return_stats else None
     ptrs = NormPtrs(xr.data_ptr(), _ptr(rr), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(t), _ptr(stats),
                     _row_stride(xr), _row_stride(rr), dim, dim)
-    with _on(dev):
-        rc = lib.mamba_layer_norm_fwd(ptrs, NormShape(rows, dim), eps, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_layer_norm_fwd")
+    _launch("mamba_layer_norm_fwd", x, lib.mamba_layer_norm_fwd, ptrs, NormShape(rows, dim), eps, dtype)
     out = y if residual is None else (y, t)
     return (out, stats) if return_stats else out
 
@@ -404,33 +410,29 @@ def layer_norm_bwd(t, weight, dy, stats, *, dresidual=None, want_dweight=True, w
     lib = _load()
     dtype = _dtype(t, "t")
     _need_gpu(t, "layer_norm_bwd")
-    dev = t.device
     for name, v in (("dy", dy), ("dresidual", dresidual)):
         if v is not None:
-            if v.dtype is not t.dtype or v.device != dev:
+            if v.dtype is not t.dtype or v.get_device() != t.get_device():
                 raise TypeError(f"{name} must have t's dtype and device")
             if v.shape != t.shape:
                 raise ValueError(f"{name} must have t's shape {tuple(t.shape)}, got {tuple(v.shape)}")
     tr, gr = _rows(t, "t"), _rows(dy, "dy")
     rr = None if dresidual is None else _rows(dresidual, "dresidual")
     rows, dim = tr.shape
-    weight, stats = _f32(weight, "weight", (dim,), dev), _f32(stats, "stats", (rows, 2), dev)
-    dx = torch.empty(t.shape, dtype=t.dtype, device=dev)
+    weight, stats = _f32(weight, "weight", (dim,), t), _f32(stats, "stats", (rows, 2), t)
+    dx = t.new_empty(t.shape)
     out = {"x": dx}
     if want_dweight:
-        out["weight"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+        out["weight"] = t.new_empty((dim,), dtype=torch.float32)
     if want_dbias:
-        out["bias"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+        out["bias"] = t.new_empty((dim,), dtype=torch.float32)
     shape = NormShape(rows, dim)
     n = lib.mamba_layer_norm_bwd_workspace_bytes(shape) if want_dweight or want_dbias else 0
-    ws = _workspace(n, "mamba_layer_norm_bwd_workspace_bytes", dev)
+    ws = _workspace(n, "mamba_layer_norm_bwd_workspace_bytes", t)
     ptrs = NormBwdPtrs(tr.data_ptr(), _ptr(weight), stats.data_ptr(), gr.data_ptr(), _ptr(rr), dx.data_ptr(),
                        _ptr(out.get("weight")), _ptr(out.get("bias")), _row_stride(tr), _row_stride(gr), _row_stride(rr), dim,
                        _ptr(ws), n)
-    with _on(dev):
-        rc = lib.mamba_layer_norm_bwd(ptrs, shape, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_layer_norm_bwd")
+    _launch("mamba_layer_norm_bwd", t, lib.mamba_layer_norm_bwd, ptrs, shape, dtype)
     return out
 
 
@@ -468,10 +470,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, residual=None):
 
 # ---- token embedding ----
 
-def _ids(ids, dev):
+def _ids(ids, like):
     if ids.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"ids must be int64 or int32, got {ids.dtype}")
-    if ids.device != dev:
+    if ids.get_device() != like.get_device():
         raise ValueError("ids must be on the weight's device")
     return ids if ids.is_contiguous() else ids.contiguous()
 
@@ -482,18 +484,14 @@ def embedding_fn(ids, weight, scale=1.0):
     lib = _load()
     dtype = _dtype(weight, "weight")
     _need_gpu(weight, "embedding_fn")
-    dev = weight.device
     if weight.dim() != 2:
         raise ValueError(f"weight must be (vocab, dim), got {tuple(weight.shape)}")
-    ids = _ids(ids, dev)
+    ids = _ids(ids, weight)
     weight = weight if weight.is_contiguous() else weight.contiguous()
     vocab, dim = weight.shape
-    y = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=dev)
-    with _on(dev):
-        rc = lib.mamba_embedding_fwd(ids.data_ptr(), ids.dtype is torch.int64, weight.data_ptr(), y.data_ptr(),
-                                     EmbeddingShape(ids.numel(), vocab, dim), scale, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_embedding_fwd")
+    y = weight.new_empty((*ids.shape, dim))
+    _launch("mamba_embedding_fwd", weight, lib.mamba_embedding_fwd, ids.data_ptr(), ids.dtype is torch.int64, weight.data_ptr(),
+            y.data_ptr(), EmbeddingShape(ids.numel(), vocab, dim), scale, dtype)
     return y
 
 
@@ -503,21 +501,17 @@ def embedding_bwd(ids, dy, vocab, scale=1.0):
     lib = _load()
     dtype = _dtype(dy, "dy")
     _need_gpu(dy, "embedding_bwd")
-    dev = dy.device
-    ids = _ids(ids, dev)
+    ids = _ids(ids, dy)
     if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
         raise ValueError(f"dy must be ids.shape + (dim,), got {tuple(dy.shape)} for ids {tuple(ids.shape)}")
     dy = dy if dy.is_contiguous() else dy.contiguous()
     dim = dy.shape[-1]
-    dw = torch.empty((vocab, dim), dtype=dy.dtype, device=dev)
+    dw = dy.new_empty((vocab, dim))
     shape = EmbeddingShape(ids.numel(), vocab, dim)
     n = lib.mamba_embedding_bwd_workspace_bytes(shape)
-    ws = _workspace(n, "mamba_embedding_bwd_workspace_bytes", dev)
-    with _on(dev):
-        rc = lib.mamba_embedding_bwd(ids.data_ptr(), ids.dtype is torch.int64, dy.data_ptr(), dw.data_ptr(), _ptr(ws), n,
-                                     shape, scale, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_embedding_bwd")
+    ws = _workspace(n, "mamba_embedding_bwd_workspace_bytes", dy)
+    _launch("mamba_embedding_bwd", dy, lib.mamba_embedding_bwd, ids.data_ptr(), ids.dtype is torch.int64, dy.data_ptr(),
+            dw.data_ptr(), _ptr(ws), n, shape, scale, dtype)
     return dw
 
 
@@ -551,7 +545,7 @@ def _ffn_inputs(x, w_gate, w_up, activation, entry):
     if x.dim() < 1 or w_gate.dim() != 2:
         raise ValueError("x must be (..., dim) and w_gate (hidden, dim)")
     for name, w in (("w_gate", w_gate), ("w_up", w_up)):
-        if w.dtype is not x.dtype or w.device != x.device:
+        if w.dtype is not x.dtype or w.get_device() != x.get_device():
             raise TypeError(f"{name} must have x's dtype and device")
         if w.dim() != 2 or w.shape != w_gate.shape or w.shape[1] != x.shape[-1]:
             raise ValueError(f"{name} must be (hidden, dim) with dim = {x.shape[-1]}, got {tuple(w.shape)}")
@@ -566,19 +560,15 @@ def gated_ffn_fn(x, w_gate, w_up, activation="silu"):
     dtype, act, xr, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_fn")
     rows, dim = xr.shape
     hidden = wg.shape[0]
-    dev = x.device
-    h = torch.empty((*x.shape[:-1], hidden), dtype=x.dtype, device=dev)
+    h = x.new_empty((*x.shape[:-1], hidden))
     shape = FfnShape(rows, dim, hidden)
     ptrs = FfnPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu),
                    hidden, None, 0)
-    n = lib.mamba_gated_ffn_workspace_bytes(ptrs, shape)
+    n = _on_device(x, lib.mamba_gated_ffn_workspace_bytes, ptrs, shape)
     if n:
-        ws = _workspace(n, "mamba_gated_ffn_workspace_bytes", dev)
+        ws = _workspace(n, "mamba_gated_ffn_workspace_bytes", x)
         ptrs.workspace, ptrs.workspace_bytes = ws.data_ptr(), n
-    with _on(dev):
-        rc = lib.mamba_gated_ffn_fwd(ptrs, shape, act, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_gated_ffn_fwd")
+    _launch("mamba_gated_ffn_fwd", x, lib.mamba_gated_ffn_fwd, ptrs, shape, act, dtype)
     return h
 
 
@@ -590,23 +580,18 @@ def gated_ffn_bwd(x, w_gate, w_up, dh, activation="silu"):
     dtype, act, xr, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_bwd")
     rows, dim = xr.shape
     hidden = wg.shape[0]
-    dev = x.device
-    if dh.dtype is not x.dtype or dh.device != dev:
+    if dh.dtype is not x.dtype or dh.get_device() != x.get_device():
         raise TypeError("dh must have x's dtype and device")
     if dh.shape != (*x.shape[:-1], hidden):
         raise ValueError(f"dh must be {(*x.shape[:-1], hidden)}, got {tuple(dh.shape)}")
     gr = _rows(dh, "dh")
-    out = {"x": torch.empty(x.shape, dtype=x.dtype, device=dev), "w_gate": torch.empty((hidden, dim), dtype=x.dtype, device=dev),
-           "w_up": torch.empty((hidden, dim), dtype=x.dtype, device=dev)}
+    out = {"x": x.new_empty(x.shape), "w_gate": x.new_empty((hidden, dim)), "w_up": x.new_empty((hidden, dim))}
     shape = FfnShape(rows, dim, hidden)
-    n = lib.mamba_gated_ffn_bwd_workspace_bytes(shape)
-    ws = _workspace(n, "mamba_gated_ffn_bwd_workspace_bytes", dev)
+    n = _on_device(x, lib.mamba_gated_ffn_bwd_workspace_bytes, shape)
+    ws = _workspace(n, "mamba_gated_ffn_bwd_workspace_bytes", x)
     ptrs = FfnBwdPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), gr.data_ptr(), out["x"].data_ptr(), out["w_gate"].data_ptr(),
                       out["w_up"].data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu), _row_stride(gr), _ptr(ws), n)
-    with _on(dev):
-        rc = lib.mamba_gated_ffn_bwd(ptrs, shape, act, dtype, _stream(dev))
-    if rc != 0:
-        _raise(rc, "mamba_gated_ffn_bwd")
+    _launch("mamba_gated_ffn_bwd", x, lib.mamba_gated_ffn_bwd, ptrs, shape, act, dtype)
     return out
 
 
