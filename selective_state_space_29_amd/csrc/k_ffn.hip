@@ -3,22 +3,33 @@
 //   h = act(g) u,  g = x Wg^T, u = x Wu^T          dg = dh u act'(g), du = dh act(g)
 //   dx = dg Wg + du Wu;   dWg = dg^T x;   dWu = du^T x
 //
-// One matrix kernel, C[p][q] = sum_c X(p, c) Y(q, c), serves all products. A workgroup computes a TP x TQ
-// tile: it moves 64 steps of c of both operands through LDS a stage ahead of the one its waves multiply
-// (v_mfma_f32_16x16x32_bf16, fp32 sums). An operand lies with c contiguous (x and the weights in the
-// forward product) or with c as its rows (the weights in dx; both operands in dW); the latter is read
-// from LDS with the transposing ds_read_b64_tr_b16, so no operand is ever transposed in memory. 16-byte
-// chunks are placed in LDS at an index XORed with their row, so that the reads of both kinds meet no bank
-// twice. The rows of the MFMA are the q's: a lane then holds 4 consecutive q of one p, stored as one
-// 8-byte access.
+// One matrix kernel, C[p][q] = sum_c X(p, c) Y(q, c), serves all products. A workgroup of 8 waves computes
+// a tile of 256 x 256 (or 256 x 192; 4 waves 128 x 128): it loads 64 steps of c of both operands straight
+// into LDS, a stage ahead of the one its waves multiply (v_mfma_f32_16x16x32_bf16, fp32 sums). An operand
+// lies with c contiguous (x and the weights in the forward product) or with c as its rows (the weights in
+// dx; both operands in dW); the latter is read from LDS with the transposing ds_read_b64_tr_b16, so no
+// operand is ever transposed in memory. 16-byte chunks lie in LDS at an index XORed with their row, so that
+// the reads of both kinds meet no bank twice; the lanes of a load into LDS fill consecutive places, so each
+// lane loads the chunk whose place it fills. The rows of the MFMA are the q's: a lane then holds 4
+// consecutive q of one p, and a tile's results pass through the LDS that its stages no longer need, so
+// that whole rows are stored 16 bytes a lane.
 //
-// The forward tile holds 64 or 128 hidden units' gate rows and the same units' up rows, so that both
+// The forward tile holds 128 or 64 hidden units' gate rows and the same units' up rows, so that both
 // projections of a unit meet in the same lane and only h is written. The backward pass recomputes g and
 // u the same way (keeping them in fp32 would move more bytes than the product takes) and rounds dg and
 // du to bf16 once, as the operands of the other two products.
 //
+// Measured at 16384 rows, dim 768, hidden 2048 (103 GFLOP a product): forward 120 us, dg and du 160, dx 102,
+// dW 121 and 12 for the join of its splits, 0.64 to 1.0 PFLOP/s; at 8192 rows, dim 4096, hidden 4096 the
+// forward product reaches 1.1, where a library's plain product of 8192 x 8192 x 8192 reaches 1.4 with the
+// clock at its power limit. Tiles loaded through registers took 130 us (forward) and 165 (dg and du);
+// 128 x 256 with two workgroups a CU, and one wave's fragments read a half stage ahead, were slower. At
+// dim 768 a tile has 12 stages, and filling the first and storing the results cost as much as 3.
+//
 // Operands whose rows are not 16-byte aligned or not a multiple of 8 long are first copied into padded
 // rows of the workspace.
+#include <type_traits>
+
 #include "layers_common.hpp"
 #include "layers_launch.hpp"
 
@@ -27,13 +38,16 @@ namespace mscan {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTC = 64;                       // contraction steps per stage
 constexpr uint32_t kDrop = 0xFFFFFFF0u;       // a byte offset past every buffer: reads 0
 constexpr int kRsrcWord3 = 0x00020000;
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 enum { kEpiDual = 0, kEpiDualBwd = 1, kEpiStore = 2, kEpiPartial = 3 };
 
@@ -63,9 +77,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int6
     const int64_t n = bytes < 0 ? 0 : bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)n, kRsrcWord3);
 }
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+// 16 bytes a lane straight from memory into LDS: the wave's lanes fill 1 KB of consecutive places.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint16_t* to, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, (int)off, 0, 0, 0);
 }
+__device__ __forceinline__ void lds_arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
 
 // act and its derivative; silu(g) = g sg(g), gelu(g) = g/2 (1 + tanh(k (g + 0.044715 g^3))), where
 // (1 + tanh(z)) / 2 = sg(2z).
@@ -88,20 +104,29 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ float half_f32(uint32_t w, int k) { return __uint_as_float(k ? w & 0xFFFF0000u : w << 16); }
 
-// Where chunk `c` (8 values) of row `row` lies in its LDS row: rows of 64 c (8 chunks of 128 bytes), or of
-// T values of a c (tr), where the 8 rows that a half wave's transposing read touches take 8 distinct pairs.
-__device__ __forceinline__ int swz(int row, int c) { return c ^ (row & 7); }
-__device__ __forceinline__ int swz_tr(int row, int c) { return c ^ (((row & 3) | ((row >> 1) & 4)) << 1); }
+// Where chunk `c` (8 values) of row `row` lies in its LDS row: rows of 64 c (8 chunks, 128 bytes), of which
+// 16 lanes read the same chunk of 16 rows, or of T values of a c (tr), where the 8 rows that a half wave's
+// transposing read touches take 8 distinct pairs of chunks.
+__device__ __forceinline__ int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
+template <int T>
+__device__ __forceinline__ int swz_tr(int row, int c) {
+    if constexpr (T % 128 != 0) return c ^ (((row >> 1 & 1) | (row >> 2 & 2)) << 1);  // odd rows lie 128 bytes further
+    return c ^ (((row & 3) | ((row >> 1) & 4)) << 1);
+}
 
 template <int TP, int TQ, int WP, int WQ, bool XTR, bool YTR, int EPI>
-__global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
+__global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2))) void ffn_mat_kernel(FfnMat m) {
     constexpr bool DUAL = EPI == kEpiDual || EPI == kEpiDualBwd;
     constexpr int NT = WP * WQ * 64;
-    constexpr int PT = TP / WP / 16, QT = TQ / WQ / 16;
-    constexpr int XN = TP * 8 / NT, YN = TQ * 8 / NT;  // chunks a thread moves per stage
+    constexpr int PT = TP / WP / 16, QT = TQ / WQ / 16, QG = QT % 4 == 0 ? 4 : 3;  // QG: tiles read at a time
+    constexpr int CH = kTC / 8;  // chunks of a row of c
+    constexpr int XN = TP * CH / NT, YN = TQ * CH / NT;  // chunks a thread moves per stage
     static_assert(!(DUAL && (XTR || YTR)) && XN >= 1 && YN >= 1 && (!DUAL || QT % 2 == 0));
-    __shared__ __align__(16) uint16_t sx[2][TP * kTC];
-    __shared__ __align__(16) uint16_t sy[2][TQ * kTC];
+    constexpr int OQ = DUAL ? TQ / 2 : TQ, PITCH = OQ + 8;  // of the results' rows in LDS, 16 bytes apart in the banks
+    constexpr int STAGES = 2 * (TP + TQ) * kTC, RESULTS = EPI == kEpiPartial ? 0 : TP * PITCH;
+    __shared__ __align__(16) uint16_t lds[STAGES > RESULTS ? STAGES : RESULTS];
+    uint16_t(&sx)[2][TP * kTC] = *reinterpret_cast<uint16_t(*)[2][TP * kTC]>(&lds[0]);
+    uint16_t(&sy)[2][TQ * kTC] = *reinterpret_cast<uint16_t(*)[2][TQ * kTC]>(&lds[2 * TP * kTC]);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -124,33 +149,32 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
     const int per = (total + m.splits - 1) / m.splits;
     const int s_begin = (int)blockIdx.y * per, s_end = s_begin + per < total ? s_begin + per : total;
 
-    // this thread's chunks: its row and chunk in the tile, and their LDS place
-    int xr[XN], xc[XN], xl[XN], yr[YN], yc[YN], yl[YN];
+    // Each lane's chunks of a stage: 16 bytes straight into LDS, a wave's 64 lanes to 1 KB of consecutive
+    // places, so a lane picks the chunk whose place it fills.
+    int xr[XN], xc[XN], yr[YN], yc[YN];
 #pragma unroll
     for (int k = 0; k < XN; ++k) {
         const int l = k * NT + tid;
-        xr[k] = XTR ? l / (TP / 8) : l / 8;
-        xc[k] = XTR ? l % (TP / 8) : l % 8;
-        xl[k] = XTR ? xr[k] * TP + swz_tr(xr[k], xc[k]) * 8 : xr[k] * kTC + swz(xr[k], xc[k]) * 8;
+        xr[k] = XTR ? l / (TP / 8) : l / CH;
+        xc[k] = XTR ? swz_tr<TP>(xr[k], l % (TP / 8)) : swz(xr[k], l % CH);
     }
 #pragma unroll
     for (int k = 0; k < YN; ++k) {
         const int l = k * NT + tid;
-        yr[k] = YTR ? l / (TQ / 8) : l / 8;
-        yc[k] = YTR ? l % (TQ / 8) : l % 8;
-        yl[k] = YTR ? yr[k] * TQ + swz_tr(yr[k], yc[k]) * 8 : yr[k] * kTC + swz(yr[k], yc[k]) * 8;
+        yr[k] = YTR ? l / (TQ / 8) : l / CH;
+        yc[k] = YTR ? swz_tr<TQ>(yr[k], l % (TQ / 8)) : swz(yr[k], l % CH);
     }
-
-    u32x4 vx[XN], vy[YN];
-    auto fetch = [&](int step) __attribute__((always_inline)) {
+    auto fetch = [&](int step, int buf) __attribute__((always_inline)) {
         const int seg = step >= m.steps ? 1 : 0;
         const int64_t c0 = (int64_t)(step - seg * m.steps) * kTC;
+        uint16_t* tx = &sx[buf][wave * 512];
+        uint16_t* ty = &sy[buf][wave * 512];
         if constexpr (XTR) {  // rows c0 + row of X, columns p
             const __amdgpu_buffer_rsrc_t r = rsrc_of(m.x + c0 * m.x_stride + p0, ((m.C - c0 - 1) * m.x_stride + m.P - p0) * 2);
 #pragma unroll
             for (int k = 0; k < XN; ++k) {
                 const bool ok = c0 + xr[k] < m.C && p0 + xc[k] * 8 < m.P;
-                vx[k] = load16(r, ok ? (uint32_t)((xr[k] * (int)m.x_stride + xc[k] * 8) * 2) : kDrop);
+                load_lds(r, tx + k * NT * 8, ok ? (uint32_t)((xr[k] * (int)m.x_stride + xc[k] * 8) * 2) : kDrop);
             }
         } else {
             const int64_t col = seg * m.x_seg + c0;
@@ -158,7 +182,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
 #pragma unroll
             for (int k = 0; k < XN; ++k) {
                 const bool ok = p0 + xr[k] < m.P && c0 + xc[k] * 8 < m.x_cols;
-                vx[k] = load16(r, ok ? (uint32_t)((xr[k] * (int)m.x_stride + xc[k] * 8) * 2) : kDrop);
+                load_lds(r, tx + k * NT * 8, ok ? (uint32_t)((xr[k] * (int)m.x_stride + xc[k] * 8) * 2) : kDrop);
             }
         }
         if constexpr (YTR) {
@@ -167,7 +191,7 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
 #pragma unroll
             for (int k = 0; k < YN; ++k) {
                 const bool ok = c0 + yr[k] < m.C && q0 + yc[k] * 8 < m.Q;
-                vy[k] = load16(r, ok ? (uint32_t)((yr[k] * (int)m.y_stride + yc[k] * 8) * 2) : kDrop);
+                load_lds(r, ty + k * NT * 8, ok ? (uint32_t)((yr[k] * (int)m.y_stride + yc[k] * 8) * 2) : kDrop);
             }
         } else {
             const int64_t bytes = ((m.Q - q0 - 1) * m.y_stride + m.C - c0) * 2;
@@ -179,15 +203,9 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
                 const bool up = DUAL && k >= YN / 2;
                 const int row = up ? yr[k] - TQ / 2 : yr[k];
                 const bool ok = q0 + row < m.Q && c0 + yc[k] * 8 < m.C;
-                vy[k] = load16(up ? r1 : r0, ok ? (uint32_t)((row * (int)m.y_stride + yc[k] * 8) * 2) : kDrop);
+                load_lds(up ? r1 : r0, ty + k * NT * 8, ok ? (uint32_t)((row * (int)m.y_stride + yc[k] * 8) * 2) : kDrop);
             }
         }
-    };
-    auto put = [&](int buf) __attribute__((always_inline)) {
-#pragma unroll
-        for (int k = 0; k < XN; ++k) *reinterpret_cast<u32x4*>(&sx[buf][xl[k]]) = vx[k];
-#pragma unroll
-        for (int k = 0; k < YN; ++k) *reinterpret_cast<u32x4*>(&sy[buf][yl[k]]) = vy[k];
     };
 
     // tile t (16 p's or q's) of a wave: where its rows begin in the workgroup's tile
@@ -200,19 +218,48 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
         const int row = row0 + (lane & 15);
         return *reinterpret_cast<const bf16x8*>(&s[row * kTC + swz(row, kk * 4 + (lane >> 4)) * 8]);
     };
-    auto frag_tr = [&](const uint16_t* s, int T, int row0, int kk) __attribute__((always_inline)) {
-        const int i = lane & 15, n = row0 + 4 * (i & 3);
-        s16x4 v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = kk * 32 + 8 * (lane >> 4) + 4 * h + (i >> 2);
-            const uint16_t* a = &s[c * T + swz_tr(c, n >> 3) * 8 + (n & 7)];
-            v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
-        }
-        bf16x8 r;
-        __builtin_memcpy(&r, v, 16);
-        return r;
+    // Transposing reads of N tiles of 16: the lane's address of a tile in the stage's first rows, the rows of
+    // half kk of the stage and the second four of a lane's eight in the offset (the places' XOR depends on the
+    // lane alone). Reads and their wait in one asm block: the compiler's own form of these reads waits for
+    // every load that is on its way into LDS as well, here those of the next stage.
+    auto tr_at = [&](auto width, int row0) {
+        constexpr int T = decltype(width)::value;
+        const int i = lane & 15, n = row0 + 4 * (i & 3), c = 8 * (lane >> 4) + (i >> 2);
+        return (uint32_t)(c * T + swz_tr<T>(c, n >> 3) * 8 + (n & 7)) * 2;
     };
+    auto frags_tr = [&](auto width, auto count, bf16x8* to, const uint32_t* at, const uint16_t* s, auto step) __attribute__((always_inline)) {
+        constexpr int T = decltype(width)::value, N = decltype(count)::value, K0 = decltype(step)::value * 32 * T * 2, K1 = K0 + 4 * T * 2;
+        const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)s;
+        u32x2 r[2 * N];
+        if constexpr (N == 4) {
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+                "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+                "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+                "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+                : "v"(at[0] + base), "v"(at[1] + base), "v"(at[2] + base), "v"(at[3] + base), "n"(K0), "n"(K1)
+                : "memory");
+        } else {
+            static_assert(N == 3);
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %6 offset:%9\n\tds_read_b64_tr_b16 %1, %6 offset:%10\n\t"
+                "ds_read_b64_tr_b16 %2, %7 offset:%9\n\tds_read_b64_tr_b16 %3, %7 offset:%10\n\t"
+                "ds_read_b64_tr_b16 %4, %8 offset:%9\n\tds_read_b64_tr_b16 %5, %8 offset:%10\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5])
+                : "v"(at[0] + base), "v"(at[1] + base), "v"(at[2] + base), "n"(K0), "n"(K1)
+                : "memory");
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) __builtin_memcpy(&to[k], &r[2 * k], 16);
+    };
+    uint32_t qa[QT], pa[PT];
+#pragma unroll
+    for (int q = 0; q < QT; ++q) qa[q] = YTR ? tr_at(Int<TQ>{}, q_row(q)) : 0;
+#pragma unroll
+    for (int p = 0; p < PT; ++p) pa[p] = XTR ? tr_at(Int<TP>{}, p_row(p)) : 0;
 
     f32x4 acc[QT][PT];
 #pragma unroll
@@ -221,105 +268,152 @@ __global__ __launch_bounds__(WP * WQ * 64) void ffn_mat_kernel(FfnMat m) {
         for (int p = 0; p < PT; ++p) acc[q][p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     if (s_begin < s_end) {
-        fetch(s_begin);
-        put(0);
-        __syncthreads();
+        fetch(s_begin, 0);
         int buf = 0;
         for (int s = s_begin; s < s_end; ++s, buf ^= 1) {
-            if (s + 1 < s_end) fetch(s + 1);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
+            lds_arrived();
+            __syncthreads();  // this stage is in LDS, and every wave is done with the other one
+            if (s + 1 < s_end) fetch(s + 1, buf ^ 1);
+            auto half = [&](auto step) __attribute__((always_inline)) {
+                constexpr int kk = decltype(step)::value;
                 bf16x8 a[QT], b[PT];
+                if constexpr (YTR) {
 #pragma unroll
-                for (int q = 0; q < QT; ++q) a[q] = YTR ? frag_tr(sy[buf], TQ, q_row(q), kk) : frag(sy[buf], q_row(q), kk);
+                    for (int q = 0; q < QT; q += QG) frags_tr(Int<TQ>{}, Int<QG>{}, a + q, qa + q, sy[buf], step);
+                } else {
 #pragma unroll
-                for (int p = 0; p < PT; ++p) b[p] = XTR ? frag_tr(sx[buf], TP, p_row(p), kk) : frag(sx[buf], p_row(p), kk);
+                    for (int q = 0; q < QT; ++q) a[q] = frag(sy[buf], q_row(q), kk);
+                }
+                if constexpr (XTR) {
+#pragma unroll
+                    for (int p = 0; p < PT; p += 4) frags_tr(Int<TP>{}, Int<4>{}, b + p, pa + p, sx[buf], step);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < PT; ++p) b[p] = frag(sx[buf], p_row(p), kk);
+                }
 #pragma unroll
                 for (int q = 0; q < QT; ++q)
 #pragma unroll
                     for (int p = 0; p < PT; ++p)
                         acc[q][p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b[p], acc[q][p], 0, 0, 0);
-            }
-            if (s + 1 < s_end) put(buf ^ 1);  // last read a stage ago, before the barrier below
-            __syncthreads();
+            };
+            half(Int<0>{});
+            half(Int<1>{});
         }
     }
 
-    // lane: q = q0 + q_row(t) + 4 (lane / 16) .. + 3 of p = p0 + p_row(t) + lane % 16
+    // A lane holds q = q0 + q_row(t) + 4 (lane / 16) .. + 3 of p = p0 + p_row(t) + lane % 16.
     const int lq = 4 * (lane >> 4), lp = lane & 15;
+    if constexpr (EPI == kEpiPartial) {
 #pragma unroll
-    for (int p = 0; p < PT; ++p) {
-        const int64_t pr = p0 + p_row(p) + lp;
-        if (pr >= m.P) continue;
-        if constexpr (DUAL) {
-#pragma unroll
-            for (int q = 0; q < QT / 2; ++q) {
-                const int64_t f = q0 + q_row(q) + lq;
-                const f32x4 g = acc[q][p], u = acc[q + QT / 2][p];
-                if constexpr (EPI == kEpiDual) {
-                    uint16_t* o = m.out + pr * m.out_stride + f;
-                    float h[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = act_of(g[j], m.act) * u[j];
-                    if (f + 3 < m.Q && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
-                        *reinterpret_cast<uint2*>(o) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (f + j < m.Q) o[j] = to_bf16(h[j]).bits;
-                    }
-                } else {
-                    if (f >= m.seg_rows) continue;
-                    const uint16_t* dh = m.dh + pr * m.dh_stride + f;
-                    float dv[4];
-                    if (f + 3 < m.Q && (reinterpret_cast<uintptr_t>(dh) & 7) == 0) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(dh);
-                        dv[0] = half_f32(w.x, 0), dv[1] = half_f32(w.x, 1), dv[2] = half_f32(w.y, 0), dv[3] = half_f32(w.y, 1);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) dv[j] = f + j < m.Q ? half_f32(dh[j], 0) : 0.0f;
-                    }
-                    float dg[4], du[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a, da;
-                        act_grad(g[j], m.act, a, da);
-                        dg[j] = f + j < m.Q ? dv[j] * u[j] * da : 0.0f;
-                        du[j] = f + j < m.Q ? dv[j] * a : 0.0f;
-                    }
-                    uint16_t* o = m.d + pr * 2 * m.seg_rows + f;
-                    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(dg[0], dg[1]), pack2(dg[2], dg[3]));
-                    *reinterpret_cast<uint2*>(o + m.seg_rows) = make_uint2(pack2(du[0], du[1]), pack2(du[2], du[3]));
-                }
-            }
-        } else {
+        for (int p = 0; p < PT; ++p) {
+            const int64_t pr = p0 + p_row(p) + lp;
+            if (pr >= m.P) continue;
 #pragma unroll
             for (int q = 0; q < QT; ++q) {
                 const int64_t qc = q0 + q_row(q) + lq;
                 if (qc >= m.Q) continue;
-                const f32x4 v = acc[q][p];
-                if constexpr (EPI == kEpiPartial) {
-                    float* o = m.part + ((int64_t)blockIdx.y * m.P + pr) * m.Q + qc;
-                    if (m.Q % 4 == 0) {
-                        *reinterpret_cast<f32x4*>(o) = v;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (qc + j < m.Q) o[j] = v[j];
-                    }
+                float* o = m.part + ((int64_t)blockIdx.y * m.P + pr) * m.Q + qc;
+                if (m.Q % 4 == 0) {
+                    *reinterpret_cast<f32x4*>(o) = acc[q][p];
                 } else {
-                    const int64_t row = pr < m.seg_rows ? pr : pr - m.seg_rows;
-                    if (row >= m.seg_valid) continue;
-                    uint16_t* o = (pr < m.seg_rows ? m.out : m.out2) + row * m.out_stride + qc;
-                    if (qc + 3 < m.Q && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
-                        *reinterpret_cast<uint2*>(o) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (qc + j < m.Q) o[j] = to_bf16(v[j]).bits;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        if (qc + j < m.Q) o[j] = acc[q][p][j];
                 }
             }
+        }
+    } else {
+        // The bf16 results pass through LDS, so that rows are moved 16 bytes a lane.
+        constexpr int OC = OQ / 8;  // chunks a row
+        uint16_t* stage = &lds[0];
+        auto place = [&](int t, int p) { return &stage[(p_row(p) + lp) * PITCH + q_row(t) + lq]; };
+        // rows of the tile to or from memory, in chunks; f(row of the tile, first column, pointer into stage)
+        auto rows = [&](int64_t end, auto&& f) __attribute__((always_inline)) {
+            for (int k = tid; k < TP * OC; k += NT) {
+                const int r = k / OC, c = k % OC * 8;
+                if (p0 + r < m.P && q0 + c < end) f(p0 + r, q0 + c, &stage[r * PITCH + c]);
+            }
+        };
+        auto store_row = [&](uint16_t* o, int64_t col, int64_t end, const uint16_t* s) __attribute__((always_inline)) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(s);
+            if (col + 8 <= end && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+                *reinterpret_cast<u32x4*>(o) = v;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col + j < end) o[j] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
+            }
+        };
+        __syncthreads();  // every wave has read its last fragments
+        if constexpr (EPI == kEpiDualBwd) {
+            // zeros in units past Q, up to the padded width that is written
+            rows(m.seg_rows, [&](int64_t pr, int64_t f, uint16_t* s) {
+                const uint16_t* dh = m.dh + pr * m.dh_stride + f;
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (f + 8 <= m.Q && (reinterpret_cast<uintptr_t>(dh) & 15) == 0) {
+                    v = *reinterpret_cast<const u32x4*>(dh);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (f + j < m.Q) v[j / 2] |= (uint32_t)dh[j] << (16 * (j & 1));
+                }
+                *reinterpret_cast<u32x4*>(s) = v;
+            });
+            __syncthreads();
+            // dg overwrites dh in place; du follows after the rows of dg are out
+            uint2 du[QT / 2][PT];
+#pragma unroll
+            for (int p = 0; p < PT; ++p)
+#pragma unroll
+                for (int q = 0; q < QT / 2; ++q) {
+                    uint16_t* s = place(q, p);
+                    const uint2 w = *reinterpret_cast<const uint2*>(s);
+                    const float dv[4] = {half_f32(w.x, 0), half_f32(w.x, 1), half_f32(w.y, 0), half_f32(w.y, 1)};
+                    float dg[4], dd[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, da;
+                        act_grad(acc[q][p][j], m.act, a, da);
+                        dg[j] = dv[j] * acc[q + QT / 2][p][j] * da;
+                        dd[j] = dv[j] * a;
+                    }
+                    *reinterpret_cast<uint2*>(s) = make_uint2(pack2(dg[0], dg[1]), pack2(dg[2], dg[3]));
+                    du[q][p] = make_uint2(pack2(dd[0], dd[1]), pack2(dd[2], dd[3]));
+                }
+            auto out = [&](int64_t shift) __attribute__((always_inline)) {
+                __syncthreads();
+                rows(m.seg_rows, [&](int64_t pr, int64_t f, const uint16_t* s) {
+                    *reinterpret_cast<u32x4*>(m.d + pr * 2 * m.seg_rows + shift + f) = *reinterpret_cast<const u32x4*>(s);
+                });
+            };
+            out(0);
+            __syncthreads();
+#pragma unroll
+            for (int p = 0; p < PT; ++p)
+#pragma unroll
+                for (int q = 0; q < QT / 2; ++q) *reinterpret_cast<uint2*>(place(q, p)) = du[q][p];
+            out(m.seg_rows);
+        } else {
+#pragma unroll
+            for (int p = 0; p < PT; ++p)
+#pragma unroll
+                for (int q = 0; q < (DUAL ? QT / 2 : QT); ++q) {
+                    float h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        h[j] = DUAL ? act_of(acc[q][p][j], m.act) * acc[q + (DUAL ? QT / 2 : 0)][p][j] : acc[q][p][j];
+                    *reinterpret_cast<uint2*>(place(q, p)) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+                }
+            __syncthreads();
+            rows(m.Q, [&](int64_t pr, int64_t qc, const uint16_t* s) {
+                if constexpr (DUAL) {
+                    store_row(m.out + pr * m.out_stride + qc, qc, m.Q, s);
+                } else {
+                    const int64_t row = pr < m.seg_rows ? pr : pr - m.seg_rows;
+                    if (row < m.seg_valid) store_row((pr < m.seg_rows ? m.out : m.out2) + row * m.out_stride + qc, qc, m.Q, s);
+                }
+            });
         }
     }
 }
@@ -367,38 +461,55 @@ bool row_aligned(const void* p, int64_t stride, int64_t rows) {
 }
 
 struct Tiling {
-    int t;  // tile edge: 256 or 128
+    int tp, tq;  // 256 x 256, 256 x 192 or 128 x 128
     int tiles_p, tiles_q, splits;
 };
 
-// 256-wide tiles where they fill the GPU, else 128; the contraction split where even those leave half of
-// it idle and it is long.
-Tiling tiling(int64_t P, int64_t Q, int64_t q_per_tile_256, int steps, bool may_split) {
+// The tile and the split of the contraction whose rounds over the GPU's CUs take least. A stage of a tile
+// takes its area over the tile's rate (measured against the largest: dx of 16384 x 768 from 4096, 64 x 3
+// tiles of 256 x 256 in 119 us, 64 x 4 of 256 x 192 in 102; 128 x 128 forward 138 us against 119); two
+// workgroups of the smallest share a CU, where one alone takes kAlone of a pair's rounds. Splits add their
+// partial sums' way through memory and the kernel that joins them. Forward and backward together, always
+// 256 x 256, always 128 x 128 and this rule: 512 rows, dim 768, hidden 2048: 115, 61, 60 us; 2048 rows: 139,
+// 104, 100; 8192 rows, dim 1536, hidden 4096: 814, 923, 790.
+Tiling tiling(int64_t P, int64_t Q, bool dual, int steps, bool may_split) {
     const int64_t cus = layers_cus();
     auto div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    Tiling t{256, (int)div(P, 256), (int)div(Q, q_per_tile_256), 1};
-    if ((int64_t)t.tiles_p * t.tiles_q < cus / 2 * 3 && !(may_split && steps >= 64)) {
-        t.t = 128;
-        t.tiles_p = (int)div(P, 128);
-        t.tiles_q = (int)div(Q, q_per_tile_256 / 2);
+    constexpr int kTiles[3][3] = {{256, 256, 100}, {256, 192, 88}, {128, 128, 80}};
+    constexpr double kStage = 2.4e-6 * 100 / (256 * 256), kAlone = 1.4, kJoinBytes = 8.0 / 5e12, kJoin = 4e-6;
+    Tiling best{};
+    double least = 0.0;
+    for (const auto& k : kTiles) {
+        if (dual && k[1] == 192) continue;
+        Tiling t{k[0], k[1], (int)div(P, k[0]), (int)div(Q, dual ? k[1] / 2 : k[1]), 1};
+        const int64_t n = (int64_t)t.tiles_p * t.tiles_q, room = k[0] == 128 ? 2 * cus : cus;
+        const int most = may_split ? (int)(room / n < steps / 4 ? room / n : steps / 4) : 1;
+        for (int s = 1; s == 1 || s <= most; ++s) {
+            const int64_t wgs = n * s;
+            double rounds = k[0] == 128 && wgs <= cus ? kAlone : (double)div(wgs, cus);
+            double cost = rounds * div(steps, s) * k[0] * k[1] / k[2] * kStage;
+            if (s > 1) cost += kJoin + kJoinBytes * s * (double)P * Q;
+            if (best.tp == 0 || cost < least) t.splits = s, best = t, least = cost;
+        }
     }
-    if (may_split) {
-        const int64_t n = (int64_t)t.tiles_p * t.tiles_q, room = t.t == 256 ? cus : 2 * cus;
-        int64_t s = n < room ? room / n : 1;
-        if (s > steps / 4) s = steps / 4;
-        t.splits = s < 1 ? 1 : s > 64 ? 64 : (int)s;
-    }
-    return t;
+    return best;
 }
 
 template <bool XTR, bool YTR, int EPI>
 void run_mat(FfnMat m, const Tiling& t, hipStream_t stream) {
     m.tiles_p = t.tiles_p, m.tiles_q = t.tiles_q, m.splits = t.splits;
     const dim3 grid((unsigned)(t.tiles_p * t.tiles_q), (unsigned)t.splits);
-    if (t.t == 256)
-        hipLaunchKernelGGL((ffn_mat_kernel<256, 256, 2, 4, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
-    else
+    if (t.tp == 128) {
         hipLaunchKernelGGL((ffn_mat_kernel<128, 128, 2, 2, XTR, YTR, EPI>), grid, dim3(256), 0, stream, m);
+        return;
+    }
+    if constexpr (EPI == kEpiStore || EPI == kEpiPartial) {
+        if (t.tq == 192) {
+            hipLaunchKernelGGL((ffn_mat_kernel<256, 192, 2, 4, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((ffn_mat_kernel<256, 256, 2, 4, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
 }
 
 template <bool XTR, bool YTR>
@@ -462,9 +573,9 @@ struct BwdPlan {
 BwdPlan bwd_plan(const mamba_ffn_shape& s) {
     BwdPlan b;
     b.fp = up(s.hidden, kTC);
-    b.dual = tiling(s.rows, b.fp, 128, steps_of(s.dim), false);
-    b.dx = tiling(s.rows, s.dim, 256, 2 * steps_of(s.hidden), true);
-    b.dw = tiling(2 * b.fp, s.dim, 256, steps_of(s.rows), true);
+    b.dual = tiling(s.rows, b.fp, true, steps_of(s.dim), false);
+    b.dx = tiling(s.rows, s.dim, false, 2 * steps_of(s.hidden), true);
+    b.dw = tiling(2 * b.fp, s.dim, false, steps_of(s.rows), true);
     b.copy = 0;  // room for the copies whether or not the call needs them: the size depends on the shape alone
     b.d = copy_bytes(s);
     b.part = b.d + align256(s.rows * 2 * b.fp * 2);
@@ -496,7 +607,7 @@ int launch_ffn_fwd(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s, int act, h
                                 static_cast<char*>(p.workspace), stream);
     FfnMat m = dual_mat(s, o, act);
     m.out = static_cast<uint16_t*>(p.h), m.out_stride = p.h_stride;
-    run_mat<false, false, kEpiDual>(m, tiling(s.rows, s.hidden, 128, m.steps, false), stream);
+    run_mat<false, false, kEpiDual>(m, tiling(s.rows, s.hidden, true, m.steps, false), stream);
     return launch_status();
 }
 
