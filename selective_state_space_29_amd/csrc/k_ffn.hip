@@ -55,6 +55,7 @@ struct FfnMat {
     const uint16_t* x;      // X(p, c): [p][c], or [c][p] where XTR
     const uint16_t* y[2];   // Y(q, c); dual: gate and up rows; dx: the weights of the two stretches of c
     int64_t x_stride, y_stride;
+    int64_t up_stride;      // few rows: of y[1], where it may differ
     int64_t P, Q;           // extents; dual: Q hidden units
     int64_t C;              // contraction length of a stretch
     int64_t x_cols;         // X not XTR: columns of a stretch that may be read (a multiple of 8)
@@ -418,6 +419,123 @@ __global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2)
     }
 }
 
+// ---- few rows ----
+//
+// The forward product of up to kFewRows rows: every weight is used once or a few times, so it goes from
+// memory straight into the MFMA operand of the lane that loads it. A workgroup takes 16 hidden units, its
+// 8 waves take stretches of 64 c in turn (128 bytes of each weight row: a lane 16 c of one unit's gate and
+// up rows, in two steps of the MFMA, whose order of c is the same in both operands and otherwise free), and
+// their sums meet in LDS, added in the waves' order. Loads need no alignment, so no operand is copied.
+//
+// Bound by the weights' bytes: 8 rows, dim 2048, hidden 8192 read 67 MB in 12.6 us, 5.3 TB/s (the tiles
+// above take 24: 128 of them on 256 CUs). Up to 48 rows, as x is read again by every 16 units: with the
+// call's host side, few rows against tiles, 16 rows 16.6 and 26.6 us, 32 rows 20 and 26.7, 48 rows 25.5 and
+// 27.0 (dim 4096, hidden 11008: 69.5 and 67.8), 64 rows 29.6 and 27.1.
+constexpr int kFewRows = 16 * 3, kFewUnits = 16, kFewWaves = 8, kFewC = 64, kFewAhead = 4;
+
+__device__ __forceinline__ bf16x8 load_any(const uint16_t* p) {
+    bf16x8 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+template <int NR>
+__global__ __launch_bounds__(kFewWaves * 64) void ffn_few_kernel(FfnMat m) {
+    __shared__ float sums[kFewWaves][2][NR * 256];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t f0 = (int64_t)blockIdx.x * kFewUnits;
+
+    // rows past the last repeat it: their products are not stored, and none enters another's
+    const int row = lane & 15, at = (lane >> 4) * 16;
+    const int64_t f = f0 + row < m.Q ? f0 + row : m.Q - 1;
+    const uint16_t* w[2] = {m.y[0] + f * m.y_stride + at, m.y[1] + f * m.up_stride + at};
+    const uint16_t* x[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int64_t pr = r * 16 + row < m.P ? r * 16 + row : m.P - 1;
+        x[r] = m.x + pr * m.x_stride + at;
+    }
+
+    f32x4 acc[2][NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) acc[0][r] = acc[1][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](const bf16x8 (&a)[2][2], const bf16x8 (&b)[NR][2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) acc[g][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[g][k], b[r][k], acc[g][r], 0, 0, 0);
+    };
+
+    const int64_t whole = m.C / kFewC;
+    for (int64_t u = wave; u < whole; u += kFewWaves * kFewAhead) {
+        bf16x8 a[kFewAhead][2][2], b[kFewAhead][NR][2];
+        // all loads of a round before its first product; a stretch past the end repeats the round's first
+#pragma unroll
+        for (int i = 0; i < kFewAhead; ++i) {
+            const int64_t c = (u + i * kFewWaves < whole ? u + i * kFewWaves : u) * kFewC;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) a[i][g][k] = load_any(w[g] + c + k * 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFewAhead; ++i) {
+            const int64_t c = (u + i * kFewWaves < whole ? u + i * kFewWaves : u) * kFewC;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) b[i][r][k] = load_any(x[r] + c + k * 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFewAhead; ++i)
+            if (u + i * kFewWaves < whole) add(a[i], b[i]);
+    }
+    if (m.C % kFewC != 0 && wave == (int)(whole % kFewWaves)) {  // the last, part stretch value by value, zeros past its end
+        const int64_t c = whole * kFewC;
+        const int left = (int)(m.C - c) - at;  // of this lane's 16
+        auto part = [&](const uint16_t* p, int k) __attribute__((always_inline)) {
+            uint16_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int o = k * 8 + j < left ? k * 8 + j : left - 1;  // the row's last value, before this lane's 16 if none is left
+                v[j] = p[c + o];
+                if (k * 8 + j >= left) v[j] = 0;
+            }
+            bf16x8 r;
+            __builtin_memcpy(&r, v, 16);
+            return r;
+        };
+        bf16x8 a[2][2], b[NR][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) a[g][k] = part(w[g], k);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) b[r][k] = part(x[r], k);
+        }
+        add(a, b);
+    }
+
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) *reinterpret_cast<f32x4*>(&sums[wave][g][r * 256 + lane * 4]) = acc[g][r];
+    __syncthreads();
+    for (int e = tid; e < NR * 256; e += kFewWaves * 64) {
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kFewWaves; ++k) g += sums[k][0][e], u += sums[k][1][e];
+        const int l = e / 4 % 64;
+        const int64_t pr = e / 256 * 16 + (l & 15), unit = f0 + 4 * (l >> 4) + e % 4;
+        if (pr < m.P && unit < m.Q) m.out[pr * m.out_stride + unit] = to_bf16(act_of(g, m.act) * u).bits;
+    }
+}
+
 // The splits' partial sums of a product, added in order.
 __global__ __launch_bounds__(256) void ffn_join_kernel(FfnMat m) {
     const int64_t n = m.P * m.Q;
@@ -597,12 +715,29 @@ int launch_ffn_zero(void* p, int64_t rows, int64_t cols, int64_t stride, hipStre
 }
 
 int64_t ffn_workspace(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s) {
+    if (s.rows <= kFewRows) return 0;
     return needs_copy(s, p.x, p.x_stride, p.w_gate, p.w_gate_stride, p.w_up, p.w_up_stride) ? copy_bytes(s) : 0;
 }
 
 int64_t ffn_bwd_workspace(const mamba_ffn_shape& s) { return bwd_plan(s).total; }
 
 int launch_ffn_fwd(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s, int act, hipStream_t stream) {
+    if (s.rows <= kFewRows) {
+        FfnMat m{};
+        m.x = static_cast<const uint16_t*>(p.x), m.x_stride = p.x_stride;
+        m.y[0] = static_cast<const uint16_t*>(p.w_gate), m.y_stride = p.w_gate_stride;
+        m.y[1] = static_cast<const uint16_t*>(p.w_up), m.up_stride = p.w_up_stride;
+        m.P = s.rows, m.Q = s.hidden, m.C = s.dim, m.act = act;
+        m.out = static_cast<uint16_t*>(p.h), m.out_stride = p.h_stride;
+        const dim3 grid((unsigned)((s.hidden + kFewUnits - 1) / kFewUnits)), block(kFewWaves * 64);
+        if (s.rows <= 16)
+            hipLaunchKernelGGL(ffn_few_kernel<1>, grid, block, 0, stream, m);
+        else if (s.rows <= 32)
+            hipLaunchKernelGGL(ffn_few_kernel<2>, grid, block, 0, stream, m);
+        else
+            hipLaunchKernelGGL(ffn_few_kernel<3>, grid, block, 0, stream, m);
+        return launch_status();
+    }
     const Operands o = operands(s, p.x, p.x_stride, p.w_gate, p.w_gate_stride, p.w_up, p.w_up_stride,
                                 static_cast<char*>(p.workspace), stream);
     FfnMat m = dual_mat(s, o, act);

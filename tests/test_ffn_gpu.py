@@ -138,3 +138,55 @@ def test_ffn_autograd_and_empty():
         g = layers.gated_ffn_bwd(x, wg, wu, dh)
         assert g["x"].shape == (M, K) and g["w_gate"].shape == g["w_up"].shape == (F, K)
         assert not any(v.any() for v in g.values())
+
+
+def check_fwd(x, wg, wu, got, kind="silu"):
+    K = x.shape[1]
+    xd, gd, ud = x.double(), wg.double(), wu.double()
+    room = K * 2.0 ** -24 * 1.2 * ((xd.abs() @ gd.abs().t()) * (xd @ ud.t()).abs() +
+                                   (xd.abs() @ ud.abs().t()) * ref.act(xd @ gd.t(), kind).abs())
+    check(got, ref.gated_ffn(x, wg, wu, kind), room)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("K,F", [(1, 1), (8, 15), (63, 16), (64, 17), (65, 33), (512, 40), (513, 40), (1001, 100), (2120, 72)], ids=str)
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 32, 33, 48, 49])
+def test_ffn_few_rows(M, K, F, kind):
+    x, wg, wu, _ = data(M, K, F, 11)
+    check_fwd(x, wg, wu, layers.gated_ffn_fn(*(t.to(DEV) for t in (x, wg, wu)), kind), kind)
+
+
+@pytest.mark.parametrize("M", [1, 20, 48])
+def test_ffn_few_rows_at_odd_places(M):
+    K, F = 330, 50
+    x, wg, wu, _ = data(M, K, F, 12)
+
+    def at(t, left, wide):
+        to = torch.full((t.shape[0], wide), float("nan"), dtype=BF16, device=DEV)
+        to[:, left:left + K] = t.to(DEV)
+        return to[:, left:left + K]
+
+    X, G, U = at(x, 3, 337), at(wg, 1, 331), at(wu, 5, 400)
+    got = layers.gated_ffn_fn(X, G, U)
+    check_fwd(x, wg, wu, got)
+    assert torch.equal(got, layers.gated_ffn_fn(*(t.to(DEV) for t in (x, wg, wu))))
+
+
+@pytest.mark.parametrize("M", [9, 40, 64, 300])
+def test_ffn_bad_values_past_odd_sizes(M):
+    """Units and dimensions that fill no tile: what pads them never meets a bad value of another row or unit."""
+    K, F = 72 + 5, 100
+    X, G, U, H = (t.to(DEV) for t in data(M, K, F, 13))
+    h0, g0 = layers.gated_ffn_fn(X, G, U), layers.gated_ffn_bwd(X, G, U, H)
+    X[4, K - 1] = float("inf")
+    H[6, F - 1] = float("nan")
+    h, g = layers.gated_ffn_fn(X, G, U), layers.gated_ffn_bwd(X, G, U, H)
+    keep = torch.arange(M, device=DEV) != 4
+    assert torch.equal(h[keep], h0[keep]) and not h[4].isfinite().all()
+    keep[6] = False
+    assert torch.equal(g["x"][keep], g0["x"][keep]) and g["x"][6].isnan().all()
+    X[4, K - 1] = 0
+    h0 = layers.gated_ffn_fn(X, G, U)
+    G[F - 1, K - 1] = float("nan")
+    h = layers.gated_ffn_fn(X, G, U)
+    assert torch.equal(h[:, :F - 1], h0[:, :F - 1]) and h[:, F - 1].isnan().all()
