@@ -1,7 +1,8 @@
 """MI355X-native Mamba selective-scan forward: a C-ABI HIP library plus a thin Python binding.
 
-``selective_scan_fn`` (in :mod:`.scan`) is the user entry point; :mod:`.gen` and
-:mod:`.workloads` provide the seeded synthetic inputs.
+``selective_scan_fn`` (in :mod:`.scan`) is the user entry point; :mod:`.layers` has the layer
+operators around a scan (gated linear recurrence, layer norm, token embedding, gated feed-forward) with
+their gradients; :mod:`.gen` and :mod:`.workloads` provide the seeded synthetic inputs.
 """
 
 __all__ = ["selective_scan_fn"]

@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .scan import BF16, F32, MambaScanError, _raise, load_library
 
@@ -335,6 +336,7 @@ class GatedScan(torch.autograd.Function):
         return y, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dlast):
         x, r, i, lam, h0, reset, ck = ctx.saved_tensors
         if dy is None:
@@ -449,6 +451,7 @@ class LayerNorm(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dt=None):
         t, weight, bias, stats = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -523,6 +526,7 @@ class Embedding(torch.autograd.Function):
         return embedding_fn(ids, weight, scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         return None, embedding_bwd(ctx.saved_tensors[0], dy, ctx.vocab, ctx.scale), None
 
@@ -603,6 +607,7 @@ class GatedFfn(torch.autograd.Function):
         return gated_ffn_fn(x, w_gate, w_up, activation)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         g = gated_ffn_bwd(*ctx.saved_tensors, dh, ctx.activation)
         return g["x"], g["w_gate"], g["w_up"], None
