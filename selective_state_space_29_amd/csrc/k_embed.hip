@@ -2,7 +2,7 @@
 //
 // Forward: one wave a token, 16 bytes a lane where rows allow it; bound by HBM.
 //
-// Gradient: dweight[v] = scale * sum of dy over the tokens of v. The tokens are gathered into one
+// Gradient (of more than 2048 tokens; fewer: direct_kernel): dweight[v] = scale * sum of dy over the tokens of v. The tokens are gathered into one
 // list per id and each id's rows are added in token order, so every row of dweight is written exactly
 // once, by one wave, and the sums do not depend on timing:
 //   count    how many tokens each id has, and each token's place among its id's (in no order: whoever
@@ -316,6 +316,118 @@ __device__ __forceinline__ void sum_rows(const S* dy, int64_t dim, int64_t c, in
     else if (n - k == 1) add(k, 1, std::integral_constant<int, 1>{});
 }
 
+// The whole gradient of few tokens in one launch and no workspace: a workgroup takes 64 ids and 64 packs of
+// columns, finds its ids' tokens among all of them, in order, and its 16 waves take an id in turn; those
+// with more than kPiece tokens afterwards, a piece a wave. The sums are those of the launches above, bit
+// for bit. Bound by its launch for few tokens, then by the workgroup that has the most frequent ids; with the
+// call's host side, this and the launches above, at uneven frequencies: 700 tokens, 5000 x 256 bf16 13.9 and
+// 34.6 us, 1500 tokens, 5000 x 1024 27.5 and 35.5, 2000 tokens, 50000 x 768 37.9 and 44.4; 1500 tokens,
+// 200 x 2048 36.0 and 34.5; sums of long lists one after another took 142 us at 4096 tokens.
+constexpr int kDirect = 2048, kDirectLongs = kDirect / (kPiece + 1), kDirectPieces = kDirect / kPiece + kDirectLongs;
+constexpr int kDirectIds = 64;
+bool direct(const mamba_embedding_shape& s) { return s.tokens <= kDirect && s.dim <= 1 << 16; }  // 65536 blocks of columns at most
+
+template <typename S, int V, typename I>
+__global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int tokens, int64_t vocab, const S* dy, S* dweight,
+                                                      int64_t dim, float scale) {
+    using P = Pack<S, V>;
+    constexpr int U = kDirect / 1024;      // groups of 64 tokens a wave looks through
+    __shared__ uint32_t s_list[kDirect];   // token, and its id less v0 in the upper half; in token order
+    __shared__ int s_count[16], s_longs[kDirectLongs], s_long_n[kDirectLongs], s_nlong;
+    __shared__ int s_tok[16][kPiece];
+    __shared__ float s_part[kDirectPieces][64 * V];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t v0 = (int64_t)blockIdx.x * kDirectIds, c = (int64_t)blockIdx.y * 64 * V + lane * V;
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+
+    const int groups = ((tokens + 63) / 64 + 15) / 16;  // of each wave
+    int64_t id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int t = (wave * groups + u) * 64 + lane;
+        id[u] = tokens > 0 ? id_at<I>(ids, t < tokens ? t : 0) : -1;
+        if (u >= groups || t >= tokens || id[u] >= vocab) id[u] = -1;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mine += (int)__popcll(__ballot(id[u] >= v0 && id[u] < v0 + kDirectIds));
+    if (lane == 0) s_count[wave] = mine;
+    if (threadIdx.x == 0) s_nlong = 0;
+    __syncthreads();
+    int at = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        at += w < wave ? s_count[w] : 0;
+        all += s_count[w];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool hit = id[u] >= v0 && id[u] < v0 + kDirectIds;
+        const uint64_t hits = __ballot(hit);
+        if (hit) s_list[at + __popcll(hits & below)] = (uint32_t)((wave * groups + u) * 64 + lane) | (uint32_t)(id[u] - v0) << 16;
+        at += (int)__popcll(hits);
+    }
+    __syncthreads();
+
+    // the tokens `from` .. `from` + kPiece - 1 of a local id into the wave's s_tok; how many it has in all
+    auto gather = [&](int local, int from) {
+        int n = 0;
+        for (int k = 0; k < all; k += 64) {
+            const uint32_t e = k + lane < all ? s_list[k + lane] : 0xFFFFFFFFu;
+            const uint64_t hits = __ballot((int)(e >> 16) == local);
+            const int rank = n + (int)__popcll(hits & below) - from;
+            if ((hits >> lane & 1) && rank >= 0 && rank < kPiece) s_tok[wave][rank] = (int)(e & 0xFFFFu);
+            n += (int)__popcll(hits);
+        }
+        return n;
+    };
+    auto store = [&](int64_t v, const float* s) {
+        if (c >= dim) return;
+        P o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(s[j] * scale);
+        *reinterpret_cast<P*>(dweight + v * dim + c) = o;
+    };
+    for (int local = wave; local < kDirectIds && v0 + local < vocab; local += 16) {
+        const int n = gather(local, 0);
+        if (n > kPiece) {
+            if (lane == 0) {
+                const int q = atomicAdd(&s_nlong, 1);
+                s_longs[q] = local, s_long_n[q] = n;
+            }
+            continue;
+        }
+        float s[V];
+        sum_rows<S, V>(dy, dim, c, lane < n ? s_tok[wave][lane] : 0, n, s);
+        store(v0 + local, s);
+    }
+    __syncthreads();
+    const int longs = s_nlong;
+    for (int q = 0, p = 0; q < longs; ++q)
+        for (int from = 0; from < s_long_n[q]; from += kPiece, ++p) {
+            if (p % 16 != wave) continue;
+            const int left = gather(s_longs[q], from) - from, n = left < kPiece ? left : kPiece;
+            float s[V];
+            sum_rows<S, V>(dy, dim, c, lane < n ? s_tok[wave][lane] : 0, n, s);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s_part[p][j * 64 + lane] = s[j];
+        }
+    __syncthreads();
+    for (int q = 0, p = 0; q < longs; ++q) {
+        const int pieces = (s_long_n[q] + kPiece - 1) / kPiece;
+        if (q % 16 == wave) {
+            float s[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = 0.0f;
+            for (int k = 0; k < pieces; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] += s_part[p + k][j * 64 + lane];
+            store(v0 + s_longs[q], s);
+        }
+        p += pieces;
+    }
+}
+
 // The pieces and the ids with up to kPiece tokens, a wave for every 64 packs of columns of each, in turns.
 template <typename S, int V>
 __global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l) {
@@ -392,11 +504,21 @@ int fwd_typed(const void* ids, const void* w, void* y, const mamba_embedding_sha
 template <typename S, typename I>
 int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_embedding_shape& s, float scale,
               hipStream_t stream) {
+    if (direct(s)) {
+        with_pack<S>(s.dim, dy, dw, [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            const dim3 grid((unsigned)((s.vocab + kDirectIds - 1) / kDirectIds), (unsigned)((s.dim + 64 * V - 1) / (64 * V)));
+            hipLaunchKernelGGL((direct_kernel<S, V, I>), grid, dim3(1024), 0, stream, ids, (int)s.tokens, s.vocab,
+                               static_cast<const S*>(dy), static_cast<S*>(dw), s.dim, scale);
+            return 0;
+        });
+        return launch_status();
+    }
     const Lists l = lists_of(ws, s);
     auto grid = [](int64_t n, int64_t per) { return dim3((unsigned)((n + per - 1) / per)); };
     const int64_t zb = (l.clear + 255) / 256;
     hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(zb < 2048 ? zb : 2048)), dim3(256), 0, stream, l.totals, l.clear);
-    if (s.tokens > 0) {
+    if (s.tokens > 0) {  // (a wide row of no tokens comes here too)
         hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
         hipLaunchKernelGGL(place_kernel, grid(s.vocab, 1024), dim3(1024), 0, stream, s.vocab, l);
         hipLaunchKernelGGL((fill_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
@@ -421,7 +543,7 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
 
 }  // namespace
 
-int64_t embedding_bwd_workspace(const mamba_embedding_shape& s) { return lists_of(nullptr, s).bytes; }
+int64_t embedding_bwd_workspace(const mamba_embedding_shape& s) { return direct(s) ? 0 : lists_of(nullptr, s).bytes; }
 
 int launch_embedding_fwd(const void* ids, bool ids64, const void* weight, void* y, const mamba_embedding_shape& s, float scale,
                          bool bf16, hipStream_t stream) {

@@ -146,9 +146,10 @@ def test_embedding_refusals(bwd):
                      (dict(out=a), ARGS)):
         assert embed(bwd, **kw) == code, kw
     if bwd:
-        assert embed(True, ws_bytes=4) == WORKSPACE
-        assert embed(True, ws=a + 3 * GAP + 8) == ARGS
-        assert embed(True, out=a + 3 * GAP) == ARGS
+        more = (3000, 30, 20)  # a few tokens need no workspace
+        assert embed(True, more, ws_bytes=4) == WORKSPACE
+        assert embed(True, more, ws=a + 3 * GAP + 8) == ARGS
+        assert embed(True, more, out=a + 3 * GAP) == ARGS
 
 
 def ffn(ptrs={}, shape=(40, 100, 60), act=0, dtype=scan.BF16, bwd=False):
@@ -195,6 +196,7 @@ def test_workspace_queries():
     assert lib.mamba_layer_norm_bwd_workspace_bytes(N(0, 8)) == 0
     assert lib.mamba_layer_norm_bwd_workspace_bytes(N(8, -1)) == SHAPE
     assert lib.mamba_embedding_bwd_workspace_bytes(E(8, 0, 4)) == 0
+    assert lib.mamba_embedding_bwd_workspace_bytes(E(2048, 100, 4)) == 0 < lib.mamba_embedding_bwd_workspace_bytes(E(2049, 100, 4))
     assert lib.mamba_embedding_bwd_workspace_bytes(E(8, 4, -1)) == SHAPE
     assert lib.mamba_gated_ffn_bwd_workspace_bytes(F(-1, 2, 3)) == SHAPE
     for s in ((0, 8, 8), (8, 0, 8), (8, 8, 0)):

@@ -10,6 +10,7 @@ rounding, at most 2^-8 of it (8 significant bits).
 import numpy as np
 import pytest
 import torch
+import torch.nn.functional as F
 
 import layers_ref as ref
 from selective_state_space_29_amd import layers
@@ -422,3 +423,32 @@ def test_embedding_offsets_past_32_bits():
     assert torch.equal(y[0], w[-1]) and bool((y[1] == 1).all())
     dw = layers.embedding_bwd(ids, y, V)
     assert torch.equal(dw[-1], y[0]) and bool((dw[0] == 1).all()) and not dw[1:-1].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab,dim", [(1, 8), (2, 520), (64, 33), (65, 1030), (700, 264), (5000, 6)])
+@pytest.mark.parametrize("power", [1, 6])
+def test_embedding_gradient_of_few_and_of_more_tokens_is_the_same(vocab, dim, dtype, power):
+    """Up to 2048 tokens take another kernel: padding that lifts a list above that changes no bit."""
+    g = gen(31 + vocab)
+    for tokens in (1, 63, 1000, 2048):
+        ids = (torch.rand(tokens, generator=g) ** power * vocab).long().to(DEV)
+        dy = torch.randn(tokens, dim, generator=g).to(dtype).to(DEV)
+        a = layers.embedding_bwd(ids, dy, vocab, 0.7)
+        b = layers.embedding_bwd(F.pad(ids, (0, 2100), value=-1), F.pad(dy, (0, 0, 0, 2100), value=float("nan")), vocab, 0.7)
+        assert torch.equal(a, b)
+        c = layers.embedding_bwd(F.pad(ids.int(), (0, 2048 - tokens), value=vocab), F.pad(dy, (0, 0, 0, 2048 - tokens)), vocab, 0.7)
+        assert torch.equal(a, c)
+        close(a, ref.embedding_bwd(ids.cpu(), dy.cpu(), vocab, 0.7), TOL * max(1, tokens / 200))
+
+
+def test_embedding_gradient_of_wide_rows_and_far_offsets():
+    wide = torch.randn(3, 70001, device=DEV)
+    ids = torch.tensor([1, 0, 1], device=DEV)
+    assert torch.equal(layers.embedding_bwd(ids, wide, 3), torch.stack([wide[1], wide[0] + wide[2], torch.zeros_like(wide[0])]))
+    V, D, N = 1_200_000, 2048, 2049
+    dy = torch.arange(D, device=DEV).to(BF16).expand(N, D)
+    ids = torch.full((N,), -1, device=DEV)
+    ids[7], ids[2040] = V - 1, 0
+    dw = layers.embedding_bwd(ids, dy, V)
+    assert torch.equal(dw[-1], dy[0]) and torch.equal(dw[0], dy[0]) and not dw[1:-1].any()
