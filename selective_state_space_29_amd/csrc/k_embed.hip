@@ -316,71 +316,99 @@ __device__ __forceinline__ void sum_rows(const S* dy, int64_t dim, int64_t c, in
     else if (n - k == 1) add(k, 1, std::integral_constant<int, 1>{});
 }
 
+// The tokens of kGroupIds ids, from v0 up, among all: a workgroup of 16 waves looks through up to G groups of
+// 64 tokens a wave, one stretch of the list each. s_sorted receives them by id and in token order, those of
+// v0 + k from s_start[k] to s_start[k + 1].
+constexpr int kGroupIds = 64;
+
+template <int G, typename I>
+__device__ __forceinline__ void find_tokens(const void* ids, int tokens, int64_t v0, int64_t vocab, uint16_t* s_sorted,
+                                            int (&s_at)[16][kGroupIds], int (&s_start)[kGroupIds + 1]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    const int stretch = (tokens + 1023) / 1024 * 64, begin = wave * stretch;
+    const int mine = tokens - begin < stretch ? tokens - begin : stretch;  // of this wave; may be negative
+    const uint32_t first = (uint32_t)v0, here = (uint32_t)(vocab - v0 < kGroupIds ? vocab - v0 : kGroupIds);
+    const I* from = static_cast<const I*>(ids) + (mine > 0 ? begin : 0);
+    int local[G];  // the id less v0, or -1
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+        const int k = u * 64 + lane;
+        const I id = mine > 0 ? from[k < mine ? k : 0] : (I)-1;
+        const uint32_t d = (uint32_t)id - first;
+        bool hit = k < mine && d < here;
+        if constexpr (sizeof(I) == 8) hit = hit && (uint32_t)((uint64_t)id >> 32) == 0;
+        local[u] = hit ? (int)d : -1;
+    }
+    s_at[wave][lane] = 0;
+    // each token found, in order, gets the place that s_at has for its id
+    auto walk = [&](auto&& to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            const int l = local[u];
+            const uint64_t hits = __ballot(l >= 0);
+            if (!hits) continue;
+            uint64_t same = hits;  // the lanes with this lane's id
+#pragma unroll
+            for (int b = 0; b < 6; ++b) {
+                const uint64_t set = __ballot(l >> b & 1);
+                same &= l >> b & 1 ? set : ~set;
+            }
+            if (l >= 0) {
+                const int at = s_at[wave][l], rank = (int)__popcll(same & below);
+                to(at + rank, begin + u * 64 + lane);
+                if (rank == 0) s_at[wave][l] = at + (int)__popcll(same);
+            }
+        }
+    };
+    walk([](int, int) {});
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        const int n = s_at[w][lane];
+        before += w < wave ? n : 0;
+        total += n;
+    }
+    int sum = total;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const int o = __shfl_up(sum, k, 64);
+        if (lane >= k) sum += o;
+    }
+    __syncthreads();
+    s_at[wave][lane] = sum - total + before;
+    if (wave == 0) {
+        s_start[lane] = sum - total;
+        if (lane == 63) s_start[kGroupIds] = sum;
+    }
+    walk([&](int at, int t) { s_sorted[at] = (uint16_t)t; });
+    __syncthreads();
+}
+
 // The whole gradient of few tokens in one launch and no workspace: a workgroup takes 64 ids and 64 packs of
 // columns, finds its ids' tokens among all of them, in order, and its 16 waves take an id in turn; those
 // with more than kPiece tokens afterwards, a piece a wave. The sums are those of the launches above, bit
 // for bit. Bound by its launch for few tokens, then by the workgroup that has the most frequent ids; with the
-// call's host side, this and the launches above, at uneven frequencies: 700 tokens, 5000 x 256 bf16 13.9 and
-// 34.6 us, 1500 tokens, 5000 x 1024 27.5 and 35.5, 2000 tokens, 50000 x 768 37.9 and 44.4; 1500 tokens,
-// 200 x 2048 36.0 and 34.5; sums of long lists one after another took 142 us at 4096 tokens.
+// call's host side, this and the launches above, at uneven frequencies: 128 tokens, 1000 x 256 bf16 12.4 and
+// 34.7 us, 1500 tokens, 5000 x 1024 21.6 and 35.5, 2000 tokens, 50000 x 768 33.5 and 44.4; 1500 tokens,
+// 200 x 2048 24.9 and 34.5. The same search through more tokens, with long lists left to a second launch, was
+// slower than counting (16384 tokens, 50000 x 768: 57 us against 48), as each group of ids reads them all.
 constexpr int kDirect = 2048, kDirectLongs = kDirect / (kPiece + 1), kDirectPieces = kDirect / kPiece + kDirectLongs;
-constexpr int kDirectIds = 64;
 bool direct(const mamba_embedding_shape& s) { return s.tokens <= kDirect && s.dim <= 1 << 16; }  // 65536 blocks of columns at most
 
 template <typename S, int V, typename I>
 __global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int tokens, int64_t vocab, const S* dy, S* dweight,
                                                       int64_t dim, float scale) {
     using P = Pack<S, V>;
-    constexpr int U = kDirect / 1024;      // groups of 64 tokens a wave looks through
-    __shared__ uint32_t s_list[kDirect];   // token, and its id less v0 in the upper half; in token order
-    __shared__ int s_count[16], s_longs[kDirectLongs], s_long_n[kDirectLongs], s_nlong;
-    __shared__ int s_tok[16][kPiece];
+    __shared__ uint16_t s_sorted[kDirect];
+    __shared__ int s_at[16][kGroupIds], s_start[kGroupIds + 1], s_longs[kDirectLongs], s_nlong;
     __shared__ float s_part[kDirectPieces][64 * V];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t v0 = (int64_t)blockIdx.x * kDirectIds, c = (int64_t)blockIdx.y * 64 * V + lane * V;
-    const uint64_t below = ((uint64_t)1 << lane) - 1;
-
-    const int groups = ((tokens + 63) / 64 + 15) / 16;  // of each wave
-    int64_t id[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int t = (wave * groups + u) * 64 + lane;
-        id[u] = tokens > 0 ? id_at<I>(ids, t < tokens ? t : 0) : -1;
-        if (u >= groups || t >= tokens || id[u] >= vocab) id[u] = -1;
-    }
-    int mine = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) mine += (int)__popcll(__ballot(id[u] >= v0 && id[u] < v0 + kDirectIds));
-    if (lane == 0) s_count[wave] = mine;
+    const int64_t v0 = (int64_t)blockIdx.x * kGroupIds, c = (int64_t)blockIdx.y * 64 * V + lane * V;
     if (threadIdx.x == 0) s_nlong = 0;
-    __syncthreads();
-    int at = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-        at += w < wave ? s_count[w] : 0;
-        all += s_count[w];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const bool hit = id[u] >= v0 && id[u] < v0 + kDirectIds;
-        const uint64_t hits = __ballot(hit);
-        if (hit) s_list[at + __popcll(hits & below)] = (uint32_t)((wave * groups + u) * 64 + lane) | (uint32_t)(id[u] - v0) << 16;
-        at += (int)__popcll(hits);
-    }
-    __syncthreads();
+    find_tokens<kDirect / 1024, I>(ids, tokens, v0, vocab, s_sorted, s_at, s_start);
 
-    // the tokens `from` .. `from` + kPiece - 1 of a local id into the wave's s_tok; how many it has in all
-    auto gather = [&](int local, int from) {
-        int n = 0;
-        for (int k = 0; k < all; k += 64) {
-            const uint32_t e = k + lane < all ? s_list[k + lane] : 0xFFFFFFFFu;
-            const uint64_t hits = __ballot((int)(e >> 16) == local);
-            const int rank = n + (int)__popcll(hits & below) - from;
-            if ((hits >> lane & 1) && rank >= 0 && rank < kPiece) s_tok[wave][rank] = (int)(e & 0xFFFFu);
-            n += (int)__popcll(hits);
-        }
-        return n;
-    };
     auto store = [&](int64_t v, const float* s) {
         if (c >= dim) return;
         P o;
@@ -388,33 +416,30 @@ __global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int token
         for (int j = 0; j < V; ++j) o.v[j] = from_f32<S>(s[j] * scale);
         *reinterpret_cast<P*>(dweight + v * dim + c) = o;
     };
-    for (int local = wave; local < kDirectIds && v0 + local < vocab; local += 16) {
-        const int n = gather(local, 0);
+    for (int local = wave; local < kGroupIds && v0 + local < vocab; local += 16) {
+        const int from = s_start[local], n = s_start[local + 1] - from;
         if (n > kPiece) {
-            if (lane == 0) {
-                const int q = atomicAdd(&s_nlong, 1);
-                s_longs[q] = local, s_long_n[q] = n;
-            }
+            if (lane == 0) s_longs[atomicAdd(&s_nlong, 1)] = local;
             continue;
         }
         float s[V];
-        sum_rows<S, V>(dy, dim, c, lane < n ? s_tok[wave][lane] : 0, n, s);
+        sum_rows<S, V>(dy, dim, c, lane < n ? s_sorted[from + lane] : 0, n, s);
         store(v0 + local, s);
     }
     __syncthreads();
     const int longs = s_nlong;
     for (int q = 0, p = 0; q < longs; ++q)
-        for (int from = 0; from < s_long_n[q]; from += kPiece, ++p) {
+        for (int from = s_start[s_longs[q]]; from < s_start[s_longs[q] + 1]; from += kPiece, ++p) {
             if (p % 16 != wave) continue;
-            const int left = gather(s_longs[q], from) - from, n = left < kPiece ? left : kPiece;
+            const int left = s_start[s_longs[q] + 1] - from, n = left < kPiece ? left : kPiece;
             float s[V];
-            sum_rows<S, V>(dy, dim, c, lane < n ? s_tok[wave][lane] : 0, n, s);
+            sum_rows<S, V>(dy, dim, c, lane < n ? s_sorted[from + lane] : 0, n, s);
 #pragma unroll
             for (int j = 0; j < V; ++j) s_part[p][j * 64 + lane] = s[j];
         }
     __syncthreads();
     for (int q = 0, p = 0; q < longs; ++q) {
-        const int pieces = (s_long_n[q] + kPiece - 1) / kPiece;
+        const int l = s_longs[q], pieces = (s_start[l + 1] - s_start[l] + kPiece - 1) / kPiece;
         if (q % 16 == wave) {
             float s[V];
 #pragma unroll
@@ -422,7 +447,7 @@ __global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int token
             for (int k = 0; k < pieces; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) s[j] += s_part[p + k][j * 64 + lane];
-            store(v0 + s_longs[q], s);
+            store(v0 + l, s);
         }
         p += pieces;
     }
@@ -507,7 +532,7 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
     if (direct(s)) {
         with_pack<S>(s.dim, dy, dw, [&](auto v) {
             constexpr int V = decltype(v)::value;
-            const dim3 grid((unsigned)((s.vocab + kDirectIds - 1) / kDirectIds), (unsigned)((s.dim + 64 * V - 1) / (64 * V)));
+            const dim3 grid((unsigned)((s.vocab + kGroupIds - 1) / kGroupIds), (unsigned)((s.dim + 64 * V - 1) / (64 * V)));
             hipLaunchKernelGGL((direct_kernel<S, V, I>), grid, dim3(1024), 0, stream, ids, (int)s.tokens, s.vocab,
                                static_cast<const S*>(dy), static_cast<S*>(dw), s.dim, scale);
             return 0;
