@@ -9,11 +9,15 @@ namespace {
 constexpr int kStepMaxLen = 8;  // calls up to this length run the short kernel
 
 // Workgroups per chain of 64 channels of a batch: as many as fill the GPU (a workgroup of 16 waves is all
-// a compute unit holds) where there are fewer chains, and chunks for each.
+// a compute unit holds) where there are fewer chains, down to one chunk for each (1 x 2000 x 2560 forward
+// 29.6 us, 41.8 with four chunks for each; 2 x 3000 x 512 forward and backward 70 and 105). Short rows are
+// not shared: clearing the chain and waiting costs more (1 x 500 x 700 fp32 forward and backward 46 us
+// alone, 53 shared; 3 x 777 x 1000 forward 28 and 22).
+constexpr int kShareLen = 640;
 int ways_for(const mamba_gated_shape& s, int cus, int chunk) {
     const int64_t chains = s.batch * ((s.dim + kChans - 1) / kChans), chunks = (s.len + chunk - 1) / chunk;
-    int64_t w = chains > 0 ? cus / chains : 1;
-    if (w > chunks / 4) w = chunks / 4;
+    if (chains < 1 || s.len < kShareLen) return 1;
+    const int64_t w = cus / chains < chunks ? cus / chains : chunks;
     return w < 1 ? 1 : (int)w;
 }
 
