@@ -22,7 +22,8 @@
 // through memory that all XCDs see: 1855 us at 4 x 100000 x 1024 where 64 unshared workgroups take 1336.)
 // Every wait ends: of the chunks not yet done, the first is the earliest ticket of the workgroup that
 // holds it (tickets are taken in rising order, up to two ahead), so it is being worked on, and what it
-// waits for belongs to chunks before it.
+// waits for belongs to chunks before it. (fp32 workgroups scan their next chunk, which waits for nothing,
+// before they finish one.)
 #pragma once
 
 #include <type_traits>
@@ -74,27 +75,46 @@ struct GatedBwdParams {
 constexpr int kGatedCk = MAMBA_GATED_CHECKPOINT;
 
 // Steps of a run of the forward. Alone on its chain a workgroup walks 128-step chunks (8 x 2048 x 1536
-// bf16: 58 us; 64 with 256 steps, where the first chunk's load and the last one's stores stand alone, and
-// 62 with 128 steps loaded two chunks ahead). Chained workgroups exchange a pair per chunk, and 256 steps
-// halve that (4 x 100000 x 1024: 1002 us, 1366 with 128); fp32 rows take twice the registers and keep 128.
+// bf16, before the loop's last savings: 58 us; 64 with 256 steps, where the first chunk's load and the last
+// one's stores stand alone, and 62 with 128 steps loaded two chunks ahead). Chained workgroups exchange a
+// pair per chunk, and 256 steps halve that (4 x 100000 x 1024 bf16: 926 us; 1130 with 128 whose states wait
+// for the next chunk, 1366 with 128 as they come); fp32 loads take twice the bytes and keep 128.
+//
+// Bound by the VALU and HBM together: an element takes 24 vector instructions and 6 transcendental ones (30
+// and 6 with copies of the loaded values and without the DPP forms below). 8 x 2048 x 1536 bf16 54.5 us, 3.7
+// TB/s with 192 of 256 compute units at work; 32 x 2000 x 2500 290 us, 4.4 TB/s; 8 x 2048 x 1536 fp32 90 us,
+// 4.5 TB/s; a large copy reaches 4.6.
 constexpr int gated_fwd_ts(int bytes, bool chain) { return bytes == 2 && chain ? 16 : 8; }
 
-__device__ __forceinline__ float sigmoid_f(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
+__device__ __forceinline__ float sigmoid_of_scaled(float s) { return hw_rcp(1.0f + hw_exp2(s)); }  // s = -log2(e) v
+__device__ __forceinline__ float sigmoid_f(float v) { return sigmoid_of_scaled(-v * kLog2e); }
+// Computes a value here: what was loaded for a chunk becomes what the chunk works on, without a copy, before
+// the next chunk's loads take its registers.
+__device__ __forceinline__ float here(float v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
-// 1 - a^2 = 1 - e^-v at v = 2 ln(2) e, given a. Below v = 1/4 the series
+// 1 - a^2 = 1 - e^-v at v = 2 ln(2) e, given a. For fp32 activations, below v = 1/4 the series
 // v (1 - v/2 + v^2/6 - v^3/24 + v^4/120 - v^5/720), coefficients scaled to e (truncation below 2^-24
-// relative); above, 1 - a^2 in one rounding, whose cancellation costs at most 3.6 times a's own error.
+// relative); above, 1 - a^2 in one rounding, whose cancellation costs at most 3.6 times a's own error. For
+// bf16, whose results are rounded by 2^-9, three terms below v = 1/64: 2^-17 at most from cancellation, and
+// 3 instructions an element fewer.
+template <typename S>
 __device__ __forceinline__ float one_minus_sq(float e, float a) {
     constexpr float k = 1.3862943611198906f;  // 2 ln 2
     constexpr float c1 = k, c2 = -k * k / 2, c3 = k * k * k / 6, c4 = -k * k * k * k / 24,
                     c5 = k * k * k * k * k / 120, c6 = -k * k * k * k * k * k / 720;
-    float q = __builtin_fmaf(e, c6, c5);
-    q = __builtin_fmaf(e, q, c4);
-    q = __builtin_fmaf(e, q, c3);
+    float q = c3;
+    if constexpr (sizeof(S) == 4) {
+        q = __builtin_fmaf(e, c6, c5);
+        q = __builtin_fmaf(e, q, c4);
+        q = __builtin_fmaf(e, q, c3);
+    }
     q = __builtin_fmaf(e, q, c2);
     q = __builtin_fmaf(e, q, c1);
     const float big = __builtin_fmaf(-a, a, 1.0f);
-    return e < 0.25f / k ? e * q : big;
+    return e < (sizeof(S) == 4 ? 0.25f : 0.015625f) / k ? e * q : big;
 }
 
 // a h + b of the recurrence and of its folds. A reset's decay is exactly 0 and has to forget a state
@@ -115,7 +135,7 @@ __device__ __forceinline__ float decay_mul(float a, float v) {
 }
 template <bool RESET>
 __device__ __forceinline__ float pair_product(float a, float b) {
-    if constexpr (RESET) return a > 0.0f && b > 0.0f ? __builtin_fmaxf(a * b, kMinDecay) : 0.0f;
+    if constexpr (RESET) return __builtin_fmaxf(a * b, __builtin_fminf(__builtin_fminf(a, b), kMinDecay));
     return a * b;
 }
 // The decay of a run, 2^-e, and of a step: `on` is whether the step is a reset.
@@ -235,22 +255,40 @@ __device__ __forceinline__ void row_scan(float& a, float& h) {
         h = decay_fma<RESET>(a, ph, h);
         a = pair_product<RESET>(a, pa);
     };
+    if constexpr (!RESET) {  // the same with the lane shift inside the instructions: lanes without a source keep a, add 0 to h
+#define MSCAN_ROW_STEP(N)                                                                                             \
+    if constexpr (UP)                                                                                                 \
+        asm("s_nop 1\n\tv_fmac_f32_dpp %1, %1, %0 row_shr:" #N " row_mask:0xf bank_mask:0xf bound_ctrl:0\n\t"          \
+            "v_mul_f32_dpp %0, %0, %0 row_shr:" #N " row_mask:0xf bank_mask:0xf"                                      \
+            : "+v"(a), "+v"(h));                                                                                      \
+    else                                                                                                              \
+        asm("s_nop 1\n\tv_fmac_f32_dpp %1, %1, %0 row_shl:" #N " row_mask:0xf bank_mask:0xf bound_ctrl:0\n\t"          \
+            "v_mul_f32_dpp %0, %0, %0 row_shl:" #N " row_mask:0xf bank_mask:0xf"                                      \
+            : "+v"(a), "+v"(h))
+        MSCAN_ROW_STEP(1);
+        MSCAN_ROW_STEP(2);
+        MSCAN_ROW_STEP(4);
+        MSCAN_ROW_STEP(8);
+        return;
+    }
     step(dpp_from<shift + 1>(a, 1.0f), dpp_from<shift + 1>(h, 0.0f));
     step(dpp_from<shift + 2>(a, 1.0f), dpp_from<shift + 2>(h, 0.0f));
     step(dpp_from<shift + 4>(a, 1.0f), dpp_from<shift + 4>(h, 0.0f));
     step(dpp_from<shift + 8>(a, 1.0f), dpp_from<shift + 8>(h, 0.0f));
 }
 
-// The value entering chunk `cur` of a chain's walk, in every lane of the channel's DPP row: `pair` is the
-// chunk's own, published first; `first` enters chunk 0.
+// The pair of chunk `cur` of a chain's walk, for the chunks after it.
+__device__ __forceinline__ void chain_publish(const GatedChain& c, int64_t b, int64_t D, int64_t ds, bool owner, int n, int cur,
+                                              float2 pair) {
+    if (!owner) return;
+    uint64_t* w = c.pairs + ((b * n + cur) * D + ds) * 2;
+    word_put(w, pair.x);
+    word_put(w + 1, pair.y);
+}
+// The value entering chunk `cur`, in every lane of the channel's DPP row; `first` enters chunk 0.
 template <bool RESET>
-__device__ __forceinline__ float chain_entry(const GatedChain& c, int64_t b, int64_t D, int64_t ds, bool live, int n, int cur,
-                                             int row_lane, float2 pair, float first) {
-    if (row_lane == 15 && live) {
-        uint64_t* w = c.pairs + ((b * n + cur) * D + ds) * 2;
-        word_put(w, pair.x);
-        word_put(w + 1, pair.y);
-    }
+__device__ __forceinline__ float chain_state(const GatedChain& c, int64_t b, int64_t D, int64_t ds, int n, int cur, int row_lane,
+                                             float first) {
     const int block = cur / 16, j = cur % 16;
     float a = 1.0f, h = 0.0f, state = first;
     if (row_lane < j) {
@@ -377,61 +415,155 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
     };
     if (walk.cur < n) fetch(walk.cur);
     walk.second();
-    auto chunk = [&](auto tail) __attribute__((always_inline)) {
-        constexpr bool TAIL = decltype(tail)::value;
-        const int64_t t0 = (int64_t)walk.cur * STEPS, tr = t0 + run * TS;
-        S cx[TS], cr[TS], ci[TS];
-#pragma unroll
-        for (int k = 0; k < TS; ++k) cx[k] = nx[k], cr[k] = nr[k], ci[k] = ni[k];
-        const uint64_t bits = nbits;
-        walk.ask();
-        if (walk.next < n) fetch(walk.next);
-        const int left = (int)(L - tr < TS ? L - tr : TS);  // steps of this run that exist
 
-        float a[TS], bb[TS], esum = 0.0f, h = 0.0f;
-#pragma unroll
-        for (int k = 0; k < TS; ++k) {
-            float e = tl * sigmoid_f(to_f32(cr[k]));
-            a[k] = decay_step<RESET>(e, (bits >> k) & 1);
-            const float m = __builtin_amdgcn_sqrtf(one_minus_sq(e, a[k]));
-            bb[k] = m * (sigmoid_f(to_f32(ci[k])) * to_f32(cx[k]));
-            if constexpr (TAIL) {  // past the end the state is carried
-                if (k >= left) {
-                    a[k] = 1.0f;
-                    bb[k] = e = 0.0f;
-                }
-            }
-            esum += e;
-            h = decay_fma<RESET>(a[k], h, bb[k]);
-        }
-        s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), h);
-        __syncthreads();
-        {
-            float2 v = s_pair[s_run * kPitch + s_ch];
-            row_scan<true, RESET>(v.x, v.y);
-            if constexpr (CHAIN) carry = chain_entry<RESET>(chain, b, D, ds, s_live, n, walk.cur, s_run, v, first);
-            const float after = decay_fma<RESET>(v.x, carry, v.y);
-            if constexpr (CHAIN) chain_exit(chain, b, D, ds, s_live && s_run == 15, n, walk.cur, after);
-            s_in[s_run * kPitch + s_ch] = dpp_from<kRowShr + 1>(after, carry);
-            carry = dpp_from<kRowBcast + 15>(after, 0.0f);
-        }
-        __syncthreads();
-        float in = s_in[run * kPitch + lane];
-        if (p.ck && live && tr % kGatedCk == 0 && left > 0) p.ck[(b * p.nck + tr / kGatedCk) * D + d] = in;
-        if (STATES) {
-            const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + tr * y.st);
+    const int whole = (int)(L / STEPS);
+    // bf16 runs of 16 steps have no registers for a second chunk's (4 x 100000 x 1024: 3500 us with it, 926 without)
+    constexpr bool DEFER = CHAIN && sizeof(S) == 4;
+    if constexpr (!DEFER) {
+        auto chunk = [&](auto tail) __attribute__((always_inline)) {
+            constexpr bool TAIL = decltype(tail)::value;
+            const int64_t t0 = (int64_t)walk.cur * STEPS, tr = t0 + run * TS;
+            float cx[TS], cr[TS], ci[TS];
 #pragma unroll
             for (int k = 0; k < TS; ++k) {
-                in = decay_fma<RESET>(a[k], in, bb[k]);
-                row_store(from_f32<S>(in), o, live && (!TAIL || k < left) ? y.off : kGatedDrop, k * y.row_bytes());
+                cr[k] = here(to_f32(nr[k]) * -kLog2e);
+                ci[k] = here(to_f32(ni[k]) * -kLog2e);
+                cx[k] = here(to_f32(nx[k]));
             }
-            if (p.last && walk.cur == n - 1 && s_run == 15 && s_live) p.last[b * D + ds] = carry;
-        }
-        walk.advance();
-    };
-    const int whole = (int)(L / STEPS);
-    while (walk.cur < whole) chunk(std::false_type{});
-    if (walk.cur < n) chunk(std::true_type{});
+            const uint64_t bits = nbits;
+            walk.ask();
+            if (walk.next < n) fetch(walk.next);
+            const int left = (int)(L - tr < TS ? L - tr : TS);  // steps of this run that exist
+            float a[TS], bb[TS], esum = 0.0f, h = 0.0f;
+#pragma unroll
+            for (int k = 0; k < TS; ++k) {
+                float e = tl * sigmoid_of_scaled(cr[k]);
+                a[k] = decay_step<RESET>(e, (bits >> k) & 1);
+                const float m = __builtin_amdgcn_sqrtf(one_minus_sq<S>(e, a[k]));
+                bb[k] = m * (sigmoid_of_scaled(ci[k]) * cx[k]);
+                if constexpr (TAIL) {  // past the end the state is carried
+                    if (k >= left) {
+                        a[k] = 1.0f;
+                        bb[k] = e = 0.0f;
+                    }
+                }
+                esum += e;
+                h = decay_fma<RESET>(a[k], h, bb[k]);
+            }
+            s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), h);
+            __syncthreads();
+            {
+                float2 v = s_pair[s_run * kPitch + s_ch];
+                row_scan<true, RESET>(v.x, v.y);
+                if constexpr (CHAIN) {
+                    chain_publish(chain, b, D, ds, s_live && s_run == 15, n, walk.cur, v);
+                    carry = chain_state<RESET>(chain, b, D, ds, n, walk.cur, s_run, first);
+                }
+                const float after = decay_fma<RESET>(v.x, carry, v.y);
+                if constexpr (CHAIN) chain_exit(chain, b, D, ds, s_live && s_run == 15, n, walk.cur, after);
+                s_in[s_run * kPitch + s_ch] = dpp_from<kRowShr + 1>(after, carry);
+                carry = dpp_from<kRowBcast + 15>(after, 0.0f);
+            }
+            __syncthreads();
+            float in = s_in[run * kPitch + lane];
+            if (p.ck && live && tr % kGatedCk == 0 && left > 0) p.ck[(b * p.nck + tr / kGatedCk) * D + d] = in;
+            if (STATES) {
+                const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + tr * y.st);
+#pragma unroll
+                for (int k = 0; k < TS; ++k) {
+                    in = decay_fma<RESET>(a[k], in, bb[k]);
+                    row_store(from_f32<S>(in), o, live && (!TAIL || k < left) ? y.off : kGatedDrop, k * y.row_bytes());
+                }
+                if (p.last && walk.cur == n - 1 && s_run == 15 && s_live) p.last[b * D + ds] = carry;
+            }
+            walk.advance();
+        };
+        while (walk.cur < whole) chunk(std::false_type{});
+        if (walk.cur < n) chunk(std::true_type{});
+    } else {
+        // A chunk's states wait until the workgroup's next chunk is scanned: its neighbours' pairs are there by
+        // then, and whoever has chunks before it finishes them without waiting for this one (2 x 8000 x 1024 fp32
+        // forward: 65 us, 82 without). The steps are written out again: sharing code with the loop above costs
+        // that one spilled registers (4 x 100000 x 1024 bf16: 970 us instead of 926).
+        int held = -1;
+        float a[TS], bb[TS];
+        float2 pairs = make_float2(1.0f, 0.0f);
+        auto resolve = [&]() __attribute__((always_inline)) {
+            carry = chain_state<RESET>(chain, b, D, ds, n, held, s_run, first);
+            const float after = decay_fma<RESET>(pairs.x, carry, pairs.y);
+            chain_exit(chain, b, D, ds, s_live && s_run == 15, n, held, after);
+            s_in[s_run * kPitch + s_ch] = dpp_from<kRowShr + 1>(after, carry);
+            carry = dpp_from<kRowBcast + 15>(after, 0.0f);
+        };
+        auto finish = [&](auto tail) __attribute__((always_inline)) {
+            constexpr bool TAIL = decltype(tail)::value;
+            const int64_t tr = (int64_t)held * STEPS + run * TS;
+            const int left = (int)(L - tr < TS ? L - tr : TS);
+            float in = s_in[run * kPitch + lane];
+            if (p.ck && live && tr % kGatedCk == 0 && left > 0) p.ck[(b * p.nck + tr / kGatedCk) * D + d] = in;
+            if (STATES) {
+                const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + tr * y.st);
+#pragma unroll
+                for (int k = 0; k < TS; ++k) {
+                    in = decay_fma<RESET>(a[k], in, bb[k]);
+                    row_store(from_f32<S>(in), o, live && (!TAIL || k < left) ? y.off : kGatedDrop, k * y.row_bytes());
+                }
+                if (p.last && held == n - 1 && s_run == 15 && s_live) p.last[b * D + ds] = carry;
+            }
+        };
+        auto chunk = [&](auto tail) __attribute__((always_inline)) {
+            constexpr bool TAIL = decltype(tail)::value;
+            const int64_t tr = (int64_t)walk.cur * STEPS + run * TS;
+            float cx[TS], cr[TS], ci[TS], na[TS], nb[TS];
+#pragma unroll
+            for (int k = 0; k < TS; ++k) {
+                cr[k] = here(to_f32(nr[k]) * -kLog2e);
+                ci[k] = here(to_f32(ni[k]) * -kLog2e);
+                cx[k] = here(to_f32(nx[k]));
+            }
+            const uint64_t bits = nbits;
+            walk.ask();
+            if (walk.next < n) fetch(walk.next);
+            const int left = (int)(L - tr < TS ? L - tr : TS);  // steps of this run that exist
+            float esum = 0.0f, h = 0.0f;
+#pragma unroll
+            for (int k = 0; k < TS; ++k) {
+                float e = tl * sigmoid_of_scaled(cr[k]);
+                na[k] = decay_step<RESET>(e, (bits >> k) & 1);
+                const float m = __builtin_amdgcn_sqrtf(one_minus_sq<S>(e, na[k]));
+                nb[k] = m * (sigmoid_of_scaled(ci[k]) * cx[k]);
+                if constexpr (TAIL) {  // past the end the state is carried
+                    if (k >= left) {
+                        na[k] = 1.0f;
+                        nb[k] = e = 0.0f;
+                    }
+                }
+                esum += e;
+                h = decay_fma<RESET>(na[k], h, nb[k]);
+            }
+            s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), h);
+            __syncthreads();
+            float2 v = s_pair[s_run * kPitch + s_ch];
+            row_scan<true, RESET>(v.x, v.y);
+            chain_publish(chain, b, D, ds, s_live && s_run == 15, n, walk.cur, v);
+            if (held >= 0) resolve();
+            __syncthreads();
+            if (held >= 0) finish(std::false_type{});
+#pragma unroll
+            for (int k = 0; k < TS; ++k) a[k] = na[k], bb[k] = nb[k];
+            pairs = v;
+            held = walk.cur;
+            walk.advance();
+        };
+        while (walk.cur < whole) chunk(std::false_type{});
+        if (walk.cur < n) chunk(std::true_type{});
+        if (held < 0) return;
+        __syncthreads();
+        resolve();
+        __syncthreads();
+        if (held < whole) finish(std::false_type{});
+        else finish(std::true_type{});
+    }
 }
 
 // Short calls (decode): one thread per channel of a batch, step after step.
@@ -454,7 +586,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p) {
             h = 0.0f;
         }
         const float a = hw_exp2(-e);
-        const float m = __builtin_amdgcn_sqrtf(one_minus_sq(e, a));
+        const float m = __builtin_amdgcn_sqrtf(one_minus_sq<S>(e, a));
         h = __builtin_fmaf(a, h, m * (sigmoid_f(to_f32(i[t * p.si_t])) * to_f32(x[t * p.sx_t])));
         y[t * p.sy_t] = from_f32<S>(h);
     }
@@ -541,31 +673,36 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
         constexpr bool TAIL = decltype(tail)::value;
         const int which = n - 1 - walk.cur;
         const int64_t tr = (int64_t)which * STEPS + run * TS;
-        S cx[TS], cr[TS], ci[TS], cg[TS];
+        auto start = [](float v) __attribute__((always_inline)) { return CHAIN ? v : here(v); };  // (chained: 44 spills with it, 19 without)
+        float cx[TS], cr[TS], ci[TS], g[TS];
 #pragma unroll
-        for (int k = 0; k < TS; ++k) cx[k] = nx[k], cr[k] = nr[k], ci[k] = ni[k], cg[k] = ng[k];
+        for (int k = 0; k < TS; ++k) {
+            cr[k] = start(to_f32(nr[k]) * -kLog2e);
+            g[k] = start(to_f32(ng[k]));
+            ci[k] = start(to_f32(ni[k]) * -kLog2e);
+            cx[k] = start(to_f32(nx[k]));
+        }
         const uint64_t bits = nbits;
         const float ck = nck;
         walk.ask();
         if (walk.next < n) fetch_as(n - 1 - walk.next, std::true_type{});  // only the walk's first chunk is cut short
         const int left = (int)(L - tr < TS ? L - tr : TS);
 
-        float e[TS], a[TS], bb[TS], ms[TS], bi[TS], z[TS], g[TS];
+        float e[TS], a[TS], bb[TS], ms[TS], bi[TS], z[TS];
         float esum = 0.0f, hl = 0.0f, mu = 0.0f;
 #pragma unroll
         for (int k = 0; k < TS; ++k) {
             const bool past = TAIL && k >= left;
-            e[k] = tl * sigmoid_f(to_f32(cr[k]));
+            e[k] = tl * sigmoid_of_scaled(cr[k]);
             a[k] = decay_step<RESET>(e[k], (bits >> k) & 1);
-            g[k] = to_f32(cg[k]);
             if constexpr (TAIL) {  // past the end the state and the adjoint are carried
                 if (past) a[k] = 1.0f, e[k] = g[k] = 0.0f;
             }
             esum += e[k];
-            const float w = one_minus_sq(e[k], a[k]);
+            const float w = one_minus_sq<S>(e[k], a[k]);
             const float rm = w > 1.1754944e-38f ? __builtin_amdgcn_rsqf(w) : 0.0f;  // 1 / m, or 0 with m
-            const float si = sigmoid_f(to_f32(ci[k]));
-            const float gx = past ? 0.0f : si * to_f32(cx[k]);
+            const float si = sigmoid_of_scaled(ci[k]);
+            const float gx = past ? 0.0f : si * cx[k];
             const float m = w * rm;
             ms[k] = m * si;
             bb[k] = m * gx;
@@ -582,9 +719,10 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
             float2 v = s_pair[s_run * kPitch + s_ch];
             float ra = v.x, rmu = s_mu[s_run * kPitch + s_ch];
             row_scan<false, RESET>(ra, rmu);
-            if constexpr (CHAIN)  // the chunk's adjoint pair is lane 0's, published by lane 15
-                carry = chain_entry<RESET>(chain, b, D, ds, s_live, n, walk.cur, s_run,
-                                           make_float2(dpp_from<kRowBcast + 0>(ra, 0.0f), dpp_from<kRowBcast + 0>(rmu, 0.0f)), first);
+            if constexpr (CHAIN) {
+                chain_publish(chain, b, D, ds, s_live && s_run == 0, n, walk.cur, make_float2(ra, rmu));
+                carry = chain_state<RESET>(chain, b, D, ds, n, walk.cur, s_run, first);
+            }
             const float after = decay_fma<RESET>(ra, carry, rmu);
             if constexpr (CHAIN) chain_exit(chain, b, D, ds, s_live && s_run == 0, n, walk.cur, after);
             float2 o;
