@@ -255,22 +255,20 @@ __device__ __forceinline__ void row_scan(float& a, float& h) {
         h = decay_fma<RESET>(a, ph, h);
         a = pair_product<RESET>(a, pa);
     };
-    if constexpr (!RESET) {  // the same with the lane shift inside the instructions: lanes without a source keep a, add 0 to h
-#define MSCAN_ROW_STEP(N)                                                                                             \
-    if constexpr (UP)                                                                                                 \
-        asm("s_nop 1\n\tv_fmac_f32_dpp %1, %1, %0 row_shr:" #N " row_mask:0xf bank_mask:0xf bound_ctrl:0\n\t"          \
-            "v_mul_f32_dpp %0, %0, %0 row_shr:" #N " row_mask:0xf bank_mask:0xf"                                      \
-            : "+v"(a), "+v"(h));                                                                                      \
-    else                                                                                                              \
-        asm("s_nop 1\n\tv_fmac_f32_dpp %1, %1, %0 row_shl:" #N " row_mask:0xf bank_mask:0xf bound_ctrl:0\n\t"          \
-            "v_mul_f32_dpp %0, %0, %0 row_shl:" #N " row_mask:0xf bank_mask:0xf"                                      \
-            : "+v"(a), "+v"(h))
-        MSCAN_ROW_STEP(1);
-        MSCAN_ROW_STEP(2);
-        MSCAN_ROW_STEP(4);
-        MSCAN_ROW_STEP(8);
+    // The same with the lane shift inside the instructions: lanes without a source keep a and add 0 to h. A
+    // DPP operand is read 2 wait states after its write at the earliest, also by what follows the block.
+#define MSCAN_ROW_STEP(DIR, N)                                                                    \
+    "s_nop 1\n\tv_fmac_f32_dpp %1, %1, %0 " DIR ":" N " row_mask:0xf bank_mask:0xf bound_ctrl:0\n\t" \
+    "v_mul_f32_dpp %0, %0, %0 " DIR ":" N " row_mask:0xf bank_mask:0xf\n\t"
+#define MSCAN_ROW_STEPS(DIR) \
+    MSCAN_ROW_STEP(DIR, "1") MSCAN_ROW_STEP(DIR, "2") MSCAN_ROW_STEP(DIR, "4") MSCAN_ROW_STEP(DIR, "8") "s_nop 1"
+    if constexpr (!RESET) {
+        if constexpr (UP) asm(MSCAN_ROW_STEPS("row_shr") : "+v"(a), "+v"(h));
+        else asm(MSCAN_ROW_STEPS("row_shl") : "+v"(a), "+v"(h));
         return;
     }
+#undef MSCAN_ROW_STEPS
+#undef MSCAN_ROW_STEP
     step(dpp_from<shift + 1>(a, 1.0f), dpp_from<shift + 1>(h, 0.0f));
     step(dpp_from<shift + 2>(a, 1.0f), dpp_from<shift + 2>(h, 0.0f));
     step(dpp_from<shift + 4>(a, 1.0f), dpp_from<shift + 4>(h, 0.0f));
