@@ -12,15 +12,15 @@
 //   fill     tokens into their id's stretch
 //   order    stretches above kPiece tokens copied in token order: up to kRank tokens by counting the
 //            smaller ones, more by walking all ids in order and keeping the id's
-//            (other workgroups of this launch write zeros for ids without tokens)
 //   reduce   one wave an id and 64 packs of columns: the sum of its rows, sorted by the wave itself up
-//            to kPiece tokens; pieces of longer stretches give partial sums
+//            to kPiece tokens; pieces of longer stretches give partial sums (other workgroups of this
+//            launch write zeros for ids without tokens)
 //   join     the partial sums of the long stretches, in order
 // Words are frequent unevenly, and integer atomics on one address are served one by one (1100 tokens of
-// one id among 16384 made the count 14 us, now 7), so a wave adds the tokens of an id at once.
+// one id among 16384 made the count 14 us, now 6), so a wave adds the tokens of an id at once.
 // The bytes that must move are dy read once and dweight written once: 102 MB, 22 us at the rate of a large
-// copy, at 16384 tokens (a quarter of them padding), 50000 x 768 bf16. Measured there: 48 us in seven
-// launches, of which zeros and order 15, reduce 11, count 8; the plain index_add form takes 295.
+// copy, at 16384 tokens (a quarter of them padding), 50000 x 768 bf16. Measured there: 44 us in seven
+// launches, of which sums and zeros 17, order 6, count 6, place 5; the plain index_add form takes 310.
 #include <type_traits>
 
 #include "layers_common.hpp"
@@ -122,24 +122,22 @@ __global__ __launch_bounds__(256) void zero_kernel(int* p, int64_t n) {
 struct Mates {
     int n, first, rank;
 };
-__device__ __forceinline__ Mates mates_of(int id, bool ok, int lane) {
-    Mates m{0, lane, 0};
-    for (uint64_t todo = __ballot(ok); todo;) {
-        const int first = __builtin_ctzll(todo), want = __builtin_amdgcn_readlane(id, first);
-        const uint64_t same = __ballot(ok && id == want);
-        if (ok && id == want) m = Mates{(int)__popcll(same), first, (int)__popcll(same & (((uint64_t)1 << lane) - 1))};
-        todo &= ~same;
+__device__ __forceinline__ Mates mates_of(int id, bool ok, int bits, int lane) {  // ids below 2^bits
+    uint64_t same = __ballot(ok);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot(id >> b & 1);
+        same &= id >> b & 1 ? set : ~set;
     }
-    return m;
+    return Mates{(int)__popcll(same), (int)__builtin_ctzll(same | (uint64_t)1 << 63), (int)__popcll(same & (((uint64_t)1 << lane) - 1))};
 }
 
 template <typename I>
-__global__ __launch_bounds__(256) void count_kernel(const void* ids, int64_t tokens, int64_t vocab, Lists l) {
+__global__ __launch_bounds__(256) void count_kernel(const void* ids, int64_t tokens, int64_t vocab, int bits, Lists l) {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int lane = threadIdx.x & 63;
     const int64_t id = t < tokens ? id_at<I>(ids, t) : -1;
     const bool ok = id >= 0 && id < vocab;
-    const Mates m = mates_of((int)id, ok, lane);
+    const Mates m = mates_of((int)id, ok, bits, lane);
     int base = 0;
     if (ok && m.first == lane) base = atomicAdd(&l.count[id], m.n);
     base = __shfl(base, m.first, 64);
@@ -203,12 +201,12 @@ __global__ __launch_bounds__(256) void fill_kernel(const void* ids, int64_t toke
     if (id >= 0 && id < vocab) l.list[l.start[id] + l.place[t]] = (int)t;
 }
 
-constexpr int kZeroIds = 64;  // ids a workgroup looks at for rows of zeros
+constexpr int kZeroIds = 16;  // ids a workgroup looks at for rows of zeros
 
 // Rows of zeros for the ids without tokens among kZeroIds.
 __device__ __forceinline__ void zero_rows(char* dweight, int64_t row_bytes, int64_t v0, int64_t vocab, const int* count) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int k = wave; k < kZeroIds; k += 16) {
+    for (int k = wave; k < kZeroIds; k += 4) {
         const int64_t v = v0 + k;
         if (v >= vocab || count[v] != 0) continue;
         char* row = dweight + v * row_bytes;
@@ -222,23 +220,17 @@ __device__ __forceinline__ void zero_rows(char* dweight, int64_t row_bytes, int6
     }
 }
 
-// The first `order` workgroups put long stretches into order, slice by slice; the others write the rows of
-// ids without tokens, which fill the memory system meanwhile.
+// Long stretches put into order, slice by slice.
 template <typename I>
-__global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t tokens, Lists l, int order, char* dweight,
-                                                     int64_t row_bytes, int64_t vocab) {
+__global__ __launch_bounds__(1024) void order_kernel(const void* ids, int64_t tokens, Lists l) {
     __shared__ __align__(16) int s_tok[kRank + 16];
     __shared__ int s_part[4][kSlice];
     constexpr int U = 8;  // of 1024 ids walked at a time
     __shared__ int s_hits[U][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     constexpr int slices = kRank / kSlice;
-    if ((int)blockIdx.x >= order) {
-        zero_rows(dweight, row_bytes, (int64_t)(blockIdx.x - order) * kZeroIds, vocab, l.count);
-        return;
-    }
     const int slice = blockIdx.x % slices;
-    for (int q = blockIdx.x / slices; q < l.totals[2]; q += order / slices) {
+    for (int q = blockIdx.x / slices; q < l.totals[2]; q += gridDim.x / slices) {
         const int id = l.longs[q], n = l.count[id], start = l.start[id];
         if (n <= kRank) {
             const int k0 = slice * kSlice;
@@ -454,14 +446,22 @@ __global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int token
 }
 
 // The pieces and the ids with up to kPiece tokens, a wave for every 64 packs of columns of each, in turns.
+// `zeros` workgroups, spread among the others, write the rows of ids without tokens meanwhile: those stream,
+// while the sums wait for rows from all over dy (as launches of their own 10 and 12 us, together 17).
 template <typename S, int V>
-__global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l) {
+__global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l, int zeros, int64_t vocab) {
     using P = Pack<S, V>;
+    const int64_t zero = (int64_t)blockIdx.x * zeros / gridDim.x;
+    if (((int64_t)blockIdx.x + 1) * zeros / gridDim.x > zero) {
+        zero_rows(reinterpret_cast<char*>(dweight), dim * (int64_t)sizeof(S), zero * kZeroIds, vocab, l.count);
+        return;
+    }
+    const int64_t block = (int64_t)blockIdx.x - zero, blocks = (int64_t)gridDim.x - zeros;
     const int lane = threadIdx.x & 63;
     const int cols = (int)((dim + 64 * V - 1) / (64 * V));
     const int pieces = l.totals[3], shorts = l.totals[1];
-    const int64_t items = (int64_t)(pieces + shorts) * cols, step = (int64_t)gridDim.x * 4;
-    for (int64_t k = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); k < items; k += step) {
+    const int64_t items = (int64_t)(pieces + shorts) * cols, step = blocks * 4;
+    for (int64_t k = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); k < items; k += step) {
         const int64_t q = k / cols, c = (k - q * cols) * 64 * V + lane * V;
         const bool whole = q >= pieces;  // of an id's tokens
         const int id = __builtin_amdgcn_readfirstlane(whole ? l.shorts[q - pieces] : l.piece_id[q]);
@@ -542,22 +542,23 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
     const Lists l = lists_of(ws, s);
     auto grid = [](int64_t n, int64_t per) { return dim3((unsigned)((n + per - 1) / per)); };
     const int64_t zb = (l.clear + 255) / 256;
+    int bits = 0;
+    while (s.vocab - 1 >> bits > 0) ++bits;
     hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(zb < 2048 ? zb : 2048)), dim3(256), 0, stream, l.totals, l.clear);
     if (s.tokens > 0) {  // (a wide row of no tokens comes here too)
-        hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
+        hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, bits, l);
         hipLaunchKernelGGL(place_kernel, grid(s.vocab, 1024), dim3(1024), 0, stream, s.vocab, l);
         hipLaunchKernelGGL((fill_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
     }
     const unsigned longs = (unsigned)(l.max_long < 512 ? l.max_long : 512);
-    const unsigned order = longs * (kRank / kSlice);
-    hipLaunchKernelGGL((order_kernel<I>), dim3(order + (unsigned)((s.vocab + kZeroIds - 1) / kZeroIds)), dim3(1024), 0, stream,
-                       ids, s.tokens, l, (int)order, static_cast<char*>(dw), s.dim * (int64_t)sizeof(S), s.vocab);
+    if (longs)
+        hipLaunchKernelGGL((order_kernel<I>), dim3(longs * (kRank / kSlice)), dim3(1024), 0, stream, ids, s.tokens, l);
     with_pack<S>(s.dim, dy, dw, [&](auto v) {
-        const int64_t cols = (s.dim + 64 * decltype(v)::value - 1) / (64 * decltype(v)::value);
-        const int64_t waves = (l.max_piece + l.max_short) * cols, most = (int64_t)layers_cus() * 64;
-        if (waves == 0) return 0;
-        hipLaunchKernelGGL((reduce_kernel<S, decltype(v)::value>), grid(waves < most ? waves : most, 4), dim3(256), 0, stream, static_cast<const S*>(dy),
-                           static_cast<S*>(dw), s.dim, scale, l);
+        constexpr int V = decltype(v)::value;
+        const int64_t waves = (l.max_piece + l.max_short) * ((s.dim + 64 * V - 1) / (64 * V)), most = (int64_t)layers_cus() * 64;
+        const int64_t zeros = (s.vocab + kZeroIds - 1) / kZeroIds, sums = ((waves < most ? waves : most) + 3) / 4;
+        hipLaunchKernelGGL((reduce_kernel<S, V>), dim3((unsigned)(zeros + sums)), dim3(256), 0, stream, static_cast<const S*>(dy),
+                           static_cast<S*>(dw), s.dim, scale, l, (int)zeros, s.vocab);
         return 0;
     });
     if (longs)

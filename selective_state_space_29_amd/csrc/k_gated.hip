@@ -42,14 +42,14 @@ __global__ __launch_bounds__(1024) void gated_dlam_kernel(const float* part, int
     dlam[d] = v < -20.0f ? s : s * (sigmoid_f(v) * hw_rcp(softplus_f(v)));
 }
 
-__global__ __launch_bounds__(256) void gated_clear_kernel(uint64_t* p, int64_t n) {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k < n) p[k] = 0;
+__global__ __launch_bounds__(256) void gated_clear_kernel(uint4* p, int64_t n) {
+    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) p[k] = make_uint4(0, 0, 0, 0);
 }
 
 void clear_chain(uint64_t* p, int64_t batch, int64_t dim, int64_t len, int chunk, hipStream_t stream) {
-    const int64_t words = GatedChain::words(batch, dim, (len + chunk - 1) / chunk);
-    hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream, p, words);
+    const int64_t n = (GatedChain::words(batch, dim, (len + chunk - 1) / chunk) + 1) / 2;  // the workspace ends on 256 bytes
+    const int64_t g = (n + 511) / 512;
+    hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), 0, stream, reinterpret_cast<uint4*>(p), n);
 }
 
 template <typename S, bool STATES>
