@@ -2,8 +2,8 @@
 //
 // Forward: one wave a token, 16 bytes a lane where rows allow it; bound by HBM.
 //
-// Gradient (of more than 2048 tokens; fewer: direct_kernel): dweight[v] = scale * sum of dy over the tokens of v. The tokens are gathered into one
-// list per id and each id's rows are added in token order, so every row of dweight is written exactly
+// Gradient, dweight[v] = scale * sum of dy over the tokens of v: up to 2048 tokens direct_kernel; more are
+// gathered into one list per id and each id's rows are added in token order, so every row of dweight is written exactly
 // once, by one wave, and the sums do not depend on timing:
 //   count    how many tokens each id has, and each token's place among its id's (in no order: whoever
 //            adds to the count first)
@@ -128,7 +128,8 @@ __device__ __forceinline__ Mates mates_of(int id, bool ok, int bits, int lane) {
         const uint64_t set = __ballot(id >> b & 1);
         same &= id >> b & 1 ? set : ~set;
     }
-    return Mates{(int)__popcll(same), (int)__builtin_ctzll(same | (uint64_t)1 << 63), (int)__popcll(same & (((uint64_t)1 << lane) - 1))};
+    return Mates{(int)__popcll(same), (int)__builtin_ctzll(same | (uint64_t)1 << 63),
+                 (int)__popcll(same & (((uint64_t)1 << lane) - 1))};
 }
 
 template <typename I>
@@ -449,7 +450,8 @@ __global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int token
 // `zeros` workgroups, spread among the others, write the rows of ids without tokens meanwhile: those stream,
 // while the sums wait for rows from all over dy (as launches of their own 10 and 12 us, together 17).
 template <typename S, int V>
-__global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l, int zeros, int64_t vocab) {
+__global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l, int zeros,
+                                                     int64_t vocab) {
     using P = Pack<S, V>;
     const int64_t zero = (int64_t)blockIdx.x * zeros / gridDim.x;
     if (((int64_t)blockIdx.x + 1) * zeros / gridDim.x > zero) {
@@ -543,7 +545,7 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
     auto grid = [](int64_t n, int64_t per) { return dim3((unsigned)((n + per - 1) / per)); };
     const int64_t zb = (l.clear + 255) / 256;
     int bits = 0;
-    while (s.vocab - 1 >> bits > 0) ++bits;
+    while ((s.vocab - 1) >> bits > 0) ++bits;
     hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(zb < 2048 ? zb : 2048)), dim3(256), 0, stream, l.totals, l.clear);
     if (s.tokens > 0) {  // (a wide row of no tokens comes here too)
         hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, bits, l);

@@ -19,8 +19,8 @@
 // u the same way (keeping them in fp32 would move more bytes than the product takes) and rounds dg and
 // du to bf16 once, as the operands of the other two products.
 //
-// Measured at 16384 rows, dim 768, hidden 2048 (103 GFLOP a product): forward 120 us, dg and du 160, dx 102,
-// dW 121 and 12 for the join of its splits, 0.64 to 1.0 PFLOP/s; at 8192 rows, dim 4096, hidden 4096 the
+// Measured at 16384 rows, dim 768, hidden 2048 (103 GFLOP a product): forward 119 us, dg and du 150, dx 99,
+// dW 113 and 12 for the join of its splits, 0.7 to 1.0 PFLOP/s; at 8192 rows, dim 4096, hidden 4096 the
 // forward product reaches 1.1, where a library's plain product of 8192 x 8192 x 8192 reaches 1.4 with the
 // clock at its power limit. Tiles loaded through registers took 130 us (forward) and 165 (dg and du);
 // 128 x 256 with two workgroups a CU, and one wave's fragments read a half stage ahead, were slower. At
@@ -268,6 +268,7 @@ __global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2)
 #pragma unroll
         for (int p = 0; p < PT; ++p) acc[q][p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+    uint32_t warm = 0;
     if (s_begin < s_end) {
         fetch(s_begin, 0);
         int buf = 0;
@@ -275,6 +276,11 @@ __global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2)
             lds_arrived();
             __syncthreads();  // this stage is in LDS, and every wave is done with the other one
             if (s + 1 < s_end) fetch(s + 1, buf ^ 1);
+            // one load a cache line of dh's tile: the epilogue finds it in L2 (dg and du 162 us, 168 without)
+            if (EPI == kEpiDualBwd && s == s_end - 2) {
+                const int64_t pr = p0 + (tid >> 1) % TP, c = q0 + (tid & 1) * 64;
+                warm = m.dh[(pr < m.P ? pr : m.P - 1) * m.dh_stride + (c < m.Q ? c : m.Q - 1)];
+            }
             auto half = [&](auto step) __attribute__((always_inline)) {
                 constexpr int kk = decltype(step)::value;
                 bf16x8 a[QT], b[PT];
@@ -303,6 +309,7 @@ __global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2)
         }
     }
 
+    asm volatile("" ::"v"(warm));
     // A lane holds q = q0 + q_row(t) + 4 (lane / 16) .. + 3 of p = p0 + p_row(t) + lane % 16.
     const int lq = 4 * (lane >> 4), lp = lane & 15;
     if constexpr (EPI == kEpiPartial) {
@@ -536,17 +543,27 @@ __global__ __launch_bounds__(kFewWaves * 64) void ffn_few_kernel(FfnMat m) {
     }
 }
 
-// The splits' partial sums of a product, added in order.
+// The splits' partial sums of a product, added in order: V columns a lane, V = 4 where Q is a multiple of it.
+template <int V>
 __global__ __launch_bounds__(256) void ffn_join_kernel(FfnMat m) {
-    const int64_t n = m.P * m.Q;
-    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) {
-        const int64_t pr = k / m.Q, qc = k - pr * m.Q;
+    const int64_t n = m.P * m.Q, cols = m.Q / V;
+    typedef float vec __attribute__((ext_vector_type(V)));
+    const vec* part = reinterpret_cast<const vec*>(m.part);
+    for (int64_t pr = blockIdx.x; pr < m.P; pr += gridDim.x) {
         const int64_t row = pr < m.seg_rows ? pr : pr - m.seg_rows;
         if (row >= m.seg_valid) continue;
-        float s = 0.0f;
+        uint16_t* out = (pr < m.seg_rows ? m.out : m.out2) + row * m.out_stride;
+        for (int64_t c = threadIdx.x; c < cols; c += 256) {
+            vec s = 0.0f;
 #pragma unroll 4
-        for (int q = 0; q < m.splits; ++q) s += m.part[q * n + k];
-        (pr < m.seg_rows ? m.out : m.out2)[row * m.out_stride + qc] = to_bf16(s).bits;
+            for (int q = 0; q < m.splits; ++q) s += part[q * (n / V) + pr * cols + c];
+            if constexpr (V == 4) {
+                const uint2 w = make_uint2(pack2(s[0], s[1]), pack2(s[2], s[3]));
+                __builtin_memcpy(out + c * 4, &w, 8);
+            } else {
+                out[c] = to_bf16(s[0]).bits;
+            }
+        }
     }
 }
 
@@ -639,8 +656,9 @@ void run_product(const FfnMat& m, const Tiling& t, hipStream_t stream) {
     run_mat<XTR, YTR, kEpiPartial>(m, t, stream);
     FfnMat j = m;
     j.splits = t.splits;
-    const int64_t n = (m.P * m.Q + 255) / 256;
-    hipLaunchKernelGGL(ffn_join_kernel, dim3((unsigned)(n < 8192 ? n : 8192)), dim3(256), 0, stream, j);
+    const dim3 grid((unsigned)(m.P < 16384 ? m.P : 16384));
+    if (m.Q % 4 == 0) hipLaunchKernelGGL(ffn_join_kernel<4>, grid, dim3(256), 0, stream, j);
+    else hipLaunchKernelGGL(ffn_join_kernel<1>, grid, dim3(256), 0, stream, j);
 }
 
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
