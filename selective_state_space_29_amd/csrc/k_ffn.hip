@@ -576,10 +576,21 @@ struct FfnCopy {
 __global__ __launch_bounds__(256) void ffn_copy_kernel(FfnCopy m) {
     const int which = blockIdx.y;
     if (!m.src[which]) return;
-    const int64_t n = m.rows[which] * m.wide;
-    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) {
-        const int64_t r = k / m.wide, c = k - r * m.wide;
-        m.dst[which][k] = c < m.cols ? m.src[which][r * m.stride[which] + c] : (uint16_t)0;
+    // a wave a row
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < m.rows[which]; r += (int64_t)gridDim.x * 4) {
+        const uint16_t* src = m.src[which] + r * m.stride[which];
+        uint16_t* dst = m.dst[which] + r * m.wide;
+        // 8 values a lane, the loads without a branch around them
+        for (int64_t c = (int64_t)(threadIdx.x & 63) * 8; c < m.wide; c += 64 * 8) {
+            uint16_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = src[c + j < m.cols ? c + j : m.cols - 1];
+            u32x4 w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = (uint32_t)(c + 2 * j < m.cols ? v[2 * j] : 0) | (uint32_t)(c + 2 * j + 1 < m.cols ? v[2 * j + 1] : 0) << 16;
+            *reinterpret_cast<u32x4*>(dst + c) = w;
+        }
     }
 }
 
@@ -687,8 +698,8 @@ Operands operands(const mamba_ffn_shape& s, const void* x, int64_t xs, const voi
     c.src[0] = o.x, c.dst[0] = to, c.rows[0] = s.rows, c.stride[0] = xs;
     c.src[1] = o.wg, c.dst[1] = to + xb, c.rows[1] = s.hidden, c.stride[1] = gs;
     c.src[2] = o.wu, c.dst[2] = to + xb + wb, c.rows[2] = s.hidden, c.stride[2] = us;
-    const int64_t n = ((s.rows > s.hidden ? s.rows : s.hidden) * c.wide + 255) / 256;
-    hipLaunchKernelGGL(ffn_copy_kernel, dim3((unsigned)(n < 4096 ? n : 4096), 3), dim3(256), 0, stream, c);
+    const int64_t n = s.rows > s.hidden ? s.rows : s.hidden;
+    hipLaunchKernelGGL(ffn_copy_kernel, dim3((unsigned)(n < 32768 ? (n + 3) / 4 : 8192), 3), dim3(256), 0, stream, c);
     o.x = c.dst[0], o.wg = c.dst[1], o.wu = c.dst[2], o.xs = o.ws = o.dim8 = c.wide;
     return o;
 }
