@@ -630,7 +630,7 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
     const Seq<S> di(static_cast<S*>(p.di) + b * p.sdi_b, p.sdi_t, d);
     const uint8_t* reset = RESET ? p.reset + b * L : nullptr;
     const float tl = p.c * kLog2e * softplus_f(p.lam[d]);
-    const float inv_tl = tl > 1e-30f ? hw_rcp(tl) : 0.0f;  // sigmoid(r) = e / tl; below, every q is 0
+    const float inv_tl = tl > 1e-30f ? hw_rcp(tl) * kLn2 : 0.0f;  // sigmoid(r) = e / tl; below, every q is 0
 
     float carry = p.dlast ? p.dlast[b * D + ds] : 0.0f;  // mu entering the chunk from the right
     const int n = (int)((L + STEPS - 1) / STEPS);  // chunk n - 1 - (number of the walk)
@@ -698,14 +698,13 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
             }
             esum += e[k];
             const float w = one_minus_sq<S>(e[k], a[k]);
-            const float rm = w > 1.1754944e-38f ? __builtin_amdgcn_rsqf(w) : 0.0f;  // 1 / m, or 0 with m
-            const float si = sigmoid_of_scaled(ci[k]);
-            const float gx = past ? 0.0f : si * cx[k];
-            const float m = w * rm;
-            ms[k] = m * si;
-            bb[k] = m * gx;
-            bi[k] = bb[k] * (1.0f - si);
-            z[k] = gx * a[k] * rm;
+            // 1 / m; where m is 0, so are e and with it all that 1 / m enters, as long as it is finite
+            const float rm = __builtin_amdgcn_rsqf(__builtin_fmaxf(w, 1.1754944e-38f));
+            const float si = sigmoid_of_scaled(ci[k]), v = past ? 0.0f : cx[k], rs = rm * si;
+            ms[k] = w * rs;
+            bb[k] = ms[k] * v;
+            bi[k] = __builtin_fmaf(-bb[k], si, bb[k]);
+            z[k] = a[k] * (rs * v);
             hl = decay_fma<RESET>(a[k], hl, bb[k]);
         }
 #pragma unroll
@@ -750,14 +749,14 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
             const float gk = g[k] + in;
             in = decay_mul<RESET>(a[k], gk);
             const float ek = RESET ? __builtin_fminf(e[k], 1e30f) : e[k];
-            const float q = decay_mul<RESET>(in * (ek * kLn2), z[k]);
+            const float q = decay_mul<RESET>(in * ek, z[k]);  // without its factor ln 2
             acc += !TAIL || k < left ? q : 0.0f;
             row_store(from_f32<S>(gk * ms[k]), ox, put ? dx.off : kGatedDrop, k * dx.row_bytes());
             row_store(from_f32<S>(gk * bi[k]), oi, put ? di.off : kGatedDrop, k * di.row_bytes());
-            row_store(from_f32<S>(decay_mul<RESET>(q, __builtin_fmaf(-ek, inv_tl, 1.0f))), orr, put ? dr.off : kGatedDrop,
+            row_store(from_f32<S>(decay_mul<RESET>(q, __builtin_fmaf(-ek, inv_tl, kLn2))), orr, put ? dr.off : kGatedDrop,
                       k * dr.row_bytes());
         }
-        s_acc[run * kPitch + lane] = acc;
+        s_acc[run * kPitch + lane] = acc * kLn2;
         sums_of = which;
         if (p.dh0 && walk.cur == n - 1 && s_run == 0 && s_live) p.dh0[b * D + ds] = carry;
         walk.advance();

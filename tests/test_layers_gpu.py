@@ -452,3 +452,41 @@ def test_embedding_gradient_of_wide_rows_and_far_offsets():
     ids[7], ids[2040] = V - 1, 0
     dw = layers.embedding_bwd(ids, dy, V)
     assert torch.equal(dw[-1], dy[0]) and torch.equal(dw[0], dy[0]) and not dw[1:-1].any()
+
+
+def test_replayed_graphs_repeat_the_eager_calls():
+    """Every operator, forward and backward, captured once and replayed between eager work on other inputs."""
+    g = gen(40)
+    x, r, i, dy = (torch.randn(2, 1500, 200, generator=g).to(DEV) for _ in range(4))
+    lam = torch.randn(200, generator=g).to(DEV)
+    reset = (torch.rand(2, 1500, generator=g) < 0.01).to(DEV)
+    ids = (torch.rand(3000, generator=g) ** 4 * 90).long().to(DEV)
+    table, de = torch.randn(90, 200, generator=g).to(DEV), torch.randn(3000, 200, generator=g).to(DEV)
+    xb, dh = torch.randn(300, 72, generator=g).to(BF16).to(DEV), torch.randn(300, 104, generator=g).to(BF16).to(DEV)
+    wg, wu = (torch.randn(104, 72, generator=g).to(BF16).to(DEV) for _ in range(2))
+
+    def calls():
+        y, last = layers.gated_scan_fn(x, r, i, lam, reset=reset, return_last_state=True)
+        gs = layers.gated_scan_bwd(x, r, i, lam, dy, reset=reset)
+        n, stats = layers.layer_norm_fn(y, lam, return_stats=True)
+        gn = layers.layer_norm_bwd(y, lam, dy, stats)
+        return [y, last, *gs.values(), n, *gn.values(), layers.embedding_fn(ids, table), layers.embedding_bwd(ids, de, 90),
+                layers.embedding_bwd(ids[:500], de[:500], 90), layers.gated_ffn_fn(xb, wg, wu), layers.gated_ffn_fn(xb[:9], wg, wu),
+                *layers.gated_ffn_bwd(xb, wg, wu, dh).values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for k in range(4):
+        for t in (x, dy, de, xb, dh):
+            t.mul_(-1.25 if k % 2 else 0.8)
+        want = [t.clone() for t in calls()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, want):
+            assert torch.equal(a, b), k
