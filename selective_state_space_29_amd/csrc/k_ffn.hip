@@ -5,8 +5,9 @@
 //
 // One matrix kernel, C[p][q] = sum_c X(p, c) Y(q, c), serves all products. A workgroup of 8 waves computes
 // a tile of 256 x 256 (or 256 x 192; 4 waves 128 x 128): it loads 64 steps of c of both operands straight
-// into LDS, a stage ahead of the one its waves multiply (v_mfma_f32_16x16x32_bf16, fp32 sums). An operand
-// lies with c contiguous (x and the weights in the forward product) or with c as its rows (the weights in
+// into LDS, a stage ahead of the one its waves multiply (v_mfma_f32_16x16x32_bf16, fp32 sums); workgroups of
+// 128 x 128 that have a CU to themselves, three stages ahead (64 rows, dim 2048, hidden 8192, forward and
+// backward: 102 us, 112 one stage ahead). An operand lies with c contiguous (x and the weights in the forward product) or with c as its rows (the weights in
 // dx; both operands in dW); the latter is read from LDS with the transposing ds_read_b64_tr_b16, so no
 // operand is ever transposed in memory. 16-byte chunks lie in LDS at an index XORed with their row, so that
 // the reads of both kinds meet no bank twice; the lanes of a load into LDS fill consecutive places, so each
@@ -21,7 +22,7 @@
 //
 // Measured at 16384 rows, dim 768, hidden 2048 (103 GFLOP a product): forward 119 us, dg and du 150, dx 99,
 // dW 113 and 12 for the join of its splits, 0.7 to 1.0 PFLOP/s; at 8192 rows, dim 4096, hidden 4096 the
-// forward product reaches 1.1, where a library's plain product of 8192 x 8192 x 8192 reaches 1.4 with the
+// forward product reaches 1.27, where a library's plain product of 8192 x 8192 x 8192 reaches 1.4 with the
 // clock at its power limit. Tiles loaded through registers took 130 us (forward) and 165 (dg and du);
 // 128 x 256 with two workgroups a CU, and one wave's fragments read a half stage ahead, were slower. At
 // dim 768 a tile has 12 stages, and filling the first and storing the results cost as much as 3.
@@ -82,7 +83,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int6
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint16_t* to, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, (int)off, 0, 0, 0);
 }
-__device__ __forceinline__ void lds_arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+// Waits until at most N of the wave's loads are on their way, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void stage_ready() {
+    static_assert(N < 64);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N)
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 // act and its derivative; silu(g) = g sg(g), gelu(g) = g/2 (1 + tanh(k (g + 0.044715 g^3))), where
 // (1 + tanh(z)) / 2 = sg(2z).
@@ -115,8 +124,8 @@ __device__ __forceinline__ int swz_tr(int row, int c) {
     return c ^ (((row & 3) | ((row >> 1) & 4)) << 1);
 }
 
-template <int TP, int TQ, int WP, int WQ, bool XTR, bool YTR, int EPI>
-__global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2))) void ffn_mat_kernel(FfnMat m) {
+template <int TP, int TQ, int WP, int WQ, int DEPTH, bool XTR, bool YTR, int EPI>
+__global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(DEPTH > 2 ? 1 : 2))) void ffn_mat_kernel(FfnMat m) {
     constexpr bool DUAL = EPI == kEpiDual || EPI == kEpiDualBwd;
     constexpr int NT = WP * WQ * 64;
     constexpr int PT = TP / WP / 16, QT = TQ / WQ / 16, QG = QT % 4 == 0 ? 4 : 3;  // QG: tiles read at a time
@@ -124,10 +133,10 @@ __global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2)
     constexpr int XN = TP * CH / NT, YN = TQ * CH / NT;  // chunks a thread moves per stage
     static_assert(!(DUAL && (XTR || YTR)) && XN >= 1 && YN >= 1 && (!DUAL || QT % 2 == 0));
     constexpr int OQ = DUAL ? TQ / 2 : TQ, PITCH = OQ + 8;  // of the results' rows in LDS, 16 bytes apart in the banks
-    constexpr int STAGES = 2 * (TP + TQ) * kTC, RESULTS = EPI == kEpiPartial ? 0 : TP * PITCH;
+    constexpr int STAGES = DEPTH * (TP + TQ) * kTC, RESULTS = EPI == kEpiPartial ? 0 : TP * PITCH;
     __shared__ __align__(16) uint16_t lds[STAGES > RESULTS ? STAGES : RESULTS];
-    uint16_t(&sx)[2][TP * kTC] = *reinterpret_cast<uint16_t(*)[2][TP * kTC]>(&lds[0]);
-    uint16_t(&sy)[2][TQ * kTC] = *reinterpret_cast<uint16_t(*)[2][TQ * kTC]>(&lds[2 * TP * kTC]);
+    uint16_t(&sx)[DEPTH][TP * kTC] = *reinterpret_cast<uint16_t(*)[DEPTH][TP * kTC]>(&lds[0]);
+    uint16_t(&sy)[DEPTH][TQ * kTC] = *reinterpret_cast<uint16_t(*)[DEPTH][TQ * kTC]>(&lds[DEPTH * TP * kTC]);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -270,12 +279,23 @@ __global__ __launch_bounds__(WP * WQ * 64) __attribute__((amdgpu_waves_per_eu(2)
 
     uint32_t warm = 0;
     if (s_begin < s_end) {
-        fetch(s_begin, 0);
-        int buf = 0;
-        for (int s = s_begin; s < s_end; ++s, buf ^= 1) {
-            lds_arrived();
-            __syncthreads();  // this stage is in LDS, and every wave is done with the other one
-            if (s + 1 < s_end) fetch(s + 1, buf ^ 1);
+        constexpr int LOADS = XN + YN;  // a stage's
+#pragma unroll
+        for (int d = 0; d < DEPTH - 1; ++d)
+            if (s_begin + d < s_end) fetch(s_begin + d, d);
+        unsigned buf = 0;
+        for (int s = s_begin; s < s_end; ++s, buf = (buf + 1) % DEPTH) {
+            // this stage is in LDS, and every wave is done with the one before it
+            if constexpr (DEPTH == 2) {
+                __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+                __syncthreads();
+            } else {
+                static_assert(DEPTH == 4);
+                if (s + 2 < s_end) stage_ready<2 * LOADS>();
+                else if (s + 1 < s_end) stage_ready<LOADS>();
+                else stage_ready<0>();
+            }
+            if (s + DEPTH - 1 < s_end) fetch(s + DEPTH - 1, (buf + DEPTH - 1) % DEPTH);
             // one load a cache line of dh's tile: the epilogue finds it in L2 (dg and du 162 us, 168 without)
             if (EPI == kEpiDualBwd && s == s_end - 2) {
                 const int64_t pr = p0 + (tid >> 1) % TP, c = q0 + (tid & 1) * 64;
@@ -608,6 +628,7 @@ bool row_aligned(const void* p, int64_t stride, int64_t rows) {
 
 struct Tiling {
     int tp, tq;  // 256 x 256, 256 x 192 or 128 x 128
+    bool alone;  // no more workgroups than CUs
     int tiles_p, tiles_q, splits;
 };
 
@@ -627,7 +648,7 @@ Tiling tiling(int64_t P, int64_t Q, bool dual, int steps, bool may_split) {
     double least = 0.0;
     for (const auto& k : kTiles) {
         if (dual && k[1] == 192) continue;
-        Tiling t{k[0], k[1], (int)div(P, k[0]), (int)div(Q, dual ? k[1] / 2 : k[1]), 1};
+        Tiling t{k[0], k[1], false, (int)div(P, k[0]), (int)div(Q, dual ? k[1] / 2 : k[1]), 1};
         const int64_t n = (int64_t)t.tiles_p * t.tiles_q, room = k[0] == 128 ? 2 * cus : cus;
         const int most = may_split ? (int)(room / n < steps / 4 ? room / n : steps / 4) : 1;
         for (int s = 1; s == 1 || s <= most; ++s) {
@@ -635,7 +656,7 @@ Tiling tiling(int64_t P, int64_t Q, bool dual, int steps, bool may_split) {
             double rounds = k[0] == 128 && wgs <= cus ? kAlone : (double)div(wgs, cus);
             double cost = rounds * div(steps, s) * k[0] * k[1] / k[2] * kStage;
             if (s > 1) cost += kJoin + kJoinBytes * s * (double)P * Q;
-            if (best.tp == 0 || cost < least) t.splits = s, best = t, least = cost;
+            if (best.tp == 0 || cost < least) t.splits = s, t.alone = wgs <= cus, best = t, least = cost;
         }
     }
     return best;
@@ -646,16 +667,17 @@ void run_mat(FfnMat m, const Tiling& t, hipStream_t stream) {
     m.tiles_p = t.tiles_p, m.tiles_q = t.tiles_q, m.splits = t.splits;
     const dim3 grid((unsigned)(t.tiles_p * t.tiles_q), (unsigned)t.splits);
     if (t.tp == 128) {
-        hipLaunchKernelGGL((ffn_mat_kernel<128, 128, 2, 2, XTR, YTR, EPI>), grid, dim3(256), 0, stream, m);
+        if (t.alone) hipLaunchKernelGGL((ffn_mat_kernel<128, 128, 2, 2, 4, XTR, YTR, EPI>), grid, dim3(256), 0, stream, m);
+        else hipLaunchKernelGGL((ffn_mat_kernel<128, 128, 2, 2, 2, XTR, YTR, EPI>), grid, dim3(256), 0, stream, m);
         return;
     }
     if constexpr (EPI == kEpiStore || EPI == kEpiPartial) {
         if (t.tq == 192) {
-            hipLaunchKernelGGL((ffn_mat_kernel<256, 192, 2, 4, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
+            hipLaunchKernelGGL((ffn_mat_kernel<256, 192, 2, 4, 2, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
             return;
         }
     }
-    hipLaunchKernelGGL((ffn_mat_kernel<256, 256, 2, 4, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
+    hipLaunchKernelGGL((ffn_mat_kernel<256, 256, 2, 4, 2, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
 }
 
 template <bool XTR, bool YTR>
