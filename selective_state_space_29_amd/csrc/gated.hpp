@@ -599,7 +599,8 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p) {
 // runs have the same product of a: one exchange serves both directions. Kept per step between the scans
 // and the outputs: a, b, e, m sigmoid(i), b (1 - sigmoid(i)), (s / m) a sigmoid(i) x / s, dy. Each
 // chunk's sum of q is written by itself (added up in order afterwards), so that it does not matter which
-// workgroup of a chain had which chunk.
+// workgroup of a chain had which chunk. Bound by the VALU (49 plain and 6 transcendental instructions an
+// element) and HBM: 8 x 2048 x 1536 bf16 97 us for 352 MB with 192 of 256 compute units at work, 3.6 TB/s.
 template <typename S, int TS, bool RESET, bool CHAIN>
 __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
     constexpr int STEPS = kRuns * TS;
@@ -671,7 +672,8 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
         constexpr bool TAIL = decltype(tail)::value;
         const int which = n - 1 - walk.cur;
         const int64_t tr = (int64_t)which * STEPS + run * TS;
-        auto start = [](float v) __attribute__((always_inline)) { return CHAIN ? v : here(v); };  // (chained: 44 spills with it, 19 without)
+        // (chained, with its pointers: 44 registers spilled with it, 19 without)
+        auto start = [](float v) __attribute__((always_inline)) { return CHAIN ? v : here(v); };
         float cx[TS], cr[TS], ci[TS], g[TS];
 #pragma unroll
         for (int k = 0; k < TS; ++k) {

@@ -7,13 +7,13 @@
 // a tile of 256 x 256 (or 256 x 192; 4 waves 128 x 128): it loads 64 steps of c of both operands straight
 // into LDS, a stage ahead of the one its waves multiply (v_mfma_f32_16x16x32_bf16, fp32 sums); workgroups of
 // 128 x 128 that have a CU to themselves, three stages ahead (64 rows, dim 2048, hidden 8192, forward and
-// backward: 102 us, 112 one stage ahead). An operand lies with c contiguous (x and the weights in the forward product) or with c as its rows (the weights in
-// dx; both operands in dW); the latter is read from LDS with the transposing ds_read_b64_tr_b16, so no
-// operand is ever transposed in memory. 16-byte chunks lie in LDS at an index XORed with their row, so that
-// the reads of both kinds meet no bank twice; the lanes of a load into LDS fill consecutive places, so each
-// lane loads the chunk whose place it fills. The rows of the MFMA are the q's: a lane then holds 4
-// consecutive q of one p, and a tile's results pass through the LDS that its stages no longer need, so
-// that whole rows are stored 16 bytes a lane.
+// backward: 102 us, 112 one stage ahead). An operand lies with c contiguous (x and the weights in the forward
+// product) or with c as its rows (the weights in dx; both operands in dW); the latter is read from LDS with
+// the transposing ds_read_b64_tr_b16, so no operand is ever transposed in memory. 16-byte chunks lie in LDS
+// at an index XORed with their row, so that the reads of both kinds meet no bank twice; the lanes of a load
+// into LDS fill consecutive places, so each lane loads the chunk whose place it fills. The rows of the MFMA
+// are the q's: a lane then holds 4 consecutive q of one p, and a tile's results pass through the LDS that its
+// stages no longer need, so that whole rows are stored 16 bytes a lane.
 //
 // The forward tile holds 128 or 64 hidden units' gate rows and the same units' up rows, so that both
 // projections of a unit meet in the same lane and only h is written. The backward pass recomputes g and

@@ -9,6 +9,9 @@
 //   dx = rstd (g - mean(g) - n mean(g n)) + dresidual,   dweight = sum_rows dy n,   dbias = sum_rows dy.
 // A workgroup walks its rows and keeps the two column sums in registers; it writes one row of partial
 // sums, and a second kernel adds the workgroups' in order, so the result does not depend on timing.
+//
+// Measured: forward 16384 x 768 bf16 with residual 22 us (100 MB, 4.5 TB/s; a large copy 4.6); 16384 x 2048
+// 50 forward (5.4 TB/s, partly cached), 44 + 4 backward and its column sums; 4000 x 8192 fp32 103 and 112.
 #include <initializer_list>
 #include <type_traits>
 #include <utility>
