@@ -141,24 +141,45 @@ def _need_gpu(x, entry):
 
 # The handle of a device's current stream: torch's own getter where it has one (0.1 us), else by way of
 # a Stream object (2 us of the 12 that a decode step's call may take).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _launch(entry, x, f, *args):
-    """Call a library entry on x's device and its current stream; raise what it refuses."""
+def _call(x, f, *args):
+    """The return code of a library entry called on x's device and its current stream."""
     dev = x.get_device()
-    if torch.cuda.current_device() == dev:
-        rc = f(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            rc = f(*args, _raw_stream(dev))
+    if _current_device() == dev:
+        return f(*args, _raw_stream(dev))
+    with torch.cuda.device(dev):
+        return f(*args, _raw_stream(dev))
+
+
+def _launch(entry, x, f, *args):
+    """:func:`_call`, raising what the library refuses."""
+    rc = _call(x, f, *args)
+    if rc != 0:
+        _raise(rc, entry)
+
+
+_NEEDS_WORKSPACE = -9
+
+
+def _launch_maybe_workspace(entry, x, f, size, ptrs, *args):
+    """:func:`_launch` of an entry that seldom needs a workspace (``size()`` bytes): tried without one
+    first, as the library refuses before it enqueues anything and the query costs a short call 0.7 us."""
+    rc = _call(x, f, ptrs, *args)
+    if rc == _NEEDS_WORKSPACE:
+        n = size()
+        ws = _workspace(n, entry, x)
+        ptrs.workspace, ptrs.workspace_bytes = ws.data_ptr(), n
+        rc = _call(x, f, ptrs, *args)
     if rc != 0:
         _raise(rc, entry)
 
 
 def _on_device(x, f, *args):
     """A size query that depends on the device it is asked for."""
-    if torch.cuda.current_device() == x.get_device():
+    if _current_device() == x.get_device():
         return f(*args)
     with torch.cuda.device(x.get_device()):
         return f(*args)
@@ -219,11 +240,12 @@ def _reset(reset, batch, length, like):
 def _gated_inputs(x, r, i, lam, h0, reset, entry):
     dtype = _dtype(x, "x")
     _need_gpu(x, entry)
-    if x.dim() != 3:
-        raise ValueError(f"x must be (batch, len, dim), got {tuple(x.shape)}")
-    batch, length, dim = x.shape
-    return (dtype, x, _same(r, x, "r"), _same(i, x, "i"), _f32(lam, "lam", (dim,), x), _f32(h0, "h0", (batch, dim), x),
-            _reset(reset, batch, length, x))
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must be (batch, len, dim), got {tuple(shape)}")
+    batch, length, dim = shape
+    return (dtype, x, _same(r, x, "r"), _same(i, x, "i"), _f32(lam, "lam", (dim,), x),
+            None if h0 is None else _f32(h0, "h0", (batch, dim), x), None if reset is None else _reset(reset, batch, length, x))
 
 
 _MAX_ROW_STRIDE = 1 << 21  # elements; the kernels' offsets within a run are 32-bit
@@ -274,13 +296,12 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
     if checkpoints_out is not None:
         _check_gated_checkpoints(checkpoints_out, x)
     shape = GatedShape(batch, length, dim)
-    n = _on_device(x, lib.mamba_gated_workspace_bytes, shape, dtype)
-    ws = _workspace(n, "mamba_gated_workspace_bytes", x) if n else None
     ys = y.stride()
     ptrs = GatedPtrs(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _ptr(h0), _ptr(reset), y.data_ptr(), _ptr(last),
-                     _ptr(checkpoints_out), _ptr(ws), n)
+                     _ptr(checkpoints_out), None, 0)
     st = GatedStrides(*xs, *rs, *is_, ys[0], ys[1])
-    _launch("mamba_gated_scan_fwd", x, lib.mamba_gated_scan_fwd, ptrs, shape, st, c, dtype)
+    _launch_maybe_workspace("mamba_gated_scan_fwd", x, lib.mamba_gated_scan_fwd,
+                            lambda: _on_device(x, lib.mamba_gated_workspace_bytes, shape, dtype), ptrs, shape, st, c, dtype)
     return (y, last) if return_last_state else y
 
 
@@ -568,11 +589,8 @@ def gated_ffn_fn(x, w_gate, w_up, activation="silu"):
     shape = FfnShape(rows, dim, hidden)
     ptrs = FfnPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu),
                    hidden, None, 0)
-    n = _on_device(x, lib.mamba_gated_ffn_workspace_bytes, ptrs, shape)
-    if n:
-        ws = _workspace(n, "mamba_gated_ffn_workspace_bytes", x)
-        ptrs.workspace, ptrs.workspace_bytes = ws.data_ptr(), n
-    _launch("mamba_gated_ffn_fwd", x, lib.mamba_gated_ffn_fwd, ptrs, shape, act, dtype)
+    _launch_maybe_workspace("mamba_gated_ffn_fwd", x, lib.mamba_gated_ffn_fwd,
+                            lambda: _on_device(x, lib.mamba_gated_ffn_workspace_bytes, ptrs, shape), ptrs, shape, act, dtype)
     return h
 
 
