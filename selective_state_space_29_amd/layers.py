@@ -382,16 +382,21 @@ def gated_scan(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state=Fa
 # ---- layer norm ----
 
 def _rows(x, name):
-    """x as (rows, dim) with unit stride along dim, without a copy where its rows are evenly spaced."""
-    if x.dim() == 0:
-        raise ValueError(f"{name} must have at least one dimension")
+    """x as rows of its last dimension with unit stride, without a copy where they are evenly spaced: a
+    tensor that begins with them, their number and the stride between them."""
     if x.dim() != 2:
-        x = x.reshape(-1, x.shape[-1]) if x.numel() else x.reshape(x.shape[:-1].numel(), x.shape[-1])
-    return _inner(x)
+        if x.dim() == 0:
+            raise ValueError(f"{name} must have at least one dimension")
+        dim = x.shape[-1]
+        if x.is_contiguous():  # no view made: it costs a short call 2 us
+            return x, x.numel() // dim if dim else x.shape[:-1].numel(), dim
+        x = x.reshape(-1, dim) if x.numel() else x.reshape(x.shape[:-1].numel(), dim)
+    x = _inner(x)
+    return x, x.shape[0], _row_stride(x)
 
 
 def _row_stride(x):
-    return 0 if x is None else x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
 def layer_norm_fn(x, weight=None, bias=None, eps=1e-5, *, residual=None, return_stats=False):
@@ -412,15 +417,15 @@ def layer_norm_fn(x, weight=None, bias=None, eps=1e-5, *, residual=None, return_
             raise TypeError("residual must have x's dtype and device")
         if residual.shape != shape:
             raise ValueError(f"residual must have x's shape {tuple(shape)}, got {tuple(residual.shape)}")
-    xr = _rows(x, "x")
-    rows, dim = xr.shape
-    rr = None if residual is None else _rows(residual, "residual")
+    xr, rows, xs = _rows(x, "x")
+    dim = shape[-1]
+    rr, _, rs = (None, 0, 0) if residual is None else _rows(residual, "residual")
     weight, bias = _f32(weight, "weight", (dim,), x), _f32(bias, "bias", (dim,), x)
     y = x.new_empty(shape)
     t = None if residual is None else x.new_empty(shape)
     stats = x.new_empty((rows, 2), dtype=torch.float32) if return_stats else None
     ptrs = NormPtrs(xr.data_ptr(), _ptr(rr), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(t), _ptr(stats),
-                    _row_stride(xr), _row_stride(rr), dim, dim)
+                    xs, rs, dim, dim)
     _launch("mamba_layer_norm_fwd", x, lib.mamba_layer_norm_fwd, ptrs, NormShape(rows, dim), eps, dtype)
     out = y if residual is None else (y, t)
     return (out, stats) if return_stats else out
@@ -439,9 +444,9 @@ def layer_norm_bwd(t, weight, dy, stats, *, dresidual=None, want_dweight=True, w
                 raise TypeError(f"{name} must have t's dtype and device")
             if v.shape != t.shape:
                 raise ValueError(f"{name} must have t's shape {tuple(t.shape)}, got {tuple(v.shape)}")
-    tr, gr = _rows(t, "t"), _rows(dy, "dy")
-    rr = None if dresidual is None else _rows(dresidual, "dresidual")
-    rows, dim = tr.shape
+    (tr, rows, ts), (gr, _, gs) = _rows(t, "t"), _rows(dy, "dy")
+    rr, _, rs = (None, 0, 0) if dresidual is None else _rows(dresidual, "dresidual")
+    dim = t.shape[-1]
     weight, stats = _f32(weight, "weight", (dim,), t), _f32(stats, "stats", (rows, 2), t)
     dx = t.new_empty(t.shape)
     out = {"x": dx}
@@ -453,7 +458,7 @@ def layer_norm_bwd(t, weight, dy, stats, *, dresidual=None, want_dweight=True, w
     n = lib.mamba_layer_norm_bwd_workspace_bytes(shape) if want_dweight or want_dbias else 0
     ws = _workspace(n, "mamba_layer_norm_bwd_workspace_bytes", t)
     ptrs = NormBwdPtrs(tr.data_ptr(), _ptr(weight), stats.data_ptr(), gr.data_ptr(), _ptr(rr), dx.data_ptr(),
-                       _ptr(out.get("weight")), _ptr(out.get("bias")), _row_stride(tr), _row_stride(gr), _row_stride(rr), dim,
+                       _ptr(out.get("weight")), _ptr(out.get("bias")), ts, gs, rs, dim,
                        _ptr(ws), n)
     _launch("mamba_layer_norm_bwd", t, lib.mamba_layer_norm_bwd, ptrs, shape, dtype)
     return out
@@ -574,7 +579,7 @@ def _ffn_inputs(x, w_gate, w_up, activation, entry):
             raise TypeError(f"{name} must have x's dtype and device")
         if w.dim() != 2 or w.shape != w_gate.shape or w.shape[1] != x.shape[-1]:
             raise ValueError(f"{name} must be (hidden, dim) with dim = {x.shape[-1]}, got {tuple(w.shape)}")
-    return dtype, _ACTS[activation], _rows(x, "x"), _inner(w_gate), _inner(w_up)
+    return dtype, _ACTS[activation], *_rows(x, "x"), _inner(w_gate), _inner(w_up)
 
 
 def gated_ffn_fn(x, w_gate, w_up, activation="silu"):
@@ -582,12 +587,11 @@ def gated_ffn_fn(x, w_gate, w_up, activation="silu"):
     in its tanh form) and the product in one kernel. x: (..., dim), w_gate, w_up: (hidden, dim), all
     bfloat16; fp32 sums; returns (..., hidden) in bfloat16."""
     lib = _load()
-    dtype, act, xr, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_fn")
-    rows, dim = xr.shape
-    hidden = wg.shape[0]
+    dtype, act, xr, rows, xs, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_fn")
+    hidden, dim = wg.shape
     h = x.new_empty((*x.shape[:-1], hidden))
     shape = FfnShape(rows, dim, hidden)
-    ptrs = FfnPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu),
+    ptrs = FfnPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), xs, _row_stride(wg), _row_stride(wu),
                    hidden, None, 0)
     _launch_maybe_workspace("mamba_gated_ffn_fwd", x, lib.mamba_gated_ffn_fwd,
                             lambda: _on_device(x, lib.mamba_gated_ffn_workspace_bytes, ptrs, shape), ptrs, shape, act, dtype)
@@ -599,20 +603,19 @@ def gated_ffn_bwd(x, w_gate, w_up, dh, activation="silu"):
     w_up in bfloat16. Both projections are recomputed from x; the gradients of their outputs are rounded
     to bfloat16 once, as the operands of the products."""
     lib = _load()
-    dtype, act, xr, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_bwd")
-    rows, dim = xr.shape
-    hidden = wg.shape[0]
+    dtype, act, xr, rows, xs, wg, wu = _ffn_inputs(x, w_gate, w_up, activation, "gated_ffn_bwd")
+    hidden, dim = wg.shape
     if dh.dtype is not x.dtype or dh.get_device() != x.get_device():
         raise TypeError("dh must have x's dtype and device")
     if dh.shape != (*x.shape[:-1], hidden):
         raise ValueError(f"dh must be {(*x.shape[:-1], hidden)}, got {tuple(dh.shape)}")
-    gr = _rows(dh, "dh")
+    gr, _, gs = _rows(dh, "dh")
     out = {"x": x.new_empty(x.shape), "w_gate": x.new_empty((hidden, dim)), "w_up": x.new_empty((hidden, dim))}
     shape = FfnShape(rows, dim, hidden)
     n = _on_device(x, lib.mamba_gated_ffn_bwd_workspace_bytes, shape)
     ws = _workspace(n, "mamba_gated_ffn_bwd_workspace_bytes", x)
     ptrs = FfnBwdPtrs(xr.data_ptr(), wg.data_ptr(), wu.data_ptr(), gr.data_ptr(), out["x"].data_ptr(), out["w_gate"].data_ptr(),
-                      out["w_up"].data_ptr(), _row_stride(xr), _row_stride(wg), _row_stride(wu), _row_stride(gr), _ptr(ws), n)
+                      out["w_up"].data_ptr(), xs, _row_stride(wg), _row_stride(wu), gs, _ptr(ws), n)
     _launch("mamba_gated_ffn_bwd", x, lib.mamba_gated_ffn_bwd, ptrs, shape, act, dtype)
     return out
 
