@@ -47,8 +47,8 @@ extern "C" {
  *    state before steps 0, 128, 256, ... for the backward pass.
  *  - workspace: mamba_gated_workspace_bytes(), 256-byte aligned (0 bytes unless several workgroups share
  *    a row's sequence, as for few long rows: they pass the state on through it).
- *  - Row strides up to 2^22 elements or so (64 stride + dim < 2^28), dim < 2^28, and batch * dim / 64
- *    below 2^23; MAMBA_SCAN_ERR_UNSUPPORTED otherwise.
+ *  - Row strides up to 2^22 elements or so (64 stride + dim < 2^28), dim < 2^28, and batch * ceil(dim / 64)
+ *    below 2^23 - 8; MAMBA_SCAN_ERR_UNSUPPORTED otherwise.
  *  - c must be finite and >= 0.
  */
 #define MAMBA_GATED_CHECKPOINT 128

@@ -163,7 +163,7 @@ struct GatedPlace {
     bool ok;
 };
 __device__ __forceinline__ GatedPlace gated_place(int64_t groups, int64_t batch, int ways) {
-    const int64_t id = blockIdx.x;
+    const int64_t id = grid_block();
     GatedPlace p;
     const int64_t per = (groups * batch + 7) / 8, slot = id / (8 * ways);
     p.chain = id % 8 * per + slot;

@@ -389,7 +389,8 @@ __device__ __forceinline__ void find_tokens(const void* ids, int tokens, int64_t
 // 200 x 2048 24.9 and 34.5. The same search through more tokens, with long lists left to a second launch, was
 // slower than counting (16384 tokens, 50000 x 768: 57 us against 48), as each group of ids reads them all.
 constexpr int kDirect = 2048, kDirectLongs = kDirect / (kPiece + 1), kDirectPieces = kDirect / kPiece + kDirectLongs;
-bool direct(const mamba_embedding_shape& s) { return s.tokens <= kDirect && s.dim <= 1 << 16; }  // 65536 blocks of columns at most
+// (65536 blocks of columns at most; 16 threads an id, whose number has to stay below 2^32)
+bool direct(const mamba_embedding_shape& s) { return s.tokens <= kDirect && s.dim <= 1 << 16 && s.vocab <= 1 << 27; }
 
 template <typename S, int V, typename I>
 __global__ __launch_bounds__(1024) void direct_kernel(const void* ids, int tokens, int64_t vocab, const S* dy, S* dweight,
@@ -454,12 +455,12 @@ template <typename S, int V>
 __global__ __launch_bounds__(256) void reduce_kernel(const S* dy, S* dweight, int64_t dim, float scale, Lists l, int zeros,
                                                      int64_t vocab) {
     using P = Pack<S, V>;
-    const int64_t zero = (int64_t)blockIdx.x * zeros / gridDim.x;
-    if (((int64_t)blockIdx.x + 1) * zeros / gridDim.x > zero) {
+    const int64_t id_block = grid_block(), all = grid_blocks(), zero = id_block * zeros / all;
+    if ((id_block + 1) * zeros / all > zero) {
         zero_rows(reinterpret_cast<char*>(dweight), dim * (int64_t)sizeof(S), zero * kZeroIds, vocab, l.count);
         return;
     }
-    const int64_t block = (int64_t)blockIdx.x - zero, blocks = (int64_t)gridDim.x - zeros;
+    const int64_t block = id_block - zero, blocks = all - zeros;
     const int lane = threadIdx.x & 63;
     const int cols = (int)((dim + 64 * V - 1) / (64 * V));
     const int pieces = l.totals[3], shorts = l.totals[1];
@@ -560,7 +561,7 @@ int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_e
         constexpr int V = decltype(v)::value;
         const int64_t waves = (l.max_piece + l.max_short) * ((s.dim + 64 * V - 1) / (64 * V)), most = (int64_t)layers_cus() * 64;
         const int64_t zeros = (s.vocab + kZeroIds - 1) / kZeroIds, sums = ((waves < most ? waves : most) + 3) / 4;
-        hipLaunchKernelGGL((reduce_kernel<S, V>), dim3((unsigned)(zeros + sums)), dim3(256), 0, stream, static_cast<const S*>(dy),
+        hipLaunchKernelGGL((reduce_kernel<S, V>), grid_of(zeros + sums, 256), dim3(256), 0, stream, static_cast<const S*>(dy),
                            static_cast<S*>(dw), s.dim, scale, l, (int)zeros, s.vocab);
         return 0;
     });

@@ -26,7 +26,7 @@ int ways_for(const mamba_gated_shape& s, int cus, int chunk) {
 __global__ __launch_bounds__(1024) void gated_dlam_kernel(const float* part, int64_t parts, const float* lam, float* dlam,
                                                           int64_t D) {
     __shared__ float lds[16][64];
-    const int64_t d = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int64_t d = grid_block() * 64 + (threadIdx.x & 63);
     const int g = threadIdx.x >> 6;
     const int64_t per = (parts + 15) / 16, q1 = (g + 1) * per < parts ? (g + 1) * per : parts;
     float s = 0.0f;
@@ -55,7 +55,7 @@ void clear_chain(uint64_t* p, int64_t batch, int64_t dim, int64_t len, int chunk
 template <typename S, bool STATES>
 void run_fwd(const GatedParams& q, hipStream_t stream) {
     constexpr int TS = gated_fwd_ts(sizeof(S), false), TC = gated_fwd_ts(sizeof(S), true);
-    const dim3 grid((unsigned)gated_blocks(q.batch * ((q.dim + kChans - 1) / kChans), q.ways)), block(1024);
+    const dim3 grid = grid_of(gated_blocks(q.batch * ((q.dim + kChans - 1) / kChans), q.ways), 1024), block(1024);
     if (q.ways > 1) {
         clear_chain(q.chain, q.batch, q.dim, q.len, kRuns * TC, stream);
         if (q.reset) hipLaunchKernelGGL((gated_fwd_kernel<S, TC, true, STATES, true>), grid, block, 0, stream, q);
@@ -68,7 +68,7 @@ void run_fwd(const GatedParams& q, hipStream_t stream) {
 
 template <typename S>
 void run_bwd(const GatedBwdParams& q, hipStream_t stream) {
-    const dim3 grid((unsigned)gated_blocks(q.batch * ((q.dim + kChans - 1) / kChans), q.ways)), block(1024);
+    const dim3 grid = grid_of(gated_blocks(q.batch * ((q.dim + kChans - 1) / kChans), q.ways), 1024), block(1024);
     if (q.ways > 1) {
         clear_chain(q.chain, q.batch, q.dim, q.len, kGatedCk, stream);
         if (q.reset) hipLaunchKernelGGL((gated_bwd_kernel<S, 8, true, true>), grid, block, 0, stream, q);
@@ -77,7 +77,7 @@ void run_bwd(const GatedBwdParams& q, hipStream_t stream) {
         if (q.reset) hipLaunchKernelGGL((gated_bwd_kernel<S, 8, true, false>), grid, block, 0, stream, q);
         else hipLaunchKernelGGL((gated_bwd_kernel<S, 8, false, false>), grid, block, 0, stream, q);
     }
-    hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)((q.dim + 63) / 64)), dim3(1024), 0, stream, q.part, q.batch * q.nck,
+    hipLaunchKernelGGL(gated_dlam_kernel, grid_of((q.dim + 63) / 64, 1024), dim3(1024), 0, stream, q.part, q.batch * q.nck,
                        q.lam, q.dlam, q.dim);
 }
 

@@ -168,7 +168,8 @@ template <typename S>
 __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(NormArgs p) {
     __shared__ float lds[2][2][16];
     const int wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x;
+    const int64_t row = grid_block();
+    if (row >= p.rows) return;
     const S* x = static_cast<const S*>(p.x) + row * p.sx;
     const S* r = static_cast<const S*>(p.res) + row * p.sres;
     S* y = static_cast<S*>(p.y) + row * p.sy;
@@ -325,7 +326,8 @@ template <typename S>
 __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdArgs p) {
     __shared__ float lds[2][2][16];
     const int wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x;
+    const int64_t row = grid_block();
+    if (row >= p.rows) return;
     const S* t = static_cast<const S*>(p.t) + row * p.st;
     const S* dy = static_cast<const S*>(p.dy) + row * p.sdy;
     const S* dres = static_cast<const S*>(p.dres) + row * p.sdres;
@@ -427,7 +429,7 @@ int fwd_vec(const NormArgs& q, hipStream_t stream) {
     if (q.dim <= 64 * fwd_vals(1)) return fwd_width<S, V, 1>(q, stream);
     if (q.dim <= 256 * fwd_vals(4)) return fwd_width<S, V, 4>(q, stream);
     if (q.dim <= 1024 * fwd_vals(16)) return fwd_width<S, V, 16>(q, stream);
-    hipLaunchKernelGGL((norm_fwd_wide_kernel<S>), dim3((unsigned)q.rows), dim3(1024), 0, stream, q);
+    hipLaunchKernelGGL((norm_fwd_wide_kernel<S>), grid_of(q.rows, 1024), dim3(1024), 0, stream, q);
     return launch_status();
 }
 
@@ -450,7 +452,7 @@ int64_t bwd_vec(const NormBwdArgs& q, hipStream_t stream) {
     if (q.dim <= 64 * bwd_vals(1)) return bwd_width<S, V, 1>(q, stream);
     if (q.dim <= 256 * bwd_vals(4)) return bwd_width<S, V, 4>(q, stream);
     if (q.dim <= 1024 * bwd_vals(16)) return bwd_width<S, V, 16>(q, stream);
-    hipLaunchKernelGGL((norm_bwd_wide_kernel<S>), dim3((unsigned)q.rows), dim3(1024), 0, stream, q);
+    hipLaunchKernelGGL((norm_bwd_wide_kernel<S>), grid_of(q.rows, 1024), dim3(1024), 0, stream, q);
     if (!q.part) return 0;
     const int64_t n = q.rows < 64 ? q.rows : 64;
     hipLaunchKernelGGL((norm_cols_wide_kernel<S>), dim3((unsigned)((q.dim + 255) / 256), (unsigned)n), dim3(256), 0, stream, q);

@@ -51,6 +51,16 @@ inline int launch_status() { return hipGetLastError() == hipSuccess ? MAMBA_SCAN
 
 inline int64_t align256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
+// A grid of at least n workgroups. The threads of a grid's dimension are counted in 32 bits, and a launch
+// past them runs what is left of the count without an error; so more workgroups than that lie over y too.
+// The kernel's number of a workgroup is grid_block(); those from n on have nothing to do.
+inline dim3 grid_of(int64_t n, int threads) {
+    const int64_t most = (int64_t)0xFFFFFFFF / threads / 8 * 8;  // whole turns over the 8 XCDs
+    return n <= most ? dim3((unsigned)n) : dim3((unsigned)most, (unsigned)((n + most - 1) / most));
+}
+__device__ __forceinline__ int64_t grid_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+__device__ __forceinline__ int64_t grid_blocks() { return (int64_t)gridDim.y * gridDim.x; }
+
 int layers_cus();  // compute units of the current device (layers.hip); 256 if the runtime cannot say
 
 }  // namespace mscan
