@@ -38,8 +38,10 @@ extern "C" {
  *   y[b,t,d] = h_t;   last_state[b,d] = h after the last step
  *
  * A reset forgets the state before that step: sequences packed one after another do not see each
- * other. The recurrence's associative form, (a1, b1) then (a2, b2) = (a1 a2, a2 b1 + b2), is that of
- * the parallel scan of "手把手用PyTorch实现Mamba的SSM层从HiPPO矩阵到选择性扫描算法" §3.2.
+ * other. Nothing else forgets a NaN: one in x, r, i, lam or h0 reaches every state from there to the next
+ * reset (a reset step does not use its r). The recurrence's associative form, (a1, b1) then (a2, b2) =
+ * (a1 a2, a2 b1 + b2), is that of the parallel scan of "手把手用PyTorch实现Mamba的SSM层从HiPPO矩阵到
+ * 选择性扫描算法" §3.2.
  *  - x, r, i, y: `dtype`, strides {batch, len} free and >= 0 (slices of a projection's output are
  *    fine). h0, last_state: (batch, dim) fp32 contiguous; last_state may be h0's own buffer (a
  *    decoder's state updated in place). reset: (batch, len) bytes, contiguous, or NULL.

@@ -95,6 +95,14 @@ __device__ __forceinline__ float here(float v) {
     return v;
 }
 
+// A chunk's resets for a second loop over its steps: read again from the bits there, one scalar, where the
+// compiler would keep the first loop's selections, two scalars a step.
+template <bool RESET>
+__device__ __forceinline__ uint32_t again(uint32_t bits) {
+    if constexpr (RESET) asm volatile("" : "+s"(bits));
+    return bits;
+}
+
 // 1 - a^2 = 1 - e^-v at v = 2 ln(2) e, given a. For fp32 activations, below v = 1/4 the series
 // v (1 - v/2 + v^2/6 - v^3/24 + v^4/120 - v^5/720), coefficients scaled to e (truncation below 2^-24
 // relative); above, 1 - a^2 in one rounding, whose cancellation costs at most 3.6 times a's own error. For
@@ -117,41 +125,45 @@ __device__ __forceinline__ float one_minus_sq(float e, float a) {
     return e < (sizeof(S) == 4 ? 0.25f : 0.015625f) / k ? e * q : big;
 }
 
-// a h + b of the recurrence and of its folds. A reset's decay is exactly 0 and has to forget a state
-// that is infinite or NaN too: with resets the product is the one in which 0 times anything is 0, and
-// every other decay is kept above 0 (kMinDecay), so that only a reset forgets such a state.
-// v_mul_legacy_f32: 0 times anything is 0
-__device__ float mul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+// One step, `on` being whether it is a reset (the same for the whole wave): a h + b, and a v of the adjoint.
+// A reset forgets what lies before it, infinities and NaN among it, by a selection; every other step passes
+// them on, a NaN of its own decay too.
+template <bool RESET>
+__device__ __forceinline__ float step_fma(float a, float h, float b, bool on) {
+    const float v = __builtin_fmaf(a, h, b);
+    return RESET && on ? b : v;
+}
+template <bool RESET>
+__device__ __forceinline__ float step_mul(float a, float v, bool on) {
+    const float w = a * v;
+    return RESET && on ? 0.0f : w;
+}
+// A step's decay 2^-e; a reset's e is infinite.
+template <bool RESET>
+__device__ __forceinline__ float decay_step(float& e, bool on) {
+    if constexpr (RESET) e = on ? __builtin_inff() : e;
+    return hw_exp2(-e);
+}
+// Runs are folded as pairs (product of the decays, end state). A product of exactly 0 says that a reset lies
+// in the run; every other is kept above 0 (kMinDecay). A run with a NaN decay and no reset has a NaN end state
+// in either direction, so its product may be any but 0.
 constexpr float kMinDecay = 1.1754944e-38f;
 template <bool RESET>
 __device__ __forceinline__ float decay_fma(float a, float h, float b) {
-    if constexpr (RESET) return mul_legacy(a, h) + b;
-    return __builtin_fmaf(a, h, b);
-}
-template <bool RESET>
-__device__ __forceinline__ float decay_mul(float a, float v) {
-    if constexpr (RESET) return mul_legacy(a, v);
-    return a * v;
+    const float v = __builtin_fmaf(a, h, b);
+    return RESET && a == 0.0f ? b : v;
 }
 template <bool RESET>
 __device__ __forceinline__ float pair_product(float a, float b) {
     if constexpr (RESET) return __builtin_fmaxf(a * b, __builtin_fminf(__builtin_fminf(a, b), kMinDecay));
     return a * b;
 }
-// The decay of a run, 2^-e, and of a step: `on` is whether the step is a reset.
+// The product of a run, 2^-(the sum of its e); bits: its resets.
 template <bool RESET>
-__device__ __forceinline__ float decay_of(float e) {
-    const float a = hw_exp2(-e);
-    if constexpr (RESET) return e < __builtin_inff() ? __builtin_fmaxf(a, kMinDecay) : 0.0f;
+__device__ __forceinline__ float decay_of(float esum, uint32_t bits) {
+    const float a = hw_exp2(-esum);
+    if constexpr (RESET) return bits ? 0.0f : __builtin_fmaxf(a, kMinDecay);
     return a;
-}
-template <bool RESET>
-__device__ __forceinline__ float decay_step(float& e, bool on) {
-    if constexpr (RESET) {
-        e = __builtin_fmaxf(e, on ? __builtin_inff() : 0.0f);
-        return __builtin_fmaxf(hw_exp2(-e), on ? 0.0f : kMinDecay);
-    }
-    return hw_exp2(-e);
 }
 
 // A workgroup's chain (batch, channel group). Workgroups go to the 8 XCDs in turn: the ways of one chain are 8
@@ -232,13 +244,13 @@ __device__ __forceinline__ void gated_rows(S (&v)[TS], const Seq<const S>& q, in
     for (int k = 0; k < TS; ++k) row_load(v[k], r, FULL || k < left ? q.off : kGatedDrop, k * q.row_bytes());
 }
 
-// The reset bytes of a run as one bit each.
+// The reset bytes of a run, a lane's own each, 0 past the run's or the sequence's end; loaded before the run's
+// rows, so that no wait for them waits for the rows too, and one bit each where they are used.
 template <int N>
-__device__ __forceinline__ uint64_t gated_reset_bits(const uint8_t* reset, int64_t t_run, int64_t len, int lane) {
-    const int64_t t = t_run + lane;
-    const bool on = lane < N && t < len && reset[t < len ? t : len - 1] != 0;
-    return __ballot(on);
+__device__ __forceinline__ uint32_t gated_reset_byte(const uint8_t* reset, int64_t t_run, int left, int lane) {
+    return __builtin_amdgcn_raw_buffer_load_b8(gated_rsrc(reset + t_run), lane < N && lane < left ? lane : (int)kGatedDrop, 0, 0);
 }
+__device__ __forceinline__ uint32_t gated_reset_bits(uint32_t byte) { return (uint32_t)__ballot(byte != 0); }
 
 // Scans of the 16 lanes of a DPP row, one run's pair a lane (mul, add): the composition of the runs up to
 // and including the lane's, in run order (UP) or from the last run down.
@@ -396,15 +408,15 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
     ChunkWalk<CHAIN> walk(chain.tickets + at.chain, s_ticket, n);
 
     S nx[TS], nr[TS], ni[TS];
-    uint64_t nbits = 0;
+    uint32_t nreset = 0;
     auto fetch_as = [&](int64_t t0, auto full) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
         const int64_t tr = t0 + run * TS;
         const int left = (int)(L - tr < TS ? L - tr : TS);
+        if (RESET) nreset = gated_reset_byte<TS>(reset, tr, left, lane);
         gated_rows<S, TS, FULL>(nr, r, tr, left);
         gated_rows<S, TS, FULL>(ni, i, tr, left);
         gated_rows<S, TS, FULL>(nx, x, tr, left);
-        if (RESET) nbits = gated_reset_bits<TS>(reset, tr, L, lane);
     };
     auto fetch = [&](int chunk) __attribute__((always_inline)) {
         const int64_t t0 = (int64_t)chunk * STEPS;
@@ -428,7 +440,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
                 ci[k] = here(to_f32(ni[k]) * -kLog2e);
                 cx[k] = here(to_f32(nx[k]));
             }
-            const uint64_t bits = nbits;
+            const uint32_t bits = RESET ? gated_reset_bits(nreset) : 0;
             walk.ask();
             if (walk.next < n) fetch(walk.next);
             const int left = (int)(L - tr < TS ? L - tr : TS);  // steps of this run that exist
@@ -446,9 +458,9 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
                     }
                 }
                 esum += e;
-                h = decay_fma<RESET>(a[k], h, bb[k]);
+                h = step_fma<RESET>(a[k], h, bb[k], (bits >> k) & 1);
             }
-            s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), h);
+            s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum, bits), h);
             __syncthreads();
             {
                 float2 v = s_pair[s_run * kPitch + s_ch];
@@ -467,9 +479,10 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
             if (p.ck && live && tr % kGatedCk == 0 && left > 0) p.ck[(b * p.nck + tr / kGatedCk) * D + d] = in;
             if (STATES) {
                 const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + tr * y.st);
+                const uint32_t resets = again<RESET>(bits);
 #pragma unroll
                 for (int k = 0; k < TS; ++k) {
-                    in = decay_fma<RESET>(a[k], in, bb[k]);
+                    in = step_fma<RESET>(a[k], in, bb[k], (resets >> k) & 1);
                     row_store(from_f32<S>(in), o, live && (!TAIL || k < left) ? y.off : kGatedDrop, k * y.row_bytes());
                 }
                 if (p.last && walk.cur == n - 1 && s_run == 15 && s_live) p.last[b * D + ds] = carry;
@@ -484,6 +497,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
         // forward: 65 us, 82 without). The steps are written out again: sharing code with the loop above costs
         // that one spilled registers (4 x 100000 x 1024 bf16: 970 us instead of 926).
         int held = -1;
+        uint32_t held_bits = 0;
         float a[TS], bb[TS];
         float2 pairs = make_float2(1.0f, 0.0f);
         auto resolve = [&]() __attribute__((always_inline)) {
@@ -503,7 +517,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
                 const __amdgpu_buffer_rsrc_t o = gated_rsrc(y.base + tr * y.st);
 #pragma unroll
                 for (int k = 0; k < TS; ++k) {
-                    in = decay_fma<RESET>(a[k], in, bb[k]);
+                    in = step_fma<RESET>(a[k], in, bb[k], (held_bits >> k) & 1);
                     row_store(from_f32<S>(in), o, live && (!TAIL || k < left) ? y.off : kGatedDrop, k * y.row_bytes());
                 }
                 if (p.last && held == n - 1 && s_run == 15 && s_live) p.last[b * D + ds] = carry;
@@ -519,7 +533,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
                 ci[k] = here(to_f32(ni[k]) * -kLog2e);
                 cx[k] = here(to_f32(nx[k]));
             }
-            const uint64_t bits = nbits;
+            const uint32_t bits = RESET ? gated_reset_bits(nreset) : 0;
             walk.ask();
             if (walk.next < n) fetch(walk.next);
             const int left = (int)(L - tr < TS ? L - tr : TS);  // steps of this run that exist
@@ -537,9 +551,9 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
                     }
                 }
                 esum += e;
-                h = decay_fma<RESET>(na[k], h, nb[k]);
+                h = step_fma<RESET>(na[k], h, nb[k], (bits >> k) & 1);
             }
-            s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), h);
+            s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum, bits), h);
             __syncthreads();
             float2 v = s_pair[s_run * kPitch + s_ch];
             row_scan<true, RESET>(v.x, v.y);
@@ -550,6 +564,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
 #pragma unroll
             for (int k = 0; k < TS; ++k) a[k] = na[k], bb[k] = nb[k];
             pairs = v;
+            held_bits = bits;
             held = walk.cur;
             walk.advance();
         };
@@ -640,17 +655,17 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
     ChunkWalk<CHAIN> walk(chain.tickets + at.chain, s_ticket, n);
 
     S nx[TS], nr[TS], ni[TS], ng[TS];
-    uint64_t nbits = 0;
+    uint32_t nreset = 0;
     float nck = 0.0f;
     auto fetch_as = [&](int chunk, auto full) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
         const int64_t tr = (int64_t)chunk * STEPS + run * TS;
         const int left = (int)(L - tr < TS ? L - tr : TS);
+        if (RESET) nreset = gated_reset_byte<TS>(reset, tr, left, lane);
         gated_rows<S, TS, FULL>(nr, r, tr, left);
         gated_rows<S, TS, FULL>(ng, dy, tr, left);
         gated_rows<S, TS, FULL>(ni, i, tr, left);
         gated_rows<S, TS, FULL>(nx, x, tr, left);
-        if (RESET) nbits = gated_reset_bits<TS>(reset, tr, L, lane);
         nck = p.ck[(b * p.nck + chunk) * D + ds];
     };
     if (walk.cur < n) {
@@ -682,7 +697,7 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
             ci[k] = start(to_f32(ni[k]) * -kLog2e);
             cx[k] = start(to_f32(nx[k]));
         }
-        const uint64_t bits = nbits;
+        const uint32_t bits = RESET ? gated_reset_bits(nreset) : 0;
         const float ck = nck;
         walk.ask();
         if (walk.next < n) fetch_as(n - 1 - walk.next, std::true_type{});  // only the walk's first chunk is cut short
@@ -707,11 +722,11 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
             bb[k] = ms[k] * v;
             bi[k] = __builtin_fmaf(-bb[k], si, bb[k]);
             z[k] = a[k] * (rs * v);
-            hl = decay_fma<RESET>(a[k], hl, bb[k]);
+            hl = step_fma<RESET>(a[k], hl, bb[k], (bits >> k) & 1);
         }
 #pragma unroll
-        for (int k = TS - 1; k >= 0; --k) mu = decay_mul<RESET>(a[k], g[k] + mu);
-        s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum), hl);
+        for (int k = TS - 1; k >= 0; --k) mu = step_mul<RESET>(a[k], g[k] + mu, (bits >> k) & 1);
+        s_pair[run * kPitch + lane] = make_float2(decay_of<RESET>(esum, bits), hl);
         s_mu[run * kPitch + lane] = mu;
         __syncthreads();
         {
@@ -737,25 +752,26 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
         float in = o.y, acc = 0.0f;
         {
             float h = o.x;
+            const uint32_t resets = again<RESET>(bits);
 #pragma unroll
             for (int k = 0; k < TS; ++k) {  // z becomes z - h before the step
                 z[k] -= h;
-                h = decay_fma<RESET>(a[k], h, bb[k]);
+                h = step_fma<RESET>(a[k], h, bb[k], (resets >> k) & 1);
             }
         }
         const __amdgpu_buffer_rsrc_t ox = gated_rsrc(dx.base + tr * dx.st), oi = gated_rsrc(di.base + tr * di.st),
                                      orr = gated_rsrc(dr.base + tr * dr.st);
+        const uint32_t resets = again<RESET>(bits);
 #pragma unroll
         for (int k = TS - 1; k >= 0; --k) {
-            const bool put = live && (!TAIL || k < left);
+            const bool put = live && (!TAIL || k < left), on = (resets >> k) & 1;
             const float gk = g[k] + in;
-            in = decay_mul<RESET>(a[k], gk);
-            const float ek = RESET ? __builtin_fminf(e[k], 1e30f) : e[k];
-            const float q = decay_mul<RESET>(in * ek, z[k]);  // without its factor ln 2
+            in = step_mul<RESET>(a[k], gk, on);
+            const float q = step_mul<RESET>(in * e[k], z[k], on);  // without its factor ln 2; 0 at a reset
             acc += !TAIL || k < left ? q : 0.0f;
             row_store(from_f32<S>(gk * ms[k]), ox, put ? dx.off : kGatedDrop, k * dx.row_bytes());
             row_store(from_f32<S>(gk * bi[k]), oi, put ? di.off : kGatedDrop, k * di.row_bytes());
-            row_store(from_f32<S>(decay_mul<RESET>(q, __builtin_fmaf(-ek, inv_tl, kLn2))), orr, put ? dr.off : kGatedDrop,
+            row_store(from_f32<S>(step_mul<RESET>(q, __builtin_fmaf(-e[k], inv_tl, kLn2), on)), orr, put ? dr.off : kGatedDrop,
                       k * dr.row_bytes());
         }
         s_acc[run * kPitch + lane] = acc * kLn2;
