@@ -7,7 +7,7 @@ fallback. For each operator there is
 
 * ``<name>_fn``: the forward call;
 * ``<name>_bwd``: the gradients, given the incoming one;
-* ``<name>``: the differentiable form (torch autograd over the two).
+* ``<name>``: the differentiable form (torch autograd over the two; reverse mode, first derivatives).
 
 Activations are float32 or bfloat16; the recurrence's ``lam``, the norm's ``weight`` and ``bias``,
 states and statistics are taken in float32. Arithmetic is fp32; an activation's gradient has the
@@ -19,9 +19,10 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
-from .scan import BF16, F32, MambaScanError, _raise, load_library
+from .scan import BF16, F32, _raise, load_library
 
 _I64 = ctypes.c_int64
 _P = ctypes.c_void_p
@@ -368,6 +369,12 @@ class GatedScan(torch.autograd.Function):
 
 
 def _grad_on(*ts):
+    """Whether a gradient may be asked of what is computed from these. Forward-mode tangents are refused: the
+    kernels would return a result without one."""
+    # (outside every dual level, the usual case, no tensor is asked)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in ts):
+        raise NotImplementedError("the layer operators have no forward-mode derivative (an input has a tangent)")
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
 
 
