@@ -19,10 +19,9 @@ from __future__ import annotations
 import ctypes
 
 import torch
-from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
-from .scan import BF16, F32, _raise, load_library
+from .scan import BF16, F32, _raise, load_library, refuse_tangents
 
 _I64 = ctypes.c_int64
 _P = ctypes.c_void_p
@@ -368,19 +367,15 @@ class GatedScan(torch.autograd.Function):
         return g["x"], g["r"], g["i"], g["lam"].to(lam.dtype), dh0, None, None
 
 
-def _grad_on(*ts):
-    """Whether a gradient may be asked of what is computed from these. Forward-mode tangents are refused: the
-    kernels would return a result without one."""
-    # (outside every dual level, the usual case, no tensor is asked)
-    if getattr(forward_ad, "_current_level", 0) >= 0 and any(
-            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in ts):
-        raise NotImplementedError("the layer operators have no forward-mode derivative (an input has a tangent)")
+def _grad_on(entry, *ts):
+    """Whether a gradient may be asked of what is computed from these; forward-mode tangents are refused."""
+    refuse_tangents(ts, entry)
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
 
 
 def gated_scan(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state=False):
     """Differentiable :func:`gated_scan_fn`."""
-    if not _grad_on(x, r, i, lam, h0):
+    if not _grad_on("gated_scan", x, r, i, lam, h0):
         return gated_scan_fn(x, r, i, lam, c=c, h0=h0, reset=reset, return_last_state=return_last_state)
     y, last = GatedScan.apply(x, r, i, lam, h0, c, reset)
     return (y, last) if return_last_state else y
@@ -499,7 +494,7 @@ class LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, *, residual=None):
     """Differentiable :func:`layer_norm_fn`: y, or (y, t) with a residual."""
-    if not _grad_on(x, residual, weight, bias):
+    if not _grad_on("layer_norm", x, residual, weight, bias):
         return layer_norm_fn(x, weight, bias, eps, residual=residual)
     return LayerNorm.apply(x, residual, weight, bias, eps)
 
@@ -566,7 +561,7 @@ class Embedding(torch.autograd.Function):
 
 def embedding(ids, weight, scale=1.0):
     """Differentiable :func:`embedding_fn`."""
-    return Embedding.apply(ids, weight, scale) if _grad_on(weight) else embedding_fn(ids, weight, scale)
+    return Embedding.apply(ids, weight, scale) if _grad_on("embedding", weight) else embedding_fn(ids, weight, scale)
 
 
 # ---- gated feed-forward ----
@@ -643,6 +638,6 @@ class GatedFfn(torch.autograd.Function):
 
 def gated_ffn(x, w_gate, w_up, activation="silu"):
     """Differentiable :func:`gated_ffn_fn`."""
-    if not _grad_on(x, w_gate, w_up):
+    if not _grad_on("gated_ffn", x, w_gate, w_up):
         return gated_ffn_fn(x, w_gate, w_up, activation)
     return GatedFfn.apply(x, w_gate, w_up, activation)

@@ -17,6 +17,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmamba_scan.so")
@@ -384,6 +385,14 @@ def selective_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, d
     return g
 
 
+def refuse_tangents(inputs, entry):
+    """Raise where an input has a forward-mode tangent: the kernels would return a result without one."""
+    # (outside every dual level, the usual case, no tensor is asked)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in inputs):
+        raise NotImplementedError(f"{entry} has no forward-mode derivative (an input has a tangent)")
+
+
 class SelectiveScan(torch.autograd.Function):
     """y (and last_state) = selective_scan(...) with a backward pass through ``mamba_scan_bwd``.
 
@@ -434,8 +443,9 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
                    return_last_state=False, h0=None, zoh_b=False):
     """Differentiable form of ``selective_scan_fn`` (torch autograd through the HIP backward).
     When no gradient can flow (grad mode off, or no input requires one) it is the plain forward:
-    no states are saved for a backward that will not run."""
+    no states are saved for a backward that will not run. Forward-mode tangents are refused."""
     inputs = (u, delta, A, B, C, D, z, delta_bias, h0)
+    refuse_tangents(inputs, "selective_scan")
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)):
         return selective_scan_fn(u, delta, A, B, C, D=D, z=z, delta_bias=delta_bias,
                                  delta_softplus=delta_softplus, return_last_state=return_last_state,
