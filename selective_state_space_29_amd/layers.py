@@ -237,13 +237,17 @@ def _reset(reset, batch, length, like):
     return reset if reset.is_contiguous() else reset.contiguous()
 
 
-def _gated_inputs(x, r, i, lam, h0, reset, entry):
-    dtype = _dtype(x, "x")
-    _need_gpu(x, entry)
+def _gated_sizes(x):
     shape = x.shape
     if len(shape) != 3:
         raise ValueError(f"x must be (batch, len, dim), got {tuple(shape)}")
-    batch, length, dim = shape
+    return shape
+
+
+def _gated_inputs(x, r, i, lam, h0, reset, entry):
+    dtype = _dtype(x, "x")
+    _need_gpu(x, entry)
+    batch, length, dim = _gated_sizes(x)
     return (dtype, x, _same(r, x, "r"), _same(i, x, "i"), _f32(lam, "lam", (dim,), x),
             None if h0 is None else _f32(h0, "h0", (batch, dim), x), None if reset is None else _reset(reset, batch, length, x))
 
@@ -349,7 +353,7 @@ class GatedScan(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, r, i, lam, h0, c, reset):
-        ck = torch.empty(gated_checkpoint_shape(*x.shape), dtype=torch.float32, device=x.device)
+        ck = torch.empty(gated_checkpoint_shape(*_gated_sizes(x)), dtype=torch.float32, device=x.device)
         y, last = gated_scan_fn(x, r, i, lam, c=c, h0=h0, reset=reset, return_last_state=True, checkpoints_out=ck)
         ctx.save_for_backward(x, r, i, lam, h0, reset, ck)
         ctx.c = c

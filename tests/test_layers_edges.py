@@ -43,3 +43,10 @@ def test_forward_mode_tangents_of_the_scan_are_refused():
             given = list(inputs)
             given[k] = fwd.make_dual(inputs[k], torch.ones_like(inputs[k]))
             scan.selective_scan(*given)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_gated_scan_of_two_dimensions_is_refused_by_its_shape(grad):
+    x = torch.randn(5, 8, requires_grad=grad)
+    with pytest.raises(ValueError, match="GPU" if not grad else "batch, len, dim"):
+        layers.gated_scan(x, x, x, torch.randn(8))
