@@ -103,26 +103,23 @@ __device__ __forceinline__ uint32_t again(uint32_t bits) {
     return bits;
 }
 
-// 1 - a^2 = 1 - e^-v at v = 2 ln(2) e, given a. For fp32 activations, below v = 1/4 the series
+// 1 - a^2 = 1 - e^-v at v = 2 ln(2) e, given a. Below v = 1/4 the series
 // v (1 - v/2 + v^2/6 - v^3/24 + v^4/120 - v^5/720), coefficients scaled to e (truncation below 2^-24
-// relative); above, 1 - a^2 in one rounding, whose cancellation costs at most 3.6 times a's own error. For
-// bf16, whose results are rounded by 2^-9, three terms below v = 1/64: 2^-17 at most from cancellation, and
-// 3 instructions an element fewer.
-template <typename S>
+// relative); above, 1 - a^2 in one rounding, where cancellation costs at most 7.1 times a's own relative
+// error, and its square root 3.6 times. For bf16 activations too: states, checkpoints and lam's gradient are
+// fp32 there as well (three terms below v = 1/64 cost them 4 bits and saved 3 instructions of an element's
+// 33: 8 x 2048 x 1536 bf16 forward 55.2 us, 56.6 so).
 __device__ __forceinline__ float one_minus_sq(float e, float a) {
     constexpr float k = 1.3862943611198906f;  // 2 ln 2
     constexpr float c1 = k, c2 = -k * k / 2, c3 = k * k * k / 6, c4 = -k * k * k * k / 24,
                     c5 = k * k * k * k * k / 120, c6 = -k * k * k * k * k * k / 720;
-    float q = c3;
-    if constexpr (sizeof(S) == 4) {
-        q = __builtin_fmaf(e, c6, c5);
-        q = __builtin_fmaf(e, q, c4);
-        q = __builtin_fmaf(e, q, c3);
-    }
+    float q = __builtin_fmaf(e, c6, c5);
+    q = __builtin_fmaf(e, q, c4);
+    q = __builtin_fmaf(e, q, c3);
     q = __builtin_fmaf(e, q, c2);
     q = __builtin_fmaf(e, q, c1);
     const float big = __builtin_fmaf(-a, a, 1.0f);
-    return e < (sizeof(S) == 4 ? 0.25f : 0.015625f) / k ? e * q : big;
+    return e < 0.25f / k ? e * q : big;
 }
 
 // One step, `on` being whether it is a reset (the same for the whole wave): a h + b, and a v of the adjoint.
@@ -449,7 +446,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
             for (int k = 0; k < TS; ++k) {
                 float e = tl * sigmoid_of_scaled(cr[k]);
                 a[k] = decay_step<RESET>(e, (bits >> k) & 1);
-                const float m = __builtin_amdgcn_sqrtf(one_minus_sq<S>(e, a[k]));
+                const float m = __builtin_amdgcn_sqrtf(one_minus_sq(e, a[k]));
                 bb[k] = m * (sigmoid_of_scaled(ci[k]) * cx[k]);
                 if constexpr (TAIL) {  // past the end the state is carried
                     if (k >= left) {
@@ -542,7 +539,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
             for (int k = 0; k < TS; ++k) {
                 float e = tl * sigmoid_of_scaled(cr[k]);
                 na[k] = decay_step<RESET>(e, (bits >> k) & 1);
-                const float m = __builtin_amdgcn_sqrtf(one_minus_sq<S>(e, na[k]));
+                const float m = __builtin_amdgcn_sqrtf(one_minus_sq(e, na[k]));
                 nb[k] = m * (sigmoid_of_scaled(ci[k]) * cx[k]);
                 if constexpr (TAIL) {  // past the end the state is carried
                     if (k >= left) {
@@ -599,7 +596,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p) {
             h = 0.0f;
         }
         const float a = hw_exp2(-e);
-        const float m = __builtin_amdgcn_sqrtf(one_minus_sq<S>(e, a));
+        const float m = __builtin_amdgcn_sqrtf(one_minus_sq(e, a));
         h = __builtin_fmaf(a, h, m * (sigmoid_f(to_f32(i[t * p.si_t])) * to_f32(x[t * p.sx_t])));
         y[t * p.sy_t] = from_f32<S>(h);
     }
@@ -714,7 +711,7 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
                 if (past) a[k] = 1.0f, e[k] = g[k] = 0.0f;
             }
             esum += e[k];
-            const float w = one_minus_sq<S>(e[k], a[k]);
+            const float w = one_minus_sq(e[k], a[k]);
             // 1 / m; where m is 0, so are e and with it all that 1 / m enters, as long as it is finite
             const float rm = __builtin_amdgcn_rsqf(__builtin_fmaxf(w, 1.1754944e-38f));
             const float si = sigmoid_of_scaled(ci[k]), v = past ? 0.0f : cx[k], rs = rm * si;

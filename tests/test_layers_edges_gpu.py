@@ -1,4 +1,5 @@
-"""The layer operators at their edges: NaN in gates, decays and initial states of packed sequences.
+"""The layer operators at their edges: NaN in gates, decays and initial states of packed sequences, and the
+accuracy of the recurrence's fp32 results.
 
 A sequence that begins with a reset neither sees what lies before it nor passes a gradient there, so a bad
 value is judged against the clean call: where it reaches, NaN; everywhere else the same bits.
@@ -132,3 +133,34 @@ def test_gated_infinite_state_is_forgotten_by_a_reset_alone(B, L, D):
     assert not got["y"][0, :at[0], 3].isfinite().any()
     got["y"][0, :at[0], 3] = clean["y"][0, :at[0], 3]
     assert torch.equal(got["y"], clean["y"]) and torch.equal(got["last"], clean["last"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [1, 8, 9, 300, 700])
+def test_gated_states_are_fp32_whatever_the_activations(L, dtype):
+    """A state that is one step's input alone: sqrt(1 - a^2), at small decays, where 1 - a^2 cancels.
+
+    v = -2 log a = 2 c softplus(0) sigmoid(r) between 2^-8 and 2^-3, |r| <= 1. In units of 2^-24: c log2(e)
+    softplus 4, exp 3 (its argument's rounding and 1 ulp), 1 + exp 1, its reciprocal 2, the product 1: e errs by
+    11 of itself; 1 - a^2 by that and 3 of its own, and its root by half, 7, and 2 for itself. sigmoid(30) rounds
+    to 1 within 2^-24, two products: 12 in all.
+    """
+    D = 2048
+    c = (2.0 ** -8 * 32 ** torch.linspace(0, 1, 40, dtype=torch.float64) / (2 * 0.6931 * 0.7)).float()
+    r = (2 * torch.rand(40, 1, L, D, generator=torch.Generator().manual_seed(L)) - 1).to(dtype)
+    x = torch.zeros(1, L, D, dtype=dtype, device=DEV)
+    x[:, -1] = 1
+    i, lam = torch.full_like(x, 30.0), torch.zeros(D, device=DEV)
+    for k in range(40):
+        v = 2 * float(c[k]) * torch.log(torch.tensor(2.0, dtype=torch.float64)) * torch.sigmoid(r[k, 0, -1].double())
+        want = torch.sqrt(-torch.expm1(-v))
+        _, last = layers.gated_scan_fn(x, r[k].to(DEV), i, lam, c=float(c[k]), return_last_state=True)
+        assert float(((last[0].cpu().double() - want) / want).abs().max()) <= 12 * 2.0 ** -24
+        if L == 300:                                # the state after step 127, saved for the backward
+            u = torch.zeros_like(x)
+            u[:, 127] = 1
+            ck = torch.empty(layers.gated_checkpoint_shape(1, L, D), device=DEV)
+            layers.gated_scan_fn(u, r[k].to(DEV), i, lam, c=float(c[k]), checkpoints_out=ck)
+            v = 2 * float(c[k]) * torch.log(torch.tensor(2.0, dtype=torch.float64)) * torch.sigmoid(r[k, 0, 127].double())
+            want = torch.sqrt(-torch.expm1(-v))
+            assert float(((ck[0, 1].cpu().double() - want) / want).abs().max()) <= 12 * 2.0 ** -24
