@@ -133,7 +133,8 @@ int64_t mamba_gated_bwd_workspace_bytes(const mamba_gated_shape* s, mamba_scan_d
  *    fp32, each may be NULL (1, 0). stats: (rows, 2) fp32 {mean, rstd} or NULL.
  *  - sum is written exactly when residual is given. y or sum may be x's or residual's own buffer
  *    with the same stride (in place), but not each other's.
- *  - eps must be finite and >= 0. With eps = 0 a constant row is 0 * inf = NaN, as the formula says.
+ *  - eps must be finite and >= 0. With eps = 0 a constant row is 0 * inf = NaN, as the formula says. The
+ *    statistics of a row with a NaN are NaN.
  */
 typedef struct mamba_norm_shape {
     int64_t rows, dim;

@@ -68,6 +68,9 @@ __device__ __forceinline__ void row_sum(float (&v)[2], float (*lds)[2][WAVES], i
     }
 }
 
+// A variance, up from its rounding below 0; a row with a NaN keeps it (a maximum would drop it).
+__device__ __forceinline__ float no_less_than_0(float v) { return v < 0.0f ? 0.0f : v; }
+
 constexpr int kFwdWaves = 4;  // waves of a forward workgroup, unless a row takes more
 
 template <typename S, int V, int NV, int WPR>
@@ -144,7 +147,7 @@ __global__ __launch_bounds__(64 * (WPR > kFwdWaves ? WPR : kFwdWaves)) void norm
         }
         row_sum<2, WPR, WAVES>(q, lds, slot, wave);
         slot ^= 1;
-        const float off = q[0] * inv, var = __builtin_fmaxf(__builtin_fmaf(-off, off, q[1] * inv), 0.0f);
+        const float off = q[0] * inv, var = no_less_than_0(__builtin_fmaf(-off, off, q[1] * inv));
         const float rstd = __builtin_amdgcn_rsqf(var + p.eps);
         if (on) {
 #pragma unroll
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(NormArgs p) {
         q[1] = __builtin_fmaf(d, d, q[1]);
     }
     row_sum<2, 16, 16>(q, lds, 1, wave);
-    const float off = q[0] / (float)p.dim, var = __builtin_fmaxf(__builtin_fmaf(-off, off, q[1] / (float)p.dim), 0.0f);
+    const float off = q[0] / (float)p.dim, var = no_less_than_0(__builtin_fmaf(-off, off, q[1] / (float)p.dim));
     const float rstd = __builtin_amdgcn_rsqf(var + p.eps);
     for (int64_t c = threadIdx.x; c < p.dim; c += 1024) {
         const float v = at(c);  // before either store: y or sum may be x's or residual's buffer

@@ -164,3 +164,15 @@ def test_gated_states_are_fp32_whatever_the_activations(L, dtype):
             v = 2 * float(c[k]) * torch.log(torch.tensor(2.0, dtype=torch.float64)) * torch.sigmoid(r[k, 0, 127].double())
             want = torch.sqrt(-torch.expm1(-v))
             assert float(((ck[0, 1].cpu().double() - want) / want).abs().max()) <= 12 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [1, 40, 768, 2048, 9000, 40001])
+def test_norm_statistics_of_a_row_with_a_nan(dim, dtype):
+    x = torch.randn(5, dim, device=DEV).to(dtype)
+    y0, s0 = layers.layer_norm_fn(x, return_stats=True)
+    x[3, dim // 2] = float("nan")
+    y, s = layers.layer_norm_fn(x, return_stats=True)
+    keep = torch.arange(5, device=DEV) != 3
+    assert y[3].isnan().all() and s[3].isnan().all()
+    assert torch.equal(y[keep], y0[keep]) and torch.equal(s[keep], s0[keep])
