@@ -134,7 +134,7 @@ int64_t mamba_gated_bwd_workspace_bytes(const mamba_gated_shape* s, mamba_scan_d
  *  - sum is written exactly when residual is given. y or sum may be x's or residual's own buffer
  *    with the same stride (in place), but not each other's.
  *  - eps must be finite and >= 0. With eps = 0 a constant row is 0 * inf = NaN, as the formula says. The
- *    statistics of a row with a NaN are NaN.
+ *    statistics of a row with a NaN, and of a row without columns (dim = 0), are NaN.
  */
 typedef struct mamba_norm_shape {
     int64_t rows, dim;

@@ -313,8 +313,8 @@ int mamba_layer_norm_fwd(const mamba_norm_ptrs* p, const mamba_norm_shape* s, fl
         return MAMBA_SCAN_ERR_ARGS;
     const Bytes ins[] = {w, b}, outs[] = {y, sum, st};
     if (any_overlap(ins, outs) || meet(st, x) || meet(st, res)) return MAMBA_SCAN_ERR_ARGS;
-    if (s->rows == 0) return MAMBA_SCAN_OK;
-    if (s->dim == 0) return MAMBA_SCAN_OK;
+    // rows without columns have statistics all the same: 0 / 0
+    if (s->rows == 0 || (s->dim == 0 && !p->stats)) return MAMBA_SCAN_OK;
     return launch_norm_fwd(*p, *s, eps, dtype == MAMBA_SCAN_BF16, static_cast<hipStream_t>(stream));
 }
 

@@ -176,3 +176,15 @@ def test_norm_statistics_of_a_row_with_a_nan(dim, dtype):
     keep = torch.arange(5, device=DEV) != 3
     assert y[3].isnan().all() and s[3].isnan().all()
     assert torch.equal(y[keep], y0[keep]) and torch.equal(s[keep], s0[keep])
+
+
+def test_norm_statistics_of_rows_without_columns():
+    stale = torch.full((1000, 2), 7.0, device=DEV)
+    del stale
+    x = torch.zeros(1000, 0, device=DEV)
+    y, s = layers.layer_norm_fn(x, return_stats=True)
+    assert y.shape == (1000, 0) and s.isnan().all()
+    (y, t), s = layers.layer_norm_fn(x, residual=x, return_stats=True)
+    assert y.shape == t.shape == (1000, 0) and s.isnan().all()
+    g = layers.layer_norm_bwd(x, None, x, s)
+    assert g["x"].shape == (1000, 0) and g["weight"].shape == g["bias"].shape == (0,)
