@@ -29,6 +29,7 @@
 #include <type_traits>
 
 #include "layers_common.hpp"
+#include "xcd.hpp"
 
 namespace mscan {
 
@@ -163,25 +164,26 @@ __device__ __forceinline__ float decay_of(float esum, uint32_t bits) {
     return a;
 }
 
-// A workgroup's chain (batch, channel group). Workgroups go to the 8 XCDs in turn: the ways of one chain are 8
-// apart, so that they run on the same XCD and the slots pass through its L2, and an XCD has neighbouring
-// groups, so that rows that begin inside a cache line are fetched once for two groups (32 x 1000 x 700 fp32,
-// forward and backward: 300 us with neighbours on neighbouring XCDs, 248 so; no difference at whole lines).
+// A workgroup's chain (batch, channel group). The ways of the chains lie one after another, and an XCD takes one
+// stretch of them: neighbouring groups, so that rows that begin inside a cache line are fetched once for two
+// groups (32 x 1000 x 700 fp32, forward and backward: 300 us with neighbours on neighbouring XCDs, 248 so; no
+// difference at whole lines), a chain's ways together where they fit, and every XCD the same number of
+// workgroups. (Whole chains on one XCD leave XCDs idle where there are few: 1 x 100000 x 64 bf16 forward 152 us
+// on one XCD, 47 on all eight; 1 x 20000 x 768 80 and 59.)
 struct GatedPlace {
     int64_t chain, group, b;
     bool ok;
 };
 __device__ __forceinline__ GatedPlace gated_place(int64_t groups, int64_t batch, int ways) {
-    const int64_t id = grid_block();
+    const int64_t id = grid_block(), n = groups * batch * ways;
     GatedPlace p;
-    const int64_t per = (groups * batch + 7) / 8, slot = id / (8 * ways);
-    p.chain = id % 8 * per + slot;
-    p.ok = p.chain < groups * batch && slot < per;
+    p.chain = xcd_item(id, n) / ways;
+    p.ok = id < n;
     p.group = p.chain % groups;
     p.b = p.chain / groups;
     return p;
 }
-inline int64_t gated_blocks(int64_t chains, int ways) { return (chains + 7) / 8 * 8 * ways; }
+inline int64_t gated_blocks(int64_t chains, int ways) { return chains * ways; }
 
 // What the workgroups of a chain pass on: values beside a mark that they are there.
 __device__ __forceinline__ void word_put(uint64_t* w, float v) {

@@ -1,5 +1,9 @@
 """What the binding of the layer operators and of the scan refuses on the host, before anything runs."""
 
+import ctypes
+import os
+import subprocess
+
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
@@ -50,3 +54,21 @@ def test_gated_scan_of_two_dimensions_is_refused_by_its_shape(grad):
     x = torch.randn(5, 8, requires_grad=grad)
     with pytest.raises(ValueError, match="GPU" if not grad else "batch, len, dim"):
         layers.gated_scan(x, x, x, torch.randn(8))
+
+
+def test_workgroups_take_every_item_once_and_the_xcds_the_same_number(tmp_path):
+    """The placement of the recurrence's workgroups, built as host code: XCD k has the workgroups k, k + 8, ..."""
+    csrc = os.path.join(os.path.dirname(layers.__file__), "csrc")
+    src, lib = tmp_path / "place.cpp", tmp_path / "place.so"
+    src.write_text('#include "xcd.hpp"\nextern "C" int64_t place(int64_t id, int64_t n) { return mscan::xcd_item(id, n); }\n')
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", csrc, "-o", str(lib), str(src)], check=True)
+    place = ctypes.CDLL(str(lib)).place
+    place.restype, place.argtypes = ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64]
+    for n in [*range(1, 70), 192, 240, 252, 256, 257, 288, 1000, 4099]:
+        items = [[place(k, n) for k in range(xcd, n, 8)] for xcd in range(8)]
+        assert sorted(sum(items, [])) == list(range(n)), n
+        assert max(map(len, items)) - min(map(len, items)) <= 1, n
+        for own in items:
+            assert own == list(range(own[0], own[0] + len(own))) if own else True, n
+    # a chain of 64 channels shared by 256 workgroups: 32 of them on every XCD
+    assert [place(xcd, 256) // 32 for xcd in range(8)] == list(range(8))
