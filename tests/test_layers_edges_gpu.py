@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from selective_state_space_29_amd import layers
+from test_layers_gpu import check_gated, dev, gated_case
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +189,72 @@ def test_norm_statistics_of_rows_without_columns():
     assert y.shape == t.shape == (1000, 0) and s.isnan().all()
     g = layers.layer_norm_bwd(x, None, x, s)
     assert g["x"].shape == (1000, 0) and g["weight"].shape == g["bias"].shape == (0,)
+
+
+# Few chains of 64 channels, each shared by workgroups on one XCD or several; more than 16 chunks, whose states
+# pass on by blocks; a last chunk and a last group of channels that are cut short.
+SHARED = [(1, 9001, 40), (1, 5001, 70), (2, 2777, 130), (1, 4400, 576), (3, 1500, 200), (2, 700, 70)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("reset", [False, True])
+@pytest.mark.parametrize("B,L,D", SHARED)
+def test_gated_shared_sequences(B, L, D, reset, dtype):
+    """Against the 64-bit reference, by that test file's bars: forward, and the backward with and without states."""
+    check_gated(gated_case(21, B, L, D, dtype, reset=reset))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,L,D", SHARED)
+def test_gated_shared_sequences_repeat_bit_for_bit(B, L, D, dtype):
+    """Calls on other inputs in between leave their own marks in the same workspace."""
+    cases = [dev(gated_case(seed, B, L, D, dtype)) for seed in (22, 23)]
+
+    def once(t):
+        y, last = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], h0=t["h0"], return_last_state=True)
+        g = layers.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], h0=t["h0"], dlast_state=t["dlast"])
+        return [y, last, *g.values()]
+
+    want = [once(t) for t in cases]
+    for _ in range(20):
+        for t, w in zip(cases, want):
+            for a, b in zip(once(t), w):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,L,D", SHARED)
+def test_gated_shared_prompt_updates_its_state_in_place(B, L, D, dtype):
+    t = dev(gated_case(24, B, L, D, dtype))
+    args = (t["x"], t["r"], t["i"], t["lam"])
+    y, last = layers.gated_scan_fn(*args, h0=t["h0"], return_last_state=True)
+    for _ in range(10):
+        state = t["h0"].clone()
+        y2, same = layers.gated_scan_fn(*args, h0=state, return_last_state=True, last_state_out=state)
+        assert same is state and torch.equal(state, last) and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gated_shared_sequences_in_a_replayed_graph(dtype):
+    t = dev(gated_case(25, 1, 5001, 70, dtype))
+
+    def calls():
+        y, last = layers.gated_scan_fn(t["x"], t["r"], t["i"], t["lam"], h0=t["h0"], return_last_state=True)
+        return [y, last, *layers.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], h0=t["h0"]).values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for k in range(4):
+        for name in ("x", "dy"):
+            t[name].mul_(-1.25 if k % 2 else 0.8)
+        want = [v.clone() for v in calls()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, want):
+            assert torch.equal(a, b), k
