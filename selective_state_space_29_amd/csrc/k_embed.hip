@@ -310,6 +310,13 @@ __device__ __forceinline__ void sum_rows(const S* dy, int64_t dim, int64_t c, in
     else if (n - k == 1) add(k, 1, std::integral_constant<int, 1>{});
 }
 
+// What the lanes of a wave wrote to LDS before is what its lanes read after. A wave's accesses to LDS are in
+// order as it is; this keeps the compiler's order too, and is no instruction.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // The tokens of kGroupIds ids, from v0 up, among all: a workgroup of 16 waves looks through up to G groups of
 // 64 tokens a wave, one stretch of the list each. s_sorted receives them by id and in token order, those of
 // v0 + k from s_start[k] to s_start[k + 1].
@@ -335,6 +342,7 @@ __device__ __forceinline__ void find_tokens(const void* ids, int tokens, int64_t
         local[u] = hit ? (int)d : -1;
     }
     s_at[wave][lane] = 0;
+    wave_order();
     // each token found, in order, gets the place that s_at has for its id
     auto walk = [&](auto&& to) __attribute__((always_inline)) {
 #pragma unroll
@@ -353,6 +361,7 @@ __device__ __forceinline__ void find_tokens(const void* ids, int tokens, int64_t
                 to(at + rank, begin + u * 64 + lane);
                 if (rank == 0) s_at[wave][l] = at + (int)__popcll(same);
             }
+            wave_order();
         }
     };
     walk([](int, int) {});
@@ -372,6 +381,7 @@ __device__ __forceinline__ void find_tokens(const void* ids, int tokens, int64_t
     }
     __syncthreads();
     s_at[wave][lane] = sum - total + before;
+    wave_order();
     if (wave == 0) {
         s_start[lane] = sum - total;
         if (lane == 63) s_start[kGroupIds] = sum;
