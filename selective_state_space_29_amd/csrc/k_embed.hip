@@ -517,68 +517,64 @@ __global__ __launch_bounds__(256) void join_kernel(S* dweight, int64_t dim, floa
 }
 
 template <typename S, int V, typename I>
-int fwd_go(const void* ids, const void* w, void* y, const mamba_embedding_shape& s, float scale, hipStream_t stream) {
+void fwd_go(const void* ids, const void* w, void* y, const mamba_embedding_shape& s, float scale, Launches& on) {
     const int64_t need = (s.tokens + 3) / 4, most = (int64_t)layers_cus() * 64;
-    hipLaunchKernelGGL((embed_fwd_kernel<S, V, I>), dim3((unsigned)(need < most ? need : most)), dim3(256), 0, stream, ids,
-                       static_cast<const S*>(w), static_cast<S*>(y), s.tokens, s.vocab, s.dim, scale);
-    return launch_status();
+    on(embed_fwd_kernel<S, V, I>, dim3((unsigned)(need < most ? need : most)), dim3(256), ids,
+       static_cast<const S*>(w), static_cast<S*>(y), s.tokens, s.vocab, s.dim, scale);
 }
 
 // The widest pack (16 bytes and down) that rows of `dim` elements at both pointers are multiples of.
 template <typename S, int V = 16 / sizeof(S), typename F>
-int with_pack(int64_t dim, const void* a, const void* b, F&& f) {
+void with_pack(int64_t dim, const void* a, const void* b, F&& f) {
     if constexpr (V == 1) {
-        return f(std::integral_constant<int, 1>{});
+        f(std::integral_constant<int, 1>{});
     } else {
         const bool ok = dim % V == 0 && (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) % (V * sizeof(S)) == 0;
-        return ok ? f(std::integral_constant<int, V>{}) : with_pack<S, V / 2>(dim, a, b, f);
+        ok ? f(std::integral_constant<int, V>{}) : with_pack<S, V / 2>(dim, a, b, f);
     }
 }
 
 template <typename S, typename I>
-int fwd_typed(const void* ids, const void* w, void* y, const mamba_embedding_shape& s, float scale, hipStream_t stream) {
-    return with_pack<S>(s.dim, w, y, [&](auto v) { return fwd_go<S, decltype(v)::value, I>(ids, w, y, s, scale, stream); });
+void fwd_typed(const void* ids, const void* w, void* y, const mamba_embedding_shape& s, float scale, Launches& on) {
+    with_pack<S>(s.dim, w, y, [&](auto v) { fwd_go<S, decltype(v)::value, I>(ids, w, y, s, scale, on); });
 }
 
 template <typename S, typename I>
-int bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_embedding_shape& s, float scale,
-              hipStream_t stream) {
+void bwd_typed(const void* ids, const void* dy, void* dw, void* ws, const mamba_embedding_shape& s, float scale,
+               Launches& on) {
     if (direct(s)) {
         with_pack<S>(s.dim, dy, dw, [&](auto v) {
             constexpr int V = decltype(v)::value;
             const dim3 grid((unsigned)((s.vocab + kGroupIds - 1) / kGroupIds), (unsigned)((s.dim + 64 * V - 1) / (64 * V)));
-            hipLaunchKernelGGL((direct_kernel<S, V, I>), grid, dim3(1024), 0, stream, ids, (int)s.tokens, s.vocab,
-                               static_cast<const S*>(dy), static_cast<S*>(dw), s.dim, scale);
-            return 0;
+            on(direct_kernel<S, V, I>, grid, dim3(1024), ids, (int)s.tokens, s.vocab,
+               static_cast<const S*>(dy), static_cast<S*>(dw), s.dim, scale);
         });
-        return launch_status();
+        return;
     }
     const Lists l = lists_of(ws, s);
     auto grid = [](int64_t n, int64_t per) { return dim3((unsigned)((n + per - 1) / per)); };
     const int64_t zb = (l.clear + 255) / 256;
     int bits = 0;
     while ((s.vocab - 1) >> bits > 0) ++bits;
-    hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(zb < 2048 ? zb : 2048)), dim3(256), 0, stream, l.totals, l.clear);
+    on(zero_kernel, dim3((unsigned)(zb < 2048 ? zb : 2048)), dim3(256), l.totals, l.clear);
     if (s.tokens > 0) {  // (a wide row of no tokens comes here too)
-        hipLaunchKernelGGL((count_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, bits, l);
-        hipLaunchKernelGGL(place_kernel, grid(s.vocab, 1024), dim3(1024), 0, stream, s.vocab, l);
-        hipLaunchKernelGGL((fill_kernel<I>), grid(s.tokens, 256), dim3(256), 0, stream, ids, s.tokens, s.vocab, l);
+        on(count_kernel<I>, grid(s.tokens, 256), dim3(256), ids, s.tokens, s.vocab, bits, l);
+        on(place_kernel, grid(s.vocab, 1024), dim3(1024), s.vocab, l);
+        on(fill_kernel<I>, grid(s.tokens, 256), dim3(256), ids, s.tokens, s.vocab, l);
     }
     const unsigned longs = (unsigned)(l.max_long < 512 ? l.max_long : 512);
     if (longs)
-        hipLaunchKernelGGL((order_kernel<I>), dim3(longs * (kRank / kSlice)), dim3(1024), 0, stream, ids, s.tokens, l);
+        on(order_kernel<I>, dim3(longs * (kRank / kSlice)), dim3(1024), ids, s.tokens, l);
     with_pack<S>(s.dim, dy, dw, [&](auto v) {
         constexpr int V = decltype(v)::value;
         const int64_t waves = (l.max_piece + l.max_short) * ((s.dim + 64 * V - 1) / (64 * V)), most = (int64_t)layers_cus() * 64;
         const int64_t zeros = (s.vocab + kZeroIds - 1) / kZeroIds, sums = ((waves < most ? waves : most) + 3) / 4;
-        hipLaunchKernelGGL((reduce_kernel<S, V>), grid_of(zeros + sums, 256), dim3(256), 0, stream, static_cast<const S*>(dy),
-                           static_cast<S*>(dw), s.dim, scale, l, (int)zeros, s.vocab);
-        return 0;
+        on(reduce_kernel<S, V>, grid_of(zeros + sums, 256), dim3(256), static_cast<const S*>(dy),
+           static_cast<S*>(dw), s.dim, scale, l, (int)zeros, s.vocab);
     });
     if (longs)
-        hipLaunchKernelGGL((join_kernel<S>), dim3((unsigned)((s.dim + 255) / 256), longs), dim3(256), 0, stream,
-                           static_cast<S*>(dw), s.dim, scale, l);
-    return launch_status();
+        on(join_kernel<S>, dim3((unsigned)((s.dim + 255) / 256), longs), dim3(256),
+           static_cast<S*>(dw), s.dim, scale, l);
 }
 
 }  // namespace
@@ -587,20 +583,26 @@ int64_t embedding_bwd_workspace(const mamba_embedding_shape& s) { return direct(
 
 int launch_embedding_fwd(const void* ids, bool ids64, const void* weight, void* y, const mamba_embedding_shape& s, float scale,
                          bool bf16, hipStream_t stream) {
+    Launches on(stream);
     if (bf16)
-        return ids64 ? fwd_typed<bf16_t, int64_t>(ids, weight, y, s, scale, stream)
-                     : fwd_typed<bf16_t, int32_t>(ids, weight, y, s, scale, stream);
-    return ids64 ? fwd_typed<float, int64_t>(ids, weight, y, s, scale, stream)
-                 : fwd_typed<float, int32_t>(ids, weight, y, s, scale, stream);
+        ids64 ? fwd_typed<bf16_t, int64_t>(ids, weight, y, s, scale, on)
+              : fwd_typed<bf16_t, int32_t>(ids, weight, y, s, scale, on);
+    else
+        ids64 ? fwd_typed<float, int64_t>(ids, weight, y, s, scale, on)
+              : fwd_typed<float, int32_t>(ids, weight, y, s, scale, on);
+    return on.status;
 }
 
 int launch_embedding_bwd(const void* ids, bool ids64, const void* dy, void* dweight, void* ws, const mamba_embedding_shape& s,
                          float scale, bool bf16, hipStream_t stream) {
+    Launches on(stream);
     if (bf16)
-        return ids64 ? bwd_typed<bf16_t, int64_t>(ids, dy, dweight, ws, s, scale, stream)
-                     : bwd_typed<bf16_t, int32_t>(ids, dy, dweight, ws, s, scale, stream);
-    return ids64 ? bwd_typed<float, int64_t>(ids, dy, dweight, ws, s, scale, stream)
-                 : bwd_typed<float, int32_t>(ids, dy, dweight, ws, s, scale, stream);
+        ids64 ? bwd_typed<bf16_t, int64_t>(ids, dy, dweight, ws, s, scale, on)
+              : bwd_typed<bf16_t, int32_t>(ids, dy, dweight, ws, s, scale, on);
+    else
+        ids64 ? bwd_typed<float, int64_t>(ids, dy, dweight, ws, s, scale, on)
+              : bwd_typed<float, int32_t>(ids, dy, dweight, ws, s, scale, on);
+    return on.status;
 }
 
 }  // namespace mscan

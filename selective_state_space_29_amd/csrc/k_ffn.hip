@@ -663,35 +663,35 @@ Tiling tiling(int64_t P, int64_t Q, bool dual, int steps, bool may_split) {
 }
 
 template <bool XTR, bool YTR, int EPI>
-void run_mat(FfnMat m, const Tiling& t, hipStream_t stream) {
+void run_mat(FfnMat m, const Tiling& t, Launches& on) {
     m.tiles_p = t.tiles_p, m.tiles_q = t.tiles_q, m.splits = t.splits;
     const dim3 grid((unsigned)(t.tiles_p * t.tiles_q), (unsigned)t.splits);
     if (t.tp == 128) {
-        if (t.alone) hipLaunchKernelGGL((ffn_mat_kernel<128, 128, 2, 2, 4, XTR, YTR, EPI>), grid, dim3(256), 0, stream, m);
-        else hipLaunchKernelGGL((ffn_mat_kernel<128, 128, 2, 2, 2, XTR, YTR, EPI>), grid, dim3(256), 0, stream, m);
+        if (t.alone) on(ffn_mat_kernel<128, 128, 2, 2, 4, XTR, YTR, EPI>, grid, dim3(256), m);
+        else on(ffn_mat_kernel<128, 128, 2, 2, 2, XTR, YTR, EPI>, grid, dim3(256), m);
         return;
     }
     if constexpr (EPI == kEpiStore || EPI == kEpiPartial) {
         if (t.tq == 192) {
-            hipLaunchKernelGGL((ffn_mat_kernel<256, 192, 2, 4, 2, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
+            on(ffn_mat_kernel<256, 192, 2, 4, 2, XTR, YTR, EPI>, grid, dim3(512), m);
             return;
         }
     }
-    hipLaunchKernelGGL((ffn_mat_kernel<256, 256, 2, 4, 2, XTR, YTR, EPI>), grid, dim3(512), 0, stream, m);
+    on(ffn_mat_kernel<256, 256, 2, 4, 2, XTR, YTR, EPI>, grid, dim3(512), m);
 }
 
 template <bool XTR, bool YTR>
-void run_product(const FfnMat& m, const Tiling& t, hipStream_t stream) {
+void run_product(const FfnMat& m, const Tiling& t, Launches& on) {
     if (t.splits == 1) {
-        run_mat<XTR, YTR, kEpiStore>(m, t, stream);
+        run_mat<XTR, YTR, kEpiStore>(m, t, on);
         return;
     }
-    run_mat<XTR, YTR, kEpiPartial>(m, t, stream);
+    run_mat<XTR, YTR, kEpiPartial>(m, t, on);
     FfnMat j = m;
     j.splits = t.splits;
     const dim3 grid((unsigned)(m.P < 16384 ? m.P : 16384));
-    if (m.Q % 4 == 0) hipLaunchKernelGGL(ffn_join_kernel<4>, grid, dim3(256), 0, stream, j);
-    else hipLaunchKernelGGL(ffn_join_kernel<1>, grid, dim3(256), 0, stream, j);
+    if (m.Q % 4 == 0) on(ffn_join_kernel<4>, grid, dim3(256), j);
+    else on(ffn_join_kernel<1>, grid, dim3(256), j);
 }
 
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -710,7 +710,7 @@ struct Operands {
 int64_t copy_bytes(const mamba_ffn_shape& s) { return align256(s.rows * up(s.dim, 8) * 2) + 2 * align256(s.hidden * up(s.dim, 8) * 2); }
 
 Operands operands(const mamba_ffn_shape& s, const void* x, int64_t xs, const void* wg, int64_t gs, const void* wu, int64_t us,
-                  char* ws, hipStream_t stream) {
+                  char* ws, Launches& on) {
     Operands o{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(wg), static_cast<const uint16_t*>(wu), xs, gs, s.dim};
     if (!needs_copy(s, x, xs, wg, gs, wu, us)) return o;
     FfnCopy c{};
@@ -721,7 +721,7 @@ Operands operands(const mamba_ffn_shape& s, const void* x, int64_t xs, const voi
     c.src[1] = o.wg, c.dst[1] = to + xb, c.rows[1] = s.hidden, c.stride[1] = gs;
     c.src[2] = o.wu, c.dst[2] = to + xb + wb, c.rows[2] = s.hidden, c.stride[2] = us;
     const int64_t n = s.rows > s.hidden ? s.rows : s.hidden;
-    hipLaunchKernelGGL(ffn_copy_kernel, dim3((unsigned)(n < 32768 ? (n + 3) / 4 : 8192), 3), dim3(256), 0, stream, c);
+    on(ffn_copy_kernel, dim3((unsigned)(n < 32768 ? (n + 3) / 4 : 8192), 3), dim3(256), c);
     o.x = c.dst[0], o.wg = c.dst[1], o.wu = c.dst[2], o.xs = o.ws = o.dim8 = c.wide;
     return o;
 }
@@ -760,9 +760,9 @@ int launch_ffn_zero(void* p, int64_t rows, int64_t cols, int64_t stride, hipStre
     const int64_t n = rows * cols;
     if (n <= 0) return MAMBA_SCAN_OK;
     const int64_t g = (n + 255) / 256;
-    hipLaunchKernelGGL(ffn_zero_kernel, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), 0, stream, static_cast<uint16_t*>(p), n,
-                       cols, stride);
-    return launch_status();
+    Launches on(stream);
+    on(ffn_zero_kernel, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), static_cast<uint16_t*>(p), n, cols, stride);
+    return on.status;
 }
 
 int64_t ffn_workspace(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s) {
@@ -773,6 +773,7 @@ int64_t ffn_workspace(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s) {
 int64_t ffn_bwd_workspace(const mamba_ffn_shape& s) { return bwd_plan(s).total; }
 
 int launch_ffn_fwd(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s, int act, hipStream_t stream) {
+    Launches on(stream);
     if (s.rows <= kFewRows) {
         FfnMat m{};
         m.x = static_cast<const uint16_t*>(p.x), m.x_stride = p.x_stride;
@@ -782,29 +783,30 @@ int launch_ffn_fwd(const mamba_ffn_ptrs& p, const mamba_ffn_shape& s, int act, h
         m.out = static_cast<uint16_t*>(p.h), m.out_stride = p.h_stride;
         const dim3 grid((unsigned)((s.hidden + kFewUnits - 1) / kFewUnits)), block(kFewWaves * 64);
         if (s.rows <= 16)
-            hipLaunchKernelGGL(ffn_few_kernel<1>, grid, block, 0, stream, m);
+            on(ffn_few_kernel<1>, grid, block, m);
         else if (s.rows <= 32)
-            hipLaunchKernelGGL(ffn_few_kernel<2>, grid, block, 0, stream, m);
+            on(ffn_few_kernel<2>, grid, block, m);
         else
-            hipLaunchKernelGGL(ffn_few_kernel<3>, grid, block, 0, stream, m);
-        return launch_status();
+            on(ffn_few_kernel<3>, grid, block, m);
+        return on.status;
     }
     const Operands o = operands(s, p.x, p.x_stride, p.w_gate, p.w_gate_stride, p.w_up, p.w_up_stride,
-                                static_cast<char*>(p.workspace), stream);
+                                static_cast<char*>(p.workspace), on);
     FfnMat m = dual_mat(s, o, act);
     m.out = static_cast<uint16_t*>(p.h), m.out_stride = p.h_stride;
-    run_mat<false, false, kEpiDual>(m, tiling(s.rows, s.hidden, true, m.steps, false), stream);
-    return launch_status();
+    run_mat<false, false, kEpiDual>(m, tiling(s.rows, s.hidden, true, m.steps, false), on);
+    return on.status;
 }
 
 int launch_ffn_bwd(const mamba_ffn_bwd_ptrs& p, const mamba_ffn_shape& s, int act, hipStream_t stream) {
+    Launches on(stream);
     const BwdPlan b = bwd_plan(s);
     char* ws = static_cast<char*>(p.workspace);
-    const Operands o = operands(s, p.x, p.x_stride, p.w_gate, p.w_gate_stride, p.w_up, p.w_up_stride, ws + b.copy, stream);
+    const Operands o = operands(s, p.x, p.x_stride, p.w_gate, p.w_gate_stride, p.w_up, p.w_up_stride, ws + b.copy, on);
     uint16_t* d = reinterpret_cast<uint16_t*>(ws + b.d);
     FfnMat m = dual_mat(s, o, act);
     m.dh = static_cast<const uint16_t*>(p.dh), m.dh_stride = p.dh_stride, m.d = d, m.seg_rows = b.fp;
-    run_mat<false, false, kEpiDualBwd>(m, b.dual, stream);
+    run_mat<false, false, kEpiDualBwd>(m, b.dual, on);
 
     FfnMat x{};  // dx[p][q] = sum over gate and up units c of d[p][c] W[c][q]
     x.x = d, x.x_stride = 2 * b.fp, x.x_cols = b.fp, x.x_seg = b.fp;
@@ -813,7 +815,7 @@ int launch_ffn_bwd(const mamba_ffn_bwd_ptrs& p, const mamba_ffn_shape& s, int ac
     x.steps = steps_of(s.hidden), x.stretches = 2;
     x.out = x.out2 = static_cast<uint16_t*>(p.dx), x.out_stride = s.dim, x.seg_rows = x.seg_valid = s.rows;
     x.part = reinterpret_cast<float*>(ws + b.part);
-    run_product<false, true>(x, b.dx, stream);
+    run_product<false, true>(x, b.dx, on);
 
     FfnMat w{};  // dW[f][q] = sum over tokens c of d[c][f] x[c][q]
     w.x = d, w.x_stride = 2 * b.fp;
@@ -823,8 +825,8 @@ int launch_ffn_bwd(const mamba_ffn_bwd_ptrs& p, const mamba_ffn_shape& s, int ac
     w.out = static_cast<uint16_t*>(p.dw_gate), w.out2 = static_cast<uint16_t*>(p.dw_up), w.out_stride = s.dim;
     w.seg_rows = b.fp, w.seg_valid = s.hidden;
     w.part = reinterpret_cast<float*>(ws + b.part);
-    run_product<true, true>(w, b.dw, stream);
-    return launch_status();
+    run_product<true, true>(w, b.dw, on);
+    return on.status;
 }
 
 }  // namespace mscan

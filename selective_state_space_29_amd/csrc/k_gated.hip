@@ -46,48 +46,48 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint4* p, int64_t n) {
     for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) p[k] = make_uint4(0, 0, 0, 0);
 }
 
-void clear_chain(uint64_t* p, int64_t batch, int64_t dim, int64_t len, int chunk, hipStream_t stream) {
+void clear_chain(uint64_t* p, int64_t batch, int64_t dim, int64_t len, int chunk, Launches& on) {
     const int64_t n = (GatedChain::words(batch, dim, (len + chunk - 1) / chunk) + 1) / 2;  // the workspace ends on 256 bytes
     const int64_t g = (n + 511) / 512;
-    hipLaunchKernelGGL(gated_clear_kernel, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), 0, stream, reinterpret_cast<uint4*>(p), n);
+    on(gated_clear_kernel, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), reinterpret_cast<uint4*>(p), n);
 }
 
 template <typename S, bool STATES>
-void run_fwd(const GatedParams& q, hipStream_t stream) {
+void run_fwd(const GatedParams& q, Launches& on) {
     constexpr int TS = gated_fwd_ts(sizeof(S), false), TC = gated_fwd_ts(sizeof(S), true);
     const dim3 grid = grid_of(gated_blocks(q.batch * ((q.dim + kChans - 1) / kChans), q.ways), 1024), block(1024);
     if (q.ways > 1) {
-        clear_chain(q.chain, q.batch, q.dim, q.len, kRuns * TC, stream);
-        if (q.reset) hipLaunchKernelGGL((gated_fwd_kernel<S, TC, true, STATES, true>), grid, block, 0, stream, q);
-        else hipLaunchKernelGGL((gated_fwd_kernel<S, TC, false, STATES, true>), grid, block, 0, stream, q);
+        clear_chain(q.chain, q.batch, q.dim, q.len, kRuns * TC, on);
+        if (q.reset) on(gated_fwd_kernel<S, TC, true, STATES, true>, grid, block, q);
+        else on(gated_fwd_kernel<S, TC, false, STATES, true>, grid, block, q);
     } else {
-        if (q.reset) hipLaunchKernelGGL((gated_fwd_kernel<S, TS, true, STATES, false>), grid, block, 0, stream, q);
-        else hipLaunchKernelGGL((gated_fwd_kernel<S, TS, false, STATES, false>), grid, block, 0, stream, q);
+        if (q.reset) on(gated_fwd_kernel<S, TS, true, STATES, false>, grid, block, q);
+        else on(gated_fwd_kernel<S, TS, false, STATES, false>, grid, block, q);
     }
 }
 
 template <typename S>
-void run_bwd(const GatedBwdParams& q, hipStream_t stream) {
+void run_bwd(const GatedBwdParams& q, Launches& on) {
     const dim3 grid = grid_of(gated_blocks(q.batch * ((q.dim + kChans - 1) / kChans), q.ways), 1024), block(1024);
     if (q.ways > 1) {
-        clear_chain(q.chain, q.batch, q.dim, q.len, kGatedCk, stream);
-        if (q.reset) hipLaunchKernelGGL((gated_bwd_kernel<S, 8, true, true>), grid, block, 0, stream, q);
-        else hipLaunchKernelGGL((gated_bwd_kernel<S, 8, false, true>), grid, block, 0, stream, q);
+        clear_chain(q.chain, q.batch, q.dim, q.len, kGatedCk, on);
+        if (q.reset) on(gated_bwd_kernel<S, 8, true, true>, grid, block, q);
+        else on(gated_bwd_kernel<S, 8, false, true>, grid, block, q);
     } else {
-        if (q.reset) hipLaunchKernelGGL((gated_bwd_kernel<S, 8, true, false>), grid, block, 0, stream, q);
-        else hipLaunchKernelGGL((gated_bwd_kernel<S, 8, false, false>), grid, block, 0, stream, q);
+        if (q.reset) on(gated_bwd_kernel<S, 8, true, false>, grid, block, q);
+        else on(gated_bwd_kernel<S, 8, false, false>, grid, block, q);
     }
-    hipLaunchKernelGGL(gated_dlam_kernel, grid_of((q.dim + 63) / 64, 1024), dim3(1024), 0, stream, q.part, q.batch * q.nck,
-                       q.lam, q.dlam, q.dim);
+    on(gated_dlam_kernel, grid_of((q.dim + 63) / 64, 1024), dim3(1024), q.part, q.batch * q.nck,
+       q.lam, q.dlam, q.dim);
 }
 
 template <typename S>
-void fwd_typed(const GatedParams& q, hipStream_t stream) {
+void fwd_typed(const GatedParams& q, Launches& on) {
     if (q.len <= kStepMaxLen) {
         const int64_t n = q.batch * q.dim;
-        hipLaunchKernelGGL((gated_step_kernel<S>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, q);
+        on(gated_step_kernel<S>, dim3((unsigned)((n + 255) / 256)), dim3(256), q);
     } else {
-        run_fwd<S, true>(q, stream);
+        run_fwd<S, true>(q, on);
     }
 }
 
@@ -97,19 +97,22 @@ int gated_fwd_ways(const mamba_gated_shape& s, bool bf16, int cus) { return ways
 int gated_bwd_ways(const mamba_gated_shape& s, int cus) { return ways_for(s, cus, kGatedCk); }
 
 int launch_gated_fwd(const GatedParams& q, bool bf16, hipStream_t stream) {
-    bf16 ? fwd_typed<bf16_t>(q, stream) : fwd_typed<float>(q, stream);
-    return launch_status();
+    Launches on(stream);
+    bf16 ? fwd_typed<bf16_t>(q, on) : fwd_typed<float>(q, on);
+    return on.status;
 }
 
 // The checkpoints alone, for a backward that was not given them.
 int launch_gated_checkpoints(const GatedParams& q, bool bf16, hipStream_t stream) {
-    bf16 ? run_fwd<bf16_t, false>(q, stream) : run_fwd<float, false>(q, stream);
-    return launch_status();
+    Launches on(stream);
+    bf16 ? run_fwd<bf16_t, false>(q, on) : run_fwd<float, false>(q, on);
+    return on.status;
 }
 
 int launch_gated_bwd(const GatedBwdParams& q, bool bf16, hipStream_t stream) {
-    bf16 ? run_bwd<bf16_t>(q, stream) : run_bwd<float>(q, stream);
-    return launch_status();
+    Launches on(stream);
+    bf16 ? run_bwd<bf16_t>(q, on) : run_bwd<float>(q, on);
+    return on.status;
 }
 
 }  // namespace mscan

@@ -402,12 +402,11 @@ constexpr int kFwdWavesPerCu = 16;  // 25.5 us at 16384 x 768; 33 with 32 (fewer
 constexpr int64_t kBwdBlocks = 256;  // of 16 waves; their partial column sums are written and read once more
 
 template <typename S, int V, int NV, int WPR>
-int fwd_go(const NormArgs& q, hipStream_t stream) {
+void fwd_go(const NormArgs& q, Launches& on) {
     constexpr int WAVES = WPR > kFwdWaves ? WPR : kFwdWaves, RPB = WAVES / WPR;
     const int64_t need = (q.rows + RPB - 1) / RPB;
     const int64_t most = (int64_t)layers_cus() * kFwdWavesPerCu / WAVES;  // a few rows a wave: the weights are read once for them
-    hipLaunchKernelGGL((norm_fwd_kernel<S, V, NV, WPR>), dim3((unsigned)(need < most ? need : most)), dim3(64 * WAVES), 0, stream, q);
-    return launch_status();
+    on(norm_fwd_kernel<S, V, NV, WPR>, dim3((unsigned)(need < most ? need : most)), dim3(64 * WAVES), q);
 }
 
 // The smallest instantiated number of packs that holds `nv` (1, 2, 3, 4, 6, 8, 12, 16, 24, 32; at most M).
@@ -422,43 +421,42 @@ auto with_packs(int64_t nv, F&& f) {
 }
 
 template <typename S, int V, int WPR>
-int fwd_width(const NormArgs& q, hipStream_t stream) {
-    return with_packs<(fwd_vals(WPR) / V > 1 ? fwd_vals(WPR) / V : 1)>(
-        (q.dim + 64 * WPR * V - 1) / (64 * WPR * V), [&](auto nv) { return fwd_go<S, V, decltype(nv)::value, WPR>(q, stream); });
+void fwd_width(const NormArgs& q, Launches& on) {
+    with_packs<(fwd_vals(WPR) / V > 1 ? fwd_vals(WPR) / V : 1)>(
+        (q.dim + 64 * WPR * V - 1) / (64 * WPR * V), [&](auto nv) { fwd_go<S, V, decltype(nv)::value, WPR>(q, on); });
 }
 
 template <typename S, int V>
-int fwd_vec(const NormArgs& q, hipStream_t stream) {
-    if (q.dim <= 64 * fwd_vals(1)) return fwd_width<S, V, 1>(q, stream);
-    if (q.dim <= 256 * fwd_vals(4)) return fwd_width<S, V, 4>(q, stream);
-    if (q.dim <= 1024 * fwd_vals(16)) return fwd_width<S, V, 16>(q, stream);
-    hipLaunchKernelGGL((norm_fwd_wide_kernel<S>), grid_of(q.rows, 1024), dim3(1024), 0, stream, q);
-    return launch_status();
+void fwd_vec(const NormArgs& q, Launches& on) {
+    if (q.dim <= 64 * fwd_vals(1)) return fwd_width<S, V, 1>(q, on);
+    if (q.dim <= 256 * fwd_vals(4)) return fwd_width<S, V, 4>(q, on);
+    if (q.dim <= 1024 * fwd_vals(16)) return fwd_width<S, V, 16>(q, on);
+    on(norm_fwd_wide_kernel<S>, grid_of(q.rows, 1024), dim3(1024), q);
 }
 
 template <typename S, int V, int NV, int WPR>
-int64_t bwd_go(const NormBwdArgs& q, hipStream_t stream) {
+int64_t bwd_go(const NormBwdArgs& q, Launches& on) {
     constexpr int RPB = kBwdWaves / WPR;
     const int64_t need = (q.rows + RPB - 1) / RPB, n = need < kBwdBlocks ? need : kBwdBlocks;
-    hipLaunchKernelGGL((norm_bwd_kernel<S, V, NV, WPR>), dim3((unsigned)n), dim3(64 * kBwdWaves), 0, stream, q);
+    on(norm_bwd_kernel<S, V, NV, WPR>, dim3((unsigned)n), dim3(64 * kBwdWaves), q);
     return n;
 }
 
 template <typename S, int V, int WPR>
-int64_t bwd_width(const NormBwdArgs& q, hipStream_t stream) {
+int64_t bwd_width(const NormBwdArgs& q, Launches& on) {
     return with_packs<(bwd_vals(WPR) / V > 1 ? bwd_vals(WPR) / V : 1)>(
-        (q.dim + 64 * WPR * V - 1) / (64 * WPR * V), [&](auto nv) { return bwd_go<S, V, decltype(nv)::value, WPR>(q, stream); });
+        (q.dim + 64 * WPR * V - 1) / (64 * WPR * V), [&](auto nv) { return bwd_go<S, V, decltype(nv)::value, WPR>(q, on); });
 }
 
 template <typename S, int V>
-int64_t bwd_vec(const NormBwdArgs& q, hipStream_t stream) {
-    if (q.dim <= 64 * bwd_vals(1)) return bwd_width<S, V, 1>(q, stream);
-    if (q.dim <= 256 * bwd_vals(4)) return bwd_width<S, V, 4>(q, stream);
-    if (q.dim <= 1024 * bwd_vals(16)) return bwd_width<S, V, 16>(q, stream);
-    hipLaunchKernelGGL((norm_bwd_wide_kernel<S>), grid_of(q.rows, 1024), dim3(1024), 0, stream, q);
+int64_t bwd_vec(const NormBwdArgs& q, Launches& on) {
+    if (q.dim <= 64 * bwd_vals(1)) return bwd_width<S, V, 1>(q, on);
+    if (q.dim <= 256 * bwd_vals(4)) return bwd_width<S, V, 4>(q, on);
+    if (q.dim <= 1024 * bwd_vals(16)) return bwd_width<S, V, 16>(q, on);
+    on(norm_bwd_wide_kernel<S>, grid_of(q.rows, 1024), dim3(1024), q);
     if (!q.part) return 0;
     const int64_t n = q.rows < 64 ? q.rows : 64;
-    hipLaunchKernelGGL((norm_cols_wide_kernel<S>), dim3((unsigned)((q.dim + 255) / 256), (unsigned)n), dim3(256), 0, stream, q);
+    on(norm_cols_wide_kernel<S>, dim3((unsigned)((q.dim + 255) / 256), (unsigned)n), dim3(256), q);
     return n;
 }
 
@@ -478,15 +476,15 @@ auto with_pack(int64_t dim, std::initializer_list<std::pair<const void*, int64_t
 }
 
 template <typename S>
-int fwd_typed(const NormArgs& q, hipStream_t stream) {
-    return with_pack<S>(q.dim, {{q.x, q.sx}, {q.res, q.sres}, {q.y, q.sy}, {q.sum, q.ssum}},
-                        [&](auto v) { return fwd_vec<S, decltype(v)::value>(q, stream); });
+void fwd_typed(const NormArgs& q, Launches& on) {
+    with_pack<S>(q.dim, {{q.x, q.sx}, {q.res, q.sres}, {q.y, q.sy}, {q.sum, q.ssum}},
+                 [&](auto v) { fwd_vec<S, decltype(v)::value>(q, on); });
 }
 
 template <typename S>
-int64_t bwd_typed(const NormBwdArgs& q, hipStream_t stream) {
+int64_t bwd_typed(const NormBwdArgs& q, Launches& on) {
     return with_pack<S>(q.dim, {{q.t, q.st}, {q.dy, q.sdy}, {q.dres, q.sdres}, {q.dx, q.sdx}},
-                        [&](auto v) { return bwd_vec<S, decltype(v)::value>(q, stream); });
+                        [&](auto v) { return bwd_vec<S, decltype(v)::value>(q, on); });
 }
 
 }  // namespace
@@ -496,18 +494,21 @@ int64_t norm_bwd_workspace(const mamba_norm_shape& s) { return align256(kBwdBloc
 int launch_norm_fwd(const mamba_norm_ptrs& p, const mamba_norm_shape& s, float eps, bool bf16, hipStream_t stream) {
     NormArgs q{p.x, p.residual, p.weight, p.bias, p.y, p.sum, p.stats, s.rows, s.dim, p.x_stride, p.residual_stride,
                p.y_stride, p.sum_stride, eps};
-    return bf16 ? fwd_typed<bf16_t>(q, stream) : fwd_typed<float>(q, stream);
+    Launches on(stream);
+    bf16 ? fwd_typed<bf16_t>(q, on) : fwd_typed<float>(q, on);
+    return on.status;
 }
 
 int launch_norm_bwd(const mamba_norm_bwd_ptrs& p, const mamba_norm_shape& s, bool bf16, hipStream_t stream) {
     const bool sums = p.dweight || p.dbias;
     NormBwdArgs q{p.t, p.weight, p.stats, p.dy, p.dresidual, p.dx, sums ? static_cast<float*>(p.workspace) : nullptr,
                   s.rows, s.dim, p.t_stride, p.dy_stride, p.dresidual_stride, p.dx_stride};
-    const int64_t blocks = bf16 ? bwd_typed<bf16_t>(q, stream) : bwd_typed<float>(q, stream);
+    Launches on(stream);
+    const int64_t blocks = bf16 ? bwd_typed<bf16_t>(q, on) : bwd_typed<float>(q, on);
     if (sums)
-        hipLaunchKernelGGL(norm_cols_kernel, dim3((unsigned)((2 * s.dim + 31) / 32)), dim3(256), 0, stream,
-                           static_cast<const float*>(p.workspace), (int)blocks, s.dim, p.dweight, p.dbias);
-    return launch_status();
+        on(norm_cols_kernel, dim3((unsigned)((2 * s.dim + 31) / 32)), dim3(256),
+           static_cast<const float*>(p.workspace), (int)blocks, s.dim, p.dweight, p.dbias);
+    return on.status;
 }
 
 }  // namespace mscan

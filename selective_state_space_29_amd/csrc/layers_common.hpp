@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <tuple>
+
 #include "../../include/mamba_layers.h"
 #include "common.hpp"
 
@@ -47,7 +49,26 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-inline int launch_status() { return hipGetLastError() == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_LAUNCH; }
+// The launches of one call, on its stream: on(kernel, grid, block, arguments ...). The first that the runtime
+// refuses is the call's status, and none follows it. (The runtime's last error is no measure: it may be that
+// of another call of the thread, and belongs to that call's maker.)
+struct Launches {
+    hipStream_t stream;
+    int status = MAMBA_SCAN_OK;
+    explicit Launches(hipStream_t s) : stream(s) {}
+    template <typename... P, typename... A>
+    void operator()(void (*kernel)(P...), dim3 grid, dim3 block, const A&... args) {
+        if (status != MAMBA_SCAN_OK) return;
+        std::tuple<P...> held(args...);
+        std::apply(
+            [&](auto&... v) {
+                void* at[] = {const_cast<void*>(static_cast<const void*>(&v))...};
+                if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, at, 0, stream) != hipSuccess)
+                    status = MAMBA_SCAN_ERR_LAUNCH;
+            },
+            held);
+    }
+};
 
 inline int64_t align256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 

@@ -5,6 +5,8 @@ A sequence that begins with a reset neither sees what lies before it nor passes 
 value is judged against the clean call: where it reaches, NaN; everywhere else the same bits.
 """
 
+import ctypes
+
 import pytest
 import torch
 
@@ -258,3 +260,25 @@ def test_gated_shared_sequences_in_a_replayed_graph(dtype):
         torch.cuda.synchronize()
         for a, b in zip(captured, want):
             assert torch.equal(a, b), k
+
+
+def test_an_error_of_another_call_is_neither_reported_nor_taken():
+    """The runtime keeps a thread's last error until somebody asks for it; here that of a device that is not there."""
+    hip = ctypes.CDLL("libamdhip64.so")
+    x, ids = torch.randn(2, 9, 16, device=DEV), torch.zeros(2, 9, dtype=torch.int64, device=DEV)
+    lam, table = torch.zeros(16, device=DEV), torch.randn(5, 16, device=DEV)
+    xb, wb = x[0].bfloat16(), torch.randn(8, 16, device=DEV).bfloat16()
+    st, dh = layers.layer_norm_fn(x, return_stats=True)[1], torch.ones(9, 8, device=DEV).bfloat16()
+    for f in (lambda: layers.gated_scan_fn(x, x, x, lam), lambda: layers.gated_scan_bwd(x, x, x, lam, x),
+              lambda: layers.layer_norm_fn(x), lambda: layers.layer_norm_bwd(x, None, x, st),
+              lambda: layers.embedding_fn(ids, table), lambda: layers.embedding_bwd(ids, x, 5),
+              lambda: layers.gated_ffn_fn(xb, wb, wb), lambda: layers.gated_ffn_bwd(xb, wb, wb, dh)):
+        f()
+        torch.cuda.synchronize()
+        bad = hip.hipSetDevice(1000)
+        assert bad != 0
+        try:
+            f()
+        finally:
+            left = hip.hipGetLastError()
+        assert left == bad
