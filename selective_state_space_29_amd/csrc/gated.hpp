@@ -79,12 +79,13 @@ constexpr int kGatedCk = MAMBA_GATED_CHECKPOINT;
 // bf16, before the loop's last savings: 58 us; 64 with 256 steps, where the first chunk's load and the last
 // one's stores stand alone, and 62 with 128 steps loaded two chunks ahead). Chained workgroups exchange a
 // pair per chunk, and 256 steps halve that (4 x 100000 x 1024 bf16: 926 us; 1130 with 128 whose states wait
-// for the next chunk, 1366 with 128 as they come); fp32 loads take twice the bytes and keep 128.
+// for the next chunk, 1366 with 128 as they come; 940 since resets are selected and the series is whole);
+// fp32 loads take twice the bytes and keep 128.
 //
-// Bound by the VALU and HBM together: an element takes 24 vector instructions and 6 transcendental ones (30
-// and 6 with copies of the loaded values and without the DPP forms below). 8 x 2048 x 1536 bf16 54.5 us, 3.7
-// TB/s with 192 of 256 compute units at work; 32 x 2000 x 2500 290 us, 4.4 TB/s; 8 x 2048 x 1536 fp32 90 us,
-// 4.5 TB/s; a large copy reaches 4.6.
+// Bound by the VALU and HBM together: an element takes 27 vector instructions and 6 transcendental ones (33
+// and 6 with copies of the loaded values and without the DPP forms below). 8 x 2048 x 1536 bf16 56 us, 3.6
+// TB/s with 192 of 256 compute units at work; 32 x 2000 x 2500 293 us, 4.4 TB/s; 8 x 2048 x 1536 fp32 91 us,
+// 4.4 TB/s; a large copy reaches 4.6.
 constexpr int gated_fwd_ts(int bytes, bool chain) { return bytes == 2 && chain ? 16 : 8; }
 
 __device__ __forceinline__ float sigmoid_of_scaled(float s) { return hw_rcp(1.0f + hw_exp2(s)); }  // s = -log2(e) v
@@ -426,7 +427,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
     walk.second();
 
     const int whole = (int)(L / STEPS);
-    // bf16 runs of 16 steps have no registers for a second chunk's (4 x 100000 x 1024: 3500 us with it, 926 without)
+    // bf16 runs of 16 steps have no registers for a second chunk's (4 x 100000 x 1024: 3500 us with it where it took 926 without)
     constexpr bool DEFER = CHAIN && sizeof(S) == 4;
     if constexpr (!DEFER) {
         auto chunk = [&](auto tail) __attribute__((always_inline)) {
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(1024) void gated_fwd_kernel(GatedParams p) {
         // A chunk's states wait until the workgroup's next chunk is scanned: its neighbours' pairs are there by
         // then, and whoever has chunks before it finishes them without waiting for this one (2 x 8000 x 1024 fp32
         // forward: 65 us, 82 without). The steps are written out again: sharing code with the loop above costs
-        // that one spilled registers (4 x 100000 x 1024 bf16: 970 us instead of 926).
+        // that one spilled registers (4 x 100000 x 1024 bf16: 970 us where it took 926).
         int held = -1;
         uint32_t held_bits = 0;
         float a[TS], bb[TS];
@@ -613,8 +614,8 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedParams p) {
 // runs have the same product of a: one exchange serves both directions. Kept per step between the scans
 // and the outputs: a, b, e, m sigmoid(i), b (1 - sigmoid(i)), (s / m) a sigmoid(i) x / s, dy. Each
 // chunk's sum of q is written by itself (added up in order afterwards), so that it does not matter which
-// workgroup of a chain had which chunk. Bound by the VALU (49 plain and 6 transcendental instructions an
-// element) and HBM: 8 x 2048 x 1536 bf16 97 us for 352 MB with 192 of 256 compute units at work, 3.6 TB/s.
+// workgroup of a chain had which chunk. Bound by the VALU (52 plain and 6 transcendental instructions an
+// element) and HBM: 8 x 2048 x 1536 bf16 98 us for 352 MB with 192 of 256 compute units at work, 3.6 TB/s.
 template <typename S, int TS, bool RESET, bool CHAIN>
 __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
     constexpr int STEPS = kRuns * TS;
@@ -645,7 +646,8 @@ __global__ __launch_bounds__(1024) void gated_bwd_kernel(GatedBwdParams p) {
     const Seq<S> di(static_cast<S*>(p.di) + b * p.sdi_b, p.sdi_t, d);
     const uint8_t* reset = RESET ? p.reset + b * L : nullptr;
     const float tl = p.c * kLog2e * softplus_f(p.lam[d]);
-    const float inv_tl = tl > 1e-30f ? hw_rcp(tl) * kLn2 : 0.0f;  // sigmoid(r) = e / tl; below, every q is 0
+    // sigmoid(r) = e / tl. Below 1e-30 |q| is under 1e-14 |g sigmoid(i) x|, and its factor 1 - sigmoid(r) is left out.
+    const float inv_tl = tl > 1e-30f ? hw_rcp(tl) * kLn2 : 0.0f;
 
     float carry = p.dlast ? p.dlast[b * D + ds] : 0.0f;  // mu entering the chunk from the right
     const int n = (int)((L + STEPS - 1) / STEPS);  // chunk n - 1 - (number of the walk)
