@@ -9,6 +9,7 @@ import torch
 import torch.autograd.forward_ad as fwd
 
 from selective_state_space_29_amd import layers, scan
+from test_layers_abi import UNSUPPORTED, gated
 
 
 def operators():
@@ -72,3 +73,9 @@ def test_workgroups_take_every_item_once_and_the_xcds_the_same_number(tmp_path):
             assert own == list(range(own[0], own[0] + len(own))) if own else True, n
     # a chain of 64 channels shared by 256 workgroups: 32 of them on every XCD
     assert [place(xcd, 256) // 32 for xcd in range(8)] == list(range(8))
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_gated_limit_counts_groups_of_channels(bwd):
+    assert gated(shape=((1 << 23) - 8, 9, 1), bwd=bwd) == UNSUPPORTED  # a narrow row is a whole group
+    assert gated(shape=(1 << 18, 9, 1985), bwd=bwd) == UNSUPPORTED     # 32 groups a row
