@@ -1,0 +1,649 @@
+"""Python binding of the block operators' C ABI (``include/mamba_block.h``): what makes a Mamba block and its
+language model complete around the scan. The short causal convolution, the block's step from one token to the
+next, the norms before and after a block, and the cross entropy over the vocabulary.
+
+As in :mod:`.layers`, every step runs in ``libmamba_scan.so``; this module checks arguments, allocates outputs
+and workspaces with torch and launches on torch's current HIP stream. There is no CPU fallback. ``<name>_fn`` is
+the forward call, ``<name>_bwd`` the gradients given the incoming one, ``<name>`` the differentiable form (torch
+autograd over the two; reverse mode, first derivatives). ``block_step`` is for decoding and has no gradient.
+
+Activations are float32 or bfloat16 (the cross entropy bfloat16 only); convolution weights, norm weights,
+biases, ``A``, ``D``, scan states and statistics are taken in float32. Arithmetic is fp32; an activation's
+gradient has the activation's dtype, a parameter's the parameter's.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from .layers import (_dtype, _f32, _grad_on, _inner, _launch, _need_gpu, _on_device, _ptr, _reset, _row_stride, _rows,
+                     _same, _workspace)
+from .scan import load_library
+
+_I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
+_P = ctypes.c_void_p
+_F = ctypes.c_float
+_I = ctypes.c_int
+
+
+def _fields(pointers, sizes=(), flags=(), workspace=False):
+    return [(n, _P) for n in pointers.split()] + [(n, _I64) for n in sizes] + [(n, _I32) for n in flags] + (
+        [("workspace", _P), ("workspace_bytes", _I64)] if workspace else [])
+
+
+def _shape(*names):
+    return [(n, _I64) for n in names]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = _shape("batch", "len", "dim", "width")
+
+
+class ConvPtrs(ctypes.Structure):
+    _fields_ = _fields("x weight bias initial_state reset y last_state", ("x_batch", "x_row", "y_batch", "y_row"), ("x_steps", "y_steps"))
+
+
+class ConvBwdPtrs(ctypes.Structure):
+    _fields_ = _fields("x weight bias initial_state reset dy dlast_state dx dweight dbias dinitial_state",
+                       ("x_batch", "x_row", "dy_batch", "dy_row", "dx_batch", "dx_row"), ("x_steps", "dy_steps"), True)
+
+
+class StepShape(ctypes.Structure):
+    _fields_ = _shape("batch", "dim", "dstate", "dt_rank", "width")
+
+
+class StepPtrs(ctypes.Structure):
+    _fields_ = _fields("x z conv_state ssm_state conv_w conv_b w_x w_dt dt_bias A D conv_state_out ssm_state_out y",
+                       ("x_stride", "z_stride"), workspace=True)
+
+
+class RmsShape(ctypes.Structure):
+    _fields_ = _shape("rows", "dim")
+
+
+class RmsPtrs(ctypes.Structure):
+    _fields_ = _fields("x residual weight y sum stats", ("x_stride", "residual_stride", "y_stride", "sum_stride"))
+
+
+class RmsBwdPtrs(ctypes.Structure):
+    _fields_ = _fields("t weight stats dy dsum dx dresidual dweight",
+                       ("t_stride", "dy_stride", "dsum_stride", "dx_stride", "dresidual_stride"), workspace=True)
+
+
+class GatedRmsShape(ctypes.Structure):
+    _fields_ = _shape("rows", "dim", "groups")
+
+
+class GatedRmsPtrs(ctypes.Structure):
+    _fields_ = _fields("x z weight y stats", ("x_stride", "z_stride", "y_stride"))
+
+
+class GatedRmsBwdPtrs(ctypes.Structure):
+    _fields_ = _fields("x z weight stats dy dx dz dweight", ("x_stride", "z_stride", "dy_stride", "dx_stride", "dz_stride"),
+                       workspace=True)
+
+
+class XentShape(ctypes.Structure):
+    _fields_ = _shape("rows", "dim", "vocab")
+
+
+class XentPtrs(ctypes.Structure):
+    _fields_ = _fields("x weight target loss lse total", ("x_stride", "weight_stride"), workspace=True)
+
+
+class XentBwdPtrs(ctypes.Structure):
+    _fields_ = _fields("x weight target lse dloss dlse dx dweight", ("x_stride", "weight_stride", "dloss_stride", "dlse_stride"),
+                       workspace=True)
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = load_library()
+    ref = ctypes.POINTER
+    for name, restype, argtypes in (
+            ("mamba_block_abi_version", _I, []),
+            ("mamba_conv_fwd", _I, [ref(ConvPtrs), ref(ConvShape), _I, _I, _P]),
+            ("mamba_conv_bwd", _I, [ref(ConvBwdPtrs), ref(ConvShape), _I, _I, _P]),
+            ("mamba_conv_bwd_workspace_bytes", _I64, [ref(ConvShape), _I, _I]),
+            ("mamba_block_step", _I, [ref(StepPtrs), ref(StepShape), _I, _P]),
+            ("mamba_block_step_workspace_bytes", _I64, [ref(StepShape)]),
+            ("mamba_rms_norm_fwd", _I, [ref(RmsPtrs), ref(RmsShape), _F, _F, _I, _P]),
+            ("mamba_rms_norm_bwd", _I, [ref(RmsBwdPtrs), ref(RmsShape), _F, _I, _P]),
+            ("mamba_rms_norm_bwd_workspace_bytes", _I64, [ref(RmsShape)]),
+            ("mamba_gated_rms_norm_fwd", _I, [ref(GatedRmsPtrs), ref(GatedRmsShape), _I, _F, _I, _P]),
+            ("mamba_gated_rms_norm_bwd", _I, [ref(GatedRmsBwdPtrs), ref(GatedRmsShape), _I, _I, _P]),
+            ("mamba_gated_rms_norm_bwd_workspace_bytes", _I64, [ref(GatedRmsShape)]),
+            ("mamba_xent_fwd", _I, [ref(XentPtrs), ref(XentShape), _I, _F, _I, _P]),
+            ("mamba_xent_bwd", _I, [ref(XentBwdPtrs), ref(XentShape), _I, _F, _I, _P]),
+            ("mamba_xent_workspace_bytes", _I64, [ref(XentPtrs), ref(XentShape)]),
+            ("mamba_xent_bwd_workspace_bytes", _I64, [ref(XentBwdPtrs), ref(XentShape)])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = restype, argtypes
+    _lib = lib
+    return lib
+
+
+# ---- causal convolution ----
+
+_CONV_ACTS = {None: 0, "silu": 1}
+
+
+def _conv_layout(x):
+    """x of (batch, len, dim) as it lies: itself (copied where neither its channels nor its steps are side by
+    side), the strides of its batches and rows, and whether its rows are steps of a channel."""
+    batch, length, dim = x.stride()
+    B, L, D = x.shape
+    if dim == 1 or D <= 1:
+        return x, batch, length, 0
+    if length == 1 or L <= 1:
+        return x, batch, dim, 1
+    x = x.contiguous()
+    return x, x.stride(0), x.stride(1), 0
+
+
+def _conv_args(x, weight, bias, activation, initial_state, reset, entry):
+    dtype = _dtype(x, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x must be (batch, len, dim), got {tuple(x.shape)}")
+    if activation not in _CONV_ACTS:
+        raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
+    _need_gpu(x, entry)
+    batch, length, dim = x.shape
+    if weight.dim() == 3 and weight.shape[1] == 1:
+        weight = weight[:, 0]
+    if weight.dim() != 2 or weight.shape[0] != dim or not 1 <= weight.shape[1] <= 4:
+        raise ValueError(f"weight must be (dim, width) or (dim, 1, width) with dim = {dim} and width 1 to 4, got {tuple(weight.shape)}")
+    width = weight.shape[1]
+    weight, bias = _f32(weight, "weight", weight.shape, x), _f32(bias, "bias", (dim,), x)
+    state = _conv_state(initial_state, "initial_state", (batch, width - 1, dim), x)
+    return dtype, _CONV_ACTS[activation], weight, bias, state, _reset(reset, batch, length, x), width
+
+
+def _conv_state(state, name, shape, x):
+    if state is None:
+        return None
+    if state.dtype is not x.dtype or state.get_device() != x.get_device():
+        raise TypeError(f"{name} must have x's dtype and device")
+    if tuple(state.shape) != shape:
+        raise ValueError(f"{name} must be (batch, width - 1, dim) = {shape}, got {tuple(state.shape)}")
+    return state if state.is_contiguous() else state.contiguous()
+
+
+def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=None, reset=None, return_last_state=False,
+                   scan_layout=False, out=None, last_state_out=None):
+    """Short causal convolution of each channel and its activation::
+
+        y_t = silu(bias + sum_k weight[:, k] x_{t - width + 1 + k})
+
+    x: (batch, len, dim), float32 or bfloat16, with its channels or its steps side by side (a slice of a
+    projection's output, or the scan's (batch, dim, len) transposed, is read in place). weight: (dim, width) or
+    a Conv1d's (dim, 1, width), width 1 to 4. ``activation``: "silu" or None. ``initial_state``: (batch,
+    width - 1, dim) in x's dtype, the inputs before the first, oldest first (default: zeros). ``reset``: (batch,
+    len) bool or uint8; a set entry begins a sequence, which sees nothing from before it.
+
+    Returns y (batch, len, dim) in x's dtype, its channels side by side as x's or, with ``scan_layout`` or where
+    x's are not, its steps (``y.transpose(1, 2)`` is then what the scan takes as u); with ``return_last_state``
+    also the state to go on from. ``out``: y's tensor, of that layout; ``last_state_out``: the state's, which
+    may be ``initial_state`` itself (a decoder's state updated in place)."""
+    lib = _load()
+    dtype, act, weight, bias, state, reset, width = _conv_args(x, weight, bias, activation, initial_state, reset, "causal_conv_fn")
+    batch, length, dim = x.shape
+    x, xb, xr, steps = _conv_layout(x)
+    y_steps = 1 if steps or scan_layout else 0
+    if out is None:
+        y = x.new_empty((batch, dim, length)).transpose(1, 2) if y_steps else x.new_empty((batch, length, dim))
+    else:
+        y = out
+        if y.shape != x.shape or y.dtype is not x.dtype or y.device != x.device:
+            raise ValueError("out must have x's shape, dtype and device")
+        if y.stride(1 if y_steps else 2) != 1 and y.shape[1 if y_steps else 2] > 1:
+            raise ValueError(f"out must have its {'steps' if y_steps else 'channels'} side by side, as y has")
+    last = None
+    if return_last_state:
+        last = last_state_out
+        if last is None:
+            last = x.new_empty((batch, width - 1, dim))
+        elif last.shape != (batch, width - 1, dim) or last.dtype is not x.dtype or last.device != x.device or not last.is_contiguous():
+            raise ValueError("last_state_out must be a contiguous (batch, width - 1, dim) tensor of x's dtype and device")
+    ptrs = ConvPtrs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), y.data_ptr(), _ptr(last),
+                    xb, xr, y.stride(0), y.stride(2 if y_steps else 1), steps, y_steps)
+    _launch("mamba_conv_fwd", x, lib.mamba_conv_fwd, ptrs, ConvShape(batch, length, dim, width), act, dtype)
+    return (y, last) if return_last_state else y
+
+
+def causal_conv_bwd(x, weight, bias, dy, *, activation="silu", initial_state=None, reset=None, dlast_state=None,
+                    want_dinitial=None):
+    """Gradients of :func:`causal_conv_fn` for incoming ``dy`` (x's shape and dtype, either layout) and,
+    optionally, ``dlast_state`` (batch, width - 1, dim). Returns a dict: x in x's dtype and layout, weight
+    (dim, width) in fp32, bias (fp32) where there is one, and initial_state in x's dtype when ``want_dinitial``
+    (default: when one is given)."""
+    lib = _load()
+    dtype, act, weight, bias, state, reset, width = _conv_args(x, weight, bias, activation, initial_state, reset, "causal_conv_bwd")
+    batch, length, dim = x.shape
+    _same(dy, x, "dy")
+    x, xb, xr, steps = _conv_layout(x)
+    dy, gb, gr, g_steps = _conv_layout(dy)
+    if steps and not g_steps:
+        dy = dy.transpose(1, 2).contiguous().transpose(1, 2)
+        gb, gr, g_steps = dy.stride(0), dy.stride(2), 1
+    dlast = _conv_state(dlast_state, "dlast_state", (batch, width - 1, dim), x)
+    if want_dinitial is None:
+        want_dinitial = state is not None
+    dx = x.new_empty((batch, dim, length)).transpose(1, 2) if steps else x.new_empty((batch, length, dim))
+    out = {"x": dx, "weight": x.new_empty((dim, width), dtype=torch.float32)}
+    if bias is not None:
+        out["bias"] = x.new_empty((dim,), dtype=torch.float32)
+    if want_dinitial:
+        out["initial_state"] = x.new_empty((batch, width - 1, dim))
+    shape = ConvShape(batch, length, dim, width)
+    n = _on_device(x, lib.mamba_conv_bwd_workspace_bytes, shape, dtype, steps)
+    ws = _workspace(n, "mamba_conv_bwd_workspace_bytes", x)
+    ptrs = ConvBwdPtrs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), dy.data_ptr(), _ptr(dlast),
+                       dx.data_ptr(), out["weight"].data_ptr(), _ptr(out.get("bias")), _ptr(out.get("initial_state")),
+                       xb, xr, gb, gr, dx.stride(0), dx.stride(2 if steps else 1), steps, g_steps, _ptr(ws), n)
+    _launch("mamba_conv_bwd", x, lib.mamba_conv_bwd, ptrs, shape, act, dtype)
+    return out
+
+
+class CausalConv(torch.autograd.Function):
+    """y and the state after the last step, differentiable."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial_state, reset, activation, scan_layout):
+        y, last = causal_conv_fn(x, weight, bias, activation=activation, initial_state=initial_state, reset=reset,
+                                 return_last_state=True, scan_layout=scan_layout)
+        ctx.save_for_backward(x, weight, bias, initial_state, reset)
+        ctx.activation = activation
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        x, weight, bias, state, reset = ctx.saved_tensors
+        if dy is None and dlast is None:
+            return (None,) * 7
+        if dy is None:
+            dy = torch.zeros_like(x)
+        g = causal_conv_bwd(x, weight, bias, dy, activation=ctx.activation, initial_state=state, reset=reset, dlast_state=dlast)
+        return (g["x"], g["weight"].reshape(weight.shape).to(weight.dtype), None if bias is None else g["bias"].to(bias.dtype),
+                g.get("initial_state"), None, None, None)
+
+
+def causal_conv(x, weight, bias=None, *, activation="silu", initial_state=None, reset=None, return_last_state=False,
+                scan_layout=False):
+    """Differentiable :func:`causal_conv_fn`."""
+    if not _grad_on("causal_conv", x, weight, bias, initial_state):
+        return causal_conv_fn(x, weight, bias, activation=activation, initial_state=initial_state, reset=reset,
+                              return_last_state=return_last_state, scan_layout=scan_layout)
+    y, last = CausalConv.apply(x, weight, bias, initial_state, reset, activation, scan_layout)
+    return (y, last) if return_last_state else y
+
+
+# ---- block step ----
+
+def _state_out(given, old, name):
+    if given is None:
+        return old
+    if given.shape != old.shape or given.dtype is not old.dtype or given.device != old.device or not given.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of the state's shape, dtype and device")
+    return given
+
+
+def block_step(x, conv_state, ssm_state, conv_w, conv_b, w_x, w_dt, dt_bias, A, D=None, z=None, *, conv_state_out=None,
+               ssm_state_out=None):
+    """One token of each stream through a Mamba block's path from the convolution to the gate, what
+    :func:`.scan.block_ssm` does for whole sequences (there with u, the projections and delta rounded to
+    bfloat16, here kept in fp32)::
+
+        u = silu(conv_b + sum_k conv_w[:, k] v_k)     v = conv_state's rows, then x
+        dt, B, C = split(w_x u);  s = softplus(w_dt dt + dt_bias)
+        h = exp(s A) h + s B u;  y = (C h + D u) silu(z)
+
+    x, z: (batch, dim) float32 or bfloat16 (slices of one projection's output are read in place). conv_state:
+    (batch, width - 1, dim) in x's dtype, the last inputs, oldest first (:func:`causal_conv_fn`'s state);
+    ssm_state: (batch, dim, dstate) float32 (the scan's last_state). Both are updated in place, or left as they
+    are and the new ones written to ``conv_state_out`` and ``ssm_state_out``. conv_w: (dim, width) or (dim, 1,
+    width), width 2 to 4; w_x: (dt_rank + 2 dstate, dim) and w_dt: (dim, dt_rank) in x's dtype; conv_b, dt_bias, D: (dim,)
+    or None; A: (dim, dstate). Returns y (batch, dim) in float32, as the scan does."""
+    lib = _load()
+    dtype = _dtype(x, "x")
+    _need_gpu(x, "block_step")
+    if x.dim() != 2 or ssm_state.dim() != 3 or w_dt.dim() != 2:
+        raise ValueError("x must be (batch, dim), ssm_state (batch, dim, dstate) and w_dt (dim, dt_rank)")
+    batch, dim = x.shape
+    dstate, rank = ssm_state.shape[2], w_dt.shape[1]
+    if conv_w.dim() == 3 and conv_w.shape[1] == 1:
+        conv_w = conv_w[:, 0]
+    if conv_w.dim() != 2 or conv_w.shape[0] != dim or not 2 <= conv_w.shape[1] <= 4:
+        raise ValueError(f"conv_w must be (dim, width) with dim = {dim} and width 2 to 4, got {tuple(conv_w.shape)}")
+    width = conv_w.shape[1]
+    for name, t, shape, dt in (("conv_state", conv_state, (batch, width - 1, dim), x.dtype),
+                               ("ssm_state", ssm_state, (batch, dim, dstate), torch.float32),
+                               ("w_x", w_x, (rank + 2 * dstate, dim), x.dtype), ("w_dt", w_dt, (dim, rank), x.dtype)):
+        if t.dtype is not dt or t.get_device() != x.get_device():
+            raise TypeError(f"{name} must be {dt} on x's device")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if not conv_state.is_contiguous() or not ssm_state.is_contiguous():
+        raise ValueError("conv_state and ssm_state must be contiguous")
+    conv_out, ssm_out = _state_out(conv_state_out, conv_state, "conv_state_out"), _state_out(ssm_state_out, ssm_state, "ssm_state_out")
+    if z is not None:
+        z = _inner(_same(z, x, "z"))
+    x, w_x, w_dt = _inner(x), w_x.contiguous(), w_dt.contiguous()
+    conv_w, conv_b = _f32(conv_w, "conv_w", (dim, width), x), _f32(conv_b, "conv_b", (dim,), x)
+    dt_bias, A, D = _f32(dt_bias, "dt_bias", (dim,), x), _f32(A, "A", (dim, dstate), x), _f32(D, "D", (dim,), x)
+    y = x.new_empty((batch, dim), dtype=torch.float32)
+    shape = StepShape(batch, dim, dstate, rank, width)
+    n = lib.mamba_block_step_workspace_bytes(shape)
+    ws = _workspace(n, "mamba_block_step_workspace_bytes", x)
+    ptrs = StepPtrs(x.data_ptr(), _ptr(z), conv_state.data_ptr(), ssm_state.data_ptr(), conv_w.data_ptr(), _ptr(conv_b),
+                    w_x.data_ptr(), w_dt.data_ptr(), _ptr(dt_bias), A.data_ptr(), _ptr(D), conv_out.data_ptr(),
+                    ssm_out.data_ptr(), y.data_ptr(), _row_stride(x), 0 if z is None else _row_stride(z), _ptr(ws), n)
+    _launch("mamba_block_step", x, lib.mamba_block_step, ptrs, shape, dtype)
+    return y
+
+
+# ---- root-mean-square norms ----
+
+def rms_norm_fn(x, weight=None, eps=1e-5, *, residual=None, scale=1.0, return_stats=False):
+    """Root-mean-square norm over the last dimension, with the scaled residual added on the way::
+
+        t = residual + scale x, rounded to x's dtype     (t = x without a residual, scale unused)
+        y = t / sqrt(mean(t^2) + eps) * weight
+
+    x, residual: (..., dim), float32 or bfloat16; weight: (dim,) or None. Returns y, or (y, t) with a residual;
+    with ``return_stats`` a pair of that and the (rows,) fp32 inverse deviations that :func:`rms_norm_bwd`
+    takes."""
+    lib = _load()
+    dtype = _dtype(x, "x")
+    _need_gpu(x, "rms_norm_fn")
+    shape = x.shape
+    xr, rows, xs = _rows(x, "x")
+    dim = shape[-1]
+    rr, _, rs = (None, 0, 0) if residual is None else _rows(_same(residual, x, "residual"), "residual")
+    weight = _f32(weight, "weight", (dim,), x)
+    y = x.new_empty(shape)
+    t = None if residual is None else x.new_empty(shape)
+    stats = x.new_empty((rows,), dtype=torch.float32) if return_stats else None
+    ptrs = RmsPtrs(xr.data_ptr(), _ptr(rr), _ptr(weight), y.data_ptr(), _ptr(t), _ptr(stats), xs, rs, dim, dim)
+    _launch("mamba_rms_norm_fwd", x, lib.mamba_rms_norm_fwd, ptrs, RmsShape(rows, dim), scale, eps, dtype)
+    out = y if residual is None else (y, t)
+    return (out, stats) if return_stats else out
+
+
+def rms_norm_bwd(t, weight, dy, stats, *, dresidual=None, scale=1.0, want_dweight=True):
+    """Gradients of :func:`rms_norm_fn` at ``t`` (its x, or the sum it returned) with its ``stats``.
+    ``dresidual``: the gradient that reaches t by the residual stream, added to the result; ``scale``: the
+    forward's, with a residual. Returns a dict: residual (the gradient at t) and x (scale times that; the same
+    tensor where scale is 1) in t's dtype, weight (fp32) where wanted."""
+    lib = _load()
+    dtype = _dtype(t, "t")
+    _need_gpu(t, "rms_norm_bwd")
+    for name, v in (("dy", dy), ("dresidual", dresidual)):
+        if v is not None:
+            _same(v, t, name)
+    (tr, rows, ts), (gr, _, gs) = _rows(t, "t"), _rows(dy, "dy")
+    rr, _, rs = (None, 0, 0) if dresidual is None else _rows(dresidual, "dresidual")
+    dim = t.shape[-1]
+    weight, stats = _f32(weight, "weight", (dim,), t), _f32(stats, "stats", (rows,), t)
+    dt = t.new_empty(t.shape)
+    dx = t.new_empty(t.shape) if scale != 1.0 else None
+    out = {"x": dt if dx is None else dx, "residual": dt}
+    if want_dweight:
+        out["weight"] = t.new_empty((dim,), dtype=torch.float32)
+    shape = RmsShape(rows, dim)
+    n = lib.mamba_rms_norm_bwd_workspace_bytes(shape) if want_dweight else 0
+    ws = _workspace(n, "mamba_rms_norm_bwd_workspace_bytes", t)
+    ptrs = RmsBwdPtrs(tr.data_ptr(), _ptr(weight), stats.data_ptr(), gr.data_ptr(), _ptr(rr), _ptr(dx), dt.data_ptr(),
+                      _ptr(out.get("weight")), ts, gs, rs, dim, dim, _ptr(ws), n)
+    _launch("mamba_rms_norm_bwd", t, lib.mamba_rms_norm_bwd, ptrs, shape, scale, dtype)
+    return out
+
+
+class RmsNorm(torch.autograd.Function):
+    """y, and the residual stream t where a residual is given."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, scale):
+        out, stats = rms_norm_fn(x, weight, eps, residual=residual, scale=scale, return_stats=True)
+        ctx.save_for_backward(x if residual is None else out[1], weight, stats)
+        ctx.scale = None if residual is None else scale
+        ctx.set_materialize_grads(False)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dt=None):
+        t, weight, stats = ctx.saved_tensors
+        if dy is None and dt is None:
+            return (None,) * 5
+        if dy is None:
+            dy = torch.zeros_like(t)
+        g = rms_norm_bwd(t, weight, dy, stats, dresidual=dt, scale=1.0 if ctx.scale is None else ctx.scale,
+                         want_dweight=ctx.needs_input_grad[2])
+        return (g["x"], None if ctx.scale is None else g["residual"], g["weight"].to(weight.dtype) if "weight" in g else None,
+                None, None)
+
+
+def rms_norm(x, weight=None, eps=1e-5, *, residual=None, scale=1.0):
+    """Differentiable :func:`rms_norm_fn`: y, or (y, t) with a residual."""
+    if not _grad_on("rms_norm", x, residual, weight):
+        return rms_norm_fn(x, weight, eps, residual=residual, scale=scale)
+    return RmsNorm.apply(x, residual, weight, eps, scale)
+
+
+def _gated_args(x, z, weight, groups, entry):
+    dtype = _dtype(x, "x")
+    _need_gpu(x, entry)
+    _same(z, x, "z")
+    xr, rows, xs = _rows(x, "x")
+    zr, _, zs = _rows(z, "z")
+    dim = x.shape[-1]
+    if groups < 1 or dim % groups:
+        raise ValueError(f"groups must divide dim = {dim}, got {groups}")
+    return dtype, xr, xs, zr, zs, _f32(weight, "weight", (dim,), x), rows, dim
+
+
+def gated_rms_norm_fn(x, z, weight=None, eps=1e-5, *, groups=1, gate_first=True, return_stats=False):
+    """The root-mean-square norm after a block's scan, with its gate z; each of ``groups`` stretches of the last
+    dimension is normalised by itself::
+
+        gate_first:  v = x silu(z),  y = v / sqrt(mean(v^2) + eps) * weight
+        otherwise:   y = x / sqrt(mean(x^2) + eps) * weight * silu(z)
+
+    x, z: (..., dim), float32 or bfloat16 (slices of one projection's output are read in place); weight: (dim,)
+    or None. Returns y in x's dtype; with ``return_stats`` also the (rows, groups) fp32 inverse deviations that
+    :func:`gated_rms_norm_bwd` takes."""
+    lib = _load()
+    dtype, xr, xs, zr, zs, weight, rows, dim = _gated_args(x, z, weight, groups, "gated_rms_norm_fn")
+    y = x.new_empty(x.shape)
+    stats = x.new_empty((rows, groups), dtype=torch.float32) if return_stats else None
+    ptrs = GatedRmsPtrs(xr.data_ptr(), zr.data_ptr(), _ptr(weight), y.data_ptr(), _ptr(stats), xs, zs, dim)
+    _launch("mamba_gated_rms_norm_fwd", x, lib.mamba_gated_rms_norm_fwd, ptrs, GatedRmsShape(rows, dim, groups), gate_first, eps, dtype)
+    return (y, stats) if return_stats else y
+
+
+def gated_rms_norm_bwd(x, z, weight, dy, stats, *, groups=1, gate_first=True, want_dweight=True):
+    """Gradients of :func:`gated_rms_norm_fn` with its ``stats``: a dict of x and z in x's dtype, weight (fp32)
+    where wanted."""
+    lib = _load()
+    dtype, xr, xs, zr, zs, weight, rows, dim = _gated_args(x, z, weight, groups, "gated_rms_norm_bwd")
+    gr, _, gs = _rows(_same(dy, x, "dy"), "dy")
+    stats = _f32(stats, "stats", (rows, groups), x)
+    out = {"x": x.new_empty(x.shape), "z": x.new_empty(x.shape)}
+    if want_dweight:
+        out["weight"] = x.new_empty((dim,), dtype=torch.float32)
+    shape = GatedRmsShape(rows, dim, groups)
+    n = lib.mamba_gated_rms_norm_bwd_workspace_bytes(shape) if want_dweight else 0
+    ws = _workspace(n, "mamba_gated_rms_norm_bwd_workspace_bytes", x)
+    ptrs = GatedRmsBwdPtrs(xr.data_ptr(), zr.data_ptr(), _ptr(weight), stats.data_ptr(), gr.data_ptr(), out["x"].data_ptr(),
+                           out["z"].data_ptr(), _ptr(out.get("weight")), xs, zs, gs, dim, dim, _ptr(ws), n)
+    _launch("mamba_gated_rms_norm_bwd", x, lib.mamba_gated_rms_norm_bwd, ptrs, shape, gate_first, dtype)
+    return out
+
+
+class GatedRmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, z, weight, eps, groups, gate_first):
+        y, stats = gated_rms_norm_fn(x, z, weight, eps, groups=groups, gate_first=gate_first, return_stats=True)
+        ctx.save_for_backward(x, z, weight, stats)
+        ctx.kw = dict(groups=groups, gate_first=gate_first)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, z, weight, stats = ctx.saved_tensors
+        g = gated_rms_norm_bwd(x, z, weight, dy, stats, want_dweight=ctx.needs_input_grad[2], **ctx.kw)
+        return g["x"], g["z"], g["weight"].to(weight.dtype) if "weight" in g else None, None, None, None
+
+
+def gated_rms_norm(x, z, weight=None, eps=1e-5, *, groups=1, gate_first=True):
+    """Differentiable :func:`gated_rms_norm_fn`."""
+    if not _grad_on("gated_rms_norm", x, z, weight):
+        return gated_rms_norm_fn(x, z, weight, eps, groups=groups, gate_first=gate_first)
+    return GatedRmsNorm.apply(x, z, weight, eps, groups, gate_first)
+
+
+# ---- cross entropy over the vocabulary ----
+
+def _xent_args(x, weight, target, entry):
+    dtype = _dtype(x, "x")
+    _need_gpu(x, entry)
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError("x must be (..., dim) and weight (vocab, dim)")
+    if weight.dtype is not x.dtype or weight.get_device() != x.get_device():
+        raise TypeError("weight must have x's dtype and device")
+    if weight.shape[1] != x.shape[-1]:
+        raise ValueError(f"weight must be (vocab, dim) with dim = {x.shape[-1]}, got {tuple(weight.shape)}")
+    if target is not None:
+        if target.dtype not in (torch.int64, torch.int32):
+            raise TypeError(f"target must be int64 or int32, got {target.dtype}")
+        if target.shape != x.shape[:-1] or target.get_device() != x.get_device():
+            raise ValueError(f"target must be {tuple(x.shape[:-1])} on x's device, got {tuple(target.shape)}")
+        target = target.contiguous()
+    xr, rows, xs = _rows(x, "x")
+    weight = _inner(weight)
+    return dtype, xr, rows, xs, weight, _row_stride(weight), target
+
+
+def _xent_launch(name, x, f, size, ptrs, shape, *args):
+    n = _on_device(x, size, ptrs, shape)
+    ws = _workspace(n, name, x)
+    ptrs.workspace, ptrs.workspace_bytes = _ptr(ws), n
+    _launch(name, x, f, ptrs, shape, *args)
+
+
+def _xent_fwd(x, weight, target, scale, want_lse, want_total, entry):
+    lib = _load()
+    dtype, xr, rows, xs, weight, ws, target = _xent_args(x, weight, target, entry)
+    loss = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    lse = x.new_empty(x.shape[:-1], dtype=torch.float32) if want_lse else None
+    total = x.new_empty(2, dtype=torch.float32) if want_total else None
+    ptrs = XentPtrs(xr.data_ptr(), weight.data_ptr(), target.data_ptr(), loss.data_ptr(), _ptr(lse), _ptr(total), xs, ws, None, 0)
+    _xent_launch("mamba_xent_fwd", x, lib.mamba_xent_fwd, lib.mamba_xent_workspace_bytes, ptrs,
+                 XentShape(rows, weight.shape[1], weight.shape[0]), target.dtype is torch.int64, scale, dtype)
+    return loss, lse, total
+
+
+def linear_cross_entropy_fn(x, weight, target, *, scale=1.0, return_lse=False):
+    """Softmax cross entropy of hidden states against a large output matrix, without ever storing the logits::
+
+        l = scale x weight^T;  lse = logsumexp(l);  loss = lse - l[target]
+
+    x: (..., dim) and weight: (vocab, dim), bfloat16; target: x.shape[:-1], int64 or int32; one outside [0,
+    vocab) (such as -100) gives a loss of 0. Returns the fp32 losses of target's shape, and with ``return_lse``
+    the lse that :func:`linear_cross_entropy_bwd` takes."""
+    loss, lse, _ = _xent_fwd(x, weight, target, scale, return_lse, False, "linear_cross_entropy_fn")
+    return (loss, lse) if return_lse else loss
+
+
+def _factor(g, name, like):
+    """An incoming gradient of the rows: its tensor and the stride between rows, 0 for one value for all."""
+    if g is None:
+        return None, 0
+    if g.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on x's device")
+    if g.shape != like.shape[:-1]:
+        raise ValueError(f"{name} must be {tuple(like.shape[:-1])}, got {tuple(g.shape)}")
+    g = g.float()
+    if g.numel() > 1 and all(s == 0 or n == 1 for n, s in zip(g.shape, g.stride())):  # broadcast from one value
+        return g, 0
+    return g if g.is_contiguous() else g.contiguous(), 1
+
+
+def linear_cross_entropy_bwd(x, weight, target, lse, dloss, *, dlse=None, scale=1.0, want_dx=True, want_dweight=True):
+    """Gradients of :func:`linear_cross_entropy_fn` with its ``lse``, for incoming ``dloss`` and, optionally,
+    ``dlse``, of target's shape (either may be None). Returns a dict of x and weight in bfloat16, where wanted.
+    The logits are computed again piece by piece of the vocabulary; their gradients are rounded to bfloat16
+    once, as the operands of the products. A row without a target or whose incoming gradients are 0 takes no
+    part, whatever x holds there."""
+    lib = _load()
+    dtype, xr, rows, xs, weight, ws, target = _xent_args(x, weight, target, "linear_cross_entropy_bwd")
+    lse = _f32(lse, "lse", x.shape[:-1], x)
+    (a, sa), (b, sb) = _factor(dloss, "dloss", x), _factor(dlse, "dlse", x)
+    out = {}
+    if want_dx:
+        out["x"] = x.new_empty(x.shape)
+    if want_dweight:
+        out["weight"] = weight.new_empty(weight.shape)
+    ptrs = XentBwdPtrs(xr.data_ptr(), weight.data_ptr(), target.data_ptr(), lse.data_ptr(), _ptr(a), _ptr(b), _ptr(out.get("x")),
+                       _ptr(out.get("weight")), xs, ws, sa, sb, None, 0)
+    _xent_launch("mamba_xent_bwd", x, lib.mamba_xent_bwd, lib.mamba_xent_bwd_workspace_bytes, ptrs,
+                 XentShape(rows, weight.shape[1], weight.shape[0]), target.dtype is torch.int64, scale, dtype)
+    return out
+
+
+_REDUCTIONS = ("mean", "sum", "none")
+
+
+def _reduced(loss, total, reduction):
+    return loss if reduction == "none" else total[0] / total[1] if reduction == "mean" else total[0]
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """The rows' losses, reduced, and their lse."""
+
+    @staticmethod
+    def forward(ctx, x, weight, target, scale, reduction):
+        loss, lse, total = _xent_fwd(x, weight, target, scale, True, reduction != "none", "linear_cross_entropy")
+        ctx.save_for_backward(x, weight, target, lse, total)
+        ctx.scale, ctx.reduction = scale, reduction
+        ctx.set_materialize_grads(False)
+        return _reduced(loss, total, reduction), lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, dlse):
+        x, weight, target, lse, total = ctx.saved_tensors
+        if dloss is None and dlse is None:
+            return (None,) * 5
+        if dloss is not None and ctx.reduction != "none":  # one value for all rows
+            dloss = (dloss / total[1] if ctx.reduction == "mean" else dloss).expand(lse.shape)
+        g = linear_cross_entropy_bwd(x, weight, target, lse, dloss, dlse=dlse, scale=ctx.scale, want_dx=ctx.needs_input_grad[0],
+                                     want_dweight=ctx.needs_input_grad[1])
+        return g.get("x"), g.get("weight"), None, None, None
+
+
+def linear_cross_entropy(x, weight, target, *, scale=1.0, reduction="mean", return_lse=False):
+    """Differentiable :func:`linear_cross_entropy_fn`. ``reduction``: "mean" over the targets inside [0, vocab)
+    (NaN if there are none), "sum", or "none" (the rows' losses). ``return_lse``: the rows' lse too, whose
+    gradient is taken as well."""
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be one of {_REDUCTIONS}, got {reduction!r}")
+    if _grad_on("linear_cross_entropy", x, weight):
+        loss, lse = LinearCrossEntropy.apply(x, weight, target, scale, reduction)
+    else:
+        loss, lse, total = _xent_fwd(x, weight, target, scale, return_lse, reduction != "none", "linear_cross_entropy")
+        loss = _reduced(loss, total, reduction)
+    return (loss, lse) if return_lse else loss

@@ -1,0 +1,243 @@
+// One token of each stream through a Mamba block's path from the convolution to the gate (mamba_block.h), on
+// gfx950, in two launches.
+//
+//   first:   u = silu(conv_b + sum_k conv_w v_k) and the conv state's new rows; each workgroup's 64 channels'
+//            share of w_x u, for up to kRows streams (its part of w_x is read once for them)
+//   second:  (dt rows, B, C) = the shares added in channel order; delta = w_dt dt;  s = softplus(delta + dt_bias);
+//            h' = exp(s A) h + s B u;   y = (sum_n C h' + D u) silu(z)
+//
+// The x projection needs every channel before any can go on, which is the boundary between the launches. All of it
+// stays in fp32 from one to the other: u and the shares go through the workspace (at 64 streams of 1536 channels
+// 0.9 MB beside 12.6 MB of scan state). In the second launch 4 lanes hold a channel, 4 of every 16 states each, so
+// that states and A move 16 bytes a lane and the sums over states and dt rows stay within a quad; everything
+// that does not depend on the first launch's sums is loaded before they are.
+#include "block_launch.hpp"
+#include "layers_common.hpp"
+#include "rows.hpp"
+
+namespace mscan {
+
+namespace {
+
+constexpr int kCh = 64;       // channels of a workgroup, in either launch
+constexpr int kRows = 16;     // streams of a workgroup of the first launch
+constexpr int kThreads = 256;
+constexpr int kMaxJ = 512 + 2 * 256;
+
+struct StepArgs {
+    const void* x;
+    const void* z;
+    const void* conv_state;
+    const float* h;
+    const float* conv_w;
+    const float* conv_b;
+    const void* w_x;
+    const void* w_dt;
+    const float* dt_bias;
+    const float* A;
+    const float* D;
+    void* conv_out;
+    float* h_out;
+    float* y;
+    float* u;      // (batch, dim)
+    float* part;   // (chunks, batch, J)
+    int64_t sx, sz;
+    int64_t batch, dim;
+    int dstate, rank, J, chunks;
+};
+
+// Sum over a quad's lanes, the same bits in each: lane pairs, then the pairs.
+template <int CTRL>
+__device__ __forceinline__ float quad_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float quad_sum(float v) { return quad_add<0x4e>(quad_add<0xb1>(v)); }
+// Over 8 lanes: the quads' sums, then the half row mirrored.
+__device__ __forceinline__ float oct_sum(float v) { return quad_add<0x141>(quad_sum(v)); }
+
+template <typename S, int W>
+__global__ __launch_bounds__(kThreads) void step_conv_kernel(StepArgs p) {
+    __shared__ __align__(16) float us[kRows][kCh];
+    const int tid = threadIdx.x;
+    const int chunk = blockIdx.x % p.chunks;
+    const int64_t b0 = (int64_t)(blockIdx.x / p.chunks) * kRows, c0 = (int64_t)chunk * kCh;
+    const int rows = (int)(p.batch - b0 < kRows ? p.batch - b0 : kRows);
+
+    // the first rows of w_x are on their way while u is computed
+    const int part = tid & 7, j0 = tid >> 3;
+    const int n = (int)(p.dim - c0 < kCh ? p.dim - c0 : kCh) - part * 8;
+    const S* wx = static_cast<const S*>(p.w_x) + c0 + part * 8;
+    constexpr int AHEAD = 3;  // rounds of 32 rows: 96 rows, more than dt_rank 48 and 16 states need
+    Pack<S, 8> w[AHEAD];
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) {
+        const int j = j0 + 32 * r;
+        w[r] = load_some<S, 8>(wx + (int64_t)(j < p.J ? j : 0) * p.dim, j < p.J ? n : 0);
+    }
+
+    const int64_t c = c0 + (tid & (kCh - 1));
+    float cw[W], cb = 0.0f;
+    if (c < p.dim) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) cw[k] = p.conv_w[c * W + k];
+        cb = p.conv_b ? p.conv_b[c] : 0.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < kRows * kCh / kThreads; ++r) {
+        const int row = r * (kThreads / kCh) + (tid / kCh);
+        float u = 0.0f;
+        if (row < rows && c < p.dim) {
+            const int64_t b = b0 + row;
+            const S x = static_cast<const S*>(p.x)[b * p.sx + c];
+            const S* st = static_cast<const S*>(p.conv_state) + b * (W - 1) * p.dim + c;
+            S v[W];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) v[k] = st[k * p.dim];
+            v[W - 1] = x;
+            float pre = cb;
+#pragma unroll
+            for (int k = 0; k < W; ++k) pre = __builtin_fmaf(cw[k], to_f32(v[k]), pre);
+            u = silu_f(pre);
+            S* to = static_cast<S*>(p.conv_out) + b * (W - 1) * p.dim + c;
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) to[k * p.dim] = v[k + 1];
+            p.u[b * p.dim + c] = u;
+        }
+        us[row][tid & (kCh - 1)] = u;
+    }
+    __syncthreads();
+    auto share = [&](const Pack<S, 8>& wr, int j) __attribute__((always_inline)) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = to_f32(wr.v[k]);
+        for (int row = 0; row < rows; ++row) {
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s = __builtin_fmaf(f[k], us[row][part * 8 + k], s);
+            s = oct_sum(s);
+            if (part == 0 && j < p.J) p.part[((int64_t)chunk * p.batch + b0 + row) * p.J + j] = s;
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r)
+        if (32 * r < p.J) share(w[r], j0 + 32 * r);
+    for (int j = j0 + 32 * AHEAD; j - j0 < p.J; j += 32)
+        share(load_some<S, 8>(wx + (int64_t)(j < p.J ? j : 0) * p.dim, j < p.J ? n : 0), j);
+}
+
+// ONE: at most 16 states, held in registers from the start.
+template <typename S, bool ONE>
+__global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
+    __shared__ __align__(16) float sums[kThreads], xd[kMaxJ];
+    const int tid = threadIdx.x, q = tid & 3;
+    const int64_t b = blockIdx.x / p.chunks, d0 = (int64_t)(blockIdx.x % p.chunks) * kCh;
+    const bool valid = d0 + (tid >> 2) < p.dim;
+    const int64_t d = valid ? d0 + (tid >> 2) : p.dim - 1;
+    const int N = p.dstate, R = p.rank, J = p.J;
+
+    // what does not wait for the projection
+    const float* h = p.h + (b * p.dim + d) * N;
+    const float* A = p.A + d * N;
+    Pack<float, 4> h0{}, a0{};
+    if constexpr (ONE) {
+        h0 = load_some<float, 4>(h + q * 4, N - q * 4);
+        a0 = load_some<float, 4>(A + q * 4, N - q * 4);
+    }
+    const S* wd = static_cast<const S*>(p.w_dt) + d * R;
+    constexpr int AHEAD = 4;  // 64 dt rows
+    Pack<S, 4> w[AHEAD];
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) w[r] = load_some<S, 4>(wd + r * 16 + q * 4, R - r * 16 - q * 4);
+    const float u = p.u[b * p.dim + d];
+    const float z = p.z ? to_f32(static_cast<const S*>(p.z)[b * p.sz + d]) : 0.0f;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.0f, skip = p.D ? p.D[d] : 0.0f;
+
+    // the chunks' shares of row j: `ways` stretches of the chunks side by side, added in order
+    const float* part = p.part + b * J;
+    const int64_t next = p.batch * J;
+    if (J <= kThreads) {
+        const int ways = kThreads / J, way = tid / J, j = tid - way * J;
+        const int per = (p.chunks + ways - 1) / ways, k1 = (way + 1) * per < p.chunks ? (way + 1) * per : p.chunks;
+        float s = 0.0f;
+        if (way < ways) {
+#pragma unroll 8
+            for (int k = way * per; k < k1; ++k) s += part[k * next + j];
+        }
+        sums[tid] = s;
+        __syncthreads();
+        if (tid < J) {
+            for (int k = 1; k < ways; ++k) s += sums[k * J + tid];
+            xd[tid] = s;
+        }
+    } else {
+        for (int j = tid; j < J; j += kThreads) {
+            float s = 0.0f;
+#pragma unroll 8
+            for (int k = 0; k < p.chunks; ++k) s += part[k * next + j];
+            xd[j] = s;
+        }
+    }
+    __syncthreads();
+
+    float delta = 0.0f;
+    auto dot = [&](const Pack<S, 4>& wr, int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (r + k < R) delta = __builtin_fmaf(to_f32(wr.v[k]), xd[r + k], delta);
+    };
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) dot(w[r], r * 16 + q * 4);
+    for (int r = AHEAD * 16 + q * 4; r < R; r += 16) dot(load_some<S, 4>(wd + r, R - r), r);
+    const float s = softplus_f(quad_sum(delta) + bias), su = s * u;
+
+    float* ho = p.h_out + (b * p.dim + d) * N;
+    float o = 0.0f;
+    auto states = [&](const Pack<float, 4>& hv, const Pack<float, 4>& av, int n0) __attribute__((always_inline)) {
+        Pack<float, 4> r{};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (n0 + k < N) {
+                r.v[k] = __builtin_fmaf(hw_exp2(s * av.v[k] * kLog2e), hv.v[k], su * xd[R + n0 + k]);
+                o = __builtin_fmaf(xd[R + N + n0 + k], r.v[k], o);
+            }
+        if (valid) store_some<float, 4>(ho + n0, r, N - n0);
+    };
+    if constexpr (ONE) {
+        states(h0, a0, q * 4);
+    } else {
+#pragma unroll 4
+        for (int n0 = q * 4; n0 < N; n0 += 16) states(load_some<float, 4>(h + n0, N - n0), load_some<float, 4>(A + n0, N - n0), n0);
+    }
+    o = __builtin_fmaf(skip, u, quad_sum(o));
+    if (p.z) o *= silu_f(z);
+    if (valid && q == 0) p.y[b * p.dim + d] = o;
+}
+
+int chunks_of(const mamba_step_shape& s) { return (int)((s.dim + kCh - 1) / kCh); }
+
+}  // namespace
+
+int64_t block_step_workspace(const mamba_step_shape& s) {
+    return align256(s.batch * s.dim * 4) + align256((int64_t)chunks_of(s) * s.batch * (s.dt_rank + 2 * s.dstate) * 4);
+}
+
+int launch_block_step(const mamba_step_ptrs& p, const mamba_step_shape& s, bool bf16, hipStream_t stream) {
+    char* ws = static_cast<char*>(p.workspace);
+    StepArgs q{p.x, p.z, p.conv_state, p.ssm_state, p.conv_w, p.conv_b, p.w_x, p.w_dt, p.dt_bias, p.A, p.D, p.conv_state_out,
+               p.ssm_state_out, p.y, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + align256(s.batch * s.dim * 4)),
+               p.x_stride, p.z_stride, s.batch, s.dim, (int)s.dstate, (int)s.dt_rank, (int)(s.dt_rank + 2 * s.dstate), chunks_of(s)};
+    Launches on(stream);
+    const dim3 first((unsigned)(q.chunks * ((s.batch + kRows - 1) / kRows))), second((unsigned)(q.chunks * s.batch)), block(kThreads);
+    auto go = [&](auto zero) {
+        using S = decltype(zero);
+        if (s.width == 2) on(step_conv_kernel<S, 2>, first, block, q);
+        else if (s.width == 3) on(step_conv_kernel<S, 3>, first, block, q);
+        else on(step_conv_kernel<S, 4>, first, block, q);
+        if (s.dstate <= 16) on(step_scan_kernel<S, true>, second, block, q);
+        else on(step_scan_kernel<S, false>, second, block, q);
+    };
+    bf16 ? go(bf16_t{}) : go(0.0f);
+    return on.status;
+}
+
+}  // namespace mscan

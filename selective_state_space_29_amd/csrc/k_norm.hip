@@ -12,12 +12,9 @@
 //
 // Measured: forward 16384 x 768 bf16 with residual 22 us (100 MB, 4.5 TB/s; a large copy 4.6); 16384 x 2048
 // 50 forward (5.4 TB/s, partly cached), 44 + 4 backward and its column sums; 4000 x 8192 fp32 103 and 112.
-#include <initializer_list>
-#include <type_traits>
-#include <utility>
-
 #include "layers_common.hpp"
 #include "layers_launch.hpp"
+#include "rows.hpp"
 
 namespace mscan {
 
@@ -45,28 +42,6 @@ struct NormBwdArgs {
     float* part;  // (blocks, 2, dim)
     int64_t rows, dim, st, sdy, sdres, sdx;
 };
-
-// Sums of N values over the WPR waves of a row, the same bits in every thread. `slot` alternates
-// between calls, so one barrier a call is enough.
-template <int N, int WPR, int WAVES>
-__device__ __forceinline__ void row_sum(float (&v)[2], float (*lds)[2][WAVES], int slot, int wave) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
-    if constexpr (WPR > 1) {
-        if ((threadIdx.x & 63) == 0)
-#pragma unroll
-            for (int k = 0; k < N; ++k) lds[slot][k][wave] = v[k];
-        __syncthreads();
-        const int first = wave / WPR * WPR;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            float s = 0.0f;
-#pragma unroll
-            for (int q = 0; q < WPR; ++q) s += lds[slot][k][first + q];
-            v[k] = s;
-        }
-    }
-}
 
 // A variance, up from its rounding below 0; a row with a NaN keeps it (a maximum would drop it).
 __device__ __forceinline__ float no_less_than_0(float v) { return v < 0.0f ? 0.0f : v; }
@@ -409,17 +384,6 @@ void fwd_go(const NormArgs& q, Launches& on) {
     on(norm_fwd_kernel<S, V, NV, WPR>, dim3((unsigned)(need < most ? need : most)), dim3(64 * WAVES), q);
 }
 
-// The smallest instantiated number of packs that holds `nv` (1, 2, 3, 4, 6, 8, 12, 16, 24, 32; at most M).
-template <int M, int N = 1, typename F>
-auto with_packs(int64_t nv, F&& f) {
-    constexpr int next = N < 4 ? N + 1 : N % 3 == 0 ? N / 3 * 4 : N / 2 * 3;
-    if constexpr (next > M || N >= M) {
-        return f(std::integral_constant<int, N < M ? M : N>{});
-    } else {
-        return nv <= N ? f(std::integral_constant<int, N>{}) : with_packs<M, next>(nv, f);
-    }
-}
-
 template <typename S, int V, int WPR>
 void fwd_width(const NormArgs& q, Launches& on) {
     with_packs<(fwd_vals(WPR) / V > 1 ? fwd_vals(WPR) / V : 1)>(
@@ -458,21 +422,6 @@ int64_t bwd_vec(const NormBwdArgs& q, Launches& on) {
     const int64_t n = q.rows < 64 ? q.rows : 64;
     on(norm_cols_wide_kernel<S>, dim3((unsigned)((q.dim + 255) / 256), (unsigned)n), dim3(256), q);
     return n;
-}
-
-// The widest pack (16 bytes and down) that the width, pointers and row strides are multiples of, and that
-// leaves less than half of a wave idle over the width (200000 x 100 bf16: 141 us with packs of 4, on 25
-// lanes, 113 with single elements).
-template <typename S, int V = 16 / sizeof(S), typename F>
-auto with_pack(int64_t dim, std::initializer_list<std::pair<const void*, int64_t>> rows, F&& f) {
-    if constexpr (V == 1) {
-        return f(std::integral_constant<int, 1>{});
-    } else {
-        bool ok = dim % V == 0 && dim > 32 * V;
-        for (const auto& r : rows)
-            ok = ok && (!r.first || (reinterpret_cast<uintptr_t>(r.first) % (V * sizeof(S)) == 0 && r.second % V == 0));
-        return ok ? f(std::integral_constant<int, V>{}) : with_pack<S, V / 2>(dim, rows, f);
-    }
 }
 
 template <typename S>

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <stdint.h>
 
+#include "checks.hpp"
 #include "gated.hpp"
 #include "layers_common.hpp"
 #include "launch.hpp"
@@ -31,33 +32,6 @@ int layers_cus() {
 
 namespace {
 
-struct Bytes {
-    uintptr_t lo = 0, hi = 0;
-};
-
-// Bytes of n0 rows, `s0` elements apart, of n1 rows, `s1` apart, of n2 elements of `es` bytes.
-Bytes bytes_of(const void* p, int64_t es, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2) {
-    Bytes b;
-    if (!p || n0 <= 0 || n1 <= 0 || n2 <= 0) return b;
-    b.lo = reinterpret_cast<uintptr_t>(p);
-    b.hi = b.lo + (uintptr_t)(((n0 - 1) * s0 + (n1 - 1) * s1 + n2) * es);
-    return b;
-}
-Bytes flat(const void* p, int64_t bytes) { return bytes_of(p, 1, 1, 0, 1, 0, bytes); }
-
-bool meet(const Bytes& a, const Bytes& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-template <int NI, int NO>
-bool any_overlap(const Bytes (&ins)[NI], const Bytes (&outs)[NO]) {
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (meet(outs[o], ins[i])) return true;
-        for (int o2 = 0; o2 < o; ++o2)
-            if (meet(outs[o], outs[o2])) return true;
-    }
-    return false;
-}
-
 // Slices of one tensor whose rows lie side by side (dx, dr and di of a merged projection): the same
 // strides, and starts at least a row's width apart within the row stride and the batch stride.
 bool interleaved(const Bytes& a, const Bytes& b, const int64_t* sa, const int64_t* sb, const mamba_gated_shape& s, int64_t es) {
@@ -65,22 +39,6 @@ bool interleaved(const Bytes& a, const Bytes& b, const int64_t* sa, const int64_
     return (s.batch <= 1 || sa[0] == sb[0]) && (s.len <= 1 || sa[1] == sb[1]) && off >= s.dim &&
            (s.len <= 1 || off + s.dim <= sa[1]) && (s.batch <= 1 || (s.len - 1) * sa[1] + off + s.dim <= sa[0]);
 }
-
-// Whether n rows `s` elements apart could not be addressed in 64 bits (or a size is negative).
-bool bad_span(int64_t n, int64_t s) { return n < 0 || s < 0 || (n > 1 && s > ((int64_t)1 << 58) / n); }
-
-bool bad_dtype(mamba_scan_dtype t) { return t != MAMBA_SCAN_F32 && t != MAMBA_SCAN_BF16; }
-bool misaligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)a != 0; }
-
-// A workspace of at least `need` bytes, 256-byte aligned.
-int check_workspace(const void* ws, int64_t have, int64_t need) {
-    if (have < 0 || (have > 0 && !ws)) return MAMBA_SCAN_ERR_ARGS;
-    if (need > have) return MAMBA_SCAN_ERR_WORKSPACE;
-    if (need > 0 && misaligned(ws, 256)) return MAMBA_SCAN_ERR_ARGS;
-    return MAMBA_SCAN_OK;
-}
-
-constexpr int64_t kMaxGrid = 0x7fffffff;
 
 // ---- gated linear recurrence ----
 

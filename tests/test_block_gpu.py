@@ -1,0 +1,692 @@
+"""The block operators on the GPU against 64-bit references (tests/block_ref.py).
+
+Bars, as |g - r| <= tol (1 + |r|): fp32 1e-4, the scan's and the layer operators' bar. The operators' own errors
+stay below it: a convolution adds at most 5 products and a few roundings; norms and losses sum n terms, an error of
+at most n 2^-24 of the terms' magnitude (n up to 2^11 here, typically its root), and the step's projections and
+states likewise. A bf16 output adds its own rounding, at most 2^-8 of it. Where an operand is rounded to bf16
+inside (the gradients of the logits), the test adds 2^-8 of the sum of the terms' magnitudes.
+"""
+
+import pytest
+import torch
+
+import block_ref as ref
+from selective_state_space_29_amd import block
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TOL = 1e-4
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def close(got, want, tol=TOL, room=0.0):
+    got, want = got.detach().cpu(), want.detach().cpu()
+    assert got.shape == want.shape, (got.shape, want.shape)
+    if got.numel() == 0:
+        return
+    room = tol * (1 + want.abs()) + room + (2.0 ** -8 * want.abs() if got.dtype == BF16 else 0.0)
+    err = (got.double() - want).abs()
+    assert bool((err <= room).all()), f"max error {float((err - room).max()):.3e} over the bar, at {int((err - room).argmax())}"
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def dev(t):
+    return {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in t.items()}
+
+
+# ---- causal convolution ----
+
+def conv_case(seed, B, L, D, W, dtype, state=True, reset=False, bias=True):
+    g = gen(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    t = dict(x=r(B, L, D).to(dtype), weight=r(D, W) * W ** -0.5, bias=r(D) if bias else None,
+             state=r(B, W - 1, D).to(dtype) if state else None, reset=torch.rand(B, L, generator=g) < 0.2 if reset else None,
+             dy=r(B, L, D).to(dtype), dlast=r(B, W - 1, D).to(dtype))
+    return t
+
+
+def lay(x, how):
+    """x (batch, len, dim) on the GPU: rows of channels, a slice of a wider tensor, or rows of steps."""
+    x = x.to(DEV)
+    if how == "steps":
+        return x.transpose(1, 2).contiguous().transpose(1, 2)
+    if how == "slice":
+        B, L, D = x.shape
+        wide = torch.full((B, L, 2 * D + 3), float("nan"), dtype=x.dtype, device=DEV)
+        wide[..., D + 1:2 * D + 1] = x
+        return wide[..., D + 1:2 * D + 1]
+    return x
+
+
+LAYOUTS = [("rows", "rows"), ("rows", "steps"), ("slice", "rows"), ("slice", "steps"), ("steps", "steps")]
+
+
+def check_conv(t, x_as="rows", y_as="rows", activation="silu", tol=TOL):
+    d = dev(t)
+    x = lay(t["x"], x_as)
+    kw = dict(activation=activation, initial_state=d["state"], reset=d["reset"])
+    y, last = block.causal_conv_fn(x, d["weight"], d["bias"], return_last_state=True, scan_layout=y_as == "steps", **kw)
+    assert y.stride(1 if y_as == "steps" else 2) == 1 or 1 in y.shape or 0 in y.shape
+    yr, lr, want = ref.causal_conv(t["x"], t["weight"], t["bias"], t["state"], t["reset"], activation, t["dy"], t["dlast"])
+    close(y, yr, tol)
+    assert torch.equal(last.cpu().double(), lr)
+    g = block.causal_conv_bwd(x, d["weight"], d["bias"], lay(t["dy"], y_as), dlast_state=d["dlast"], want_dinitial=True, **kw)
+    close(g["x"], want["x"], tol)
+    close(g["initial_state"], want["initial_state"], tol)
+    n = t["x"].shape[0] * t["x"].shape[1]
+    for k in ("weight", "bias"):  # sums of n terms of either sign
+        if k in g:
+            close(g[k], want[k], tol, room=tol * n * 1e-2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+@pytest.mark.parametrize("B,L,D", [(1, 1, 1), (2, 1, 64), (3, 2, 5), (2, 3, 70), (2, 7, 9), (1, 8, 128), (2, 9, 63), (1, 17, 65), (2, 63, 31),
+                                   (3, 130, 8)])
+def test_conv_sizes(B, L, D, x_as, y_as, dtype):
+    W = 1 + (B + L + D) % 4
+    check_conv(conv_case(B * 100 + L + D, B, L, D, W, dtype, state=L % 2 == 1, reset=D % 2 == 1), x_as, y_as)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_conv_many_runs(W, x_as, y_as, dtype):
+    """Workgroups that walk over several stretches of runs, sequences of different workgroups."""
+    check_conv(conv_case(W, 40, 61, 200, W, dtype, reset=True), x_as, y_as)
+
+
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+@pytest.mark.parametrize("where", ["first", "last", "all", "none", "last_but_one"])
+def test_conv_resets(where, x_as, y_as):
+    t = conv_case(5, 2, 21, 10, 4, F32, reset=True)
+    t["reset"].zero_()
+    if where == "first":
+        t["reset"][:, 0] = True
+    elif where == "last":
+        t["reset"][:, -1] = True
+    elif where == "last_but_one":
+        t["reset"][:, -2] = True
+    elif where == "all":
+        t["reset"].fill_(True)
+    check_conv(t, x_as, y_as)
+
+
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+def test_conv_without_activation_bias_or_state(x_as, y_as):
+    check_conv(conv_case(6, 2, 40, 33, 4, F32, state=False, bias=False), x_as, y_as, activation=None)
+    check_conv(conv_case(7, 1, 2, 33, 4, BF16, state=False, bias=False, reset=True), x_as, y_as)
+
+
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+def test_conv_bad_values_before_a_reset_are_forgotten(x_as, y_as):
+    """NaN and infinities in a sequence, its state and its incoming gradients do not reach the one packed behind it."""
+    t = conv_case(8, 1, 40, 12, 4, F32, reset=True)
+    t["reset"].zero_()
+    t["reset"][0, 19] = True
+    d = dev(t)
+    kw = dict(reset=d["reset"])
+
+    def run(x, state, dy):
+        y, last = block.causal_conv_fn(lay(x, x_as), d["weight"], d["bias"], return_last_state=True, initial_state=state.to(DEV),
+                                       scan_layout=y_as == "steps", **kw)
+        g = block.causal_conv_bwd(lay(x, x_as), d["weight"], d["bias"], lay(dy, y_as), initial_state=state.to(DEV), dlast_state=d["dlast"], **kw)
+        return y, last, g["x"]
+
+    good = run(t["x"], t["state"], t["dy"])
+    x, state, dy = t["x"].clone(), t["state"].clone(), t["dy"].clone()
+    x[:, :19], state[:], dy[:, :19] = float("nan"), float("inf"), float("inf")
+    bad = run(x, state, dy)
+    assert torch.equal(bad[0][:, 19:], good[0][:, 19:]) and torch.equal(bad[1], good[1]) and torch.equal(bad[2][:, 19:], good[2][:, 19:])
+    # and the other way: the one behind does not reach the one before
+    x, dy = t["x"].clone(), t["dy"].clone()
+    x[:, 19:], dy[:, 19:] = float("nan"), float("inf")
+    bad = run(x, t["state"], dy)
+    assert torch.equal(bad[0][:, :19], good[0][:, :19]) and torch.equal(bad[2][:, :19], good[2][:, :19])
+
+
+def test_conv_nan_stays_in_its_channel():
+    t = conv_case(9, 2, 30, 70, 4, F32)
+    d = dev(t)
+    y = block.causal_conv_fn(d["x"], d["weight"], d["bias"])
+    x = d["x"].clone()
+    x[1, 7, 33] = float("nan")
+    y2 = block.causal_conv_fn(x, d["weight"], d["bias"])
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[1, 7:11, 33] = True
+    assert torch.equal(y2.isnan(), bad) and torch.equal(y2[~bad], y[~bad])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+def test_conv_pieces_with_the_state_in_place(x_as, y_as, dtype):
+    """A sequence in pieces of any length, the state updated in place, gives the bits of the whole."""
+    t = conv_case(10, 3, 150, 70, 4, dtype, state=True, reset=True)
+    d = dev(t)
+    kw = dict(scan_layout=y_as == "steps", return_last_state=True)
+    y, last = block.causal_conv_fn(lay(t["x"], x_as), d["weight"], d["bias"], initial_state=d["state"], reset=d["reset"], **kw)
+    state = d["state"].clone()
+    at, parts = 0, []
+    for n in (1, 1, 2, 3, 1, 8, 9, 100, 5, 20):
+        part, got = block.causal_conv_fn(lay(t["x"], x_as)[:, at:at + n], d["weight"], d["bias"], initial_state=state,
+                                         reset=d["reset"][:, at:at + n], last_state_out=state, **kw)
+        assert got is state
+        parts.append(part)
+        at += n
+    assert at == 150
+    assert torch.equal(torch.cat(parts, 1), y) and torch.equal(state, last)
+
+
+@pytest.mark.parametrize("x_as,y_as", LAYOUTS)
+def test_conv_empty(x_as, y_as):
+    t = conv_case(11, 2, 0, 6, 4, F32, reset=True)
+    check_conv(t, x_as, y_as)  # no step: the state is handed on, dinitial is dlast
+    for shape in ((0, 5, 6), (2, 5, 0)):
+        t = conv_case(12, *shape, 3, BF16)
+        d = dev(t)
+        y, last = block.causal_conv_fn(lay(t["x"], x_as), d["weight"], d["bias"], initial_state=d["state"], return_last_state=True,
+                                       scan_layout=y_as == "steps")
+        assert y.shape == shape and last.shape == (shape[0], 2, shape[2])
+        g = block.causal_conv_bwd(lay(t["x"], x_as), d["weight"], d["bias"], lay(t["dy"], y_as))
+        assert g["weight"].shape == (shape[2], 3) and not g["weight"].any() and not g["bias"].any()
+
+
+def test_conv_leaves_what_is_around_its_outputs():
+    t = dev(conv_case(13, 2, 13, 9, 4, BF16))
+    for steps in (False, True):
+        big = torch.full((4, 20, 20), 7.0, dtype=BF16, device=DEV)
+        view = big[1:3, 3:12, 4:17].transpose(1, 2) if steps else big[1:3, 4:17, 3:12]
+        y = block.causal_conv_fn(t["x"], t["weight"], t["bias"], scan_layout=steps, out=view)
+        assert y is view and torch.equal(y, block.causal_conv_fn(t["x"], t["weight"], t["bias"]))
+        keep = torch.ones_like(big, dtype=torch.bool)
+        keep[1:3, 3:12, 4:17] = False if steps else True
+        if not steps:
+            keep[1:3, 4:17, 3:12] = False
+        assert bool((big[keep] == 7.0).all())
+
+
+def test_conv_offsets_past_32_bits():
+    """Rows and channels beyond 4 GiB of x and y, in both layouts."""
+    B, L, D = 3, 70000, 12000  # 5 GB of bf16
+    g = torch.Generator(device=DEV).manual_seed(14)
+    base = torch.randn(97, D, generator=g, device=DEV, dtype=BF16)
+    x = base.repeat(-(-L // 97), 1)[:L].expand(B, L, D).contiguous()
+    x[1:] *= 2
+    w, b = torch.randn(D, 4, generator=g, device=DEV), torch.randn(D, generator=g, device=DEV)
+    for xv in (x, x.transpose(1, 2).contiguous().transpose(1, 2)):
+        y = block.causal_conv_fn(xv, w, b)
+        want = block.causal_conv_fn(x[-1:, L - 500:].contiguous(), w, b)
+        assert torch.equal(y[-1:, L - 400:], want[:, 100:])
+        want = block.causal_conv_fn(x[:1, :300].contiguous(), w, b)
+        assert torch.equal(y[:1, :300], want)
+        del y
+        dx = block.causal_conv_bwd(xv, w, b, xv)["x"]
+        part = x[-1:, L - 500:].contiguous()
+        want = block.causal_conv_bwd(part, w, b, part)["x"]
+        assert torch.equal(dx[-1:, L - 400:], want[:, 100:])
+        del dx, xv
+
+
+def test_conv_autograd():
+    t = conv_case(15, 2, 50, 24, 4, F32, reset=True)
+    d = dev(t)
+    leaves = {k: d[k].clone().requires_grad_() for k in ("x", "weight", "bias", "state")}
+    w3 = leaves["weight"][:, None]  # a Conv1d's weight
+    y, last = block.causal_conv(leaves["x"], w3, leaves["bias"], initial_state=leaves["state"], reset=d["reset"], return_last_state=True)
+    ((y * d["dy"]).sum() + (last * d["dlast"]).sum()).backward()
+    want = ref.causal_conv(t["x"], t["weight"], t["bias"], t["state"], t["reset"], "silu", t["dy"], t["dlast"])[2]
+    for k, name in (("x", "x"), ("weight", "weight"), ("bias", "bias"), ("state", "initial_state")):
+        close(leaves[k].grad, want[name], TOL, room=1e-4)
+    # only the state's gradient, then only y's from a broadcast gradient
+    leaves["x"].grad = None
+    block.causal_conv(leaves["x"], d["weight"], d["bias"], return_last_state=True)[1].sum().backward()
+    assert torch.equal(leaves["x"].grad[:, -3:], torch.ones(2, 3, 24, device=DEV)) and not leaves["x"].grad[:, :-3].any()
+    leaves["x"].grad = None
+    block.causal_conv(leaves["x"], d["weight"], d["bias"], scan_layout=True).sum().backward()
+    close(leaves["x"].grad, ref.causal_conv(t["x"], t["weight"], t["bias"], dy=torch.ones(2, 50, 24))[2]["x"])
+
+
+# ---- block step ----
+
+def step_case(seed, B, D, N, R, W, dtype, gate=True, optional=True):
+    g = gen(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    return dict(x=r(B, D).to(dtype), conv_state=r(B, W - 1, D).to(dtype), ssm_state=r(B, D, N), conv_w=r(D, W) * W ** -0.5,
+                conv_b=r(D) * 0.5 if optional else None, w_x=(r(R + 2 * N, D) * D ** -0.5).to(dtype),
+                w_dt=(r(D, R) * R ** -0.5).to(dtype), dt_bias=-4 + 3 * torch.rand(D, generator=g) if optional else None,
+                A=-torch.rand(D, N, generator=g) * N, D=r(D) if optional else None, z=r(B, D).to(dtype) if gate else None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,D,N,R,W", [(1, 1, 1, 1, 2), (2, 5, 3, 2, 3), (1, 64, 16, 4, 4), (3, 65, 16, 7, 4), (17, 130, 8, 48, 2), (2, 200, 17, 70, 3),
+                                       (33, 63, 64, 3, 4), (1, 1536, 16, 48, 4), (5, 100, 256, 512, 4), (2, 333, 128, 21, 2)])
+def test_step(B, D, N, R, W, dtype):
+    t = step_case(B + D, B, D, N, R, W, dtype, gate=D % 2 == 0, optional=B != 2)
+    y, conv, h = ref.block_step(**t)
+    d = dev(t)
+    conv0, h0 = d["conv_state"].clone(), d["ssm_state"].clone()
+    conv1, h1 = torch.full_like(conv0, float("nan")), torch.full_like(h0, float("nan"))
+    got = block.block_step(**d, conv_state_out=conv1, ssm_state_out=h1)
+    close(got, y)
+    close(h1, h)
+    assert torch.equal(conv1.cpu().double(), conv)
+    assert torch.equal(d["conv_state"], conv0) and torch.equal(d["ssm_state"], h0)  # given outputs: the old states stay
+    got2 = block.block_step(**d)
+    assert torch.equal(got2, got) and torch.equal(d["conv_state"], conv1) and torch.equal(d["ssm_state"], h1)  # in place, the same bits
+
+
+def test_step_rows_do_not_see_each_other():
+    t = step_case(20, 40, 100, 16, 6, 4, BF16)
+    d = dev(t)
+    o1 = {k: torch.empty_like(d[k]) for k in ("conv_state", "ssm_state")}
+    y = block.block_step(**d, conv_state_out=o1["conv_state"], ssm_state_out=o1["ssm_state"])
+    d["x"][7], d["ssm_state"][21] = float("nan"), float("inf")
+    y2 = block.block_step(**d)
+    rest = [k for k in range(40) if k not in (7, 21)]
+    assert torch.equal(y2[rest], y[rest]) and torch.equal(d["ssm_state"][rest], o1["ssm_state"][rest])
+    assert bool(y2[7].isnan().all()) and not bool(y2[21].isfinite().any())
+    assert block.block_step(**{k: v[:0] if k in ("x", "conv_state", "ssm_state", "z") else v for k, v in d.items()}).shape == (0, 100)
+
+
+def test_step_reads_slices_and_repeats_on_another_stream():
+    t = step_case(21, 6, 96, 16, 5, 4, BF16)
+    d = dev(t)
+    p = torch.full((6, 2 * 96 + 7), float("nan"), dtype=BF16, device=DEV)
+    p[:, 1:97], p[:, 99:195] = d["x"], d["z"]
+    kw = dict(d, x=p[:, 1:97], z=p[:, 99:195])
+    first = [torch.empty_like(d["conv_state"]), torch.empty_like(d["ssm_state"])]
+    y = block.block_step(**d, conv_state_out=first[0], ssm_state_out=first[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            again = [torch.empty_like(f) for f in first]
+            y2 = block.block_step(**kw, conv_state_out=again[0], ssm_state_out=again[1])
+            assert torch.equal(y2, y) and all(torch.equal(a, b) for a, b in zip(again, first))
+    torch.cuda.current_stream().wait_stream(side)
+
+
+# ---- root-mean-square norms ----
+
+NORM_SIZES = [(1, 1), (3, 2), (5, 63), (4, 64), (2, 130), (7, 256), (6, 257), (9, 768), (3, 1001), (2, 1024), (5, 1536), (3, 2049), (2, 4096),
+              (2, 8192), (2, 8193), (1, 16384), (2, 16391), (300, 40), (5000, 96)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim", NORM_SIZES)
+def test_rms_norm(rows, dim, dtype):
+    g = gen(rows + dim)
+    x, res, dy, ds = (torch.randn(rows, dim, generator=g).to(dtype) for _ in range(4))
+    w = torch.randn(dim, generator=g)
+    room = TOL * rows * 1e-2
+    # with the scaled residual
+    (y, t), stats = block.rms_norm_fn(x.to(DEV), w.to(DEV), residual=res.to(DEV), scale=0.3, return_stats=True)
+    exact = res.double() + 0.3 * x.double()
+    close(t, exact)
+    t0 = t.cpu()
+    close(y, ref.rms_norm(t0, w))
+    want = ref.rms_norm(t0, w, dy=dy, dsum=ds)
+    b = block.rms_norm_bwd(t, w.to(DEV), dy.to(DEV), stats, dresidual=ds.to(DEV), scale=0.3)
+    close(b["residual"], want["t"])
+    close(b["x"], 0.3 * want["t"])
+    close(b["weight"], want["weight"], room=room)
+    # alone
+    y, stats = block.rms_norm_fn(x.to(DEV), w.to(DEV), return_stats=True)
+    close(y, ref.rms_norm(x, w))
+    want = ref.rms_norm(x, w, dy=dy)
+    b = block.rms_norm_bwd(x.to(DEV), w.to(DEV), dy.to(DEV), stats)
+    assert b["x"] is b["residual"]
+    close(b["x"], want["t"])
+    close(b["weight"], want["weight"], room=room)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate_first", [True, False])
+@pytest.mark.parametrize("rows,dim,groups", [(1, 1, 1), (3, 6, 3), (5, 64, 2), (4, 130, 1), (6, 515, 5), (3, 1001, 7), (2, 1536, 1), (3, 2048, 8),
+                                             (2, 4096, 1), (1, 8200, 1), (2, 40000, 2), (1000, 48, 4), (2, 96, 96)])
+def test_gated_rms_norm(rows, dim, groups, gate_first, dtype):
+    g = gen(rows + dim + groups)
+    x, z, dy = (torch.randn(rows, dim, generator=g).to(dtype) for _ in range(3))
+    w = torch.randn(dim, generator=g)
+    kw = dict(groups=groups, gate_first=gate_first)
+    eps = 1e-2  # groups of one value: its inverse deviation stays moderate
+    y, stats = block.gated_rms_norm_fn(x.to(DEV), z.to(DEV), w.to(DEV), eps, return_stats=True, **kw)
+    assert stats.shape == (rows, groups)
+    close(y, ref.gated_rms_norm(x, z, w, eps, **kw))
+    want = ref.gated_rms_norm(x, z, w, eps, dy=dy, **kw)
+    b = block.gated_rms_norm_bwd(x.to(DEV), z.to(DEV), w.to(DEV), dy.to(DEV), stats, **kw)
+    close(b["x"], want["x"])
+    close(b["z"], want["z"])
+    close(b["weight"], want["weight"], room=TOL * rows * 1e-2)
+
+
+def test_norms_of_slices_and_without_weight():
+    g = gen(30)
+    p = torch.randn(3, 5, 2 * 72 + 5, generator=g).to(BF16).to(DEV)
+    x, z = p[..., 1:73], p[..., 74:146]
+    xc, zc = x.contiguous(), z.contiguous()
+    assert torch.equal(block.rms_norm_fn(x), block.rms_norm_fn(xc))
+    assert torch.equal(block.gated_rms_norm_fn(x, z, groups=3), block.gated_rms_norm_fn(xc, zc, groups=3))
+    y, t = block.rms_norm_fn(x, residual=z, scale=2.0)
+    yc, tc = block.rms_norm_fn(xc, residual=zc, scale=2.0)
+    assert torch.equal(y, yc) and torch.equal(t, tc)
+    close(block.rms_norm_fn(x), ref.rms_norm(xc.cpu()))
+    for gate_first in (True, False):
+        _, stats = block.gated_rms_norm_fn(x, z, groups=3, gate_first=gate_first, return_stats=True)
+        a = block.gated_rms_norm_bwd(x, z, None, z, stats, groups=3, gate_first=gate_first)
+        b = block.gated_rms_norm_bwd(xc, zc, None, zc, stats, groups=3, gate_first=gate_first)
+        assert all(torch.equal(a[k], b[k]) for k in a)
+    assert list(block.gated_rms_norm_bwd(x, z, None, z, stats, groups=3, gate_first=False, want_dweight=False)) == ["x", "z"]
+
+
+def test_norms_keep_bad_values_in_their_row_and_group():
+    g = gen(31)
+    x, z = torch.randn(6, 40, generator=g).to(DEV), torch.randn(6, 40, generator=g).to(DEV)
+    y, yg = block.rms_norm_fn(x), block.gated_rms_norm_fn(x, z, groups=2)
+    x[2, 5], x[4, 30] = float("nan"), float("inf")
+    y2, yg2 = block.rms_norm_fn(x), block.gated_rms_norm_fn(x, z, groups=2)
+    rows = [0, 1, 3, 5]
+    assert torch.equal(y2[rows], y[rows]) and torch.equal(yg2[rows], yg[rows])
+    assert bool(y2[2].isnan().all()) and bool(yg2[2, :20].isnan().all()) and torch.equal(yg2[2, 20:], yg[2, 20:])
+    assert torch.equal(yg2[4, :20], yg[4, :20]) and bool(y2[4, 30].isnan()) and not y2[4, :30].any()
+    assert not block.rms_norm_fn(torch.zeros(3, 8, device=DEV)).any()  # eps keeps a row of zeros
+
+
+def test_norms_autograd_and_empty():
+    g = gen(32)
+    x, r, z, dy, dt = (torch.randn(4, 30, generator=g) for _ in range(5))
+    w = torch.randn(30, generator=g)
+    a = {k: v.to(DEV).requires_grad_() for k, v in dict(x=x, r=r, z=z, w=w).items()}
+    y, t = block.rms_norm(a["x"], a["w"], residual=a["r"], scale=0.5)
+    ((y * dy.to(DEV)).sum() + (t * dt.to(DEV)).sum()).backward()
+    want = ref.rms_norm((r + 0.5 * x), w, dy=dy, dsum=dt)
+    close(a["r"].grad, want["t"])
+    close(a["x"].grad, 0.5 * want["t"])
+    close(a["w"].grad, want["weight"])
+    a["x"].grad = a["w"].grad = None
+    block.gated_rms_norm(a["x"], a["z"], a["w"], groups=2, gate_first=False).backward(dy.to(DEV))
+    want = ref.gated_rms_norm(x, z, w, groups=2, gate_first=False, dy=dy)
+    for k, v in a.items():
+        if k != "r":
+            close(v.grad, want["weight" if k == "w" else k])
+    a["x"].grad = None
+    block.rms_norm(a["x"], scale=3.0).backward(dy.to(DEV))  # no residual: its scale has no part
+    close(a["x"].grad, ref.rms_norm(x, dy=dy)["t"])
+    for shape in ((0, 8), (3, 0), (0, 0)):
+        e = torch.zeros(shape, device=DEV)
+        y, stats = block.rms_norm_fn(e, return_stats=True)
+        assert y.shape == shape and stats.shape == shape[:1]
+        b = block.rms_norm_bwd(e, None, e, stats)
+        assert b["weight"].shape == shape[1:] and not b["weight"].any()
+        y, stats = block.gated_rms_norm_fn(e, e, return_stats=True)
+        assert not block.gated_rms_norm_bwd(e, e, None, e, stats)["weight"].any()
+
+
+# ---- cross entropy ----
+
+def xent_case(seed, M, K, V, ids=torch.int64, pad=0.2):
+    g = gen(seed)
+    t = dict(x=torch.randn(M, K, generator=g).to(BF16), weight=(torch.randn(V, K, generator=g) * max(K, 1) ** -0.5).to(BF16))
+    t["target"] = torch.randint(0, V, (M,), generator=g)
+    t["target"][torch.rand(M, generator=g) < pad] = -100
+    if M > 3:
+        t["target"][1], t["target"][2] = V, V - 1  # just outside, the last column
+    t["target"] = t["target"].to(ids)
+    t["dloss"], t["dlse"] = torch.randn(M, generator=g), torch.randn(M, generator=g)
+    return t
+
+
+def check_xent(t, scale=1.0, dlse=True):
+    d = dev(t)
+    loss, lse, want = ref.linear_cross_entropy(t["x"], t["weight"], t["target"], scale, t["dloss"], t["dlse"] if dlse else None)
+    got, got_lse = block.linear_cross_entropy_fn(d["x"], d["weight"], d["target"], scale=scale, return_lse=True)
+    close(got, loss)
+    close(got_lse, lse)
+    g = block.linear_cross_entropy_bwd(d["x"], d["weight"], d["target"], got_lse, d["dloss"], dlse=d["dlse"] if dlse else None, scale=scale)
+    slack = xent_slack(t["x"], t["weight"], t["target"], lse, t["dloss"], t["dlse"] if dlse else None, scale)
+    close(g["x"], want["x"], 1e-5, room=slack @ t["weight"].double().abs())
+    close(g["weight"], want["weight"], 1e-5, room=slack.t() @ t["x"].double().abs())
+
+
+def xent_slack(x, w, target, lse, dloss, dlse=None, scale=1.0):
+    """What each gradient of a logit may be off by: its rounding to bf16, at most 2^-8 of it, and the fp32
+    arithmetic of softmax and target where they cancel, below 1e-5 of the softmax's part."""
+    x, w = x.double(), w.double()
+    hit = (target >= 0) & (target < w.shape[0])
+    a = torch.where(hit, dloss.double(), torch.zeros_like(lse))
+    f = a if dlse is None else a + dlse.double()
+    p = f[:, None] * torch.exp(scale * x @ w.t() - lse[:, None])
+    d = p.clone()
+    d[torch.arange(len(hit)), target.long().clamp(0, w.shape[0] - 1)] -= a
+    return scale * (2.0 ** -8 * d.abs() + 1e-5 * p.abs())
+
+
+XENT_SIZES = [(1, 8, 1), (1, 1, 2), (5, 3, 7), (4, 64, 128), (130, 72, 129), (64, 100, 1000), (129, 65, 255), (300, 256, 513), (700, 24, 3001),
+              (1, 512, 5000), (33, 1001, 1000), (513, 128, 2000)]
+
+
+@pytest.mark.parametrize("M,K,V", XENT_SIZES)
+def test_cross_entropy(M, K, V):
+    check_xent(xent_case(M + K + V, M, K, V, torch.int32 if M % 2 else torch.int64), scale=1.0 if K % 2 else 0.6, dlse=V % 2 == 1)
+
+
+def test_cross_entropy_large_tiles_and_pieces():
+    """Enough rows and columns for the largest tiles and several pieces of the vocabulary, odd in every size."""
+    M, K, V = 20011, 136, 9001
+    g = torch.Generator(device=DEV).manual_seed(40)
+    x = torch.randn(M, K, generator=g, device=DEV).to(BF16)
+    w = (torch.randn(V, K, generator=g, device=DEV) * K ** -0.5).to(BF16)
+    t = torch.randint(0, V, (M,), generator=g, device=DEV)
+    t[::7] = -1
+    dloss = torch.randn(M, generator=g, device=DEV)
+    loss, lse = block.linear_cross_entropy_fn(x, w, t, return_lse=True)
+    out = block.linear_cross_entropy_bwd(x, w, t, lse, dloss)
+    # 64-bit on the GPU by blocks of rows
+    dw, room_w = torch.zeros(V, K, dtype=torch.float64, device=DEV), torch.zeros(V, K, dtype=torch.float64, device=DEV)
+    wd = w.double()
+    for s in range(0, M, 4096):
+        r = slice(s, min(s + 4096, M))
+        xd = x[r].double()
+        logits = xd @ wd.t()
+        want = torch.logsumexp(logits, -1)
+        hit = t[r] >= 0
+        at = t[r].clamp(min=0)[:, None]
+        close(lse[r], want)
+        close(loss[r], torch.where(hit, want - logits.gather(1, at)[:, 0], torch.zeros_like(want)))
+        p = torch.exp(logits - want[:, None])
+        a = torch.where(hit, dloss[r].double(), torch.zeros_like(want))[:, None]
+        d = a * p
+        d.scatter_add_(1, at, -a)
+        slack = 2.0 ** -8 * d.abs() + 1e-5 * (a.abs() * p)  # as xent_slack
+        close(out["x"][r], d @ wd, 1e-5, room=(slack @ wd.abs()).cpu())
+        dw += d.t() @ xd
+        room_w += slack.t() @ xd.abs()
+    close(out["weight"], dw, 1e-5, room=room_w.cpu())
+
+
+def test_cross_entropy_rows_without_a_part():
+    """Padding takes no part, whatever its hidden states hold; a row's NaN stays in its loss."""
+    t = xent_case(41, 200, 40, 600, pad=0.4)
+    d = dev(t)
+    out = (t["target"] < 0) | (t["target"] >= 600)
+    loss, lse = block.linear_cross_entropy_fn(d["x"], d["weight"], d["target"], return_lse=True)
+    g = block.linear_cross_entropy_bwd(d["x"], d["weight"], d["target"], lse, d["dloss"])
+    assert not loss[out.to(DEV)].any() and not g["x"][out.to(DEV)].any()
+    bad = d["x"].clone()
+    bad[out.to(DEV)] = float("nan")
+    loss2, lse2 = block.linear_cross_entropy_fn(bad, d["weight"], d["target"], return_lse=True)
+    g2 = block.linear_cross_entropy_bwd(bad, d["weight"], d["target"], lse2, d["dloss"])
+    assert torch.equal(loss2, loss) and torch.equal(g2["x"], g["x"]) and torch.equal(g2["weight"], g["weight"])
+    bad = d["x"].clone()
+    row = int((~out).nonzero()[3])
+    bad[row, 7] = float("nan")
+    loss3 = block.linear_cross_entropy_fn(bad, d["weight"], d["target"])
+    rest = torch.arange(200, device=DEV) != row
+    assert bool(loss3[row].isnan()) and torch.equal(loss3[rest], loss[rest])
+    # no target at all
+    none = torch.full_like(d["target"], -100)
+    loss, lse = block.linear_cross_entropy_fn(d["x"], d["weight"], none, return_lse=True)
+    g = block.linear_cross_entropy_bwd(d["x"], d["weight"], none, lse, d["dloss"])
+    assert not loss.any() and not g["x"].any() and not g["weight"].any()
+
+
+def test_cross_entropy_infinite_logits():
+    """A column of -inf has no part in the sum, one of +inf makes it infinite, rows of nothing but -inf are log 0."""
+    x, w = torch.zeros(3, 8, dtype=BF16, device=DEV), torch.zeros(5, 8, dtype=BF16, device=DEV)
+    x[:, 0] = torch.tensor([1.0, -1.0, 1.0])
+    x[2, 1] = 1.0
+    w[:, 0] = torch.tensor([1.0, 2.0, -3e38, 0.5, 0.0])
+    w[2, 0] = float("-inf")
+    t = torch.tensor([1, 0, 0], device=DEV)
+    loss, lse = block.linear_cross_entropy_fn(x, w, t, return_lse=True)
+    want = torch.logsumexp(torch.tensor([1.0, 2.0, 0.5, 0.0], dtype=torch.float64), 0)
+    assert abs(float(lse[0]) - float(want)) < 1e-5 and abs(float(loss[0]) - float(want - 2)) < 1e-5
+    assert float(lse[1]) == float("inf") and float(loss[1]) == float("inf")
+    w[:, 0] = float("-inf")
+    assert float(block.linear_cross_entropy_fn(x, w, t, return_lse=True)[1][0]) == float("-inf")
+
+
+def test_cross_entropy_large_logits():
+    """Logits of hundreds: the maximum is taken out."""
+    t = xent_case(42, 40, 64, 300)
+    t["x"] = (t["x"].float() * 200).to(BF16)
+    d = dev(t)
+    loss, lse = ref.linear_cross_entropy(t["x"], t["weight"], t["target"])
+    got, got_lse = block.linear_cross_entropy_fn(d["x"], d["weight"], d["target"], return_lse=True)
+    close(got_lse, lse)
+    close(got, loss, room=2.0 ** -22 * lse.abs().max())  # a difference of two numbers of lse's size
+
+
+def test_cross_entropy_strided_operands_and_wanted_gradients():
+    t = dev(xent_case(43, 70, 40, 200))
+    wide_x = torch.full((70, 57), float("nan"), dtype=BF16, device=DEV)
+    wide_w = torch.full((200, 48), float("nan"), dtype=BF16, device=DEV)
+    wide_x[:, 3:43], wide_w[:, 8:48] = t["x"], t["weight"]
+    x, w = wide_x[:, 3:43], wide_w[:, 8:48]
+    loss, lse = block.linear_cross_entropy_fn(t["x"], t["weight"], t["target"], return_lse=True)
+    a, b = block.linear_cross_entropy_fn(x, w, t["target"], return_lse=True)
+    assert torch.equal(a, loss) and torch.equal(b, lse)
+    full = block.linear_cross_entropy_bwd(t["x"], t["weight"], t["target"], lse, t["dloss"])
+    for kw, keys in ((dict(want_dx=False), ["weight"]), (dict(want_dweight=False), ["x"]), (dict(), ["x", "weight"])):
+        g = block.linear_cross_entropy_bwd(x, w, t["target"], lse, t["dloss"], **kw)
+        assert list(g) == keys and all(torch.equal(g[k], full[k]) for k in keys)
+    assert torch.equal(block.linear_cross_entropy_fn(x.unflatten(0, (7, 10)), w, t["target"].view(7, 10)), loss.view(7, 10))
+
+
+def test_cross_entropy_autograd():
+    t = xent_case(44, 60, 32, 210)
+    d = dev(t)
+    hit = (t["target"] >= 0) & (t["target"] < 210)
+    n = int(hit.sum())
+    for reduction, a in (("mean", torch.full((60,), 1.0 / n)), ("sum", torch.ones(60)), ("none", t["dloss"])):
+        x, w = d["x"].clone().requires_grad_(), d["weight"].clone().requires_grad_()
+        loss, lse = block.linear_cross_entropy(x, w, d["target"], reduction=reduction, return_lse=True)
+        want, want_lse, g = ref.linear_cross_entropy(t["x"], t["weight"], t["target"], dloss=a, dlse=0.01 * torch.ones(60))
+        want = want if reduction == "none" else want.sum() / (n if reduction == "mean" else 1)
+        close(loss, want)
+        ((loss * d["dloss"]).sum() if reduction == "none" else loss).add((0.01 * lse).sum()).backward()
+        slack = xent_slack(t["x"], t["weight"], t["target"], want_lse, a, 0.01 * torch.ones(60))
+        close(x.grad, g["x"], 1e-5, room=slack @ t["weight"].double().abs())
+        close(w.grad, g["weight"], 1e-5, room=slack.t() @ t["x"].double().abs())
+        with torch.no_grad():
+            assert torch.equal(block.linear_cross_entropy(x, w, d["target"], reduction=reduction), loss)
+    w = d["weight"].clone().requires_grad_()  # a frozen trunk
+    block.linear_cross_entropy(d["x"], w, d["target"]).backward()
+    assert w.grad is not None
+    # a loss with no targets
+    none = torch.full_like(d["target"], -1)
+    x = d["x"].clone().requires_grad_()
+    loss = block.linear_cross_entropy(x, d["weight"], none)
+    loss.backward()
+    assert bool(loss.isnan()) and not x.grad.any()
+
+
+def test_cross_entropy_empty():
+    x, w = torch.zeros(0, 8, dtype=BF16, device=DEV), torch.zeros(5, 8, dtype=BF16, device=DEV)
+    t = torch.zeros(0, dtype=torch.int64, device=DEV)
+    loss, lse = block.linear_cross_entropy_fn(x, w, t, return_lse=True)
+    assert loss.shape == (0,)
+    g = block.linear_cross_entropy_bwd(x, w, t, lse, loss)
+    assert g["x"].shape == (0, 8) and not g["weight"].any()
+    assert float(block.linear_cross_entropy(x, w, t, reduction="sum")) == 0.0
+    x, w, t = torch.zeros(3, 0, dtype=BF16, device=DEV), torch.zeros(7, 0, dtype=BF16, device=DEV), torch.tensor([1, -1, 6], device=DEV)
+    loss, lse = block.linear_cross_entropy_fn(x, w, t, return_lse=True)  # logits of nothing: all 0
+    want = torch.log(torch.tensor(7.0, dtype=torch.float64))
+    close(lse, want.expand(3))
+    assert float(loss[1]) == 0.0
+    assert block.linear_cross_entropy_bwd(x, w, t, lse, loss)["weight"].shape == (7, 0)
+
+
+# ---- all of them: repeats, streams, replays ----
+
+def every_call():
+    """A call of each operator and its gradient on fixed inputs: functions of no argument that return tensors."""
+    c = dev(conv_case(50, 3, 300, 72, 4, BF16, reset=True))
+    s = dev(step_case(51, 5, 72, 16, 5, 4, BF16))
+    n = dev(dict(zip("xzd", (torch.randn(700, 72, generator=gen(52)).to(BF16) for _ in range(3)))))
+    e = dev(xent_case(53, 300, 72, 1000))
+    w = torch.randn(72, generator=gen(54)).to(DEV)
+    conv = dict(initial_state=c["state"], reset=c["reset"])
+    outs = [torch.empty_like(s["conv_state"]), torch.empty_like(s["ssm_state"])]
+    stats = block.rms_norm_fn(n["x"], w, return_stats=True)[1]
+    gstats = block.gated_rms_norm_fn(n["x"], n["z"], w, groups=2, return_stats=True)[1]
+    lse = block.linear_cross_entropy_fn(e["x"], e["weight"], e["target"], return_lse=True)[1]
+    steps = lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    xs, dys = steps(c["x"]), steps(c["dy"])
+    values = lambda d: tuple(d.values())  # noqa: E731
+    return [
+        lambda: block.causal_conv_fn(c["x"], c["weight"], c["bias"], return_last_state=True, **conv),
+        lambda: block.causal_conv_fn(c["x"], c["weight"], c["bias"], return_last_state=True, scan_layout=True, **conv),
+        lambda: block.causal_conv_fn(xs, c["weight"], c["bias"], return_last_state=True, **conv),
+        lambda: values(block.causal_conv_bwd(c["x"], c["weight"], c["bias"], c["dy"], dlast_state=c["dlast"], **conv)),
+        lambda: values(block.causal_conv_bwd(c["x"], c["weight"], c["bias"], dys, dlast_state=c["dlast"], **conv)),
+        lambda: values(block.causal_conv_bwd(xs, c["weight"], c["bias"], dys, dlast_state=c["dlast"], **conv)),
+        lambda: (block.block_step(**s, conv_state_out=outs[0], ssm_state_out=outs[1]), outs[0].clone(), outs[1].clone()),
+        lambda: block.rms_norm_fn(n["x"], w, residual=n["z"], scale=0.5),
+        lambda: values(block.rms_norm_bwd(n["x"], w, n["d"], stats, dresidual=n["z"], scale=0.5)),
+        lambda: (block.gated_rms_norm_fn(n["x"], n["z"], w, groups=2),),
+        lambda: values(block.gated_rms_norm_bwd(n["x"], n["z"], w, n["d"], gstats, groups=2)),
+        lambda: block.linear_cross_entropy_fn(e["x"], e["weight"], e["target"], return_lse=True),
+        lambda: (block.linear_cross_entropy(e["x"], e["weight"], e["target"]),),
+        lambda: values(block.linear_cross_entropy_bwd(e["x"], e["weight"], e["target"], lse, e["dloss"], dlse=e["dlse"])),
+    ]
+
+
+def same(a, b):
+    return len(a) == len(b) and all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_repeats_bit_for_bit_and_on_another_stream():
+    for k, f in enumerate(every_call()):
+        want = tuple(t.clone() for t in f())
+        assert same(f(), want), k
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = f()
+        torch.cuda.current_stream().wait_stream(side)
+        assert same(got, want), k
+
+
+def test_replayed_graphs_repeat_the_eager_calls():
+    for k, f in enumerate(every_call()):
+        want = tuple(t.clone() for t in f())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            f()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = f()
+        for turn in range(4):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert same(got, want), (k, turn)
+            assert same(f(), want), (k, turn)  # the program's own eager work between the replays
