@@ -25,9 +25,8 @@ namespace mscan {
 
 namespace {
 
-constexpr int kRun = 8;       // steps of a thread's run
+constexpr int kRun = 8;       // steps of a thread's run where steps lie side by side
 constexpr int kConvThreads = 256;
-constexpr int kGroup = 64;    // channels of a "rows" workgroup: lines of 128 or 256 bytes
 constexpr int kMaxWidth = 4;
 
 struct ConvArgs {
@@ -101,266 +100,342 @@ __device__ __forceinline__ bool left_alive(const uint8_t* reset, int64_t len, in
 }
 
 // ---- channels side by side ----
+//
+// A wave takes a run of steps of 64 packs of channels, so that the step, and whether a sequence begins at it, are the
+// same for all its lanes: the resets around a run are one 64-bit mask, and a run without any goes without a test.
+// Rows are loaded kAhead at a time, the next ones while these are worked on; a value stays in registers for the
+// W - 1 steps that see it.
 
-template <typename S, int W, bool STEPS_OUT>
-__global__ __launch_bounds__(kConvThreads) void conv_rows_fwd_kernel(ConvArgs p) {
-    constexpr int V = 16 / sizeof(S), CG = kGroup / V, TG = kConvThreads / CG;
-    constexpr int QPI = kRun / V, SLOTS = TG * QPI;  // 16-byte pieces of a run; of a workgroup's runs
-    static_assert(SLOTS == 32 && CG <= SLOTS);
-    using P = Pack<S, V>;
-    __shared__ P tile[STEPS_OUT ? kGroup * SLOTS : 1];
-    const int tid = threadIdx.x, cg = tid % CG, tg = tid / CG;
-    const int groups = (int)((p.dim + kGroup - 1) / kGroup);
+constexpr int kV = 2;              // channels of a lane
+constexpr int kCols = 64 * kV;     // of a workgroup
+constexpr int kWaves = 4;
+constexpr int kRowRun = 32;        // steps of a wave's run, in the backward with the W - 1 behind it
+constexpr int kAhead = 8;
+
+// A lane's kV channels of a row that begins at `row`. EVEN (an even number of channels): lanes past the last pair
+// repeat it, in the same wave, so that neither loads nor stores are masked.
+template <typename S, bool EVEN>
+struct Cols {
+    uint32_t at;  // bytes from a row's start
+    int n;        // channels that are there
+    __device__ __forceinline__ Cols(int64_t c0, int64_t dim) {
+        n = (int)(dim - c0 < kV ? dim - c0 : kV);
+        at = (uint32_t)((EVEN && n < kV ? dim - kV : c0) * sizeof(S));
+    }
+    __device__ __forceinline__ Pack<S, kV> load(const void* row) const {
+        const S* p = reinterpret_cast<const S*>(static_cast<const char*>(row) + at);
+        if constexpr (EVEN) {
+            Pack<S, kV> r;
+            __builtin_memcpy(&r, p, sizeof(r));
+            return r;
+        } else {
+            return load_some<S, kV>(p, n);
+        }
+    }
+    __device__ __forceinline__ void store(void* row, const Pack<S, kV>& r) const {
+        S* p = reinterpret_cast<S*>(static_cast<char*>(row) + at);
+        if constexpr (EVEN) __builtin_memcpy(p, &r, sizeof(r));
+        else store_some<S, kV>(p, r, n);
+    }
+};
+
+// Bit i: whether a sequence begins at step t0 - 2 + i.
+__device__ __forceinline__ uint64_t reset_mask(const uint8_t* row, int t0, int len) {
+    if (!row) return 0;
+    const int t = t0 - 2 + (int)(threadIdx.x & 63);
+    return __ballot(t >= 0 && t < len && row[t] != 0);
+}
+
+// Steps since the last reset, as a run's steps are walked through.
+struct Age {
+    uint64_t mask;
+    int age;
+    __device__ __forceinline__ explicit Age(uint64_t m) : mask(m), age(kMaxWidth) { next(), next(); }
+    __device__ __forceinline__ void next() { age = mask & 1 ? 0 : age + 1, mask >>= 1; }
+};
+
+template <typename S, int W, bool STEPS_OUT, bool EVEN>
+__global__ __launch_bounds__(64 * kWaves) void conv_rows_fwd_kernel(ConvArgs p) {
+    constexpr int Q = 16 / sizeof(S), QPI = kRowRun / Q, SLOTS = kWaves * QPI;  // 16-byte pieces of a run's steps; of all
+    using P = Pack<S, kV>;
+    using Line = Pack<S, Q>;
+    __shared__ Line tile[STEPS_OUT ? kCols * SLOTS : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int groups = (int)((p.dim + kCols - 1) / kCols);
     const int group = blockIdx.x % groups;
-    const int64_t c0 = (int64_t)group * kGroup + cg * V;
-    const int n = (int)(p.dim - c0 < V ? p.dim - c0 : V);  // channels of this thread's pack, none if n <= 0
+    const int64_t c0 = (int64_t)group * kCols + lane * kV;
+    const Cols<S, EVEN> cols(c0, p.dim);
+    const int64_t cw = EVEN && c0 > p.dim - kV ? p.dim - kV : c0;  // the channels themselves
     const int len = (int)p.len;
 
-    float w[V][W], b[V];
+    float w[kV][W], b[kV];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < kV; ++v) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[v][k] = v < n ? p.w[(c0 + v) * W + k] : 0.0f;
-        b[v] = p.b && v < n ? p.b[c0 + v] : 0.0f;
+        for (int k = 0; k < W; ++k) w[v][k] = EVEN || v < cols.n ? p.w[(cw + v) * W + k] : 0.0f;
+        b[v] = p.b && (EVEN || v < cols.n) ? p.b[cw + v] : 0.0f;
     }
-    for (uint32_t first = (blockIdx.x / groups) * TG; first < p.items; first += (uint32_t)p.blocks * TG) {
-        const uint32_t item = first + tg;
-        if (n > 0 && item < p.items) {
+    for (uint32_t first = (blockIdx.x / groups) * kWaves; first < p.items; first += (uint32_t)p.blocks * kWaves) {
+        const uint32_t item = first + wave;
+        if (item < p.items) {
             const uint32_t bt = item / p.runs;
-            const int t0 = (int)(item - bt * p.runs) * kRun;
-            const S* x = static_cast<const S*>(p.x) + bt * p.sx_b + c0;
-            P in[W - 1 + kRun];
-#pragma unroll
-            for (int i = 0; i < W - 1 + kRun; ++i) {
-                const int t = t0 + i - (W - 1);
-                in[i] = load_some<S, V>(x + t * p.sx_r, t >= 0 && t < len ? n : 0);
-            }
-            const S* state = static_cast<const S*>(p.state) + (int64_t)bt * (W - 1) * p.dim + c0;
-            if (t0 == 0 && p.state) {
-#pragma unroll
-                for (int i = 0; i < W - 1; ++i) in[i] = load_some<S, V>(state + i * p.dim, n);
-            }
+            const int t0 = (int)(item - bt * p.runs) * kRowRun, steps = len - t0 < kRowRun ? len - t0 : kRowRun;
+            const S* x = static_cast<const S*>(p.x) + bt * p.sx_b;
+            S* y = static_cast<S*>(p.y) + bt * p.sy_b;
             const uint8_t* reset = p.reset ? p.reset + bt * p.len : nullptr;
-            const uint32_t bits = reset_bits(reset, t0, len);
+            const int64_t st = (int64_t)bt * (W - 1) * p.dim;
+            P next[kAhead], before[W - 1 > 0 ? W - 1 : 1]{};
+            auto fetch = [&](int i0) __attribute__((always_inline)) {  // (behind the last row, that row again)
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) next[i] = cols.load(x + (t0 + (i0 + i < steps ? i0 + i : steps - 1)) * p.sx_r);
+            };
+            if (steps > 0) fetch(0);
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                if (t0 > 0) before[i] = cols.load(x + (t0 - (W - 1) + i) * p.sx_r);
+                else if (p.state) before[i] = cols.load(static_cast<const S*>(p.state) + st + i * p.dim);
+            }
+            const uint64_t mask = reset_mask(reset, t0, len);
             if (t0 == 0 && p.last) {
-                // before anything of this thread's channels is written over: the old state is in `in`
-                S* last = static_cast<S*>(p.last) + (int64_t)bt * (W - 1) * p.dim + c0;
+                // before anything of these channels is written over: the old state is in `before`
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) {
                     const int s = len - (W - 1) + j;
-                    P r;
-                    if (s >= 0) {
-                        r = load_some<S, V>(x + s * p.sx_r, n);
-                    } else {
+                    P r{};
+                    if (left_alive<W>(reset, len, j)) {
+                        if (s >= 0) r = cols.load(x + s * p.sx_r);
+                        else
 #pragma unroll
-                        for (int i = 0; i < W - 1; ++i)
-                            if (i == s + W - 1) r = in[i];
+                            for (int i = 0; i < W - 1; ++i)
+                                if (i == s + W - 1) r = before[i];
                     }
-                    if (!left_alive<W>(reset, len, j)) r = load_some<S, V>(x, 0);
-                    store_some<S, V>(last + j * p.dim, r, n);
+                    cols.store(static_cast<S*>(p.last) + st + j * p.dim, r);
                 }
             }
-            P out[kRun];
+            float seen[W][kV];  // seen[j]: the value of j steps back
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                P line[QPI];
+            for (int j = 1; j < W; ++j)
 #pragma unroll
-                for (int i = 0; i < kRun; ++i) {
-                    float pre = b[v];
-                    const int age = age_of(bits, 8 + i);
+                for (int v = 0; v < kV; ++v) seen[j - 1][v] = to_f32(before[W - 1 - j].v[v]);
+            auto run = [&](auto cut) __attribute__((always_inline)) {
+                Age age(mask);
+                for (int i0 = 0; i0 < steps; i0 += kAhead) {
+                    P now[kAhead];
 #pragma unroll
-                    for (int j = W - 1; j >= 0; --j) {
-                        const float value = to_f32(in[W - 1 + i - j].v[v]);
-                        pre = __builtin_fmaf(w[v][W - 1 - j], j <= age ? value : 0.0f, pre);
+                    for (int i = 0; i < kAhead; ++i) now[i] = next[i];
+                    if (i0 + kAhead < steps) fetch(i0 + kAhead);
+                    Line line[kV][kAhead / Q];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        P out;
+                        if constexpr (decltype(cut)::value) age.next();
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) {
+#pragma unroll
+                            for (int j = W - 1; j > 0; --j) seen[j][v] = !decltype(cut)::value || j <= age.age ? seen[j - 1][v] : 0.0f;
+                            seen[0][v] = to_f32(now[i].v[v]);
+                            float pre = b[v];
+#pragma unroll
+                            for (int j = W - 1; j >= 0; --j) pre = __builtin_fmaf(w[v][W - 1 - j], seen[j][v], pre);
+                            out.v[v] = from_f32<S>(act_f(pre, p.silu));
+                            if constexpr (STEPS_OUT) line[v][i / Q].v[i % Q] = out.v[v];
+                        }
+                        if constexpr (!STEPS_OUT)
+                            if (i0 + i < steps) cols.store(y + (t0 + i0 + i) * p.sy_r, out);
                     }
-                    const S r = from_f32<S>(act_f(pre, p.silu));
-                    if constexpr (STEPS_OUT) line[i / V].v[i % V] = r;
-                    else out[i].v[v] = r;
-                }
-                if constexpr (STEPS_OUT) {
+                    if constexpr (STEPS_OUT) {
 #pragma unroll
-                    for (int h = 0; h < QPI; ++h) tile[(cg * V + v) * SLOTS + ((tg * QPI + h) ^ cg)] = line[h];
-                }
-            }
-            if constexpr (!STEPS_OUT) {
-                S* y = static_cast<S*>(p.y) + bt * p.sy_b + c0;
+                        for (int v = 0; v < kV; ++v)
 #pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    if (t0 + i < len) store_some<S, V>(y + (t0 + i) * p.sy_r, out[i], n);
-            }
+                            for (int h = 0; h < kAhead / Q; ++h)
+                                tile[(lane * kV + v) * SLOTS + ((wave * QPI + i0 / Q + h) ^ (lane & (SLOTS - 1)))] = line[v][h];
+                    }
+                }
+            };
+            if (mask == 0) run(std::false_type{});
+            else run(std::true_type{});
         }
         if constexpr (STEPS_OUT) {
             __syncthreads();
-            for (int k = tid; k < kGroup * SLOTS; k += kConvThreads) {
+            for (int k = threadIdx.x; k < kCols * SLOTS; k += 64 * kWaves) {
                 const int c = k / SLOTS, slot = k % SLOTS;
                 const uint32_t it = first + slot / QPI;
-                const int64_t ch = (int64_t)group * kGroup + c;
+                const int64_t ch = (int64_t)group * kCols + c;
                 if (it >= p.items || ch >= p.dim) continue;
                 const uint32_t bt = it / p.runs;
-                const int t = (int)(it - bt * p.runs) * kRun + slot % QPI * V;
+                const int t = (int)(it - bt * p.runs) * kRowRun + slot % QPI * Q;
                 if (t < len)
-                    store_some<S, V>(static_cast<S*>(p.y) + bt * p.sy_b + ch * p.sy_r + t, tile[c * SLOTS + (slot ^ (c / V))],
-                                     len - t);
+                    store_some<S, Q>(static_cast<S*>(p.y) + bt * p.sy_b + ch * p.sy_r + t,
+                                     tile[c * SLOTS + (slot ^ (c / kV & (SLOTS - 1)))], len - t);
             }
             __syncthreads();
         }
     }
 }
 
-template <typename S, int W, bool STEPS_OUT>
-__global__ __launch_bounds__(kConvThreads) void conv_rows_bwd_kernel(ConvBwdArgs p) {
-    constexpr int V = 4, CG = kGroup / V, TG = kConvThreads / CG;
-    constexpr int NX = 2 * (W - 1) + kRun, NG = W - 1 + kRun, GW = 12;  // GW: steps of dy kept for a run
-    constexpr int PITCH = TG * GW + 4;                                  // of a channel's runs in LDS
-    using P = Pack<S, V>;
-    constexpr int TILE = STEPS_OUT ? kGroup * PITCH * (int)sizeof(S) : 16, SUMS = TG * kGroup * (W + 1) * 4;
+template <typename S, int W, bool STEPS_OUT, bool EVEN>
+__global__ __launch_bounds__(64 * kWaves) void conv_rows_bwd_kernel(ConvBwdArgs p) {
+    constexpr int Q = 16 / sizeof(S), QPI = kRowRun / Q, SLOTS = kWaves * QPI, RUN = kRowRun - (W - 1);
+    using P = Pack<S, kV>;
+    using Line = Pack<S, Q>;
+    constexpr int TILE = STEPS_OUT ? kCols * SLOTS * 16 : 16, SUMS = kWaves * kCols * (W + 1) * 4;
     __shared__ __align__(16) char lds[TILE > SUMS ? TILE : SUMS];
-    S* tile = reinterpret_cast<S*>(lds);
-    const int tid = threadIdx.x, cg = tid % CG, tg = tid / CG;
-    const int groups = (int)((p.dim + kGroup - 1) / kGroup);
+    Line* tile = reinterpret_cast<Line*>(lds);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int groups = (int)((p.dim + kCols - 1) / kCols);
     const int group = blockIdx.x % groups, block = blockIdx.x / groups;
-    const int64_t c0 = (int64_t)group * kGroup + cg * V;
-    const int n = (int)(p.dim - c0 < V ? p.dim - c0 : V);
+    const int64_t c0 = (int64_t)group * kCols + lane * kV;
+    const Cols<S, EVEN> cols(c0, p.dim);
+    const int64_t cw = EVEN && c0 > p.dim - kV ? p.dim - kV : c0;
+    const int pair = (int)(cw - (int64_t)group * kCols) / kV;  // of the workgroup's
     const int len = (int)p.len;
 
-    float w[V][W], b[V], dw[V][W], db[V];
+    float w[kV][W], b[kV], dw[kV][W], db[kV];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < kV; ++v) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[v][k] = v < n ? p.w[(c0 + v) * W + k] : 0.0f, dw[v][k] = 0.0f;
-        b[v] = p.b && v < n ? p.b[c0 + v] : 0.0f;
+        for (int k = 0; k < W; ++k) w[v][k] = EVEN || v < cols.n ? p.w[(cw + v) * W + k] : 0.0f, dw[v][k] = 0.0f;
+        b[v] = p.b && (EVEN || v < cols.n) ? p.b[cw + v] : 0.0f;
         db[v] = 0.0f;
     }
-    for (uint32_t first = (uint32_t)block * TG; first < p.items; first += (uint32_t)p.blocks * TG) {
+    for (uint32_t first = (uint32_t)block * kWaves; first < p.items; first += (uint32_t)p.blocks * kWaves) {
         if constexpr (STEPS_OUT) {
-            // dy's runs of 64 channels, with the W - 1 steps behind each
-            for (int k = tid; k < kGroup * TG; k += kConvThreads) {
-                const int c = k / TG, slot = k % TG;
-                const uint32_t it = first + slot;
-                const int64_t ch = (int64_t)group * kGroup + c;
+            // dy's runs of the workgroup's channels, each with the W - 1 steps behind it
+            for (int k = threadIdx.x; k < kCols * SLOTS; k += 64 * kWaves) {
+                const int c = k / SLOTS, slot = k % SLOTS;
+                const uint32_t it = first + slot / QPI;
+                const int64_t ch = (int64_t)group * kCols + c;
                 const bool on = it < p.items && ch < p.dim;
                 const uint32_t bt = on ? it / p.runs : 0;
-                const int t = on ? (int)(it - bt * p.runs) * kRun : len;
-                const S* g = static_cast<const S*>(p.dy) + bt * p.sg_b + (on ? ch : 0) * p.sg_r;
-                S* to = tile + c * PITCH + slot * GW;
-#pragma unroll
-                for (int h = 0; h < 3; ++h) {
-                    const P r = load_some<S, 4>(g + t + 4 * h, len - t - 4 * h);
-                    *reinterpret_cast<P*>(to + 4 * h) = r;
-                }
+                const int t = on ? (int)(it - bt * p.runs) * RUN + slot % QPI * Q : len;
+                tile[c * SLOTS + (slot ^ (c / kV & (SLOTS - 1)))] =
+                    load_some<S, Q>(static_cast<const S*>(p.dy) + bt * p.sg_b + (on ? ch : 0) * p.sg_r + t, len - t);
             }
             __syncthreads();
         }
-        const uint32_t item = first + tg;
-        if (n > 0 && item < p.items) {
+        const uint32_t item = first + wave;
+        if (item < p.items) {
             const uint32_t bt = item / p.runs;
-            const int t0 = (int)(item - bt * p.runs) * kRun;
-            const S* x = static_cast<const S*>(p.x) + bt * p.sx_b + c0;
-            P in[NX], g[STEPS_OUT ? 1 : NG];
-#pragma unroll
-            for (int i = 0; i < NX; ++i) {
-                const int t = t0 + i - (W - 1);
-                in[i] = load_some<S, V>(x + t * p.sx_r, t >= 0 && t < len ? n : 0);
-            }
-            if constexpr (!STEPS_OUT) {
-                const S* dy = static_cast<const S*>(p.dy) + bt * p.sg_b + c0;
-#pragma unroll
-                for (int i = 0; i < NG; ++i) g[i] = load_some<S, V>(dy + (t0 + i) * p.sg_r, t0 + i < len ? n : 0);
-            }
-            const int64_t st = (int64_t)bt * (W - 1) * p.dim + c0;
-            if (t0 == 0 && p.state) {
-#pragma unroll
-                for (int i = 0; i < W - 1; ++i) in[i] = load_some<S, V>(static_cast<const S*>(p.state) + st + i * p.dim, n);
-            }
+            const int t0 = (int)(item - bt * p.runs) * RUN;
+            const int most = len - t0 < RUN ? len - t0 : RUN;                      // steps of the run
+            const int steps = len - t0 < kRowRun ? len - t0 : kRowRun;             // that there are with those behind it
+            const S* x = static_cast<const S*>(p.x) + bt * p.sx_b;
+            const S* dy = static_cast<const S*>(p.dy) + bt * p.sg_b;
+            S* dx = static_cast<S*>(p.dx) + bt * p.sd_b;
             const uint8_t* reset = p.reset ? p.reset + bt * p.len : nullptr;
-            const uint32_t bits = reset_bits(reset, t0, len);
-            // gradients of the values of steps t0 - (W - 1) .. t0 + kRun - 1; those before t0 are the initial
-            // state's, in a sequence's first run
-            float dv[V][W - 1 + kRun];
+            const int64_t st = (int64_t)bt * (W - 1) * p.dim;
+            P nx[kAhead]{}, ng[kAhead]{}, before[W - 1 > 0 ? W - 1 : 1]{};
+            auto fetch = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int i = 0; i < W - 1 + kRun; ++i) dv[v][i] = 0.0f;
-            if (p.dlast && t0 + kRun + W - 1 > len) {
-#pragma unroll
-                for (int i = 0; i < W - 1 + kRun; ++i) {
-                    const int s = t0 + i - (W - 1), j = s - (len - (W - 1));
-                    if (j < 0 || j >= W - 1 || (t0 > 0 && i < W - 1) || !left_alive<W>(reset, len, j)) continue;
-                    const P r = load_some<S, V>(static_cast<const S*>(p.dlast) + st + j * p.dim, n);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) dv[v][i] = to_f32(r.v[v]);
+                for (int i = 0; i < kAhead; ++i) {
+                    const int t = t0 + (i0 + i < steps ? i0 + i : steps - 1);
+                    nx[i] = cols.load(x + t * p.sx_r);
+                    if constexpr (!STEPS_OUT) ng[i] = cols.load(dy + t * p.sg_r);
                 }
+            };
+            if (steps > 0) fetch(0);
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                if (t0 > 0) before[i] = cols.load(x + (t0 - (W - 1) + i) * p.sx_r);
+                else if (p.state) before[i] = cols.load(static_cast<const S*>(p.state) + st + i * p.dim);
             }
+            const uint64_t mask = reset_mask(reset, t0, len);
+            float seen[W][kV], dv[W][kV];  // the value of j steps back, and its gradient as far as it has come
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float line[GW];
-                if constexpr (STEPS_OUT) {
-                    const S* from = tile + (cg * V + v) * PITCH + tg * GW;
+            for (int v = 0; v < kV; ++v) {
 #pragma unroll
-                    for (int h = 0; h < 3; ++h) {
-                        const P r = *reinterpret_cast<const P*>(from + 4 * h);
+                for (int j = 1; j < W; ++j) seen[j - 1][v] = to_f32(before[W - 1 - j].v[v]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) line[4 * h + k] = to_f32(r.v[k]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) line[i] = to_f32(g[i].v[v]);
-                }
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    const int age = age_of(bits, 8 + i);
-                    float pre = b[v], seen[W];
-#pragma unroll
-                    for (int j = W - 1; j >= 0; --j) {
-                        const float value = to_f32(in[W - 1 + i - j].v[v]);
-                        seen[j] = j <= age ? value : 0.0f;
-                        pre = __builtin_fmaf(w[v][W - 1 - j], seen[j], pre);
-                    }
-                    const float d = t0 + i < len ? line[i] * dact_f(pre, p.silu) : 0.0f;
-                    if (i < kRun) {
-                        db[v] += d;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[v][W - 1 - j] = __builtin_fmaf(d, seen[j], dw[v][W - 1 - j]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const int to = W - 1 + i - j;
-                        if (to < W - 1 + kRun) dv[v][to] = __builtin_fmaf(w[v][W - 1 - j], j <= age ? d : 0.0f, dv[v][to]);
-                    }
-                }
+                for (int j = 0; j < W; ++j) dv[j][v] = 0.0f;
             }
-            S* dx = static_cast<S*>(p.dx) + bt * p.sd_b + c0;
-#pragma unroll
-            for (int i = 0; i < W - 1 + kRun; ++i) {
+            // the finished gradient of step s: dx, or the initial state's in a sequence's first run
+            auto emit = [&](int s, const float (&g)[kV]) __attribute__((always_inline)) {
                 P r;
+                float add[kV];
 #pragma unroll
-                for (int v = 0; v < V; ++v) r.v[v] = from_f32<S>(dv[v][i]);
-                const int t = t0 + i - (W - 1);
-                if (i >= W - 1) {
-                    if (t < len) store_some<S, V>(dx + t * p.sd_r, r, n);
-                } else if (t0 == 0 && p.dstate) {
-                    store_some<S, V>(static_cast<S*>(p.dstate) + st + i * p.dim, r, n);
+                for (int v = 0; v < kV; ++v) add[v] = 0.0f;
+                const int j = s - (len - (W - 1));
+                if (p.dlast && j >= 0 && left_alive<W>(reset, len, j)) {
+                    const P l = cols.load(static_cast<const S*>(p.dlast) + st + j * p.dim);
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) add[v] = to_f32(l.v[v]);
                 }
-            }
+#pragma unroll
+                for (int v = 0; v < kV; ++v) r.v[v] = from_f32<S>(g[v] + add[v]);
+                if (s >= 0) cols.store(dx + s * p.sd_r, r);
+                else if (p.dstate) cols.store(static_cast<S*>(p.dstate) + st + (s + W - 1) * p.dim, r);
+            };
+            auto run = [&](auto cut) __attribute__((always_inline)) {
+                Age age(mask);
+                // (the W - 1 turns behind the last step finish the gradients that wait)
+                for (int i0 = 0; i0 < most + W - 1; i0 += kAhead) {
+                    P now[kAhead], g[kAhead];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) now[i] = nx[i], g[i] = ng[i];
+                    if (i0 + kAhead < steps) fetch(i0 + kAhead);
+                    Line line[kV][kAhead / Q];
+                    if constexpr (STEPS_OUT) {
+#pragma unroll
+                        for (int v = 0; v < kV; ++v)
+#pragma unroll
+                            for (int h = 0; h < kAhead / Q; ++h)
+                                line[v][h] = tile[(pair * kV + v) * SLOTS + ((wave * QPI + i0 / Q + h) ^ (pair & (SLOTS - 1)))];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        if constexpr (decltype(cut)::value) age.next();
+                        const bool in = i0 + i < steps, own = i0 + i < most;
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) {
+#pragma unroll
+                            for (int j = W - 1; j > 0; --j) {
+                                seen[j][v] = !decltype(cut)::value || j <= age.age ? seen[j - 1][v] : 0.0f;
+                                dv[j][v] = dv[j - 1][v];
+                            }
+                            seen[0][v] = to_f32(now[i].v[v]);
+                            dv[0][v] = 0.0f;
+                            float pre = b[v];
+#pragma unroll
+                            for (int j = W - 1; j >= 0; --j) pre = __builtin_fmaf(w[v][W - 1 - j], seen[j][v], pre);
+                            float gv;
+                            if constexpr (STEPS_OUT) gv = to_f32(line[v][i / Q].v[i % Q]);
+                            else gv = to_f32(g[i].v[v]);
+                            const float d = in ? gv * dact_f(pre, p.silu) : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < W; ++j)
+                                dv[j][v] = __builtin_fmaf(w[v][W - 1 - j], !decltype(cut)::value || j <= age.age ? d : 0.0f, dv[j][v]);
+                            if (own) {
+                                db[v] += d;
+#pragma unroll
+                                for (int j = 0; j < W; ++j) dw[v][W - 1 - j] = __builtin_fmaf(d, seen[j][v], dw[v][W - 1 - j]);
+                            }
+                        }
+                        const int s = i0 + i - (W - 1);
+                        if (s < most && (s >= 0 || t0 == 0)) emit(t0 + s, dv[W - 1]);
+                    }
+                }
+            };
+            if (mask == 0) run(std::false_type{});
+            else run(std::true_type{});
         }
         if constexpr (STEPS_OUT) __syncthreads();
     }
-    // the threads' sums of a channel, in the order of their runs
-    float* sums = reinterpret_cast<float*>(lds);  // (TG, W + 1, kGroup)
+    // the waves' sums of a channel, in their order
+    float* sums = reinterpret_cast<float*>(lds);  // (kWaves, W + 1, kCols)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < kV; ++v) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) sums[(tg * (W + 1) + k) * kGroup + cg * V + v] = dw[v][k];
-        sums[(tg * (W + 1) + W) * kGroup + cg * V + v] = db[v];
+        for (int k = 0; k < W; ++k) sums[(wave * (W + 1) + k) * kCols + lane * kV + v] = dw[v][k];
+        sums[(wave * (W + 1) + W) * kCols + lane * kV + v] = db[v];
     }
     __syncthreads();
-    for (int k = tid; k < kGroup * (W + 1); k += kConvThreads) {
-        const int64_t c = (int64_t)group * kGroup + k % kGroup;
+    for (int k = threadIdx.x; k < kCols * (W + 1); k += 64 * kWaves) {
+        const int64_t c = (int64_t)group * kCols + k % kCols;
         if (c >= p.dim) continue;
         float s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < TG; ++q) s += sums[q * kGroup * (W + 1) + k];
-        p.part[((int64_t)block * (W + 1) + k / kGroup) * p.dim + c] = s;
+        for (int q = 0; q < kWaves; ++q) s += sums[q * kCols * (W + 1) + k];
+        p.part[((int64_t)block * (W + 1) + k / kCols) * p.dim + c] = s;
     }
 }
 
@@ -511,24 +586,34 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
     }
 }
 
-// The workgroups' partial sums, added in order.
+// The workgroups' partial sums, added in order: 32 columns x 8 stretches of the list a workgroup.
 __global__ __launch_bounds__(256) void conv_join_kernel(const float* part, int blocks, int width, int64_t dim, float* dw, float* db) {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= dim * (width + 1)) return;
+    __shared__ float lds[8][32];
+    const int64_t wide = dim * (width + 1), k = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    const int g = threadIdx.x >> 5, per = (blocks + 7) / 8;
     float s = 0.0f;
+    if (k < wide) {
+        const int q1 = (g + 1) * per < blocks ? (g + 1) * per : blocks;
 #pragma unroll 8
-    for (int q = 0; q < blocks; ++q) s += part[q * dim * (width + 1) + k];
-    const int64_t tap = k / dim, c = k - tap * dim;
-    if (tap < width) {
-        if (dw) dw[c * width + tap] = s;
-    } else if (db) {
-        db[c] = s;
+        for (int q = g * per; q < q1; ++q) s += part[q * wide + k];
     }
+    lds[g][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (g != 0 || k >= wide) return;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += lds[q][threadIdx.x & 31];
+    const int64_t tap = k / dim, c = k - tap * dim;
+    if (tap < width) dw[c * width + tap] = s;
+    else if (db) db[c] = s;
 }
 
-uint32_t runs_of(const mamba_conv_shape& s) { return s.len > 0 ? (uint32_t)((s.len + kRun - 1) / kRun) : 1; }
+int64_t groups_of(const mamba_conv_shape& s) { return (s.dim + kCols - 1) / kCols; }
 
-int64_t groups_of(const mamba_conv_shape& s) { return (s.dim + kGroup - 1) / kGroup; }
+// Runs of a sequence, one at least: of kRun steps where steps lie side by side, of a wave's where channels do.
+uint32_t runs_of(const mamba_conv_shape& s, bool x_steps, bool bwd) {
+    const int64_t run = x_steps ? kRun : bwd ? kRowRun - (s.width - 1) : kRowRun;
+    return s.len > 0 ? (uint32_t)((s.len + run - 1) / run) : 1;
+}
 
 // Workgroups a group of channels (or a channel): as many as the GPU holds at a time, each to take several
 // stretches of runs with the weights it has loaded.
@@ -540,9 +625,8 @@ int blocks_of(int64_t items, int64_t each, int64_t groups, int per_cu) {
 constexpr int kFwdPerCu = 8, kBwdPerCu = 4, kStepsBwdPerCu = 8;
 
 int bwd_blocks(const mamba_conv_shape& s, bool x_steps) {
-    const int64_t items = s.batch * runs_of(s);
-    return x_steps ? blocks_of(items, kConvThreads, s.dim, kStepsBwdPerCu)
-                   : blocks_of(items, kConvThreads / (kGroup / 4), groups_of(s), kBwdPerCu);
+    const int64_t items = s.batch * runs_of(s, x_steps, true);
+    return x_steps ? blocks_of(items, kConvThreads, s.dim, kStepsBwdPerCu) : blocks_of(items, kWaves, groups_of(s), kBwdPerCu);
 }
 
 template <typename S, int W>
@@ -552,10 +636,16 @@ void fwd_go(ConvArgs q, bool x_steps, bool y_steps, int64_t groups, Launches& on
         on(conv_steps_fwd_kernel<S, W>, grid_of((total + kConvThreads - 1) / kConvThreads, kConvThreads), dim3(kConvThreads), q, total);
         return;
     }
-    q.blocks = blocks_of(q.items, kConvThreads / (kGroup / (16 / (int)sizeof(S))), groups, kFwdPerCu);
+    q.blocks = blocks_of(q.items, kWaves, groups, kFwdPerCu);
     const dim3 grid((unsigned)(groups * q.blocks));
-    if (y_steps) on(conv_rows_fwd_kernel<S, W, true>, grid, dim3(kConvThreads), q);
-    else on(conv_rows_fwd_kernel<S, W, false>, grid, dim3(kConvThreads), q);
+    const dim3 block(64 * kWaves);
+    if (q.dim % 2 == 0) {
+        if (y_steps) on(conv_rows_fwd_kernel<S, W, true, true>, grid, block, q);
+        else on(conv_rows_fwd_kernel<S, W, false, true>, grid, block, q);
+    } else {
+        if (y_steps) on(conv_rows_fwd_kernel<S, W, true, false>, grid, block, q);
+        else on(conv_rows_fwd_kernel<S, W, false, false>, grid, block, q);
+    }
 }
 
 template <typename S, int W>
@@ -565,8 +655,14 @@ void bwd_go(const ConvBwdArgs& q, bool x_steps, bool g_steps, int64_t groups, La
         return;
     }
     const dim3 grid((unsigned)(groups * q.blocks));
-    if (g_steps) on(conv_rows_bwd_kernel<S, W, true>, grid, dim3(kConvThreads), q);
-    else on(conv_rows_bwd_kernel<S, W, false>, grid, dim3(kConvThreads), q);
+    const dim3 block(64 * kWaves);
+    if (q.dim % 2 == 0) {
+        if (g_steps) on(conv_rows_bwd_kernel<S, W, true, true>, grid, block, q);
+        else on(conv_rows_bwd_kernel<S, W, false, true>, grid, block, q);
+    } else {
+        if (g_steps) on(conv_rows_bwd_kernel<S, W, true, false>, grid, block, q);
+        else on(conv_rows_bwd_kernel<S, W, false, false>, grid, block, q);
+    }
 }
 
 template <typename F>
@@ -580,8 +676,9 @@ void with_width(int64_t width, F&& f) {
 }  // namespace
 
 int launch_conv_fwd(const mamba_conv_ptrs& p, const mamba_conv_shape& s, int act, bool bf16, hipStream_t stream) {
+    const uint32_t runs = runs_of(s, p.x_steps, false);
     ConvArgs q{p.x, p.weight, p.bias, p.initial_state, p.reset, p.y, p.last_state, p.x_batch, p.x_row, p.y_batch, p.y_row,
-               s.batch, s.len, s.dim, runs_of(s), (uint32_t)(s.batch * runs_of(s)), 1, act == MAMBA_CONV_SILU};
+               s.batch, s.len, s.dim, runs, (uint32_t)(s.batch * runs), 1, act == MAMBA_CONV_SILU};
     Launches on(stream);
     with_width(s.width, [&](auto w) {
         constexpr int W = decltype(w)::value;
@@ -595,16 +692,17 @@ int64_t conv_bwd_workspace(const mamba_conv_shape& s, bool bf16, bool x_steps) {
 }
 
 int launch_conv_bwd(const mamba_conv_bwd_ptrs& p, const mamba_conv_shape& s, int act, bool bf16, hipStream_t stream) {
+    const uint32_t runs = runs_of(s, p.x_steps, true);
     ConvBwdArgs q{p.x, p.weight, p.bias, p.initial_state, p.reset, p.dy, p.dlast_state, p.dx, p.dinitial_state,
                   static_cast<float*>(p.workspace), p.x_batch, p.x_row, p.dy_batch, p.dy_row, p.dx_batch, p.dx_row,
-                  s.batch, s.len, s.dim, runs_of(s), (uint32_t)(s.batch * runs_of(s)), bwd_blocks(s, p.x_steps),
+                  s.batch, s.len, s.dim, runs, (uint32_t)(s.batch * runs), bwd_blocks(s, p.x_steps),
                   act == MAMBA_CONV_SILU};
     Launches on(stream);
     with_width(s.width, [&](auto w) {
         constexpr int W = decltype(w)::value;
         bf16 ? bwd_go<bf16_t, W>(q, p.x_steps, p.dy_steps, groups_of(s), on) : bwd_go<float, W>(q, p.x_steps, p.dy_steps, groups_of(s), on);
     });
-    on(conv_join_kernel, dim3((unsigned)((s.dim * (s.width + 1) + 255) / 256)), dim3(256), static_cast<const float*>(p.workspace),
+    on(conv_join_kernel, dim3((unsigned)((s.dim * (s.width + 1) + 31) / 32)), dim3(256), static_cast<const float*>(p.workspace),
        q.blocks, (int)s.width, s.dim, p.dweight, p.dbias);
     return on.status;
 }
