@@ -15,6 +15,7 @@ gradient has the activation's dtype, a parameter's the parameter's.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -132,19 +133,38 @@ def _load():
     return lib
 
 
+def _is(t, shape, dtype, dev):
+    return t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _param(t, name, shape, like, dev):
+    """:func:`.layers._f32`, for the usual case in one test (a decode step's call checks ten tensors)."""
+    return t if t is None or _is(t, shape, torch.float32, dev) else _f32(t, name, shape, like)
+
+
+def _taken(t, name, shape, dtype, dev):
+    """A tensor of x's dtype and of the given shape, contiguous."""
+    if not _is(t, shape, dtype, dev):
+        if t.dtype is not dtype or t.get_device() != dev:
+            raise TypeError(f"{name} must have x's dtype and device")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        t = t.contiguous()
+    return t
+
+
 # ---- causal convolution ----
 
 _CONV_ACTS = {None: 0, "silu": 1}
 
 
-def _conv_layout(x):
+def _conv_layout(x, shape):
     """x of (batch, len, dim) as it lies: itself (copied where neither its channels nor its steps are side by
     side), the strides of its batches and rows, and whether its rows are steps of a channel."""
     batch, length, dim = x.stride()
-    B, L, D = x.shape
-    if dim == 1 or D <= 1:
+    if dim == 1 or shape[2] <= 1:
         return x, batch, length, 0
-    if length == 1 or L <= 1:
+    if length == 1 or shape[1] <= 1:
         return x, batch, dim, 1
     x = x.contiguous()
     return x, x.stride(0), x.stride(1), 0
@@ -162,20 +182,10 @@ def _conv_args(x, weight, bias, activation, initial_state, reset, entry):
         weight = weight[:, 0]
     if weight.dim() != 2 or weight.shape[0] != dim or not 1 <= weight.shape[1] <= 4:
         raise ValueError(f"weight must be (dim, width) or (dim, 1, width) with dim = {dim} and width 1 to 4, got {tuple(weight.shape)}")
-    width = weight.shape[1]
-    weight, bias = _f32(weight, "weight", weight.shape, x), _f32(bias, "bias", (dim,), x)
-    state = _conv_state(initial_state, "initial_state", (batch, width - 1, dim), x)
-    return dtype, _CONV_ACTS[activation], weight, bias, state, _reset(reset, batch, length, x), width
-
-
-def _conv_state(state, name, shape, x):
-    if state is None:
-        return None
-    if state.dtype is not x.dtype or state.get_device() != x.get_device():
-        raise TypeError(f"{name} must have x's dtype and device")
-    if tuple(state.shape) != shape:
-        raise ValueError(f"{name} must be (batch, width - 1, dim) = {shape}, got {tuple(state.shape)}")
-    return state if state.is_contiguous() else state.contiguous()
+    width, dev = weight.shape[1], x.get_device()
+    weight, bias = _param(weight, "weight", (dim, width), x, dev), _param(bias, "bias", (dim,), x, dev)
+    state = None if initial_state is None else _taken(initial_state, "initial_state", (batch, width - 1, dim), x.dtype, dev)
+    return dtype, _CONV_ACTS[activation], weight, bias, state, reset if reset is None else _reset(reset, batch, length, x), width
 
 
 def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=None, reset=None, return_last_state=False,
@@ -196,14 +206,14 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
     may be ``initial_state`` itself (a decoder's state updated in place)."""
     lib = _load()
     dtype, act, weight, bias, state, reset, width = _conv_args(x, weight, bias, activation, initial_state, reset, "causal_conv_fn")
-    batch, length, dim = x.shape
-    x, xb, xr, steps = _conv_layout(x)
+    whole = batch, length, dim = x.shape
+    x, xb, xr, steps = _conv_layout(x, whole)
     y_steps = 1 if steps or scan_layout else 0
     if out is None:
-        y = x.new_empty((batch, dim, length)).transpose(1, 2) if y_steps else x.new_empty((batch, length, dim))
+        y = x.new_empty((batch, dim, length)).transpose(1, 2) if y_steps else x.new_empty(whole)
     else:
         y = out
-        if y.shape != x.shape or y.dtype is not x.dtype or y.device != x.device:
+        if y.shape != whole or y.dtype is not x.dtype or y.device != x.device:
             raise ValueError("out must have x's shape, dtype and device")
         if y.stride(1 if y_steps else 2) != 1 and y.shape[1 if y_steps else 2] > 1:
             raise ValueError(f"out must have its {'steps' if y_steps else 'channels'} side by side, as y has")
@@ -212,10 +222,11 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
         last = last_state_out
         if last is None:
             last = x.new_empty((batch, width - 1, dim))
-        elif last.shape != (batch, width - 1, dim) or last.dtype is not x.dtype or last.device != x.device or not last.is_contiguous():
+        elif not _is(last, (batch, width - 1, dim), x.dtype, x.get_device()):
             raise ValueError("last_state_out must be a contiguous (batch, width - 1, dim) tensor of x's dtype and device")
+    ys = y.stride()
     ptrs = ConvPtrs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), y.data_ptr(), _ptr(last),
-                    xb, xr, y.stride(0), y.stride(2 if y_steps else 1), steps, y_steps)
+                    xb, xr, ys[0], ys[2 if y_steps else 1], steps, y_steps)
     _launch("mamba_conv_fwd", x, lib.mamba_conv_fwd, ptrs, ConvShape(batch, length, dim, width), act, dtype)
     return (y, last) if return_last_state else y
 
@@ -230,12 +241,12 @@ def causal_conv_bwd(x, weight, bias, dy, *, activation="silu", initial_state=Non
     dtype, act, weight, bias, state, reset, width = _conv_args(x, weight, bias, activation, initial_state, reset, "causal_conv_bwd")
     batch, length, dim = x.shape
     _same(dy, x, "dy")
-    x, xb, xr, steps = _conv_layout(x)
-    dy, gb, gr, g_steps = _conv_layout(dy)
+    x, xb, xr, steps = _conv_layout(x, x.shape)
+    dy, gb, gr, g_steps = _conv_layout(dy, x.shape)
     if steps and not g_steps:
         dy = dy.transpose(1, 2).contiguous().transpose(1, 2)
         gb, gr, g_steps = dy.stride(0), dy.stride(2), 1
-    dlast = _conv_state(dlast_state, "dlast_state", (batch, width - 1, dim), x)
+    dlast = None if dlast_state is None else _taken(dlast_state, "dlast_state", (batch, width - 1, dim), x.dtype, x.get_device())
     if want_dinitial is None:
         want_dinitial = state is not None
     dx = x.new_empty((batch, dim, length)).transpose(1, 2) if steps else x.new_empty((batch, length, dim))
@@ -291,12 +302,11 @@ def causal_conv(x, weight, bias=None, *, activation="silu", initial_state=None, 
 
 # ---- block step ----
 
-def _state_out(given, old, name):
-    if given is None:
-        return old
-    if given.shape != old.shape or given.dtype is not old.dtype or given.device != old.device or not given.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of the state's shape, dtype and device")
-    return given
+@functools.lru_cache(maxsize=64)
+def _step_size(batch, dim, dstate, rank, width):
+    """The shape's structure and the bytes of workspace it needs (which depend on nothing else)."""
+    shape = StepShape(batch, dim, dstate, rank, width)
+    return shape, _load().mamba_block_step_workspace_bytes(shape)
 
 
 def block_step(x, conv_state, ssm_state, conv_w, conv_b, w_x, w_dt, dt_bias, A, D=None, z=None, *, conv_state_out=None,
@@ -315,7 +325,6 @@ def block_step(x, conv_state, ssm_state, conv_w, conv_b, w_x, w_dt, dt_bias, A, 
     are and the new ones written to ``conv_state_out`` and ``ssm_state_out``. conv_w: (dim, width) or (dim, 1,
     width), width 2 to 4; w_x: (dt_rank + 2 dstate, dim) and w_dt: (dim, dt_rank) in x's dtype; conv_b, dt_bias, D: (dim,)
     or None; A: (dim, dstate). Returns y (batch, dim) in float32, as the scan does."""
-    lib = _load()
     dtype = _dtype(x, "x")
     _need_gpu(x, "block_step")
     if x.dim() != 2 or ssm_state.dim() != 3 or w_dt.dim() != 2:
@@ -327,29 +336,27 @@ def block_step(x, conv_state, ssm_state, conv_w, conv_b, w_x, w_dt, dt_bias, A, 
     if conv_w.dim() != 2 or conv_w.shape[0] != dim or not 2 <= conv_w.shape[1] <= 4:
         raise ValueError(f"conv_w must be (dim, width) with dim = {dim} and width 2 to 4, got {tuple(conv_w.shape)}")
     width = conv_w.shape[1]
-    for name, t, shape, dt in (("conv_state", conv_state, (batch, width - 1, dim), x.dtype),
-                               ("ssm_state", ssm_state, (batch, dim, dstate), torch.float32),
-                               ("w_x", w_x, (rank + 2 * dstate, dim), x.dtype), ("w_dt", w_dt, (dim, rank), x.dtype)):
-        if t.dtype is not dt or t.get_device() != x.get_device():
-            raise TypeError(f"{name} must be {dt} on x's device")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    if not conv_state.is_contiguous() or not ssm_state.is_contiguous():
-        raise ValueError("conv_state and ssm_state must be contiguous")
-    conv_out, ssm_out = _state_out(conv_state_out, conv_state, "conv_state_out"), _state_out(ssm_state_out, ssm_state, "ssm_state_out")
+    xt, per_dim, dev = x.dtype, (dim,), x.get_device()
+    conv_shape, ssm_shape = (batch, width - 1, dim), (batch, dim, dstate)
+    for name, t, shape, dt in (("conv_state", conv_state, conv_shape, xt), ("ssm_state", ssm_state, ssm_shape, torch.float32),
+                               ("conv_state_out", conv_state_out, conv_shape, xt), ("ssm_state_out", ssm_state_out, ssm_shape, torch.float32)):
+        if t is not None and not _is(t, shape, dt, dev):
+            raise (TypeError if t.dtype is not dt else ValueError)(
+                f"{name} must be a contiguous {dt} tensor of shape {shape} on x's device, got {t.dtype} {tuple(t.shape)}")
+    w_x, w_dt = _taken(w_x, "w_x", (rank + 2 * dstate, dim), xt, dev), _taken(w_dt, "w_dt", (dim, rank), xt, dev)
     if z is not None:
         z = _inner(_same(z, x, "z"))
-    x, w_x, w_dt = _inner(x), w_x.contiguous(), w_dt.contiguous()
-    conv_w, conv_b = _f32(conv_w, "conv_w", (dim, width), x), _f32(conv_b, "conv_b", (dim,), x)
-    dt_bias, A, D = _f32(dt_bias, "dt_bias", (dim,), x), _f32(A, "A", (dim, dstate), x), _f32(D, "D", (dim,), x)
-    y = x.new_empty((batch, dim), dtype=torch.float32)
-    shape = StepShape(batch, dim, dstate, rank, width)
-    n = lib.mamba_block_step_workspace_bytes(shape)
-    ws = _workspace(n, "mamba_block_step_workspace_bytes", x)
+    x = _inner(x)
+    conv_w, conv_b = _param(conv_w, "conv_w", (dim, width), x, dev), _param(conv_b, "conv_b", per_dim, x, dev)
+    dt_bias, A, D = _param(dt_bias, "dt_bias", per_dim, x, dev), _param(A, "A", (dim, dstate), x, dev), _param(D, "D", per_dim, x, dev)
+    shape, n = _step_size(batch, dim, dstate, rank, width)
+    y, ws = x.new_empty((batch, dim), dtype=torch.float32), _workspace(n, "mamba_block_step_workspace_bytes", x)
     ptrs = StepPtrs(x.data_ptr(), _ptr(z), conv_state.data_ptr(), ssm_state.data_ptr(), conv_w.data_ptr(), _ptr(conv_b),
-                    w_x.data_ptr(), w_dt.data_ptr(), _ptr(dt_bias), A.data_ptr(), _ptr(D), conv_out.data_ptr(),
-                    ssm_out.data_ptr(), y.data_ptr(), _row_stride(x), 0 if z is None else _row_stride(z), _ptr(ws), n)
-    _launch("mamba_block_step", x, lib.mamba_block_step, ptrs, shape, dtype)
+                    w_x.data_ptr(), w_dt.data_ptr(), _ptr(dt_bias), A.data_ptr(), _ptr(D),
+                    (conv_state if conv_state_out is None else conv_state_out).data_ptr(),
+                    (ssm_state if ssm_state_out is None else ssm_state_out).data_ptr(), y.data_ptr(), _row_stride(x),
+                    0 if z is None else _row_stride(z), _ptr(ws), n)
+    _launch("mamba_block_step", x, _load().mamba_block_step, ptrs, shape, dtype)
     return y
 
 

@@ -20,7 +20,7 @@ namespace mscan {
 namespace {
 
 constexpr int kCh = 64;       // channels of a workgroup, in either launch
-constexpr int kRows = 16;     // streams of a workgroup of the first launch
+constexpr int kRows = 8;      // streams of a workgroup of the first launch
 constexpr int kThreads = 256;
 constexpr int kMaxJ = 512 + 2 * 256;
 
@@ -55,6 +55,8 @@ __device__ __forceinline__ float quad_sum(float v) { return quad_add<0x4e>(quad_
 // Over 8 lanes: the quads' sums, then the half row mirrored.
 __device__ __forceinline__ float oct_sum(float v) { return quad_add<0x141>(quad_sum(v)); }
 
+// (Loads of rows, streams and channels past the end repeat the last one: without a branch around them they are all
+// on their way before the first is used.)
 template <typename S, int W>
 __global__ __launch_bounds__(kThreads) void step_conv_kernel(StepArgs p) {
     __shared__ __align__(16) float us[kRows][kCh];
@@ -63,106 +65,119 @@ __global__ __launch_bounds__(kThreads) void step_conv_kernel(StepArgs p) {
     const int64_t b0 = (int64_t)(blockIdx.x / p.chunks) * kRows, c0 = (int64_t)chunk * kCh;
     const int rows = (int)(p.batch - b0 < kRows ? p.batch - b0 : kRows);
 
-    // the first rows of w_x are on their way while u is computed
+    // 8 lanes a row of w_x, 8 channels each; its first rows are on their way while u is computed
     const int part = tid & 7, j0 = tid >> 3;
     const int n = (int)(p.dim - c0 < kCh ? p.dim - c0 : kCh) - part * 8;
     const S* wx = static_cast<const S*>(p.w_x) + c0 + part * 8;
-    constexpr int AHEAD = 3;  // rounds of 32 rows: 96 rows, more than dt_rank 48 and 16 states need
+    constexpr int AHEAD = 3;  // rounds of 32 rows: more than dt_rank 48 and 16 states need
     Pack<S, 8> w[AHEAD];
 #pragma unroll
-    for (int r = 0; r < AHEAD; ++r) {
-        const int j = j0 + 32 * r;
-        w[r] = load_some<S, 8>(wx + (int64_t)(j < p.J ? j : 0) * p.dim, j < p.J ? n : 0);
-    }
+    for (int r = 0; r < AHEAD; ++r) w[r] = load_some<S, 8>(wx + (int64_t)(j0 + 32 * r < p.J ? j0 + 32 * r : p.J - 1) * p.dim, n);
 
-    const int64_t c = c0 + (tid & (kCh - 1));
-    float cw[W], cb = 0.0f;
-    if (c < p.dim) {
+    constexpr int PER = kRows * kCh / kThreads;  // streams of a thread
+    const bool in = c0 + (tid & (kCh - 1)) < p.dim;
+    const int64_t c = in ? c0 + (tid & (kCh - 1)) : p.dim - 1;
+    float cw[W];
 #pragma unroll
-        for (int k = 0; k < W; ++k) cw[k] = p.conv_w[c * W + k];
-        cb = p.conv_b ? p.conv_b[c] : 0.0f;
+    for (int k = 0; k < W; ++k) cw[k] = p.conv_w[c * W + k];
+    const float cb = p.conv_b ? p.conv_b[c] : 0.0f;
+    S v[PER][W];
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        const int row = r * (kThreads / kCh) + tid / kCh;
+        const int64_t b = b0 + (row < rows ? row : rows - 1);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) v[r][k] = static_cast<const S*>(p.conv_state)[(b * (W - 1) + k) * p.dim + c];
+        v[r][W - 1] = static_cast<const S*>(p.x)[b * p.sx + c];
     }
 #pragma unroll
-    for (int r = 0; r < kRows * kCh / kThreads; ++r) {
-        const int row = r * (kThreads / kCh) + (tid / kCh);
-        float u = 0.0f;
-        if (row < rows && c < p.dim) {
-            const int64_t b = b0 + row;
-            const S x = static_cast<const S*>(p.x)[b * p.sx + c];
-            const S* st = static_cast<const S*>(p.conv_state) + b * (W - 1) * p.dim + c;
-            S v[W];
+    for (int r = 0; r < PER; ++r) {
+        const int row = r * (kThreads / kCh) + tid / kCh;
+        const int64_t b = b0 + row;
+        float u = cb;
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) v[k] = st[k * p.dim];
-            v[W - 1] = x;
-            float pre = cb;
+        for (int k = 0; k < W; ++k) u = __builtin_fmaf(cw[k], to_f32(v[r][k]), u);
+        u = silu_f(u);
+        us[row][tid & (kCh - 1)] = in ? u : 0.0f;
+        if (in && row < rows) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) pre = __builtin_fmaf(cw[k], to_f32(v[k]), pre);
-            u = silu_f(pre);
-            S* to = static_cast<S*>(p.conv_out) + b * (W - 1) * p.dim + c;
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) to[k * p.dim] = v[k + 1];
+            for (int k = 0; k < W - 1; ++k) static_cast<S*>(p.conv_out)[(b * (W - 1) + k) * p.dim + c] = v[r][k + 1];
             p.u[b * p.dim + c] = u;
         }
-        us[row][tid & (kCh - 1)] = u;
     }
     __syncthreads();
-    auto share = [&](const Pack<S, 8>& wr, int j) __attribute__((always_inline)) {
-        float f[8];
+    float u[kRows][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = to_f32(wr.v[k]);
-        for (int row = 0; row < rows; ++row) {
+    for (int row = 0; row < kRows; ++row)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[row][k] = us[row][part * 8 + k];
+    // a row's share for every stream: the 8 lanes' sums, each lane storing one stream's
+    auto share = [&](const Pack<S, 8>& wr, int j) __attribute__((always_inline)) {
+        float mine = 0.0f;
+#pragma unroll
+        for (int row = 0; row < kRows; ++row) {
             float s = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s = __builtin_fmaf(f[k], us[row][part * 8 + k], s);
+            for (int k = 0; k < 8; ++k) s = __builtin_fmaf(to_f32(wr.v[k]), u[row][k], s);
             s = oct_sum(s);
-            if (part == 0 && j < p.J) p.part[((int64_t)chunk * p.batch + b0 + row) * p.J + j] = s;
+            mine = part == row ? s : mine;
         }
+        if (part < rows && j < p.J) p.part[((int64_t)chunk * p.batch + b0 + part) * p.J + j] = mine;
     };
 #pragma unroll
     for (int r = 0; r < AHEAD; ++r)
         if (32 * r < p.J) share(w[r], j0 + 32 * r);
     for (int j = j0 + 32 * AHEAD; j - j0 < p.J; j += 32)
-        share(load_some<S, 8>(wx + (int64_t)(j < p.J ? j : 0) * p.dim, j < p.J ? n : 0), j);
+        share(load_some<S, 8>(wx + (int64_t)(j < p.J ? j : p.J - 1) * p.dim, n), j);
 }
 
-// ONE: at most 16 states, held in registers from the start.
-template <typename S, bool ONE>
+// WHOLE: 16 states and a multiple of 4 dt rows, held in registers from the start.
+template <typename S, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
     __shared__ __align__(16) float sums[kThreads], xd[kMaxJ];
     const int tid = threadIdx.x, q = tid & 3;
     const int64_t b = blockIdx.x / p.chunks, d0 = (int64_t)(blockIdx.x % p.chunks) * kCh;
     const bool valid = d0 + (tid >> 2) < p.dim;
     const int64_t d = valid ? d0 + (tid >> 2) : p.dim - 1;
-    const int N = p.dstate, R = p.rank, J = p.J;
-
-    // what does not wait for the projection
-    const float* h = p.h + (b * p.dim + d) * N;
-    const float* A = p.A + d * N;
-    Pack<float, 4> h0{}, a0{};
-    if constexpr (ONE) {
-        h0 = load_some<float, 4>(h + q * 4, N - q * 4);
-        a0 = load_some<float, 4>(A + q * 4, N - q * 4);
-    }
-    const S* wd = static_cast<const S*>(p.w_dt) + d * R;
-    constexpr int AHEAD = 4;  // 64 dt rows
-    Pack<S, 4> w[AHEAD];
-#pragma unroll
-    for (int r = 0; r < AHEAD; ++r) w[r] = load_some<S, 4>(wd + r * 16 + q * 4, R - r * 16 - q * 4);
-    const float u = p.u[b * p.dim + d];
-    const float z = p.z ? to_f32(static_cast<const S*>(p.z)[b * p.sz + d]) : 0.0f;
-    const float bias = p.dt_bias ? p.dt_bias[d] : 0.0f, skip = p.D ? p.D[d] : 0.0f;
+    const int N = WHOLE ? 16 : p.dstate, R = p.rank, J = p.J;
 
     // the chunks' shares of row j: `ways` stretches of the chunks side by side, added in order
     const float* part = p.part + b * J;
     const int64_t next = p.batch * J;
-    if (J <= kThreads) {
-        const int ways = kThreads / J, way = tid / J, j = tid - way * J;
-        const int per = (p.chunks + ways - 1) / ways, k1 = (way + 1) * per < p.chunks ? (way + 1) * per : p.chunks;
+    const int ways = J <= kThreads ? kThreads / J : 1, per = (p.chunks + ways - 1) / ways;
+    auto stretch = [&](int j, int way) __attribute__((always_inline)) {
+        const int k0 = way * per, k1 = k0 + per < p.chunks ? k0 + per : p.chunks;
         float s = 0.0f;
-        if (way < ways) {
-#pragma unroll 8
-            for (int k = way * per; k < k1; ++k) s += part[k * next + j];
+        for (int k = k0; k < k1; k += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = part[(k + i < k1 ? k + i : k1 - 1) * next + j];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += k + i < k1 ? v[i] : 0.0f;
         }
+        return s;
+    };
+
+    // what does not wait for the projection
+    const float* h = p.h + (b * p.dim + d) * N;
+    const float* A = p.A + d * N;
+    const S* wd = static_cast<const S*>(p.w_dt) + d * R;
+    constexpr int AHEAD = 4;  // 64 dt rows
+    Pack<float, 4> h0{}, a0{};
+    Pack<S, 4> w[AHEAD];
+    if constexpr (WHOLE) {
+        __builtin_memcpy(&h0, h + q * 4, 16);
+        __builtin_memcpy(&a0, A + q * 4, 16);
+#pragma unroll
+        for (int r = 0; r < AHEAD; ++r) __builtin_memcpy(&w[r], wd + (r * 16 + q * 4 < R ? r * 16 + q * 4 : 0), sizeof(w[r]));
+    }
+    const float u = p.u[b * p.dim + d];
+    const float z = p.z ? to_f32(static_cast<const S*>(p.z)[b * p.sz + d]) : 0.0f;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.0f, skip = p.D ? p.D[d] : 0.0f;
+
+    if (J <= kThreads) {
+        const int way = tid / J, j = tid - way * J;
+        float s = way < ways ? stretch(j, way) : 0.0f;
         sums[tid] = s;
         __syncthreads();
         if (tid < J) {
@@ -170,12 +185,7 @@ __global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
             xd[tid] = s;
         }
     } else {
-        for (int j = tid; j < J; j += kThreads) {
-            float s = 0.0f;
-#pragma unroll 8
-            for (int k = 0; k < p.chunks; ++k) s += part[k * next + j];
-            xd[j] = s;
-        }
+        for (int j = tid; j < J; j += kThreads) xd[j] = stretch(j, 0);
     }
     __syncthreads();
 
@@ -185,9 +195,12 @@ __global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
         for (int k = 0; k < 4; ++k)
             if (r + k < R) delta = __builtin_fmaf(to_f32(wr.v[k]), xd[r + k], delta);
     };
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int r = 0; r < AHEAD; ++r) dot(w[r], r * 16 + q * 4);
-    for (int r = AHEAD * 16 + q * 4; r < R; r += 16) dot(load_some<S, 4>(wd + r, R - r), r);
+        for (int r = 0; r < AHEAD; ++r) dot(w[r], r * 16 + q * 4);
+    }
+#pragma unroll 2
+    for (int r = (WHOLE ? AHEAD * 16 : 0) + q * 4; r < R; r += 16) dot(load_some<S, 4>(wd + r, R - r), r);
     const float s = softplus_f(quad_sum(delta) + bias), su = s * u;
 
     float* ho = p.h_out + (b * p.dim + d) * N;
@@ -202,7 +215,7 @@ __global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
             }
         if (valid) store_some<float, 4>(ho + n0, r, N - n0);
     };
-    if constexpr (ONE) {
+    if constexpr (WHOLE) {
         states(h0, a0, q * 4);
     } else {
 #pragma unroll 4
@@ -233,7 +246,7 @@ int launch_block_step(const mamba_step_ptrs& p, const mamba_step_shape& s, bool 
         if (s.width == 2) on(step_conv_kernel<S, 2>, first, block, q);
         else if (s.width == 3) on(step_conv_kernel<S, 3>, first, block, q);
         else on(step_conv_kernel<S, 4>, first, block, q);
-        if (s.dstate <= 16) on(step_scan_kernel<S, true>, second, block, q);
+        if (s.dstate == 16 && s.dt_rank % 4 == 0) on(step_scan_kernel<S, true>, second, block, q);
         else on(step_scan_kernel<S, false>, second, block, q);
     };
     bf16 ? go(bf16_t{}) : go(0.0f);

@@ -6,8 +6,8 @@
 // With n = v rstd and g the gradient that reaches n: dv = rstd (g - n mean(g n)), dweight = sum_rows dy n (times
 // the gate where it comes last).
 //
-// A row (or one of its groups) is held in registers by WPR waves, NV packs of V values a lane, so it is read
-// once; the next row's loads are in flight while a row is worked on. Bound by HBM. The backward keeps the
+// A row (or one of its groups) is held in registers by LPR lanes, an eighth of a wave to 16 waves, NV packs of V
+// values a lane, so it is read once; the next row's loads are in flight while a row is worked on. Bound by HBM. The backward keeps the
 // weight's column sums in registers over a workgroup's rows and writes one row of partial sums a workgroup,
 // which a second kernel adds in order.
 #include "block_launch.hpp"
@@ -56,17 +56,39 @@ __device__ __forceinline__ float normed(float x, float other, float scale) {
     return x;
 }
 
+// Sum over the LPR lanes of a row, the same bits in each.
+template <int CTRL>
+__device__ __forceinline__ float lanes_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <int LPR, int WAVES>
+__device__ __forceinline__ float lanes_sum(float v, float (*lds)[2][WAVES], int slot, int wave) {
+    if constexpr (LPR >= 64) {
+        float s[2] = {v, 0.0f};
+        row_sum<1, LPR / 64, WAVES>(s, lds, slot, wave);
+        return s[0];
+    } else {
+        v = lanes_add<0xb1>(v);   // lanes 1 and 0, 3 and 2
+        v = lanes_add<0x4e>(v);   // pairs of a quad
+        v = lanes_add<0x141>(v);  // quads of 8 lanes (half row mirrored)
+        if constexpr (LPR >= 16) v = lanes_add<0x140>(v);  // halves of 16 (row mirrored)
+        if constexpr (LPR >= 32) v += __shfl_xor(v, 16);
+        return v;
+    }
+}
+constexpr int waves_of(int lpr) { return lpr > 64 ? lpr / 64 : 1; }
+
 constexpr int kFwdWaves = 4;  // waves of a forward workgroup, unless a row takes more
 
-template <typename S, int V, int NV, int WPR, int MODE>
-__global__ __launch_bounds__(64 * (WPR > kFwdWaves ? WPR : kFwdWaves)) void rms_fwd_kernel(RmsArgs p) {
-    constexpr int WAVES = WPR > kFwdWaves ? WPR : kFwdWaves, RPB = WAVES / WPR;
+template <typename S, int V, int NV, int LPR, int MODE>
+__global__ __launch_bounds__(64 * (waves_of(LPR) > kFwdWaves ? waves_of(LPR) : kFwdWaves)) void rms_fwd_kernel(RmsArgs p) {
+    constexpr int WAVES = waves_of(LPR) > kFwdWaves ? waves_of(LPR) : kFwdWaves, RPB = WAVES * 64 / LPR;
     __shared__ float lds[2][2][WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane_row = (int)threadIdx.x - wave / WPR * WPR * 64;
+    const int sub = LPR < 64 ? (int)threadIdx.x / LPR : wave / waves_of(LPR), lane_row = (int)threadIdx.x - sub * LPR;
     const int64_t group = blockIdx.x % p.groups, block = blockIdx.x / p.groups, c0 = group * p.dim;
     const int64_t step = p.blocks * RPB;
-    int64_t row = block * RPB + wave / WPR;
+    int64_t row = block * RPB + sub;
     using P = Pack<S, V>;
     P nx[NV], no[NV];
     auto fetch = [&](int64_t r) __attribute__((always_inline)) {
@@ -74,7 +96,7 @@ __global__ __launch_bounds__(64 * (WPR > kFwdWaves ? WPR : kFwdWaves)) void rms_
         const S* o = static_cast<const S*>(p.other) + r * p.so + c0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V;
+            const int64_t c = (int64_t)(k * LPR + lane_row) * V;
             nx[k] = load_some<S, V>(x + c, (int)(p.dim - c));
             if constexpr (MODE != kPlain) no[k] = load_some<S, V>(o + c, (int)(p.dim - c));
         }
@@ -85,7 +107,7 @@ __global__ __launch_bounds__(64 * (WPR > kFwdWaves ? WPR : kFwdWaves)) void rms_
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V + j;
+            const int64_t c = (int64_t)(k * LPR + lane_row) * V + j;
             w[k][j] = p.w && c < p.dim ? p.w[c0 + c] : 1.0f;
         }
     const float inv = 1.0f / (float)p.dim;
@@ -94,10 +116,10 @@ __global__ __launch_bounds__(64 * (WPR > kFwdWaves ? WPR : kFwdWaves)) void rms_
     for (int64_t base = block * RPB; base < p.rows; base += step, row += step) {
         const bool on = row < p.rows;
         float t[NV][V], gate[MODE == kGateLast ? NV : 1][V];
-        float s[2] = {0.0f, 0.0f};
+        float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V;
+            const int64_t c = (int64_t)(k * LPR + lane_row) * V;
             P st;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -106,18 +128,18 @@ __global__ __launch_bounds__(64 * (WPR > kFwdWaves ? WPR : kFwdWaves)) void rms_
                 if constexpr (MODE == kResidual) st.v[j] = from_f32<S>(v);
                 if constexpr (MODE == kGateLast) gate[k][j] = silu_f(other);
                 t[k][j] = v;
-                s[0] = __builtin_fmaf(v, v, s[0]);
+                s = __builtin_fmaf(v, v, s);
             }
             if (MODE == kResidual && on) store_some<S, V>(static_cast<S*>(p.sum) + row * p.ssum + c0 + c, st, (int)(p.dim - c));
         }
         if (row + step < p.rows) fetch(row + step);
-        row_sum<1, WPR, WAVES>(s, lds, slot, wave);
+        s = lanes_sum<LPR, WAVES>(s, lds, slot, wave);
         slot ^= 1;
-        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], inv, p.eps));
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv, p.eps));
         if (on) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V;
+                const int64_t c = (int64_t)(k * LPR + lane_row) * V;
                 P o;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -166,6 +188,7 @@ constexpr int kBwdWaves = 16;
 template <int MODE>
 struct RmsTerm {
     float n, g, dw, gate, slope;
+    RmsTerm() = default;
     __device__ __forceinline__ RmsTerm(float x, float dy, float z, float w, float rstd) {
         gate = 1.0f, slope = 0.0f;
         if constexpr (MODE == kGateFirst || MODE == kGateLast) {
@@ -188,15 +211,14 @@ __device__ __forceinline__ void rms_out(const RmsTerm<MODE>& t, float dv, float 
 }
 
 // MODE kResidual stands for the plain norm too (dsum may be NULL, dresidual is not written).
-template <typename S, int V, int NV, int WPR, int MODE>
+template <typename S, int V, int NV, int LPR, int MODE>
 __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
-    constexpr int RPB = kBwdWaves / WPR;
+    constexpr int RPB = kBwdWaves * 64 / LPR;
     constexpr bool GATED = MODE != kResidual;
     __shared__ float lds[2][2][kBwdWaves];
-    __shared__ float cols[RPB > 1 ? 64 * WPR * NV * V : 1];
+    __shared__ float cols[RPB > 1 ? LPR * NV * V : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int sub = wave / WPR;
-    const int lane_row = (int)threadIdx.x - sub * WPR * 64;
+    const int sub = LPR < 64 ? (int)threadIdx.x / LPR : wave / waves_of(LPR), lane_row = (int)threadIdx.x - sub * LPR;
     const int64_t group = blockIdx.x % p.groups, block = blockIdx.x / p.groups, c0 = group * p.dim;
     const int64_t step = p.blocks * RPB;
     int64_t row = block * RPB + sub;
@@ -210,7 +232,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
         const S* o = static_cast<const S*>(p.other) + r * p.so + c0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V;
+            const int64_t c = (int64_t)(k * LPR + lane_row) * V;
             const int n = (int)(p.dim - c);
             nv[k] = load_some<S, V>(v + c, n);
             ng[k] = load_some<S, V>(g + c, n);
@@ -224,7 +246,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V + j;
+            const int64_t c = (int64_t)(k * LPR + lane_row) * V + j;
             w[k][j] = p.w && c < p.dim ? p.w[c0 + c] : 1.0f;
             dw[k][j] = 0.0f;
         }
@@ -233,7 +255,8 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
     for (int64_t base = block * RPB; base < p.rows; base += step, row += step) {
         const bool on = row < p.rows;
         P v[NV], g[NV], o[NV];
-        float s[2] = {0.0f, 0.0f};
+        RmsTerm<MODE> terms[NV][V];  // (gates and slopes are not computed twice: 96 us a pass at 16384 x 1536 gated, 110)
+        float s = 0.0f;
         const float rstd = nrstd;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -242,24 +265,25 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const RmsTerm<MODE> t(to_f32(v[k].v[j]), to_f32(g[k].v[j]), GATED ? to_f32(o[k].v[j]) : 0.0f, w[k][j], rstd);
+                    terms[k][j] = t;
                     dw[k][j] += t.dw;
-                    s[0] = __builtin_fmaf(t.g, t.n, s[0]);
+                    s = __builtin_fmaf(t.g, t.n, s);
                 }
             }
         }
         if (row + step < p.rows) fetch(row + step);
-        row_sum<1, WPR, kBwdWaves>(s, lds, slot, wave);
+        s = lanes_sum<LPR, kBwdWaves>(s, lds, slot, wave);
         slot ^= 1;
         if (on) {
-            const float m = s[0] * inv;
+            const float m = s * inv;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V;
+                const int64_t c = (int64_t)(k * LPR + lane_row) * V;
                 P a, b;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float x = to_f32(v[k].v[j]), dy = to_f32(g[k].v[j]), z = more ? to_f32(o[k].v[j]) : 0.0f;
-                    const RmsTerm<MODE> t(x, dy, z, w[k][j], rstd);
+                    const RmsTerm<MODE>& t = terms[k][j];
                     float dv = rstd * __builtin_fmaf(-t.n, m, t.g), ra, rb;
                     if constexpr (!GATED) dv += z;
                     rms_out<MODE>(t, dv, x, dy, w[k][j], p.scale, ra, rb);
@@ -272,15 +296,25 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
     }
     if (!p.part) return;
     float* out = p.part + block * p.dim * p.groups + c0;
-    // the row groups' column sums, added in their order
+    // the column sums of a wave's rows, of two lanes at a time, then of the rows that waves share, in their order
+    if constexpr (LPR < 64) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int far = LPR; far < 64; far *= 2) dw[k][j] += __shfl_xor(dw[k][j], far);
+    }
     if constexpr (RPB > 1) {
-        for (int q = 0; q < RPB; ++q) {
-            if (sub == q) {
+        constexpr int TURNS = LPR < 64 ? kBwdWaves : RPB;
+        const int turn = LPR < 64 ? (int)(threadIdx.x & 63) < LPR ? wave : -1 : sub;
+        for (int q = 0; q < TURNS; ++q) {
+            if (turn == q) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        float* a = &cols[(k * 64 * WPR + lane_row) * V + j];
+                        float* a = &cols[(k * LPR + lane_row) * V + j];
                         *a = q ? *a + dw[k][j] : dw[k][j];
                     }
             }
@@ -292,7 +326,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void rms_bwd_kernel(RmsBwdArgs p) {
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int64_t c = (int64_t)(k * 64 * WPR + lane_row) * V + j;
+                const int64_t c = (int64_t)(k * LPR + lane_row) * V + j;
                 if (c < p.dim) out[c] = dw[k][j];
             }
     }
@@ -367,25 +401,27 @@ __global__ __launch_bounds__(256) void rms_cols_kernel(const float* part, int bl
 // Values of a row a lane holds, few so that many rows are in flight; 16 waves have the registers for 16 and, in
 // the backward, 8 (wider rows are read twice).
 constexpr int kFwdVals = 16, kBwdVals = 8;
-constexpr int kFwdWavesPerCu = 16;
+constexpr int fwd_waves_per_cu(int wpr) { return wpr == 1 ? 16 : 32; }
 constexpr int64_t kBwdBlocks = 256;  // of 16 waves; their partial column sums are written and read once more
 
 int64_t at_least_1(int64_t n) { return n < 1 ? 1 : n; }
 
-// Calls f(values of a pack, packs a lane, waves a row) for rows of `dim` values, or `wide` where they do not fit.
-// Packs are 16 bytes wherever the rows begin; rows that would leave most of a wave idle take packs of 2.
+// Calls f(packs a lane, lanes a row) for rows of `dim` values, or `wide` where they do not fit. Packs are 16 bytes
+// wherever the rows begin; rows of less than half a wave's packs share a wave (50000 x 512 bf16 in groups of 64,
+// gated, forward and backward: 95 us; a wave a group 383).
 template <typename S, int VALS, typename F, typename W>
 auto with_layout(int64_t dim, F&& f, W&& wide) {
-    constexpr int V = 16 / sizeof(S), most = VALS / V;
-    if (dim <= 32 * V)
-        return with_packs<V / 4>((dim + 127) / 128, [&](auto nv) { return f(std::integral_constant<int, 2>{}, nv, std::integral_constant<int, 1>{}); });
-    auto go = [&](auto waves) {
-        constexpr int W1 = 64 * decltype(waves)::value * V;
-        return with_packs<most>((dim + W1 - 1) / W1, [&](auto nv) { return f(std::integral_constant<int, V>{}, nv, waves); });
+    constexpr int V = 16 / sizeof(S);
+    auto go = [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        return with_packs<(L < 64 ? 1 : VALS / V)>((dim + L * V - 1) / (L * V), [&](auto nv) { return f(nv, lanes); });
     };
-    if (dim <= 64 * VALS) return go(std::integral_constant<int, 1>{});
-    if (dim <= 256 * VALS) return go(std::integral_constant<int, 4>{});
-    if (dim <= 1024 * VALS) return go(std::integral_constant<int, 16>{});
+    if (dim <= 8 * V) return go(std::integral_constant<int, 8>{});
+    if (dim <= 16 * V) return go(std::integral_constant<int, 16>{});
+    if (dim <= 32 * V) return go(std::integral_constant<int, 32>{});
+    if (dim <= 64 * VALS) return go(std::integral_constant<int, 64>{});
+    if (dim <= 256 * VALS) return go(std::integral_constant<int, 256>{});
+    if (dim <= 1024 * VALS) return go(std::integral_constant<int, 1024>{});
     return wide();
 }
 
@@ -393,12 +429,13 @@ template <typename S, int MODE>
 void fwd_typed(RmsArgs q, Launches& on) {
     with_layout<S, kFwdVals>(
         q.dim,
-        [&](auto v, auto nv, auto wpr) {
-            constexpr int WPR = decltype(wpr)::value, WAVES = WPR > kFwdWaves ? WPR : kFwdWaves, RPB = WAVES / WPR;
+        [&](auto nv, auto lanes) {
+            constexpr int LPR = decltype(lanes)::value, WPR = waves_of(LPR), WAVES = WPR > kFwdWaves ? WPR : kFwdWaves;
+            constexpr int RPB = WAVES * 64 / LPR;
             const int64_t need = (q.rows + RPB - 1) / RPB;
-            const int64_t most = at_least_1((int64_t)layers_cus() * kFwdWavesPerCu / WAVES / q.groups);
+            const int64_t most = at_least_1((int64_t)layers_cus() * fwd_waves_per_cu(WPR) / WAVES / q.groups);
             q.blocks = need < most ? need : most;
-            on(rms_fwd_kernel<S, decltype(v)::value, decltype(nv)::value, WPR, MODE>, dim3((unsigned)(q.blocks * q.groups)),
+            on(rms_fwd_kernel<S, 16 / sizeof(S), decltype(nv)::value, LPR, MODE>, dim3((unsigned)(q.blocks * q.groups)),
                dim3(64 * WAVES), q);
         },
         [&] { on(rms_fwd_wide_kernel<S, MODE>, grid_of(q.rows * q.groups, 1024), dim3(1024), q); });
@@ -408,11 +445,11 @@ template <typename S, int MODE>
 int64_t bwd_typed(RmsBwdArgs q, Launches& on) {
     return with_layout<S, kBwdVals>(
         q.dim,
-        [&](auto v, auto nv, auto wpr) {
-            constexpr int WPR = decltype(wpr)::value, RPB = kBwdWaves / WPR;
+        [&](auto nv, auto lanes) {
+            constexpr int LPR = decltype(lanes)::value, RPB = kBwdWaves * 64 / LPR;
             const int64_t need = (q.rows + RPB - 1) / RPB, most = at_least_1(kBwdBlocks / q.groups);
             q.blocks = need < most ? need : most;
-            on(rms_bwd_kernel<S, decltype(v)::value, decltype(nv)::value, WPR, MODE>, dim3((unsigned)(q.blocks * q.groups)),
+            on(rms_bwd_kernel<S, 16 / sizeof(S), decltype(nv)::value, LPR, MODE>, dim3((unsigned)(q.blocks * q.groups)),
                dim3(64 * kBwdWaves), q);
             return q.blocks;
         },

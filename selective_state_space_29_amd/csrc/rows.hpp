@@ -35,12 +35,13 @@ __device__ __forceinline__ void row_sum(float (&v)[2], float (*lds)[2][WAVES], i
 // n of V consecutive values (all of them in one access of any alignment), zeros behind them.
 template <typename S, int V>
 __device__ __forceinline__ Pack<S, V> load_some(const S* p, int n) {
-    Pack<S, V> r;
+    Pack<S, V> r{};
     if (n >= V) {
         __builtin_memcpy(&r, p, sizeof(r));
-    } else {
+    } else if (n > 0) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) r.v[k] = k < n ? p[k] : S{};
+        for (int k = 0; k < V; ++k)
+            if (k < n) r.v[k] = p[k];
     }
     return r;
 }
@@ -48,7 +49,7 @@ template <typename S, int V>
 __device__ __forceinline__ void store_some(S* p, const Pack<S, V>& r, int n) {
     if (n >= V) {
         __builtin_memcpy(p, &r, sizeof(r));
-    } else {
+    } else if (n > 0) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
             if (k < n) p[k] = r.v[k];
