@@ -95,6 +95,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ float half_f32(uint32_t w, int k) { return __uint_as_float(k ? w & 0xFFFF0000u : w << 16); }
 
+// Two pairs {maximum, sum of powers of 2 from it} as one. A maximum drops a NaN, but the sum keeps it.
+__device__ __forceinline__ float2 join_pair(float2 a, float2 b) {
+    const float top = __builtin_fmaxf(a.x, b.x);
+    const float fa = a.x == top ? a.y : a.y * hw_exp2(a.x - top), fb = b.x == top ? b.y : b.y * hw_exp2(b.x - top);
+    return make_float2(top, fa + fb);
+}
+
 // Where chunk `c` (8 values) of row `row` lies in its LDS row: rows of 64 c (8 chunks, 128 bytes), of which
 // 16 lanes read the same chunk of 16 rows, or of T values of a c (tr), where the 8 rows that a half wave's
 // transposing read touches take 8 distinct pairs of chunks.
@@ -321,11 +328,6 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
         static_assert(WQ * TP * 8 <= STAGES * 2);
         const float s2 = m.scale * kLog2e;
         const bool whole = q0 + TQ <= m.Q;
-        auto join = [](float2 a, float2 b) {
-            const float top = __builtin_fmaxf(a.x, b.x);
-            const float fa = a.x == top ? a.y : a.y * hw_exp2(a.x - top), fb = b.x == top ? b.y : b.y * hw_exp2(b.x - top);
-            return make_float2(top, fa + fb);
-        };
         __syncthreads();  // every wave has read its last fragments
 #pragma unroll
         for (int p = 0; p < PT; ++p) {
@@ -357,15 +359,15 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
             for (int q = 0; q < QT; ++q)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r.y += hw_exp2(acc[q][p][j] - base);
-            r = join(r, make_float2(__shfl_xor(r.x, 16), __shfl_xor(r.y, 16)));
-            r = join(r, make_float2(__shfl_xor(r.x, 32), __shfl_xor(r.y, 32)));
+            r = join_pair(r, make_float2(__shfl_xor(r.x, 16), __shfl_xor(r.y, 16)));
+            r = join_pair(r, make_float2(__shfl_xor(r.x, 32), __shfl_xor(r.y, 32)));
             if (lane < 16) sums[wq][p_row(p) + lp] = r;
         }
         __syncthreads();
         if (tid < TP && p0 + tid < m.P) {
             float2 r = sums[0][tid];
 #pragma unroll
-            for (int k = 1; k < WQ; ++k) r = join(r, sums[k][tid]);
+            for (int k = 1; k < WQ; ++k) r = join_pair(r, sums[k][tid]);
             reinterpret_cast<float2*>(m.part)[q0 / TQ * m.P + p0 + tid] = r;
         }
     } else if constexpr (EPI == kEpiPartial || EPI == kEpiAdd) {
