@@ -121,7 +121,7 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
     constexpr int XN = TP * CH / NT, YN = TQ * CH / NT;  // chunks a thread moves per stage
     static_assert(!(DUAL && (XTR || YTR)) && XN >= 1 && YN >= 1 && (!DUAL || QT % 2 == 0));
     constexpr int OQ = DUAL ? TQ / 2 : TQ, PITCH = OQ + 8;  // of the results' rows in LDS, 16 bytes apart in the banks
-    constexpr int STAGES = DEPTH * (TP + TQ) * kTC, RESULTS = EPI == kEpiPartial || EPI == kEpiAdd ? 0 : TP * PITCH;
+    constexpr int STAGES = DEPTH * (TP + TQ) * kTC, RESULTS = EPI == kEpiPartial || EPI == kEpiAdd ? 0 : TP * PITCH + (EPI == kEpiDlogits ? TP * 8 : 0);
     __shared__ __align__(16) uint16_t lds[STAGES > RESULTS ? STAGES : RESULTS];
     uint16_t(&sx)[DEPTH][TP * kTC] = *reinterpret_cast<uint16_t(*)[DEPTH][TP * kTC]>(&lds[0]);
     uint16_t(&sy)[DEPTH][TQ * kTC] = *reinterpret_cast<uint16_t(*)[DEPTH][TQ * kTC]>(&lds[DEPTH * TP * kTC]);
@@ -265,6 +265,16 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
 #pragma unroll
         for (int p = 0; p < PT; ++p) acc[q][p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+    // what the epilogue needs of each row of the tile, a row a thread, on its way while the stages run (loaded by
+    // every lane behind them, the targets cost 5 us of a tile's 26)
+    f32x4 of_row = {0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t target = -1;
+    if constexpr (EPI == kEpiLse || EPI == kEpiDlogits) {
+        const int64_t pr = p0 + tid % TP < m.P ? p0 + tid % TP : m.P - 1;
+        if constexpr (EPI == kEpiDlogits) of_row = *reinterpret_cast<const f32x4*>(m.row + pr * 4);
+        else if (m.target) target = m.target64 ? static_cast<const int64_t*>(m.target)[pr] : static_cast<const int32_t*>(m.target)[pr];
+    }
+
     uint32_t warm = 0;
     if (s_begin < s_end) {
         constexpr int LOADS = XN + YN;  // a stage's
@@ -325,23 +335,23 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
         // the row, over the waves in order. With an infinite maximum the powers are taken as they are: a sum of
         // zeros, infinity or NaN is then the row's.
         float2(*sums)[TP] = reinterpret_cast<float2(*)[TP]>(&lds[0]);
-        static_assert(WQ * TP * 8 <= STAGES * 2);
+        int* rel_of = reinterpret_cast<int*>(&sums[WQ][0]);  // each row's target as a column of this tile, or -1
+        static_assert(WQ * TP * 8 + TP * 4 <= STAGES * 2);
         const float s2 = m.scale * kLog2e;
         const bool whole = q0 + TQ <= m.Q;
         __syncthreads();  // every wave has read its last fragments
+        if (tid < TP) rel_of[tid] = target >= q0 && target < q0 + TQ && target < m.Q && p0 + tid < m.P ? (int)(target - q0) : -1;
+        __syncthreads();
 #pragma unroll
         for (int p = 0; p < PT; ++p) {
             const int64_t pr = p0 + p_row(p) + lp;
-            if (m.target && pr < m.P) {
-                const int64_t t = m.target64 ? static_cast<const int64_t*>(m.target)[pr] : static_cast<const int32_t*>(m.target)[pr];
-                const int64_t rel = t - q0;
-                if (rel >= 0 && rel < TQ && t < m.Q) {
+            const int rel = rel_of[p_row(p) + lp];
+            if (rel >= 0) {
 #pragma unroll
-                    for (int q = 0; q < QT; ++q)
+                for (int q = 0; q < QT; ++q)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (q_row(q) + lq + j == (int)rel) m.at_target[pr] = acc[q][p][j] * m.scale;
-                }
+                    for (int j = 0; j < 4; ++j)
+                        if (q_row(q) + lq + j == rel) m.at_target[pr] = acc[q][p][j] * m.scale;
             }
             float top = -__builtin_inff();
 #pragma unroll
@@ -474,10 +484,13 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
                 // (factor softmax - [target] factor) rounded; a row whose factors are 0 takes no part, whatever its
                 // logits. Columns past Q, up to the padded width that is written, are zeros.
                 const float s2 = m.scale * kLog2e;
+                static_assert(TP * 16 + TP * PITCH * 2 <= (STAGES > RESULTS ? STAGES : RESULTS) * 2);
+                f32x4* rows_of = reinterpret_cast<f32x4*>(&lds[TP * PITCH]);
+                if (tid < TP) rows_of[tid] = of_row;
+                __syncthreads();
 #pragma unroll
                 for (int p = 0; p < PT; ++p) {
-                    const int64_t pr = p0 + p_row(p) + lp;
-                    const f32x4 row = *reinterpret_cast<const f32x4*>(m.row + (pr < m.P ? pr : m.P - 1) * 4);
+                    const f32x4 row = rows_of[p_row(p) + lp];
                     const bool on = row[1] != 0.0f || row[2] != 0.0f;
                     const int64_t rel = (int64_t)__float_as_int(row[3]) - m.q_first - q0;
 #pragma unroll
