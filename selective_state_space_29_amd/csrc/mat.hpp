@@ -331,54 +331,76 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
     // A lane holds q = q0 + q_row(t) + 4 (lane / 16) .. + 3 of p = p0 + p_row(t) + lane % 16.
     const int lq = 4 * (lane >> 4), lp = lane & 15;
     if constexpr (EPI == kEpiLse) {
-        // Maximum and sum of powers of 2 of the tile's columns, of each row: in a lane, over the 4 lanes that share
-        // the row, over the waves in order. With an infinite maximum the powers are taken as they are: a sum of
-        // zeros, infinity or NaN is then the row's.
+        // Maximum and sum of powers of 2 of the tile's columns, of each row: first in each of the 4 WQ lanes that hold
+        // a part of the row, then over them. With an infinite maximum the powers are taken as they are: a sum of
+        // zeros, infinity or NaN is then the row's. (Of a tile's 26 us at dim 768 this takes about 3, VALU instructions,
+        // a third of them the exponentials; with the lanes joined by shuffles it took 5.)
+        constexpr int PARTS = 4 * WQ;
         float2(*sums)[TP] = reinterpret_cast<float2(*)[TP]>(&lds[0]);
-        int* rel_of = reinterpret_cast<int*>(&sums[WQ][0]);  // each row's target as a column of this tile, or -1
-        static_assert(WQ * TP * 8 + TP * 4 <= STAGES * 2);
-        const float s2 = m.scale * kLog2e;
+        int* rel_of = reinterpret_cast<int*>(&sums[PARTS][0]);  // each row's target as a column of this tile, or -1
+        static_assert(PARTS * TP * 8 + TP * 4 <= STAGES * 2 && NT >= TP);
+        float s2 = m.scale * kLog2e;
         const bool whole = q0 + TQ <= m.Q;
+        if (s2 == 0.0f) {  // logits of 0 (or NaN), which a column past the last must not turn into 0 times infinity
+#pragma unroll
+            for (int q = 0; q < QT; ++q)
+#pragma unroll
+                for (int p = 0; p < PT; ++p) acc[q][p] *= s2;
+            s2 = 1.0f;
+        }
         __syncthreads();  // every wave has read its last fragments
         if (tid < TP) rel_of[tid] = target >= q0 && target < q0 + TQ && target < m.Q && p0 + tid < m.P ? (int)(target - q0) : -1;
         __syncthreads();
+        int rel[PT];
+#pragma unroll
+        for (int p = 0; p < PT; ++p) rel[p] = rel_of[p_row(p) + lp];
 #pragma unroll
         for (int p = 0; p < PT; ++p) {
-            const int64_t pr = p0 + p_row(p) + lp;
-            const int rel = rel_of[p_row(p) + lp];
-            if (rel >= 0) {
+            if (rel[p] >= 0) {
 #pragma unroll
                 for (int q = 0; q < QT; ++q)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (q_row(q) + lq + j == rel) m.at_target[pr] = acc[q][p][j] * m.scale;
+                        if (q_row(q) + lq + j == rel[p]) m.at_target[p0 + p_row(p) + lp] = acc[q][p][j] * m.scale;
             }
-            float top = -__builtin_inff();
+            // the largest logit is that of the largest product, or of the smallest where scale is negative
+            if (!whole) {
+                const float none = s2 < 0.0f ? __builtin_inff() : -__builtin_inff();
 #pragma unroll
-            for (int q = 0; q < QT; ++q)
+                for (int q = 0; q < QT; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float v = acc[q][p][j] * s2;
-                    if (!whole) v = q0 + q_row(q) + lq + j < m.Q ? v : -__builtin_inff();
-                    acc[q][p][j] = v;
-                    top = __builtin_fmaxf(top, v);
-                }
+                    for (int j = 0; j < 4; ++j) acc[q][p][j] = q0 + q_row(q) + lq + j < m.Q ? acc[q][p][j] : none;
+            }
+            float top = acc[0][p][0];
+            if (s2 < 0.0f) {
+#pragma unroll
+                for (int q = 0; q < QT; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top = __builtin_fminf(top, acc[q][p][j]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < QT; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, acc[q][p][j]);
+            }
+            top *= s2;
             const float base = __builtin_fabsf(top) == __builtin_inff() ? 0.0f : top;
-            float2 r = make_float2(top, 0.0f);
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < QT; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r.y += hw_exp2(acc[q][p][j] - base);
-            r = join_pair(r, make_float2(__shfl_xor(r.x, 16), __shfl_xor(r.y, 16)));
-            r = join_pair(r, make_float2(__shfl_xor(r.x, 32), __shfl_xor(r.y, 32)));
-            if (lane < 16) sums[wq][p_row(p) + lp] = r;
+                for (int j = 0; j < 4; ++j) s[j] += hw_exp2(__builtin_fmaf(acc[q][p][j], s2, -base));
+            sums[wq * 4 + (lane >> 4)][p_row(p) + lp] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
         }
         __syncthreads();
         if (tid < TP && p0 + tid < m.P) {
-            float2 r = sums[0][tid];
+            float2 r[PARTS];
+            float top = -__builtin_inff(), s = 0.0f;
 #pragma unroll
-            for (int k = 1; k < WQ; ++k) r = join_pair(r, sums[k][tid]);
-            reinterpret_cast<float2*>(m.part)[q0 / TQ * m.P + p0 + tid] = r;
+            for (int k = 0; k < PARTS; ++k) r[k] = sums[k][tid], top = __builtin_fmaxf(top, r[k].x);
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) s += r[k].x == top ? r[k].y : r[k].y * hw_exp2(r[k].x - top);
+            reinterpret_cast<float2*>(m.part)[q0 / TQ * m.P + p0 + tid] = make_float2(top, s);
         }
     } else if constexpr (EPI == kEpiPartial || EPI == kEpiAdd) {
 #pragma unroll

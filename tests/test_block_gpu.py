@@ -462,7 +462,7 @@ def xent_slack(x, w, target, lse, dloss, dlse=None, scale=1.0):
     p = f[:, None] * torch.exp(scale * x @ w.t() - lse[:, None])
     d = p.clone()
     d[torch.arange(len(hit)), target.long().clamp(0, w.shape[0] - 1)] -= a
-    return scale * (2.0 ** -8 * d.abs() + 1e-5 * p.abs())
+    return abs(scale) * (2.0 ** -8 * d.abs() + 1e-5 * p.abs())
 
 
 XENT_SIZES = [(1, 8, 1), (1, 1, 2), (5, 3, 7), (4, 64, 128), (130, 72, 129), (64, 100, 1000), (129, 65, 255), (300, 256, 513), (700, 24, 3001),
@@ -472,6 +472,21 @@ XENT_SIZES = [(1, 8, 1), (1, 1, 2), (5, 3, 7), (4, 64, 128), (130, 72, 129), (64
 @pytest.mark.parametrize("M,K,V", XENT_SIZES)
 def test_cross_entropy(M, K, V):
     check_xent(xent_case(M + K + V, M, K, V, torch.int32 if M % 2 else torch.int64), scale=1.0 if K % 2 else 0.6, dlse=V % 2 == 1)
+
+
+@pytest.mark.parametrize("scale", [-1.3, 0.0, 1e-3])
+def test_cross_entropy_scales(scale):
+    """A negative scale turns the order of the logits, 0 makes them equal; columns that end inside a tile."""
+    for M, K, V in ((5, 24, 77), (140, 40, 300)):
+        t = xent_case(M, M, K, V)
+        if scale == 0.0:
+            d = dev(t)
+            loss, lse = block.linear_cross_entropy_fn(d["x"], d["weight"], d["target"], scale=scale, return_lse=True)
+            close(lse, torch.full((M,), float(V), dtype=torch.float64).log())
+            g = block.linear_cross_entropy_bwd(d["x"], d["weight"], d["target"], lse, d["dloss"], scale=scale)
+            assert not g["x"].any() and not g["weight"].any()
+        else:
+            check_xent(t, scale=scale)
 
 
 def test_cross_entropy_large_tiles_and_pieces():
