@@ -93,6 +93,12 @@ __device__ __forceinline__ void act_grad(float g, int act, float& a, float& da) 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return (uint32_t)to_bf16(lo).bits | (uint32_t)to_bf16(hi).bits << 16;
 }
+// The same in one instruction (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
 __device__ __forceinline__ float half_f32(uint32_t w, int k) { return __uint_as_float(k ? w & 0xFFFF0000u : w << 16); }
 
 // Two pairs {maximum, sum of powers of 2 from it} as one. A maximum drops a NaN, but the sum keeps it.
@@ -504,8 +510,11 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
         } else {
             if constexpr (EPI == kEpiDlogits) {
                 // (factor softmax - [target] factor) rounded; a row whose factors are 0 takes no part, whatever its
-                // logits. Columns past Q, up to the padded width that is written, are zeros.
+                // logits. Columns past Q, up to the padded width that is written, are zeros. The target is seen to
+                // apart, as hardly any lane holds one (a piece of 7168 columns and 16384 rows, the target and the
+                // last column tested at every value 215 us, so 204).
                 const float s2 = m.scale * kLog2e;
+                const bool whole = q0 + TQ <= m.Q;
                 static_assert(TP * 16 + TP * PITCH * 2 <= (STAGES > RESULTS ? STAGES : RESULTS) * 2);
                 f32x4* rows_of = reinterpret_cast<f32x4*>(&lds[TP * PITCH]);
                 if (tid < TP) rows_of[tid] = of_row;
@@ -516,16 +525,30 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
                     const bool on = row[1] != 0.0f || row[2] != 0.0f;
                     const int64_t rel = (int64_t)__float_as_int(row[3]) - m.q_first - q0;
 #pragma unroll
-                    for (int q = 0; q < QT; ++q) {
-                        float h[4];
+                    for (int q = 0; q < QT; ++q)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int col = q_row(q) + lq + j;
-                            float v = row[1] * hw_exp2(__builtin_fmaf(acc[q][p][j], s2, -row[0]));
-                            if (col == rel) v -= row[2];
-                            h[j] = on && q0 + col < m.Q ? v : 0.0f;
-                        }
-                        *reinterpret_cast<uint2*>(place(q, p)) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+                        for (int j = 0; j < 4; ++j) acc[q][p][j] = hw_exp2(__builtin_fmaf(acc[q][p][j], s2, -row[0]));
+                    // (apart from the products: an exponential's result may not be used by the next instruction)
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int q = 0; q < QT; ++q) acc[q][p] *= row[1];
+                    if (rel >= 0 && rel < TQ) {
+#pragma unroll
+                        for (int q = 0; q < QT; ++q)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (q_row(q) + lq + j == (int)rel) acc[q][p][j] -= row[2];
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int q = 0; q < QT; ++q)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[q][p][j] = q0 + q_row(q) + lq + j < m.Q ? acc[q][p][j] : 0.0f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < QT; ++q) {
+                        const uint32_t lo = pack_pair(acc[q][p][0], acc[q][p][1]), hi = pack_pair(acc[q][p][2], acc[q][p][3]);
+                        *reinterpret_cast<uint2*>(place(q, p)) = make_uint2(on ? lo : 0u, on ? hi : 0u);
                     }
                 }
                 __syncthreads();
