@@ -3,18 +3,21 @@
 //   pre_t = bias + sum_{j < W} w_{W-1-j} v_{t-j},   y_t = silu(pre_t)        (tap j reaches j steps back)
 //   dpre_t = dy_t silu'(pre_t);   dv_s = sum_j w_{W-1-j} dpre_{s+j};   dw_{W-1-j} = sum_t dpre_t v_{t-j}
 //
-// A thread computes a run of kRun steps: of one pack of channels where channels lie side by side ("rows"
-// kernels), of one channel where steps do ("steps" kernels, the scan's layout). It loads what the run needs,
-// the W - 1 steps before it (and, in the backward, after it) among them: they are the neighbouring runs' and
-// come from the cache. A tap is dropped where a sequence begins between the value and the step: the leading
-// zeros of the resets' bits up to a step are the number of steps since.
+// Where channels lie side by side ("rows" kernels), a wave takes a run of 32 steps of 128 channels and walks through
+// it with the last W values, and in the backward the W gradients that are not finished, in registers. Where steps do
+// ("steps" kernels, the scan's layout), a thread takes a run of 8 steps of one channel. What a run needs of its
+// neighbours (W - 1 steps before it and, in the backward, behind it) is loaded again, from the cache, or read from the
+// next lane. A tap is dropped where a sequence begins between the value and the step: the number of steps since the
+// last reset is counted along the run, or is the leading zeros of the resets' bits up to a step.
 //
-// Rows in, steps out (a projection's output handed to the scan): the results of 64 channels x the runs of a
-// workgroup pass through LDS in 16-byte pieces whose places are XORed with the channel, so that rows are read
-// and rows are written in whole lines; the backward takes dy the same way.
+// Rows in, steps out (a projection's output handed to the scan): a workgroup's results pass through LDS in 16-byte
+// pieces whose places are XORed with the channel, so that rows are read and rows are written in whole lines; the
+// backward takes dy the same way.
 //
-// Every kernel is bound by HBM: it reads and writes each value once. The weight's gradient is summed in
-// registers over a workgroup's runs, then over its threads in order, and a second kernel adds the workgroups'.
+// Bound by HBM, each value read and written once; the weight's gradient is summed in registers over a workgroup's
+// runs, then over its waves in order, and a second kernel adds the workgroups'. 8 x 2048 x 1536 bf16: forward 21.8 us
+// (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 44.5 + 4.8 (151 MB, 3.4); in the
+// scan's layout 27 and 70. 3 x 2777 x 1001 fp32 in the scan's layout 18 and 28. One step of 32 x 1536: 3.6.
 #include <type_traits>
 
 #include "block_launch.hpp"
@@ -62,12 +65,13 @@ struct ConvBwdArgs {
     int silu;
 };
 
-// The resets of steps t0 - 8 .. t0 + 15 as bits 0 .. 23; steps outside the sequence have none.
+// The resets of steps t0 - 8 .. t0 + kRun + 7 as bits from 0 on; steps outside the sequence have none.
 __device__ __forceinline__ uint32_t reset_bits(const uint8_t* row, int t0, int len) {
+    static_assert(kRun + 16 <= 32);
     uint32_t m = 0;
     if (!row) return m;
 #pragma unroll
-    for (int part = 0; part < 3; ++part) {
+    for (int part = 0; part < kRun / 8 + 2; ++part) {
         const int s = t0 - 8 + part * 8;
         if (s < 0 || s >= len) continue;
         const Pack<uint8_t, 8> r = load_some<uint8_t, 8>(row + s, len - s);
@@ -113,24 +117,28 @@ constexpr int kRowRun = 32;        // steps of a wave's run, in the backward wit
 constexpr int kAhead = 8;
 
 // A lane's kV channels of a row that begins at `row`. EVEN (an even number of channels): lanes past the last pair
-// repeat it, in the same wave, so that neither loads nor stores are masked.
+// repeat it, in the same wave, so that neither loads nor stores are masked. Otherwise each channel is loaded by itself,
+// the last one again where there is none, as a branch around every load costs more (8 x 2048 x 1537 bf16, forward
+// and backward: 147 us, 205 with branches).
 template <typename S, bool EVEN>
 struct Cols {
-    uint32_t at;  // bytes from a row's start
-    int n;        // channels that are there
+    static_assert(kV == 2);
+    uint32_t at, at1;  // bytes from a row's start; of the second channel
+    int n;             // channels that are there
     __device__ __forceinline__ Cols(int64_t c0, int64_t dim) {
         n = (int)(dim - c0 < kV ? dim - c0 : kV);
-        at = (uint32_t)((EVEN && n < kV ? dim - kV : c0) * sizeof(S));
+        if constexpr (EVEN) {
+            at = (uint32_t)((n < kV ? dim - kV : c0) * sizeof(S)), at1 = at + sizeof(S);
+        } else {
+            at = (uint32_t)((n < 1 ? dim - 1 : c0) * sizeof(S)), at1 = n < 2 ? at : at + sizeof(S);
+        }
     }
     __device__ __forceinline__ Pack<S, kV> load(const void* row) const {
-        const S* p = reinterpret_cast<const S*>(static_cast<const char*>(row) + at);
-        if constexpr (EVEN) {
-            Pack<S, kV> r;
-            __builtin_memcpy(&r, p, sizeof(r));
-            return r;
-        } else {
-            return load_some<S, kV>(p, n);
-        }
+        const char* p = static_cast<const char*>(row);
+        Pack<S, kV> r;
+        if constexpr (EVEN) __builtin_memcpy(&r, p + at, sizeof(r));
+        else r.v[0] = *reinterpret_cast<const S*>(p + at), r.v[1] = *reinterpret_cast<const S*>(p + at1);
+        return r;
     }
     __device__ __forceinline__ void store(void* row, const Pack<S, kV>& r) const {
         S* p = reinterpret_cast<S*>(static_cast<char*>(row) + at);
@@ -506,33 +514,63 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_fwd_kernel(ConvArgs p
     store_some<S, kRun>(static_cast<S*>(p.y) + bt * p.sy_b + c * p.sy_r + t0, out, len - t0);
 }
 
-// A workgroup: one channel, every `blocks`-th stretch of its sequences' runs.
+// A workgroup: one channel, every `blocks`-th stretch of its sequences' runs. A wave takes 63 runs and the one behind
+// them, whose dpre the last of them needs as each needs its neighbour's: a lane reads it from the next lane instead
+// of computing it again (8 x 2048 x 1536 bf16: 70 us, 90 with 11 steps computed for 8 and a load before each use).
+constexpr int kOwn = 63;
+
 template <typename S, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArgs p) {
     const int64_t c = blockIdx.x / p.blocks;
-    const int block = blockIdx.x % p.blocks;
+    const int block = blockIdx.x % p.blocks, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int len = (int)p.len;
     float w[W], dw[W], db = 0.0f;
 #pragma unroll
     for (int k = 0; k < W; ++k) w[k] = p.w[c * W + k], dw[k] = 0.0f;
     const float b = p.b ? p.b[c] : 0.0f;
-    for (uint32_t item = (uint32_t)block * kConvThreads + threadIdx.x; item < p.items; item += (uint32_t)p.blocks * kConvThreads) {
+
+    struct Run {
+        Pack<S, 4> before;
+        Pack<S, kRun> x, g;
+        uint32_t bits;
+    };
+    const uint32_t stride = (uint32_t)p.blocks * (kConvThreads / 64) * kOwn;
+    auto fetch = [&](uint32_t item) __attribute__((always_inline)) {
+        Run r{};
+        if (item >= p.items) return r;
         const uint32_t bt = item / p.runs;
         const int t0 = (int)(item - bt * p.runs) * kRun;
-        float in[4 + kRun + 4], g[kRun + 4];
-        load_line<S, 4>(static_cast<const S*>(p.x) + bt * p.sx_b + c * p.sx_r, t0, len, in);
-        load_line<S, 0>(static_cast<const S*>(p.dy) + bt * p.sg_b + c * p.sg_r, t0, len, g);
+        const S* x = static_cast<const S*>(p.x) + bt * p.sx_b + c * p.sx_r + t0;
+        if (t0 > 0) r.before = load_some<S, 4>(x - 4, 4);
+        r.x = load_some<S, kRun>(x, len - t0);
+        r.g = load_some<S, kRun>(static_cast<const S*>(p.dy) + bt * p.sg_b + c * p.sg_r + t0, len - t0);
+        r.bits = reset_bits(p.reset ? p.reset + bt * p.len : nullptr, t0, len);
+        return r;
+    };
+    uint32_t item = ((uint32_t)block * (kConvThreads / 64) + wave) * kOwn + lane;
+    Run next = fetch(item);
+    // (a whole wave makes the same turns: lanes read their neighbours')
+    for (uint32_t first = item - lane; first < p.items; first += stride, item += stride) {
+        const Run now = next;
+        next = fetch(item + stride);
+        const bool in = item < p.items, own = in && lane < kOwn;
+        const uint32_t bt = in ? item / p.runs : 0;
+        const int t0 = in ? (int)(item - bt * p.runs) * kRun : len;
+        float v[4 + kRun];  // values of steps t0 - 4 ..
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = to_f32(now.before.v[i]);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) v[4 + i] = to_f32(now.x.v[i]);
         const int64_t st = (int64_t)bt * (W - 1) * p.dim + c;
         if (t0 == 0 && p.state) {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) in[4 - (W - 1) + i] = to_f32(static_cast<const S*>(p.state)[st + i * p.dim]);
+            for (int i = 0; i < W - 1; ++i) v[4 - (W - 1) + i] = to_f32(static_cast<const S*>(p.state)[st + i * p.dim]);
         }
-        const uint8_t* reset = p.reset ? p.reset + bt * p.len : nullptr;
-        const uint32_t bits = reset_bits(reset, t0, len);
         float dv[W - 1 + kRun];
 #pragma unroll
         for (int i = 0; i < W - 1 + kRun; ++i) dv[i] = 0.0f;
-        if (p.dlast && t0 + kRun + W - 1 > len) {
+        const uint8_t* reset = p.reset ? p.reset + bt * p.len : nullptr;
+        if (own && p.dlast && t0 + kRun + W - 1 > len) {
 #pragma unroll
             for (int i = 0; i < W - 1 + kRun; ++i) {
                 const int s = t0 + i - (W - 1), j = s - (len - (W - 1));
@@ -540,27 +578,43 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
                 dv[i] = to_f32(static_cast<const S*>(p.dlast)[st + j * p.dim]);
             }
         }
+        auto run = [&](auto cut) __attribute__((always_inline)) {
+            constexpr bool CUT = decltype(cut)::value;
+            float d[kRun + W - 1];
 #pragma unroll
-        for (int i = 0; i < W - 1 + kRun; ++i) {
-            const int age = age_of(bits, 8 + i);
-            float pre = b, seen[W];
+            for (int i = 0; i < kRun; ++i) {
+                const int age = age_of(now.bits, 8 + i);
+                float pre = b, seen[W];
 #pragma unroll
-            for (int j = W - 1; j >= 0; --j) {
-                seen[j] = j <= age ? in[4 + i - j] : 0.0f;
-                pre = __builtin_fmaf(w[W - 1 - j], seen[j], pre);
+                for (int j = W - 1; j >= 0; --j) {
+                    seen[j] = !CUT || j <= age ? v[4 + i - j] : 0.0f;
+                    pre = __builtin_fmaf(w[W - 1 - j], seen[j], pre);
+                }
+                d[i] = t0 + i < len ? to_f32(now.g.v[i]) * dact_f(pre, p.silu) : 0.0f;
+                if (own) {
+                    db += d[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[W - 1 - j] = __builtin_fmaf(d[i], seen[j], dw[W - 1 - j]);
+                }
             }
-            const float d = t0 + i < len ? g[i] * dact_f(pre, p.silu) : 0.0f;
-            if (i < kRun) {
-                db += d;
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[W - 1 - j] = __builtin_fmaf(d, seen[j], dw[W - 1 - j]);
+            for (int i = 0; i < W - 1; ++i) {
+                const float behind = __shfl_down(d[i], 1);
+                d[kRun + i] = t0 + kRun + i < len ? behind : 0.0f;  // behind a sequence the next lane has another
             }
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int to = W - 1 + i - j;
-                if (to < W - 1 + kRun) dv[to] = __builtin_fmaf(w[W - 1 - j], j <= age ? d : 0.0f, dv[to]);
+            for (int i = 0; i < kRun + W - 1; ++i) {
+                const int age = age_of(now.bits, 8 + i);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int to = W - 1 + i - j;
+                    if (to < W - 1 + kRun) dv[to] = __builtin_fmaf(w[W - 1 - j], !CUT || j <= age ? d[i] : 0.0f, dv[to]);
+                }
             }
-        }
+        };
+        if (__ballot(now.bits != 0) == 0) run(std::false_type{});
+        else run(std::true_type{});
+        if (!own) continue;
         Pack<S, kRun> out;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) out.v[i] = from_f32<S>(dv[W - 1 + i]);
@@ -571,11 +625,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
         }
     }
     __shared__ float sums[kConvThreads / 64][kMaxWidth + 1];
-    const int wave = threadIdx.x >> 6;
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
         const float s = wave_sum(k < W ? dw[k < W ? k : 0] : db);
-        if ((threadIdx.x & 63) == 0) sums[wave][k] = s;
+        if (lane == 0) sums[wave][k] = s;
     }
     __syncthreads();
     if (threadIdx.x <= W) {
@@ -622,11 +675,12 @@ int blocks_of(int64_t items, int64_t each, int64_t groups, int per_cu) {
     const int64_t n = need < most ? need : most;
     return (int)(n < 1 ? 1 : n);
 }
-constexpr int kFwdPerCu = 8, kBwdPerCu = 4, kStepsBwdPerCu = 8;
+// (rows, gradient: 66.2 us a pass at 8 x 2048 x 1536 with 4 a CU, 67.8 with 8; steps: 106 with 8, 100 with 32, 104 with 64)
+constexpr int kFwdPerCu = 8, kBwdPerCu = 4, kStepsBwdPerCu = 32;
 
 int bwd_blocks(const mamba_conv_shape& s, bool x_steps) {
     const int64_t items = s.batch * runs_of(s, x_steps, true);
-    return x_steps ? blocks_of(items, kConvThreads, s.dim, kStepsBwdPerCu) : blocks_of(items, kWaves, groups_of(s), kBwdPerCu);
+    return x_steps ? blocks_of(items, kConvThreads / 64 * kOwn, s.dim, kStepsBwdPerCu) : blocks_of(items, kWaves, groups_of(s), kBwdPerCu);
 }
 
 template <typename S, int W>
