@@ -142,6 +142,19 @@ def _param(t, name, shape, like, dev):
     return t if t is None or _is(t, shape, torch.float32, dev) else _f32(t, name, shape, like)
 
 
+def _rows_as(t, x, name, shape, dev, dim):
+    """A tensor of x's shape, dtype and device as evenly spaced rows: it, or a copy, and the stride between them."""
+    if _is(t, shape, x.dtype, dev):
+        return t, dim
+    rows, _, stride = _rows(_same(t, x, name), name)
+    return rows, stride
+
+
+def _new_like(x, shape):
+    """An uninitialised contiguous tensor of x's dtype (the shorter way of the two where x is one)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+
+
 def _taken(t, name, shape, dtype, dev):
     """A tensor of x's dtype and of the given shape, contiguous."""
     if not _is(t, shape, dtype, dev):
@@ -168,6 +181,12 @@ def _conv_layout(x, shape):
         return x, batch, dim, 1
     x = x.contiguous()
     return x, x.stride(0), x.stride(1), 0
+
+
+def _new_steps(x, batch, length, dim):
+    """An uninitialised (batch, len, dim) with its steps side by side: no view, so that it can be changed in place as
+    a result of autograd."""
+    return x.new_empty_strided((batch, length, dim), (dim * length, 1, length))
 
 
 def _conv_args(x, weight, bias, activation, initial_state, reset, entry):
@@ -210,7 +229,7 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
     x, xb, xr, steps = _conv_layout(x, whole)
     y_steps = 1 if steps or scan_layout else 0
     if out is None:
-        y = x.new_empty((batch, dim, length)).transpose(1, 2) if y_steps else x.new_empty(whole)
+        y = _new_steps(x, batch, length, dim) if y_steps else x.new_empty(whole)
     else:
         y = out
         if y.shape != whole or y.dtype is not x.dtype or y.device != x.device:
@@ -231,6 +250,13 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
     return (y, last) if return_last_state else y
 
 
+@functools.lru_cache(maxsize=64)
+def _conv_bwd_bytes(batch, length, dim, width, dtype, steps, dev):
+    """The gradient's workspace: by the sizes and, as workgroups are counted in compute units, the device."""
+    with torch.cuda.device(dev):
+        return _load().mamba_conv_bwd_workspace_bytes(ConvShape(batch, length, dim, width), dtype, steps)
+
+
 def causal_conv_bwd(x, weight, bias, dy, *, activation="silu", initial_state=None, reset=None, dlast_state=None,
                     want_dinitial=None):
     """Gradients of :func:`causal_conv_fn` for incoming ``dy`` (x's shape and dtype, either layout) and,
@@ -241,26 +267,26 @@ def causal_conv_bwd(x, weight, bias, dy, *, activation="silu", initial_state=Non
     dtype, act, weight, bias, state, reset, width = _conv_args(x, weight, bias, activation, initial_state, reset, "causal_conv_bwd")
     batch, length, dim = x.shape
     _same(dy, x, "dy")
-    x, xb, xr, steps = _conv_layout(x, x.shape)
-    dy, gb, gr, g_steps = _conv_layout(dy, x.shape)
+    whole, dev = x.shape, x.get_device()
+    x, xb, xr, steps = _conv_layout(x, whole)
+    dy, gb, gr, g_steps = _conv_layout(dy, whole)
     if steps and not g_steps:
         dy = dy.transpose(1, 2).contiguous().transpose(1, 2)
         gb, gr, g_steps = dy.stride(0), dy.stride(2), 1
-    dlast = None if dlast_state is None else _taken(dlast_state, "dlast_state", (batch, width - 1, dim), x.dtype, x.get_device())
+    dlast = None if dlast_state is None else _taken(dlast_state, "dlast_state", (batch, width - 1, dim), x.dtype, dev)
     if want_dinitial is None:
         want_dinitial = state is not None
-    dx = x.new_empty((batch, dim, length)).transpose(1, 2) if steps else x.new_empty((batch, length, dim))
+    dx = _new_steps(x, batch, length, dim) if steps else x.new_empty(whole)
     out = {"x": dx, "weight": x.new_empty((dim, width), dtype=torch.float32)}
     if bias is not None:
         out["bias"] = x.new_empty((dim,), dtype=torch.float32)
     if want_dinitial:
         out["initial_state"] = x.new_empty((batch, width - 1, dim))
-    shape = ConvShape(batch, length, dim, width)
-    n = _on_device(x, lib.mamba_conv_bwd_workspace_bytes, shape, dtype, steps)
-    ws = _workspace(n, "mamba_conv_bwd_workspace_bytes", x)
+    shape, n = ConvShape(batch, length, dim, width), _conv_bwd_bytes(batch, length, dim, width, dtype, steps, dev)
+    ws, ds = _workspace(n, "mamba_conv_bwd_workspace_bytes", x), dx.stride()
     ptrs = ConvBwdPtrs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), dy.data_ptr(), _ptr(dlast),
                        dx.data_ptr(), out["weight"].data_ptr(), _ptr(out.get("bias")), _ptr(out.get("initial_state")),
-                       xb, xr, gb, gr, dx.stride(0), dx.stride(2 if steps else 1), steps, g_steps, _ptr(ws), n)
+                       xb, xr, gb, gr, ds[0], ds[2 if steps else 1], steps, g_steps, _ptr(ws), n)
     _launch("mamba_conv_bwd", x, lib.mamba_conv_bwd, ptrs, shape, act, dtype)
     return out
 
@@ -371,21 +397,25 @@ def rms_norm_fn(x, weight=None, eps=1e-5, *, residual=None, scale=1.0, return_st
     x, residual: (..., dim), float32 or bfloat16; weight: (dim,) or None. Returns y, or (y, t) with a residual;
     with ``return_stats`` a pair of that and the (rows,) fp32 inverse deviations that :func:`rms_norm_bwd`
     takes."""
-    lib = _load()
     dtype = _dtype(x, "x")
     _need_gpu(x, "rms_norm_fn")
-    shape = x.shape
+    shape, dev = x.shape, x.get_device()
     xr, rows, xs = _rows(x, "x")
     dim = shape[-1]
-    rr, _, rs = (None, 0, 0) if residual is None else _rows(_same(residual, x, "residual"), "residual")
-    weight = _f32(weight, "weight", (dim,), x)
-    y = x.new_empty(shape)
-    t = None if residual is None else x.new_empty(shape)
+    rr, rs = (None, 0) if residual is None else _rows_as(residual, x, "residual", shape, dev, dim)
+    weight = _param(weight, "weight", (dim,), x, dev)
+    y = _new_like(x, shape)
+    t = None if residual is None else _new_like(x, shape)
     stats = x.new_empty((rows,), dtype=torch.float32) if return_stats else None
     ptrs = RmsPtrs(xr.data_ptr(), _ptr(rr), _ptr(weight), y.data_ptr(), _ptr(t), _ptr(stats), xs, rs, dim, dim)
-    _launch("mamba_rms_norm_fwd", x, lib.mamba_rms_norm_fwd, ptrs, RmsShape(rows, dim), scale, eps, dtype)
+    _launch("mamba_rms_norm_fwd", x, _load().mamba_rms_norm_fwd, ptrs, RmsShape(rows, dim), scale, eps, dtype)
     out = y if residual is None else (y, t)
     return (out, stats) if return_stats else out
+
+
+@functools.lru_cache(maxsize=64)
+def _rms_bwd_bytes(rows, dim):
+    return _load().mamba_rms_norm_bwd_workspace_bytes(RmsShape(rows, dim))
 
 
 def rms_norm_bwd(t, weight, dy, stats, *, dresidual=None, scale=1.0, want_dweight=True):
@@ -393,27 +423,24 @@ def rms_norm_bwd(t, weight, dy, stats, *, dresidual=None, scale=1.0, want_dweigh
     ``dresidual``: the gradient that reaches t by the residual stream, added to the result; ``scale``: the
     forward's, with a residual. Returns a dict: residual (the gradient at t) and x (scale times that; the same
     tensor where scale is 1) in t's dtype, weight (fp32) where wanted."""
-    lib = _load()
     dtype = _dtype(t, "t")
     _need_gpu(t, "rms_norm_bwd")
-    for name, v in (("dy", dy), ("dresidual", dresidual)):
-        if v is not None:
-            _same(v, t, name)
-    (tr, rows, ts), (gr, _, gs) = _rows(t, "t"), _rows(dy, "dy")
-    rr, _, rs = (None, 0, 0) if dresidual is None else _rows(dresidual, "dresidual")
-    dim = t.shape[-1]
-    weight, stats = _f32(weight, "weight", (dim,), t), _f32(stats, "stats", (rows,), t)
-    dt = t.new_empty(t.shape)
-    dx = t.new_empty(t.shape) if scale != 1.0 else None
+    whole, dev = t.shape, t.get_device()
+    tr, rows, ts = _rows(t, "t")
+    dim = whole[-1]
+    gr, gs = _rows_as(dy, t, "dy", whole, dev, dim)
+    rr, rs = (None, 0) if dresidual is None else _rows_as(dresidual, t, "dresidual", whole, dev, dim)
+    weight, stats = _param(weight, "weight", (dim,), t, dev), _param(stats, "stats", (rows,), t, dev)
+    dt = _new_like(t, whole)
+    dx = _new_like(t, whole) if scale != 1.0 else None
     out = {"x": dt if dx is None else dx, "residual": dt}
     if want_dweight:
         out["weight"] = t.new_empty((dim,), dtype=torch.float32)
-    shape = RmsShape(rows, dim)
-    n = lib.mamba_rms_norm_bwd_workspace_bytes(shape) if want_dweight else 0
+    n = _rms_bwd_bytes(rows, dim) if want_dweight else 0
     ws = _workspace(n, "mamba_rms_norm_bwd_workspace_bytes", t)
     ptrs = RmsBwdPtrs(tr.data_ptr(), _ptr(weight), stats.data_ptr(), gr.data_ptr(), _ptr(rr), _ptr(dx), dt.data_ptr(),
                       _ptr(out.get("weight")), ts, gs, rs, dim, dim, _ptr(ws), n)
-    _launch("mamba_rms_norm_bwd", t, lib.mamba_rms_norm_bwd, ptrs, shape, scale, dtype)
+    _launch("mamba_rms_norm_bwd", t, _load().mamba_rms_norm_bwd, ptrs, RmsShape(rows, dim), scale, dtype)
     return out
 
 
@@ -452,13 +479,13 @@ def rms_norm(x, weight=None, eps=1e-5, *, residual=None, scale=1.0):
 def _gated_args(x, z, weight, groups, entry):
     dtype = _dtype(x, "x")
     _need_gpu(x, entry)
-    _same(z, x, "z")
+    shape, dev = x.shape, x.get_device()
     xr, rows, xs = _rows(x, "x")
-    zr, _, zs = _rows(z, "z")
-    dim = x.shape[-1]
+    dim = shape[-1]
+    zr, zs = _rows_as(z, x, "z", shape, dev, dim)
     if groups < 1 or dim % groups:
         raise ValueError(f"groups must divide dim = {dim}, got {groups}")
-    return dtype, xr, xs, zr, zs, _f32(weight, "weight", (dim,), x), rows, dim
+    return dtype, xr, xs, zr, zs, _param(weight, "weight", (dim,), x, dev), rows, dim, shape, dev
 
 
 def gated_rms_norm_fn(x, z, weight=None, eps=1e-5, *, groups=1, gate_first=True, return_stats=False):
@@ -471,31 +498,34 @@ def gated_rms_norm_fn(x, z, weight=None, eps=1e-5, *, groups=1, gate_first=True,
     x, z: (..., dim), float32 or bfloat16 (slices of one projection's output are read in place); weight: (dim,)
     or None. Returns y in x's dtype; with ``return_stats`` also the (rows, groups) fp32 inverse deviations that
     :func:`gated_rms_norm_bwd` takes."""
-    lib = _load()
-    dtype, xr, xs, zr, zs, weight, rows, dim = _gated_args(x, z, weight, groups, "gated_rms_norm_fn")
-    y = x.new_empty(x.shape)
+    dtype, xr, xs, zr, zs, weight, rows, dim, shape, _ = _gated_args(x, z, weight, groups, "gated_rms_norm_fn")
+    y = _new_like(x, shape)
     stats = x.new_empty((rows, groups), dtype=torch.float32) if return_stats else None
     ptrs = GatedRmsPtrs(xr.data_ptr(), zr.data_ptr(), _ptr(weight), y.data_ptr(), _ptr(stats), xs, zs, dim)
-    _launch("mamba_gated_rms_norm_fwd", x, lib.mamba_gated_rms_norm_fwd, ptrs, GatedRmsShape(rows, dim, groups), gate_first, eps, dtype)
+    _launch("mamba_gated_rms_norm_fwd", x, _load().mamba_gated_rms_norm_fwd, ptrs, GatedRmsShape(rows, dim, groups), gate_first, eps,
+            dtype)
     return (y, stats) if return_stats else y
+
+
+@functools.lru_cache(maxsize=64)
+def _gated_bwd_bytes(rows, dim, groups):
+    return _load().mamba_gated_rms_norm_bwd_workspace_bytes(GatedRmsShape(rows, dim, groups))
 
 
 def gated_rms_norm_bwd(x, z, weight, dy, stats, *, groups=1, gate_first=True, want_dweight=True):
     """Gradients of :func:`gated_rms_norm_fn` with its ``stats``: a dict of x and z in x's dtype, weight (fp32)
     where wanted."""
-    lib = _load()
-    dtype, xr, xs, zr, zs, weight, rows, dim = _gated_args(x, z, weight, groups, "gated_rms_norm_bwd")
-    gr, _, gs = _rows(_same(dy, x, "dy"), "dy")
-    stats = _f32(stats, "stats", (rows, groups), x)
-    out = {"x": x.new_empty(x.shape), "z": x.new_empty(x.shape)}
+    dtype, xr, xs, zr, zs, weight, rows, dim, whole, dev = _gated_args(x, z, weight, groups, "gated_rms_norm_bwd")
+    gr, gs = _rows_as(dy, x, "dy", whole, dev, dim)
+    stats = _param(stats, "stats", (rows, groups), x, dev)
+    out = {"x": _new_like(x, whole), "z": _new_like(x, whole)}
     if want_dweight:
         out["weight"] = x.new_empty((dim,), dtype=torch.float32)
-    shape = GatedRmsShape(rows, dim, groups)
-    n = lib.mamba_gated_rms_norm_bwd_workspace_bytes(shape) if want_dweight else 0
+    n = _gated_bwd_bytes(rows, dim, groups) if want_dweight else 0
     ws = _workspace(n, "mamba_gated_rms_norm_bwd_workspace_bytes", x)
     ptrs = GatedRmsBwdPtrs(xr.data_ptr(), zr.data_ptr(), _ptr(weight), stats.data_ptr(), gr.data_ptr(), out["x"].data_ptr(),
                            out["z"].data_ptr(), _ptr(out.get("weight")), xs, zs, gs, dim, dim, _ptr(ws), n)
-    _launch("mamba_gated_rms_norm_bwd", x, lib.mamba_gated_rms_norm_bwd, ptrs, shape, gate_first, dtype)
+    _launch("mamba_gated_rms_norm_bwd", x, _load().mamba_gated_rms_norm_bwd, ptrs, GatedRmsShape(rows, dim, groups), gate_first, dtype)
     return out
 
 
@@ -527,39 +557,40 @@ def gated_rms_norm(x, z, weight=None, eps=1e-5, *, groups=1, gate_first=True):
 def _xent_args(x, weight, target, entry):
     dtype = _dtype(x, "x")
     _need_gpu(x, entry)
-    if x.dim() < 1 or weight.dim() != 2:
+    shape, wshape, dev = x.shape, weight.shape, x.get_device()
+    if len(shape) < 1 or len(wshape) != 2:
         raise ValueError("x must be (..., dim) and weight (vocab, dim)")
-    if weight.dtype is not x.dtype or weight.get_device() != x.get_device():
+    if weight.dtype is not x.dtype or weight.get_device() != dev:
         raise TypeError("weight must have x's dtype and device")
-    if weight.shape[1] != x.shape[-1]:
-        raise ValueError(f"weight must be (vocab, dim) with dim = {x.shape[-1]}, got {tuple(weight.shape)}")
-    if target is not None:
-        if target.dtype not in (torch.int64, torch.int32):
-            raise TypeError(f"target must be int64 or int32, got {target.dtype}")
-        if target.shape != x.shape[:-1] or target.get_device() != x.get_device():
-            raise ValueError(f"target must be {tuple(x.shape[:-1])} on x's device, got {tuple(target.shape)}")
-        target = target.contiguous()
+    if wshape[1] != shape[-1]:
+        raise ValueError(f"weight must be (vocab, dim) with dim = {shape[-1]}, got {tuple(wshape)}")
+    ids64, lead = target.dtype is torch.int64, shape[:-1]
+    if not ids64 and target.dtype is not torch.int32:
+        raise TypeError(f"target must be int64 or int32, got {target.dtype}")
+    if target.shape != lead or target.get_device() != dev:
+        raise ValueError(f"target must be {tuple(lead)} on x's device, got {tuple(target.shape)}")
     xr, rows, xs = _rows(x, "x")
     weight = _inner(weight)
-    return dtype, xr, rows, xs, weight, _row_stride(weight), target
+    return (dtype, xr, xs, weight, _row_stride(weight), target if target.is_contiguous() else target.contiguous(), ids64, lead, dev,
+            XentShape(rows, wshape[1], wshape[0]))
 
 
 def _xent_launch(name, x, f, size, ptrs, shape, *args):
     n = _on_device(x, size, ptrs, shape)
-    ws = _workspace(n, name, x)
-    ptrs.workspace, ptrs.workspace_bytes = _ptr(ws), n
+    if n != 0:
+        ws = _workspace(n, name, x)
+        ptrs.workspace, ptrs.workspace_bytes = ws.data_ptr(), n
     _launch(name, x, f, ptrs, shape, *args)
 
 
 def _xent_fwd(x, weight, target, scale, want_lse, want_total, entry):
     lib = _load()
-    dtype, xr, rows, xs, weight, ws, target = _xent_args(x, weight, target, entry)
-    loss = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    lse = x.new_empty(x.shape[:-1], dtype=torch.float32) if want_lse else None
+    dtype, xr, xs, weight, ws, target, ids64, lead, _, shape = _xent_args(x, weight, target, entry)
+    loss = x.new_empty(lead, dtype=torch.float32)
+    lse = x.new_empty(lead, dtype=torch.float32) if want_lse else None
     total = x.new_empty(2, dtype=torch.float32) if want_total else None
     ptrs = XentPtrs(xr.data_ptr(), weight.data_ptr(), target.data_ptr(), loss.data_ptr(), _ptr(lse), _ptr(total), xs, ws, None, 0)
-    _xent_launch("mamba_xent_fwd", x, lib.mamba_xent_fwd, lib.mamba_xent_workspace_bytes, ptrs,
-                 XentShape(rows, weight.shape[1], weight.shape[0]), target.dtype is torch.int64, scale, dtype)
+    _xent_launch("mamba_xent_fwd", x, lib.mamba_xent_fwd, lib.mamba_xent_workspace_bytes, ptrs, shape, ids64, scale, dtype)
     return loss, lse, total
 
 
@@ -575,18 +606,20 @@ def linear_cross_entropy_fn(x, weight, target, *, scale=1.0, return_lse=False):
     return (loss, lse) if return_lse else loss
 
 
-def _factor(g, name, like):
+def _factor(g, name, lead, dev):
     """An incoming gradient of the rows: its tensor and the stride between rows, 0 for one value for all."""
     if g is None:
         return None, 0
-    if g.get_device() != like.get_device():
+    if _is(g, lead, torch.float32, dev):
+        return g, 1
+    if g.get_device() != dev:
         raise ValueError(f"{name} must be on x's device")
-    if g.shape != like.shape[:-1]:
-        raise ValueError(f"{name} must be {tuple(like.shape[:-1])}, got {tuple(g.shape)}")
+    if g.shape != lead:
+        raise ValueError(f"{name} must be {tuple(lead)}, got {tuple(g.shape)}")
     g = g.float()
     if g.numel() > 1 and all(s == 0 or n == 1 for n, s in zip(g.shape, g.stride())):  # broadcast from one value
         return g, 0
-    return g if g.is_contiguous() else g.contiguous(), 1
+    return g.contiguous(), 1
 
 
 def linear_cross_entropy_bwd(x, weight, target, lse, dloss, *, dlse=None, scale=1.0, want_dx=True, want_dweight=True):
@@ -596,18 +629,17 @@ def linear_cross_entropy_bwd(x, weight, target, lse, dloss, *, dlse=None, scale=
     once, as the operands of the products. A row without a target or whose incoming gradients are 0 takes no
     part, whatever x holds there."""
     lib = _load()
-    dtype, xr, rows, xs, weight, ws, target = _xent_args(x, weight, target, "linear_cross_entropy_bwd")
-    lse = _f32(lse, "lse", x.shape[:-1], x)
-    (a, sa), (b, sb) = _factor(dloss, "dloss", x), _factor(dlse, "dlse", x)
+    dtype, xr, xs, weight, ws, target, ids64, lead, dev, shape = _xent_args(x, weight, target, "linear_cross_entropy_bwd")
+    lse = _param(lse, "lse", lead, x, dev)
+    (a, sa), (b, sb) = _factor(dloss, "dloss", lead, dev), _factor(dlse, "dlse", lead, dev)
     out = {}
     if want_dx:
-        out["x"] = x.new_empty(x.shape)
+        out["x"] = _new_like(x, x.shape)
     if want_dweight:
-        out["weight"] = weight.new_empty(weight.shape)
+        out["weight"] = _new_like(weight, weight.shape)
     ptrs = XentBwdPtrs(xr.data_ptr(), weight.data_ptr(), target.data_ptr(), lse.data_ptr(), _ptr(a), _ptr(b), _ptr(out.get("x")),
                        _ptr(out.get("weight")), xs, ws, sa, sb, None, 0)
-    _xent_launch("mamba_xent_bwd", x, lib.mamba_xent_bwd, lib.mamba_xent_bwd_workspace_bytes, ptrs,
-                 XentShape(rows, weight.shape[1], weight.shape[0]), target.dtype is torch.int64, scale, dtype)
+    _xent_launch("mamba_xent_bwd", x, lib.mamba_xent_bwd, lib.mamba_xent_bwd_workspace_bytes, ptrs, shape, ids64, scale, dtype)
     return out
 
 

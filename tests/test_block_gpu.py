@@ -705,3 +705,190 @@ def test_replayed_graphs_repeat_the_eager_calls():
             torch.cuda.synchronize()
             assert same(got, want), (k, turn)
             assert same(f(), want), (k, turn)  # the program's own eager work between the replays
+
+
+# ---- calls at once, captured backward passes, tensors beyond 4 GiB ----
+
+def test_calls_at_once_on_two_streams():
+    """The same call on two streams at a time, and two replayed graphs of it: workspaces are each call's own."""
+    for k, f in enumerate(every_call()):
+        if k == 6:  # (writes its states to one pair of buffers)
+            continue
+        want = tuple(t.clone() for t in f())
+        streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(8):
+            for s, out in zip(streams, got):
+                with torch.cuda.stream(s):
+                    out.append(f())
+        graphs = []
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        assert all(same(o, want) for out in got for o in out), k
+        for _ in streams:
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                out = f()
+            got[len(graphs) - 1] = out
+        for _ in range(3):
+            for out in got:
+                for t in out:
+                    t.zero_()
+            torch.cuda.synchronize()
+            for s, graph in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    graph.replay()
+            torch.cuda.synchronize()
+            assert same(got[0], want) and same(got[1], want), k
+
+
+def test_captured_forward_and_backward_passes():
+    """The differentiable forms with their gradients in one graph, replayed on new inputs."""
+    g = gen(60)
+    r = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    x, z, wn = r(3, 50, 24).to(BF16), r(3, 50, 24).to(BF16), r(24)
+    cw, cb, w = r(24, 1, 4), r(24), r(70, 24).to(BF16)
+    target = torch.randint(-1, 71, (3, 50), generator=g).to(DEV)
+    leaves = [t.requires_grad_() for t in (x, z, wn, cw, cb, w)]
+
+    def step():
+        t, _ = block.rms_norm(x, wn, residual=z, scale=0.5)
+        c = block.causal_conv(t, cw, cb, scan_layout=True)
+        y = block.gated_rms_norm(c.transpose(1, 2).contiguous().transpose(1, 2), z, wn, groups=2)
+        loss = block.linear_cross_entropy(y, w, target)
+        return (loss.detach(), *torch.autograd.grad(loss, leaves))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for turn in range(3):
+        with torch.no_grad():
+            x.copy_(r(3, 50, 24)), target.copy_(torch.randint(-1, 71, (3, 50), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, step()), turn
+
+
+def test_conv_result_can_be_changed_in_place():
+    t = dev(conv_case(61, 2, 20, 16, 4, F32, state=False))
+    for scan_layout in (False, True):
+        x = t["x"].clone().requires_grad_()
+        block.causal_conv(x, t["weight"], t["bias"], scan_layout=scan_layout).mul_(2.0).backward(t["dy"])
+        want = block.causal_conv_bwd(t["x"], t["weight"], t["bias"], 2 * t["dy"])["x"]
+        assert torch.equal(x.grad, want)
+
+
+def test_norms_offsets_past_32_bits():
+    rows, dim = 300001, 8192  # 4.9 GB of bf16
+    g = torch.Generator(device=DEV).manual_seed(62)
+    base = torch.randn(997, dim, generator=g, device=DEV, dtype=BF16)
+    x = base.repeat(-(-rows // 997), 1)[:rows]
+    w, tail, dy = torch.randn(dim, generator=g, device=DEV), slice(rows - 500, rows), base[:1].expand(rows, dim)
+    other = x.roll(1, 0)
+    part, part_o, part_dy = x[tail].clone(), other[tail].clone(), dy[tail].contiguous()
+    y, t = block.rms_norm_fn(x, w, residual=other, scale=0.5)
+    got, stats = (y[tail].clone(), t[tail].clone()), torch.ones(rows, device=DEV)
+    del y, t
+    assert same(got, block.rms_norm_fn(part, w, residual=part_o, scale=0.5))
+    dx = block.rms_norm_bwd(x, w, other, stats, dresidual=x, want_dweight=False)["x"]
+    assert torch.equal(dx[tail], block.rms_norm_bwd(part, w, part_o, stats[tail], dresidual=part)["x"])
+    del dx
+    y, stats = block.gated_rms_norm_fn(x, other, w, groups=4, return_stats=True)
+    want, want_stats = block.gated_rms_norm_fn(part, part_o, w, groups=4, return_stats=True)
+    assert torch.equal(y[tail], want) and torch.equal(stats[tail], want_stats)
+    del y
+    b = block.gated_rms_norm_bwd(x, other, w, dy, stats, groups=4)
+    want = block.gated_rms_norm_bwd(part, part_o, w, part_dy, want_stats, groups=4)
+    assert torch.equal(b["x"][tail], want["x"]) and torch.equal(b["z"][tail], want["z"])
+
+
+def test_cross_entropy_hidden_states_past_32_bits():
+    """300 rows behind 4 GiB of others, whose losses have no part in the gradients."""
+    M, N = 1400003, 300
+    t = xent_case(63, N, 1600, 100)
+    d = dev(t)
+    x = torch.ones(M, 1600, dtype=BF16, device=DEV)
+    target, dloss, dlse = torch.zeros(M, dtype=d["target"].dtype, device=DEV), torch.zeros(M, device=DEV), torch.zeros(M, device=DEV)
+    x[-N:], target[-N:], dloss[-N:], dlse[-N:] = d["x"], d["target"], d["dloss"], d["dlse"]
+    loss, lse = block.linear_cross_entropy_fn(x, d["weight"], target, return_lse=True)
+    want_loss, want_lse, want = ref.linear_cross_entropy(t["x"], t["weight"], t["target"], 1.0, t["dloss"], t["dlse"])
+    close(loss[-N:], want_loss)
+    close(lse[-N:], want_lse)
+    g = block.linear_cross_entropy_bwd(x, d["weight"], target, lse, dloss, dlse=dlse)
+    slack = xent_slack(t["x"], t["weight"], t["target"], want_lse, t["dloss"], t["dlse"])
+    close(g["x"][-N:], want["x"], 1e-5, room=slack @ t["weight"].double().abs())
+    assert not g["x"][:-N].any()
+    close(g["weight"], want["weight"], 1e-5, room=slack.t() @ t["x"].double().abs())
+
+
+def test_cross_entropy_output_matrix_past_32_bits():
+    """A vocabulary whose matrix takes more than 4 GiB: 997 rows over and over, so that the sums are those of 997
+    logits, each as often as it comes."""
+    V, K, M, P = 1400003, 1600, 20, 997
+    g = torch.Generator(device=DEV).manual_seed(64)
+    base = (torch.randn(P, K, generator=g, device=DEV) * K ** -0.5).to(BF16)
+    w = base.repeat(-(-V // P), 1)[:V]
+    x = torch.randn(M, K, generator=g, device=DEV).to(BF16)
+    target = torch.randint(V - 3000, V, (M,), generator=g, device=DEV)
+    dloss = torch.randn(M, generator=g, device=DEV)
+    loss, lse = block.linear_cross_entropy_fn(x, w, target, return_lse=True)
+    count = torch.full((P,), V // P, dtype=torch.float64, device=DEV)
+    count[:V % P] += 1
+    xd, wd, a = x.double(), base.double(), dloss.double()[:, None]
+    logits = xd @ wd.t()
+    want = torch.logsumexp(logits + count.log(), -1)
+    at = (target % P)[:, None]
+    close(lse, want)
+    close(loss, want - logits.gather(1, at)[:, 0])
+    p = torch.exp(logits - want[:, None])
+    out = block.linear_cross_entropy_bwd(x, w, target, lse, dloss)
+    # dx: a softmax part for every column and the targets'; each rounded once, as xent_slack
+    d = a * p * count
+    slack = (2.0 ** -8 + 1e-5) * d.abs()
+    dx = d @ wd - a * wd[target % P]
+    close(out["x"], dx, 1e-5, room=(slack @ wd.abs() + 2.0 ** -8 * a.abs() * wd[target % P].abs()).cpu())
+    tail = torch.arange(V - 4000, V, device=DEV)
+    d = a * p[:, tail % P] - a * (target[:, None] == tail)
+    slack = 2.0 ** -8 * d.abs() + 1e-5 * (a.abs() * p[:, tail % P])
+    close(out["weight"][tail], d.t() @ xd, 1e-5, room=(slack.t() @ xd.abs()).cpu())
+
+
+def test_one_tensor_in_two_roles():
+    """A leaf given twice gets the sum of its two gradients; rows that lie on each other are read as what they are."""
+    g = gen(65)
+    for scale in (1.0, 0.5):
+        x, dy, dt = (torch.randn(6, 40, generator=g) for _ in range(3))
+        leaf = x.to(DEV).requires_grad_()
+        y, t = block.rms_norm(leaf, residual=leaf, scale=scale)
+        ((y * dy.to(DEV)).sum() + (t * dt.to(DEV)).sum()).backward()
+        close(leaf.grad, (1 + scale) * ref.rms_norm((1 + scale) * x, dy=dy, dsum=dt)["t"])
+    leaf = x.to(DEV).requires_grad_()
+    block.gated_rms_norm(leaf, leaf).backward(dy.to(DEV))
+    want = ref.gated_rms_norm(x, x, dy=dy)
+    close(leaf.grad, want["x"] + want["z"])
+    leaf = x.to(BF16).to(DEV).requires_grad_()
+    target = torch.arange(6, device=DEV)
+    block.linear_cross_entropy(leaf, leaf, target).backward()
+    a, b = leaf.detach().clone().requires_grad_(), leaf.detach().clone().requires_grad_()
+    block.linear_cross_entropy(a, b, target).backward()
+    assert torch.equal(leaf.grad, a.grad + b.grad)
+    row = torch.randn(1, 40, generator=g).to(DEV)
+    assert torch.equal(block.rms_norm_fn(row.expand(5, 40)), block.rms_norm_fn(row.repeat(5, 1)))
+    seq = torch.randn(1, 12, 40, generator=g).to(DEV)
+    w = torch.randn(40, 4, generator=g).to(DEV)
+    for x in (seq, seq[:, :1], seq.transpose(1, 2).contiguous().transpose(1, 2)):
+        many = x.expand(3, *x.shape[1:])
+        assert torch.equal(block.causal_conv_fn(many, w), block.causal_conv_fn(many.contiguous(), w))
+        got, want = block.causal_conv_bwd(many, w, None, many), block.causal_conv_bwd(many.contiguous(), w, None, many.contiguous())
+        close(got["x"], want["x"].double())
+        close(got["weight"], want["weight"].double())
+    same_row = row.bfloat16().expand(7, 40)
+    ids = torch.arange(7, device=DEV) % 6
+    assert torch.equal(block.linear_cross_entropy_fn(same_row, leaf.detach(), ids), block.linear_cross_entropy_fn(same_row.contiguous(), leaf.detach(), ids))
