@@ -16,8 +16,9 @@
 //
 // Bound by HBM, each value read and written once; the weight's gradient is summed in registers over a workgroup's
 // runs, then over its waves in order, and a second kernel adds the workgroups'. 8 x 2048 x 1536 bf16: forward 21.8 us
-// (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 44.5 + 4.8 (151 MB, 3.4); in the
-// scan's layout 27 and 70. 3 x 2777 x 1001 fp32 in the scan's layout 18 and 28. One step of 32 x 1536: 3.6.
+// (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 41.5 + 4.8 (151 MB, 3.6; the
+// vector instructions alone 22); in the scan's layout 27 and 70. 3 x 2777 x 1001 fp32 in the scan's layout 18 and 28.
+// One step of 32 x 1536: 3.6.
 #include <type_traits>
 
 #include "block_launch.hpp"
@@ -115,11 +116,12 @@ constexpr int kCols = 64 * kV;     // of a workgroup
 constexpr int kWaves = 4;
 constexpr int kRowRun = 32;        // steps of a wave's run, in the backward with the W - 1 behind it
 constexpr int kAhead = 8;
+enum { kAny, kFirst, kMiddle, kLast };  // turns of the backward
 
 // A lane's kV channels of a row that begins at `row`. EVEN (an even number of channels): lanes past the last pair
 // repeat it, in the same wave, so that neither loads nor stores are masked. Otherwise each channel is loaded by itself,
 // the last one again where there is none, as a branch around every load costs more (8 x 2048 x 1537 bf16, forward
-// and backward: 147 us, 205 with branches).
+// and backward: 205 us with branches, 147 without; 121 with the backward's turns of whole runs).
 template <typename S, bool EVEN>
 struct Cols {
     static_assert(kV == 2);
@@ -281,8 +283,9 @@ __global__ __launch_bounds__(64 * kWaves) void conv_rows_fwd_kernel(ConvArgs p) 
     }
 }
 
+// (bf16: registers for 4 workgroups a CU; left to the compiler 139 and 3: 8 x 2048 x 1536, dy as steps, 80.6 us a pass, 76.6)
 template <typename S, int W, bool STEPS_OUT, bool EVEN>
-__global__ __launch_bounds__(64 * kWaves) void conv_rows_bwd_kernel(ConvBwdArgs p) {
+__global__ __launch_bounds__(64 * kWaves, sizeof(S) == 2 ? 4 : 1) void conv_rows_bwd_kernel(ConvBwdArgs p) {
     constexpr int Q = 16 / sizeof(S), QPI = kRowRun / Q, SLOTS = kWaves * QPI, RUN = kRowRun - (W - 1);
     using P = Pack<S, kV>;
     using Line = Pack<S, Q>;
@@ -373,58 +376,85 @@ __global__ __launch_bounds__(64 * kWaves) void conv_rows_bwd_kernel(ConvBwdArgs 
                 if (s >= 0) cols.store(dx + s * p.sd_r, r);
                 else if (p.dstate) cols.store(static_cast<S*>(p.dstate) + st + (s + W - 1) * p.dim, r);
             };
-            auto run = [&](auto cut) __attribute__((always_inline)) {
-                Age age(mask);
-                // (the W - 1 turns behind the last step finish the gradients that wait)
-                for (int i0 = 0; i0 < most + W - 1; i0 += kAhead) {
-                    P now[kAhead], g[kAhead];
+            // kAhead steps from i0 on. KIND: kAny, or the first, a middle or the last turn of a run without a reset whose
+            // steps, and those behind them, are all there: no test between the steps (8 x 2048 x 1537 bf16, forward and
+            // backward: 147 us with the tests, 121).
+            auto turn = [&](int i0, Age& age, auto cut, auto kind) __attribute__((always_inline)) {
+                constexpr bool CUT = decltype(cut)::value;
+                constexpr int KIND = decltype(kind)::value;
+                P now[kAhead], g[kAhead];
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) now[i] = nx[i], g[i] = ng[i];
+                for (int i = 0; i < kAhead; ++i) now[i] = nx[i], g[i] = ng[i];
+                if constexpr (KIND == kAny) {
                     if (i0 + kAhead < steps) fetch(i0 + kAhead);
-                    Line line[kV][kAhead / Q];
-                    if constexpr (STEPS_OUT) {
+                } else if constexpr (KIND != kLast) {
+                    const S* px = x + (t0 + i0 + kAhead) * p.sx_r;
+                    const S* pg = dy + (t0 + i0 + kAhead) * p.sg_r;
 #pragma unroll
-                        for (int v = 0; v < kV; ++v)
-#pragma unroll
-                            for (int h = 0; h < kAhead / Q; ++h)
-                                line[v][h] = tile[(pair * kV + v) * SLOTS + ((wave * QPI + i0 / Q + h) ^ (pair & (SLOTS - 1)))];
+                    for (int i = 0; i < kAhead; ++i, px += p.sx_r, pg += p.sg_r) {
+                        nx[i] = cols.load(px);
+                        if constexpr (!STEPS_OUT) ng[i] = cols.load(pg);
                     }
+                }
+                Line line[kV][kAhead / Q];
+                if constexpr (STEPS_OUT) {
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        if constexpr (decltype(cut)::value) age.next();
-                        const bool in = i0 + i < steps, own = i0 + i < most;
+                    for (int v = 0; v < kV; ++v)
 #pragma unroll
-                        for (int v = 0; v < kV; ++v) {
+                        for (int h = 0; h < kAhead / Q; ++h)
+                            line[v][h] = tile[(pair * kV + v) * SLOTS + ((wave * QPI + i0 / Q + h) ^ (pair & (SLOTS - 1)))];
+                }
+                S* pd = dx + (t0 + i0 - (W - 1)) * p.sd_r;
 #pragma unroll
-                            for (int j = W - 1; j > 0; --j) {
-                                seen[j][v] = !decltype(cut)::value || j <= age.age ? seen[j - 1][v] : 0.0f;
-                                dv[j][v] = dv[j - 1][v];
-                            }
-                            seen[0][v] = to_f32(now[i].v[v]);
-                            dv[0][v] = 0.0f;
-                            float pre = b[v];
+                for (int i = 0; i < kAhead; ++i, pd += p.sd_r) {
+                    if constexpr (CUT) age.next();
+                    const bool in = KIND != kAny || i0 + i < steps;
+                    const bool own = KIND == kAny ? i0 + i < most : KIND != kLast || i < kAhead - (W - 1);
 #pragma unroll
-                            for (int j = W - 1; j >= 0; --j) pre = __builtin_fmaf(w[v][W - 1 - j], seen[j][v], pre);
-                            float gv;
-                            if constexpr (STEPS_OUT) gv = to_f32(line[v][i / Q].v[i % Q]);
-                            else gv = to_f32(g[i].v[v]);
-                            const float d = in ? gv * dact_f(pre, p.silu) : 0.0f;
+                    for (int v = 0; v < kV; ++v) {
 #pragma unroll
-                            for (int j = 0; j < W; ++j)
-                                dv[j][v] = __builtin_fmaf(w[v][W - 1 - j], !decltype(cut)::value || j <= age.age ? d : 0.0f, dv[j][v]);
-                            if (own) {
-                                db[v] += d;
-#pragma unroll
-                                for (int j = 0; j < W; ++j) dw[v][W - 1 - j] = __builtin_fmaf(d, seen[j][v], dw[v][W - 1 - j]);
-                            }
+                        for (int j = W - 1; j > 0; --j) {
+                            seen[j][v] = !CUT || j <= age.age ? seen[j - 1][v] : 0.0f;
+                            dv[j][v] = dv[j - 1][v];
                         }
-                        const int s = i0 + i - (W - 1);
+                        seen[0][v] = to_f32(now[i].v[v]);
+                        dv[0][v] = 0.0f;
+                        float pre = b[v];
+#pragma unroll
+                        for (int j = W - 1; j >= 0; --j) pre = __builtin_fmaf(w[v][W - 1 - j], seen[j][v], pre);
+                        float gv;
+                        if constexpr (STEPS_OUT) gv = to_f32(line[v][i / Q].v[i % Q]);
+                        else gv = to_f32(g[i].v[v]);
+                        const float d = in ? gv * dact_f(pre, p.silu) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < W; ++j)
+                            dv[j][v] = __builtin_fmaf(w[v][W - 1 - j], !CUT || j <= age.age ? d : 0.0f, dv[j][v]);
+                        if (own) {
+                            db[v] += d;
+#pragma unroll
+                            for (int j = 0; j < W; ++j) dw[v][W - 1 - j] = __builtin_fmaf(d, seen[j][v], dw[v][W - 1 - j]);
+                        }
+                    }
+                    const int s = i0 + i - (W - 1);
+                    if (KIND == kAny || (KIND == kFirst && i < W - 1)) {
                         if (s < most && (s >= 0 || t0 == 0)) emit(t0 + s, dv[W - 1]);
+                    } else {
+                        P r;
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) r.v[v] = from_f32<S>(dv[W - 1][v]);
+                        cols.store(pd, r);
                     }
                 }
             };
-            if (mask == 0) run(std::false_type{});
-            else run(std::true_type{});
+            Age age(mask);
+            if (mask == 0 && steps == kRowRun) {
+                turn(0, age, std::false_type{}, std::integral_constant<int, kFirst>{});
+                for (int i0 = kAhead; i0 < kRowRun - kAhead; i0 += kAhead) turn(i0, age, std::false_type{}, std::integral_constant<int, kMiddle>{});
+                turn(kRowRun - kAhead, age, std::false_type{}, std::integral_constant<int, kLast>{});
+            } else {
+                // (the W - 1 steps behind the last one finish the gradients that wait)
+                for (int i0 = 0; i0 < most + W - 1; i0 += kAhead) turn(i0, age, std::true_type{}, std::integral_constant<int, kAny>{});
+            }
         }
         if constexpr (STEPS_OUT) __syncthreads();
     }
