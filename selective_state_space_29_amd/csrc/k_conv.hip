@@ -17,7 +17,8 @@
 // Bound by HBM, each value read and written once; the weight's gradient is summed in registers over a workgroup's
 // runs, then over its waves in order, and a second kernel adds the workgroups'. 8 x 2048 x 1536 bf16: forward 21.8 us
 // (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 41.5 + 4.8 (151 MB, 3.6; the
-// vector instructions alone 22); in the scan's layout 27 and 70. 3 x 2777 x 1001 fp32 in the scan's layout 18 and 28.
+// vector instructions alone 22); in the scan's layout 21 and 66 (in the latter the
+// vector instructions take 40, a third of them a turn's loads and a workgroup's sums). 3 x 2777 x 1001 fp32 in the scan's layout 17 and 30.
 // One step of 32 x 1536: 3.6.
 #include <type_traits>
 
@@ -479,38 +480,56 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(S) == 2 ? 4 : 1) void conv_rows
 
 // ---- steps side by side ----
 
-// kRun + M values of a channel from step t0 - B on, zeros outside the sequence.
-template <typename S, int B, int N>
-__device__ __forceinline__ void load_line(const S* row, int t0, int len, float (&to)[N]) {
-    static_assert(N % 4 == 0);
-#pragma unroll
-    for (int h = 0; h < N / 4; ++h) {
-        const int t = t0 - B + 4 * h;
-        const Pack<S, 4> r = load_some<S, 4>(row + t, t < 0 ? 0 : len - t);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) to[4 * h + k] = to_f32(r.v[k]);
+// n / d for n below 2^31, by the product with a rounded-up 2^(31 + s) / d, s = ceil(log2 d): m = (2^(31 + s) + e) / d
+// with e < d <= 2^s adds less than 1 / d to the quotient, which the floor drops.
+struct Div {
+    uint32_t d, m, s;
+    explicit Div(int64_t by) : d((uint32_t)by), m(0), s(0) {
+        while (((int64_t)1 << s) < by) ++s;
+        if (s) m = (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d);
     }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return s ? __umulhi(n, m) >> (s - 1) : n; }
+};
+
+// A whole run in one access, without a test of its own where every lane of the wave has one.
+template <typename S>
+__device__ __forceinline__ Pack<S, kRun> load_run(const S* p, int n, bool whole) {
+    Pack<S, kRun> r;
+    if (whole) __builtin_memcpy(&r, p, sizeof(r));
+    else r = load_some<S, kRun>(p, n);
+    return r;
 }
 
-template <typename S, int W>
-__global__ __launch_bounds__(kConvThreads) void conv_steps_fwd_kernel(ConvArgs p, int64_t total) {
+// SMALL: fewer than 2^31 runs in all.
+template <typename S, int W, bool SMALL>
+__global__ __launch_bounds__(kConvThreads) void conv_steps_fwd_kernel(ConvArgs p, int64_t total, Div by_runs, Div by_dim) {
     const int64_t id = grid_block() * kConvThreads + threadIdx.x;
     if (id >= total) return;
     const int len = (int)p.len;
     // rows (batch, channel) one after another, each of `runs` runs
-    const int64_t row = id / p.runs;
+    const int64_t row = SMALL ? by_runs((uint32_t)id) : id / p.runs;
     const int t0 = (int)(id - row * p.runs) * kRun;
-    const int64_t bt = row / p.dim, c = row - bt * p.dim;
+    const int64_t bt = SMALL ? by_dim((uint32_t)row) : row / p.dim, c = row - bt * p.dim;
     const S* x = static_cast<const S*>(p.x) + bt * p.sx_b + c * p.sx_r;
+    const uint8_t* reset = p.reset ? p.reset + bt * p.len : nullptr;
+    const bool whole = __ballot(t0 + kRun > len) == 0;
+    const Pack<S, kRun> now = load_run<S>(x + t0, len - t0, whole);
+    const Pack<S, 4> before = load_some<S, 4>(x + t0 - 4, t0 > 0 ? 4 : 0);
+    const uint32_t bits = reset_bits(reset, t0, len);
+    float w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = p.w[c * W + k];
+    const float b = p.b ? p.b[c] : 0.0f;
     float in[4 + kRun];  // steps t0 - 4 ..
-    load_line<S, 4>(x, t0, len, in);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in[i] = to_f32(before.v[i]);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) in[4 + i] = to_f32(now.v[i]);
     const int64_t st = bt * (W - 1) * p.dim + c;
     if (t0 == 0 && p.state) {
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) in[4 - (W - 1) + i] = to_f32(static_cast<const S*>(p.state)[st + i * p.dim]);
     }
-    const uint8_t* reset = p.reset ? p.reset + bt * p.len : nullptr;
-    const uint32_t bits = reset_bits(reset, t0, len);
     if (t0 == 0 && p.last) {
         S* last = static_cast<S*>(p.last) + st;
 #pragma unroll
@@ -528,20 +547,23 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_fwd_kernel(ConvArgs p
             last[j * p.dim] = from_f32<S>(r);
         }
     }
-    float w[W];
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = p.w[c * W + k];
-    const float b = p.b ? p.b[c] : 0.0f;
     Pack<S, kRun> out;
+    auto run = [&](auto cut) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        const int age = age_of(bits, 8 + i);
-        float pre = b;
+        for (int i = 0; i < kRun; ++i) {
+            const int age = age_of(bits, 8 + i);
+            float pre = b;
 #pragma unroll
-        for (int j = W - 1; j >= 0; --j) pre = __builtin_fmaf(w[W - 1 - j], j <= age ? in[4 + i - j] : 0.0f, pre);
-        out.v[i] = from_f32<S>(act_f(pre, p.silu));
-    }
-    store_some<S, kRun>(static_cast<S*>(p.y) + bt * p.sy_b + c * p.sy_r + t0, out, len - t0);
+            for (int j = W - 1; j >= 0; --j)
+                pre = __builtin_fmaf(w[W - 1 - j], !decltype(cut)::value || j <= age ? in[4 + i - j] : 0.0f, pre);
+            out.v[i] = from_f32<S>(act_f(pre, p.silu));
+        }
+    };
+    if (__ballot(bits != 0) == 0) run(std::false_type{});
+    else run(std::true_type{});
+    S* y = static_cast<S*>(p.y) + bt * p.sy_b + c * p.sy_r + t0;
+    if (whole) __builtin_memcpy(y, &out, sizeof(out));
+    else store_some<S, kRun>(y, out, len - t0);
 }
 
 // A workgroup: one channel, every `blocks`-th stretch of its sequences' runs. A wave takes 63 runs and the one behind
@@ -564,28 +586,38 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
         Pack<S, kRun> x, g;
         uint32_t bits;
     };
+    // The item's batch and run, and how far both go from turn to turn.
     const uint32_t stride = (uint32_t)p.blocks * (kConvThreads / 64) * kOwn;
-    auto fetch = [&](uint32_t item) __attribute__((always_inline)) {
-        Run r{};
-        if (item >= p.items) return r;
-        const uint32_t bt = item / p.runs;
-        const int t0 = (int)(item - bt * p.runs) * kRun;
+    const uint32_t bt_by = stride / p.runs, run_by = stride - bt_by * p.runs;
+    uint32_t item = ((uint32_t)block * (kConvThreads / 64) + wave) * kOwn + lane;
+    uint32_t nbt = item / p.runs, nrun = item - nbt * p.runs;
+    auto fetch = [&](uint32_t it, uint32_t bt, uint32_t rn) __attribute__((always_inline)) {
+        Run r;
+        const bool in = it < p.items;
+        if (__ballot(in) == 0) return Run{};
+        if (!in) bt = 0, rn = 0;  // (reads what is there, its gradient as zeros)
+        const int t0 = (int)rn * kRun;
+        const bool whole = __ballot(t0 + kRun > len) == 0;
         const S* x = static_cast<const S*>(p.x) + bt * p.sx_b + c * p.sx_r + t0;
-        if (t0 > 0) r.before = load_some<S, 4>(x - 4, 4);
-        r.x = load_some<S, kRun>(x, len - t0);
-        r.g = load_some<S, kRun>(static_cast<const S*>(p.dy) + bt * p.sg_b + c * p.sg_r + t0, len - t0);
+        const S* g = static_cast<const S*>(p.dy) + bt * p.sg_b + c * p.sg_r + t0;
+        r.before = load_some<S, 4>(x - 4, t0 > 0 ? 4 : 0);
+        r.x = load_run<S>(x, len - t0, whole);
+        r.g = load_run<S>(g, len - t0, whole);
+        if (!in) r.g = Pack<S, kRun>{};
         r.bits = reset_bits(p.reset ? p.reset + bt * p.len : nullptr, t0, len);
         return r;
     };
-    uint32_t item = ((uint32_t)block * (kConvThreads / 64) + wave) * kOwn + lane;
-    Run next = fetch(item);
+    Run next = fetch(item, nbt, nrun);
     // (a whole wave makes the same turns: lanes read their neighbours')
     for (uint32_t first = item - lane; first < p.items; first += stride, item += stride) {
         const Run now = next;
-        next = fetch(item + stride);
         const bool in = item < p.items, own = in && lane < kOwn;
-        const uint32_t bt = in ? item / p.runs : 0;
-        const int t0 = in ? (int)(item - bt * p.runs) * kRun : len;
+        const uint32_t bt = in ? nbt : 0;
+        const int t0 = in ? (int)nrun * kRun : len;
+        nbt += bt_by, nrun += run_by;
+        if (nrun >= p.runs) nrun -= p.runs, ++nbt;
+        next = fetch(item + stride, nbt, nrun);
+        const bool whole = __ballot(in && t0 + kRun > len) == 0;
         float v[4 + kRun];  // values of steps t0 - 4 ..
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = to_f32(now.before.v[i]);
@@ -608,8 +640,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
                 dv[i] = to_f32(static_cast<const S*>(p.dlast)[st + j * p.dim]);
             }
         }
-        auto run = [&](auto cut) __attribute__((always_inline)) {
-            constexpr bool CUT = decltype(cut)::value;
+        auto run = [&](auto cut, auto inside) __attribute__((always_inline)) {
+            constexpr bool CUT = decltype(cut)::value, INSIDE = decltype(inside)::value;
             float d[kRun + W - 1];
 #pragma unroll
             for (int i = 0; i < kRun; ++i) {
@@ -620,12 +652,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
                     seen[j] = !CUT || j <= age ? v[4 + i - j] : 0.0f;
                     pre = __builtin_fmaf(w[W - 1 - j], seen[j], pre);
                 }
-                d[i] = t0 + i < len ? to_f32(now.g.v[i]) * dact_f(pre, p.silu) : 0.0f;
-                if (own) {
-                    db += d[i];
+                d[i] = INSIDE || t0 + i < len ? to_f32(now.g.v[i]) * dact_f(pre, p.silu) : 0.0f;
+                db += d[i];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[W - 1 - j] = __builtin_fmaf(d[i], seen[j], dw[W - 1 - j]);
-                }
+                for (int j = 0; j < W; ++j) dw[W - 1 - j] = __builtin_fmaf(d[i], seen[j], dw[W - 1 - j]);
             }
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
@@ -642,8 +672,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
                 }
             }
         };
-        if (__ballot(now.bits != 0) == 0) run(std::false_type{});
-        else run(std::true_type{});
+        if (whole && __ballot(now.bits != 0) == 0) run(std::false_type{}, std::true_type{});
+        else run(std::true_type{}, std::false_type{});
         if (!own) continue;
         Pack<S, kRun> out;
 #pragma unroll
@@ -657,7 +687,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_steps_bwd_kernel(ConvBwdArg
     __shared__ float sums[kConvThreads / 64][kMaxWidth + 1];
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
-        const float s = wave_sum(k < W ? dw[k < W ? k : 0] : db);
+        const float s = wave_sum(lane < kOwn ? k < W ? dw[k < W ? k : 0] : db : 0.0f);
         if (lane == 0) sums[wave][k] = s;
     }
     __syncthreads();
@@ -705,8 +735,9 @@ int blocks_of(int64_t items, int64_t each, int64_t groups, int per_cu) {
     const int64_t n = need < most ? need : most;
     return (int)(n < 1 ? 1 : n);
 }
-// (rows, gradient: 66.2 us a pass at 8 x 2048 x 1536 with 4 a CU, 67.8 with 8; steps: 106 with 8, 100 with 32, 104 with 64)
-constexpr int kFwdPerCu = 8, kBwdPerCu = 4, kStepsBwdPerCu = 32;
+// (rows, gradient: 66.2 us a pass at 8 x 2048 x 1536 with 4 a CU, 67.8 with 8; steps,
+// forward and gradient: 92.8 with 12, 96.7 with 32, 118 with 48)
+constexpr int kFwdPerCu = 8, kBwdPerCu = 4, kStepsBwdPerCu = 12;
 
 int bwd_blocks(const mamba_conv_shape& s, bool x_steps) {
     const int64_t items = s.batch * runs_of(s, x_steps, true);
@@ -717,7 +748,9 @@ template <typename S, int W>
 void fwd_go(ConvArgs q, bool x_steps, bool y_steps, int64_t groups, Launches& on) {
     if (x_steps) {
         const int64_t total = q.batch * q.dim * q.runs;
-        on(conv_steps_fwd_kernel<S, W>, grid_of((total + kConvThreads - 1) / kConvThreads, kConvThreads), dim3(kConvThreads), q, total);
+        const dim3 grid = grid_of((total + kConvThreads - 1) / kConvThreads, kConvThreads);
+        if (total < (int64_t)1 << 31) on(conv_steps_fwd_kernel<S, W, true>, grid, dim3(kConvThreads), q, total, Div(q.runs), Div(q.dim));
+        else on(conv_steps_fwd_kernel<S, W, false>, grid, dim3(kConvThreads), q, total, Div(1), Div(1));
         return;
     }
     q.blocks = blocks_of(q.items, kWaves, groups, kFwdPerCu);

@@ -892,3 +892,16 @@ def test_one_tensor_in_two_roles():
     same_row = row.bfloat16().expand(7, 40)
     ids = torch.arange(7, device=DEV) % 6
     assert torch.equal(block.linear_cross_entropy_fn(same_row, leaf.detach(), ids), block.linear_cross_entropy_fn(same_row.contiguous(), leaf.detach(), ids))
+
+
+def test_conv_more_runs_than_31_bits():
+    B, L, D = 600, 2, 3600001  # 8.6 GB of bf16, a run a row
+    g = torch.Generator(device=DEV).manual_seed(66)
+    x = torch.randn(1, D, L, generator=g, device=DEV, dtype=BF16).repeat(B, 1, 1)
+    x[-1] *= 2
+    x = x.transpose(1, 2)
+    w, b = torch.randn(D, 4, generator=g, device=DEV), torch.randn(D, generator=g, device=DEV)
+    y, last = block.causal_conv_fn(x, w, b, return_last_state=True)
+    for at in (0, B - 1):
+        want, state = block.causal_conv_fn(x[at:at + 1], w, b, return_last_state=True)
+        assert torch.equal(y[at], want[0]) and torch.equal(last[at], state[0])
