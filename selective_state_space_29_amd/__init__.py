@@ -2,7 +2,9 @@
 
 ``selective_scan_fn`` (in :mod:`.scan`) is the user entry point; :mod:`.layers` has the layer
 operators around a scan (gated linear recurrence, layer norm, token embedding, gated feed-forward) with
-their gradients; :mod:`.gen` and :mod:`.workloads` provide the seeded synthetic inputs.
+their gradients, :mod:`.block` the operators of a Mamba language model around it (short causal
+convolution, one-token block step, root-mean-square norms, cross entropy over the vocabulary);
+:mod:`.gen` and :mod:`.workloads` provide the seeded synthetic inputs.
 """
 
 __all__ = ["selective_scan_fn"]

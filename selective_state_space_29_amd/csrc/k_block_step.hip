@@ -11,6 +11,9 @@
 // 0.9 MB beside 12.6 MB of scan state). In the second launch 4 lanes hold a channel, 4 of every 16 states each, so
 // that states and A move 16 bytes a lane and the sums over states and dt rows stay within a quad; everything
 // that does not depend on the first launch's sums is loaded before they are.
+//
+// Bound by latency: at 1536 channels, 16 states and 48 dt rows bf16 one stream takes 4.2 + 3.7 us, 64 streams 5.4 +
+// 6.8, of which their 15 MB need 3.3.
 #include "block_launch.hpp"
 #include "layers_common.hpp"
 #include "rows.hpp"

@@ -7,9 +7,12 @@
 // the gate where it comes last).
 //
 // A row (or one of its groups) is held in registers by LPR lanes, an eighth of a wave to 16 waves, NV packs of V
-// values a lane, so it is read once; the next row's loads are in flight while a row is worked on. Bound by HBM. The backward keeps the
-// weight's column sums in registers over a workgroup's rows and writes one row of partial sums a workgroup,
+// values a lane, so it is read once; the next row's loads are in flight while a row is worked on. The backward keeps
+// the weight's column sums in registers over a workgroup's rows and writes one row of partial sums a workgroup,
 // which a second kernel adds in order.
+//
+// Bound by HBM. 16384 x 768 bf16 with residual 25.4 us (101 MB, 4.0 TB/s); 16384 x 1536 bf16 gated 36.3 (4.2), its
+// gradient 57.6 + 4 (252 MB, 4.4); 5003 x 1001 fp32 with residual 19.8 (80 MB, 4.0), its gradient 17.2 + 3.4.
 #include "block_launch.hpp"
 #include "layers_common.hpp"
 #include "rows.hpp"

