@@ -221,8 +221,8 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
 
     Returns y (batch, len, dim) in x's dtype, its channels side by side as x's or, with ``scan_layout`` or where
     x's are not, its steps (``y.transpose(1, 2)`` is then what the scan takes as u); with ``return_last_state``
-    also the state to go on from. ``out``: y's tensor, of that layout; ``last_state_out``: the state's, which
-    may be ``initial_state`` itself (a decoder's state updated in place)."""
+    also the state to go on from. ``out``: y's tensor, of that layout; ``last_state_out``: the state's, written
+    whether it is returned or not, which may be ``initial_state`` itself (a decoder's state updated in place)."""
     lib = _load()
     dtype, act, weight, bias, state, reset, width = _conv_args(x, weight, bias, activation, initial_state, reset, "causal_conv_fn")
     whole = batch, length, dim = x.shape
@@ -236,13 +236,12 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
             raise ValueError("out must have x's shape, dtype and device")
         if y.stride(1 if y_steps else 2) != 1 and y.shape[1 if y_steps else 2] > 1:
             raise ValueError(f"out must have its {'steps' if y_steps else 'channels'} side by side, as y has")
-    last = None
-    if return_last_state:
-        last = last_state_out
-        if last is None:
+    last = last_state_out
+    if last is None:
+        if return_last_state:
             last = x.new_empty((batch, width - 1, dim))
-        elif not _is(last, (batch, width - 1, dim), x.dtype, x.get_device()):
-            raise ValueError("last_state_out must be a contiguous (batch, width - 1, dim) tensor of x's dtype and device")
+    elif not _is(last, (batch, width - 1, dim), x.dtype, x.get_device()):
+        raise ValueError("last_state_out must be a contiguous (batch, width - 1, dim) tensor of x's dtype and device")
     ys = y.stride()
     ptrs = ConvPtrs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), y.data_ptr(), _ptr(last),
                     xb, xr, ys[0], ys[2 if y_steps else 1], steps, y_steps)

@@ -905,3 +905,53 @@ def test_conv_more_runs_than_31_bits():
     for at in (0, B - 1):
         want, state = block.causal_conv_fn(x[at:at + 1], w, b, return_last_state=True)
         assert torch.equal(y[at], want[0]) and torch.equal(last[at], state[0])
+
+
+def test_conv_writes_the_state_it_is_given():
+    t = dev(conv_case(67, 3, 5, 24, 4, BF16))
+    want_y, want = block.causal_conv_fn(t["x"], t["weight"], t["bias"], initial_state=t["state"], return_last_state=True)
+    state = t["state"].clone()
+    y = block.causal_conv_fn(t["x"], t["weight"], t["bias"], initial_state=state, last_state_out=state)
+    assert torch.equal(y, want_y) and torch.equal(state, want)
+
+
+def test_step_empty():
+    z = lambda *s, dt=F32: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+    for B, D in ((0, 24), (3, 0)):
+        t = dict(x=z(B, D, dt=BF16), conv_state=z(B, 3, D, dt=BF16), ssm_state=z(B, D, 16), conv_w=z(D, 4), conv_b=None,
+                 w_x=z(35, D, dt=BF16), w_dt=z(D, 3, dt=BF16), dt_bias=None, A=z(D, 16))
+        before = t["conv_state"].clone()
+        y = block.block_step(**t)
+        assert y.shape == (B, D) and y.dtype == F32 and torch.equal(t["conv_state"], before)
+
+
+def test_parameters_in_bf16():
+    """A model cast as a whole: parameters are taken in fp32, their gradients come back in bf16."""
+    g = gen(69)
+    r = lambda *s: torch.randn(*s, generator=g).to(BF16)  # noqa: E731
+    x, z, dy, cw, cb, w = r(2, 30, 24), r(2, 30, 24), r(2, 30, 24), r(24, 1, 4), r(24), r(24)
+    a = [t.to(DEV).requires_grad_() for t in (cw, cb, w)]
+    block.causal_conv(x.to(DEV), a[0], a[1]).backward(dy.to(DEV))
+    want = ref.causal_conv(x, cw[:, 0].float(), cb.float(), None, None, "silu", dy)[2]
+    for got, k, v in ((a[0], "weight", cw), (a[1], "bias", cb)):
+        assert got.grad.dtype == BF16 and got.grad.shape == v.shape
+        close(got.grad, want[k].reshape(v.shape), room=TOL * 60 * 1e-2)
+    block.rms_norm(x.to(DEV), a[2]).backward(dy.to(DEV))
+    close(a[2].grad, ref.rms_norm(x, w, dy=dy)["weight"], room=TOL * 60 * 1e-2)
+    a[2].grad = None
+    block.gated_rms_norm(x.to(DEV), z.to(DEV), a[2], groups=3).backward(dy.to(DEV))
+    close(a[2].grad, ref.gated_rms_norm(x, z, w, groups=3, dy=dy)["weight"], room=TOL * 60 * 1e-2)
+
+
+def test_cross_entropy_of_the_next_tokens():
+    """Hidden states and targets as shifted slices of (batch, len): the last step has no next token, and no gradient."""
+    g = gen(70)
+    h = torch.randn(3, 20, 32, generator=g).to(BF16).to(DEV).requires_grad_()
+    w = torch.randn(90, 32, generator=g).to(BF16).to(DEV)
+    ids = torch.randint(0, 90, (3, 20), generator=g).to(DEV)
+    loss = block.linear_cross_entropy(h[:, :-1], w, ids[:, 1:])
+    loss.backward()
+    x = h.detach()[:, :-1].contiguous().requires_grad_()
+    want = block.linear_cross_entropy(x, w, ids[:, 1:].contiguous())
+    want.backward()
+    assert torch.equal(loss, want) and torch.equal(h.grad[:, :-1], x.grad) and not h.grad[:, -1].any()
