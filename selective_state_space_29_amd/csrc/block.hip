@@ -92,12 +92,13 @@ int mamba_conv_fwd(const mamba_conv_ptrs* p, const mamba_conv_shape* s, int act,
     if (conv_bad_shape(*s) || bad_strides(*s, p->x_steps, p->x_batch, p->x_row) || bad_strides(*s, p->y_steps, p->y_batch, p->y_row))
         return MAMBA_SCAN_ERR_SHAPE;
     if (act != MAMBA_CONV_NONE && act != MAMBA_CONV_SILU) return MAMBA_SCAN_ERR_ARGS;
+    if (conv_too_large(*s)) return MAMBA_SCAN_ERR_UNSUPPORTED;  // before its sizes are multiplied
     const int64_t es = size_of(dtype), rows = s->batch * s->dim, state = rows * (s->width - 1) * es;
     if ((rows * s->len > 0 && (!p->x || !p->y)) || (s->dim > 0 && !p->weight)) return MAMBA_SCAN_ERR_NULL;
     if (any_misaligned({p->x, p->initial_state, p->y, p->last_state}, es) || any_misaligned({p->weight, p->bias}, 4) ||
         rows_meet(*s, p->y_steps, p->y_batch, p->y_row))
         return MAMBA_SCAN_ERR_ARGS;
-    if (conv_too_large(*s) || (p->x_steps && !p->y_steps)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    if (p->x_steps && !p->y_steps) return MAMBA_SCAN_ERR_UNSUPPORTED;
     const Bytes old = flat(p->initial_state, state);
     const Bytes ins[] = {conv_bytes(p->x, es, *s, p->x_steps, p->x_batch, p->x_row), flat(p->weight, s->dim * s->width * 4),
                          flat(p->bias, s->dim * 4), flat(p->reset, s->batch * s->len)};
@@ -123,12 +124,13 @@ int mamba_conv_bwd(const mamba_conv_bwd_ptrs* p, const mamba_conv_shape* s, int 
         bad_strides(*s, p->dy_steps, p->dy_batch, p->dy_row))
         return MAMBA_SCAN_ERR_SHAPE;
     if (act != MAMBA_CONV_NONE && act != MAMBA_CONV_SILU) return MAMBA_SCAN_ERR_ARGS;
+    if (conv_too_large(*s)) return MAMBA_SCAN_ERR_UNSUPPORTED;  // before its sizes are multiplied
     const int64_t es = size_of(dtype), rows = s->batch * s->dim, state = rows * (s->width - 1) * es;
     if ((rows * s->len > 0 && (!p->x || !p->dy || !p->dx)) || (s->dim > 0 && (!p->weight || !p->dweight))) return MAMBA_SCAN_ERR_NULL;
     if (any_misaligned({p->x, p->initial_state, p->dy, p->dlast_state, p->dx, p->dinitial_state}, es) ||
         any_misaligned({p->weight, p->bias, p->dweight, p->dbias}, 4) || rows_meet(*s, p->x_steps, p->dx_batch, p->dx_row))
         return MAMBA_SCAN_ERR_ARGS;
-    if (conv_too_large(*s) || (p->x_steps && !p->dy_steps)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+    if (p->x_steps && !p->dy_steps) return MAMBA_SCAN_ERR_UNSUPPORTED;
     const int rc = check_workspace(p->workspace, p->workspace_bytes, mamba_conv_bwd_workspace_bytes(s, dtype, p->x_steps));
     if (rc != MAMBA_SCAN_OK) return rc;
     const Bytes ins[] = {conv_bytes(p->x, es, *s, p->x_steps, p->x_batch, p->x_row), flat(p->weight, s->dim * s->width * 4),
