@@ -6,6 +6,8 @@ As in :mod:`.layers`, every step runs in ``libmamba_scan.so``; this module check
 and workspaces with torch and launches on torch's current HIP stream. There is no CPU fallback. ``<name>_fn`` is
 the forward call, ``<name>_bwd`` the gradients given the incoming one, ``<name>`` the differentiable form (torch
 autograd over the two; reverse mode, first derivatives). ``block_step`` is for decoding and has no gradient.
+Every call can be captured into a HIP graph, forward and backward together too; as with any torch operator, a
+backward pass is captured only while no eager graph of the same leaves is alive.
 
 Activations are float32 or bfloat16 (the cross entropy bfloat16 only); convolution weights, norm weights,
 biases, ``A``, ``D``, scan states and statistics are taken in float32. Arithmetic is fp32; an activation's
@@ -229,7 +231,7 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
     x, xb, xr, steps = _conv_layout(x, whole)
     y_steps = 1 if steps or scan_layout else 0
     if out is None:
-        y = _new_steps(x, batch, length, dim) if y_steps else x.new_empty(whole)
+        y = _new_steps(x, batch, length, dim) if y_steps else _new_like(x, whole)
     else:
         y = out
         if y.shape != whole or y.dtype is not x.dtype or y.device != x.device:
@@ -239,7 +241,7 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
     last = last_state_out
     if last is None:
         if return_last_state:
-            last = x.new_empty((batch, width - 1, dim))
+            last = x.new_empty((batch, width - 1, dim)) if state is None else torch.empty_like(state)
     elif not _is(last, (batch, width - 1, dim), x.dtype, x.get_device()):
         raise ValueError("last_state_out must be a contiguous (batch, width - 1, dim) tensor of x's dtype and device")
     ys = y.stride()

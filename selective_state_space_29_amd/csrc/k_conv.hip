@@ -17,9 +17,9 @@
 // Bound by HBM, each value read and written once; the weight's gradient is summed in registers over a workgroup's
 // runs, then over its waves in order, and a second kernel adds the workgroups'. 8 x 2048 x 1536 bf16: forward 21.8 us
 // (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 41.5 + 4.8 (151 MB, 3.6; the
-// vector instructions alone 22); in the scan's layout 21 and 66 (in the latter the
-// vector instructions take 40, a third of them a turn's loads and a workgroup's sums). 3 x 2777 x 1001 fp32 in the scan's layout 17 and 30.
-// One step of 32 x 1536: 3.6.
+// vector instructions alone about 16); in the scan's layout 21 and 66 (in the latter the vector instructions take
+// about 30, a third of them loading a turn and joining a workgroup's sums after four or five). 3 x 2777 x 1001 fp32 in
+// the scan's layout 17 and 30. One step of 32 x 1536: 3.6.
 #include <type_traits>
 
 #include "block_launch.hpp"
