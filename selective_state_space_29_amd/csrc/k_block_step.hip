@@ -1,5 +1,5 @@
 // One token of each stream through a Mamba block's path from the convolution to the gate (mamba_block.h), on
-// gfx950, in two launches.
+// gfx950, in two launches or three.
 //
 //   first:   u = silu(conv_b + sum_k conv_w v_k) and the conv state's new rows; each workgroup's 64 channels'
 //            share of w_x u, for up to kRows streams (its part of w_x is read once for them)
@@ -12,8 +12,12 @@
 // that states and A move 16 bytes a lane and the sums over states and dt rows stay within a quad; everything
 // that does not depend on the first launch's sums is loaded before they are.
 //
+// Many streams of many channels share workgroups in the second launch, behind one that adds the shares (below).
+//
 // Bound by latency: at 1536 channels, 16 states and 48 dt rows bf16 one stream takes 4.2 + 3.7 us, 64 streams 5.4 +
 // 6.8, of which their 15 MB need 3.3.
+#include <type_traits>
+
 #include "block_launch.hpp"
 #include "layers_common.hpp"
 #include "rows.hpp"
@@ -26,6 +30,9 @@ constexpr int kCh = 64;       // channels of a workgroup, in either launch
 constexpr int kRows = 8;      // streams of a workgroup of the first launch
 constexpr int kThreads = 256;
 constexpr int kMaxJ = 512 + 2 * 256;
+constexpr int64_t kManyGroups = 512;
+
+__host__ __device__ constexpr int up4(int n) { return (n + 3) / 4 * 4; }
 
 struct StepArgs {
     const void* x;
@@ -229,12 +236,143 @@ __global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
     if (valid && q == 0) p.y[b * p.dim + d] = o;
 }
 
+// ---- many streams ----
+//
+// The shares are added once, by a kernel of their own, and a workgroup of the scan takes kRows streams of its 64
+// channels: w_dt and A are read once for them, and their states are on their way together. The sums' order is
+// step_scan_kernel's, and so are the bits. At 256 streams of 4096 channels (16 states, 128 dt rows, bf16) 19 + 5 + 59
+// us: 2.3 TB/s of states, bound by the latencies that 3 workgroups a CU expose one after another.
+
+// The chunks' shares of each stream's rows, in the order of step_scan_kernel.
+__global__ __launch_bounds__(kThreads) void step_join_kernel(StepArgs p, float* xd) {
+    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, next = p.batch * p.J;
+    if (at >= next) return;
+    const int ways = p.J <= kThreads ? kThreads / p.J : 1, per = (p.chunks + ways - 1) / ways;
+    float sum = 0.0f;
+    for (int way = 0; way < ways; ++way) {
+        const int k0 = way * per, k1 = k0 + per < p.chunks ? k0 + per : p.chunks;
+        float s = 0.0f;
+        for (int k = k0; k < k1; k += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = p.part[(k + i < k1 ? k + i : k1 - 1) * next + at];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += k + i < k1 ? v[i] : 0.0f;
+        }
+        sum = way ? sum + s : s;
+    }
+    xd[at] = sum;
+}
+
+// LDS holds each stream's dt rows, B and C padded to multiples of 4. JM: the most that it is kept for. FULL: a
+// multiple of 4 states.
+template <typename S, int JM, bool FULL>
+__global__ __launch_bounds__(kThreads) void step_scan_many_kernel(StepArgs p, const float* xd_all) {
+    __shared__ __align__(16) float xd[kRows][JM];
+    const int tid = threadIdx.x, q = tid & 3;
+    const int64_t b0 = (int64_t)(blockIdx.x / p.chunks) * kRows, d0 = (int64_t)(blockIdx.x % p.chunks) * kCh;
+    const int rows = (int)(p.batch - b0 < kRows ? p.batch - b0 : kRows);
+    const bool valid = d0 + (tid >> 2) < p.dim;
+    const int64_t d = valid ? d0 + (tid >> 2) : p.dim - 1;
+    const int N = p.dstate, R = p.rank, J = p.J, at_b = up4(R), at_c = at_b + up4(N);
+    const float* A = p.A + d * N;
+    const S* wd = static_cast<const S*>(p.w_dt) + d * R;
+    // streams past the last repeat it
+    auto cell = [&](int s) __attribute__((always_inline)) { return (b0 + (s < rows ? s : rows - 1)) * p.dim + d; };
+    Pack<float, 4> a, h[kRows];
+    auto fetch = [&](int n0) __attribute__((always_inline)) {
+        a = load_some<float, 4>(A + n0, N - n0);
+#pragma unroll
+        for (int s = 0; s < kRows; ++s) h[s] = load_some<float, 4>(p.h + cell(s) * N + n0, N - n0);
+    };
+    fetch(q * 4);
+    constexpr int AHEAD = 4;  // 64 dt rows
+    Pack<S, 4> w[AHEAD];
+    auto fetch_w = [&](int r0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) w[i] = load_some<S, 4>(wd + r0 + 16 * i, R - r0 - 16 * i);
+    };
+    fetch_w(q * 4);
+    float u[kRows], z[kRows], delta[kRows];
+#pragma unroll
+    for (int s = 0; s < kRows; ++s) {
+        u[s] = p.u[cell(s)];
+        z[s] = p.z ? to_f32(static_cast<const S*>(p.z)[(b0 + (s < rows ? s : rows - 1)) * p.sz + d]) : 0.0f;
+        delta[s] = 0.0f;
+    }
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.0f, skip = p.D ? p.D[d] : 0.0f;
+    for (int j = tid; j < at_c + up4(N); j += kThreads) {
+        const int k = j < at_b ? j : j < at_c ? j - at_b + R : j - at_c + R + N;
+        const bool in = j < at_b ? j < R : j < at_c ? j - at_b < N : j - at_c < N;
+        float v[kRows];
+#pragma unroll
+        for (int s = 0; s < kRows; ++s) v[s] = in ? xd_all[(b0 + (s < rows ? s : rows - 1)) * J + k] : 0.0f;
+#pragma unroll
+        for (int s = 0; s < kRows; ++s) xd[s][j] = v[s];
+    }
+    __syncthreads();
+
+    auto four = [&](int s, int j) __attribute__((always_inline)) { return *reinterpret_cast<const Pack<float, 4>*>(&xd[s][j]); };
+    for (int r0 = q * 4; r0 < R; r0 += 16 * AHEAD) {
+        if (r0 >= 16 * AHEAD) fetch_w(r0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int r = r0 + 16 * i;
+            if (r >= R) continue;
+#pragma unroll
+            for (int s = 0; s < kRows; ++s) {
+                const Pack<float, 4> x = four(s, r);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) delta[s] = __builtin_fmaf(to_f32(w[i].v[k]), x.v[k], delta[s]);
+            }
+        }
+    }
+    float su[kRows], o[kRows];
+#pragma unroll
+    for (int s = 0; s < kRows; ++s) {
+        delta[s] = softplus_f(quad_sum(delta[s]) + bias);
+        su[s] = delta[s] * u[s];
+        o[s] = 0.0f;
+    }
+    for (int n0 = q * 4; n0 < N; n0 += 16) {
+        if (n0 >= 16) fetch(n0);
+#pragma unroll
+        for (int s = 0; s < kRows; ++s) {
+            const Pack<float, 4> B = four(s, at_b + n0), C = four(s, at_c + n0);
+            Pack<float, 4> r{};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (FULL || n0 + k < N) {
+                    r.v[k] = __builtin_fmaf(hw_exp2(delta[s] * a.v[k] * kLog2e), h[s].v[k], su[s] * B.v[k]);
+                    o[s] = __builtin_fmaf(C.v[k], r.v[k], o[s]);
+                }
+            if (valid && s < rows) store_some<float, 4>(p.h_out + cell(s) * N + n0, r, N - n0);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kRows; ++s) {
+        float v = __builtin_fmaf(skip, u[s], quad_sum(o[s]));
+        if (p.z) v *= silu_f(z[s]);
+        if (valid && s < rows && q == s % 4) p.y[cell(s)] = v;
+    }
+}
+
 int chunks_of(const mamba_step_shape& s) { return (int)((s.dim + kCh - 1) / kCh); }
+
+// Whether kRows streams a workgroup leave enough workgroups, and the shares that every workgroup of one stream would
+// add again are many enough to pay for a launch. us a call, bf16, each stream by itself / together: 256 x 1536, J = 80
+// (47 MB of shares) 24.5 / 28.1; 256 x 2048, J = 96 (100 MB) 32.3 / 35.9; J = 193 (202 MB) 146 / 128; 128 x 4096, J =
+// 160 (335 MB) 62 / 42; 256 x 4096, J = 160 (671 MB) 127 / 81, with 128 states, J = 385, 608 / 436.
+bool many_streams(const mamba_step_shape& s) {
+    const int64_t chunks = chunks_of(s), shares = s.batch * chunks * chunks * (s.dt_rank + 2 * s.dstate) * 4;
+    return (s.batch + kRows - 1) / kRows * chunks >= kManyGroups && shares >= (int64_t)128 << 20;
+}
 
 }  // namespace
 
 int64_t block_step_workspace(const mamba_step_shape& s) {
-    return align256(s.batch * s.dim * 4) + align256((int64_t)chunks_of(s) * s.batch * (s.dt_rank + 2 * s.dstate) * 4);
+    const int64_t sums = s.batch * (s.dt_rank + 2 * s.dstate) * 4;
+    return align256(s.batch * s.dim * 4) + align256(chunks_of(s) * sums) + align256(sums);
 }
 
 int launch_block_step(const mamba_step_ptrs& p, const mamba_step_shape& s, bool bf16, hipStream_t stream) {
@@ -249,7 +387,17 @@ int launch_block_step(const mamba_step_ptrs& p, const mamba_step_shape& s, bool 
         if (s.width == 2) on(step_conv_kernel<S, 2>, first, block, q);
         else if (s.width == 3) on(step_conv_kernel<S, 3>, first, block, q);
         else on(step_conv_kernel<S, 4>, first, block, q);
-        if (s.dstate == 16 && s.dt_rank % 4 == 0) on(step_scan_kernel<S, true>, second, block, q);
+        if (many_streams(s)) {
+            float* xd = q.part + align256((int64_t)q.chunks * s.batch * q.J * 4) / 4;
+            on(step_join_kernel, dim3((unsigned)((s.batch * q.J + kThreads - 1) / kThreads)), block, q, xd);
+            const bool full = s.dstate % 4 == 0;
+            auto scan = [&](auto most) {
+                constexpr int JM = decltype(most)::value;
+                if (full) on(step_scan_many_kernel<S, JM, true>, first, block, q, static_cast<const float*>(xd));
+                else on(step_scan_many_kernel<S, JM, false>, first, block, q, static_cast<const float*>(xd));
+            };
+            up4(q.rank) + 2 * up4(q.dstate) <= 256 ? scan(std::integral_constant<int, 256>{}) : scan(std::integral_constant<int, kMaxJ>{});
+        } else if (s.dstate == 16 && s.dt_rank % 4 == 0) on(step_scan_kernel<S, true>, second, block, q);
         else on(step_scan_kernel<S, false>, second, block, q);
     };
     bf16 ? go(bf16_t{}) : go(0.0f);

@@ -955,3 +955,23 @@ def test_cross_entropy_of_the_next_tokens():
     want = block.linear_cross_entropy(x, w, ids[:, 1:].contiguous())
     want.backward()
     assert torch.equal(loss, want) and torch.equal(h.grad[:, :-1], x.grad) and not h.grad[:, -1].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,D,N,R,W", [(261, 2048, 16, 100, 4), (300, 2001, 17, 118, 3), (257, 2048, 132, 20, 2), (700, 1500, 8, 200, 4)])
+def test_step_of_many_streams(B, D, N, R, W, dtype):
+    """Batches that share workgroups: the formula's values, and the bits of the same streams a few at a time."""
+    t = step_case(71, B, D, N, R, W, dtype, gate=N != 17, optional=N != 8)
+    d = dev(t)
+    outs = dict(conv_state_out=torch.empty_like(d["conv_state"]), ssm_state_out=torch.empty_like(d["ssm_state"]))
+    y = block.block_step(**d, **outs)
+    want_y, want_conv, want_h = ref.block_step(**t)
+    close(y, want_y)
+    assert torch.equal(outs["conv_state_out"].cpu().double(), want_conv)
+    close(outs["ssm_state_out"], want_h)
+    for b in (slice(0, 5), slice(B - 21, B)):
+        part = {k: v[b].clone() if k in ("x", "z", "conv_state", "ssm_state") and v is not None else v for k, v in d.items()}
+        assert torch.equal(block.block_step(**part), y[b])
+        assert torch.equal(part["ssm_state"], outs["ssm_state_out"][b]) and torch.equal(part["conv_state"], outs["conv_state_out"][b])
+    assert torch.equal(block.block_step(**d), y)  # in place
+    assert torch.equal(d["ssm_state"], outs["ssm_state_out"]) and torch.equal(d["conv_state"], outs["conv_state_out"])
