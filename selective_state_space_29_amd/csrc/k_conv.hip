@@ -150,11 +150,11 @@ struct Cols {
     }
 };
 
-// Bit i: whether a sequence begins at step t0 - 2 + i.
+// Bit i: whether a sequence begins at step t0 - 2 + i, of a run's steps and the two before it.
 __device__ __forceinline__ uint64_t reset_mask(const uint8_t* row, int t0, int len) {
     if (!row) return 0;
-    const int t = t0 - 2 + (int)(threadIdx.x & 63);
-    return __ballot(t >= 0 && t < len && row[t] != 0);
+    const int lane = threadIdx.x & 63, t = t0 - 2 + lane;
+    return __ballot(lane < kRowRun + 2 && t >= 0 && t < len && row[t] != 0);
 }
 
 // Steps since the last reset, as a run's steps are walked through.
