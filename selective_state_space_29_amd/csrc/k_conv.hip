@@ -16,7 +16,7 @@
 //
 // Bound by HBM, each value read and written once; the weight's gradient is summed in registers over a workgroup's
 // runs, then over its waves in order, and a second kernel adds the workgroups'. 8 x 2048 x 1536 bf16: forward 21.8 us
-// (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 41.5 + 4.8 (151 MB, 3.6; the
+// (101 MB, 4.6 TB/s, a large copy's rate), into the scan's layout 24 (4.2), gradient 39.5 + 4.8 (151 MB, 3.8; the
 // vector instructions alone about 16); in the scan's layout 21 and 66 (in the latter the vector instructions take
 // about 30, a third of them loading a turn and joining a workgroup's sums after four or five). 3 x 2777 x 1001 fp32 in
 // the scan's layout 17 and 30. One step of 32 x 1536: 3.6.
@@ -705,11 +705,7 @@ __global__ __launch_bounds__(256) void conv_join_kernel(const float* part, int b
     const int64_t wide = dim * (width + 1), k = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const int g = threadIdx.x >> 5, per = (blocks + 7) / 8;
     float s = 0.0f;
-    if (k < wide) {
-        const int q1 = (g + 1) * per < blocks ? (g + 1) * per : blocks;
-#pragma unroll 8
-        for (int q = g * per; q < q1; ++q) s += part[q * wide + k];
-    }
+    if (k < wide) s = column_sum(part, wide, k, g * per, (g + 1) * per < blocks ? (g + 1) * per : blocks);
     lds[g][threadIdx.x & 31] = s;
     __syncthreads();
     if (g != 0 || k >= wide) return;

@@ -387,11 +387,7 @@ __global__ __launch_bounds__(256) void rms_cols_kernel(const float* part, int bl
     const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const int g = threadIdx.x >> 5, per = (blocks + 7) / 8;
     float s = 0.0f;
-    if (c < wide) {
-        const int q1 = (g + 1) * per < blocks ? (g + 1) * per : blocks;
-#pragma unroll 8
-        for (int q = g * per; q < q1; ++q) s += part[(int64_t)q * wide + c];
-    }
+    if (c < wide) s = column_sum(part, wide, c, g * per, (g + 1) * per < blocks ? (g + 1) * per : blocks);
     lds[g][threadIdx.x & 31] = s;
     __syncthreads();
     if (g == 0 && c < wide) {
