@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kJoinRows * kJoinWays) void xent_join_kernel(const 
                                                                         float* lse) {
     __shared__ float2 sums[kJoinWays / 4][kJoinRows];
     const int r = threadIdx.x % kJoinRows, way = threadIdx.x / kJoinRows;
-    const int64_t row = (int64_t)blockIdx.x * kJoinRows + r, at = row < rows ? row : rows - 1;
+    const int64_t row = grid_block() * kJoinRows + r, at = row < rows ? row : rows - 1;  // (2^26 rows and more: 2^32 threads)
     const int per = (tiles + kJoinWays - 1) / kJoinWays, k0 = way * per, k1 = k0 + per < tiles ? k0 + per : tiles;
     float2 v = make_float2(-__builtin_inff(), 0.0f);
     for (int k = k0; k < k1; k += 4) {
@@ -240,8 +240,8 @@ int launch_xent_fwd(const mamba_xent_ptrs& p, const mamba_xent_shape& s, bool ta
     m.scale = scale, m.target = p.loss ? p.target : nullptr, m.target64 = target64;
     m.at_target = reinterpret_cast<float*>(ws + f.at), m.part = reinterpret_cast<float*>(ws + f.part);
     run_mat<false, false, kEpiLse>(m, f.t, on);
-    on(xent_join_kernel, dim3((unsigned)((s.rows + kJoinRows - 1) / kJoinRows)), dim3(kJoinRows * kJoinWays), reinterpret_cast<const float2*>(m.part), f.t.tiles_q, s.rows,
-       static_cast<const float*>(m.at_target), p.target, (int)target64, s.vocab, p.loss, p.lse);
+    on(xent_join_kernel, grid_of((s.rows + kJoinRows - 1) / kJoinRows, kJoinRows * kJoinWays), dim3(kJoinRows * kJoinWays),
+       reinterpret_cast<const float2*>(m.part), f.t.tiles_q, s.rows, static_cast<const float*>(m.at_target), p.target, (int)target64, s.vocab, p.loss, p.lse);
     if (p.total) on(xent_total_kernel, dim3(1), dim3(1024), static_cast<const float*>(p.loss), p.target, (int)target64, s.rows, s.vocab, p.total);
     return on.status;
 }
