@@ -243,9 +243,10 @@ __global__ __launch_bounds__(kThreads) void step_scan_kernel(StepArgs p) {
 // step_scan_kernel's, and so are the bits. At 256 streams of 4096 channels (16 states, 128 dt rows, bf16) 19 + 5 + 59
 // us: 2.3 TB/s of states, bound by the latencies that 3 workgroups a CU expose one after another.
 
-// The chunks' shares of each stream's rows, in the order of step_scan_kernel.
+// The chunks' shares of each stream's rows, in the order of step_scan_kernel. (2^23 streams of up to 1024 sums: more
+// threads than a dimension of the grid counts.)
 __global__ __launch_bounds__(kThreads) void step_join_kernel(StepArgs p, float* xd) {
-    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, next = p.batch * p.J;
+    const int64_t at = grid_block() * kThreads + threadIdx.x, next = p.batch * p.J;
     if (at >= next) return;
     const int ways = p.J <= kThreads ? kThreads / p.J : 1, per = (p.chunks + ways - 1) / ways;
     float sum = 0.0f;
@@ -389,7 +390,7 @@ int launch_block_step(const mamba_step_ptrs& p, const mamba_step_shape& s, bool 
         else on(step_conv_kernel<S, 4>, first, block, q);
         if (many_streams(s)) {
             float* xd = q.part + align256((int64_t)q.chunks * s.batch * q.J * 4) / 4;
-            on(step_join_kernel, dim3((unsigned)((s.batch * q.J + kThreads - 1) / kThreads)), block, q, xd);
+            on(step_join_kernel, grid_of((s.batch * q.J + kThreads - 1) / kThreads, kThreads), block, q, xd);
             const bool full = s.dstate % 4 == 0;
             auto scan = [&](auto most) {
                 constexpr int JM = decltype(most)::value;

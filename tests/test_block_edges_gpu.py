@@ -44,3 +44,16 @@ def test_cross_entropy_more_rows_than_a_grid_counts_threads():
     want = block.linear_cross_entropy_bwd(x, w, t, small[1], torch.ones(few, device=DEV), want_dweight=False)["x"]
     got = block.linear_cross_entropy_bwd(X, w, T, lse, torch.ones(1, device=DEV).expand(rows), want_dweight=False)["x"]
     assert torch.equal(got, over(want, rows))
+
+
+def test_step_of_more_sums_than_a_grid_counts_threads():
+    batch, few, rank = 1 << 23, 97, 512  # a thread for each of the 514 sums of a stream
+    g = gen(2)
+    r = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    t = dict(x=r(few, 1), conv_state=r(few, 1, 1), ssm_state=r(few, 1, 1))
+    weights = dict(conv_w=r(1, 2), conv_b=r(1), w_x=r(rank + 2, 1), w_dt=r(1, rank) * rank ** -0.5, dt_bias=r(1), A=-torch.ones(1, 1, device=DEV))
+    many = {k: over(v, batch) for k, v in t.items()}
+    y = block.block_step(**t, **weights)
+    stale(batch, rank)
+    got = block.block_step(**many, **weights)
+    assert torch.equal(got, over(y, batch)) and torch.equal(many["ssm_state"], over(t["ssm_state"], batch))
