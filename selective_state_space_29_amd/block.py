@@ -6,6 +6,8 @@ As in :mod:`.layers`, every step runs in ``libmamba_scan.so``; this module check
 and workspaces with torch and launches on torch's current HIP stream. There is no CPU fallback. ``<name>_fn`` is
 the forward call, ``<name>_bwd`` the gradients given the incoming one, ``<name>`` the differentiable form (torch
 autograd over the two; reverse mode, first derivatives). ``block_step`` is for decoding and has no gradient.
+Tensors that a call writes in place (states, ``out``) must not want a gradient themselves; autograd sees that they
+have changed, so that a backward pass that still needs the old values is refused.
 Every call can be captured into a HIP graph, forward and backward together too; as with any torch operator, a
 backward pass is captured only while no eager graph of the same leaves is alive.
 
@@ -21,10 +23,11 @@ import functools
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from .layers import (_dtype, _f32, _grad_on, _inner, _launch, _need_gpu, _on_device, _ptr, _reset, _row_stride, _rows,
                      _same, _workspace)
-from .scan import load_library
+from .scan import load_library, refuse_graph
 
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -238,16 +241,23 @@ def causal_conv_fn(x, weight, bias=None, *, activation="silu", initial_state=Non
             raise ValueError("out must have x's shape, dtype and device")
         if y.stride(1 if y_steps else 2) != 1 and y.shape[1 if y_steps else 2] > 1:
             raise ValueError(f"out must have its {'steps' if y_steps else 'channels'} side by side, as y has")
+        refuse_graph("out", out)
     last = last_state_out
     if last is None:
         if return_last_state:
             last = x.new_empty((batch, width - 1, dim)) if state is None else torch.empty_like(state)
     elif not _is(last, (batch, width - 1, dim), x.dtype, x.get_device()):
         raise ValueError("last_state_out must be a contiguous (batch, width - 1, dim) tensor of x's dtype and device")
+    else:
+        refuse_graph("last_state_out", last)
     ys = y.stride()
     ptrs = ConvPtrs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), y.data_ptr(), _ptr(last),
                     xb, xr, ys[0], ys[2 if y_steps else 1], steps, y_steps)
     _launch("mamba_conv_fwd", x, lib.mamba_conv_fwd, ptrs, ConvShape(batch, length, dim, width), act, dtype)
+    if out is not None:
+        increment_version(out)
+    if last_state_out is not None:
+        increment_version(last)
     return (y, last) if return_last_state else y
 
 
@@ -370,6 +380,9 @@ def block_step(x, conv_state, ssm_state, conv_w, conv_b, w_x, w_dt, dt_bias, A, 
         if t is not None and not _is(t, shape, dt, dev):
             raise (TypeError if t.dtype is not dt else ValueError)(
                 f"{name} must be a contiguous {dt} tensor of shape {shape} on x's device, got {t.dtype} {tuple(t.shape)}")
+    conv_new, ssm_new = conv_state if conv_state_out is None else conv_state_out, ssm_state if ssm_state_out is None else ssm_state_out
+    refuse_graph("conv_state" if conv_state_out is None else "conv_state_out", conv_new)
+    refuse_graph("ssm_state" if ssm_state_out is None else "ssm_state_out", ssm_new)
     w_x, w_dt = _taken(w_x, "w_x", (rank + 2 * dstate, dim), xt, dev), _taken(w_dt, "w_dt", (dim, rank), xt, dev)
     if z is not None:
         z = _inner(_same(z, x, "z"))
@@ -379,11 +392,10 @@ def block_step(x, conv_state, ssm_state, conv_w, conv_b, w_x, w_dt, dt_bias, A, 
     shape, n = _step_size(batch, dim, dstate, rank, width)
     y, ws = x.new_empty((batch, dim), dtype=torch.float32), _workspace(n, "mamba_block_step_workspace_bytes", x)
     ptrs = StepPtrs(x.data_ptr(), _ptr(z), conv_state.data_ptr(), ssm_state.data_ptr(), conv_w.data_ptr(), _ptr(conv_b),
-                    w_x.data_ptr(), w_dt.data_ptr(), _ptr(dt_bias), A.data_ptr(), _ptr(D),
-                    (conv_state if conv_state_out is None else conv_state_out).data_ptr(),
-                    (ssm_state if ssm_state_out is None else ssm_state_out).data_ptr(), y.data_ptr(), _row_stride(x),
-                    0 if z is None else _row_stride(z), _ptr(ws), n)
+                    w_x.data_ptr(), w_dt.data_ptr(), _ptr(dt_bias), A.data_ptr(), _ptr(D), conv_new.data_ptr(), ssm_new.data_ptr(),
+                    y.data_ptr(), _row_stride(x), 0 if z is None else _row_stride(z), _ptr(ws), n)
     _launch("mamba_block_step", x, _load().mamba_block_step, ptrs, shape, dtype)
+    increment_version((conv_new, ssm_new))
     return y
 
 

@@ -393,6 +393,12 @@ def refuse_tangents(inputs, entry):
         raise NotImplementedError(f"{entry} has no forward-mode derivative (an input has a tangent)")
 
 
+def refuse_graph(name, t):
+    """Raise where a tensor that a call is to write in place wants a gradient, which would go past what is written."""
+    if t is not None and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} is written in place and must not want a gradient (outside torch.no_grad())")
+
+
 class SelectiveScan(torch.autograd.Function):
     """y (and last_state) = selective_scan(...) with a backward pass through ``mamba_scan_bwd``.
 

@@ -57,3 +57,61 @@ def test_step_of_more_sums_than_a_grid_counts_threads():
     stale(batch, rank)
     got = block.block_step(**many, **weights)
     assert torch.equal(got, over(y, batch)) and torch.equal(many["ssm_state"], over(t["ssm_state"], batch))
+
+
+def moved(call, *tensors):
+    """Whether the call advances the versions of all the tensors (by which autograd sees a change in place)."""
+    before = [t._version for t in tensors]
+    call()
+    return [t._version > v for t, v in zip(tensors, before)]
+
+
+def step_inputs():
+    g = gen(3)
+    r = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    return dict(x=r(3, 24), conv_state=r(3, 3, 24), ssm_state=r(3, 24, 16), conv_w=r(24, 4), conv_b=r(24), w_x=r(36, 24), w_dt=r(24, 4),
+                dt_bias=r(24), A=-torch.rand(24, 16, generator=g).to(DEV))
+
+
+def test_autograd_sees_what_the_block_operators_write():
+    t = step_inputs()
+    state, ssm = t["conv_state"], t["ssm_state"]
+    assert moved(lambda: block.block_step(**t), state, ssm) == [True, True]
+    out = dict(conv_state_out=torch.empty_like(state), ssm_state_out=torch.empty_like(ssm))
+    assert moved(lambda: block.block_step(**t, **out), state, ssm, *out.values()) == [False, False, True, True]
+    x, w = torch.randn(3, 7, 24, device=DEV), t["conv_w"]
+    y, last = torch.empty_like(x), torch.empty_like(state)
+    assert moved(lambda: block.causal_conv_fn(x, w, out=y), x, y) == [False, True]
+    assert moved(lambda: block.causal_conv_fn(x, w, initial_state=state, last_state_out=last), state, last) == [False, True]
+    assert moved(lambda: block.causal_conv_fn(x, w, initial_state=state, last_state_out=state), state) == [True]
+    # a state that a backward pass still needs
+    leaf = x.clone().requires_grad_()
+    for change in (lambda: block.causal_conv_fn(x, w, initial_state=state, last_state_out=state), lambda: block.block_step(**t)):
+        y = block.causal_conv(leaf, w, initial_state=state)
+        change()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+
+
+def test_block_operators_write_no_tensor_that_wants_a_gradient():
+    """Its gradient would go past what was written; without a graph, or without grad mode, the call is taken."""
+    t = step_inputs()
+    x, w, state = torch.randn(3, 7, 24, device=DEV), t["conv_w"], t["conv_state"].clone()
+    kept = {k: t[k].clone() for k in ("conv_state", "ssm_state")}
+    calls = {"conv_state": lambda s: block.block_step(**dict(t, conv_state=s)), "ssm_state": lambda s: block.block_step(**dict(t, ssm_state=s)),
+             "conv_state_out": lambda s: block.block_step(**t, conv_state_out=s), "ssm_state_out": lambda s: block.block_step(**t, ssm_state_out=s),
+             "last_state_out": lambda s: block.causal_conv_fn(x, w, last_state_out=s), "out": lambda s: block.causal_conv_fn(x, w, out=s)}
+    for name, call in calls.items():
+        like = x if name == "out" else kept["ssm_state" if name.startswith("ssm") else "conv_state"]
+        for s in (like.clone().requires_grad_(), like.clone().requires_grad_() * 1):
+            with pytest.raises(ValueError, match=f"{name} .*gradient"):
+                call(s)
+            assert torch.equal(s, like) and all(torch.equal(t[k], v) for k, v in kept.items())
+            with torch.no_grad():
+                call(s)
+            assert not torch.equal(s, like)
+            t.update({k: v.clone() for k, v in kept.items()})
+    with torch.inference_mode():
+        s = torch.zeros_like(state)
+        block.causal_conv_fn(x, w, last_state_out=s)
+        assert bool(s.any())
