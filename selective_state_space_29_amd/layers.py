@@ -20,8 +20,9 @@ import ctypes
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
-from .scan import BF16, F32, _raise, load_library, refuse_tangents
+from .scan import BF16, F32, _raise, load_library, refuse_graph, refuse_tangents
 
 _I64 = ctypes.c_int64
 _P = ctypes.c_void_p
@@ -278,7 +279,8 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
     Returns y in x's dtype and, with ``return_last_state``, the fp32 state after the last step.
     ``checkpoints_out``: contiguous fp32 tensor of ``gated_checkpoint_shape`` that receives the states
     ``gated_scan_bwd(checkpoints=)`` starts from. ``out``: y's tensor; ``last_state_out``: the final
-    state's, which may be ``h0`` itself (a decoder's state updated in place).
+    state's, which may be ``h0`` itself (a decoder's state updated in place). Autograd sees that these three have
+    changed; they must not want a gradient themselves.
     """
     lib = _load()
     dtype, x, r, i, lam, h0, reset = _gated_inputs(x, r, i, lam, h0, reset, "gated_scan_fn")
@@ -290,6 +292,7 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
         y = out
         if y.shape != x.shape or y.dtype is not x.dtype or y.device != x.device or (dim > 1 and y.stride(2) != 1):
             raise ValueError("out must have x's shape, dtype and device and unit stride along dim")
+        refuse_graph("out", out)
     last = None
     if return_last_state:
         last = last_state_out
@@ -297,8 +300,11 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
             last = x.new_empty((batch, dim), dtype=torch.float32)
         elif last.shape != (batch, dim) or last.dtype is not torch.float32 or last.device != x.device or not last.is_contiguous():
             raise ValueError("last_state_out must be a contiguous float32 (batch, dim) tensor on x's device")
+        else:
+            refuse_graph("last_state_out", last)
     if checkpoints_out is not None:
         _check_gated_checkpoints(checkpoints_out, x)
+        refuse_graph("checkpoints_out", checkpoints_out)
     shape = GatedShape(batch, length, dim)
     ys = y.stride()
     ptrs = GatedPtrs(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _ptr(h0), _ptr(reset), y.data_ptr(), _ptr(last),
@@ -306,6 +312,12 @@ def gated_scan_fn(x, r, i, lam, *, c=8.0, h0=None, reset=None, return_last_state
     st = GatedStrides(*xs, *rs, *is_, ys[0], ys[1])
     _launch_maybe_workspace("mamba_gated_scan_fwd", x, lib.mamba_gated_scan_fwd,
                             lambda: _on_device(x, lib.mamba_gated_workspace_bytes, shape, dtype), ptrs, shape, st, c, dtype)
+    if out is not None:
+        increment_version(out)
+    if return_last_state and last_state_out is not None:
+        increment_version(last)
+    if checkpoints_out is not None:
+        increment_version(checkpoints_out)
     return (y, last) if return_last_state else y
 
 

@@ -18,6 +18,7 @@ import os
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmamba_scan.so")
@@ -245,9 +246,14 @@ def selective_scan_fn(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_
     states) or "step" (short calls such as decode, at most 64 steps; 16 states).
     ``checkpoints_out``: a contiguous fp32 (batch, dim, ceil(L/16), N) tensor that receives the
     state before every 16-step segment, for ``selective_scan_bwd(checkpoints=...)``
-    (lane-per-state and chunked kernels only).
+    (lane-per-state and chunked kernels only). Autograd sees that ``out``, ``last_state_out`` and
+    ``checkpoints_out`` have changed; they must not want a gradient themselves.
     """
     lib = load_library()
+    given = [(n, t) for n, t in (("out", out), ("last_state_out", last_state_out if return_last_state else None),
+                                 ("checkpoints_out", checkpoints_out)) if t is not None]
+    for name, t in given:
+        refuse_graph(name, t)
     ptrs, shape, st, dtype, flags, y, ls, ws, keep = _fwd_args(
         u, delta, A, B, C, D, z, delta_bias, delta_softplus, return_last_state, h0, kernel, out,
         last_state_out, zoh_b, checkpoints_out)
@@ -259,6 +265,7 @@ def selective_scan_fn(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_
     del keep
     if rc != 0:
         _raise(rc)
+    increment_version([t for _, t in given])
     if ws is not None and checkpoints_out is None:
         ws.record_stream(torch.cuda.current_stream(dev))
     return (y, ls) if return_last_state else y
@@ -488,6 +495,8 @@ def block_upstream(x, conv_w, conv_b, w_x, w_dt, dstate, dt_rank, out=None):
         delta = torch.empty_like(x)
     else:
         u, xdbl, delta = out
+        for t in out:
+            refuse_graph("out", t)
     ptrs = UpPtrs(_ptr(x), _ptr(conv_w), _ptr(conv_b), _ptr(w_x), _ptr(w_dt), _ptr(u), _ptr(xdbl), _ptr(delta))
     shape = UpShape(batch, dim, L, dstate, dt_rank, conv_w.shape[1])
     with torch.cuda.device(x.device):
@@ -495,6 +504,8 @@ def block_upstream(x, conv_w, conv_b, w_x, w_dt, dstate, dt_rank, out=None):
                                       torch.cuda.current_stream(x.device).cuda_stream)
     if rc != 0:
         _raise(rc, "mamba_block_upstream")
+    if out is not None:
+        increment_version(list(out))
     return u, xdbl, delta
 
 
