@@ -62,11 +62,11 @@ __global__ __launch_bounds__(kJoinRows * kJoinWays) void xent_join_kernel(const 
     if (threadIdx.x >= kJoinRows || row >= rows) return;
 #pragma unroll
     for (int k = 1; k < kJoinWays / 4; ++k) v = join_pair(v, sums[k][r]);
-    const float s = (v.x + hw_log2(v.y)) * kLn2;
-    if (lse) lse[row] = s;
-    if (loss) {
+    const float s = hw_log2(v.y) * kLn2;
+    if (lse) lse[row] = v.x + s;
+    if (loss) {  // (a difference of logits, and the rest: the largest cancels whole)
         const int64_t t = target_of(target, target64, row);
-        loss[row] = t >= 0 && t < vocab ? s - at_target[row] : 0.0f;
+        loss[row] = t >= 0 && t < vocab ? v.x - at_target[row] + s : 0.0f;
     }
 }
 

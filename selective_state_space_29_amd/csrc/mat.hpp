@@ -101,10 +101,10 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 }
 __device__ __forceinline__ float half_f32(uint32_t w, int k) { return __uint_as_float(k ? w & 0xFFFF0000u : w << 16); }
 
-// Two pairs {maximum, sum of powers of 2 from it} as one. A maximum drops a NaN, but the sum keeps it.
+// Two pairs {maximum, sum of exponentials from it} as one. A maximum drops a NaN, but the sum keeps it.
 __device__ __forceinline__ float2 join_pair(float2 a, float2 b) {
     const float top = __builtin_fmaxf(a.x, b.x);
-    const float fa = a.x == top ? a.y : a.y * hw_exp2(a.x - top), fb = b.x == top ? b.y : b.y * hw_exp2(b.x - top);
+    const float fa = a.x == top ? a.y : a.y * hw_exp2((a.x - top) * kLog2e), fb = b.x == top ? b.y : b.y * hw_exp2((b.x - top) * kLog2e);
     return make_float2(top, fa + fb);
 }
 
@@ -337,22 +337,22 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
     // A lane holds q = q0 + q_row(t) + 4 (lane / 16) .. + 3 of p = p0 + p_row(t) + lane % 16.
     const int lq = 4 * (lane >> 4), lp = lane & 15;
     if constexpr (EPI == kEpiLse) {
-        // Maximum and sum of powers of 2 of the tile's columns, of each row: first in each of the 4 WQ lanes that hold
-        // a part of the row, then over them. With an infinite maximum the powers are taken as they are: a sum of
-        // zeros, infinity or NaN is then the row's. (Of a tile's 26 us at dim 768 this takes about 3, VALU instructions,
-        // a third of them the exponentials; with the lanes joined by shuffles it took 5.)
+        // Maximum and sum of exponentials of the tile's columns, of each row: first in each of the 4 WQ lanes that hold a
+        // part of the row, then over them. The maximum stays a logit and is subtracted before the exponential's factor, so
+        // that the largest term is 1 and a loss at the maximum has its own digits. With an infinite maximum the
+        // exponentials are taken as they are: a sum of zeros, infinity or NaN is then the row's. (Of a tile's 26 us at dim
+        // 768 this takes about 3, VALU instructions, a third of them the exponentials; with the lanes joined by shuffles it
+        // took 5.)
         constexpr int PARTS = 4 * WQ;
         float2(*sums)[TP] = reinterpret_cast<float2(*)[TP]>(&lds[0]);
         int* rel_of = reinterpret_cast<int*>(&sums[PARTS][0]);  // each row's target as a column of this tile, or -1
         static_assert(PARTS * TP * 8 + TP * 4 <= STAGES * 2 && NT >= TP);
-        float s2 = m.scale * kLog2e;
         const bool whole = q0 + TQ <= m.Q;
-        if (s2 == 0.0f) {  // logits of 0 (or NaN), which a column past the last must not turn into 0 times infinity
+        if (m.scale != 1.0f) {
 #pragma unroll
             for (int q = 0; q < QT; ++q)
 #pragma unroll
-                for (int p = 0; p < PT; ++p) acc[q][p] *= s2;
-            s2 = 1.0f;
+                for (int p = 0; p < PT; ++p) acc[q][p] *= m.scale;
         }
         __syncthreads();  // every wave has read its last fragments
         if (tid < TP) rel_of[tid] = target >= q0 && target < q0 + TQ && target < m.Q && p0 + tid < m.P ? (int)(target - q0) : -1;
@@ -367,35 +367,25 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
                 for (int q = 0; q < QT; ++q)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (q_row(q) + lq + j == rel[p]) m.at_target[p0 + p_row(p) + lp] = acc[q][p][j] * m.scale;
+                        if (q_row(q) + lq + j == rel[p]) m.at_target[p0 + p_row(p) + lp] = acc[q][p][j];
             }
-            // the largest logit is that of the largest product, or of the smallest where scale is negative
             if (!whole) {
-                const float none = s2 < 0.0f ? __builtin_inff() : -__builtin_inff();
 #pragma unroll
                 for (int q = 0; q < QT; ++q)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[q][p][j] = q0 + q_row(q) + lq + j < m.Q ? acc[q][p][j] : none;
+                    for (int j = 0; j < 4; ++j) acc[q][p][j] = q0 + q_row(q) + lq + j < m.Q ? acc[q][p][j] : -__builtin_inff();
             }
             float top = acc[0][p][0];
-            if (s2 < 0.0f) {
 #pragma unroll
-                for (int q = 0; q < QT; ++q)
+            for (int q = 0; q < QT; ++q)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) top = __builtin_fminf(top, acc[q][p][j]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < QT; ++q)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, acc[q][p][j]);
-            }
-            top *= s2;
+                for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, acc[q][p][j]);
             const float base = __builtin_fabsf(top) == __builtin_inff() ? 0.0f : top;
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < QT; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += hw_exp2(__builtin_fmaf(acc[q][p][j], s2, -base));
+                for (int j = 0; j < 4; ++j) s[j] += hw_exp2((acc[q][p][j] - base) * kLog2e);
             sums[wq * 4 + (lane >> 4)][p_row(p) + lp] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
         }
         __syncthreads();
@@ -405,7 +395,7 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) r[k] = sums[k][tid], top = __builtin_fmaxf(top, r[k].x);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) s += r[k].x == top ? r[k].y : r[k].y * hw_exp2(r[k].x - top);
+            for (int k = 0; k < PARTS; ++k) s += r[k].x == top ? r[k].y : r[k].y * hw_exp2((r[k].x - top) * kLog2e);
             reinterpret_cast<float2*>(m.part)[q0 / TQ * m.P + p0 + tid] = make_float2(top, s);
         }
     } else if constexpr (EPI == kEpiPartial || EPI == kEpiAdd) {

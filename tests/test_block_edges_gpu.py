@@ -7,6 +7,7 @@ Bars stand beside the tests that need one; elsewhere results are the bits of a s
 import pytest
 import torch
 
+import block_ref as ref
 from selective_state_space_29_amd import block, layers, scan
 
 pytestmark = pytest.mark.gpu
@@ -149,3 +150,46 @@ def test_autograd_sees_what_the_scans_write():
         layers.gated_scan_fn(x, gate, inp, lam, return_last_state=True, last_state_out=h.clone().requires_grad_())
     with pytest.raises(ValueError, match="out .*gradient"):
         scan.block_upstream(*up, 16, 8, out=[outs[0].clone().requires_grad_(), *outs[1:]])
+
+
+def exact_logits(seed, scale=1.0):
+    """Hidden states and an output matrix whose products are multiples of 1/8 below 2^11, exact in fp32 in any order. Of
+    each row one column stands out, by hundreds; a quarter of the rows have a second one nearby."""
+    g = gen(seed)
+    M, K, V = 200, 64, 1000
+    w = torch.randint(-8, 9, (V, K), generator=g).double()
+    w[V // 2:] = torch.randint(-8, 9, (V // 2, K), generator=g)
+    top = torch.randint(0, V // 2, (M,), generator=g)
+    x = 2 * w[top]
+    near = torch.arange(M) % 4 == 0
+    w[V // 2:V // 2 + M] = w[top]
+    w[V // 2:V // 2 + M, 0] -= torch.where(x[:, 0] > 0, 1.0, -1.0)  # below by |x_0| / 8
+    for k in range(M):  # the copies of the other rows' columns are out of the way
+        if not near[k]:
+            w[V // 2 + k] = 0
+    target = torch.where(torch.arange(M) % 8 == 4, (top + 7) % (V // 2), top)
+    target[::16] = V // 2 + torch.arange(M)[::16]  # the second one
+    return x.to(BF16), (w / 8).to(BF16), target
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.5, -1.0, 0.7])
+def test_cross_entropy_digits_of_confident_rows(scale):
+    """The largest logit cancels: a loss has its own last digits, not those of logits of hundreds.
+
+    Bar. Logits are exact, or rounded once by scale; with the target's the largest, its difference from the largest is 0.
+    A sum of powers is 1 and up; 16 terms in a lane and at most 14 joins around it (lanes, tiles, stretches) each add half
+    a unit of it at most, and its logarithm one: 32 2^-24 (1 + loss). Where the target's logit is another than the largest, or
+    another column is near, the difference of two logits has two roundings by a scale that is no power of 2: 2^-23 of it."""
+    x, w, target = exact_logits(5)
+    if scale < 0:
+        x = -x
+    loss, lse, _ = ref.linear_cross_entropy(x, w, target, scale, torch.ones(len(target)))
+    got, got_lse = (t.cpu().double() for t in block.linear_cross_entropy_fn(x.to(DEV), w.to(DEV), target.to(DEV), scale=scale, return_lse=True))
+    logits = scale * x.double() @ w.double().t()
+    largest = logits.gather(1, target[:, None])[:, 0] == logits.amax(1)
+    assert int(largest.sum()) > 100 and float(lse.max()) > 150
+    alone = largest & (torch.exp(logits.amax(1) - lse) > 1 - 1e-12)
+    other = torch.where(alone, 0.0, 2.0 ** -23 * logits.abs().amax(1)) if scale == 0.7 else 0.0
+    assert bool((got >= 0).all())
+    assert bool(((got - loss).abs() <= 2.0 ** -19 * (1 + loss) + other).all()), float((got - loss).abs()[largest].max())
+    assert bool(((got_lse - lse).abs() <= 2.0 ** -23 * (1 + lse.abs())).all())
