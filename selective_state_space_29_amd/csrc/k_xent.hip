@@ -114,7 +114,10 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(XentRows p) {
         const bool hit = t >= 0 && t < p.vocab && p.dloss;
         const float a = hit ? p.dloss[r * p.sloss] * p.scale : 0.0f;
         const float f = a + (p.dlse ? p.dlse[r * p.slse] * p.scale : 0.0f);
-        if ((threadIdx.x & 63) == 0) p.row[r] = f32x4{p.lse[r] * kLog2e, f, a, __builtin_bit_cast(float, hit ? (int)t : -1)};
+        // 2^(l log2(e) - top) f 2^(top - lse log2(e)), top the rounded lse log2(e)
+        const float top = p.lse[r] * kLog2e, rest = __builtin_fmaf(p.lse[r], kLog2e, -top);
+        const float above = __builtin_fabsf(top) < __builtin_inff() ? f * hw_exp2(-rest) : f;
+        if ((threadIdx.x & 63) == 0) p.row[r] = f32x4{top, above, a, __builtin_bit_cast(float, hit ? (int)t : -1)};
         const bool on = a != 0.0f || f != 0.0f;
         for (int64_t c = (int64_t)(threadIdx.x & 63) * 8; c < p.wide; c += 64 * 8) {
             const Pack<uint16_t, 8> v = load_some<uint16_t, 8>(p.x + r * p.sx + c, on ? (int)(p.dim - c) : 0);

@@ -52,7 +52,7 @@ struct MatArgs {
     const void* target;     // lse: (P) int64 or int32, or NULL
     int target64;
     float* at_target;       // lse: (P), the target's logit where it is one of this product's columns
-    const float* row;       // dlogits: (P) of {lse log2(e), factor of the softmax, factor of the target, target's bits}
+    const float* row;       // dlogits: (P) of {lse log2(e) rounded, factor of 2 to what is above it, factor of the target, target's bits}
     int64_t q_first;        // dlogits: the vocabulary's column that is column 0 here
 };
 
@@ -502,8 +502,14 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
                 // (factor softmax - [target] factor) rounded; a row whose factors are 0 takes no part, whatever its
                 // logits. Columns past Q, up to the padded width that is written, are zeros. The target is seen to
                 // apart, as hardly any lane holds one (a piece of 7168 columns and 16384 rows, the target and the
-                // last column tested at every value 215 us, so 204).
-                const float s2 = m.scale * kLog2e;
+                // last column tested at every value 215 us, so 204). The factor makes up for the rounding of lse log2(e), so
+                // that a softmax of 1 is 1 to its last bits and leaves nothing behind when the target is taken from it.
+                if (m.scale != 1.0f) {  // the forward's logits, rounded as there
+#pragma unroll
+                    for (int q = 0; q < QT; ++q)
+#pragma unroll
+                        for (int p = 0; p < PT; ++p) acc[q][p] *= m.scale;
+                }
                 const bool whole = q0 + TQ <= m.Q;
                 static_assert(TP * 16 + TP * PITCH * 2 <= (STAGES > RESULTS ? STAGES : RESULTS) * 2);
                 f32x4* rows_of = reinterpret_cast<f32x4*>(&lds[TP * PITCH]);
@@ -517,7 +523,7 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
 #pragma unroll
                     for (int q = 0; q < QT; ++q)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[q][p][j] = hw_exp2(__builtin_fmaf(acc[q][p][j], s2, -row[0]));
+                        for (int j = 0; j < 4; ++j) acc[q][p][j] = hw_exp2(__builtin_fmaf(acc[q][p][j], kLog2e, -row[0]));
                     // (apart from the products: an exponential's result may not be used by the next instruction)
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -193,3 +193,31 @@ def test_cross_entropy_digits_of_confident_rows(scale):
     assert bool((got >= 0).all())
     assert bool(((got - loss).abs() <= 2.0 ** -19 * (1 + loss) + other).all()), float((got - loss).abs()[largest].max())
     assert bool(((got_lse - lse).abs() <= 2.0 ** -23 * (1 + lse.abs())).all())
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.5, -1.0, 0.7])
+def test_cross_entropy_gradient_of_confident_rows(scale):
+    """Where the softmax of the target is 1, the gradient is what is left of 1 - 1.
+
+    Bar. As in the loss's test the logits are exact or rounded once; the softmax is off by the rounding of lse, which is
+    exact where one column has it all, and otherwise half a unit of it, by a rounding of the logit of another column (2^-24
+    of each), and by a few units of the exponential: 2^-20. Its difference from the target is rounded to bf16, 2^-8 of it."""
+    x, w, target = exact_logits(6)
+    if scale < 0:
+        x = -x
+    dloss = torch.randn(len(target), generator=gen(7))
+    xd, wd = x.to(DEV), w.to(DEV)
+    lse = block.linear_cross_entropy_fn(xd, wd, target.to(DEV), scale=scale, return_lse=True)[1]
+    g = block.linear_cross_entropy_bwd(xd, wd, target.to(DEV), lse, dloss.to(DEV), scale=scale)
+    _, want_lse, want = ref.linear_cross_entropy(x, w, target, scale, dloss)
+    logits = scale * x.double() @ w.double().t()
+    p = torch.exp(logits - want_lse[:, None])
+    a = dloss.double()[:, None]
+    d = a * p
+    d[torch.arange(len(target)), target] -= dloss.double()
+    alone = p.amax(1, keepdim=True) > 1 - 1e-12
+    assert int(alone.sum()) > 100
+    slack = abs(scale) * (2.0 ** -8 * d.abs() + (a * p).abs() * (2.0 ** -20 + torch.where(alone, 0.0, 2.0 ** -22 * want_lse.abs()[:, None])))
+    for name, room in (("x", slack @ w.double().abs()), ("weight", slack.t() @ x.double().abs())):
+        err = (g[name].cpu().double() - want[name]).abs()
+        assert bool((err <= room + 2.0 ** -8 * want[name].abs() + 2.0 ** -24).all()), (name, float((err - room).max()))
