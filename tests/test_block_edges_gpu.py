@@ -221,3 +221,22 @@ def test_cross_entropy_gradient_of_confident_rows(scale):
     for name, room in (("x", slack @ w.double().abs()), ("weight", slack.t() @ x.double().abs())):
         err = (g[name].cpu().double() - want[name]).abs()
         assert bool((err <= room + 2.0 ** -8 * want[name].abs() + 2.0 ** -24).all()), (name, float((err - room).max()))
+
+
+def test_cross_entropy_of_rows_that_lie_far_apart():
+    """The last step of long sequences, and every n-th row of a large matrix: more than 2^21 elements from row to row."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    h = torch.randn(4, 2800, 768, generator=g, device=DEV, dtype=BF16)
+    w = torch.randn(6, 2800, 768, generator=g, device=DEV, dtype=BF16)
+    x, wv, target = h[:, -1], w[:, 3], torch.tensor([0, 5, -100, 2], device=DEV)
+    assert x.stride(0) > 1 << 21 and wv.stride(0) > 1 << 21
+    want = block.linear_cross_entropy_fn(x.contiguous(), wv.contiguous(), target, return_lse=True)
+    for a, b in ((x, wv), (x, wv.contiguous()), (x.contiguous(), wv)):
+        got = block.linear_cross_entropy_fn(a, b, target, return_lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        g1 = block.linear_cross_entropy_bwd(a, b, target, got[1], want[0])
+        g2 = block.linear_cross_entropy_bwd(x.contiguous(), wv.contiguous(), target, got[1], want[0])
+        assert torch.equal(g1["x"], g2["x"]) and torch.equal(g1["weight"], g2["weight"])
+    leaf = h.requires_grad_()
+    block.linear_cross_entropy(leaf[:, -1], wv, target).backward()
+    assert bool(leaf.grad[:, -1].any()) and not leaf.grad[:, :-1].any()
