@@ -281,7 +281,7 @@ int mamba_xent_fwd(const mamba_xent_ptrs* p, const mamba_xent_shape* s, int targ
 int mamba_xent_bwd(const mamba_xent_bwd_ptrs* p, const mamba_xent_shape* s, int target64, float scale, mamba_scan_dtype dtype,
                    void* stream);
 /* Workspace bytes, or a negative error code. They depend on the operands' pointers and strides (rows that are not
- * 16-byte aligned are copied) and on the current device's compute-unit count. */
+ * 16-byte aligned are copied), on which gradients are asked for, and on the current device's compute-unit count. */
 int64_t mamba_xent_workspace_bytes(const mamba_xent_ptrs* p, const mamba_xent_shape* s);
 int64_t mamba_xent_bwd_workspace_bytes(const mamba_xent_bwd_ptrs* p, const mamba_xent_shape* s);
 

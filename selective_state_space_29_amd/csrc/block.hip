@@ -114,7 +114,7 @@ int64_t mamba_conv_bwd_workspace_bytes(const mamba_conv_shape* s, mamba_scan_dty
     if (bad_dtype(dtype)) return MAMBA_SCAN_ERR_DTYPE;
     if (conv_bad_shape(*s)) return MAMBA_SCAN_ERR_SHAPE;
     if (conv_too_large(*s)) return MAMBA_SCAN_ERR_UNSUPPORTED;
-    return s->batch * s->dim == 0 ? 0 : conv_bwd_workspace(*s, dtype == MAMBA_SCAN_BF16, x_steps != 0);
+    return s->batch * s->dim == 0 ? 0 : conv_bwd_workspace(*s, x_steps != 0);
 }
 
 int mamba_conv_bwd(const mamba_conv_bwd_ptrs* p, const mamba_conv_shape* s, int act, mamba_scan_dtype dtype, void* stream) {

@@ -10,7 +10,7 @@ namespace mscan {
 
 int launch_conv_fwd(const mamba_conv_ptrs& p, const mamba_conv_shape& s, int act, bool bf16, hipStream_t stream);
 int launch_conv_bwd(const mamba_conv_bwd_ptrs& p, const mamba_conv_shape& s, int act, bool bf16, hipStream_t stream);
-int64_t conv_bwd_workspace(const mamba_conv_shape& s, bool bf16, bool x_steps);
+int64_t conv_bwd_workspace(const mamba_conv_shape& s, bool x_steps);
 
 int launch_block_step(const mamba_step_ptrs& p, const mamba_step_shape& s, bool bf16, hipStream_t stream);
 int64_t block_step_workspace(const mamba_step_shape& s);

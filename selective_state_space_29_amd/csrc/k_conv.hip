@@ -800,7 +800,7 @@ int launch_conv_fwd(const mamba_conv_ptrs& p, const mamba_conv_shape& s, int act
     return on.status;
 }
 
-int64_t conv_bwd_workspace(const mamba_conv_shape& s, bool bf16, bool x_steps) {
+int64_t conv_bwd_workspace(const mamba_conv_shape& s, bool x_steps) {
     return align256((int64_t)bwd_blocks(s, x_steps) * (s.width + 1) * s.dim * 4);
 }
 

@@ -201,7 +201,7 @@ BwdPlan bwd_plan(const mamba_xent_bwd_ptrs& p, const mamba_xent_shape& s) {
     b.pieces = (s.vocab + b.width - 1) / b.width;
     b.tx = tiling(s.rows, s.dim, false, steps_of(b.width < s.vocab ? b.width : s.vocab), true);
     int64_t dw = 0;
-    for (int64_t k = 0; k < b.pieces; ++k) {
+    for (int64_t k = 0; k < (p.dweight ? b.pieces : 0); ++k) {
         const int64_t width = s.vocab - k * b.width < b.width ? s.vocab - k * b.width : b.width;
         const int splits = dw_tiling(s, width).splits;
         if (splits > 1 && splits * up(width, kTC) > dw) dw = splits * up(width, kTC);
@@ -211,7 +211,7 @@ BwdPlan bwd_plan(const mamba_xent_bwd_ptrs& p, const mamba_xent_shape& s) {
     b.w = b.x + align256(s.rows * up(s.dim, 8) * 2);
     b.d = b.w + (b.copy_w ? align256(s.vocab * up(s.dim, 8) * 2) : 0);
     b.dx = b.d + align256(s.rows * b.width * 2);
-    b.dw = b.dx + (b.pieces > 1 || b.tx.splits > 1 ? align256(b.tx.splits * s.rows * s.dim * 4) : 0);
+    b.dw = b.dx + (p.dx && (b.pieces > 1 || b.tx.splits > 1) ? align256(b.tx.splits * s.rows * s.dim * 4) : 0);
     b.total = b.dw + align256(dw * s.dim * 4);
     return b;
 }

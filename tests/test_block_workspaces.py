@@ -1,0 +1,29 @@
+"""Host-only checks of the block operators' workspace sizes: what a call does not need is not asked for. No call is
+made; pointers are made-up addresses that are never followed."""
+
+import pytest
+
+from selective_state_space_29_amd import block, scan
+
+BASE = 1 << 40
+
+
+def up(n, a=256):
+    return -(-n // a) * a
+
+
+def xent_bwd(rows, dim, vocab, dx=True, dweight=True):
+    p = block.XentBwdPtrs(x=BASE, weight=BASE * 2, target=BASE * 3, lse=BASE * 4, dloss=BASE * 5, dx=BASE * 6 if dx else None,
+                          dweight=BASE * 7 if dweight else None, x_stride=dim, weight_stride=dim, dloss_stride=1)
+    return block._load().mamba_xent_bwd_workspace_bytes(p, block.XentShape(rows, dim, vocab))
+
+
+@pytest.mark.parametrize("rows,dim,vocab", [(16384, 768, 50000), (16384, 64, 9000), (300, 64, 1000)])
+def test_cross_entropy_gradients_that_are_not_asked_for_take_no_room(rows, dim, vocab):
+    both, dx, dw, none = (xent_bwd(rows, dim, vocab, a, b) for a, b in ((1, 1), (1, 0), (0, 1), (0, 0)))
+    # of each row its factors and its part of x; at most 256 MB of the logits' gradients and a piece's rounding
+    base = up(rows * 16) + up(rows * dim * 2)
+    assert base < none <= base + (1 << 28) + rows * 512
+    assert both - none == (dx - none) + (dw - none)
+    if rows == 16384:  # several pieces: dx's sums in fp32; the parts of dweight's sums
+        assert dx - none >= rows * dim * 4 and dw - none > 0
