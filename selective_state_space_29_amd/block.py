@@ -25,8 +25,8 @@ import torch
 from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
-from .layers import (_MAX_ROW_STRIDE, _dtype, _f32, _grad_on, _inner, _launch, _need_gpu, _on_device, _ptr, _reset, _row_stride,
-                     _rows, _same, _workspace)
+from .layers import (_dtype, _f32, _grad_on, _inner, _launch, _near_rows, _need_gpu, _on_device, _ptr, _reset, _row_stride, _rows,
+                     _same, _workspace)
 from .scan import load_library, refuse_graph
 
 _I64 = ctypes.c_int64
@@ -583,13 +583,9 @@ def _xent_args(x, weight, target, entry):
     if target.shape != lead or target.get_device() != dev:
         raise ValueError(f"target must be {tuple(lead)} on x's device, got {tuple(target.shape)}")
     xr, rows, xs = _rows(x, "x")
+    xr, xs = _near_rows(xr, xs)
     weight = _inner(weight)
-    ws = _row_stride(weight)
-    # rows that lie further apart than a tile's 32-bit offsets reach (the last step of long sequences) are copied
-    if xs > _MAX_ROW_STRIDE:
-        xr, xs = xr.contiguous(), shape[-1]
-    if ws > _MAX_ROW_STRIDE:
-        weight, ws = weight.contiguous(), wshape[1]
+    weight, ws = _near_rows(weight, _row_stride(weight))
     return (dtype, xr, xs, weight, ws, target if target.is_contiguous() else target.contiguous(), ids64, lead, dev,
             XentShape(rows, wshape[1], wshape[0]))
 

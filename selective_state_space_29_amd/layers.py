@@ -417,6 +417,12 @@ def _row_stride(x):
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
+def _near_rows(x, stride):
+    """Rows for the matrix kernels, and their stride: copied where they lie further apart than a tile's 32-bit offsets
+    reach (the last step of long sequences)."""
+    return (x.contiguous(), x.shape[-1]) if stride > _MAX_ROW_STRIDE else (x, stride)
+
+
 def layer_norm_fn(x, weight=None, bias=None, eps=1e-5, *, residual=None, return_stats=False):
     """Layer norm over the last dimension, with the residual added on the way::
 
@@ -597,7 +603,10 @@ def _ffn_inputs(x, w_gate, w_up, activation, entry):
             raise TypeError(f"{name} must have x's dtype and device")
         if w.dim() != 2 or w.shape != w_gate.shape or w.shape[1] != x.shape[-1]:
             raise ValueError(f"{name} must be (hidden, dim) with dim = {x.shape[-1]}, got {tuple(w.shape)}")
-    return dtype, _ACTS[activation], *_rows(x, "x"), _inner(w_gate), _inner(w_up)
+    xr, rows, xs = _rows(x, "x")
+    xr, xs = _near_rows(xr, xs)
+    wg, wu = (_near_rows(w, _row_stride(w))[0] for w in (_inner(w_gate), _inner(w_up)))
+    return dtype, _ACTS[activation], xr, rows, xs, wg, wu
 
 
 def gated_ffn_fn(x, w_gate, w_up, activation="silu"):

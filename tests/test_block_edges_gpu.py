@@ -240,3 +240,15 @@ def test_cross_entropy_of_rows_that_lie_far_apart():
     leaf = h.requires_grad_()
     block.linear_cross_entropy(leaf[:, -1], wv, target).backward()
     assert bool(leaf.grad[:, -1].any()) and not leaf.grad[:, :-1].any()
+
+
+def test_feed_forward_of_rows_that_lie_far_apart():
+    g = torch.Generator(device=DEV).manual_seed(11)
+    h = torch.randn(60, 2800, 768, generator=g, device=DEV, dtype=BF16)
+    w = torch.randn(9, 2800, 768, generator=g, device=DEV, dtype=BF16)
+    wg, wu = w[:, 3], w[:, 4]
+    for x in (h[:, -1], h[:5, -1]):
+        want = layers.gated_ffn_fn(x.contiguous(), wg.contiguous(), wu.contiguous())
+        assert torch.equal(layers.gated_ffn_fn(x, wg, wu), want) and torch.equal(layers.gated_ffn_fn(x, wg.contiguous(), wu.contiguous()), want)
+        got, want = layers.gated_ffn_bwd(x, wg, wu, want), layers.gated_ffn_bwd(x.contiguous(), wg.contiguous(), wu.contiguous(), want)
+        assert all(torch.equal(got[k], want[k]) for k in want)
