@@ -186,8 +186,8 @@ struct BwdPlan {
 };
 
 int64_t piece_of(const mamba_xent_shape& s) {
-    const int64_t most = kPieceBytes / (s.rows * 2), n = (s.vocab + most) / (most < 1 ? 1 : most);
-    int64_t width = up((s.vocab + n - 1) / (n < 1 ? 1 : n), 256);
+    const int64_t fit = kPieceBytes / (s.rows * 2), most = fit < 1 ? 1 : fit, n = (s.vocab + most - 1) / most;
+    int64_t width = up((s.vocab + n - 1) / n, 256);
     if (width < kPieceLeast) width = kPieceLeast;
     return width < up(s.vocab, 256) ? width : up(s.vocab, 256);
 }

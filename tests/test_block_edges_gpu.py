@@ -252,3 +252,30 @@ def test_feed_forward_of_rows_that_lie_far_apart():
         assert torch.equal(layers.gated_ffn_fn(x, wg, wu), want) and torch.equal(layers.gated_ffn_fn(x, wg.contiguous(), wu.contiguous()), want)
         got, want = layers.gated_ffn_bwd(x, wg, wu, want), layers.gated_ffn_bwd(x.contiguous(), wg.contiguous(), wu.contiguous(), want)
         assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("vocab", [8192, 16384])
+def test_cross_entropy_of_whole_pieces(vocab):
+    """A vocabulary of one and of two pieces to their last column. Bars: the logits' gradients are rounded to bf16, 2^-8 of
+    them, their softmax is off by 1e-5 of it, results by their own rounding and 1e-5."""
+    M, K = 16384, 64
+    g = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.randn(M, K, generator=g, device=DEV).to(BF16)
+    w = (torch.randn(vocab, K, generator=g, device=DEV) * K ** -0.5).to(BF16)
+    t = torch.randint(0, vocab, (M,), generator=g, device=DEV)
+    dloss = torch.randn(M, generator=g, device=DEV)
+    lse = block.linear_cross_entropy_fn(x, w, t, return_lse=True)[1]
+    out = block.linear_cross_entropy_bwd(x, w, t, lse, dloss)
+    dw, room_w = (torch.zeros(vocab, K, dtype=torch.float64, device=DEV) for _ in range(2))
+    wd = w.double()
+    for s in range(0, M, 4096):
+        r = slice(s, s + 4096)
+        xd, a = x[r].double(), dloss[r].double()[:, None]
+        p = a * torch.softmax(xd @ wd.t(), -1)
+        d = p.scatter_add(1, t[r][:, None], -a)
+        slack = 2.0 ** -8 * d.abs() + 1e-5 * p.abs()
+        want = d @ wd
+        assert bool(((out["x"][r].double() - want).abs() <= slack @ wd.abs() + (2.0 ** -8 + 1e-5) * want.abs() + 1e-5).all())
+        dw += d.t() @ xd
+        room_w += slack.t() @ xd.abs()
+    assert bool(((out["weight"].double() - dw).abs() <= room_w + (2.0 ** -8 + 1e-5) * dw.abs() + 1e-5).all())

@@ -27,3 +27,11 @@ def test_cross_entropy_gradients_that_are_not_asked_for_take_no_room(rows, dim, 
     assert both - none == (dx - none) + (dw - none)
     if rows == 16384:  # several pieces: dx's sums in fp32; the parts of dweight's sums
         assert dx - none >= rows * dim * 4 and dw - none > 0
+
+
+@pytest.mark.parametrize("rows,vocab,pieces", [(16384, 32768, 4), (8192, 32768, 2), (16384, 32769, 5), (16384, 8192, 1), (1 << 18, 100000, 98)])
+def test_cross_entropy_pieces_are_as_many_as_their_bytes_ask_for(rows, vocab, pieces):
+    """256 MB of the logits' gradients a piece, of 1024 columns at least and a multiple of 256."""
+    dim = 64
+    width = max(1024, up(-(-vocab // pieces)))
+    assert xent_bwd(rows, dim, vocab, False, False) == up(rows * 16) + up(rows * dim * 2) + up(rows * width * 2)
