@@ -381,10 +381,11 @@ __global__ __launch_bounds__(256) void rms_cols_wide_kernel(RmsBwdArgs p) {
     p.part[blockIdx.y * wide + c] = s;
 }
 
-// The workgroups' partial column sums, added in order: 32 columns x 8 stretches of the list a workgroup.
+// The workgroups' partial column sums, added in order: 32 columns x 8 stretches of the list a workgroup (of 2^29
+// columns and more, more threads than a dimension of the grid counts).
 __global__ __launch_bounds__(256) void rms_cols_kernel(const float* part, int blocks, int64_t wide, float* dweight) {
     __shared__ float lds[8][32];
-    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    const int64_t c = grid_block() * 32 + (threadIdx.x & 31);
     const int g = threadIdx.x >> 5, per = (blocks + 7) / 8;
     float s = 0.0f;
     if (c < wide) s = column_sum(part, wide, c, g * per, (g + 1) * per < blocks ? (g + 1) * per : blocks);
@@ -464,7 +465,7 @@ int64_t bwd_typed(RmsBwdArgs q, Launches& on) {
 void join(const RmsBwdArgs& q, int64_t blocks, float* dweight, Launches& on) {
     if (!dweight) return;
     const int64_t wide = q.dim * q.groups;
-    on(rms_cols_kernel, dim3((unsigned)((wide + 31) / 32)), dim3(256), static_cast<const float*>(q.part), (int)blocks, wide, dweight);
+    on(rms_cols_kernel, grid_of((wide + 31) / 32, 256), dim3(256), static_cast<const float*>(q.part), (int)blocks, wide, dweight);
 }
 
 }  // namespace
@@ -488,8 +489,10 @@ int launch_gated_rms_fwd(const mamba_gated_rms_ptrs& p, const mamba_gated_rms_sh
     return on.status;
 }
 
-int64_t rms_bwd_workspace(const mamba_rms_shape& s) { return align256(kBwdBlocks * s.dim * 4); }
-int64_t gated_rms_bwd_workspace(const mamba_gated_rms_shape& s) { return align256(kBwdBlocks * s.dim * 4); }
+// A row of partial sums for each workgroup, of which there are no more than rows.
+int64_t parts_bytes(int64_t rows, int64_t dim) { return align256((rows < kBwdBlocks ? rows : kBwdBlocks) * dim * 4); }
+int64_t rms_bwd_workspace(const mamba_rms_shape& s) { return parts_bytes(s.rows, s.dim); }
+int64_t gated_rms_bwd_workspace(const mamba_gated_rms_shape& s) { return parts_bytes(s.rows, s.dim); }
 
 int launch_rms_bwd(const mamba_rms_bwd_ptrs& p, const mamba_rms_shape& s, float scale, bool bf16, hipStream_t stream) {
     RmsBwdArgs q{p.t, p.dy, p.dsum, p.weight, p.stats, p.dx, p.dresidual, p.dweight ? static_cast<float*>(p.workspace) : nullptr,

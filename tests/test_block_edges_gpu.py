@@ -279,3 +279,17 @@ def test_cross_entropy_of_whole_pieces(vocab):
         dw += d.t() @ xd
         room_w += slack.t() @ xd.abs()
     assert bool(((out["weight"].double() - dw).abs() <= room_w + (2.0 ** -8 + 1e-5) * dw.abs() + 1e-5).all())
+
+
+def test_rms_gradient_of_more_columns_than_a_grid_counts_threads():
+    """One row whose weight's gradient is joined by 8 threads a column: dweight = dy t rstd, one product rounded twice."""
+    dim = (1 << 29) + 1000
+    g = torch.Generator(device=DEV).manual_seed(9)
+    piece = torch.randn(2, 1 << 20, generator=g, device=DEV, dtype=BF16)
+    t, dy = (p.repeat(-(-dim // p.numel()))[None, :dim] for p in piece)
+    stale(dim)
+    rstd = torch.full((1,), 0.75, device=DEV)
+    got = block.rms_norm_bwd(t, None, dy, rstd)["weight"]
+    for s in range(0, dim, 1 << 27):
+        c = slice(s, s + (1 << 27))
+        assert torch.equal(got[c], dy[0, c].float() * (t[0, c].float() * 0.75)), s

@@ -35,3 +35,11 @@ def test_cross_entropy_pieces_are_as_many_as_their_bytes_ask_for(rows, vocab, pi
     dim = 64
     width = max(1024, up(-(-vocab // pieces)))
     assert xent_bwd(rows, dim, vocab, False, False) == up(rows * 16) + up(rows * dim * 2) + up(rows * width * 2)
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 1 << 20), (3, 1001), (100, 64), (256, 768), (16384, 1536)])
+def test_norm_gradients_ask_for_no_more_partial_sums_than_rows(rows, dim):
+    lib = block._load()
+    most = up(min(rows, 256) * dim * 4)
+    assert lib.mamba_rms_norm_bwd_workspace_bytes(block.RmsShape(rows, dim)) == most
+    assert lib.mamba_gated_rms_norm_bwd_workspace_bytes(block.GatedRmsShape(rows, dim, 1)) == most
