@@ -42,7 +42,8 @@ extern "C" {
  *    stride over steps: the scan's). y_steps = 0 with x_steps = 1 is MAMBA_SCAN_ERR_UNSUPPORTED.
  *  - weight (dim, width), bias (dim) or NULL; initial_state, last_state: (batch, width - 1, dim) dtype
  *    contiguous, or NULL; last_state may be initial_state's own buffer. reset: (batch, len) bytes or NULL.
- *  - batch * ceil(len / 8) below 2^31, len below 2^30 and dim up to 2^22 (MAMBA_SCAN_ERR_UNSUPPORTED).
+ *  - batch * ceil(len / 8), or batch where len is 0, below 2^31, len below 2^30 and dim up to 2^22
+ *    (MAMBA_SCAN_ERR_UNSUPPORTED).
  */
 #define MAMBA_CONV_NONE 0
 #define MAMBA_CONV_SILU 1

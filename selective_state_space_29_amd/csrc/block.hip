@@ -37,8 +37,9 @@ int zeros(float* p, int64_t n, hipStream_t stream) { return p && n > 0 ? launch_
 bool conv_bad_shape(const mamba_conv_shape& s) {
     return s.batch < 0 || s.len < 0 || s.dim < 0 || s.width < 1 || s.width > 4 || s.batch > kMaxGrid || s.len > kMaxGrid || s.dim > kMaxGrid;
 }
+// Runs of all sequences, one at least of each, are counted in 31 bits.
 bool conv_too_large(const mamba_conv_shape& s) {
-    return s.len >= (int64_t)1 << 30 || s.dim > (int64_t)1 << 22 || s.batch * ((s.len + 7) / 8 + 1) > kMaxGrid;
+    return s.len >= (int64_t)1 << 30 || s.dim > (int64_t)1 << 22 || s.batch * (s.len > 0 ? (s.len + 7) / 8 : 1) > kMaxGrid;
 }
 
 // The layout of a (batch, len, dim) tensor: rows of channels or of steps.

@@ -293,3 +293,19 @@ def test_rms_gradient_of_more_columns_than_a_grid_counts_threads():
     for s in range(0, dim, 1 << 27):
         c = slice(s, s + (1 << 27))
         assert torch.equal(got[c], dy[0, c].float() * (t[0, c].float() * 0.75)), s
+
+
+@pytest.mark.parametrize("scan_layout", [False, True])
+def test_conv_of_many_short_sequences(scan_layout):
+    """2^30 sequences of 8 steps."""
+    B, L = 1 << 30, 8
+    few = 1021
+    g = gen(10)
+    x = torch.randn(few, L, 1, generator=g).to(BF16).to(DEV)
+    w, b = torch.randn(1, 2, generator=g).to(DEV), torch.randn(1, generator=g).to(DEV)
+    want = block.causal_conv_fn(x, w, b)
+    many = x.repeat(-(-B // few), 1, 1)[:B]
+    y = block.causal_conv_fn(many, w, b, scan_layout=scan_layout)
+    for s in (slice(0, few), slice(B // 2 // few * few, B // 2 // few * few + few), slice(B // few * few - few, B // few * few)):
+        assert torch.equal(y[s], want)
+    assert torch.equal(y[B // few * few:], want[:B % few])

@@ -43,3 +43,12 @@ def test_norm_gradients_ask_for_no_more_partial_sums_than_rows(rows, dim):
     most = up(min(rows, 256) * dim * 4)
     assert lib.mamba_rms_norm_bwd_workspace_bytes(block.RmsShape(rows, dim)) == most
     assert lib.mamba_gated_rms_norm_bwd_workspace_bytes(block.GatedRmsShape(rows, dim, 1)) == most
+
+
+@pytest.mark.parametrize("steps", [0, 1])
+def test_conv_takes_as_many_runs_as_the_header_says(steps):
+    size = lambda *s: block._load().mamba_conv_bwd_workspace_bytes(block.ConvShape(*s), scan.BF16, steps)  # noqa: E731
+    for batch, length in ((1 << 30, 8), ((1 << 31) - 1, 1), ((1 << 31) - 1, 0), ((1 << 30) - 1, 9), (1, (1 << 30) - 1)):
+        assert size(batch, length, 1, 4) > 0, (batch, length)
+    for batch, length in ((1 << 30, 9), (1 << 31, 0), (1, 1 << 30), (1 << 27, 128)):
+        assert size(batch, length, 1, 4) < 0, (batch, length)
