@@ -238,7 +238,8 @@ int64_t mamba_gated_rms_norm_bwd_workspace_bytes(const mamba_gated_rms_shape* s)
  *
  * and its gradient for incoming dloss and, optionally, dlse (rows, or one value for all with stride 0). With
  * a = dloss where the target is inside [0, vocab), else 0:
- *   dl_v = (a + dlse) exp(l_v - lse) - a [v = target], rounded to bf16 as the operand of the products
+ *   dl_v = (a + dlse) exp(l_v - lse) - a [v = target], rounded to bf16 as the operand of the products (where all rows
+ *   with a target have the same a, as in a mean, without that factor, which then multiplies the fp32 sums)
  *   dx = scale dl weight;   dweight = scale dl^T x
  * A row with a + dlse = a = 0 takes no part in the gradients, whatever x holds there. The gradient works on
  * pieces of the vocabulary whose dl fit the workspace.

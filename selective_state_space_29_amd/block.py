@@ -641,7 +641,8 @@ def linear_cross_entropy_bwd(x, weight, target, lse, dloss, *, dlse=None, scale=
     """Gradients of :func:`linear_cross_entropy_fn` with its ``lse``, for incoming ``dloss`` and, optionally,
     ``dlse``, of target's shape (either may be None). Returns a dict of x and weight in bfloat16, where wanted.
     The logits are computed again piece by piece of the vocabulary; their gradients are rounded to bfloat16
-    once, as the operands of the products. A row without a target or whose incoming gradients are 0 takes no
+    once, as the operands of the products, without the factor of dloss where it is the same for all rows with a
+    target (a mean, a sum). A row without a target or whose incoming gradients are 0 takes no
     part, whatever x holds there."""
     lib = _load()
     dtype, xr, xs, weight, ws, target, ids64, lead, dev, shape = _xent_args(x, weight, target, "linear_cross_entropy_bwd")

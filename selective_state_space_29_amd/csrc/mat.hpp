@@ -47,6 +47,7 @@ struct MatArgs {
     int add;                // add: the partial sums are added to what is there
     float* part;            // (splits, P, Q); lse: (tiles_q, P) pairs of a row's maximum and sum of a tile
     int act;
+    const float* factor;    // or NULL: what the bf16 results are multiplied with before they are rounded
     // cross entropy: logits are scale C
     float scale;
     const void* target;     // lse: (P) int64 or int32, or NULL
@@ -553,6 +554,15 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
                 });
                 return;
             }
+            if constexpr (EPI == kEpiStore) {
+                if (m.factor) {
+                    const float by = *m.factor;
+#pragma unroll
+                    for (int q = 0; q < QT; ++q)
+#pragma unroll
+                        for (int p = 0; p < PT; ++p) acc[q][p] *= by;
+                }
+            }
 #pragma unroll
             for (int p = 0; p < PT; ++p)
 #pragma unroll
@@ -582,6 +592,7 @@ __global__ __launch_bounds__(256) void mat_join_kernel(MatArgs m) {
     const int64_t n = m.P * m.Q, cols = m.Q / V;
     typedef float vec __attribute__((ext_vector_type(V)));
     const vec* part = reinterpret_cast<const vec*>(m.part);
+    const float by = m.factor ? *m.factor : 1.0f;
     for (int64_t pr = blockIdx.x; pr < m.P; pr += gridDim.x) {
         const int64_t row = pr < m.seg_rows ? pr : pr - m.seg_rows;
         if (row >= m.seg_valid) continue;
@@ -590,6 +601,7 @@ __global__ __launch_bounds__(256) void mat_join_kernel(MatArgs m) {
             vec s = 0.0f;
 #pragma unroll 4
             for (int q = 0; q < m.splits; ++q) s += part[q * (n / V) + pr * cols + c];
+            s *= by;
             if constexpr (V == 4) {
                 const uint2 w = make_uint2(pack2(s[0], s[1]), pack2(s[2], s[3]));
                 __builtin_memcpy(out + c * 4, &w, 8);

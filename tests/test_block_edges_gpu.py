@@ -309,3 +309,70 @@ def test_conv_of_many_short_sequences(scan_layout):
     for s in (slice(0, few), slice(B // 2 // few * few, B // 2 // few * few + few), slice(B // few * few - few, B // few * few)):
         assert torch.equal(y[s], want)
     assert torch.equal(y[B // few * few:], want[:B % few])
+
+
+@pytest.mark.parametrize("how", ["rows", "mean", "sum", "lse"])
+def test_cross_entropy_gradient_does_not_round_a_common_factor(how):
+    """One factor for all rows, halfway between two values of bf16: it is in the results' last rounding alone.
+
+    Bar. A rounding is off by 2^-8 at most, and over many results by 0.43 of that at the root of their mean square (evenly
+    spread errors over evenly spread logarithms of values); what is left of the targets' entries, 1 - p with p below 2^-8 in
+    nearly all rows, and the small entries' own roundings add little: half of 2^-8 of the norm. The factor rounded as well
+    would add 2^-8 of it."""
+    g = gen(13)
+    M, K, V = 500, 256, 3000
+    x, w = torch.randn(M, K, generator=g).to(BF16), (torch.randn(V, K, generator=g) * K ** -0.5).to(BF16)
+    target = torch.randint(0, V, (M,), generator=g)
+    target[::10] = -100
+    factor = 1 + 2.0 ** -8
+    lead = torch.full((M,), factor)
+    if how in ("mean", "sum"):
+        a, b = (t.to(DEV).requires_grad_() for t in (x, w))
+        n = int((target >= 0).sum()) if how == "mean" else 1
+        block.linear_cross_entropy(a, b, target.to(DEV), reduction=how).mul(factor * n).backward()
+        got = {"x": a.grad, "weight": b.grad}
+        dlse = None
+    else:
+        dlse = torch.full((M,), 2.0 ** -6) if how == "lse" else None
+        lse = block.linear_cross_entropy_fn(x.to(DEV), w.to(DEV), target.to(DEV), return_lse=True)[1]
+        got = block.linear_cross_entropy_bwd(x.to(DEV), w.to(DEV), target.to(DEV), lse, lead.to(DEV), dlse=None if dlse is None else dlse.to(DEV))
+    want = ref.linear_cross_entropy(x, w, target, 1.0, lead, dlse)[2]
+    for k in want:
+        far = float((got[k].cpu().double() - want[k]).norm() / want[k].norm())
+        assert far <= 2.0 ** -9, (k, far)
+
+
+@pytest.mark.parametrize("dloss,dlse", [(1e-30, 1e8), (1e30, 1e-30), (float(2.0 ** -100), None), (3e37, None)])
+def test_cross_entropy_gradient_of_factors_far_from_one(dloss, dlse):
+    """Factors that are alike, and a softmax's far from them. Bars as in the small sizes' tests, over the results' sizes."""
+    g = gen(14)
+    M, K, V = 60, 64, 200
+    x, w = torch.randn(M, K, generator=g).to(BF16), (torch.randn(V, K, generator=g) * K ** -0.5).to(BF16)
+    target = torch.randint(-1, V, (M,), generator=g)
+    a, b = torch.full((M,), dloss), None if dlse is None else torch.full((M,), dlse) * torch.rand(M, generator=g)
+    xd, wd, td = x.to(DEV), w.to(DEV), target.to(DEV)
+    lse = block.linear_cross_entropy_fn(xd, wd, td, return_lse=True)[1]
+    got = block.linear_cross_entropy_bwd(xd, wd, td, lse, a.to(DEV), dlse=None if b is None else b.to(DEV))
+    _, want_lse, want = ref.linear_cross_entropy(x, w, target, 1.0, a, b)
+    p = torch.softmax(x.double() @ w.double().t(), -1)
+    hit = torch.where(target >= 0, a.double(), 0.0)[:, None]
+    f = hit if b is None else hit + b.double()[:, None]
+    d = f * p
+    d[torch.arange(M), target.clamp(min=0)] -= hit[:, 0]
+    slack = 2.0 ** -8 * d.abs() + 1e-5 * (f * p).abs()
+    for k, room in (("x", slack @ w.double().abs()), ("weight", slack.t() @ x.double().abs())):
+        err = (got[k].cpu().double() - want[k]).abs()
+        assert bool((err <= room + 2.0 ** -8 * want[k].abs() + 2.0 ** -120).all()), (k, float((err / (room + 1e-300)).max()))
+
+
+def test_cross_entropy_gradient_beside_a_row_without_a_finite_factor():
+    g = gen(15)
+    x, w = torch.randn(40, 64, generator=g).to(BF16).to(DEV), torch.randn(100, 64, generator=g).to(BF16).to(DEV)
+    target, a = torch.randint(0, 100, (40,), generator=g).to(DEV), torch.full((40,), 0.5, device=DEV)
+    lse = block.linear_cross_entropy_fn(x, w, target, return_lse=True)[1]
+    want = block.linear_cross_entropy_bwd(x, w, target, lse, a)["x"]
+    for bad in (float("inf"), float("nan")):
+        a[7] = bad
+        got = block.linear_cross_entropy_bwd(x, w, target, lse, a)["x"]
+        rest = torch.arange(40, device=DEV) != 7
+        assert torch.equal(got[rest], want[rest]) and not bool(got[7].isfinite().all())
