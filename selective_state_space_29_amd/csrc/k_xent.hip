@@ -110,73 +110,104 @@ struct XentRows {
     const float* dlse;
     f32x4* row;
     uint16_t* copy;
+    f32x4* part;   // (parts): extremes of the factors; none where one value of dloss stands for all and there is no dlse
     float* factor;
     int64_t rows, dim, wide, vocab, sx, sloss, slse;
-    int target64;
+    int target64, parts;
     float scale;
 };
 
-// Row r's target or -1, and the factors of its target and of its softmax.
-__device__ __forceinline__ int64_t factors_of(const XentRows& p, int64_t r, float& a, float& f) {
-    const int64_t t = p.target ? target_of(p.target, p.target64, r) : -1;
-    const bool hit = t >= 0 && t < p.vocab && p.dloss;
-    a = hit ? p.dloss[r * p.sloss] * p.scale : 0.0f;
-    f = a + (p.dlse ? p.dlse[r * p.slse] * p.scale : 0.0f);
-    return hit ? t : -1;
+// The factors of a row's target and of its softmax, from the gradients at its loss (where it has a target) and its lse.
+__device__ __forceinline__ void factors_of(const XentRows& p, bool hit, float dloss, float dlse, float& a, float& f) {
+    a = hit ? dloss * p.scale : 0.0f;
+    f = a + dlse * p.scale;
 }
 
-// The targets' common factor, or 1: where they differ, and where a softmax's factor is so far from it that the quotient
-// might leave fp32's range. One workgroup.
-__global__ __launch_bounds__(1024) void xent_factor_kernel(XentRows p) {
-    __shared__ float sums[4][16];
-    // smallest and largest of the targets' factors that are not 0, the same of the softmax's; a NaN or an infinity counts as one
-    float v[4] = {__builtin_inff(), 0.0f, __builtin_inff(), 0.0f};
-#pragma unroll 4
-    for (int64_t r = threadIdx.x; r < p.rows; r += 1024) {
-        float of[2];
-        factors_of(p, r, of[0], of[1]);
+// The smallest and largest of the targets' factors that are not 0, and the same of the softmax's, over a workgroup.
+template <int WAVES>
+__device__ __forceinline__ f32x4 extremes(f32x4 v) {
+    __shared__ f32x4 all[WAVES];
+    auto join = [](f32x4 p, f32x4 q) {
+        return f32x4{__builtin_fminf(p[0], q[0]), __builtin_fmaxf(p[1], q[1]), __builtin_fminf(p[2], q[2]), __builtin_fmaxf(p[3], q[3])};
+    };
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float m = __builtin_fabsf(of[k]) < __builtin_inff() ? __builtin_fabsf(of[k]) : __builtin_inff();
-            if (m != 0.0f) v[2 * k] = __builtin_fminf(v[2 * k], m), v[2 * k + 1] = __builtin_fmaxf(v[2 * k + 1], m);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int far = 1; far < 64; far *= 2) {
-            const float o = __shfl_xor(v[k], far);
-            v[k] = k & 1 ? __builtin_fmaxf(v[k], o) : __builtin_fminf(v[k], o);
-        }
-        if ((threadIdx.x & 63) == 0) sums[k][threadIdx.x >> 6] = v[k];
-    }
+    for (int far = 1; far < 64; far *= 2)
+        v = join(v, f32x4{__shfl_xor(v[0], far), __shfl_xor(v[1], far), __shfl_xor(v[2], far), __shfl_xor(v[3], far)});
+    if ((threadIdx.x & 63) == 0) all[threadIdx.x >> 6] = v;
     __syncthreads();
-    if (threadIdx.x != 0) return;
+    v = all[0];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int w = 1; w < WAVES; ++w) v = join(v, all[w]);
+    return v;
+}
+
+// The extremes of every parts-th stretch of rows. A thread's loads are all on their way before it uses one (16384 rows
+// in one workgroup, row by row: 17 us).
+constexpr int kFactorAhead = 8, kFactorRows = 1024 * kFactorAhead, kFactorParts = 256;
+
+__global__ __launch_bounds__(1024) void xent_factor_kernel(XentRows p) {
+    f32x4 v = {__builtin_inff(), 0.0f, __builtin_inff(), 0.0f};
+    for (int64_t r0 = (int64_t)blockIdx.x * kFactorRows + threadIdx.x; r0 < p.rows; r0 += (int64_t)p.parts * kFactorRows) {
+        int64_t t[kFactorAhead];
+        float g[kFactorAhead], e[kFactorAhead];
+        auto row = [&](int i) __attribute__((always_inline)) {  // (behind the last one, that one again)
+            return r0 + 1024 * i < p.rows ? r0 + 1024 * i : p.rows - 1;
+        };
 #pragma unroll
-        for (int w = 1; w < 16; ++w) v[k] = k & 1 ? __builtin_fmaxf(v[k], sums[k][w]) : __builtin_fminf(v[k], sums[k][w]);
-    const bool one = v[0] == v[1] && v[1] < __builtin_inff() && v[2] >= v[1] * 0x1p-64f && v[3] <= v[1] * 0x1p64f;
-    *p.factor = one ? v[1] : 1.0f;
+        for (int i = 0; i < kFactorAhead; ++i) t[i] = -1, g[i] = e[i] = 0.0f;
+        if (p.dloss) {
+            if (p.target64) {
+#pragma unroll
+                for (int i = 0; i < kFactorAhead; ++i) t[i] = static_cast<const int64_t*>(p.target)[row(i)];
+            } else {
+#pragma unroll
+                for (int i = 0; i < kFactorAhead; ++i) t[i] = static_cast<const int32_t*>(p.target)[row(i)];
+            }
+#pragma unroll
+            for (int i = 0; i < kFactorAhead; ++i) g[i] = p.dloss[row(i) * p.sloss];
+        }
+        if (p.dlse) {
+#pragma unroll
+            for (int i = 0; i < kFactorAhead; ++i) e[i] = p.dlse[row(i) * p.slse];
+        }
+#pragma unroll
+        for (int i = 0; i < kFactorAhead; ++i) {
+            float of[2];
+            factors_of(p, t[i] >= 0 && t[i] < p.vocab, g[i], e[i], of[0], of[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // a NaN or an infinity counts as one
+                const float m = __builtin_fabsf(of[k]) < __builtin_inff() ? __builtin_fabsf(of[k]) : __builtin_inff();
+                if (m != 0.0f) v[2 * k] = __builtin_fminf(v[2 * k], m), v[2 * k + 1] = __builtin_fmaxf(v[2 * k + 1], m);
+            }
+        }
+    }
+    v = extremes<16>(v);
+    if (threadIdx.x == 0) p.part[blockIdx.x] = v;
 }
 
 __global__ __launch_bounds__(256) void xent_rows_kernel(XentRows p) {
+    // the targets' common factor, or 1: where they differ, and where a softmax's factor is so far from it that the quotient
+    // might leave fp32's range
     float by;
-    if (p.sloss == 0 && p.dloss && !p.dlse) {  // one value for all: the factor needs no kernel of its own
+    if (p.parts == 0) {  // one value for all
         by = __builtin_fabsf(*p.dloss * p.scale);
         by = by > 0.0f && by < __builtin_inff() ? by : 1.0f;
-        if (blockIdx.x == 0 && threadIdx.x == 0) *p.factor = by;
     } else {
-        by = *p.factor;
+        static_assert(kFactorParts <= 256);
+        const f32x4 v = extremes<4>((int)threadIdx.x < p.parts ? p.part[threadIdx.x] : f32x4{__builtin_inff(), 0.0f, __builtin_inff(), 0.0f});
+        by = v[0] == v[1] && v[1] < __builtin_inff() && v[2] >= v[1] * 0x1p-64f && v[3] <= v[1] * 0x1p64f ? v[1] : 1.0f;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.factor = by;
     for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < p.rows; r += (int64_t)gridDim.x * 4) {
+        const int64_t t = p.target ? target_of(p.target, p.target64, r) : -1;
+        const bool hit = t >= 0 && t < p.vocab && p.dloss;
         float a, f;
-        const int64_t t = factors_of(p, r, a, f);
+        factors_of(p, hit, hit ? p.dloss[r * p.sloss] : 0.0f, p.dlse ? p.dlse[r * p.slse] : 0.0f, a, f);
         a /= by, f /= by;
         // 2^(l log2(e) - top) f 2^(top - lse log2(e)), top the rounded lse log2(e)
         const float top = p.lse[r] * kLog2e, rest = __builtin_fmaf(p.lse[r], kLog2e, -top);
         const float above = __builtin_fabsf(top) < __builtin_inff() ? f * hw_exp2(-rest) : f;
-        if ((threadIdx.x & 63) == 0) p.row[r] = f32x4{top, above, a, __builtin_bit_cast(float, (int)t)};
+        if ((threadIdx.x & 63) == 0) p.row[r] = f32x4{top, above, a, __builtin_bit_cast(float, hit ? (int)t : -1)};
         const bool on = a != 0.0f || f != 0.0f;
         for (int64_t c = (int64_t)(threadIdx.x & 63) * 8; c < p.wide; c += 64 * 8) {
             const Pack<uint16_t, 8> v = load_some<uint16_t, 8>(p.x + r * p.sx + c, on ? (int)(p.dim - c) : 0);
@@ -241,7 +272,7 @@ struct BwdPlan {
     bool copy_w;
     int64_t width, pieces;  // columns of a piece
     Tiling tx;              // of dx, the same for every piece
-    int64_t row, factor, x, w, d, dx, dw, total;
+    int64_t row, factor, part, x, w, d, dx, dw, total;
 };
 
 int64_t piece_of(const mamba_xent_shape& s) {
@@ -267,7 +298,8 @@ BwdPlan bwd_plan(const mamba_xent_bwd_ptrs& p, const mamba_xent_shape& s) {
     }
     b.row = 0;
     b.factor = b.row + align256(s.rows * 16);
-    b.x = b.factor + 256;
+    b.part = b.factor + 256;
+    b.x = b.part + kFactorParts * 16;
     b.w = b.x + align256(s.rows * up(s.dim, 8) * 2);
     b.d = b.w + (b.copy_w ? align256(s.vocab * up(s.dim, 8) * 2) : 0);
     b.dx = b.d + align256(s.rows * b.width * 2);
@@ -317,8 +349,13 @@ int launch_xent_bwd(const mamba_xent_bwd_ptrs& p, const mamba_xent_shape& s, boo
     uint16_t* x = reinterpret_cast<uint16_t*>(ws + b.x);
     uint16_t* d = reinterpret_cast<uint16_t*>(ws + b.d);
     XentRows r{static_cast<const uint16_t*>(p.x), p.target, p.lse, p.dloss, p.dlse, reinterpret_cast<f32x4*>(ws + b.row), x,
-               reinterpret_cast<float*>(ws + b.factor), s.rows, s.dim, wide, s.vocab, p.x_stride, p.dloss_stride, p.dlse_stride, (int)target64, scale};
-    if (!p.dloss || p.dloss_stride != 0 || p.dlse) on(xent_factor_kernel, dim3(1), dim3(1024), r);
+               reinterpret_cast<f32x4*>(ws + b.part), reinterpret_cast<float*>(ws + b.factor), s.rows, s.dim, wide, s.vocab,
+               p.x_stride, p.dloss_stride, p.dlse_stride, (int)target64, 0, scale};
+    if (!p.dloss || p.dloss_stride != 0 || p.dlse) {
+        const int64_t parts = (s.rows + kFactorRows - 1) / kFactorRows;
+        r.parts = (int)(parts < kFactorParts ? parts : kFactorParts);
+        on(xent_factor_kernel, dim3((unsigned)r.parts), dim3(1024), r);
+    }
     on(xent_rows_kernel, dim3((unsigned)(s.rows < 32768 ? (s.rows + 3) / 4 : 8192)), dim3(256), r);
     const uint16_t* w = static_cast<const uint16_t*>(p.weight);
     int64_t ws_row = p.weight_stride;

@@ -376,3 +376,29 @@ def test_cross_entropy_gradient_beside_a_row_without_a_finite_factor():
         got = block.linear_cross_entropy_bwd(x, w, target, lse, a)["x"]
         rest = torch.arange(40, device=DEV) != 7
         assert torch.equal(got[rest], want[rest]) and not bool(got[7].isfinite().all())
+
+
+@pytest.mark.parametrize("odd_one", [None, 0, 8191, 40000, 99999])
+def test_cross_entropy_gradient_of_many_rows_factors(odd_one):
+    """Factors looked at by several workgroups: alike (and the bits of one value for all), or all but one. Bars as in the
+    other tests; the odd row's factor is another by half."""
+    g = torch.Generator(device=DEV).manual_seed(16)
+    M, K, V = 100000, 64, 300
+    x = torch.randn(M, K, generator=g, device=DEV).to(BF16)
+    w = (torch.randn(V, K, generator=g, device=DEV) * K ** -0.5).to(BF16)
+    target = torch.randint(0, V, (M,), generator=g, device=DEV)
+    lse = block.linear_cross_entropy_fn(x, w, target, return_lse=True)[1]
+    a = torch.full((M,), 0.7, device=DEV)
+    want = block.linear_cross_entropy_bwd(x, w, target, lse, a[:1].expand(M))
+    if odd_one is None:
+        got = block.linear_cross_entropy_bwd(x, w, target, lse, a)
+        assert torch.equal(got["x"], want["x"]) and torch.equal(got["weight"], want["weight"])
+        return
+    a[odd_one] *= 1.5
+    got = block.linear_cross_entropy_bwd(x, w, target, lse, a)
+    ad = a.double()[:, None]
+    p = ad * torch.softmax(x.double() @ w.double().t(), -1)
+    d = p.scatter_add(1, target[:, None], -ad)
+    slack = 2.0 ** -8 * d.abs() + 1e-5 * p.abs()
+    for k, exact, room in (("x", d @ w.double(), slack @ w.double().abs()), ("weight", d.t() @ x.double(), slack.t() @ x.double().abs())):
+        assert bool(((got[k].double() - exact).abs() <= room + (2.0 ** -8 + 1e-5) * exact.abs()).all()), k

@@ -8,6 +8,9 @@ from selective_state_space_29_amd import block, scan
 BASE = 1 << 40
 
 
+FACTORS = 256 + 256 * 16  # the rows' common factor and what it is found from
+
+
 def up(n, a=256):
     return -(-n // a) * a
 
@@ -22,7 +25,7 @@ def xent_bwd(rows, dim, vocab, dx=True, dweight=True):
 def test_cross_entropy_gradients_that_are_not_asked_for_take_no_room(rows, dim, vocab):
     both, dx, dw, none = (xent_bwd(rows, dim, vocab, a, b) for a, b in ((1, 1), (1, 0), (0, 1), (0, 0)))
     # of each row its factors and its part of x; at most 256 MB of the logits' gradients and a piece's rounding
-    base = up(rows * 16) + 256 + up(rows * dim * 2)
+    base = up(rows * 16) + FACTORS + up(rows * dim * 2)
     assert base < none <= base + (1 << 28) + rows * 512
     assert both - none == (dx - none) + (dw - none)
     if rows == 16384:  # several pieces: dx's sums in fp32; the parts of dweight's sums
@@ -34,7 +37,7 @@ def test_cross_entropy_pieces_are_as_many_as_their_bytes_ask_for(rows, vocab, pi
     """256 MB of the logits' gradients a piece, of 1024 columns at least and a multiple of 256."""
     dim = 64
     width = max(1024, up(-(-vocab // pieces)))
-    assert xent_bwd(rows, dim, vocab, False, False) == up(rows * 16) + 256 + up(rows * dim * 2) + up(rows * width * 2)
+    assert xent_bwd(rows, dim, vocab, False, False) == up(rows * 16) + FACTORS + up(rows * dim * 2) + up(rows * width * 2)
 
 
 @pytest.mark.parametrize("rows,dim", [(1, 1 << 20), (3, 1001), (100, 64), (256, 768), (16384, 1536)])
