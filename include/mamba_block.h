@@ -72,7 +72,8 @@ int mamba_conv_fwd(const mamba_conv_ptrs* p, const mamba_conv_shape* s, int act,
  *   dv_s = sum_k weight[d,k] dpre_{s + width - 1 - k} over the steps that see s, + dlast_state where it holds s
  *   dx_s = dv_s (s >= 0), dinitial_state = dv_s (s < 0);  dweight[d,k] = sum dpre_t v_{t-width+1+k};  dbias = sum dpre
  *  - dx in x's layout with strides of its own; dweight (dim, width), dbias (dim) or NULL, fp32;
- *    dinitial_state (batch, width - 1, dim) dtype or NULL.
+ *    dinitial_state (batch, width - 1, dim) dtype or NULL. The workspace depends on the current device's compute-unit
+ *    count.
  */
 typedef struct mamba_conv_bwd_ptrs {
     const void* x;
@@ -246,7 +247,8 @@ int64_t mamba_gated_rms_norm_bwd_workspace_bytes(const mamba_gated_rms_shape* s)
  *  - x (rows, dim), weight (vocab, dim): bf16, row strides free (MAMBA_SCAN_ERR_UNSUPPORTED for F32); dx, dweight
  *    contiguous bf16. target: (rows) int64 or int32 (target64). loss, lse: (rows) fp32, each may be NULL in the
  *    forward (not both); a loss needs target.
- *  - rows, vocab < 2^30, vocab >= 1 where there are rows; dim and row strides up to 2^21.
+ *  - rows, vocab < 2^30, vocab >= 1 where there are rows; dim and row strides up to 2^21, and (rows / 128 + 1) (vocab /
+ *    128 + 1) up to 2^23 (MAMBA_SCAN_ERR_UNSUPPORTED).
  */
 typedef struct mamba_xent_shape {
     int64_t rows, dim, vocab;

@@ -9,8 +9,9 @@
 // The x projection needs every channel before any can go on, which is the boundary between the launches. All of it
 // stays in fp32 from one to the other: u and the shares go through the workspace (at 64 streams of 1536 channels
 // 0.9 MB beside 12.6 MB of scan state). In the second launch 4 lanes hold a channel, 4 of every 16 states each, so
-// that states and A move 16 bytes a lane and the sums over states and dt rows stay within a quad; everything
-// that does not depend on the first launch's sums is loaded before they are.
+// that states and A move 16 bytes a lane and the sums over states and dt rows stay within a quad; at 16 states and a
+// multiple of 4 dt rows everything that does not depend on the first launch's sums is loaded before they are, otherwise
+// states, A and w_dt follow them.
 //
 // Many streams of many channels share workgroups in the second launch, behind one that adds the shares (below).
 //

@@ -4,15 +4,17 @@
 //   dl = (a + dlse) exp(l - lse) - a [target];   dx = scale dl W;   dW = scale dl^T x
 //
 // No logit is stored. Forward: the matrix kernel's tiles of 128 or 256 columns of the vocabulary end in each
-// row's maximum and sum of exponentials over their columns, and a second kernel joins a row's tiles; the tile
-// that holds a row's target writes that logit. Backward: piece by piece of the vocabulary the logits are computed
+// row's largest logit and sum of exponentials over their columns, and a second kernel joins a row's tiles; the tile
+// that holds a row's target writes that logit, and the loss is the difference of the two logits and the sum's logarithm.
+// Backward: piece by piece of the vocabulary the logits are computed
 // again and end as dl (scale folded into the row's factors), rounded to bf16 as the operand of the other two
 // products, whose inputs have 8 bits as well; dl of a piece is what the workspace holds. dx is summed in fp32 over
 // the pieces, one after another, and rounded once behind the last.
 //
-// Bound by the matrix cores. 16384 x 768, vocabulary 50000: forward 1180 us (1.07 PFLOP/s; the library's plain product
-// of this size 1298); backward, 7 pieces: logits' gradients 204 each (0.88), dx 183 (0.98; library 0.92 to 1.03), dW
-// 171 (1.05) and its join 12.6. 64 rows: 17.2 us for the matrix's 77 MB (4.5 TB/s), 4.6 for the join.
+// Bound by the matrix cores. 16384 x 768, vocabulary 50000: forward 1175 to 1220 us (1.03 to 1.07 PFLOP/s; the library's
+// plain product of this size 1298); backward, 7 pieces: logits' gradients 194 to 206 each (0.88 to 0.93), dx 174 to 187
+// (0.96 to 1.03; library 0.92 to 1.03), dW 161 to 172 (1.05 to 1.12) and its join 12.2. 64 rows: 16.7 us for the matrix's
+// 77 MB (4.6 TB/s), 4.2 for the join.
 //
 // The rows of dl that take no part are zeros, and so are those rows in the copy of x that the backward
 // multiplies with them: nothing that padding holds reaches dW.

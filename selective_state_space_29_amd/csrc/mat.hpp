@@ -343,7 +343,7 @@ __device__ __forceinline__ void mat_tile(const MatArgs& m) {
         // that the largest term is 1 and a loss at the maximum has its own digits. With an infinite maximum the
         // exponentials are taken as they are: a sum of zeros, infinity or NaN is then the row's. (Of a tile's 26 us at dim
         // 768 this takes about 3, VALU instructions, a third of them the exponentials; with the lanes joined by shuffles it
-        // took 5.)
+        // took 5. In base 2, with the maximum subtracted in the exponential's own product, it took 0.4 less.)
         constexpr int PARTS = 4 * WQ;
         float2(*sums)[TP] = reinterpret_cast<float2(*)[TP]>(&lds[0]);
         int* rel_of = reinterpret_cast<int*>(&sums[PARTS][0]);  // each row's target as a column of this tile, or -1
