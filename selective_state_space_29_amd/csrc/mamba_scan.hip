@@ -314,7 +314,7 @@ const char* mamba_scan_strerror(int code) {
             return "inconsistent flags/pointers (unknown flag, last_state vs RETURN_LAST_STATE, "
                    "workspace) or overlapping buffers";
         case MAMBA_SCAN_ERR_LAUNCH: return "the HIP runtime rejected the kernel launch";
-        case MAMBA_SCAN_ERR_UNSUPPORTED: return "the forced kernel cannot handle this shape or alignment";
+        case MAMBA_SCAN_ERR_UNSUPPORTED: return "sizes, strides, a type or an alignment that this entry point, or the kernel that is forced, cannot handle";
         case MAMBA_SCAN_ERR_WORKSPACE: return "workspace too small";
         case MAMBA_SCAN_ERR_SCRATCH:
             return "the call needs more workspace than the static scratch buffer holds "

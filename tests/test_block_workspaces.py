@@ -55,3 +55,10 @@ def test_conv_takes_as_many_runs_as_the_header_says(steps):
         assert size(batch, length, 1, 4) > 0, (batch, length)
     for batch, length in ((1 << 30, 9), (1 << 31, 0), (1, 1 << 30), (1 << 27, 128)):
         assert size(batch, length, 1, 4) < 0, (batch, length)
+
+
+def test_what_is_not_supported_is_not_blamed_on_a_forced_kernel_alone():
+    """The entry points without kernels to force refuse by the same code: fp32 in the cross entropy, sizes past a limit."""
+    p = block.XentPtrs(x=BASE, weight=BASE * 2, target=BASE * 3, loss=BASE * 4, x_stride=8, weight_stride=8)
+    code = block._load().mamba_xent_fwd(p, block.XentShape(4, 8, 9), 1, 1.0, scan.F32, None)
+    assert code == -8 and "entry point" in scan.strerror(code) and "type" in scan.strerror(code)
