@@ -101,9 +101,9 @@ __global__ __launch_bounds__(1024) void xent_total_kernel(const float* loss, con
 //
 // The logits' gradients are rounded to bf16 as operands. Where every row with a target has the same factor, as in a mean
 // or a sum, the factor is left out of them and multiplied with the products' sums in fp32: of a target's entry p - 1 is
-// rounded instead of (p - 1) factor, which for most rows is next to 1. (Errors of dx and dW against 64 bits, with their own
-// rounding 0.00166 of the norm: 0.0024 to 0.0026 with the factor in the operands, where the factor's own rounding is a
-// part of every row's, and 0.0017 to 0.0021 without.)
+// rounded instead of (p - 1) factor, and for most rows that is next to 1. (Errors of dx and dW against 64 bits, of whose
+// norm their own rounding is 0.00166: up to 0.0026 with the factor in the operands, where its rounding is the same in every
+// row, and 0.0017 to 0.0021 without.)
 struct XentRows {
     const uint16_t* x;
     const void* target;
